@@ -62,6 +62,7 @@ enum sv_status {
 #define SV_DEVERR_BAD_MAP_ID  0x1   /* a vocab_map entry outside [0, V) was skipped */
 #define SV_DEVERR_TIMEOUT     0x2   /* a pipeline wait gave up; outputs are invalid */
 #define SV_DEVERR_SMEM_ALIGN  0x4   /* shared memory not 1024-byte aligned; nothing was computed */
+#define SV_DEVERR_BAD_SLOT    0x8   /* a state_idx entry >= n_slots was skipped */
 
 /*
  * w4a16_gemm -- y[t][n] = bf16_rne( sum_g float(scales[n][g]) *
@@ -433,6 +434,128 @@ int sv_debug_set_tcgen05(int on);
  *   Errors: SV_ERR_SHAPE if ns > 10^9 (one second).
  */
 int sv_debug_set_wait_stall(uint32_t ns);
+
+/* ------------------------------------------------------------------------
+ * Between the weight reads of a decoder layer
+ *
+ * A hybrid decoder layer runs norm -> projection -> gated delta rule ->
+ * projection -> norm -> gated feed-forward -> projection.  The projections
+ * are w4a16_gemm; the calls below are the rest.  They keep the conventions
+ * above with these differences, stated per call: rows may be strided (an
+ * `ld` argument is the distance between rows in elements), row counts are
+ * not limited to 32 where the call says so, and a call with no rows (T = 0,
+ * B = 0) succeeds without a launch.  None of them allocates, and none uses
+ * the per-device scratch area, so they may overlap with other calls.  The
+ * framework serves frozen int4 weights; there are no gradients.
+ */
+
+#define SV_NORM_UNIT_OFFSET 0x1     /* the weight is stored as an offset from 1 */
+
+/*
+ * Residual addition and root-mean-square norm of T rows of D columns:
+ *   s = bf16(x + residual)        (s = x when residual is NULL)
+ *   y = s / sqrt(mean(s^2) + eps) * weight     (or * (1 + weight))
+ * s is written to residual_out, which may be residual itself (both or
+ * neither are given); y may be x.  x, residual, y: [T][D] bf16, rows ldx,
+ * ldr, ldro, ldy apart; weight [D] bf16.  Sums and the norm are fp32; the
+ * norm is that of the rounded s, the value the next layer adds to.
+ * T >= 0, 1 <= D <= 65536, eps >= 0; addresses need 2-byte alignment, and
+ * rows are read 16 bytes at a time where D, the strides and the addresses
+ * are multiples of 8 elements.  A row holding a NaN or an infinity gives
+ * NaNs as the formula does.
+ */
+int rmsnorm_residual(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long long ldr, const sv_bf16 *weight,
+                     int T, int D, float eps, int flags, sv_bf16 *residual_out, long long ldro, sv_bf16 *y,
+                     long long ldy, sv_stream stream);
+
+/*
+ * The same with an 8-bit output: y holds e4m3 bytes and scales fp32 values,
+ *   scale = max(max|y|, 448 * 2^-126) / 448,   y8 = e4m3(y / scale)
+ * over each group of 128 columns (group = 128; the last group may be short;
+ * scales [T][ceil(D / 128)], rows lds apart) or the whole row (group = 0;
+ * one scale a row).  A group holding a NaN gets a NaN scale.
+ */
+int rmsnorm_residual_fp8(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long long ldr,
+                         const sv_bf16 *weight, int T, int D, float eps, int flags, int group, sv_bf16 *residual_out,
+                         long long ldro, uint8_t *y, long long ldy, float *scales, long long lds, sv_stream stream);
+
+/*
+ * Gated delta rule.  Every value head keeps a state S [dv][dk] (fp32); a row
+ * with key k, query q (dk values), value v (dv), log decay g and rate beta
+ * does
+ *   S <- exp(g) S;  u = beta (v - S k);  S <- S + u k^T;  o = scale * S q.
+ * Value head h uses key head h / (Hv / Hk).  With SV_DELTA_L2NORM keys and
+ * queries are first divided by sqrt(|.|^2 + 1e-6).
+ */
+typedef struct sv_delta_rows {
+    const sv_bf16 *q;                      /* [rows][Hk][dk], rows ldq elements apart            */
+    const sv_bf16 *k;                      /* [rows][Hk][dk], ldk                                */
+    const sv_bf16 *v;                      /* [rows][Hv][dv], ldv                                */
+    const float *g, *beta;                 /* [rows][Hv], ldg                                    */
+    long long ldq, ldk, ldv, ldg;          /* ldq, ldk, ldv multiples of 8; q, k, v 16-byte aligned */
+} sv_delta_rows;                           /* q, k, v may be slices of one projection's output   */
+
+#define SV_DELTA_L2NORM    0x1             /* normalise keys and queries                         */
+#define SV_DELTA_COMMIT    0x2             /* step: the new rows are kept in the state           */
+#define SV_DELTA_ZERO_INIT 0x4             /* chunk: sequences start from a zero state           */
+
+typedef struct sv_delta_shape {
+    int Hk, Hv;                            /* key and value heads, Hv a multiple of Hk           */
+    int dk, dv;                            /* 64 or 128 each                                     */
+    float scale;                           /* usually 1 / sqrt(dk)                               */
+    int flags;                             /* SV_DELTA_*                                         */
+} sv_delta_shape;
+
+/*
+ * Decode and verify rows: T (0..32) new rows for each of B sequences, row t
+ * of sequence b at b * T + t, outputs o [B * T][Hv][dv] bf16 (rows ldo
+ * apart).  state [n_slots][Hv][dv][dk]; sequence b uses slot state_idx[b]
+ * (slot b when state_idx is NULL).  An entry with a negative slot is
+ * inactive: its outputs are zero and nothing else of it is touched; a slot
+ * >= n_slots is treated the same and sets SV_DEVERR_BAD_SLOT.  Two entries
+ * must not share a slot.
+ *
+ * With SV_DELTA_COMMIT the rows are final: the state after them is written
+ * (plain decode).  Without it they are drafts under verification: the state
+ * is not advanced past them, and the next call brings them again as `prev`
+ * (prev_T rows a sequence, row t of sequence b at b * prev_T + t, q unused)
+ * with accept_len [B] from lmhead_verify, on the device: the first
+ * accept_len[b] + 1 of them (the committed token and the accepted drafts;
+ * at least none, at most all; all when accept_len is NULL) are replayed
+ * into the state, which is written, before the new rows run.  T = 0 only
+ * replays.
+ */
+int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev, int prev_T,
+                     const int32_t *accept_len, int B, const sv_delta_shape *shape, float *state,
+                     const int32_t *state_idx, int n_slots, sv_bf16 *o, long long ldo, sv_stream stream);
+
+/*
+ * Whole prompts: R rows of B sequences one after another, sequence b having
+ * rows cu_seqlens[b] .. cu_seqlens[b + 1] (B + 1 entries on the device, not
+ * decreasing, within 0..R; out-of-range entries are moved into the range; a
+ * sequence may be empty).  Each sequence's state is read from its slot
+ * (taken as zero with SV_DELTA_ZERO_INIT), carried through its rows and
+ * written back.  Rows of no sequence are not touched.  `ws` is device
+ * memory of at least gated_delta_chunk_bytes(R, B, shape) bytes (0 when the
+ * sizes are invalid), 16-byte aligned, free until the call has run.
+ */
+size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape);
+int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
+                      float *state, const int32_t *state_idx, int n_slots, sv_bf16 *o, long long ldo, void *ws,
+                      size_t ws_bytes, sv_stream stream);
+
+#define SV_ACT_SILU      0                 /* g / (1 + exp(-g))                                  */
+#define SV_ACT_GELU_TANH 1                 /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))      */
+
+/*
+ * First half of a gated feed-forward block: h = act(x Wg^T) * (x Wu^T),
+ * both projections, the activation and the product in one kernel.  Wq
+ * [2F][K/8] and scales [2F][K/128] hold the F gate rows, then the F up rows
+ * (the fused gate+up matrix as w4a16_gemm reads it); x [T][K], h [T][F].
+ * The sums are fp32 and not rounded before the activation and the product.
+ */
+int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, int T, int K, int F, int act,
+                  sv_bf16 *h, sv_stream stream);
 
 #ifdef __cplusplus
 }

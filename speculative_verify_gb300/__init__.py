@@ -13,12 +13,16 @@ import os
 import re
 
 from . import build as _build
+from . import layer as _layer
+from .layer import (gated_delta_chunk, gated_delta_step, rmsnorm, rmsnorm_fp8,  # noqa: F401
+                    w4a16_gate_up)
 
 SV_OK = 0
 STATUS = {0: "SV_OK", -1: "SV_ERR_NULL", -2: "SV_ERR_SHAPE", -3: "SV_ERR_ALIGN",
           -4: "SV_ERR_CUDA", -5: "SV_ERR_NOMEM", -6: "SV_ERR_DEVICE"}
 DEVERR_BAD_MAP_ID = 0x1
 DEVERR_TIMEOUT = 0x2
+DEVERR_BAD_SLOT = 0x8
 
 _lib = None
 
@@ -108,6 +112,7 @@ def load(path: str | None = None):
     lib.sv_debug_set_tcgen05.restype = ci
     lib.sv_debug_set_wait_stall.argtypes = [ctypes.c_uint32]
     lib.sv_debug_set_wait_stall.restype = ci
+    _layer.declare(lib)
     _lib = lib
     return lib
 

@@ -1,8 +1,9 @@
 """Build the sm_103a shared library in-tree with nvcc.
 
-``build()`` compiles ``csrc/specverify.cu`` (which includes the kernel
-headers) into ``speculative_verify_gb300/_build/libspecverify.so``, one
-``-gencode`` for ``sm_103a``, position-independent, static CUDA runtime.
+``build()`` compiles the translation units of ``csrc/`` (which include the
+kernel headers) side by side and links them into
+``speculative_verify_gb300/_build/libspecverify.so``, one ``-gencode`` for
+``sm_103a``, position-independent, static CUDA runtime.
 """
 from __future__ import annotations
 
@@ -32,7 +33,7 @@ def _nvcc() -> str:
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
@@ -42,20 +43,33 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
+def _run(cmds, verbose: bool) -> None:
+    """Run the commands side by side; raise with the output of one that failed."""
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+    outs = [p.communicate()[0] for p in procs]
+    for cmd, p, out in zip(cmds, procs, outs):
+        if p.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + out)
+        if verbose:
+            print(out)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the library if any source is newer than it; return its path."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
-    tmp = LIB_PATH + ".%d.tmp" % os.getpid()
-    cmd = [_nvcc(), *ARCH_FLAGS, *NVCC_FLAGS, "-I" + INCLUDE, "-shared", "-o", tmp,
-           os.path.join(CSRC, "specverify.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if verbose:
-        print(res.stdout + res.stderr)
+    tag = ".%d.tmp" % os.getpid()
+    tmp = LIB_PATH + tag
+    nvcc, flags = _nvcc(), [*ARCH_FLAGS, *NVCC_FLAGS, "-I" + INCLUDE] + (["-Xptxas=-v"] if verbose else [])
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    objs = [os.path.join(BUILD_DIR, os.path.basename(u) + tag + ".o") for u in units]
+    try:
+        _run([[nvcc, *flags, "-c", "-o", o, u] for u, o in zip(units, objs)], verbose)
+        _run([[nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]], verbose)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH

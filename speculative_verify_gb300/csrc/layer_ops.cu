@@ -1,0 +1,353 @@
+// layer_ops.cu -- the C ABI of what a hybrid decoder layer runs between its
+// weight reads (include/specverify.h): argument checks, launch shapes and
+// dispatch of the norm, gated delta rule and gated feed-forward kernels.
+#include <cstring>
+#include <mutex>
+
+#include "gated_delta.cuh"
+#include "gated_delta_chunk.cuh"
+#include "rmsnorm.cuh"
+#include "specverify.h"
+#include "sv_host.h"
+#include "w4a16_gate_up.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int MAX_DEVICES = 64;
+
+template <class F>
+cudaError_t raise(F *kernel, int bytes)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// The current device's facts, with the kernels' shared-memory limits raised
+// once per device.
+int ops_device(DeviceInfo *out)
+{
+    const int rc = device_info(out);
+    if (rc != SV_OK) return rc;
+    static std::mutex mu;
+    static bool ready[MAX_DEVICES] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (ready[out->dev]) return SV_OK;
+    cudaError_t e = cudaSuccess;
+    auto up = [&](cudaError_t r) { e = e != cudaSuccess ? e : r; };
+    up(raise(gated_delta_step_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
+    up(raise(gated_delta_step_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
+    up(raise(gated_delta_rows_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
+    up(raise(gated_delta_rows_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
+    up(raise(w4a16_gate_up_kernel<1>, gu_smem_bytes(1)));
+    up(raise(w4a16_gate_up_kernel<2>, gu_smem_bytes(2)));
+    up(raise(w4a16_gate_up_kernel<4>, gu_smem_bytes(4)));
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    ready[out->dev] = true;
+    return SV_OK;
+}
+
+template <class... P, class... A>
+int launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg;
+    launch_config(&cfg, attr, grid, threads, smem, stream);
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    return SV_OK;
+}
+
+// ----------------------------------------------------------------- norm
+
+constexpr int NORM_MAX_D = 65536;
+
+int check_norm(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long long ldr, const sv_bf16 *weight, int T,
+               int D, float eps, int flags, const sv_bf16 *residual_out, long long ldro, const void *y, long long ldy)
+{
+    if (T < 0 || D < 1 || D > NORM_MAX_D) return SV_ERR_SHAPE;
+    if (!(eps >= 0.f) || (flags & ~SV_NORM_UNIT_OFFSET)) return SV_ERR_SHAPE;
+    if (ldx < D || ldy < D || (residual && (ldr < D || ldro < D))) return SV_ERR_SHAPE;
+    if (!x || !weight || !y || (residual && !residual_out) || (!residual && residual_out)) return SV_ERR_NULL;
+    if (!aligned_to(x, 2) || !aligned_to(weight, 2) || !aligned_to(residual, 2) || !aligned_to(residual_out, 2))
+        return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
+template <int VEC, bool FP8>
+int norm_launch(const NormParams &p, int T, int vpt, int threads, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(T));
+    switch (vpt) {
+    case 1: return launch(rmsnorm_kernel<VEC, 1, FP8>, grid, threads, 0, stream, p);
+    case 2: return launch(rmsnorm_kernel<VEC, 2, FP8>, grid, threads, 0, stream, p);
+    case 4: return launch(rmsnorm_kernel<VEC, 4, FP8>, grid, threads, 0, stream, p);
+    case 8: return launch(rmsnorm_kernel<VEC, 8, FP8>, grid, threads, 0, stream, p);
+    default: break;
+    }
+    if constexpr (VEC == 1) {
+        if (vpt == 16) return launch(rmsnorm_kernel<VEC, 16, FP8>, grid, threads, 0, stream, p);
+        return launch(rmsnorm_kernel<VEC, 64, FP8>, grid, threads, 0, stream, p);
+    }
+    return SV_ERR_SHAPE;
+}
+
+template <bool FP8>
+int norm_call(NormParams p, int T, cudaStream_t stream)
+{
+    if (T == 0) return SV_OK;
+    DeviceInfo dev;
+    const int rc = ops_device(&dev);
+    if (rc != SV_OK) return rc;
+    const bool wide = p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldy % 8 == 0 && aligned_to(p.x, 16) &&
+                      aligned_to(p.weight, 16) && aligned_to(FP8 ? static_cast<const void *>(p.y8) : p.y, FP8 ? 8 : 16) &&
+                      (!p.residual || (p.ldr % 8 == 0 && p.ldro % 8 == 0 && aligned_to(p.residual, 16) &&
+                                       aligned_to(p.residual_out, 16)));
+    const int n = wide ? p.D / 8 : p.D;          // pieces of a row
+    int vpt = 1;
+    while (n > vpt * RN_MAX_THREADS) vpt *= 2;
+    if (!wide && vpt == 32) vpt = 64;
+    const int per = 128;                         // the scalar 8-bit path groups four warps
+    const int threads = ((n + vpt - 1) / vpt + per - 1) / per * per;
+    return wide ? norm_launch<8, FP8>(p, T, vpt, threads, stream) : norm_launch<1, FP8>(p, T, vpt, threads, stream);
+}
+
+// ----------------------------------------------------- gated delta rule
+
+int check_delta_shape(const sv_delta_shape *s)
+{
+    if (!s) return SV_ERR_NULL;
+    if (s->Hk < 1 || s->Hv < 1 || s->Hv > 65535 || s->Hv % s->Hk) return SV_ERR_SHAPE;
+    if ((s->dk != 64 && s->dk != 128) || (s->dv != 64 && s->dv != 128)) return SV_ERR_SHAPE;
+    if (s->scale != s->scale || (s->flags & ~(SV_DELTA_L2NORM | SV_DELTA_COMMIT | SV_DELTA_ZERO_INIT))) return SV_ERR_SHAPE;
+    return SV_OK;
+}
+
+int check_delta_rows(const sv_delta_rows *r, const sv_delta_shape *s, bool want_q)
+{
+    if (!r) return SV_ERR_NULL;
+    if ((want_q && !r->q) || !r->k || !r->v || !r->g || !r->beta) return SV_ERR_NULL;
+    const long long nk = static_cast<long long>(s->Hk) * s->dk, nv = static_cast<long long>(s->Hv) * s->dv;
+    if ((want_q && r->ldq < nk) || r->ldk < nk || r->ldv < nv || r->ldg < s->Hv) return SV_ERR_SHAPE;
+    if ((want_q && (r->ldq % 8 || !aligned_to(r->q, 16))) || r->ldk % 8 || r->ldv % 8 || !aligned_to(r->k, 16) ||
+        !aligned_to(r->v, 16) || !aligned_to(r->g, 4) || !aligned_to(r->beta, 4))
+        return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
+int check_delta_state(const sv_delta_shape *s, const float *state, const int32_t *state_idx, int n_slots, int B)
+{
+    if (B < 0 || B > 65535 || n_slots < 1 || (!state_idx && n_slots < B)) return SV_ERR_SHAPE;
+    if (!state) return SV_ERR_NULL;
+    if (!aligned_to(state, 16) || !aligned_to(state_idx, 4)) return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
+int check_delta_out(const sv_delta_shape *s, const sv_bf16 *o, long long ldo)
+{
+    if (!o) return SV_ERR_NULL;
+    if (ldo < static_cast<long long>(s->Hv) * s->dv) return SV_ERR_SHAPE;
+    if (ldo % 8 || !aligned_to(o, 16)) return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
+DeltaRows delta_rows(const sv_delta_rows *r)
+{
+    if (!r) return DeltaRows{};
+    return DeltaRows{r->q, r->k, r->v, r->g, r->beta, r->ldq, r->ldk, r->ldv, r->ldg};
+}
+
+DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, float *state, const int32_t *state_idx,
+                         int n_slots, sv_bf16 *o, long long ldo, const DeviceInfo &dev)
+{
+    DeltaParams p{};
+    p.rows = delta_rows(rows);
+    p.Hk = s->Hk;
+    p.Hv = s->Hv;
+    p.dv = s->dv;
+    p.scale = s->scale;
+    p.l2norm = (s->flags & SV_DELTA_L2NORM) != 0;
+    p.commit = (s->flags & SV_DELTA_COMMIT) != 0;
+    p.state = state;
+    p.state_idx = state_idx;
+    p.n_slots = n_slots;
+    p.o = o;
+    p.ldo = ldo;
+    p.cols = s->dv < 32 ? s->dv : 32;
+    p.err = dev.err;
+    return p;
+}
+
+// ------------------------------------------------------ gated feed-forward
+
+template <int NT>
+int gate_up_launch(const GateUpParams &p, const DeviceInfo &dev, cudaStream_t stream)
+{
+    const int grid = p.tiles < dev.sms ? p.tiles : dev.sms;
+    return launch(w4a16_gate_up_kernel<NT>, dim3(static_cast<unsigned>(grid)), GU_WARPS * 32, gu_smem_bytes(NT), stream, p);
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" {
+
+int rmsnorm_residual(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long long ldr, const sv_bf16 *weight,
+                     int T, int D, float eps, int flags, sv_bf16 *residual_out, long long ldro, sv_bf16 *y,
+                     long long ldy, sv_stream stream)
+{
+    using namespace sv;
+    const int rc = check_norm(x, ldx, residual, ldr, weight, T, D, eps, flags, residual_out, ldro, y, ldy);
+    if (rc != SV_OK) return rc;
+    if (!aligned_to(y, 2)) return SV_ERR_ALIGN;
+    NormParams p{};
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.residual_out = residual_out;
+    p.y = y;
+    p.ldx = ldx;
+    p.ldr = ldr;
+    p.ldro = ldro;
+    p.ldy = ldy;
+    p.D = D;
+    p.eps = eps;
+    p.w_add = (flags & SV_NORM_UNIT_OFFSET) ? 1.f : 0.f;
+    return norm_call<false>(p, T, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int rmsnorm_residual_fp8(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long long ldr,
+                         const sv_bf16 *weight, int T, int D, float eps, int flags, int group, sv_bf16 *residual_out,
+                         long long ldro, uint8_t *y, long long ldy, float *scales, long long lds, sv_stream stream)
+{
+    using namespace sv;
+    const int rc = check_norm(x, ldx, residual, ldr, weight, T, D, eps, flags, residual_out, ldro, y, ldy);
+    if (rc != SV_OK) return rc;
+    if (group != 0 && group != RN_GROUP) return SV_ERR_SHAPE;
+    if (lds < (group ? (D + group - 1) / group : 1)) return SV_ERR_SHAPE;
+    if (!scales) return SV_ERR_NULL;
+    if (!aligned_to(scales, 4)) return SV_ERR_ALIGN;
+    NormParams p{};
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.residual_out = residual_out;
+    p.y8 = y;
+    p.scales = scales;
+    p.ldx = ldx;
+    p.ldr = ldr;
+    p.ldro = ldro;
+    p.ldy = ldy;
+    p.lds = lds;
+    p.D = D;
+    p.eps = eps;
+    p.w_add = (flags & SV_NORM_UNIT_OFFSET) ? 1.f : 0.f;
+    p.row_scale = group == 0;
+    return norm_call<true>(p, T, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev, int prev_T,
+                     const int32_t *accept_len, int B, const sv_delta_shape *shape, float *state,
+                     const int32_t *state_idx, int n_slots, sv_bf16 *o, long long ldo, sv_stream stream)
+{
+    using namespace sv;
+    int rc = check_delta_shape(shape);
+    if (rc != SV_OK) return rc;
+    if (shape->flags & SV_DELTA_ZERO_INIT) return SV_ERR_SHAPE;
+    if (T < 0 || T > GD_MAX_ROWS || prev_T < 0 || prev_T > GD_MAX_ROWS) return SV_ERR_SHAPE;
+    if (T > 0 && (rc = check_delta_rows(rows, shape, true)) != SV_OK) return rc;
+    if (T > 0 && (rc = check_delta_out(shape, o, ldo)) != SV_OK) return rc;
+    if (prev_T > 0 && (rc = check_delta_rows(prev, shape, false)) != SV_OK) return rc;
+    if (!aligned_to(accept_len, 4)) return SV_ERR_ALIGN;
+    rc = check_delta_state(shape, state, state_idx, n_slots, B);
+    if (rc != SV_OK) return rc;
+    if (B == 0 || T + prev_T == 0) return SV_OK;
+    DeviceInfo dev;
+    rc = ops_device(&dev);
+    if (rc != SV_OK) return rc;
+    DeltaParams p = delta_params(rows, shape, state, state_idx, n_slots, o, ldo, dev);
+    p.T = T;
+    p.prev_T = prev_T;
+    if (prev_T > 0) p.prev = delta_rows(prev);
+    p.accept_len = accept_len;
+    const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
+    const int cap = T > prev_T ? T : prev_T;
+    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, 4 * p.cols, smem, cs, p)
+                           : launch(gated_delta_step_kernel<128>, grid, 4 * p.cols, smem, cs, p);
+}
+
+size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape)
+{
+    if (sv::check_delta_shape(shape) != SV_OK || R < 0 || B < 0) return 0;
+    return 16;
+}
+
+int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
+                      float *state, const int32_t *state_idx, int n_slots, sv_bf16 *o, long long ldo, void *ws,
+                      size_t ws_bytes, sv_stream stream)
+{
+    using namespace sv;
+    int rc = check_delta_shape(shape);
+    if (rc != SV_OK) return rc;
+    if (shape->flags & SV_DELTA_COMMIT) return SV_ERR_SHAPE;
+    if (R < 0) return SV_ERR_SHAPE;
+    if (R > 0 && (rc = check_delta_rows(rows, shape, true)) != SV_OK) return rc;
+    if (R > 0 && (rc = check_delta_out(shape, o, ldo)) != SV_OK) return rc;
+    rc = check_delta_state(shape, state, state_idx, n_slots, B);
+    if (rc != SV_OK) return rc;
+    if (!cu_seqlens || !ws) return SV_ERR_NULL;
+    if (!aligned_to(cu_seqlens, 4) || !aligned_to(ws, 16)) return SV_ERR_ALIGN;
+    if (ws_bytes < gated_delta_chunk_bytes(R, B, shape)) return SV_ERR_SHAPE;
+    if (B == 0) return SV_OK;
+    DeviceInfo dev;
+    rc = ops_device(&dev);
+    if (rc != SV_OK) return rc;
+    DeltaChunkParams p{};
+    p.d = delta_params(rows, shape, state, state_idx, n_slots, o, ldo, dev);
+    p.cu = cu_seqlens;
+    p.R = R;
+    p.zero_init = (shape->flags & SV_DELTA_ZERO_INIT) != 0;
+    const dim3 grid(static_cast<unsigned>(p.d.dv / p.d.cols), static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(B));
+    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(GD_MAX_ROWS, shape->dk, p.d.cols));
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    return shape->dk == 64 ? launch(gated_delta_rows_kernel<64>, grid, 4 * p.d.cols, smem, cs, p)
+                           : launch(gated_delta_rows_kernel<128>, grid, 4 * p.d.cols, smem, cs, p);
+}
+
+int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, int T, int K, int F, int act,
+                  sv_bf16 *h, sv_stream stream)
+{
+    using namespace sv;
+    if (!x || !Wq || !scales || !h) return SV_ERR_NULL;
+    if (T < 1 || T > GU_MAX_TOKENS || K < 128 || K % 128 || F < 1 || F > (1 << 30)) return SV_ERR_SHAPE;
+    if (act != SV_ACT_SILU && act != SV_ACT_GELU_TANH) return SV_ERR_SHAPE;
+    if (!aligned_to(x, 16) || !aligned_to(Wq, 16) || !aligned_to(scales, 16) || !aligned_to(h, 16)) return SV_ERR_ALIGN;
+    DeviceInfo dev;
+    const int rc = ops_device(&dev);
+    if (rc != SV_OK) return rc;
+    GateUpParams p{};
+    p.x = x;
+    p.Wq = Wq;
+    p.scales = scales;
+    p.h = h;
+    p.T = T;
+    p.K = K;
+    p.G = K / 128;
+    p.F = F;
+    p.tiles = (F + 7) / 8;
+    p.act = act;
+    const int per = (p.tiles + dev.sms - 1) / dev.sms;      // tiles of a block
+    while (p.ks_log < 4 && (per << (p.ks_log + 1)) <= GU_WARPS) ++p.ks_log;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (T <= 8) return gate_up_launch<1>(p, dev, cs);
+    if (T <= 16) return gate_up_launch<2>(p, dev, cs);
+    return gate_up_launch<4>(p, dev, cs);
+}
+
+}  // extern "C"

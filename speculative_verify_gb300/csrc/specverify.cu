@@ -15,6 +15,7 @@
 #include "hbm_read.cuh"
 #include "rescore.cuh"
 #include "specverify.h"
+#include "sv_host.h"
 #include "w4a16_stream.cuh"
 #include "w4a16_wide.cuh"
 #include "w4a16_tc.cuh"
@@ -913,6 +914,18 @@ int noalloc_state(DeviceState **out)
 }
 
 }  // namespace
+
+int device_info(DeviceInfo *out)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+    DeviceState *st = nullptr;
+    const int rc = device_state(&st);
+    if (rc != SV_OK) return rc;
+    *out = DeviceInfo{dev, st->sms, st->smem_optin, st->err};
+    return SV_OK;
+}
+
 }  // namespace sv
 
 extern "C" {
