@@ -1,6 +1,9 @@
 // layer_ops.cu -- the C ABI of what a hybrid decoder layer runs between its
 // weight reads (include/specverify.h): argument checks, launch shapes and
 // dispatch of the norm, gated delta rule and gated feed-forward kernels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cstring>
 #include <mutex>
 
@@ -15,6 +18,23 @@ namespace sv {
 namespace {
 
 constexpr int MAX_DEVICES = 64;
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+// Tensor map of `rows` bf16 rows of `cols` values, `ld` elements apart; boxes
+// of 64 rows and `width` values, 128-byte swizzled where they are 64 wide.
+int encode_rows(CUtensorMap *m, const void *base, long long cols, long long rows, long long ld, int width, bool swizzled)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), DC_ROWS};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SV_OK : SV_ERR_CUDA;
+}
 
 template <class F>
 cudaError_t raise(F *kernel, int bytes)
@@ -38,6 +58,17 @@ int ops_device(DeviceInfo *out)
     up(raise(gated_delta_step_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
     up(raise(gated_delta_rows_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
     up(raise(gated_delta_rows_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
+    up(raise(delta_prep_kernel<64>, sizeof(DcPrepSmem<64>)));
+    up(raise(delta_prep_kernel<128>, sizeof(DcPrepSmem<128>)));
+    up(raise(delta_scan_kernel<64>, DsSmem<64>::BYTES));
+    up(raise(delta_scan_kernel<128>, DsSmem<128>::BYTES));
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        up(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q));
+        if (e == cudaSuccess && (q != cudaDriverEntryPointSuccess || !fn)) return SV_ERR_CUDA;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
     up(raise(w4a16_gate_up_kernel<1>, gu_smem_bytes(1)));
     up(raise(w4a16_gate_up_kernel<2>, gu_smem_bytes(2)));
     up(raise(w4a16_gate_up_kernel<4>, gu_smem_bytes(4)));
@@ -182,6 +213,29 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
     return p;
 }
 
+// Blocks of the workspace: every sequence's whole and part blocks.
+long long delta_blocks(int R, int B) { return static_cast<long long>(R / DC_ROWS) + B; }
+
+// Short prompts (fewer rows than a block on average) go row by row.
+bool delta_by_rows(int R, int B) { return R < static_cast<long long>(DC_ROWS) * B; }
+
+template <int DK>
+int delta_chunk_launch(const DeltaChunkParams &p, cudaStream_t stream)
+{
+    CUtensorMap tmK, tmQ, tmV;
+    const DeltaRows &r = p.d.rows;
+    const long long nk = static_cast<long long>(p.d.Hk) * DK, nv = static_cast<long long>(p.d.Hv) * p.d.dv;
+    int rc = encode_rows(&tmK, r.k, nk, p.R, r.ldk, 64, true);
+    if (rc == SV_OK) rc = encode_rows(&tmQ, r.q, nk, p.R, r.ldq, 64, true);
+    if (rc == SV_OK) rc = encode_rows(&tmV, r.v, nv, p.R, r.ldv, p.d.dv, false);
+    if (rc != SV_OK) return rc;
+    rc = launch(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(delta_blocks(p.R, p.B)), static_cast<unsigned>(p.d.Hv)),
+                128, sizeof(DcPrepSmem<DK>), stream, p);
+    if (rc != SV_OK) return rc;
+    return launch(delta_scan_kernel<DK>, dim3(static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(p.B)), DS_THREADS,
+                  DsSmem<DK>::BYTES, stream, p, tmK, tmQ, tmV);
+}
+
 // ------------------------------------------------------ gated feed-forward
 
 template <int NT>
@@ -285,7 +339,9 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
 size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape)
 {
     if (sv::check_delta_shape(shape) != SV_OK || R < 0 || B < 0) return 0;
-    return 16;
+    if (sv::delta_by_rows(R, B)) return 16;
+    const size_t n = static_cast<size_t>(sv::delta_blocks(R, B)) * static_cast<size_t>(shape->Hv) * sv::DC_BLOCK;
+    return n ? n : 16;
 }
 
 int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
@@ -312,10 +368,13 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     p.d = delta_params(rows, shape, state, state_idx, n_slots, o, ldo, dev);
     p.cu = cu_seqlens;
     p.R = R;
+    p.B = B;
+    p.ws = static_cast<uint8_t *>(ws);
     p.zero_init = (shape->flags & SV_DELTA_ZERO_INIT) != 0;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (!delta_by_rows(R, B)) return shape->dk == 64 ? delta_chunk_launch<64>(p, cs) : delta_chunk_launch<128>(p, cs);
     const dim3 grid(static_cast<unsigned>(p.d.dv / p.d.cols), static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(B));
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(GD_MAX_ROWS, shape->dk, p.d.cols));
-    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     return shape->dk == 64 ? launch(gated_delta_rows_kernel<64>, grid, 4 * p.d.cols, smem, cs, p)
                            : launch(gated_delta_rows_kernel<128>, grid, 4 * p.d.cols, smem, cs, p);
 }

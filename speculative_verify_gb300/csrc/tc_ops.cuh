@@ -1,0 +1,66 @@
+// tc_ops.cuh -- tensor-memory stores of several widths, descriptors of
+// 128-byte swizzled operands and the two-term bf16 split, for the layer
+// operators' tcgen05 kernels.
+#pragma once
+
+#include <cstdint>
+
+#include "sv_ptx.cuh"
+
+namespace sv {
+
+// Two floats -> bf16x2 (round to nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// a and b as two bf16 terms each: hi the value rounded, lo what is left
+// rounded; together 16 bits of each.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// Shared-memory descriptor of an operand whose rows run along the products'
+// K: 64 columns (128 bytes) a row, 16-byte pieces swizzled within eight rows
+// (layout 2 at bits 61-63), 1024 bytes from one eight rows to the next
+// (stride byte offset >> 4 at bits 32-45), descriptor version 1 (bits 46-48).
+// A step of 16 columns along K is 32 bytes further.
+__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// The same tile read across: its rows are the products' K and its 64
+// columns their N.  Eight rows along K are 1024 bytes; a step of 16 rows is
+// 2048 bytes further.  (The leading byte offset is the distance to the next
+// 64 columns, which no product here reaches.)
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// This thread's N registers -> N consecutive tensor-memory columns of its lane.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N])
+{
+    static_assert(N == 16 || N == 32, "widths in use");
+    if constexpr (N == 32) {
+        tmem_st32(taddr, v);
+    } else {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+                     "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+                     ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                       "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+                       "r"(v[15])
+                     : "memory");
+    }
+}
+
+}  // namespace sv
