@@ -34,7 +34,8 @@ namespace sv {
 constexpr int DC_ROWS = 64;                     // rows of a block
 constexpr int DC_MAT = DC_ROWS * 128;           // bytes of one 64 x 64 bf16 matrix, 128-byte swizzled
 constexpr int DC_FACTORS = 1024;                // bytes of a block's row factors
-constexpr int DC_BLOCK = 4 * DC_MAT + DC_FACTORS;   // T (two terms), M (two terms), factors
+constexpr int DC_BLOCK = 4 * DC_MAT + DC_FACTORS;   // T transposed (two terms), M (two terms), factors
+constexpr int DC_FLAGS = 4096;                  // bytes of hand-over flags before the blocks, one word a CTA
 constexpr float DC_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
 
 struct DeltaChunkParams {
@@ -42,7 +43,8 @@ struct DeltaChunkParams {
     const int32_t *cu;                          // [B + 1] first rows
     int R, B;                                   // rows in all, sequences
     int zero_init;
-    uint8_t *ws;                                // [R / 64 + B][Hv][DC_BLOCK]
+    unsigned *flags;                            // [DC_FLAGS / 4], zero when the scan starts
+    uint8_t *blocks;                            // [R / 64 + B][Hv][DC_BLOCK]
 };
 
 // The rows of sequence b: cu[b] .. cu[b + 1], kept within [0, R].
@@ -94,6 +96,22 @@ __global__ void __launch_bounds__(512) gated_delta_rows_kernel(const DeltaChunkP
 }
 
 // ----------------------------------------------------------------- prep
+//
+// One CTA per block of rows and key head: K K^T and Q K^T once, then T and M
+// of each value head.  A warp has 16 rows (row block w) of both products and
+// keeps them in registers for all value heads.
+//
+// Decays: e^(G_i - G_j) below the diagonal blocks is e^(G_i - G_r) e^(G_r -
+// G_j) with r the first row of i's block, both at most 1 for decays; within a
+// diagonal block it is taken directly.
+//
+// T: the 16 x 16 diagonal blocks of (I + A)^-1 by forward substitution (fp32,
+// a column a lane), the others by T_IJ = -T_II sum_K A_IK T_KJ on the tensor
+// cores.  They are computed transposed, T_IJ^T = -(sum_K T_KJ^T A_IK^T) T_II^T:
+// an accumulator's registers are then the next product's A operand as they
+// stand, and warp J can do all of column block J.  Operands in two bf16 terms.
+// T diag(beta) is stored transposed, [j][i], which pairs the columns that a
+// lane has.
 
 // Byte of element (row, column) of a 64 x 64 bf16 matrix whose 128-byte rows
 // are swizzled in 16-byte pieces, as the tensor cores' descriptors expect.
@@ -102,33 +120,68 @@ __device__ __forceinline__ int dc_swizzled(int row, int col)
     return row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
 }
 
+constexpr int DC_HEADS = 4;                     // value heads whose gates are staged at once, one a warp
+constexpr int DC_AST = DC_ROWS + 8;             // columns of a row of A in shared memory
+constexpr int DC_TST = 24;                      // columns of a row of a diagonal block
+
 template <int DK>
 struct DcPrepSmem {
-    uint16_t k[DC_ROWS][DK + 8], q[DC_ROWS][DK + 8];
-    float a[DC_ROWS][DC_ROWS + 4];
-    float rk[DC_ROWS], rq[DC_ROWS], beta[DC_ROWS], g_hi[DC_ROWS], g_lo[DC_ROWS];
-    int seq, first, rows;
+    union {
+        struct {
+            uint16_t k[DC_ROWS][DK + 8], q[DC_ROWS][DK + 8];
+        } in;
+        struct {
+            uint16_t a_hi[DC_ROWS][DC_AST], a_lo[DC_ROWS][DC_AST];  // below the diagonal blocks
+            uint16_t t_hi[4][16][DC_TST], t_lo[4][16][DC_TST];      // diagonal blocks of (I + A)^-1
+            float d[4][16][20];                                     // diagonal blocks of A
+        } w;
+    } u;
+    float rk[DC_ROWS], rq[DC_ROWS];
+    float beta[DC_HEADS][DC_ROWS], g_hi[DC_HEADS][DC_ROWS], g_lo[DC_HEADS][DC_ROWS];
+    float near[DC_HEADS][DC_ROWS];              // e^(G_i - G_r)
+    float far[DC_HEADS][4][DC_ROWS];            // [row block][j]: e^(G_r - G_j)
+    int seq;
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// Grid: x = R / 64 + B blocks, y = Hv; 128 threads.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// d (two n8 tiles of 16 rows) += a x b over 16 columns, both in two terms.
+__device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&a_hi)[4], const uint32_t (&a_lo)[4],
+                                          const uint32_t (&b_hi)[4], const uint32_t (&b_lo)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        mma_bf16_16816(d[j], a_lo[0], a_lo[1], a_lo[2], a_lo[3], b_hi[2 * j], b_hi[2 * j + 1]);
+        mma_bf16_16816(d[j], a_hi[0], a_hi[1], a_hi[2], a_hi[3], b_lo[2 * j], b_lo[2 * j + 1]);
+        mma_bf16_16816(d[j], a_hi[0], a_hi[1], a_hi[2], a_hi[3], b_hi[2 * j], b_hi[2 * j + 1]);
+    }
+}
+
+// Grid: x = R / 64 + B blocks, y = Hk; 128 threads.
 template <int DK>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams cp)
+__global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkParams cp)
 {
     extern __shared__ __align__(16) uint8_t dc_smem[];
     DcPrepSmem<DK> &sm = *reinterpret_cast<DcPrepSmem<DK> *>(dc_smem);
     const DeltaParams &p = cp.d;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int id = blockIdx.x, hv = blockIdx.y, hk = hv / (p.Hv / p.Hk);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int id = blockIdx.x, hk = blockIdx.y, rep = p.Hv / p.Hk;
     pdl_launch_dependents();
     pdl_wait_prior();
-    // the sequence whose blocks hold this one (its last row decides where
-    // rows are claimed twice, which cu_seqlens must not do)
+    if (id == 0 && hk == 0)
+        for (int i = tid; i < DC_FLAGS / 4; i += 128) cp.flags[i] = 0u;
+    // the sequence whose blocks hold this one (the last such, where rows are
+    // claimed twice, which cu_seqlens must not do)
     if (tid == 0) sm.seq = -1;
     __syncthreads();
     for (int b = tid; b < cp.B; b += 128) {
@@ -147,188 +200,325 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams 
 
     // keys and queries; rows past the sequence's end are zero
     constexpr int PR = DK / 8;                  // 16-byte pieces of a row
-    for (int i = tid; i < DC_ROWS * PR; i += 128) {
-        const int t = i / PR, j = (i % PR) * 8;
-        uint4 kv = make_uint4(0u, 0u, 0u, 0u), qv = kv;
-        if (t < n) {
-            kv = __ldg(reinterpret_cast<const uint4 *>(p.rows.k + (row0 + t) * p.rows.ldk + hk * DK + j));
-            qv = __ldg(reinterpret_cast<const uint4 *>(p.rows.q + (row0 + t) * p.rows.ldq + hk * DK + j));
-        }
-        *reinterpret_cast<uint4 *>(&sm.k[t][j]) = kv;
-        *reinterpret_cast<uint4 *>(&sm.q[t][j]) = qv;
-    }
-    // the running sum of the log decays, kept to more than fp32 (differences
-    // of large sums give the decays between near rows); two rows a lane
-    if (warp == 0) {
-        double g[2];
+    {
+        constexpr int PT = DC_ROWS * PR / 128;  // pieces of a thread
+        uint4 kv[PT], qv[PT];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            float v = t < n ? p.rows.g[(row0 + t) * p.rows.ldg + hv] : 0.f;
-            if (v < DC_MIN_LOG) v = DC_MIN_LOG;
-            g[e] = static_cast<double>(v);
-            sm.beta[t] = t < n ? p.rows.beta[(row0 + t) * p.rows.ldg + hv] : 0.f;
+        for (int u = 0; u < PT; ++u) {
+            const int i = tid + u * 128, t = i / PR, j = (i % PR) * 8;
+            kv[u] = qv[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < n) {
+                kv[u] = __ldg(reinterpret_cast<const uint4 *>(p.rows.k + (row0 + t) * p.rows.ldk + hk * DK + j));
+                qv[u] = __ldg(reinterpret_cast<const uint4 *>(p.rows.q + (row0 + t) * p.rows.ldq + hk * DK + j));
+            }
         }
-        double sum = g[0] + g[1];
-        const double own = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double below = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += below;
-        }
-        const double before = sum - own;
-        const double G[2] = {before + g[0], sum};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float hi = static_cast<float>(G[e]);
-            sm.g_hi[2 * lane + e] = hi;
-            sm.g_lo[2 * lane + e] = static_cast<float>(G[e] - static_cast<double>(hi));
+        for (int u = 0; u < PT; ++u) {
+            const int i = tid + u * 128, t = i / PR, j = (i % PR) * 8;
+            *reinterpret_cast<uint4 *>(&sm.u.in.k[t][j]) = kv[u];
+            *reinterpret_cast<uint4 *>(&sm.u.in.q[t][j]) = qv[u];
         }
     }
     __syncthreads();
-    {   // inverse norms: two threads a row
-        const int t = tid >> 1, c0 = (tid & 1) * (DK / 2);
-        float kk = 0.f, qq = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < DK / 2; ++c) {
-            const float kf = bf16_bits_to_float(sm.k[t][c0 + c]), qf = bf16_bits_to_float(sm.q[t][c0 + c]);
-            kk = fmaf(kf, kf, kk);
-            qq = fmaf(qf, qf, qq);
-        }
-        kk += __shfl_xor_sync(0xFFFFFFFFu, kk, 1);
-        qq += __shfl_xor_sync(0xFFFFFFFFu, qq, 1);
-        if ((tid & 1) == 0) {
-            sm.rk[t] = p.l2norm ? 1.f / sqrtf(kk + GD_L2_EPS) : 1.f;
-            sm.rq[t] = p.scale * (p.l2norm ? 1.f / sqrtf(qq + GD_L2_EPS) : 1.f);
-        }
-    }
-    __syncthreads();
-    // k_i . k_j and q_i . k_j: a warp has 16 rows i of both
-    float ck[8][4], cq[8][4];
+    // k_i . k_j and q_i . k_j for the warp's rows i and j up to their block;
+    // q_i . q_i from the diagonal of the block's q q^T
+    float ck[8][4], cq[8][4], qq[2][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) ck[j][e] = cq[j][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qq[j][e] = 0.f;
     const uint32_t arow = static_cast<uint32_t>(((warp * 16 + (lane & 15)) * (DK + 8) + (lane >> 4) * 8) * 2);
     const uint32_t brow = static_cast<uint32_t>((((lane & 7) + ((lane >> 4) << 3)) * (DK + 8) + ((lane >> 3) & 1) * 8) * 2);
-    const uint32_t k0 = smem_addr(&sm.k[0][0]), q0 = smem_addr(&sm.q[0][0]);
+    {
+        const uint32_t k0 = smem_addr(&sm.u.in.k[0][0]), q0 = smem_addr(&sm.u.in.q[0][0]);
 #pragma unroll
-    for (int s = 0; s < DK / 16; ++s) {
-        uint32_t ak[4], aq[4];
-        ldmatrix_x4(ak, k0 + arow + 32u * s);
-        ldmatrix_x4(aq, q0 + arow + 32u * s);
+        for (int s = 0; s < DK / 16; ++s) {
+            uint32_t ak[4], aq[4], b[4];
+            ldmatrix_x4(ak, k0 + arow + 32u * s);
+            ldmatrix_x4(aq, q0 + arow + 32u * s);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t b[4];
-            ldmatrix_x4(b, k0 + brow + static_cast<uint32_t>(j * 16 * (DK + 8) * 2) + 32u * s);
-            mma_bf16_16816(ck[2 * j], ak[0], ak[1], ak[2], ak[3], b[0], b[1]);
-            mma_bf16_16816(ck[2 * j + 1], ak[0], ak[1], ak[2], ak[3], b[2], b[3]);
-            mma_bf16_16816(cq[2 * j], aq[0], aq[1], aq[2], aq[3], b[0], b[1]);
-            mma_bf16_16816(cq[2 * j + 1], aq[0], aq[1], aq[2], aq[3], b[2], b[3]);
+            for (int j = 0; j < 4; ++j) {
+                if (j > warp) break;
+                ldmatrix_x4(b, k0 + brow + static_cast<uint32_t>(j * 16 * (DK + 8) * 2) + 32u * s);
+                mma_bf16_16816(ck[2 * j], ak[0], ak[1], ak[2], ak[3], b[0], b[1]);
+                mma_bf16_16816(ck[2 * j + 1], ak[0], ak[1], ak[2], ak[3], b[2], b[3]);
+                mma_bf16_16816(cq[2 * j], aq[0], aq[1], aq[2], aq[3], b[0], b[1]);
+                mma_bf16_16816(cq[2 * j + 1], aq[0], aq[1], aq[2], aq[3], b[2], b[3]);
+            }
+            // rows as columns: tile j of the block is rows 8 j .. of it
+            mma_bf16_16816(qq[0], aq[0], aq[1], aq[2], aq[3], aq[0], aq[2]);
+            mma_bf16_16816(qq[1], aq[0], aq[1], aq[2], aq[3], aq[1], aq[3]);
         }
     }
-    uint8_t *out = cp.ws + (static_cast<size_t>(id) * p.Hv + hv) * DC_BLOCK;
+    // the diagonal: row g of tile 0 and row g + 8 of tile 1, columns 2c, 2c + 1
+    if ((g >> 1) == c) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int i = warp * 16 + (lane >> 2) + 8 * h;
-        const float gi = sm.g_hi[i], gl = sm.g_lo[i], bi = sm.beta[i] * sm.rk[i], qi = sm.rq[i];
+        for (int h = 0; h < 2; ++h) {
+            float kk = 0.f;
 #pragma unroll
-        for (int j8 = 0; j8 < 8; ++j8) {
-            float m[2];
-            const int j0 = j8 * 8 + (lane & 3) * 2;
+            for (int j = 0; j < 4; ++j)
+                if (j == warp) kk = (g & 1) ? ck[2 * j + h][2 * h + 1] : ck[2 * j + h][2 * h];
+            const float q2 = (g & 1) ? qq[h][2 * h + 1] : qq[h][2 * h];
+            const int i = warp * 16 + g + 8 * h;
+            sm.rk[i] = p.l2norm ? 1.f / sqrtf(kk + GD_L2_EPS) : 1.f;
+            sm.rq[i] = p.scale * (p.l2norm ? 1.f / sqrtf(q2 + GD_L2_EPS) : 1.f);
+        }
+    }
+    uint8_t *blocks = cp.blocks + (static_cast<size_t>(id) * p.Hv + hk * rep) * DC_BLOCK;
+    const uint32_t a_hi0 = smem_addr(&sm.u.w.a_hi[0][0]), a_lo0 = smem_addr(&sm.u.w.a_lo[0][0]);
+    const uint32_t t_hi0 = smem_addr(&sm.u.w.t_hi[0][0][0]), t_lo0 = smem_addr(&sm.u.w.t_lo[0][0][0]);
+    // a lane's row of ldmatrix: plain (B operand, two n8 tiles) and transposed (A operand)
+    const int b_r = (lane & 7) + ((lane >> 4) << 3), b_c = ((lane >> 3) & 1) * 8;
+    for (int r = 0; r < rep; ++r) {
+        __syncthreads();                        // the inputs, or the last head's matrices, have been read
+        const int e4 = r & (DC_HEADS - 1);
+        if (e4 == 0) {
+            // gates of the next heads, one a warp, two rows a lane.  The
+            // running sum keeps more than fp32: differences of large sums
+            // give the decays between near rows.
+            const int hv = hk * rep + r + warp;
+            if (r + warp < rep) {
+                double gd[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 2 * lane + e;
+                    float v = t < n ? p.rows.g[(row0 + t) * p.rows.ldg + hv] : 0.f;
+                    if (v < DC_MIN_LOG) v = DC_MIN_LOG;
+                    gd[e] = static_cast<double>(v);
+                    sm.beta[warp][t] = t < n ? p.rows.beta[(row0 + t) * p.rows.ldg + hv] : 0.f;
+                }
+                double sum = gd[0] + gd[1];
+                const double own = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double below = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                    if (lane >= o) sum += below;
+                }
+                const double G[2] = {sum - own + gd[0], sum};
+                float hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    hi[e] = static_cast<float>(G[e]);
+                    lo[e] = static_cast<float>(G[e] - static_cast<double>(hi[e]));
+                    sm.g_hi[warp][2 * lane + e] = hi[e];
+                    sm.g_lo[warp][2 * lane + e] = lo[e];
+                }
+                const float end_hi = __shfl_sync(0xFFFFFFFFu, hi[1], 31), end_lo = __shfl_sync(0xFFFFFFFFu, lo[1], 31);
+                float *f = reinterpret_cast<float *>(blocks + static_cast<size_t>(r + warp) * DC_BLOCK + 4 * DC_MAT);
+                float fe[2], fl[2], fq[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // row factors: e^G r_k, e^(G_n - G) r_k, scale e^G r_q
+                    const int t = 2 * lane + e;
+                    const float eg = expf(hi[e] + lo[e]);
+                    fe[e] = t < n ? eg * sm.rk[t] : 0.f;
+                    fl[e] = t < n ? expf((end_hi - hi[e]) + (end_lo - lo[e])) * sm.rk[t] : 0.f;
+                    fq[e] = t < n ? eg * sm.rq[t] : 0.f;
+                    const int own_block = t >> 4;
+#pragma unroll
+                    for (int I = 0; I < 4; ++I) {
+                        const float ref_hi = __shfl_sync(0xFFFFFFFFu, hi[0], 8 * I), ref_lo = __shfl_sync(0xFFFFFFFFu, lo[0], 8 * I);
+                        if (I == own_block) sm.near[warp][t] = expf((hi[e] - ref_hi) + (lo[e] - ref_lo));
+                        if (I > own_block) sm.far[warp][I][t] = expf((ref_hi - hi[e]) + (ref_lo - lo[e])) * sm.rk[t];
+                    }
+                }
+                *reinterpret_cast<float2 *>(f + 2 * lane) = make_float2(fe[0], fe[1]);
+                *reinterpret_cast<float2 *>(f + DC_ROWS + 2 * lane) = make_float2(fl[0], fl[1]);
+                *reinterpret_cast<float2 *>(f + 2 * DC_ROWS + 2 * lane) = make_float2(fq[0], fq[1]);
+                if (lane == 0) f[3 * DC_ROWS] = expf(end_hi + end_lo);
+            }
+            __syncthreads();
+        }
+        uint8_t *out = blocks + static_cast<size_t>(r) * DC_BLOCK;
+        // M, and A: its diagonal blocks in fp32, the rest in two terms
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int il = g + 8 * h, i = warp * 16 + il;
+            const float bi = i < n ? sm.beta[e4][i] * sm.rk[i] : 0.f, qi = i < n ? sm.rq[i] : 0.f;
+            const float near = sm.near[e4][i], bn = bi * near, qn = qi * near;
+            const float gi = sm.g_hi[e4][i], gl = sm.g_lo[e4][i];
+#pragma unroll
+            for (int j8 = 0; j8 < 8; ++j8) {
+                if ((j8 >> 1) > warp) break;
+                const int j0 = j8 * 8 + c * 2;
+                float m[2], a[2];
+                if ((j8 >> 1) < warp) {
+                    const float2 far = *reinterpret_cast<const float2 *>(&sm.far[e4][warp][j0]);
+                    m[0] = cq[j8][2 * h] * (far.x * qn);
+                    m[1] = cq[j8][2 * h + 1] * (far.y * qn);
+                    a[0] = ck[j8][2 * h] * (far.x * bn);
+                    a[1] = ck[j8][2 * h + 1] * (far.y * bn);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = j0 + e;
+                        const float d = j <= i ? expf((gi - sm.g_hi[e4][j]) + (gl - sm.g_lo[e4][j])) * sm.rk[j] : 0.f;
+                        m[e] = j <= i ? cq[j8][2 * h + e] * (d * qi) : 0.f;
+                        a[e] = j < i ? ck[j8][2 * h + e] * (d * bi) : 0.f;
+                    }
+                }
+                if (i >= n) m[0] = m[1] = a[0] = a[1] = 0.f;     // (0 x inf where decays grow)
+                uint32_t hi, lo;
+                split_bf16x2(m[0], m[1], hi, lo);
+                *reinterpret_cast<uint32_t *>(out + 2 * DC_MAT + dc_swizzled(i, j0)) = hi;
+                *reinterpret_cast<uint32_t *>(out + 3 * DC_MAT + dc_swizzled(i, j0)) = lo;
+                if ((j8 >> 1) < warp) {
+                    split_bf16x2(a[0], a[1], hi, lo);
+                    *reinterpret_cast<uint32_t *>(&sm.u.w.a_hi[i][j0]) = hi;
+                    *reinterpret_cast<uint32_t *>(&sm.u.w.a_lo[i][j0]) = lo;
+                } else {
+                    *reinterpret_cast<float2 *>(&sm.u.w.d[warp][il][j0 & 15]) = make_float2(a[0], a[1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane < 16) {
+            // column `lane` of the warp's diagonal block of (I + A)^-1
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+                for (int m = 0; m < i; m += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(&sm.u.w.d[warp][i][m]);
+                    s0 = fmaf(-a.x, t[m], s0);
+                    if (m + 1 < i) s1 = fmaf(-a.y, t[m + 1], s1);
+                    if (m + 2 < i) s0 = fmaf(-a.z, t[m + 2], s0);
+                    if (m + 3 < i) s1 = fmaf(-a.w, t[m + 3], s1);
+                }
+                t[i] = s0 + s1;
+            }
+            const float b = sm.beta[e4][warp * 16 + lane];
+            uint32_t oh[8], ol[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                uint32_t hi, lo;
+                split_bf16x2(t[i], t[i + 1], hi, lo);
+                sm.u.w.t_hi[warp][i][lane] = static_cast<uint16_t>(hi);
+                sm.u.w.t_hi[warp][i + 1][lane] = static_cast<uint16_t>(hi >> 16);
+                sm.u.w.t_lo[warp][i][lane] = static_cast<uint16_t>(lo);
+                sm.u.w.t_lo[warp][i + 1][lane] = static_cast<uint16_t>(lo >> 16);
+                split_bf16x2(t[i] * b, t[i + 1] * b, oh[i / 2], ol[i / 2]);
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = j0 + e;
-                float d = 0.f;
-                if (j <= i && i < n) d = expf((gi - sm.g_hi[j]) + (gl - sm.g_lo[j])) * sm.rk[j];
-                m[e] = j <= i && i < n ? cq[j8][2 * h + e] * d * qi : 0.f;
-                sm.a[i][j] = j < i && i < n ? ck[j8][2 * h + e] * d * bi : 0.f;
+                const int at = dc_swizzled(warp * 16 + lane, warp * 16 + 8 * e);
+                *reinterpret_cast<uint4 *>(out + at) = make_uint4(oh[4 * e], oh[4 * e + 1], oh[4 * e + 2], oh[4 * e + 3]);
+                *reinterpret_cast<uint4 *>(out + DC_MAT + at) = make_uint4(ol[4 * e], ol[4 * e + 1], ol[4 * e + 2], ol[4 * e + 3]);
             }
-            uint32_t hi, lo;
-            split_bf16x2(m[0], m[1], hi, lo);
-            *reinterpret_cast<uint32_t *>(out + 2 * DC_MAT + dc_swizzled(i, j0)) = hi;
-            *reinterpret_cast<uint32_t *>(out + 3 * DC_MAT + dc_swizzled(i, j0)) = lo;
         }
-    }
-    if (tid < DC_ROWS) {
-        // row factors: e^G r_k, e^(G_n - G) r_k, scale e^G r_q; the block's decay
-        float *f = reinterpret_cast<float *>(out + 4 * DC_MAT);
-        const float g = sm.g_hi[tid], gl = sm.g_lo[tid], e = expf(g + gl);
-        const float last = expf((sm.g_hi[DC_ROWS - 1] - g) + (sm.g_lo[DC_ROWS - 1] - gl));
-        f[tid] = tid < n ? e * sm.rk[tid] : 0.f;
-        f[DC_ROWS + tid] = tid < n ? last * sm.rk[tid] : 0.f;
-        f[2 * DC_ROWS + tid] = tid < n ? e * sm.rq[tid] : 0.f;
-        if (tid == 0) f[3 * DC_ROWS] = expf(sm.g_hi[DC_ROWS - 1] + sm.g_lo[DC_ROWS - 1]);
-    }
-    __syncthreads();
-    if (tid < DC_ROWS) {
-        // column tid of (I + A)^-1 by forward substitution, in registers
-        float t[DC_ROWS];
-#pragma unroll
-        for (int i = 0; i < DC_ROWS; ++i) {
-            float s0 = i == tid ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-            for (int m = 0; m + 3 < i; m += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&sm.a[i][m]);
-                s0 = fmaf(-a.x, t[m], s0);
-                s1 = fmaf(-a.y, t[m + 1], s1);
-                s2 = fmaf(-a.z, t[m + 2], s2);
-                s3 = fmaf(-a.w, t[m + 3], s3);
+        __syncthreads();
+        if (warp < 3) {
+            // column block J = warp of T below its diagonal block, transposed
+            const int J = warp;
+            uint32_t th[4][4], tl[4][4];        // [row block K]: T_KJ^T as an A operand
+            {
+                const uint32_t at = static_cast<uint32_t>(((J * 16 + (lane & 7) + ((lane >> 4) << 3)) * DC_TST + ((lane >> 3) & 1) * 8) * 2);
+                ldmatrix_x4_trans(th[0], t_hi0 + at);
+                ldmatrix_x4_trans(tl[0], t_lo0 + at);
             }
 #pragma unroll
-            for (int m = i & ~3; m < i; ++m) s0 = fmaf(-sm.a[i][m], t[m], s0);
-            t[i] = (s0 + s1) + (s2 + s3);
-        }
-        const float b = sm.beta[tid];
+            for (int d = 1; d < 4; ++d) {       // row block I = J + d
+                const int I = J + d;
+                if (I > 3) break;
+                float x[2][4];
 #pragma unroll
-        for (int i = 0; i < DC_ROWS; ++i) {
-            uint32_t hi, lo;
-            split_bf16x2(t[i] * b, 0.f, hi, lo);
-            *reinterpret_cast<uint16_t *>(out + dc_swizzled(i, tid)) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t *>(out + DC_MAT + dc_swizzled(i, tid)) = static_cast<uint16_t>(lo);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[j][e] = 0.f;
+                uint32_t bh[4], bl[4];
+#pragma unroll
+                for (int k = 0; k < d; ++k) {   // K = J + k
+                    const uint32_t at = static_cast<uint32_t>(((16 * I + b_r) * DC_AST + 16 * (J + k) + b_c) * 2);
+                    ldmatrix_x4(bh, a_hi0 + at);
+                    ldmatrix_x4(bl, a_lo0 + at);
+                    mma_split(x, th[k], tl[k], bh, bl);
+                }
+                uint32_t xh[4], xl[4];
+                split_bf16x2(-x[0][0], -x[0][1], xh[0], xl[0]);
+                split_bf16x2(-x[0][2], -x[0][3], xh[1], xl[1]);
+                split_bf16x2(-x[1][0], -x[1][1], xh[2], xl[2]);
+                split_bf16x2(-x[1][2], -x[1][3], xh[3], xl[3]);
+                const uint32_t at = static_cast<uint32_t>(((I * 16 + b_r) * DC_TST + b_c) * 2);
+                ldmatrix_x4(bh, t_hi0 + at);
+                ldmatrix_x4(bl, t_lo0 + at);
+                float y[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[j][e] = 0.f;
+                mma_split(y, xh, xl, bh, bl);
+                if (d < 3) {
+                    split_bf16x2(y[0][0], y[0][1], th[d][0], tl[d][0]);
+                    split_bf16x2(y[0][2], y[0][3], th[d][1], tl[d][1]);
+                    split_bf16x2(y[1][0], y[1][1], th[d][2], tl[d][2]);
+                    split_bf16x2(y[1][2], y[1][3], th[d][3], tl[d][3]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 16 * J + g + 8 * h;
+                    const float b = sm.beta[e4][j];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t hi, lo;
+                        split_bf16x2(y[t][2 * h] * b, y[t][2 * h + 1] * b, hi, lo);
+                        const int o = dc_swizzled(j, 16 * I + 8 * t + 2 * c);
+                        *reinterpret_cast<uint32_t *>(out + o) = hi;
+                        *reinterpret_cast<uint32_t *>(out + DC_MAT + o) = lo;
+                    }
+                }
+            }
         }
     }
 }
 
 // ----------------------------------------------------------------- scan
 //
-// One CTA per head and sequence.  Everything is transposed, with the value
-// dimension on the tensor memory's lanes (state row l on lane l), so that the
-// state, r and u are A operands in tensor memory and the keys, queries, T and
-// M are B operands in shared memory exactly as they are loaded.
+// Everything is transposed, with the value dimension on the tensor memory's
+// lanes (state row l on lane l), so that the state, r and u are A operands in
+// tensor memory and the keys, queries, T and M are B operands in shared
+// memory exactly as they are loaded.  Tensor memory, in columns:
 //
-//   phase  product                               accumulator
-//   P      S (2 terms) x K                       X
-//   O      S (2) x Q                             Y
-//   U      r (2) x T (2), without lo x lo        S_hi
-//   M      u (2) x M (2), without lo x lo        Y, after scaling its columns
-//   D      u' (2) x K, 64 keys' columns each     S_hi and X
+//   phase  product                              accumulator
+//   P      S (2 terms, 0..127) x K              P  128..191
+//   O      S x Q                                Y  320..383 or 384..447
+//   U      r (2, 192..255) x T (2)              U  256..319
+//   D      u' (2, 0..63 over S) x K             D  128..255 (over P and r)
+//   M      u (2, 448..511) x M (2)              Y, after scaling its columns
 //
-// Warps 0-7 convert: warp w has lanes 32 (w & 3) .. + 31, half w >> 2 of the
-// columns; the state's fp32 values stay in their registers.  Warp 8 issues
-// the loads and the products.  Tensor memory: S_hi, S_lo (64 columns each,
-// the state's two terms; later u's accumulator and u''s two terms), X (64: P,
-// then r's two terms, then u's, then the second half of D) and Y (64): 256
-// columns and 98 KB of shared memory, so that two CTAs share an SM and one
-// computes while the other converts.
+// (of a product of two two-term factors lo x lo is left out).  Sixteen warps
+// convert between the products: warp w has lanes 32 (w & 3) .. + 31 and a
+// quarter w >> 2 of the columns; the state's fp32 values stay in their
+// registers.  Warp 16 issues the loads, two blocks ahead, and the products.
+// The chain of a block is P, r, U, u', D, S; outputs are off it.
+//
+// Work.  The chains of all heads and sequences are laid end to end and cut
+// into equal parts, at least as long as the longest chain, one for each CTA.
+// A chain that a cut divides has its first blocks at the start of the later
+// CTA's part -- which runs them at once -- and its last ones at the end of
+// the earlier CTA's, which takes the state over when it gets there: with 192
+// chains of equal length on 152 SMs the whole takes 1.26 chains' time, not
+// two.  A CTA waits for CTAs of lower blockIdx only.
 
-constexpr int DS_THREADS = 288;
-constexpr uint32_t DS_COLS = 256;
-constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_X = 128, DS_Y = 192;
+constexpr int DS_WARPS = 16;                    // converting warps
+constexpr int DS_THREADS = DS_WARPS * 32 + 32;
+constexpr uint32_t DS_COLS = 512;
+constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_Y = 320, DS_U1 = 448;
 
 template <int DK>
 struct DsSmem {                                 // from a 1024-byte boundary
     static constexpr int TILE = DC_ROWS * DK * 2;   // keys or queries: DK / 64 boxes of [64 rows][128 bytes]
-    static constexpr int K = 0;                 // two buffers
-    static constexpr int Q = K + 2 * TILE;
-    static constexpr int MATS = Q + TILE;       // T hi, T lo, M hi, M lo
-    static constexpr int V = MATS + 4 * DC_MAT; // [64][dv]
-    static constexpr int F = V + DC_ROWS * 128 * 2;     // two buffers of row factors
-    static constexpr int BARS = F + 2 * DC_FACTORS;
+    static constexpr int K = 0, Q = TILE, MATS = 2 * TILE, F = MATS + 4 * DC_MAT, V = F + DC_FACTORS;   // V [64][dv]
+    static constexpr int STAGE = V + DC_ROWS * 128 * 2;
+    static constexpr int BARS = 2 * STAGE;
     static constexpr int BYTES = BARS + 256;
 };
 
-enum { B_K0, B_K1, B_F0, B_F1, B_V, B_Q, B_T, B_M, B_SREADY, B_RREADY, B_UREADY, B_YFREE, B_P, B_O, B_U, B_MO, B_D, B_COUNT };
+enum { B_FULL0, B_FULL1, B_P, B_O, B_U, B_D, B_M, B_SREADY, B_RREADY, B_UREADY, B_YFREE0, B_YFREE1, B_COUNT };
 
 constexpr uint32_t ds_idesc(int n, bool b_mn)
 {
@@ -350,8 +540,79 @@ struct DsWait {
     }
 };
 
+// A CTA's part of the chains: segments of one head of one sequence each.
+struct DsWalk {
+    const DeltaChunkParams *cp;
+    int pos, stop, lo;                          // next place, end and start of the part
+    int b, first;                               // the sequence of `pos` and its first place
+    // the current segment: blocks c0 .. c1 - 1 of head hv of sequence b
+    int begin, end, blocks, slot, hv, c0, c1;
+    bool takes, gives;                          // another CTA ran the blocks before, runs those after
+
+    __device__ __forceinline__ int blocks_of(int s, int &bg, int &en, int &sl) const
+    {
+        gd_range(cp->cu, cp->R, s, bg, en);
+        sl = cp->d.state_idx ? cp->d.state_idx[s] : s;
+        return sl < 0 || sl >= cp->d.n_slots ? 0 : (en - bg + DC_ROWS - 1) / DC_ROWS;
+    }
+    // Part k of `parts` (whole warps call it).
+    __device__ __forceinline__ void start(const DeltaChunkParams *c, int k, int parts)
+    {
+        cp = c;
+        const int lane = threadIdx.x & 31, Hv = cp->d.Hv;
+        int total = 0, most = 0, bg, en, sl;
+        for (int s = lane; s < cp->B; s += 32) {
+            const int nb = blocks_of(s, bg, en, sl);
+            total += nb * Hv;
+            most = max(most, nb);
+        }
+        total = __reduce_add_sync(0xFFFFFFFFu, total);
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        const int cap = max(most, (total + parts - 1) / parts);
+        // (k cap may be far past the end)
+        lo = static_cast<int>(min(static_cast<long long>(k) * cap, static_cast<long long>(total)));
+        stop = min(total, lo + cap);
+        pos = lo;
+        b = first = 0;
+        for (int s0 = 0; s0 < cp->B && lo < stop; s0 += 32) {
+            const int s = s0 + lane;
+            const int mine = s < cp->B ? blocks_of(s, bg, en, sl) * Hv : 0;
+            int run = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int below = __shfl_up_sync(0xFFFFFFFFu, run, o);
+                if (lane >= o) run += below;
+            }
+            const unsigned past = __ballot_sync(0xFFFFFFFFu, first + run > pos);
+            if (past) {
+                const int w = __ffs(past) - 1;
+                b = s0 + w;
+                first += __shfl_sync(0xFFFFFFFFu, run - mine, w);
+                break;
+            }
+            first += __shfl_sync(0xFFFFFFFFu, run, 31);
+        }
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (pos >= stop) return false;
+        while ((blocks = blocks_of(b, begin, end, slot)) * cp->d.Hv <= pos - first) {
+            first += blocks * cp->d.Hv;
+            ++b;
+        }
+        hv = (pos - first) / blocks;
+        const int s = first + hv * blocks, e = s + blocks;
+        takes = e > stop;                       // the CTA of the next part has the first e - stop blocks
+        gives = pos > s;                        // (pos == lo) the CTA of the part before has the rest
+        c0 = takes ? e - stop : 0;
+        c1 = gives ? e - pos : blocks;
+        pos = min(e, stop);
+        return true;
+    }
+};
+
 template <int DK>
-__global__ void __launch_bounds__(DS_THREADS, 2)
+__global__ void __launch_bounds__(DS_THREADS, 1)
 delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmV)
 {
@@ -359,7 +620,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
     using L = DsSmem<DK>;
     const DeltaParams &p = cp.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hv = blockIdx.x, b = blockIdx.y, hk = hv / (p.Hv / p.Hk);
+    const int part = gridDim.x - 1 - blockIdx.x;
     const uint32_t base = smem_addr(ds_smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(ds_smem + L::BARS);
     volatile int *flag = reinterpret_cast<volatile int *>(bars + B_COUNT);
@@ -372,11 +633,11 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_SREADY && i <= B_YFREE ? 8 : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_SREADY ? DS_WARPS : 1);
         *flag = 0;
         fence_barrier_init();
     }
-    if (warp == 8) {
+    if (warp == DS_WARPS) {
         tmem_alloc(smem_addr(const_cast<uint32_t *>(slot_tm)), DS_COLS);
         tmem_relinquish();
     }
@@ -386,300 +647,305 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
     const uint32_t tmem = *slot_tm;
     pdl_launch_dependents();
     pdl_wait_prior();
+    DsWalk w;
+    w.start(&cp, part, gridDim.x);
 
-    int begin, end;
-    gd_range(cp.cu, cp.R, b, begin, end);
-    const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
-    const int chunks = slot < 0 ? 0 : (end - begin + DC_ROWS - 1) / DC_ROWS;
-    const uint8_t *blocks = cp.ws + (static_cast<size_t>(dc_base(begin, b)) * p.Hv + hv) * DC_BLOCK;
-    const size_t block_step = static_cast<size_t>(p.Hv) * DC_BLOCK;
-
-    if (warp == 8) {
+    if (warp == DS_WARPS) {
         // ------------------------------------------------ loads and products
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-        auto load_rows = [&](const CUtensorMap &m, int dst, int bar_i, int c, int col, int width, bool swizzled) {
-            // 64 rows from block c; rows past the end are another sequence's
-            mbar_arrive_expect_tx(bar(bar_i), static_cast<uint32_t>(DC_ROWS * width * 2));
-            if (swizzled) {
+        // loads run ahead on a walk of their own, step lt into stage lt & 1
+        DsWalk lw = w;
+        bool left = lw.next();
+        int lc = left ? lw.c0 : 0, lt = 0;
+        auto load = [&]() {
+            if (!left) return;
+            if (lane == 0) {
+                const uint32_t st = base + static_cast<uint32_t>((lt & 1) * L::STAGE), fb = bar(B_FULL0 + (lt & 1));
+                const int row = lw.begin + lc * DC_ROWS, hk = lw.hv / (p.Hv / p.Hk);
+                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(2 * L::TILE + DC_BLOCK + DC_ROWS * p.dv * 2));
 #pragma unroll
                 for (int j = 0; j < DK / 64; ++j)
-                    tma_load_2d(base + dst + j * DC_ROWS * 128, &m, col + 64 * j, begin + c * DC_ROWS, bar(bar_i), keep);
-            } else {
-                tma_load_2d(base + dst, &m, col, begin + c * DC_ROWS, bar(bar_i), once);
+                    tma_load_2d(st + L::K + j * DC_ROWS * 128, &tmK, hk * DK + 64 * j, row, fb, keep);
+                tma_load_2d(st + L::V, &tmV, lw.hv * p.dv, row, fb, once);
+                const uint8_t *blk = cp.blocks + (static_cast<size_t>(dc_base(lw.begin, lw.b) + lc) * p.Hv + lw.hv) * DC_BLOCK;
+                bulk_g2s(st + L::MATS, blk, DC_BLOCK, fb, once);
+#pragma unroll
+                for (int j = 0; j < DK / 64; ++j)
+                    tma_load_2d(st + L::Q + j * DC_ROWS * 128, &tmQ, hk * DK + 64 * j, row, fb, keep);
+            }
+            ++lt;
+            if (++lc == lw.c1) {
+                left = lw.next();
+                lc = left ? lw.c0 : 0;
             }
         };
-        auto load_k = [&](int c) { load_rows(tmK, L::K + (c & 1) * L::TILE, B_K0 + (c & 1), c, hk * DK, DK, true); };
-        auto load_f = [&](int c) {
-            mbar_arrive_expect_tx(bar(B_F0 + (c & 1)), DC_FACTORS);
-            bulk_g2s(base + L::F + (c & 1) * DC_FACTORS, blocks + c * block_step + 4 * DC_MAT, DC_FACTORS,
-                     bar(B_F0 + (c & 1)), once);
-        };
-        auto load_v = [&](int c) { load_rows(tmV, L::V, B_V, c, hv * p.dv, p.dv, false); };
-        auto load_q = [&](int c) { load_rows(tmQ, L::Q, B_Q, c, hk * DK, DK, true); };
-        auto load_mats = [&](int c, int which) {    // 0: T, 1: M
-            mbar_arrive_expect_tx(bar(B_T + which), 2 * DC_MAT);
-            bulk_g2s(base + L::MATS + which * 2 * DC_MAT, blocks + c * block_step + which * 2 * DC_MAT, 2 * DC_MAT,
-                     bar(B_T + which), once);
-        };
-        if (lane == 0 && chunks > 0) {
-            load_k(0);
-            load_f(0);
-            load_v(0);
-            load_q(0);
-            load_mats(0, 0);
-            load_mats(0, 1);
-            if (chunks > 1) {
-                load_k(1);
-                load_f(1);
-            }
-        }
-        __syncwarp();
-        const uint32_t shi = tmem + DS_SHI, slo = tmem + DS_SLO, x = tmem + DS_X, y = tmem + DS_Y;
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = static_cast<uint32_t>(c);
-            const uint32_t kb = base + static_cast<uint32_t>(L::K + (c & 1) * L::TILE), qb = base + L::Q;
-            const bool more = c + 1 < chunks;
-            // P: S x K
-            wait(bar(B_SREADY), ph);
-            if (lane == 0 && c > 0 && more) {       // block c - 1 is done with its keys and factors
-                load_k(c + 1);
-                load_f(c + 1);
-            }
-            wait(bar(B_K0 + (c & 1)), ph >> 1);
-            __syncwarp();
-            tc_fence_after_sync();
+        load();
+        load();
+        uint32_t t = 0;
+        while (w.next())
+            for (int c = w.c0; c < w.c1; ++c, ++t) {
+                const uint32_t st = base + (t & 1) * L::STAGE, kb = st + L::K, qb = st + L::Q, mb = st + L::MATS;
+                const uint32_t y = tmem + DS_Y + 64 * (t & 1);
+                // P: S x K
+                wait(bar(B_SREADY), t);
+                wait(bar(B_FULL0 + (t & 1)), t >> 1);
+                __syncwarp();
+                tc_fence_after_sync();
 #pragma unroll
-            for (int s = 0; s < DK / 16; ++s) {
-                const uint64_t d = desc_k_sw128(kb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
-                tc_mma_f16_ts_warp(x, shi + 8 * s, d, ds_idesc(64, false), s > 0);
-                tc_mma_f16_ts_warp(x, slo + 8 * s, d, ds_idesc(64, false), 1);
-            }
-            tc_commit_warp(bar(B_P));
-            // O: S x Q
-            if (c > 0) wait(bar(B_YFREE), ph - 1);
-            wait(bar(B_Q), ph);
-            __syncwarp();
-            tc_fence_after_sync();
+                for (int s = 0; s < DK / 16; ++s) {
+                    const uint64_t d = desc_k_sw128(kb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 8 * s, d, ds_idesc(64, false), s > 0);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SLO + 8 * s, d, ds_idesc(64, false), 1);
+                }
+                tc_commit_warp(bar(B_P));
+                // O: S x Q
+                if (t > 1) wait(bar(B_YFREE0 + (t & 1)), (t >> 1) - 1);
+                __syncwarp();
+                tc_fence_after_sync();
 #pragma unroll
-            for (int s = 0; s < DK / 16; ++s) {
-                const uint64_t d = desc_k_sw128(qb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
-                tc_mma_f16_ts_warp(y, shi + 8 * s, d, ds_idesc(64, false), s > 0);
-                tc_mma_f16_ts_warp(y, slo + 8 * s, d, ds_idesc(64, false), 1);
-            }
-            tc_commit_warp(bar(B_O));
-            // U: r x T; T is lower triangular, so step s (rows 16 s .. of r)
-            // reaches the rows from 16 s on only
-            wait(bar(B_RREADY), ph);
-            if (lane == 0 && more) load_v(c + 1);
-            wait(bar(B_O), ph);                     // S_hi is free
-            if (lane == 0 && more) load_q(c + 1);
-            wait(bar(B_T), ph);
-            __syncwarp();
-            tc_fence_after_sync();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t off = static_cast<uint32_t>(16 * s * 128 + 32 * s);
-                const uint64_t hi = desc_k_sw128(base + L::MATS + off), lo = desc_k_sw128(base + L::MATS + DC_MAT + off);
-                const uint32_t id = ds_idesc(64 - 16 * s, false), d = shi + 16 * s;
-                tc_mma_f16_ts_warp(d, x + 8 * s, hi, id, s > 0);
-                tc_mma_f16_ts_warp(d, x + 32 + 8 * s, hi, id, 1);
-                tc_mma_f16_ts_warp(d, x + 8 * s, lo, id, 1);
-            }
-            tc_commit_warp(bar(B_U));
-            // M: u x M on top of the scaled S x Q
-            wait(bar(B_UREADY), ph);
-            if (lane == 0 && more) load_mats(c + 1, 0);
-            wait(bar(B_M), ph);
-            __syncwarp();
-            tc_fence_after_sync();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t off = static_cast<uint32_t>(16 * s * 128 + 32 * s);
-                const uint32_t id = ds_idesc(64 - 16 * s, false), d = y + 16 * s;
-                const uint64_t hi = desc_k_sw128(base + L::MATS + 2 * DC_MAT + off), lo = desc_k_sw128(base + L::MATS + 3 * DC_MAT + off);
-                tc_mma_f16_ts_warp(d, x + 8 * s, hi, id, 1);
-                tc_mma_f16_ts_warp(d, x + 32 + 8 * s, hi, id, 1);
-                tc_mma_f16_ts_warp(d, x + 8 * s, lo, id, 1);
-            }
-            tc_commit_warp(bar(B_MO));
-            // D: u' x K, the key columns 0..63, then 64..127 over u
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint64_t d = desc_mn_sw128(kb + s * 2048);
-                tc_mma_f16_ts_warp(shi, slo + 8 * s, d, ds_idesc(64, true), s > 0);
-                tc_mma_f16_ts_warp(shi, slo + 32 + 8 * s, d, ds_idesc(64, true), 1);
-            }
-            wait(bar(B_MO), ph);
-            if (lane == 0 && more) load_mats(c + 1, 1);
-            __syncwarp();
-            if (DK == 128) {
+                for (int s = 0; s < DK / 16; ++s) {
+                    const uint64_t d = desc_k_sw128(qb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
+                    tc_mma_f16_ts_warp(y, tmem + DS_SHI + 8 * s, d, ds_idesc(64, false), s > 0);
+                    tc_mma_f16_ts_warp(y, tmem + DS_SLO + 8 * s, d, ds_idesc(64, false), 1);
+                }
+                tc_commit_warp(bar(B_O));
+                // block t - 1 is done with its stage: its products, and (as
+                // SREADY says) its row factors
+                if (t > 0) {
+                    wait(bar(B_M), t - 1);
+                    load();
+                }
+                // U: r x T; step s (rows 16 s .. of r) reaches the rows from 16 s on only
+                wait(bar(B_RREADY), t);
+                __syncwarp();
                 tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const uint64_t d = desc_mn_sw128(kb + DC_ROWS * 128 + s * 2048);
-                    tc_mma_f16_ts_warp(x, slo + 8 * s, d, ds_idesc(64, true), s > 0);
-                    tc_mma_f16_ts_warp(x, slo + 32 + 8 * s, d, ds_idesc(64, true), 1);
+                    const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
+                    const uint64_t hi = desc_mn_sw128(mb + off), lo = desc_mn_sw128(mb + DC_MAT + off);
+                    const uint32_t id = ds_idesc(64 - 16 * s, true), d = tmem + DS_U + 16 * s, r = tmem + DS_R + 8 * s;
+                    tc_mma_f16_ts_warp(d, r, hi, id, s > 0);
+                    tc_mma_f16_ts_warp(d, r + 32, hi, id, 1);
+                    tc_mma_f16_ts_warp(d, r, lo, id, 1);
                 }
+                tc_commit_warp(bar(B_U));
+                // D: u' x K
+                wait(bar(B_UREADY), t);
+                __syncwarp();
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint64_t d = desc_mn_sw128(kb + s * 2048);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 8 * s, d, ds_idesc(DK, true), s > 0);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 32 + 8 * s, d, ds_idesc(DK, true), 1);
+                }
+                tc_commit_warp(bar(B_D));
+                // M: u x M on top of the scaled S x Q
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
+                    const uint64_t hi = desc_k_sw128(mb + 2 * DC_MAT + off), lo = desc_k_sw128(mb + 3 * DC_MAT + off);
+                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = y + 16 * s, u = tmem + DS_U1 + 8 * s;
+                    tc_mma_f16_ts_warp(d, u, hi, id, 1);
+                    tc_mma_f16_ts_warp(d, u + 32, hi, id, 1);
+                    tc_mma_f16_ts_warp(d, u, lo, id, 1);
+                }
+                tc_commit_warp(bar(B_M));
             }
-            tc_commit_warp(bar(B_D));
-        }
     } else {
         // ------------------------------------------------ conversions
         const int q = warp & 3, h = warp >> 2, l = 32 * q + lane;
         const bool live = l < p.dv;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
-        constexpr int SC = DK / 2;              // state columns of a thread
-        float st[SC];
-        const size_t srow = ((static_cast<size_t>(slot < 0 ? 0 : slot) * p.Hv + hv) * p.dv + (live ? l : 0)) * DK + h * SC;
-#pragma unroll
-        for (int i = 0; i < SC; i += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live && slot >= 0 && !cp.zero_init) v = *reinterpret_cast<const float4 *>(p.state + srow + i);
-            st[i] = v.x;
-            st[i + 1] = v.y;
-            st[i + 2] = v.z;
-            st[i + 3] = v.w;
-        }
-        uint16_t *o = p.o + static_cast<long long>(begin) * p.ldo + static_cast<long long>(hv) * p.dv;
+        constexpr int SC = DK / 4;              // state columns of a thread
+        constexpr int NTHR = DS_WARPS * 32;
+        float s[SC];
         auto arrive = [&](int i) {              // this warp's tensor memory accesses are done
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(i));
         };
-        auto pair_sync = [&]() {                // the two warps of these lanes
-            tc_fence_before_sync();
-            named_bar_sync(1 + q, 64);
+
+        // sequences without work: empty ones that start from zero, inactive
+        // entries (their outputs are zero)
+        for (int b = part; b < cp.B; b += gridDim.x) {
+            int bg, en, sl;
+            const int nb = w.blocks_of(b, bg, en, sl);
+            if (sl >= p.n_slots && threadIdx.x == 0) atomicOr(p.err, 8);
+            if (sl < 0 || sl >= p.n_slots) {
+                const int per = p.Hv * p.dv / 8;
+                for (long long i = threadIdx.x; i < static_cast<long long>(en - bg) * per; i += NTHR)
+                    *reinterpret_cast<uint4 *>(p.o + (bg + i / per) * p.ldo + (i % per) * 8) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (nb == 0 && cp.zero_init) {
+                const long long per = static_cast<long long>(p.Hv) * p.dv * DK;
+                for (long long i = threadIdx.x; i < per; i += NTHR) p.state[sl * per + i] = 0.f;
+            }
+        }
+
+        // outputs of step t, n rows from o: this thread's rows 16 h .. + 15 of
+        // value l; two lanes trade so that each stores pairs of values
+        auto store_out = [&](uint32_t t, uint16_t *o, int n) {
+            wait(bar(B_M), t);
             tc_fence_after_sync();
-        };
-        // outputs of block c: this thread's rows 32 h .. + 31 of value l;
-        // two lanes trade so that each stores pairs of values
-        auto store_out = [&](int c) {
-            wait(bar(B_MO), static_cast<uint32_t>(c));
-            tc_fence_after_sync();
-            uint32_t v[32];
-            tmem_ld32(lanes + DS_Y + 32 * h, v);
+            uint32_t v[16];
+            tmem_ld<16>(lanes + DS_Y + 64 * (t & 1) + 16 * h, v);
             tmem_wait_ld();
-            arrive(B_YFREE);
-            const int n = min(DC_ROWS, end - begin - c * DC_ROWS);
-            uint16_t *oc = o + static_cast<long long>(c) * DC_ROWS * p.ldo + (l & ~1);
+            arrive(B_YFREE0 + (t & 1));
             const bool odd = lane & 1;
+            o += (16 * h + (odd ? 1 : 0)) * p.ldo + (l & ~1);
+            n -= 16 * h + (odd ? 1 : 0);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
                 const float give = __uint_as_float(odd ? v[i] : v[i + 1]), own = __uint_as_float(odd ? v[i + 1] : v[i]);
                 const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-                const int t = 32 * h + i + (odd ? 1 : 0);
-                if (live && t < n) *reinterpret_cast<uint32_t *>(oc + t * p.ldo) = odd ? pack_bf16x2(got, own) : pack_bf16x2(own, got);
+                if (live && i < n) *reinterpret_cast<uint32_t *>(o) = odd ? pack_bf16x2(got, own) : pack_bf16x2(own, got);
+                o += 2 * p.ldo;
             }
         };
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = static_cast<uint32_t>(c);
-            const int n = min(DC_ROWS, end - begin - c * DC_ROWS);
-            if (n < DC_ROWS) {
-                // keys past the end are another sequence's and may be NaN: zero
-                wait(bar(B_K0 + (c & 1)), ph >> 1);
-                uint8_t *kt = ds_smem + L::K + (c & 1) * L::TILE;
-                for (int i = threadIdx.x; i < (DC_ROWS - n) * (DK / 8); i += 256) {
-                    const int t = n + i / (DK / 8), j = i % (DK / 8);   // swizzled pieces stay within their row
-                    *reinterpret_cast<uint4 *>(kt + (j >> 3) * DC_ROWS * 128 + t * 128 + (j & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async();
-            }
-            {   // the state's two terms
-                uint32_t hi[SC / 2], lo[SC / 2];
-#pragma unroll
-                for (int i = 0; i < SC / 2; ++i) split_bf16x2(st[2 * i], st[2 * i + 1], hi[i], lo[i]);
-                tmem_st<SC / 2>(lanes + DS_SHI + h * (SC / 2), hi);
-                tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
-                arrive(B_SREADY);
-            }
-            if (c > 0) store_out(c - 1);
-            const float *f = reinterpret_cast<const float *>(ds_smem + L::F + (c & 1) * DC_FACTORS);
-            wait(bar(B_F0 + (c & 1)), ph >> 1);
-            wait(bar(B_V), ph);
-            {   // r = v - e^G r_k (S k)
-                const uint16_t *vt = reinterpret_cast<const uint16_t *>(ds_smem + L::V) + 32 * h * p.dv + (live ? l : 0);
-                wait(bar(B_P), ph);
-                tc_fence_after_sync();
-                uint32_t v[32], hi[16], lo[16];
-                tmem_ld32(lanes + DS_X + 32 * h, v);
-                tmem_wait_ld();
-                pair_sync();                    // both have read P: r goes over it
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float r[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 32 * h + i + e;
-                        r[e] = live && t < n ? fmaf(-f[t], __uint_as_float(v[i + e]), bf16_bits_to_float(vt[(i + e) * p.dv])) : 0.f;
+
+        uint32_t t = 0;
+        while (w.next()) {
+            float *srow = p.state + ((static_cast<size_t>(w.slot) * p.Hv + w.hv) * p.dv + (live ? l : 0)) * DK + h * SC;
+            if (w.takes) {                      // the CTA of the next part hands the state over
+                const uint64_t t0 = global_timer_ns();
+                while (ld_acquire_gpu_u32(cp.flags + part + 1) == 0u)
+                    if (global_timer_ns() - t0 > (*flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) {
+                        *flag = 1;
+                        atomicOr(p.err, 2);
+                        break;
                     }
-                    split_bf16x2(r[0], r[1], hi[i / 2], lo[i / 2]);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < SC; i += 4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (live && (w.takes || !cp.zero_init)) v = __ldcg(reinterpret_cast<const float4 *>(srow + i));
+                s[i] = v.x;
+                s[i + 1] = v.y;
+                s[i + 2] = v.z;
+                s[i + 3] = v.w;
+            }
+            uint16_t *o = p.o + (static_cast<long long>(w.begin) + static_cast<long long>(w.c0) * DC_ROWS) * p.ldo +
+                          static_cast<long long>(w.hv) * p.dv;
+            for (int c = w.c0; c < w.c1; ++c, ++t) {
+                uint8_t *stage = ds_smem + (t & 1) * L::STAGE;
+                const int n = min(DC_ROWS, w.end - w.begin - c * DC_ROWS);
+                if (n < DC_ROWS) {
+                    // keys past the end are another sequence's and may be NaN: zero
+                    wait(bar(B_FULL0 + (t & 1)), t >> 1);
+                    for (int i = threadIdx.x; i < (DC_ROWS - n) * (DK / 8); i += NTHR) {
+                        const int r = n + i / (DK / 8), j = i % (DK / 8);   // swizzled pieces stay within their row
+                        *reinterpret_cast<uint4 *>(stage + L::K + (j >> 3) * DC_ROWS * 128 + r * 128 + (j & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
                 }
-                tmem_st<16>(lanes + DS_X + 16 * h, hi);
-                tmem_st<16>(lanes + DS_X + 32 + 16 * h, lo);
-                arrive(B_RREADY);
-            }
-            {   // scale the columns of S q while r x T runs
-                wait(bar(B_O), ph);
-                tc_fence_after_sync();
-                uint32_t v[32];
-                tmem_ld32(lanes + DS_Y + 32 * h, v);
-                tmem_wait_ld();
+                {   // the state's two terms
+                    uint32_t hi[SC / 2], lo[SC / 2];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[2 * DC_ROWS + 32 * h + i]);
-                tmem_st<32>(lanes + DS_Y + 32 * h, v);
-            }
-            {   // u, and u' = u e^(G_n - G) r_k in two terms
-                wait(bar(B_U), ph);
-                tc_fence_after_sync();
-                uint32_t v[32], w[16], lo[16];
-                tmem_ld32(lanes + DS_SHI + 32 * h, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    split_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), w[i], lo[i]);
-                tmem_st<16>(lanes + DS_X + 16 * h, w);
-                tmem_st<16>(lanes + DS_X + 32 + 16 * h, lo);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 32 * h + 2 * i;
-                    split_bf16x2(__uint_as_float(v[2 * i]) * f[DC_ROWS + t], __uint_as_float(v[2 * i + 1]) * f[DC_ROWS + t + 1], w[i], lo[i]);
+                    for (int i = 0; i < SC / 2; ++i) split_bf16x2(s[2 * i], s[2 * i + 1], hi[i], lo[i]);
+                    tmem_st<SC / 2>(lanes + DS_SHI + h * (SC / 2), hi);
+                    tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
+                    arrive(B_SREADY);
                 }
-                tmem_st<16>(lanes + DS_SLO + 16 * h, w);
-                tmem_st<16>(lanes + DS_SLO + 32 + 16 * h, lo);
-                arrive(B_UREADY);
-            }
-            {   // S <- e^(G_n) S + D
-                const float decay = f[3 * DC_ROWS];
-                wait(bar(B_D), ph);
-                tc_fence_after_sync();
-                const uint32_t from = DK == 128 ? (h ? DS_X : DS_SHI) : DS_SHI + 32 * h;
+                if (c > w.c0) store_out(t - 1, o - DC_ROWS * p.ldo, DC_ROWS);
+                o += DC_ROWS * p.ldo;
+                const float *f = reinterpret_cast<const float *>(stage + L::F);
+                uint32_t v[16], hi[8], lo[8];
+                wait(bar(B_FULL0 + (t & 1)), t >> 1);
+                {   // r = v - e^G r_k (S k)
+                    const uint16_t *vt = reinterpret_cast<const uint16_t *>(stage + L::V) + 16 * h * p.dv + (live ? l : 0);
+                    float val[16];
 #pragma unroll
-                for (int j = 0; j < SC; j += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(lanes + from + j, v);
+                    for (int i = 0; i < 16; ++i) val[i] = bf16_bits_to_float(vt[i * p.dv]);
+                    wait(bar(B_P), t);
+                    tc_fence_after_sync();
+                    tmem_ld<16>(lanes + DS_P + 16 * h, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) st[j + i] = fmaf(decay, st[j + i], __uint_as_float(v[i]));
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(f + 16 * h + i);
+                        val[i] = fmaf(-e.x, __uint_as_float(v[i]), val[i]);
+                        val[i + 1] = fmaf(-e.y, __uint_as_float(v[i + 1]), val[i + 1]);
+                        val[i + 2] = fmaf(-e.z, __uint_as_float(v[i + 2]), val[i + 2]);
+                        val[i + 3] = fmaf(-e.w, __uint_as_float(v[i + 3]), val[i + 3]);
+                    }
+                    const int m = live ? n - 16 * h : 0;
+                    if (m < 16)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i >= m) val[i] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split_bf16x2(val[2 * i], val[2 * i + 1], hi[i], lo[i]);
+                    tmem_st<8>(lanes + DS_R + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_R + 32 + 8 * h, lo);
+                    arrive(B_RREADY);
                 }
-                pair_sync();                    // both have read D: the state's terms go over it
+                {   // scale the columns of S q while r x T runs
+                    wait(bar(B_O), t);
+                    tc_fence_after_sync();
+                    const uint32_t y = lanes + DS_Y + 64 * (t & 1) + 16 * h;
+                    tmem_ld<16>(y, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(f + 2 * DC_ROWS + 16 * h + i);
+                        v[i] = __float_as_uint(__uint_as_float(v[i]) * e.x);
+                        v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) * e.y);
+                        v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) * e.z);
+                        v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) * e.w);
+                    }
+                    tmem_st<16>(y, v);
+                }
+                {   // u' = u e^(G_n - G) r_k, and u
+                    wait(bar(B_U), t);
+                    tc_fence_after_sync();
+                    tmem_ld<16>(lanes + DS_U + 16 * h, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(f + DC_ROWS + 16 * h + i);
+                        split_bf16x2(__uint_as_float(v[i]) * e.x, __uint_as_float(v[i + 1]) * e.y, hi[i / 2], lo[i / 2]);
+                        split_bf16x2(__uint_as_float(v[i + 2]) * e.z, __uint_as_float(v[i + 3]) * e.w, hi[i / 2 + 1], lo[i / 2 + 1]);
+                    }
+                    tmem_st<8>(lanes + DS_SHI + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_SHI + 32 + 8 * h, lo);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), hi[i], lo[i]);
+                    tmem_st<8>(lanes + DS_U1 + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_U1 + 32 + 8 * h, lo);
+                    arrive(B_UREADY);
+                }
+                {   // S <- e^(G_n) S + D
+                    const float decay = f[3 * DC_ROWS];
+                    wait(bar(B_D), t);
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int j = 0; j < SC; j += 16) {
+                        tmem_ld<16>(lanes + DS_P + h * SC + j, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[j + i] = fmaf(decay, s[j + i], __uint_as_float(v[i]));
+                    }
+                }
             }
-        }
-        if (chunks > 0) store_out(chunks - 1);
-        if (slot >= 0) {
-            if (live && (chunks > 0 || cp.zero_init))
+            store_out(t - 1, o - DC_ROWS * p.ldo, min(DC_ROWS, w.end - w.begin - (w.c1 - 1) * DC_ROWS));
+            if (live)
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
-                    *reinterpret_cast<float4 *>(p.state + srow + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
-        } else if (live) {                      // an inactive entry: its outputs are zero
-            for (int t = begin + h; t < end; t += 2, o += 2 * p.ldo) o[h * p.ldo + l] = 0;
+                    *reinterpret_cast<float4 *>(srow + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+            if (w.gives) {                      // the rest of the chain is the CTA's of the part before
+                named_bar_sync(1, NTHR);
+                if (threadIdx.x == 0) red_add_release_gpu(cp.flags + part, 1u);
+            }
         }
     }
-    // every load has landed (each was waited for) and every product is done
-    // (the last commit was waited for by the warps above)
+    // every load has landed and every product is done: the warps above have
+    // waited for each
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == DS_WARPS) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, DS_COLS);
     }

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 
@@ -220,7 +221,7 @@ long long delta_blocks(int R, int B) { return static_cast<long long>(R / DC_ROWS
 bool delta_by_rows(int R, int B) { return R < static_cast<long long>(DC_ROWS) * B; }
 
 template <int DK>
-int delta_chunk_launch(const DeltaChunkParams &p, cudaStream_t stream)
+int delta_chunk_launch(const DeltaChunkParams &p, const DeviceInfo &dev, cudaStream_t stream)
 {
     CUtensorMap tmK, tmQ, tmV;
     const DeltaRows &r = p.d.rows;
@@ -229,10 +230,11 @@ int delta_chunk_launch(const DeltaChunkParams &p, cudaStream_t stream)
     if (rc == SV_OK) rc = encode_rows(&tmQ, r.q, nk, p.R, r.ldq, 64, true);
     if (rc == SV_OK) rc = encode_rows(&tmV, r.v, nv, p.R, r.ldv, p.d.dv, false);
     if (rc != SV_OK) return rc;
-    rc = launch(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(delta_blocks(p.R, p.B)), static_cast<unsigned>(p.d.Hv)),
-                128, sizeof(DcPrepSmem<DK>), stream, p);
+    const long long blocks = delta_blocks(p.R, p.B), parts = std::min<long long>(dev.sms, blocks * p.d.Hv);
+    rc = launch(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.d.Hk)), 128,
+                sizeof(DcPrepSmem<DK>), stream, p);
     if (rc != SV_OK) return rc;
-    return launch(delta_scan_kernel<DK>, dim3(static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(p.B)), DS_THREADS,
+    return launch(delta_scan_kernel<DK>, dim3(static_cast<unsigned>(std::min<long long>(parts, DC_FLAGS / 4))), DS_THREADS,
                   DsSmem<DK>::BYTES, stream, p, tmK, tmQ, tmV);
 }
 
@@ -340,8 +342,7 @@ size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape)
 {
     if (sv::check_delta_shape(shape) != SV_OK || R < 0 || B < 0) return 0;
     if (sv::delta_by_rows(R, B)) return 16;
-    const size_t n = static_cast<size_t>(sv::delta_blocks(R, B)) * static_cast<size_t>(shape->Hv) * sv::DC_BLOCK;
-    return n ? n : 16;
+    return sv::DC_FLAGS + static_cast<size_t>(sv::delta_blocks(R, B)) * static_cast<size_t>(shape->Hv) * sv::DC_BLOCK;
 }
 
 int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
@@ -352,7 +353,7 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     int rc = check_delta_shape(shape);
     if (rc != SV_OK) return rc;
     if (shape->flags & SV_DELTA_COMMIT) return SV_ERR_SHAPE;
-    if (R < 0) return SV_ERR_SHAPE;
+    if (R < 0 || delta_blocks(R, B) * shape->Hv > 0x7FFFFFFF) return SV_ERR_SHAPE;
     if (R > 0 && (rc = check_delta_rows(rows, shape, true)) != SV_OK) return rc;
     if (R > 0 && (rc = check_delta_out(shape, o, ldo)) != SV_OK) return rc;
     rc = check_delta_state(shape, state, state_idx, n_slots, B);
@@ -369,10 +370,11 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     p.cu = cu_seqlens;
     p.R = R;
     p.B = B;
-    p.ws = static_cast<uint8_t *>(ws);
+    p.flags = static_cast<unsigned *>(ws);
+    p.blocks = static_cast<uint8_t *>(ws) + DC_FLAGS;
     p.zero_init = (shape->flags & SV_DELTA_ZERO_INIT) != 0;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (!delta_by_rows(R, B)) return shape->dk == 64 ? delta_chunk_launch<64>(p, cs) : delta_chunk_launch<128>(p, cs);
+    if (!delta_by_rows(R, B)) return shape->dk == 64 ? delta_chunk_launch<64>(p, dev, cs) : delta_chunk_launch<128>(p, dev, cs);
     const dim3 grid(static_cast<unsigned>(p.d.dv / p.d.cols), static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(B));
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(GD_MAX_ROWS, shape->dk, p.d.cols));
     return shape->dk == 64 ? launch(gated_delta_rows_kernel<64>, grid, 4 * p.d.cols, smem, cs, p)

@@ -37,9 +37,9 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr)
 }
 
 // The same tile read across: its rows are the products' K and its 64
-// columns their N.  Eight rows along K are 1024 bytes; a step of 16 rows is
-// 2048 bytes further.  (The leading byte offset is the distance to the next
-// 64 columns, which no product here reaches.)
+// columns their N.  Eight rows along K are 1024 bytes, the next 64 columns
+// along N 8192 bytes (leading byte offset >> 4 at bits 16-29) further; a step
+// of 16 rows along K is 2048 bytes, one of 16 columns along N 32 bytes.
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr)
 {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(8192 >> 4) << 16) |
@@ -50,17 +50,31 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr)
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N])
 {
-    static_assert(N == 16 || N == 32, "widths in use");
-    if constexpr (N == 32) {
-        tmem_st32(taddr, v);
-    } else {
+    static_assert(N == 8 || N == 16, "widths in use");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else
         asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
                      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
                      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
                        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
                        "r"(v[15])
                      : "memory");
-    }
+}
+
+// N consecutive tensor-memory columns of this thread's lane -> N registers.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N])
+{
+    static_assert(N == 16, "the width in use");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 }  // namespace sv
