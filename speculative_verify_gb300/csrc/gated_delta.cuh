@@ -332,4 +332,552 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
     if (p.commit) st.store(s, i);
 }
 
+// ------------------------------------------------ several rows at once
+//
+// With a few rows the state need not be walked row by row.  Let n rows (the
+// accepted ones of prev, then the new ones) have running log decays G and
+// inverse norms r_k, r_q.  From the state S before all of them
+//   r_t = beta_t (v_t - e^(G_t) r_k,t (S k_t))
+//   u_t = r_t - sum_{s<t} A_ts u_s,  A_ts = beta_t e^(G_t - G_s) r_k,t r_k,s (k_t . k_s)
+//   o_t = scale e^(G_t) r_q,t (S q_t) + sum_{s<=t} M_ts u_s,
+//         M_ts = scale e^(G_t - G_s) r_q,t r_k,s (q_t . k_s)
+//   S'  = e^(G_m) S + sum_{s<m} (e^(G_m - G_s) r_k,s u_s) k_s^T
+// where the state is wanted after the first m rows: the accepted ones, or all.
+//
+// A warp owns 16 rows of S in the accumulator layout of m16n8 products, which
+// is also their A operand's layout: S k and S q are products with S as A, and
+// the update accumulates onto S where it lies.  S enters as three bf16 terms
+// (24 bits; keys and queries are bf16 as they come) and u, in the update, as
+// two.  The block computes A and M once for its warps.  Up to 16 rows in all,
+// (I + A)^-1 and M are applied as products of three-term operands, so that r,
+// u and the outputs stay in registers; with more, u comes by substitution in
+// shared memory.
+//
+// Against the row-by-row kernel this takes about a quarter of the
+// instructions for 4 + 4 rows, which were its bound.
+
+constexpr int GB_MAX = 2 * GD_MAX_ROWS;         // rows of prev and new together
+constexpr int GB_KPAD = 8, GB_FPAD = 4;         // padding of a row in shared memory, bf16 and fp32 values
+
+__device__ __forceinline__ uint32_t gb_pack(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void gb_split(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = gb_pack(a, b);
+    lo = gb_pack(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void gb_split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = gb_pack(a, b);
+    gb_split(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u), mid, lo);
+}
+
+__device__ __forceinline__ void gb_ldmatrix(uint32_t (&r)[4], const uint16_t *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
+}
+
+__device__ __forceinline__ void gb_ldmatrix_trans(uint32_t (&r)[4], const uint16_t *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
+}
+
+// D (16x8 fp32) += A (16x8 bf16, row) * B (8x8 bf16, col).
+__device__ __forceinline__ void mma_bf16_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(b));
+}
+
+// Sums of two floats each, kept as the rounded sum and what it leaves:
+// differences of large sums give the decays between near rows.
+struct Sum2 {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b)
+{
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float hi = s + e;
+    return Sum2{hi, e - (hi - s)};
+}
+
+__device__ __forceinline__ float exp_diff(Sum2 a, float bhi, float blo) { return expf((a.hi - bhi) + (a.lo - blo)); }
+
+constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
+
+// Shared memory (bytes) for np rows in all (a multiple of 16), nq new rows (a
+// multiple of 16), `cols` state rows.
+__host__ __device__ constexpr int gb_smem_bytes(int np, int nq, int dk, int cols)
+{
+    return (np + nq) * (dk + GB_KPAD) * 2 + np * (cols + GB_KPAD) * 2 + 8 * GB_MAX * 4 +
+           (np == 16 ? np * (np + GB_FPAD) * 4 + (np + nq) * (np + GB_KPAD) * 6
+                     : (np + nq) * (np + GB_FPAD) * 4 + cols * (np + GB_FPAD) * 4);
+}
+
+// S += u' K for the eight rows of tile j, u' = u f_s r_k in two terms: x0, x1
+// are this lane's values of u for rows 8 j + 2 c, + 1 and state row g, y0, y1
+// for state row g + 8.
+template <int DK>
+__device__ __forceinline__ void gb_update(float (&st)[DK / 8][4], float x0, float x1, float y0, float y1, const float *f_s,
+                                          const float *rk, const uint16_t *ks, int kst, int j)
+{
+    const int lane = threadIdx.x & 31, t = 8 * j + 2 * (lane & 3);
+    const float w0 = f_s[t] * rk[t], w1 = f_s[t + 1] * rk[t + 1];
+    uint32_t hi[2], lo[2];
+    gb_split(x0 * w0, x1 * w1, hi[0], lo[0]);
+    gb_split(y0 * w0, y1 * w1, hi[1], lo[1]);
+#pragma unroll
+    for (int i = 0; i < DK / 32; ++i) {
+        uint32_t bb[4];
+        gb_ldmatrix_trans(bb, ks + (8 * j + (lane & 7)) * kst + 32 * i + (lane >> 3) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            mma_bf16_1688(st[4 * i + e], lo[0], lo[1], bb[e]);
+            mma_bf16_1688(st[4 * i + e], hi[0], hi[1], bb[e]);
+        }
+    }
+}
+
+// NK, NQ: most n8 tiles of rows and of new rows.  Grid: x = dv / cols,
+// y = Hv, z = B; cols / 16 warps.
+template <int DK, int NK, int NQ>
+__global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaParams p)
+{
+    extern __shared__ __align__(16) uint8_t gb_smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int cols = p.cols, col0 = blockIdx.x * cols, hv = blockIdx.y, b = blockIdx.z, hk = hv / (p.Hv / p.Hk);
+    constexpr int NP = 8 * NK < 16 ? 16 : 8 * NK, NQR = 8 * NQ < 16 ? 16 : 8 * NQ;
+    constexpr int KST = DK + GB_KPAD, AST = NP + GB_FPAD;
+    const int vst = cols + GB_KPAD;
+    uint16_t *ks = reinterpret_cast<uint16_t *>(gb_smem);       // [NP][KST]
+    uint16_t *qs = ks + NP * KST;                               // [NQR][KST]
+    uint16_t *vs = qs + NQR * KST;                              // [NP][vst]
+    float *g_hi = reinterpret_cast<float *>(vs + NP * vst), *g_lo = g_hi + GB_MAX, *beta = g_lo + GB_MAX, *rk = beta + GB_MAX,
+          *rq = rk + GB_MAX, *f_p = rq + GB_MAX, *f_s = f_p + GB_MAX, *f_o = f_s + GB_MAX;
+    float *as = f_o + GB_MAX;                                   // [NP][AST]
+    // up to 16 rows: (I + A)^-1 and M as three bf16 terms; more: M and u, fp32
+    constexpr bool SMALL = NP == 16;
+    constexpr int TST = NP + GB_KPAD, TT = NP * TST, MT = NQR * TST;
+    uint16_t *tt = reinterpret_cast<uint16_t *>(as + NP * AST), *mt3 = tt + 3 * TT;     // [3][NP][TST], [3][NQR][TST]
+    float *ms = as + NP * AST;                                  // [NQR][AST]
+    float *us = ms + NQR * AST;                                 // [cols][AST]
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
+    uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
+    if (slot < 0) {                             // an inactive entry: its outputs are zero
+        for (int i = tid; i < p.T * cols; i += nthr) o[(i / cols) * p.ldo + i % cols] = 0;
+        return;
+    }
+    // the state's rows 16 warp + g and + 8, columns 8 j + 2 c, + 1
+    float *srow = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0 + 16 * warp + g) * DK + 2 * c;
+    float st[DK / 8][4];
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j) {
+        const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * j), y = *reinterpret_cast<const float2 *>(srow + 8 * DK + 8 * j);
+        st[j][0] = x.x;
+        st[j][1] = x.y;
+        st[j][2] = y.x;
+        st[j][3] = y.y;
+    }
+    int na = p.prev_T;                          // accepted rows
+    if (p.accept_len && na > 0) na = min(na, max(0, min(p.accept_len[b], na) + 1));
+    const int ta = (na + 7) >> 3, tn = (p.T + 7) >> 3, first = 8 * ta, rows = first + 8 * tn;
+    const long long pr0 = static_cast<long long>(b) * p.prev_T, nr0 = static_cast<long long>(b) * p.T;
+
+    // ---- rows into shared memory as they are; absent rows are zero
+    constexpr int PR = DK / 8;                  // 16-byte pieces of a key row
+    for (int i = tid; i < (NP + NQR) * PR; i += nthr) {
+        const int t = i / PR, j = (i % PR) * 8;
+        const uint16_t *src = nullptr;
+        if (t >= NP) {
+            if (t - NP < p.T) src = p.rows.q + (nr0 + t - NP) * p.rows.ldq;
+        } else if (t < na) {
+            src = p.prev.k + (pr0 + t) * p.prev.ldk;
+        } else if (t >= first && t - first < p.T) {
+            src = p.rows.k + (nr0 + t - first) * p.rows.ldk;
+        }
+        uint16_t *dst = ks + t * KST + j;       // (the queries follow the keys)
+        if (src)
+            cp_async_16(smem_addr(dst), src + static_cast<long long>(hk) * DK + j);
+        else
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    const int vl = cols == 128 ? 4 : 3;         // log2 of a value row's pieces
+    for (int i = tid; i < rows << vl; i += nthr) {
+        const int t = i >> vl, j = (i & ((1 << vl) - 1)) * 8;
+        const uint16_t *src = nullptr;
+        if (t < na)
+            src = p.prev.v + (pr0 + t) * p.prev.ldv;
+        else if (t >= first && t - first < p.T)
+            src = p.rows.v + (nr0 + t - first) * p.rows.ldv;
+        uint16_t *dst = vs + t * vst + j;
+        if (src)
+            cp_async_16(smem_addr(dst), src + static_cast<long long>(hv) * p.dv + col0 + j);
+        else
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    cp_async_commit();
+    if (warp == nwarp - 1) {
+        // gates, two rows a lane, and the running sum of the log decays
+        Sum2 G[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            float gv = 0.f, bv = 0.f;
+            if (t < na) {
+                gv = p.prev.g[(pr0 + t) * p.prev.ldg + hv];
+                bv = p.prev.beta[(pr0 + t) * p.prev.ldg + hv];
+            } else if (t >= first && t - first < p.T) {
+                gv = p.rows.g[(nr0 + t - first) * p.rows.ldg + hv];
+                bv = p.rows.beta[(nr0 + t - first) * p.rows.ldg + hv];
+            }
+            if (gv < GB_MIN_LOG) gv = GB_MIN_LOG;
+            G[e] = Sum2{gv, 0.f};
+            beta[t] = bv;
+        }
+        Sum2 run = add2(G[0], G[1]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sum2 below{__shfl_up_sync(0xFFFFFFFFu, run.hi, d), __shfl_up_sync(0xFFFFFFFFu, run.lo, d)};
+            if (lane >= d) run = add2(below, run);
+        }
+        Sum2 before{__shfl_up_sync(0xFFFFFFFFu, run.hi, 1), __shfl_up_sync(0xFFFFFFFFu, run.lo, 1)};
+        if (lane == 0) before = Sum2{0.f, 0.f};
+        G[0] = add2(before, G[0]);
+        G[1] = run;
+        // where the state is wanted: after the accepted rows, or all (absent rows decay nothing)
+        const int m = p.commit ? GB_MAX : first, ml = max(m - 1, 0) >> 1;
+        const float mh = __shfl_sync(0xFFFFFFFFu, G[1].hi, ml), mlo = __shfl_sync(0xFFFFFFFFu, G[1].lo, ml);
+        const Sum2 Gm = m > 0 ? Sum2{mh, mlo} : Sum2{0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            g_hi[t] = G[e].hi;
+            g_lo[t] = G[e].lo;
+            f_p[t] = expf(G[e].hi + G[e].lo);
+            f_s[t] = t < m ? exp_diff(Gm, G[e].hi, G[e].lo) : 0.f;
+        }
+        if (lane == 0) f_o[0] = expf(Gm.hi + Gm.lo);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    // ---- inverse norms, eight lanes a row
+    for (int t0 = 4 * warp; t0 < NP + NQR; t0 += 4 * nwarp) {
+        const int t = t0 + (lane >> 3);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < DK / 64; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(ks + t * KST + 64 * j + 8 * (lane & 7));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
+                ss = fmaf(lo, lo, fmaf(hi, hi, ss));
+            }
+        }
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+        const float inv = p.l2norm ? 1.f / sqrtf(ss + GD_L2_EPS) : 1.f;
+        if ((lane & 7) == 0) {
+            if (t >= NP)
+                rq[t - NP] = inv * p.scale;
+            else
+                rk[t] = inv;
+        }
+    }
+    __syncthreads();
+
+    // ---- A and M: one 16-row tile of either a warp
+    for (int task = warp; task < NP / 16 + NQR / 16; task += nwarp) {
+        const bool is_m = task >= NP / 16;
+        const int mt = is_m ? task - NP / 16 : task;
+        const int r0 = is_m ? first + 16 * mt : 16 * mt;        // the tile's first row among all
+        if (is_m ? 16 * mt >= p.T : r0 >= rows) continue;
+        const int last = min(NK, (r0 + 15) / 8 + 1);
+        float acc[NK][4];
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+        const uint16_t *arow = (is_m ? qs : ks) + (16 * mt + (lane & 15)) * KST + (lane >> 4) * 8;
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s) {
+            uint32_t a0[4], a1[4], bb[4];
+            gb_ldmatrix(a0, arow + 32 * s);
+            gb_ldmatrix(a1, arow + 32 * s + 16);
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                if (j >= last) break;
+                gb_ldmatrix(bb, ks + (8 * j + (lane & 7)) * KST + 32 * s + (lane >> 3) * 8);
+                mma_bf16_16816(acc[j], a0[0], a0[1], a0[2], a0[3], bb[0], bb[1]);
+                mma_bf16_16816(acc[j], a1[0], a1[1], a1[2], a1[3], bb[2], bb[3]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int tl = 16 * mt + g + 8 * h, t = r0 + g + 8 * h;     // within its matrix, among all rows
+            const bool live = is_m ? tl < p.T : t < rows;
+            const Sum2 G = live ? Sum2{g_hi[t], g_lo[t]} : Sum2{0.f, 0.f};
+            const float f = !live ? 0.f : is_m ? rq[tl] : beta[t] * rk[t];
+            float *dst = (is_m && !SMALL ? ms : as) + tl * AST + 2 * c;
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int s = 8 * j + 2 * c + e;
+                    v[e] = live && (is_m ? s <= t : s < t) ? acc[j][2 * h + e] * (exp_diff(G, g_hi[s], g_lo[s]) * rk[s] * f) : 0.f;
+                }
+                if (SMALL && is_m) {
+                    uint32_t w[3];
+                    gb_split3(v[0], v[1], w[0], w[1], w[2]);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t *>(mt3 + e * MT + tl * TST + 8 * j + 2 * c) = w[e];
+                } else {
+                    *reinterpret_cast<float2 *>(dst + 8 * j) = make_float2(v[0], v[1]);
+                }
+            }
+            if (SMALL && NK == 1)               // the second half of a 16-row operand
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (is_m) *reinterpret_cast<uint32_t *>(mt3 + e * MT + tl * TST + 8 + 2 * c) = 0u;
+        }
+        if (SMALL && !is_m) {
+            // column `lane` of (I + A)^-1 by forward substitution
+            __syncwarp();
+            if (lane < 16) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
+                    if (i < 8 * NK)
+#pragma unroll
+                        for (int k = 0; k < i; k += 4) {
+                            const float4 a = *reinterpret_cast<const float4 *>(as + i * AST + k);
+                            s0 = fmaf(-a.x, x[k], s0);
+                            if (k + 1 < i) s1 = fmaf(-a.y, x[k + 1], s1);
+                            if (k + 2 < i) s0 = fmaf(-a.z, x[k + 2], s0);
+                            if (k + 3 < i) s1 = fmaf(-a.w, x[k + 3], s1);
+                        }
+                    x[i] = s0 + s1;
+                    uint32_t w[3];
+                    gb_split3(x[i], 0.f, w[0], w[1], w[2]);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) tt[e * TT + i * TST + lane] = static_cast<uint16_t>(w[e]);
+                }
+            }
+        }
+    }
+
+    // ---- S k and S q
+    float pk[NK][4], pq[NQ][4];
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pk[j][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pq[j][e] = 0.f;
+    const int nk = ta + tn;
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+        uint32_t hi[2][4], mid[2][4], lo[2][4], bb[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)         // rows g, g + 8 of columns 8 (i >> 1) ..
+                gb_split3(st[4 * s + 2 * e + (i >> 1)][2 * (i & 1)], st[4 * s + 2 * e + (i >> 1)][2 * (i & 1) + 1], hi[e][i],
+                          mid[e][i], lo[e][i]);
+        auto both = [&](float (&d)[4], const uint16_t *rowp) {
+            gb_ldmatrix(bb, rowp + (lane & 7) * KST + 32 * s + (lane >> 3) * 8);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mma_bf16_16816(d, lo[e][0], lo[e][1], lo[e][2], lo[e][3], bb[2 * e], bb[2 * e + 1]);
+                mma_bf16_16816(d, mid[e][0], mid[e][1], mid[e][2], mid[e][3], bb[2 * e], bb[2 * e + 1]);
+                mma_bf16_16816(d, hi[e][0], hi[e][1], hi[e][2], hi[e][3], bb[2 * e], bb[2 * e + 1]);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+            if (j < nk) both(pk[j], ks + 8 * j * KST);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+            if (j < tn) both(pq[j], qs + 8 * j * KST);
+    }
+    // ---- r
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+        if (j < nk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 8 * j + 2 * c + (e & 1);
+                pk[j][e] = beta[t] * (bf16_bits_to_float(vs[t * vst + 16 * warp + g + 8 * (e >> 1)]) - f_p[t] * rk[t] * pk[j][e]);
+            }
+    const float decay = f_o[0];
+    const int nu = p.commit ? nk : ta;          // tiles of the rows that the state is wanted after
+    if constexpr (SMALL) {
+        __syncthreads();                        // (I + A)^-1 and M are complete
+        // a product's 16 rows as A operands of three terms; two matrices of
+        // three terms each make 24 bits with the six largest term products
+        auto operand = [&](const float (&x)[NK][4], uint32_t (&a)[3][4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((i >> 1) < NK)
+                    gb_split3(x[(i >> 1) < NK ? i >> 1 : 0][2 * (i & 1)], x[(i >> 1) < NK ? i >> 1 : 0][2 * (i & 1) + 1], a[0][i], a[1][i], a[2][i]);
+                else
+                    a[0][i] = a[1][i] = a[2][i] = 0u;
+            }
+        };
+        auto product = [&](float (&d)[2][4], const uint32_t (&a)[3][4], const uint16_t *m, int step) {
+            uint32_t bb[3][4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                gb_ldmatrix(bb[e], m + e * step + ((lane & 7) + ((lane >> 4) << 3)) * TST + ((lane >> 3) & 1) * 8);
+#pragma unroll
+            for (int k = 4; k >= 0; --k)        // (term of a, term of b): smallest products first
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    auto one = [&](int x, int y) { mma_bf16_16816(d[j], a[x][0], a[x][1], a[x][2], a[x][3], bb[y][2 * j], bb[y][2 * j + 1]); };
+                    if (k == 4) one(1, 1);
+                    if (k == 3) one(2, 0), one(0, 2);
+                    if (k == 2) one(1, 0);
+                    if (k == 1) one(0, 1);
+                    if (k == 0) one(0, 0);
+                }
+        };
+        float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+            uint32_t a[3][4];
+            operand(pk, a);
+            product(u, a, tt, TT);
+        }
+        if (tn > 0) {
+            float s[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * j + 2 * c + (e & 1);
+                    s[j][e] = j < NQ && t < p.T ? f_p[first + t] * rq[t] * pq[j < NQ ? j : 0][e] : 0.f;
+                }
+            float uk[NK][4];
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) uk[j][e] = u[j][e];
+            uint32_t a[3][4];
+            operand(uk, a);
+            product(s, a, mt3, MT);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * j + 2 * c + (e & 1);
+                    if (t < p.T) o[t * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[j][e]));
+                }
+        }
+        if (nu == 0) return;
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[j][e] *= decay;
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+            if (j < nu) gb_update<DK>(st, u[j][0], u[j][1], u[j][2], u[j][3], f_s, rk, ks, KST, j);
+    } else {
+        float *uw = us + 16 * warp * AST;
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+            if (j < nk)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)         // r, in the warp's own rows of shared memory
+                    *reinterpret_cast<float2 *>(uw + (g + 8 * h) * AST + 8 * j + 2 * c) = make_float2(pk[j][2 * h], pk[j][2 * h + 1]);
+        __syncthreads();                            // A and M are complete
+        // ---- u by forward substitution, a state row a lane, eight rows t at a time
+        if (lane < 16) {
+            float *ur = uw + lane * AST;
+            for (int j = 0; j < nk; ++j) {
+                float u[8];
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(ur + 8 * j + i);
+                    u[i] = x.x;
+                    u[i + 1] = x.y;
+                    u[i + 2] = x.z;
+                    u[i + 3] = x.w;
+                }
+                for (int k = 0; k < 2 * j; ++k) {   // four earlier rows
+                    const float4 e = *reinterpret_cast<const float4 *>(ur + 4 * k);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 a = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 4 * k);
+                        u[i] -= (a.x * e.x + a.y * e.y) + (a.z * e.z + a.w * e.w);
+                    }
+                }
+#pragma unroll
+                for (int i = 1; i < 8; ++i) {
+                    const float4 a = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 8 * j);
+                    const float4 a2 = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 8 * j + 4);
+                    const float av[8] = {a.x, a.y, a.z, a.w, a2.x, a2.y, a2.z, a2.w};
+#pragma unroll
+                    for (int k = 0; k < i; ++k) u[i] = fmaf(-av[k], u[k], u[i]);
+                }
+                *reinterpret_cast<float4 *>(ur + 8 * j) = make_float4(u[0], u[1], u[2], u[3]);
+                *reinterpret_cast<float4 *>(ur + 8 * j + 4) = make_float4(u[4], u[5], u[6], u[7]);
+            }
+        }
+        __syncwarp();
+        // ---- outputs
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+            if (j < tn) {
+                const int t0 = 8 * j + 2 * c;
+                float s[4];                         // (t0, g) (t0 + 1, g) (t0, g + 8) (t0 + 1, g + 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = (t0 + (e & 1) < p.T ? f_p[first + t0 + (e & 1)] * rq[t0 + (e & 1)] : 0.f) * pq[j][e];
+                for (int k = 0; k < first + 8 * j + 8; k += 4) {
+                    const float4 m0 = *reinterpret_cast<const float4 *>(ms + t0 * AST + k), m1 = *reinterpret_cast<const float4 *>(ms + (t0 + 1) * AST + k);
+                    const float4 u0 = *reinterpret_cast<const float4 *>(uw + g * AST + k), u1 = *reinterpret_cast<const float4 *>(uw + (g + 8) * AST + k);
+                    s[0] = fmaf(m0.x, u0.x, fmaf(m0.y, u0.y, fmaf(m0.z, u0.z, fmaf(m0.w, u0.w, s[0]))));
+                    s[1] = fmaf(m1.x, u0.x, fmaf(m1.y, u0.y, fmaf(m1.z, u0.z, fmaf(m1.w, u0.w, s[1]))));
+                    s[2] = fmaf(m0.x, u1.x, fmaf(m0.y, u1.y, fmaf(m0.z, u1.z, fmaf(m0.w, u1.w, s[2]))));
+                    s[3] = fmaf(m1.x, u1.x, fmaf(m1.y, u1.y, fmaf(m1.z, u1.z, fmaf(m1.w, u1.w, s[3]))));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t0 + (e & 1) < p.T)
+                        o[(t0 + (e & 1)) * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[e]));
+            }
+        // ---- the state after the wanted rows
+        if (nu == 0) return;
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[j][e] *= decay;
+        for (int j = 0; j < nu; ++j) {
+            const float2 x = *reinterpret_cast<const float2 *>(uw + g * AST + 8 * j + 2 * c),
+                         y = *reinterpret_cast<const float2 *>(uw + (g + 8) * AST + 8 * j + 2 * c);
+            gb_update<DK>(st, x.x, x.y, y.x, y.y, f_s, rk, ks, KST, j);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j) {
+        *reinterpret_cast<float2 *>(srow + 8 * j) = make_float2(st[j][0], st[j][1]);
+        *reinterpret_cast<float2 *>(srow + 8 * DK + 8 * j) = make_float2(st[j][2], st[j][3]);
+    }
+}
+
 }  // namespace sv

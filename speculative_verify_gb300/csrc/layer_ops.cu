@@ -43,6 +43,9 @@ cudaError_t raise(F *kernel, int bytes)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+template <int DK>
+cudaError_t delta_block_raise();
+
 // The current device's facts, with the kernels' shared-memory limits raised
 // once per device.
 int ops_device(DeviceInfo *out)
@@ -59,6 +62,8 @@ int ops_device(DeviceInfo *out)
     up(raise(gated_delta_step_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
     up(raise(gated_delta_rows_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
     up(raise(gated_delta_rows_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
+    up(delta_block_raise<64>());
+    up(delta_block_raise<128>());
     up(raise(delta_prep_kernel<64>, sizeof(DcPrepSmem<64>)));
     up(raise(delta_prep_kernel<128>, sizeof(DcPrepSmem<128>)));
     up(raise(delta_scan_kernel<64>, DsSmem<64>::BYTES));
@@ -214,6 +219,37 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
     return p;
 }
 
+// Rows from which a step takes them all at once (gated_delta_block_kernel).
+constexpr int DELTA_BLOCK_MIN_ROWS = 3;
+
+template <int DK, int NK, int NQ>
+int delta_block_launch(const DeltaParams &p, int B, cudaStream_t stream)
+{
+    constexpr int NP = 8 * NK < 16 ? 16 : 8 * NK, NQR = 8 * NQ < 16 ? 16 : 8 * NQ;
+    const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
+    return launch(gated_delta_block_kernel<DK, NK, NQ>, grid, 2 * p.cols, gb_smem_bytes(NP, NQR, DK, p.cols), stream, p);
+}
+
+template <int DK>
+int delta_block_dispatch(const DeltaParams &p, int B, cudaStream_t stream)
+{
+    const int nk = (p.prev_T + 7) / 8 + (p.T + 7) / 8;
+    if (nk <= 1) return delta_block_launch<DK, 1, 1>(p, B, stream);
+    if (nk <= 2 && p.T <= 8) return delta_block_launch<DK, 2, 1>(p, B, stream);
+    if (nk <= 4 && p.T <= 16) return delta_block_launch<DK, 4, 2>(p, B, stream);
+    return delta_block_launch<DK, 8, 4>(p, B, stream);
+}
+
+template <int DK>
+cudaError_t delta_block_raise()
+{
+    cudaError_t e = raise(gated_delta_block_kernel<DK, 1, 1>, gb_smem_bytes(16, 16, DK, 128));
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 2, 1>, gb_smem_bytes(16, 16, DK, 128));
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 4, 2>, gb_smem_bytes(32, 16, DK, 128));
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 8, 4>, gb_smem_bytes(64, 32, DK, 128));
+    return e;
+}
+
 // Blocks of the workspace: every sequence's whole and part blocks.
 long long delta_blocks(int R, int B) { return static_cast<long long>(R / DC_ROWS) + B; }
 
@@ -334,6 +370,10 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
     const int cap = T > prev_T ? T : prev_T;
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (T + prev_T >= DELTA_BLOCK_MIN_ROWS) {
+        p.cols = static_cast<long long>(B) * p.Hv < dev.sms ? 64 : shape->dv;
+        return shape->dk == 64 ? delta_block_dispatch<64>(p, B, cs) : delta_block_dispatch<128>(p, B, cs);
+    }
     return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, 4 * p.cols, smem, cs, p)
                            : launch(gated_delta_step_kernel<128>, grid, 4 * p.cols, smem, cs, p);
 }
