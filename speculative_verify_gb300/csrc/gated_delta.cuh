@@ -420,7 +420,7 @@ constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log de
 __host__ __device__ constexpr int gb_smem_bytes(int np, int nq, int dk, int cols)
 {
     return (np + nq) * (dk + GB_KPAD) * 2 + np * (cols + GB_KPAD) * 2 + 8 * GB_MAX * 4 +
-           (np == 16 ? np * (np + GB_FPAD) * 4 + (np + nq) * (np + GB_KPAD) * 6
+           (np == 16 ? 2 * np * (np + GB_FPAD) * 4 + (np + nq) * (np + GB_KPAD) * 6
                      : (np + nq) * (np + GB_FPAD) * 4 + cols * (np + GB_FPAD) * 4);
 }
 
@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
     // up to 16 rows: (I + A)^-1 and M as three bf16 terms; more: M and u, fp32
     constexpr bool SMALL = NP == 16;
     constexpr int TST = NP + GB_KPAD, TT = NP * TST, MT = NQR * TST;
-    uint16_t *tt = reinterpret_cast<uint16_t *>(as + NP * AST), *mt3 = tt + 3 * TT;     // [3][NP][TST], [3][NQR][TST]
+    float *ed = as + NP * AST;                                  // [NP][AST], decays between rows
+    uint16_t *tt = reinterpret_cast<uint16_t *>(ed + NP * AST), *mt3 = tt + 3 * TT;     // [3][NP][TST], [3][NQR][TST]
     float *ms = as + NP * AST;                                  // [NQR][AST]
     float *us = ms + NQR * AST;                                 // [cols][AST]
     pdl_launch_dependents();
@@ -597,6 +598,12 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
                 rk[t] = inv;
         }
     }
+    // ---- decays between rows, times the earlier row's inverse norm later
+    if constexpr (SMALL)
+        for (int i = tid; i < NP * NP; i += nthr) {
+            const int t = i / NP, s = i % NP;
+            ed[t * AST + s] = s <= t ? exp_diff(Sum2{g_hi[t], g_lo[t]}, g_hi[s], g_lo[s]) : 0.f;
+        }
     __syncthreads();
 
     // ---- A and M: one 16-row tile of either a warp
@@ -638,7 +645,8 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int s = 8 * j + 2 * c + e;
-                    v[e] = live && (is_m ? s <= t : s < t) ? acc[j][2 * h + e] * (exp_diff(G, g_hi[s], g_lo[s]) * rk[s] * f) : 0.f;
+                    const float d = !live || s > t ? 0.f : SMALL ? ed[t * AST + s] : exp_diff(G, g_hi[s], g_lo[s]);
+                    v[e] = live && (is_m ? s <= t : s < t) ? acc[j][2 * h + e] * (d * rk[s] * f) : 0.f;
                 }
                 if (SMALL && is_m) {
                     uint32_t w[3];

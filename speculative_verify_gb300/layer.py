@@ -16,8 +16,7 @@ DELTA_L2NORM, DELTA_COMMIT, DELTA_ZERO_INIT = 0x1, 0x2, 0x4
 ACTS = {"silu": 0, "gelu": 1}
 FP8_GROUP = 128
 
-torch = None                            # set, with the library, by the first call
-_lib = None
+torch = _lib = _bf16 = _f32 = _raw_stream = None        # set by the first call
 
 
 class DeltaRows(ctypes.Structure):
@@ -53,11 +52,12 @@ def declare(lib) -> None:
 
 def _init():
     """Load torch and the library on the first call; the calls below are short, so nothing is looked up twice."""
-    global torch, _lib
+    global torch, _lib, _bf16, _f32, _raw_stream
     import torch as _torch
 
     import speculative_verify_gb300 as root
     torch, _lib = _torch, root.load()
+    _bf16, _f32, _raw_stream = torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream
 
 
 def _fail(fn, rc):
@@ -67,43 +67,43 @@ def _fail(fn, rc):
 
 def _raw(stream, t):
     """The stream's handle, or that of the current stream of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
-def _rows2d(t, name, dtype, T, D):
-    """The row distance of a [T][D] CUDA tensor of `dtype` with dense rows."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
+def _rows2d(t, name, dtype, shape):
+    """The row distance of a [T][D] CUDA tensor of that type with dense rows."""
+    if t.dtype is not dtype or not t.is_cuda:
         raise TypeError("%s must be a 2-D %s CUDA tensor" % (name, dtype))
-    if tuple(t.shape) != (T, D):
-        raise ValueError("%s must be [%d][%d]" % (name, T, D))
+    if t.shape != shape:
+        raise ValueError("%s must be [%d][%d]" % ((name,) + tuple(shape)))
+    if t.is_contiguous():
+        return shape[1]
     ld, one = t.stride()
-    if one != 1 and D > 1 and T:
+    if one != 1 and shape[1] > 1:
         raise ValueError("%s must have dense rows" % name)
-    return ld if ld > D else D if T < 2 else ld
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _norm_args(x, weight, residual, residual_out):
     if _lib is None:
         _init()
-    bf = torch.bfloat16
-    if x.dim() != 2:
-        raise TypeError("x must be a 2-D %s CUDA tensor" % bf)
-    T, D = x.shape
-    ldx = _rows2d(x, "x", bf, T, D)
-    if weight.dtype is not bf or not weight.is_cuda or weight.dim() != 1 or weight.shape[0] != D or \
-            not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous bf16 CUDA tensor of %d entries" % D)
+    shape = x.shape
+    if len(shape) != 2:
+        raise TypeError("x must be a 2-D %s CUDA tensor" % _bf16)
+    ldx = _rows2d(x, "x", _bf16, shape)
+    if weight.dtype is not _bf16 or not weight.is_cuda or weight.shape != shape[1:] or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bf16 CUDA tensor of %d entries" % shape[1])
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out without a residual")
-        return T, D, ldx, None, 0, None, 0
-    ldr = _rows2d(residual, "residual", bf, T, D)
+        return shape, ldx, None, 0, None, None, 0
+    ldr = _rows2d(residual, "residual", _bf16, shape)
     if residual_out is None:
-        residual_out = x.new_empty((T, D))
-        ldro = D
+        residual_out = torch.empty(shape, dtype=_bf16, device=x.device)
+        ldro = shape[1]
     else:
-        ldro = _rows2d(residual_out, "residual_out", bf, T, D)
-    return T, D, ldx, residual.data_ptr(), ldr, residual_out, ldro
+        ldro = _rows2d(residual_out, "residual_out", _bf16, shape)
+    return shape, ldx, residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), ldro
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6, unit_offset=False, y=None, residual_out=None, stream=None):
@@ -111,17 +111,17 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, unit_offset=False, y=None, resid
     root-mean-square norm of s times weight (or 1 + weight), bf16; see
     ``rmsnorm_residual`` in include/specverify.h.  residual_out=residual
     updates the residual stream in place."""
-    T, D, ldx, rp, ldr, residual_out, ldro = _norm_args(x, weight, residual, residual_out)
+    shape, ldx, rp, ldr, residual_out, rop, ldro = _norm_args(x, weight, residual, residual_out)
+    T, D = shape
     if y is None:
-        y = x.new_empty((T, D))
+        y = torch.empty(shape, dtype=_bf16, device=x.device)
         ldy = D
     else:
-        ldy = _rows2d(y, "y", torch.bfloat16, T, D)
+        ldy = _rows2d(y, "y", _bf16, shape)
     if T:
         rc = _lib.rmsnorm_residual(x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), T, D, eps,
-                                   NORM_UNIT_OFFSET if unit_offset else 0,
-                                   None if rp is None else residual_out.data_ptr(), ldro, y.data_ptr(), ldy,
-                                   _raw(stream, x))
+                                   NORM_UNIT_OFFSET if unit_offset else 0, rop, ldro, y.data_ptr(), ldy,
+                                   _raw_stream(x.get_device()) if stream is None else stream.cuda_stream)
         if rc:
             _fail("rmsnorm_residual", rc)
     return y, residual_out
@@ -131,24 +131,24 @@ def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, unit_offset=False, group=FP8
                 residual_out=None, stream=None):
     """(y8, scales, s): as :func:`rmsnorm` with y as float8_e4m3fn and fp32
     scales [T][ceil(D / 128)] (group=128) or [T][1] (group=0)."""
-    T, D, ldx, rp, ldr, residual_out, ldro = _norm_args(x, weight, residual, residual_out)
+    shape, ldx, rp, ldr, residual_out, rop, ldro = _norm_args(x, weight, residual, residual_out)
+    T, D = shape
     if group != FP8_GROUP and group != 0:
         raise ValueError("group must be 0 or %d" % FP8_GROUP)
     n = -(-D // group) if group else 1
     if y is None:
-        y = x.new_empty((T, D), dtype=torch.float8_e4m3fn)
+        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
         ldy = D
     else:
-        ldy = _rows2d(y, "y", torch.float8_e4m3fn, T, D)
+        ldy = _rows2d(y, "y", torch.float8_e4m3fn, shape)
     if scales is None:
-        scales = x.new_empty((T, n), dtype=torch.float32)
+        scales = torch.empty((T, n), dtype=_f32, device=x.device)
         lds = n
     else:
-        lds = _rows2d(scales, "scales", torch.float32, T, n)
+        lds = _rows2d(scales, "scales", _f32, (T, n))
     if T:
         rc = _lib.rmsnorm_residual_fp8(x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), T, D, eps,
-                                       NORM_UNIT_OFFSET if unit_offset else 0, group,
-                                       None if rp is None else residual_out.data_ptr(), ldro, y.data_ptr(), ldy,
+                                       NORM_UNIT_OFFSET if unit_offset else 0, group, rop, ldro, y.data_ptr(), ldy,
                                        scales.data_ptr(), lds, _raw(stream, x))
         if rc:
             _fail("rmsnorm_residual_fp8", rc)
@@ -180,7 +180,7 @@ def _row_stride(shape, stride, lead, name):
 
 def _ld(t, shape, dtype, lead, name):
     """The row distance of t, a CUDA tensor of that shape and type."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != len(shape):
+    if t.dtype is not dtype or not t.is_cuda:
         raise TypeError("%s must be a %d-D %s CUDA tensor" % (name, len(shape), dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s" % (name, "".join("[%d]" % n for n in shape)))
@@ -196,14 +196,17 @@ def _ld(t, shape, dtype, lead, name):
 
 def _delta_rows(q, k, v, g, beta, rows, Hk, Hv, dk, dv):
     """sv_delta_rows of tensors whose first dimensions are `rows`; q may be None."""
-    lead, bf = len(rows), torch.bfloat16
+    lead = len(rows)
     kshape, gshape = rows + (Hk, dk), rows + (Hv,)
-    ldg = _ld(g, gshape, torch.float32, lead, "g")
-    if _ld(beta, gshape, torch.float32, lead, "beta") != ldg:
+    ldg = _ld(g, gshape, _f32, lead, "g")
+    if _ld(beta, gshape, _f32, lead, "beta") != ldg:
         raise ValueError("g and beta must have the same row distance")
-    return DeltaRows(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                     0 if q is None else _ld(q, kshape, bf, lead, "q"), _ld(k, kshape, bf, lead, "k"),
-                     _ld(v, gshape + (dv,), bf, lead, "v"), ldg)
+    ldk = _ld(k, kshape, _bf16, lead, "k")
+    ldv = _ld(v, gshape + (dv,), _bf16, lead, "v")
+    if q is None:
+        return DeltaRows(None, k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), 0, ldk, ldv, ldg)
+    return DeltaRows(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                     _ld(q, kshape, _bf16, lead, "q"), ldk, ldv, ldg)
 
 
 def _i32(t, name, n=None):
@@ -216,9 +219,10 @@ def _i32(t, name, n=None):
 
 def _delta_state(state, k):
     """(n_slots, Hv, dv) of a state pool [slots][Hv][dv][dk], after checking it."""
-    if state.dtype is not torch.float32 or not state.is_cuda or state.dim() != 4 or not state.is_contiguous():
+    shape = state.shape
+    if state.dtype is not _f32 or not state.is_cuda or len(shape) != 4 or not state.is_contiguous():
         raise TypeError("state must be a contiguous float32 CUDA tensor [slots][Hv][dv][dk]")
-    n_slots, Hv, dv, dk = state.shape
+    n_slots, Hv, dv, dk = shape
     if dk != k.shape[-1]:
         raise ValueError("state must be [slots][Hv][dv][dk]")
     return n_slots, Hv, dv
@@ -256,10 +260,10 @@ def gated_delta_step(q, k, v, g, beta, state, state_idx=None, prev=None, accept_
             raise ValueError("accept_len needs prev")
         ap = _i32(accept_len, "accept_len", B)
     if o is None:
-        o = k.new_empty((B, T, Hv, dv))
+        o = torch.empty((B, T, Hv, dv), dtype=_bf16, device=k.device)
         ldo = Hv * dv
     else:
-        ldo = _ld(o, (B, T, Hv, dv), torch.bfloat16, 2, "o")
+        ldo = _ld(o, (B, T, Hv, dv), _bf16, 2, "o")
     if B:
         rc = _lib.gated_delta_step(
             rows, T, prows, P, ap, B,
@@ -297,19 +301,19 @@ def gated_delta_chunk(q, k, v, g, beta, cu_seqlens, state, state_idx=None, zero_
     shape = DeltaShape(Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale,
                        (DELTA_L2NORM if l2norm else 0) | (DELTA_ZERO_INIT if zero_init else 0))
     if o is None:
-        o = k.new_empty((R, Hv, dv))
+        o = torch.empty((R, Hv, dv), dtype=_bf16, device=k.device)
         ldo = Hv * dv
     else:
-        ldo = _ld(o, (R, Hv, dv), torch.bfloat16, 1, "o")
+        ldo = _ld(o, (R, Hv, dv), _bf16, 1, "o")
     if not B:
         return o
     if workspace is None:
         need = max(_lib.gated_delta_chunk_bytes(R, B, shape), 16)
         if stream is None:
-            workspace = k.new_empty(need, dtype=torch.uint8)
+            workspace = torch.empty(need, dtype=torch.uint8, device=k.device)
         else:                       # its memory may be reused only after the work on `stream`
             with torch.cuda.stream(stream):
-                workspace = k.new_empty(need, dtype=torch.uint8)
+                workspace = torch.empty(need, dtype=torch.uint8, device=k.device)
     elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
     rc = _lib.gated_delta_chunk(rows, R, cu, B, shape, state.data_ptr(),
@@ -327,21 +331,26 @@ def w4a16_gate_up(x, Wq, scales, act="silu", h=None, stream=None):
     include/specverify.h."""
     if _lib is None:
         _init()
-    import speculative_verify_gb300 as root
-    root._bits16(x, "x"), root._words(Wq, "Wq"), root._bits16(scales, "scales")
     T, K = x.shape
+    N, words = Wq.shape
+    for t, name in ((x, "x"), (scales, "scales")):
+        if t.dtype is not _bf16 and t.dtype not in (torch.int16, torch.uint16):
+            raise TypeError("%s must hold bf16 values (bfloat16, or int16/uint16 raw bits)" % name)
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous CUDA tensor" % name)
+    if Wq.dtype is not torch.int32 and Wq.dtype is not torch.uint32:
+        raise TypeError("Wq must be int32/uint32 packed nibble words")
+    if not Wq.is_cuda or not Wq.is_contiguous():
+        raise ValueError("Wq must be a contiguous CUDA tensor")
     if act not in ACTS:
         raise ValueError("act must be one of %s" % sorted(ACTS))
-    N, words = Wq.shape
     if N % 2 or words * 8 != K or scales.shape != (N, K // 128):
         raise ValueError("shape mismatch: x %s, Wq %s, scales %s" % (tuple(x.shape), tuple(Wq.shape),
                                                                       tuple(scales.shape)))
     if h is None:
-        h = x.new_empty((T, N // 2), dtype=torch.bfloat16)
-    else:
-        root._bits16(h, "h")
-        if h.shape != (T, N // 2):
-            raise ValueError("h must be [T][F]")
+        h = torch.empty((T, N // 2), dtype=_bf16, device=x.device)
+    elif h.dtype is not _bf16 or not h.is_cuda or not h.is_contiguous() or h.shape != (T, N // 2):
+        raise ValueError("h must be a contiguous bf16 CUDA tensor [T][F]")
     rc = _lib.w4a16_gate_up(x.data_ptr(), Wq.data_ptr(), scales.data_ptr(), T, K, N // 2, ACTS[act], h.data_ptr(),
                             _raw(stream, x))
     if rc:
