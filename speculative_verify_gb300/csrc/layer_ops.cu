@@ -109,6 +109,7 @@ int check_norm(const sv_bf16 *x, long long ldx, const sv_bf16 *residual, long lo
     if (T < 0 || D < 1 || D > NORM_MAX_D) return SV_ERR_SHAPE;
     if (!(eps >= 0.f) || (flags & ~SV_NORM_UNIT_OFFSET)) return SV_ERR_SHAPE;
     if (ldx < D || ldy < D || (residual && (ldr < D || ldro < D))) return SV_ERR_SHAPE;
+    if (T == 0) return SV_OK;                    // (tensors without rows have no addresses)
     if (!x || !weight || !y || (residual && !residual_out) || (!residual && residual_out)) return SV_ERR_NULL;
     if (!aligned_to(x, 2) || !aligned_to(weight, 2) || !aligned_to(residual, 2) || !aligned_to(residual_out, 2))
         return SV_ERR_ALIGN;
@@ -321,7 +322,7 @@ int rmsnorm_residual_fp8(const sv_bf16 *x, long long ldx, const sv_bf16 *residua
     if (rc != SV_OK) return rc;
     if (group != 0 && group != RN_GROUP) return SV_ERR_SHAPE;
     if (lds < (group ? (D + group - 1) / group : 1)) return SV_ERR_SHAPE;
-    if (!scales) return SV_ERR_NULL;
+    if (T > 0 && !scales) return SV_ERR_NULL;
     if (!aligned_to(scales, 4)) return SV_ERR_ALIGN;
     NormParams p{};
     p.x = x;
