@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(512) gated_delta_rows_kernel(const DeltaChunkP
 //
 // Decays: e^(G_i - G_j) below the diagonal blocks is e^(G_i - G_r) e^(G_r -
 // G_j) with r the first row of i's block, both at most 1 for decays; within a
-// diagonal block it is taken directly.
+// diagonal block it is taken directly.  Exponentials are the fast ones: their
+// error, 2^-22 and 2^-24 of the exponent, is within the operands' 16 bits.
 //
 // T: the 16 x 16 diagonal blocks of (I + A)^-1 by forward substitution (fp32,
 // a column a lane), the others by T_IJ = -T_II sum_K A_IK T_KJ on the tensor
@@ -312,24 +313,24 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
                 float fe[2], fl[2], fq[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    // row factors: e^G r_k, e^(G_n - G) r_k, scale e^G r_q
+                    // row factors: -e^G r_k, e^(G_n - G) r_k, scale e^G r_q
                     const int t = 2 * lane + e;
-                    const float eg = expf(hi[e] + lo[e]);
-                    fe[e] = t < n ? eg * sm.rk[t] : 0.f;
-                    fl[e] = t < n ? expf((end_hi - hi[e]) + (end_lo - lo[e])) * sm.rk[t] : 0.f;
+                    const float eg = __expf(hi[e] + lo[e]);
+                    fe[e] = t < n ? -eg * sm.rk[t] : 0.f;
+                    fl[e] = t < n ? __expf((end_hi - hi[e]) + (end_lo - lo[e])) * sm.rk[t] : 0.f;
                     fq[e] = t < n ? eg * sm.rq[t] : 0.f;
                     const int own_block = t >> 4;
 #pragma unroll
                     for (int I = 0; I < 4; ++I) {
                         const float ref_hi = __shfl_sync(0xFFFFFFFFu, hi[0], 8 * I), ref_lo = __shfl_sync(0xFFFFFFFFu, lo[0], 8 * I);
-                        if (I == own_block) sm.near[warp][t] = expf((hi[e] - ref_hi) + (lo[e] - ref_lo));
-                        if (I > own_block) sm.far[warp][I][t] = expf((ref_hi - hi[e]) + (ref_lo - lo[e])) * sm.rk[t];
+                        if (I == own_block) sm.near[warp][t] = __expf((hi[e] - ref_hi) + (lo[e] - ref_lo));
+                        if (I > own_block) sm.far[warp][I][t] = __expf((ref_hi - hi[e]) + (ref_lo - lo[e])) * sm.rk[t];
                     }
                 }
                 *reinterpret_cast<float2 *>(f + 2 * lane) = make_float2(fe[0], fe[1]);
                 *reinterpret_cast<float2 *>(f + DC_ROWS + 2 * lane) = make_float2(fl[0], fl[1]);
                 *reinterpret_cast<float2 *>(f + 2 * DC_ROWS + 2 * lane) = make_float2(fq[0], fq[1]);
-                if (lane == 0) f[3 * DC_ROWS] = expf(end_hi + end_lo);
+                if (lane == 0) f[3 * DC_ROWS] = __expf(end_hi + end_lo);
             }
             __syncthreads();
         }
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int j = j0 + e;
-                        const float d = j <= i ? expf((gi - sm.g_hi[e4][j]) + (gl - sm.g_lo[e4][j])) * sm.rk[j] : 0.f;
+                        const float d = j <= i ? __expf((gi - sm.g_hi[e4][j]) + (gl - sm.g_lo[e4][j])) * sm.rk[j] : 0.f;
                         m[e] = j <= i ? cq[j8][2 * h + e] * (d * qi) : 0.f;
                         a[e] = j < i ? ck[j8][2 * h + e] * (d * bi) : 0.f;
                     }
@@ -483,21 +484,30 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 // tensor memory and the keys, queries, T and M are B operands in shared
 // memory exactly as they are loaded.  Tensor memory, in columns:
 //
-//   phase  product                              accumulator
-//   P      S (2 terms, 0..127) x K              P  128..191
-//   O      S x Q                                Y  320..383 or 384..447
-//   U      r (2, 192..255) x T (2)              U  256..319
-//   D      u' (2, 0..63 over S) x K             D  128..255 (over P and r)
-//   M      u (2, 448..511) x M (2)              Y, after scaling its columns
+//   phase  product                               accumulator
+//   P      S (2 terms, 0..127) x K               P  128..191
+//   O      S x Q                                 O  320..383
+//   U      r (2, 192..255) x T (2)               U  256..319
+//   D      u' (2, 256..319 over u) x K           D  128..255 (over P and r)
+//   M      u (2, 448..511) x M (2)               M  384..447
 //
-// (of a product of two two-term factors lo x lo is left out).  Sixteen warps
+// (of a product of two two-term factors lo x lo is left out).  Warps 0-15
 // convert between the products: warp w has lanes 32 (w & 3) .. + 31 and a
 // quarter w >> 2 of the columns; the state's fp32 values stay in their
-// registers.  Warp 16 issues the loads, two blocks ahead, and the products.
-// The chain of a block is P, r, U, u', D, S; outputs are off it.
+// registers.  Warps 16-19 add up the outputs and write them, warp 20 issues
+// the products, warp 21 the loads, two blocks ahead.
 //
-// Work.  The chains of all heads and sequences are laid end to end and cut
-// into equal parts, at least as long as the longest chain, one for each CTA.
+// The chain of a block, P, r, U, u', D, S, bounds the kernel; O, M and the
+// outputs fill its gaps.  Measured (cycles of a block, 128 x 128 states): P
+// 1,100 with its hand-offs, r 550, U 650, u' 700, D 900, S 950.  A 128 x 64 x
+// 16 product with its A operand in tensor memory takes 56 cycles, one of
+// width 128 takes 88, so O is issued in two halves, into the gaps after P and
+// after U, where it delays neither.
+
+// Work.  The chains of all heads and sequences are laid end to end, each as
+// long as its blocks and DS_EXTRA more for its start and end (loading and
+// storing a state costs about two blocks' time), and cut into equal parts, at
+// least as long as the longest chain, one for each CTA.
 // A chain that a cut divides has its first blocks at the start of the later
 // CTA's part -- which runs them at once -- and its last ones at the end of
 // the earlier CTA's, which takes the state over when it gets there: with 192
@@ -505,9 +515,11 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 // two.  A CTA waits for CTAs of lower blockIdx only.
 
 constexpr int DS_WARPS = 16;                    // converting warps
-constexpr int DS_THREADS = DS_WARPS * 32 + 32;
+constexpr int DS_OUT = 16, DS_MMA = 20, DS_LOAD = 21;   // first output warp, the issuing warps
+constexpr int DS_THREADS = 22 * 32;
+constexpr int DS_EXTRA = 2;
 constexpr uint32_t DS_COLS = 512;
-constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_Y = 320, DS_U1 = 448;
+constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_O = 320, DS_M = 384, DS_U1 = 448;
 
 template <int DK>
 struct DsSmem {                                 // from a 1024-byte boundary
@@ -518,7 +530,9 @@ struct DsSmem {                                 // from a 1024-byte boundary
     static constexpr int BYTES = BARS + 256;
 };
 
-enum { B_FULL0, B_FULL1, B_P, B_O, B_U, B_D, B_M, B_SREADY, B_RREADY, B_UREADY, B_YFREE0, B_YFREE1, B_COUNT };
+// Barriers that a waiter could find two phases ahead come in pairs, one for
+// even and one for odd steps: their next phase needs the waiter to go on.
+enum { B_FULL0, B_FULL1, B_P, B_O, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_FFREE0, B_FFREE1, B_YFREE, B_COUNT };
 
 constexpr uint32_t ds_idesc(int n, bool b_mn)
 {
@@ -532,7 +546,7 @@ struct DsWait {
     int *err;
     __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const
     {
-        if (mbar_try_wait(bar, parity & 1u)) return;
+        if (mbar_sleep_wait(bar, parity & 1u, 100000u)) return;
         if (!mbar_wait_bounded(bar, parity & 1u, *flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) {
             *flag = 1;
             atomicOr(err, 2);
@@ -544,7 +558,7 @@ struct DsWait {
 struct DsWalk {
     const DeltaChunkParams *cp;
     int pos, stop, lo;                          // next place, end and start of the part
-    int b, first;                               // the sequence of `pos` and its first place
+    int b, first, length;                       // the sequence of `pos`, its first place, the length of its chains
     // the current segment: blocks c0 .. c1 - 1 of head hv of sequence b
     int begin, end, blocks, slot, hv, c0, c1;
     bool takes, gives;                          // another CTA ran the blocks before, runs those after
@@ -555,19 +569,26 @@ struct DsWalk {
         sl = cp->d.state_idx ? cp->d.state_idx[s] : s;
         return sl < 0 || sl >= cp->d.n_slots ? 0 : (en - bg + DC_ROWS - 1) / DC_ROWS;
     }
+    // Places of sequence s's chains.
+    __device__ __forceinline__ int places_of(int s) const
+    {
+        int bg, en, sl;
+        const int nb = blocks_of(s, bg, en, sl);
+        return nb ? (nb + DS_EXTRA) * cp->d.Hv : 0;
+    }
     // Part k of `parts` (whole warps call it).
     __device__ __forceinline__ void start(const DeltaChunkParams *c, int k, int parts)
     {
         cp = c;
-        const int lane = threadIdx.x & 31, Hv = cp->d.Hv;
-        int total = 0, most = 0, bg, en, sl;
+        const int lane = threadIdx.x & 31;
+        int total = 0, most = 0;
         for (int s = lane; s < cp->B; s += 32) {
-            const int nb = blocks_of(s, bg, en, sl);
-            total += nb * Hv;
-            most = max(most, nb);
+            const int n = places_of(s);
+            total += n;
+            most = max(most, n);
         }
         total = __reduce_add_sync(0xFFFFFFFFu, total);
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        most = __reduce_max_sync(0xFFFFFFFFu, most) / cp->d.Hv;
         const int cap = max(most, (total + parts - 1) / parts);
         // (k cap may be far past the end)
         lo = static_cast<int>(min(static_cast<long long>(k) * cap, static_cast<long long>(total)));
@@ -575,8 +596,7 @@ struct DsWalk {
         pos = lo;
         b = first = 0;
         for (int s0 = 0; s0 < cp->B && lo < stop; s0 += 32) {
-            const int s = s0 + lane;
-            const int mine = s < cp->B ? blocks_of(s, bg, en, sl) * Hv : 0;
+            const int s = s0 + lane, mine = s < cp->B ? places_of(s) : 0;
             int run = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -592,22 +612,32 @@ struct DsWalk {
             }
             first += __shfl_sync(0xFFFFFFFFu, run, 31);
         }
+        length = 0;
     }
+    // The next segment that has blocks; false at the part's end.
     __device__ __forceinline__ bool next()
     {
-        if (pos >= stop) return false;
-        while ((blocks = blocks_of(b, begin, end, slot)) * cp->d.Hv <= pos - first) {
-            first += blocks * cp->d.Hv;
-            ++b;
+        while (pos < stop) {
+            while (length == 0 || length * cp->d.Hv <= pos - first) {
+                // the sequence of `pos`: this one (not looked at yet) or a later one
+                if (length) {
+                    first += length * cp->d.Hv;
+                    ++b;
+                }
+                while ((blocks = blocks_of(b, begin, end, slot)) == 0) ++b;
+                length = blocks + DS_EXTRA;
+            }
+            hv = (pos - first) / length;
+            const int s = first + hv * length, e = s + length;
+            // of a chain with L places after the cut, the later part's CTA has the first L - 1 blocks
+            c0 = e > stop ? e - stop - 1 : 0;
+            c1 = pos > s ? e - pos - 1 : blocks;
+            takes = c0 > 0;                     // the CTA of the part after has the first c0 blocks
+            gives = c1 < blocks;                // (pos == lo) the CTA of the part before has the rest
+            pos = min(e, stop);
+            if (c0 < c1) return true;
         }
-        hv = (pos - first) / blocks;
-        const int s = first + hv * blocks, e = s + blocks;
-        takes = e > stop;                       // the CTA of the next part has the first e - stop blocks
-        gives = pos > s;                        // (pos == lo) the CTA of the part before has the rest
-        c0 = takes ? e - stop : 0;
-        c1 = gives ? e - pos : blocks;
-        pos = min(e, stop);
-        return true;
+        return false;
     }
 };
 
@@ -633,11 +663,11 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_SREADY ? DS_WARPS : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_YFREE ? 4 : i >= B_FFREE0 ? DS_WARPS + 4 : i >= B_SREADY ? DS_WARPS : 1);
         *flag = 0;
         fence_barrier_init();
     }
-    if (warp == DS_WARPS) {
+    if (warp == DS_MMA) {
         tmem_alloc(smem_addr(const_cast<uint32_t *>(slot_tm)), DS_COLS);
         tmem_relinquish();
     }
@@ -650,71 +680,58 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
     DsWalk w;
     w.start(&cp, part, gridDim.x);
 
-    if (warp == DS_WARPS) {
-        // ------------------------------------------------ loads and products
+    if (warp == DS_LOAD) {
+        // ------------------------------------------------ loads, step t into stage t & 1
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-        // loads run ahead on a walk of their own, step lt into stage lt & 1
-        DsWalk lw = w;
-        bool left = lw.next();
-        int lc = left ? lw.c0 : 0, lt = 0;
-        auto load = [&]() {
-            if (!left) return;
-            if (lane == 0) {
-                const uint32_t st = base + static_cast<uint32_t>((lt & 1) * L::STAGE), fb = bar(B_FULL0 + (lt & 1));
-                const int row = lw.begin + lc * DC_ROWS, hk = lw.hv / (p.Hv / p.Hk);
-                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(2 * L::TILE + DC_BLOCK + DC_ROWS * p.dv * 2));
+        uint32_t t = 0;
+        while (w.next())
+            for (int c = w.c0; c < w.c1; ++c, ++t) {
+                if (t > 1) {                    // step t - 2 has read its row factors and done its products
+                    wait(bar(B_FFREE0 + (t & 1)), (t >> 1) - 1);
+                    wait(bar(B_M0 + (t & 1)), (t >> 1) - 1);
+                }
+                if (lane == 0) {
+                    const uint32_t st = base + (t & 1) * L::STAGE, fb = bar(B_FULL0 + (t & 1));
+                    const int row = w.begin + c * DC_ROWS, hk = w.hv / (p.Hv / p.Hk);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(2 * L::TILE + DC_BLOCK + DC_ROWS * p.dv * 2));
 #pragma unroll
-                for (int j = 0; j < DK / 64; ++j)
-                    tma_load_2d(st + L::K + j * DC_ROWS * 128, &tmK, hk * DK + 64 * j, row, fb, keep);
-                tma_load_2d(st + L::V, &tmV, lw.hv * p.dv, row, fb, once);
-                const uint8_t *blk = cp.blocks + (static_cast<size_t>(dc_base(lw.begin, lw.b) + lc) * p.Hv + lw.hv) * DC_BLOCK;
-                bulk_g2s(st + L::MATS, blk, DC_BLOCK, fb, once);
+                    for (int j = 0; j < DK / 64; ++j)
+                        tma_load_2d(st + L::K + j * DC_ROWS * 128, &tmK, hk * DK + 64 * j, row, fb, keep);
+                    tma_load_2d(st + L::V, &tmV, w.hv * p.dv, row, fb, once);
+                    const uint8_t *blk = cp.blocks + (static_cast<size_t>(dc_base(w.begin, w.b) + c) * p.Hv + w.hv) * DC_BLOCK;
+                    bulk_g2s(st + L::MATS, blk, DC_BLOCK, fb, once);
 #pragma unroll
-                for (int j = 0; j < DK / 64; ++j)
-                    tma_load_2d(st + L::Q + j * DC_ROWS * 128, &tmQ, hk * DK + 64 * j, row, fb, keep);
+                    for (int j = 0; j < DK / 64; ++j)
+                        tma_load_2d(st + L::Q + j * DC_ROWS * 128, &tmQ, hk * DK + 64 * j, row, fb, keep);
+                }
+                __syncwarp();
             }
-            ++lt;
-            if (++lc == lw.c1) {
-                left = lw.next();
-                lc = left ? lw.c0 : 0;
-            }
-        };
-        load();
-        load();
+    } else if (warp == DS_MMA) {
+        // ------------------------------------------------ products
         uint32_t t = 0;
         while (w.next())
             for (int c = w.c0; c < w.c1; ++c, ++t) {
                 const uint32_t st = base + (t & 1) * L::STAGE, kb = st + L::K, qb = st + L::Q, mb = st + L::MATS;
-                const uint32_t y = tmem + DS_Y + 64 * (t & 1);
+                const uint32_t y = tmem + DS_O;
+                auto s_product = [&](uint32_t d, uint32_t rows, int s) {
+                    const uint64_t b = desc_k_sw128(rows + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
+                    tc_mma_f16_ts_warp(d, tmem + DS_SHI + 8 * s, b, ds_idesc(64, false), s > 0);
+                    tc_mma_f16_ts_warp(d, tmem + DS_SLO + 8 * s, b, ds_idesc(64, false), 1);
+                };
                 // P: S x K
-                wait(bar(B_SREADY), t);
                 wait(bar(B_FULL0 + (t & 1)), t >> 1);
+                wait(bar(B_SREADY), t);
                 __syncwarp();
                 tc_fence_after_sync();
 #pragma unroll
-                for (int s = 0; s < DK / 16; ++s) {
-                    const uint64_t d = desc_k_sw128(kb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 8 * s, d, ds_idesc(64, false), s > 0);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SLO + 8 * s, d, ds_idesc(64, false), 1);
-                }
+                for (int s = 0; s < DK / 16; ++s) s_product(tmem + DS_P, kb, s);
                 tc_commit_warp(bar(B_P));
-                // O: S x Q
-                if (t > 1) wait(bar(B_YFREE0 + (t & 1)), (t >> 1) - 1);
+                // O: S x Q, first half
+                if (t > 0) wait(bar(B_YFREE), t - 1);
                 __syncwarp();
                 tc_fence_after_sync();
 #pragma unroll
-                for (int s = 0; s < DK / 16; ++s) {
-                    const uint64_t d = desc_k_sw128(qb + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
-                    tc_mma_f16_ts_warp(y, tmem + DS_SHI + 8 * s, d, ds_idesc(64, false), s > 0);
-                    tc_mma_f16_ts_warp(y, tmem + DS_SLO + 8 * s, d, ds_idesc(64, false), 1);
-                }
-                tc_commit_warp(bar(B_O));
-                // block t - 1 is done with its stage: its products, and (as
-                // SREADY says) its row factors
-                if (t > 0) {
-                    wait(bar(B_M), t - 1);
-                    load();
-                }
+                for (int s = 0; s < DK / 32; ++s) s_product(y, qb, s);
                 // U: r x T; step s (rows 16 s .. of r) reaches the rows from 16 s on only
                 wait(bar(B_RREADY), t);
                 __syncwarp();
@@ -729,6 +746,10 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tc_mma_f16_ts_warp(d, r, lo, id, 1);
                 }
                 tc_commit_warp(bar(B_U));
+                // O, second half
+#pragma unroll
+                for (int s = DK / 32; s < DK / 16; ++s) s_product(y, qb, s);
+                tc_commit_warp(bar(B_O));
                 // D: u' x K
                 wait(bar(B_UREADY), t);
                 __syncwarp();
@@ -736,22 +757,77 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint64_t d = desc_mn_sw128(kb + s * 2048);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 8 * s, d, ds_idesc(DK, true), s > 0);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_SHI + 32 + 8 * s, d, ds_idesc(DK, true), 1);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_U + 8 * s, d, ds_idesc(DK, true), s > 0);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_U + 32 + 8 * s, d, ds_idesc(DK, true), 1);
                 }
                 tc_commit_warp(bar(B_D));
-                // M: u x M on top of the scaled S x Q
+                // M: u x M
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
                     const uint64_t hi = desc_k_sw128(mb + 2 * DC_MAT + off), lo = desc_k_sw128(mb + 3 * DC_MAT + off);
-                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = y + 16 * s, u = tmem + DS_U1 + 8 * s;
-                    tc_mma_f16_ts_warp(d, u, hi, id, 1);
+                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = tmem + DS_M + 16 * s, u = tmem + DS_U1 + 8 * s;
+                    tc_mma_f16_ts_warp(d, u, hi, id, s > 0);
                     tc_mma_f16_ts_warp(d, u + 32, hi, id, 1);
                     tc_mma_f16_ts_warp(d, u, lo, id, 1);
                 }
-                tc_commit_warp(bar(B_M));
+                tc_commit_warp(bar(B_M0 + (t & 1)));
             }
+    } else if (warp >= DS_OUT) {
+        // ------------------------------------------------ outputs
+        const int l = 32 * (warp & 3) + lane;
+        const bool live = l < p.dv;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        auto arrive = [&](int i) {
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(i));
+        };
+        uint32_t t = 0;
+        while (w.next()) {
+            uint16_t *o = p.o + (static_cast<long long>(w.begin) + static_cast<long long>(w.c0) * DC_ROWS) * p.ldo +
+                          static_cast<long long>(w.hv) * p.dv + l;
+            for (int c = w.c0; c < w.c1; ++c, ++t) {
+                const float *f = reinterpret_cast<const float *>(ds_smem + (t & 1) * L::STAGE + L::F) + 2 * DC_ROWS;
+                const int n = live ? w.end - w.begin - c * DC_ROWS : 0;
+                wait(bar(B_FULL0 + (t & 1)), t >> 1);
+                wait(bar(B_M0 + (t & 1)), t >> 1);      // (and O, issued before it)
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int j = 0; j < 64; j += 16) {
+                    uint32_t so[16], mo[16];
+                    tmem_ld<16>(lanes + DS_O + j, so);
+                    tmem_ld<16>(lanes + DS_M + j, mo);
+                    tmem_wait_ld();
+                    if (j == 48) arrive(B_YFREE);
+                    uint32_t w16[8];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 e = *reinterpret_cast<const float4 *>(f + j + i);
+                        w16[i / 2] = pack_bf16x2(fmaf(__uint_as_float(so[i]), e.x, __uint_as_float(mo[i])),
+                                                 fmaf(__uint_as_float(so[i + 1]), e.y, __uint_as_float(mo[i + 1])));
+                        w16[i / 2 + 1] = pack_bf16x2(fmaf(__uint_as_float(so[i + 2]), e.z, __uint_as_float(mo[i + 2])),
+                                                     fmaf(__uint_as_float(so[i + 3]), e.w, __uint_as_float(mo[i + 3])));
+                    }
+                    if (j + 16 <= n) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            *o = static_cast<uint16_t>((i & 1) ? w16[i / 2] >> 16 : w16[i / 2]);
+                            o += p.ldo;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (j + i < n) *o = static_cast<uint16_t>((i & 1) ? w16[i / 2] >> 16 : w16[i / 2]);
+                            o += p.ldo;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_FFREE0 + (t & 1)));
+            }
+        }
     } else {
         // ------------------------------------------------ conversions
         const int q = warp & 3, h = warp >> 2, l = 32 * q + lane;
@@ -759,7 +835,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
         constexpr int SC = DK / 4;              // state columns of a thread
         constexpr int NTHR = DS_WARPS * 32;
-        float s[SC];
+        f32x2 s[SC / 2];
         auto arrive = [&](int i) {              // this warp's tensor memory accesses are done
             tmem_wait_st();
             tc_fence_before_sync();
@@ -783,27 +859,6 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
             }
         }
 
-        // outputs of step t, n rows from o: this thread's rows 16 h .. + 15 of
-        // value l; two lanes trade so that each stores pairs of values
-        auto store_out = [&](uint32_t t, uint16_t *o, int n) {
-            wait(bar(B_M), t);
-            tc_fence_after_sync();
-            uint32_t v[16];
-            tmem_ld<16>(lanes + DS_Y + 64 * (t & 1) + 16 * h, v);
-            tmem_wait_ld();
-            arrive(B_YFREE0 + (t & 1));
-            const bool odd = lane & 1;
-            o += (16 * h + (odd ? 1 : 0)) * p.ldo + (l & ~1);
-            n -= 16 * h + (odd ? 1 : 0);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float give = __uint_as_float(odd ? v[i] : v[i + 1]), own = __uint_as_float(odd ? v[i + 1] : v[i]);
-                const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-                if (live && i < n) *reinterpret_cast<uint32_t *>(o) = odd ? pack_bf16x2(got, own) : pack_bf16x2(own, got);
-                o += 2 * p.ldo;
-            }
-        };
-
         uint32_t t = 0;
         while (w.next()) {
             float *srow = p.state + ((static_cast<size_t>(w.slot) * p.Hv + w.hv) * p.dv + (live ? l : 0)) * DK + h * SC;
@@ -821,13 +876,9 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
             for (int i = 0; i < SC; i += 4) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (live && (w.takes || !cp.zero_init)) v = __ldcg(reinterpret_cast<const float4 *>(srow + i));
-                s[i] = v.x;
-                s[i + 1] = v.y;
-                s[i + 2] = v.z;
-                s[i + 3] = v.w;
+                s[i / 2] = pack_x2(v.x, v.y);
+                s[i / 2 + 1] = pack_x2(v.z, v.w);
             }
-            uint16_t *o = p.o + (static_cast<long long>(w.begin) + static_cast<long long>(w.c0) * DC_ROWS) * p.ldo +
-                          static_cast<long long>(w.hv) * p.dv;
             for (int c = w.c0; c < w.c1; ++c, ++t) {
                 uint8_t *stage = ds_smem + (t & 1) * L::STAGE;
                 const int n = min(DC_ROWS, w.end - w.begin - c * DC_ROWS);
@@ -844,81 +895,71 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 {   // the state's two terms
                     uint32_t hi[SC / 2], lo[SC / 2];
 #pragma unroll
-                    for (int i = 0; i < SC / 2; ++i) split_bf16x2(s[2 * i], s[2 * i + 1], hi[i], lo[i]);
+                    for (int i = 0; i < SC / 2; ++i) split_bf16x2(s[i], hi[i], lo[i]);
+                    if (t > 0) wait(bar(B_O), t - 1);   // the last state's terms have been read
                     tmem_st<SC / 2>(lanes + DS_SHI + h * (SC / 2), hi);
                     tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
                     arrive(B_SREADY);
                 }
-                if (c > w.c0) store_out(t - 1, o - DC_ROWS * p.ldo, DC_ROWS);
-                o += DC_ROWS * p.ldo;
                 const float *f = reinterpret_cast<const float *>(stage + L::F);
                 uint32_t v[16], hi[8], lo[8];
                 wait(bar(B_FULL0 + (t & 1)), t >> 1);
                 {   // r = v - e^G r_k (S k)
                     const uint16_t *vt = reinterpret_cast<const uint16_t *>(stage + L::V) + 16 * h * p.dv + (live ? l : 0);
-                    float val[16];
+                    f32x2 val[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) val[i] = bf16_bits_to_float(vt[i * p.dv]);
+                    for (int i = 0; i < 8; ++i)
+                        val[i] = pack_x2(bf16_bits_to_float(vt[2 * i * p.dv]), bf16_bits_to_float(vt[(2 * i + 1) * p.dv]));
                     wait(bar(B_P), t);
                     tc_fence_after_sync();
                     tmem_ld<16>(lanes + DS_P + 16 * h, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4 *>(f + 16 * h + i);
-                        val[i] = fmaf(-e.x, __uint_as_float(v[i]), val[i]);
-                        val[i + 1] = fmaf(-e.y, __uint_as_float(v[i + 1]), val[i + 1]);
-                        val[i + 2] = fmaf(-e.z, __uint_as_float(v[i + 2]), val[i + 2]);
-                        val[i + 3] = fmaf(-e.w, __uint_as_float(v[i + 3]), val[i + 3]);
+                    for (int i = 0; i < 8; i += 2) {        // (the factors are stored negated)
+                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(f + 16 * h + 2 * i);
+                        val[i] = fma_x2(e.x, pair_x2(v[2 * i], v[2 * i + 1]), val[i]);
+                        val[i + 1] = fma_x2(e.y, pair_x2(v[2 * i + 2], v[2 * i + 3]), val[i + 1]);
                     }
                     const int m = live ? n - 16 * h : 0;
                     if (m < 16)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i >= m) val[i] = 0.f;
+                        for (int i = 0; i < 8; ++i) {
+                            if (2 * i >= m) val[i] = 0ull;
+                            if (2 * i + 1 == m) val[i] &= 0xFFFFFFFFull;
+                        }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split_bf16x2(val[2 * i], val[2 * i + 1], hi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) split_bf16x2(val[i], hi[i], lo[i]);
                     tmem_st<8>(lanes + DS_R + 8 * h, hi);
                     tmem_st<8>(lanes + DS_R + 32 + 8 * h, lo);
                     arrive(B_RREADY);
-                }
-                {   // scale the columns of S q while r x T runs
-                    wait(bar(B_O), t);
-                    tc_fence_after_sync();
-                    const uint32_t y = lanes + DS_Y + 64 * (t & 1) + 16 * h;
-                    tmem_ld<16>(y, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4 *>(f + 2 * DC_ROWS + 16 * h + i);
-                        v[i] = __float_as_uint(__uint_as_float(v[i]) * e.x);
-                        v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) * e.y);
-                        v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) * e.z);
-                        v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) * e.w);
-                    }
-                    tmem_st<16>(y, v);
                 }
                 {   // u' = u e^(G_n - G) r_k, and u
                     wait(bar(B_U), t);
                     tc_fence_after_sync();
                     tmem_ld<16>(lanes + DS_U + 16 * h, v);
                     tmem_wait_ld();
+                    tc_fence_before_sync();
+                    named_bar_sync(2 + q, 128);     // the four warps of these lanes have read u: u' goes over it
+                    tc_fence_after_sync();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4 *>(f + DC_ROWS + 16 * h + i);
-                        split_bf16x2(__uint_as_float(v[i]) * e.x, __uint_as_float(v[i + 1]) * e.y, hi[i / 2], lo[i / 2]);
-                        split_bf16x2(__uint_as_float(v[i + 2]) * e.z, __uint_as_float(v[i + 3]) * e.w, hi[i / 2 + 1], lo[i / 2 + 1]);
+                    for (int i = 0; i < 8; i += 2) {
+                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(f + DC_ROWS + 16 * h + 2 * i);
+                        split_bf16x2(mul_x2(e.x, pair_x2(v[2 * i], v[2 * i + 1])), hi[i], lo[i]);
+                        split_bf16x2(mul_x2(e.y, pair_x2(v[2 * i + 2], v[2 * i + 3])), hi[i + 1], lo[i + 1]);
                     }
-                    tmem_st<8>(lanes + DS_SHI + 8 * h, hi);
-                    tmem_st<8>(lanes + DS_SHI + 32 + 8 * h, lo);
+                    tmem_st<8>(lanes + DS_U + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_U + 32 + 8 * h, lo);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), hi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) split_bf16x2(pair_x2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
+                    if (t > 0) wait(bar(B_M0 + ((t - 1) & 1)), (t - 1) >> 1);   // the last u has been read
                     tmem_st<8>(lanes + DS_U1 + 8 * h, hi);
                     tmem_st<8>(lanes + DS_U1 + 32 + 8 * h, lo);
                     arrive(B_UREADY);
                 }
                 {   // S <- e^(G_n) S + D
-                    const float decay = f[3 * DC_ROWS];
+                    const f32x2 decay = pack_x2(f[3 * DC_ROWS], f[3 * DC_ROWS]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_FFREE0 + (t & 1)));
                     wait(bar(B_D), t);
                     tc_fence_after_sync();
 #pragma unroll
@@ -926,15 +967,14 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                         tmem_ld<16>(lanes + DS_P + h * SC + j, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) s[j + i] = fmaf(decay, s[j + i], __uint_as_float(v[i]));
+                        for (int i = 0; i < 8; ++i) s[j / 2 + i] = fma_x2(decay, s[j / 2 + i], pair_x2(v[2 * i], v[2 * i + 1]));
                     }
                 }
             }
-            store_out(t - 1, o - DC_ROWS * p.ldo, min(DC_ROWS, w.end - w.begin - (w.c1 - 1) * DC_ROWS));
             if (live)
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
-                    *reinterpret_cast<float4 *>(srow + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                    *reinterpret_cast<ulonglong2 *>(srow + i) = make_ulonglong2(s[i / 2], s[i / 2 + 1]);
             if (w.gives) {                      // the rest of the chain is the CTA's of the part before
                 named_bar_sync(1, NTHR);
                 if (threadIdx.x == 0) red_add_release_gpu(cp.flags + part, 1u);
@@ -945,7 +985,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
     // waited for each
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == DS_WARPS) {
+    if (warp == DS_MMA) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, DS_COLS);
     }

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "gated_delta.cuh"
 #include "sv_ptx.cuh"
 
 namespace sv {
@@ -23,6 +24,26 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uin
 {
     hi = pack_bf16x2(a, b);
     lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// Two fp32 values as tensor memory gives them, as a packed pair.
+__device__ __forceinline__ f32x2 pair_x2(uint32_t lo, uint32_t hi)
+{
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
+// The split of a packed pair.
+__device__ __forceinline__ void split_bf16x2(f32x2 v, uint32_t &hi, uint32_t &lo)
+{
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+    hi = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+    f32x2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(pair_x2(hi << 16, hi & 0xFFFF0000u)));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(r));
+    lo = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
 }
 
 // Shared-memory descriptor of an operand whose rows run along the products'
@@ -75,6 +96,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N])
                    "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                  : "r"(taddr)
                  : "memory");
+}
+
+// Whether the phase of that parity has completed; the thread may sleep up to
+// `ns` nanoseconds for it, so that waiting warps take no issue slots.
+__device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity, uint32_t ns)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
+    return ok != 0;
 }
 
 }  // namespace sv
