@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 //   P      S (2 terms, 0..127) x K               P  128..191
 //   O      S x Q                                 O  320..383
 //   U      r (2, 192..255) x T (2)               U  256..319
-//   D      u' (2, 256..319 over u) x K           D  128..255 (over P and r)
-//   M      u (2, 448..511) x M (2)               M  384..447
+//   D      u' (2, 448..511) x K                  D  128..255 (over P and r)
+//   M      u (2, 256..319 over U) x M (2)        M  384..447
 //
 // (of a product of two two-term factors lo x lo is left out).  Warps 0-15
 // convert between the products: warp w has lanes 32 (w & 3) .. + 31 and a
@@ -519,7 +519,7 @@ constexpr int DS_OUT = 16, DS_MMA = 20, DS_LOAD = 21;   // first output warp, th
 constexpr int DS_THREADS = 22 * 32;
 constexpr int DS_EXTRA = 2;
 constexpr uint32_t DS_COLS = 512;
-constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_O = 320, DS_M = 384, DS_U1 = 448;
+constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_O = 320, DS_M = 384, DS_UP = 448;
 
 template <int DK>
 struct DsSmem {                                 // from a 1024-byte boundary
@@ -532,7 +532,7 @@ struct DsSmem {                                 // from a 1024-byte boundary
 
 // Barriers that a waiter could find two phases ahead come in pairs, one for
 // even and one for odd steps: their next phase needs the waiter to go on.
-enum { B_FULL0, B_FULL1, B_P, B_O, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_FFREE0, B_FFREE1, B_YFREE, B_COUNT };
+enum { B_FULL0, B_FULL1, B_P, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_MREADY, B_FFREE0, B_FFREE1, B_YFREE, B_COUNT };
 
 constexpr uint32_t ds_idesc(int n, bool b_mn)
 {
@@ -541,16 +541,22 @@ constexpr uint32_t ds_idesc(int n, bool b_mn)
            ((128u >> 4) << 24);
 }
 
+// The rare long wait, out of line: the roles' loops share the instruction cache.
+static __device__ __noinline__ void ds_long_wait(uint32_t bar, uint32_t parity, volatile int *flag, int *err)
+{
+    if (mbar_wait_bounded(bar, parity, *flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) return;
+    *flag = 1;
+    atomicOr(err, 2);
+}
+
+// Whole warps wait (with one lane polling for the others the prompts' scan
+// took 298 instead of 255 us).
 struct DsWait {
     volatile int *flag;
     int *err;
     __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const
     {
-        if (mbar_sleep_wait(bar, parity & 1u, 100000u)) return;
-        if (!mbar_wait_bounded(bar, parity & 1u, *flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) {
-            *flag = 1;
-            atomicOr(err, 2);
-        }
+        if (!mbar_sleep_wait(bar, parity & 1u, 100000u)) ds_long_wait(bar, parity & 1u, flag, err);
     }
 };
 
@@ -732,6 +738,8 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < DK / 32; ++s) s_product(y, qb, s);
+                // (the last M has read its u: U goes over it)
+                if (t > 0) wait(bar(B_M0 + ((t - 1) & 1)), (t - 1) >> 1);
                 // U: r x T; step s (rows 16 s .. of r) reaches the rows from 16 s on only
                 wait(bar(B_RREADY), t);
                 __syncwarp();
@@ -749,7 +757,6 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 // O, second half
 #pragma unroll
                 for (int s = DK / 32; s < DK / 16; ++s) s_product(y, qb, s);
-                tc_commit_warp(bar(B_O));
                 // D: u' x K
                 wait(bar(B_UREADY), t);
                 __syncwarp();
@@ -757,16 +764,19 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint64_t d = desc_mn_sw128(kb + s * 2048);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_U + 8 * s, d, ds_idesc(DK, true), s > 0);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_U + 32 + 8 * s, d, ds_idesc(DK, true), 1);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 8 * s, d, ds_idesc(DK, true), s > 0);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 32 + 8 * s, d, ds_idesc(DK, true), 1);
                 }
                 tc_commit_warp(bar(B_D));
                 // M: u x M
+                wait(bar(B_MREADY), t);
+                __syncwarp();
+                tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
                     const uint64_t hi = desc_k_sw128(mb + 2 * DC_MAT + off), lo = desc_k_sw128(mb + 3 * DC_MAT + off);
-                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = tmem + DS_M + 16 * s, u = tmem + DS_U1 + 8 * s;
+                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = tmem + DS_M + 16 * s, u = tmem + DS_U + 8 * s;
                     tc_mma_f16_ts_warp(d, u, hi, id, s > 0);
                     tc_mma_f16_ts_warp(d, u + 32, hi, id, 1);
                     tc_mma_f16_ts_warp(d, u, lo, id, 1);
@@ -859,7 +869,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
             }
         }
 
-        uint32_t t = 0;
+        uint32_t t = 0, vals[8];
         while (w.next()) {
             float *srow = p.state + ((static_cast<size_t>(w.slot) * p.Hv + w.hv) * p.dv + (live ? l : 0)) * DK + h * SC;
             if (w.takes) {                      // the CTA of the next part hands the state over
@@ -896,29 +906,32 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     uint32_t hi[SC / 2], lo[SC / 2];
 #pragma unroll
                     for (int i = 0; i < SC / 2; ++i) split_bf16x2(s[i], hi[i], lo[i]);
-                    if (t > 0) wait(bar(B_O), t - 1);   // the last state's terms have been read
+                    // (the last state's terms have been read: O is issued before D, which has been waited for)
                     tmem_st<SC / 2>(lanes + DS_SHI + h * (SC / 2), hi);
                     tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
                     arrive(B_SREADY);
                 }
                 const float *f = reinterpret_cast<const float *>(stage + L::F);
                 uint32_t v[16], hi[8], lo[8];
-                wait(bar(B_FULL0 + (t & 1)), t >> 1);
-                {   // r = v - e^G r_k (S k)
-                    const uint16_t *vt = reinterpret_cast<const uint16_t *>(stage + L::V) + 16 * h * p.dv + (live ? l : 0);
-                    f32x2 val[8];
+                // this thread's values of a step, rows in pairs; read a step ahead where there is one
+                auto load_v = [&](uint32_t step) {
+                    const uint16_t *vt = reinterpret_cast<const uint16_t *>(ds_smem + (step & 1) * L::STAGE + L::V) + 16 * h * p.dv + (live ? l : 0);
+                    wait(bar(B_FULL0 + (step & 1)), step >> 1);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        val[i] = pack_x2(bf16_bits_to_float(vt[2 * i * p.dv]), bf16_bits_to_float(vt[(2 * i + 1) * p.dv]));
+                    for (int i = 0; i < 8; ++i) vals[i] = vt[2 * i * p.dv] | (static_cast<uint32_t>(vt[(2 * i + 1) * p.dv]) << 16);
+                };
+                if (c == w.c0) load_v(t);
+                {   // r = v - e^G r_k (S k)
                     wait(bar(B_P), t);
                     tc_fence_after_sync();
                     tmem_ld<16>(lanes + DS_P + 16 * h, v);
                     tmem_wait_ld();
+                    f32x2 val[8];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {        // (the factors are stored negated)
                         const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(f + 16 * h + 2 * i);
-                        val[i] = fma_x2(e.x, pair_x2(v[2 * i], v[2 * i + 1]), val[i]);
-                        val[i + 1] = fma_x2(e.y, pair_x2(v[2 * i + 2], v[2 * i + 3]), val[i + 1]);
+                        val[i] = fma_x2(e.x, pair_x2(v[2 * i], v[2 * i + 1]), pair_x2(vals[i] << 16, vals[i] & 0xFFFF0000u));
+                        val[i + 1] = fma_x2(e.y, pair_x2(v[2 * i + 2], v[2 * i + 3]), pair_x2(vals[i + 1] << 16, vals[i + 1] & 0xFFFF0000u));
                     }
                     const int m = live ? n - 16 * h : 0;
                     if (m < 16)
@@ -938,23 +951,26 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tc_fence_after_sync();
                     tmem_ld<16>(lanes + DS_U + 16 * h, v);
                     tmem_wait_ld();
-                    tc_fence_before_sync();
-                    named_bar_sync(2 + q, 128);     // the four warps of these lanes have read u: u' goes over it
-                    tc_fence_after_sync();
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(f + DC_ROWS + 16 * h + 2 * i);
                         split_bf16x2(mul_x2(e.x, pair_x2(v[2 * i], v[2 * i + 1])), hi[i], lo[i]);
                         split_bf16x2(mul_x2(e.y, pair_x2(v[2 * i + 2], v[2 * i + 3])), hi[i + 1], lo[i + 1]);
                     }
-                    tmem_st<8>(lanes + DS_U + 8 * h, hi);
-                    tmem_st<8>(lanes + DS_U + 32 + 8 * h, lo);
+                    tmem_st<8>(lanes + DS_UP + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_UP + 32 + 8 * h, lo);
+                    arrive(B_UREADY);
+                    // off the chain, while D runs: u's terms over U, which the four
+                    // warps of these lanes have read, and the next values
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split_bf16x2(pair_x2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
-                    if (t > 0) wait(bar(B_M0 + ((t - 1) & 1)), (t - 1) >> 1);   // the last u has been read
-                    tmem_st<8>(lanes + DS_U1 + 8 * h, hi);
-                    tmem_st<8>(lanes + DS_U1 + 32 + 8 * h, lo);
-                    arrive(B_UREADY);
+                    tc_fence_before_sync();
+                    named_bar_sync(2 + q, 128);
+                    tc_fence_after_sync();
+                    tmem_st<8>(lanes + DS_U + 8 * h, hi);
+                    tmem_st<8>(lanes + DS_U + 32 + 8 * h, lo);
+                    arrive(B_MREADY);
+                    if (c + 1 < w.c1) load_v(t + 1);
                 }
                 {   // S <- e^(G_n) S + D
                     const f32x2 decay = pack_x2(f[3 * DC_ROWS], f[3 * DC_ROWS]);
