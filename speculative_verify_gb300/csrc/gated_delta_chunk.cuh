@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 // (of a product of two two-term factors lo x lo is left out).  Warps 0-15
 // convert between the products: warp w has lanes 32 (w & 3) .. + 31 and a
 // quarter w >> 2 of the columns; the state's fp32 values stay in their
-// registers.  Warps 16-19 add up the outputs and write them, warp 20 issues
-// the products, warp 21 the loads, two blocks ahead.
+// registers; they write a block's outputs while the next one's P runs.  Warp
+// 16 issues the products, warp 17 the loads, two blocks ahead.
 //
 // The chain of a block, P, r, U, u', D, S, bounds the kernel; O, M and the
 // outputs fill its gaps.  Measured (cycles of a block, 128 x 128 states): P
@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 // two.  A CTA waits for CTAs of lower blockIdx only.
 
 constexpr int DS_WARPS = 16;                    // converting warps
-constexpr int DS_OUT = 16, DS_MMA = 20, DS_LOAD = 21;   // first output warp, the issuing warps
-constexpr int DS_THREADS = 22 * 32;
+constexpr int DS_MMA = 16, DS_LOAD = 17;        // the issuing warps
+constexpr int DS_THREADS = 18 * 32;
 constexpr int DS_EXTRA = 2;
 constexpr uint32_t DS_COLS = 512;
 constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, DS_O = 320, DS_M = 384, DS_UP = 448;
@@ -524,15 +524,16 @@ constexpr uint32_t DS_SHI = 0, DS_SLO = 64, DS_P = 128, DS_R = 192, DS_U = 256, 
 template <int DK>
 struct DsSmem {                                 // from a 1024-byte boundary
     static constexpr int TILE = DC_ROWS * DK * 2;   // keys or queries: DK / 64 boxes of [64 rows][128 bytes]
-    static constexpr int K = 0, Q = TILE, MATS = 2 * TILE, F = MATS + 4 * DC_MAT, V = F + DC_FACTORS;   // V [64][dv]
+    static constexpr int K = 0, Q = TILE, MATS = 2 * TILE, V = MATS + 4 * DC_MAT;   // V [64][dv]
     static constexpr int STAGE = V + DC_ROWS * 128 * 2;
-    static constexpr int BARS = 2 * STAGE;
+    static constexpr int F = 2 * STAGE;         // row factors, four buffers: they are read later than the rest
+    static constexpr int BARS = F + 4 * DC_FACTORS;
     static constexpr int BYTES = BARS + 256;
 };
 
 // Barriers that a waiter could find two phases ahead come in pairs, one for
 // even and one for odd steps: their next phase needs the waiter to go on.
-enum { B_FULL0, B_FULL1, B_P, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_MREADY, B_FFREE0, B_FFREE1, B_YFREE, B_COUNT };
+enum { B_FULL0, B_FULL1, B_P, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_MREADY, B_YFREE, B_COUNT };
 
 constexpr uint32_t ds_idesc(int n, bool b_mn)
 {
@@ -669,7 +670,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_YFREE ? 4 : i >= B_FFREE0 ? DS_WARPS + 4 : i >= B_SREADY ? DS_WARPS : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_SREADY ? DS_WARPS : 1);
         *flag = 0;
         fence_barrier_init();
     }
@@ -692,10 +693,10 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         uint32_t t = 0;
         while (w.next())
             for (int c = w.c0; c < w.c1; ++c, ++t) {
-                if (t > 1) {                    // step t - 2 has read its row factors and done its products
-                    wait(bar(B_FFREE0 + (t & 1)), (t >> 1) - 1);
-                    wait(bar(B_M0 + (t & 1)), (t >> 1) - 1);
-                }
+                // Step t - 2's products are done, so its values have been read
+                // (r came before U), and so have the row factors of step
+                // t - 4 (step t - 2's O followed the outputs of step t - 3).
+                if (t > 1) wait(bar(B_M0 + (t & 1)), (t >> 1) - 1);
                 if (lane == 0) {
                     const uint32_t st = base + (t & 1) * L::STAGE, fb = bar(B_FULL0 + (t & 1));
                     const int row = w.begin + c * DC_ROWS, hk = w.hv / (p.Hv / p.Hk);
@@ -705,10 +706,20 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                         tma_load_2d(st + L::K + j * DC_ROWS * 128, &tmK, hk * DK + 64 * j, row, fb, keep);
                     tma_load_2d(st + L::V, &tmV, w.hv * p.dv, row, fb, once);
                     const uint8_t *blk = cp.blocks + (static_cast<size_t>(dc_base(w.begin, w.b) + c) * p.Hv + w.hv) * DC_BLOCK;
-                    bulk_g2s(st + L::MATS, blk, DC_BLOCK, fb, once);
+                    bulk_g2s(st + L::MATS, blk, 4 * DC_MAT, fb, once);
+                    bulk_g2s(base + L::F + (t & 3) * DC_FACTORS, blk + 4 * DC_MAT, DC_FACTORS, fb, once);
 #pragma unroll
                     for (int j = 0; j < DK / 64; ++j)
                         tma_load_2d(st + L::Q + j * DC_ROWS * 128, &tmQ, hk * DK + 64 * j, row, fb, keep);
+                    if (c + 1 < w.c1) {         // the next block's on its way to L2
+#pragma unroll
+                        for (int j = 0; j < DK / 64; ++j) {
+                            prefetch_l2_2d(&tmK, hk * DK + 64 * j, row + DC_ROWS);
+                            prefetch_l2_2d(&tmQ, hk * DK + 64 * j, row + DC_ROWS);
+                        }
+                        prefetch_l2_2d(&tmV, w.hv * p.dv, row + DC_ROWS);
+                        prefetch_l2(blk + static_cast<size_t>(p.Hv) * DC_BLOCK, DC_BLOCK);
+                    }
                 }
                 __syncwarp();
             }
@@ -783,61 +794,6 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 }
                 tc_commit_warp(bar(B_M0 + (t & 1)));
             }
-    } else if (warp >= DS_OUT) {
-        // ------------------------------------------------ outputs
-        const int l = 32 * (warp & 3) + lane;
-        const bool live = l < p.dv;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        auto arrive = [&](int i) {
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(i));
-        };
-        uint32_t t = 0;
-        while (w.next()) {
-            uint16_t *o = p.o + (static_cast<long long>(w.begin) + static_cast<long long>(w.c0) * DC_ROWS) * p.ldo +
-                          static_cast<long long>(w.hv) * p.dv + l;
-            for (int c = w.c0; c < w.c1; ++c, ++t) {
-                const float *f = reinterpret_cast<const float *>(ds_smem + (t & 1) * L::STAGE + L::F) + 2 * DC_ROWS;
-                const int n = live ? w.end - w.begin - c * DC_ROWS : 0;
-                wait(bar(B_FULL0 + (t & 1)), t >> 1);
-                wait(bar(B_M0 + (t & 1)), t >> 1);      // (and O, issued before it)
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int j = 0; j < 64; j += 16) {
-                    uint32_t so[16], mo[16];
-                    tmem_ld<16>(lanes + DS_O + j, so);
-                    tmem_ld<16>(lanes + DS_M + j, mo);
-                    tmem_wait_ld();
-                    if (j == 48) arrive(B_YFREE);
-                    uint32_t w16[8];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4 *>(f + j + i);
-                        w16[i / 2] = pack_bf16x2(fmaf(__uint_as_float(so[i]), e.x, __uint_as_float(mo[i])),
-                                                 fmaf(__uint_as_float(so[i + 1]), e.y, __uint_as_float(mo[i + 1])));
-                        w16[i / 2 + 1] = pack_bf16x2(fmaf(__uint_as_float(so[i + 2]), e.z, __uint_as_float(mo[i + 2])),
-                                                     fmaf(__uint_as_float(so[i + 3]), e.w, __uint_as_float(mo[i + 3])));
-                    }
-                    if (j + 16 <= n) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            *o = static_cast<uint16_t>((i & 1) ? w16[i / 2] >> 16 : w16[i / 2]);
-                            o += p.ldo;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (j + i < n) *o = static_cast<uint16_t>((i & 1) ? w16[i / 2] >> 16 : w16[i / 2]);
-                            o += p.ldo;
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_FFREE0 + (t & 1)));
-            }
-        }
     } else {
         // ------------------------------------------------ conversions
         const int q = warp & 3, h = warp >> 2, l = 32 * q + lane;
@@ -869,6 +825,40 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
             }
         }
 
+        // Outputs of a step, this thread's rows 16 h .. + 15 of value l: added
+        // up as soon as O and M are there, stored later (n rows from o).
+        uint32_t outs[8];
+        auto take_out = [&](uint32_t t) {
+            const float *f = reinterpret_cast<const float *>(ds_smem + L::F + (t & 3) * DC_FACTORS) + 2 * DC_ROWS + 16 * h;
+            wait(bar(B_M0 + (t & 1)), t >> 1);      // (and O, issued before it)
+            tc_fence_after_sync();
+            uint32_t so[16], mo[16];
+            tmem_ld<16>(lanes + DS_O + 16 * h, so);
+            tmem_ld<16>(lanes + DS_M + 16 * h, mo);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 e = *reinterpret_cast<const float4 *>(f + i);
+                outs[i / 2] = pack_bf16x2(fmaf(__uint_as_float(so[i]), e.x, __uint_as_float(mo[i])),
+                                          fmaf(__uint_as_float(so[i + 1]), e.y, __uint_as_float(mo[i + 1])));
+                outs[i / 2 + 1] = pack_bf16x2(fmaf(__uint_as_float(so[i + 2]), e.z, __uint_as_float(mo[i + 2])),
+                                              fmaf(__uint_as_float(so[i + 3]), e.w, __uint_as_float(mo[i + 3])));
+            }
+            arrive(B_YFREE);
+        };
+        auto store_out = [&](uint16_t *o, int n) {
+            o += 16 * h * p.ldo + l;
+            n = live ? n - 16 * h : 0;
+            if (n >= 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i, o += p.ldo) *o = static_cast<uint16_t>((i & 1) ? outs[i / 2] >> 16 : outs[i / 2]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i, o += p.ldo)
+                    if (i < n) *o = static_cast<uint16_t>((i & 1) ? outs[i / 2] >> 16 : outs[i / 2]);
+            }
+        };
+
         uint32_t t = 0, vals[8];
         while (w.next()) {
             float *srow = p.state + ((static_cast<size_t>(w.slot) * p.Hv + w.hv) * p.dv + (live ? l : 0)) * DK + h * SC;
@@ -889,6 +879,8 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 s[i / 2] = pack_x2(v.x, v.y);
                 s[i / 2 + 1] = pack_x2(v.z, v.w);
             }
+            uint16_t *o = p.o + (static_cast<long long>(w.begin) + static_cast<long long>(w.c0) * DC_ROWS) * p.ldo +
+                          static_cast<long long>(w.hv) * p.dv;
             for (int c = w.c0; c < w.c1; ++c, ++t) {
                 uint8_t *stage = ds_smem + (t & 1) * L::STAGE;
                 const int n = min(DC_ROWS, w.end - w.begin - c * DC_ROWS);
@@ -911,16 +903,17 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
                     arrive(B_SREADY);
                 }
-                const float *f = reinterpret_cast<const float *>(stage + L::F);
+                if (c > w.c0) take_out(t - 1);
+                const float *f = reinterpret_cast<const float *>(ds_smem + L::F + (t & 3) * DC_FACTORS);
                 uint32_t v[16], hi[8], lo[8];
-                // this thread's values of a step, rows in pairs; read a step ahead where there is one
+                // this thread's values, rows in pairs
                 auto load_v = [&](uint32_t step) {
                     const uint16_t *vt = reinterpret_cast<const uint16_t *>(ds_smem + (step & 1) * L::STAGE + L::V) + 16 * h * p.dv + (live ? l : 0);
                     wait(bar(B_FULL0 + (step & 1)), step >> 1);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) vals[i] = vt[2 * i * p.dv] | (static_cast<uint32_t>(vt[(2 * i + 1) * p.dv]) << 16);
                 };
-                if (c == w.c0) load_v(t);
+                load_v(t);
                 {   // r = v - e^G r_k (S k)
                     wait(bar(B_P), t);
                     tc_fence_after_sync();
@@ -946,6 +939,10 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tmem_st<8>(lanes + DS_R + 32 + 8 * h, lo);
                     arrive(B_RREADY);
                 }
+                if (c > w.c0) {                 // while U runs
+                    store_out(o, DC_ROWS);
+                    o += DC_ROWS * p.ldo;
+                }
                 {   // u' = u e^(G_n - G) r_k, and u
                     wait(bar(B_U), t);
                     tc_fence_after_sync();
@@ -961,7 +958,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tmem_st<8>(lanes + DS_UP + 32 + 8 * h, lo);
                     arrive(B_UREADY);
                     // off the chain, while D runs: u's terms over U, which the four
-                    // warps of these lanes have read, and the next values
+                    // warps of these lanes have read
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split_bf16x2(pair_x2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
                     tc_fence_before_sync();
@@ -970,12 +967,9 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     tmem_st<8>(lanes + DS_U + 8 * h, hi);
                     tmem_st<8>(lanes + DS_U + 32 + 8 * h, lo);
                     arrive(B_MREADY);
-                    if (c + 1 < w.c1) load_v(t + 1);
                 }
                 {   // S <- e^(G_n) S + D
                     const f32x2 decay = pack_x2(f[3 * DC_ROWS], f[3 * DC_ROWS]);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_FFREE0 + (t & 1)));
                     wait(bar(B_D), t);
                     tc_fence_after_sync();
 #pragma unroll
@@ -991,6 +985,8 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
                     *reinterpret_cast<ulonglong2 *>(srow + i) = make_ulonglong2(s[i / 2], s[i / 2 + 1]);
+            take_out(t - 1);
+            store_out(o, min(DC_ROWS, w.end - w.begin - (w.c1 - 1) * DC_ROWS));
             if (w.gives) {                      // the rest of the chain is the CTA's of the part before
                 named_bar_sync(1, NTHR);
                 if (threadIdx.x == 0) red_add_release_gpu(cp.flags + part, 1u);

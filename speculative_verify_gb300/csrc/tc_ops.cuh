@@ -110,4 +110,17 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity, u
     return ok != 0;
 }
 
+// Start a later copy's way from HBM: the bytes (a multiple of 16, 16-byte
+// aligned), or a box of a tensor map, into L2.
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2_2d(const void *tmap, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1) : "memory");
+}
+
 }  // namespace sv
