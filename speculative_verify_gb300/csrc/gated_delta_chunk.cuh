@@ -278,33 +278,31 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
         __syncthreads();                        // the inputs, or the last head's matrices, have been read
         const int e4 = r & (DC_HEADS - 1);
         if (e4 == 0) {
-            // gates of the next heads, one a warp, two rows a lane.  The
-            // running sum keeps more than fp32: differences of large sums
-            // give the decays between near rows.
+            // gates of the next heads, one a warp, two rows a lane
             const int hv = hk * rep + r + warp;
             if (r + warp < rep) {
-                double gd[2];
+                Sum2 G[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
                     float v = t < n ? p.rows.g[(row0 + t) * p.rows.ldg + hv] : 0.f;
                     if (v < DC_MIN_LOG) v = DC_MIN_LOG;
-                    gd[e] = static_cast<double>(v);
+                    G[e] = Sum2{v, 0.f};
                     sm.beta[warp][t] = t < n ? p.rows.beta[(row0 + t) * p.rows.ldg + hv] : 0.f;
                 }
-                double sum = gd[0] + gd[1];
-                const double own = sum;
+                Sum2 run = add2(G[0], G[1]);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double below = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                    if (lane >= o) sum += below;
+                    const Sum2 below{__shfl_up_sync(0xFFFFFFFFu, run.hi, o), __shfl_up_sync(0xFFFFFFFFu, run.lo, o)};
+                    if (lane >= o) run = add2(below, run);
                 }
-                const double G[2] = {sum - own + gd[0], sum};
-                float hi[2], lo[2];
+                Sum2 before{__shfl_up_sync(0xFFFFFFFFu, run.hi, 1), __shfl_up_sync(0xFFFFFFFFu, run.lo, 1)};
+                if (lane == 0) before = Sum2{0.f, 0.f};
+                G[0] = add2(before, G[0]);
+                G[1] = run;
+                const float hi[2] = {G[0].hi, G[1].hi}, lo[2] = {G[0].lo, G[1].lo};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    hi[e] = static_cast<float>(G[e]);
-                    lo[e] = static_cast<float>(G[e] - static_cast<double>(hi[e]));
                     sm.g_hi[warp][2 * lane + e] = hi[e];
                     sm.g_lo[warp][2 * lane + e] = lo[e];
                 }
@@ -362,7 +360,6 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
                         a[e] = j < i ? ck[j8][2 * h + e] * (d * bi) : 0.f;
                     }
                 }
-                if (i >= n) m[0] = m[1] = a[0] = a[1] = 0.f;     // (0 x inf where decays grow)
                 uint32_t hi, lo;
                 split_bf16x2(m[0], m[1], hi, lo);
                 *reinterpret_cast<uint32_t *>(out + 2 * DC_MAT + dc_swizzled(i, j0)) = hi;
