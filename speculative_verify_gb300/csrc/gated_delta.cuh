@@ -475,28 +475,34 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
     float *us = ms + NQR * AST;                                 // [cols][AST]
     pdl_launch_dependents();
     pdl_wait_prior();
+    int na = p.prev_T;                          // accepted rows
+    const int accept = p.accept_len && na > 0 ? p.accept_len[b] : na;
     const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
     uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
     if (slot < 0) {                             // an inactive entry: its outputs are zero
         for (int i = tid; i < p.T * cols; i += nthr) o[(i / cols) * p.ldo + i % cols] = 0;
         return;
     }
-    // the state's rows 16 warp + g and + 8, columns 8 j + 2 c, + 1
-    float *srow = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0 + 16 * warp + g) * DK + 2 * c;
-    float st[DK / 8][4];
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j) {
-        const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * j), y = *reinterpret_cast<const float2 *>(srow + 8 * DK + 8 * j);
-        st[j][0] = x.x;
-        st[j][1] = x.y;
-        st[j][2] = y.x;
-        st[j][3] = y.y;
-    }
-    int na = p.prev_T;                          // accepted rows
-    if (p.accept_len && na > 0) na = min(na, max(0, min(p.accept_len[b], na) + 1));
+    if (na > 0) na = min(na, max(0, min(accept, na) + 1));
     const int ta = (na + 7) >> 3, tn = (p.T + 7) >> 3, first = 8 * ta, rows = first + 8 * tn;
     const long long pr0 = static_cast<long long>(b) * p.prev_T, nr0 = static_cast<long long>(b) * p.T;
 
+    // gates of two rows a lane, for the last warp; asked for first, as the
+    // chain of small steps that the block waits for begins with them
+    const bool gate_warp = warp == nwarp - 1;
+    float gate[2] = {0.f, 0.f}, rate[2] = {0.f, 0.f};
+    if (gate_warp)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            if (t < na) {
+                gate[e] = p.prev.g[(pr0 + t) * p.prev.ldg + hv];
+                rate[e] = p.prev.beta[(pr0 + t) * p.prev.ldg + hv];
+            } else if (t >= first && t - first < p.T) {
+                gate[e] = p.rows.g[(nr0 + t - first) * p.rows.ldg + hv];
+                rate[e] = p.rows.beta[(nr0 + t - first) * p.rows.ldg + hv];
+            }
+        }
     // ---- rows into shared memory as they are; absent rows are zero
     constexpr int PR = DK / 8;                  // 16-byte pieces of a key row
     for (int i = tid; i < (NP + NQR) * PR; i += nthr) {
@@ -530,27 +536,29 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
             *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
     }
     cp_async_commit();
-    if (warp == nwarp - 1) {
-        // gates, two rows a lane, and the running sum of the log decays
+    // the state's rows 16 warp + g and + 8, columns 8 j + 2 c, + 1
+    float *srow = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0 + 16 * warp + g) * DK + 2 * c;
+    float st[DK / 8][4];
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j) {
+        const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * j), y = *reinterpret_cast<const float2 *>(srow + 8 * DK + 8 * j);
+        st[j][0] = x.x;
+        st[j][1] = x.y;
+        st[j][2] = y.x;
+        st[j][3] = y.y;
+    }
+    if (gate_warp) {
+        // the running sum of the log decays
         Sum2 G[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            float gv = 0.f, bv = 0.f;
-            if (t < na) {
-                gv = p.prev.g[(pr0 + t) * p.prev.ldg + hv];
-                bv = p.prev.beta[(pr0 + t) * p.prev.ldg + hv];
-            } else if (t >= first && t - first < p.T) {
-                gv = p.rows.g[(nr0 + t - first) * p.rows.ldg + hv];
-                bv = p.rows.beta[(nr0 + t - first) * p.rows.ldg + hv];
-            }
-            if (gv < GB_MIN_LOG) gv = GB_MIN_LOG;
-            G[e] = Sum2{gv, 0.f};
-            beta[t] = bv;
+            G[e] = Sum2{gate[e] < GB_MIN_LOG ? GB_MIN_LOG : gate[e], 0.f};
+            beta[2 * lane + e] = rate[e];
         }
         Sum2 run = add2(G[0], G[1]);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
+            if (2 * d >= 8 * NK) break;
             const Sum2 below{__shfl_up_sync(0xFFFFFFFFu, run.hi, d), __shfl_up_sync(0xFFFFFFFFu, run.lo, d)};
             if (lane >= d) run = add2(below, run);
         }
@@ -558,19 +566,11 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
         if (lane == 0) before = Sum2{0.f, 0.f};
         G[0] = add2(before, G[0]);
         G[1] = run;
-        // where the state is wanted: after the accepted rows, or all (absent rows decay nothing)
-        const int m = p.commit ? GB_MAX : first, ml = max(m - 1, 0) >> 1;
-        const float mh = __shfl_sync(0xFFFFFFFFu, G[1].hi, ml), mlo = __shfl_sync(0xFFFFFFFFu, G[1].lo, ml);
-        const Sum2 Gm = m > 0 ? Sum2{mh, mlo} : Sum2{0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            g_hi[t] = G[e].hi;
-            g_lo[t] = G[e].lo;
-            f_p[t] = expf(G[e].hi + G[e].lo);
-            f_s[t] = t < m ? exp_diff(Gm, G[e].hi, G[e].lo) : 0.f;
+            g_hi[2 * lane + e] = G[e].hi;
+            g_lo[2 * lane + e] = G[e].lo;
         }
-        if (lane == 0) f_o[0] = expf(Gm.hi + Gm.lo);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -598,7 +598,16 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
                 rk[t] = inv;
         }
     }
-    // ---- decays between rows, times the earlier row's inverse norm later
+    // ---- decays: up to each row, from it to where the state is wanted (after
+    // the accepted rows, or all), between rows
+    if (tid < 8 * NK) {
+        const int m = p.commit ? rows : first;
+        const float mh = m > 0 ? g_hi[m - 1] : 0.f, ml = m > 0 ? g_lo[m - 1] : 0.f;
+        const Sum2 G{g_hi[tid], g_lo[tid]};
+        f_p[tid] = expf(G.hi + G.lo);
+        f_s[tid] = tid < m ? expf((mh - G.hi) + (ml - G.lo)) : 0.f;
+        if (tid == 0) f_o[0] = expf(mh + ml);
+    }
     if constexpr (SMALL)
         for (int i = tid; i < NP * NP; i += nthr) {
             const int t = i / NP, s = i % NP;
