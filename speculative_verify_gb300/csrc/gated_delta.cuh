@@ -344,17 +344,17 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 //   S'  = e^(G_m) S + sum_{s<m} (e^(G_m - G_s) r_k,s u_s) k_s^T
 // where the state is wanted after the first m rows: the accepted ones, or all.
 //
-// A warp owns 16 rows of S in the accumulator layout of m16n8 products, which
-// is also their A operand's layout: S k and S q are products with S as A, and
-// the update accumulates onto S where it lies.  S enters as three bf16 terms
-// (24 bits; keys and queries are bf16 as they come) and u, in the update, as
-// two.  The block computes A and M once for its warps.  Up to 16 rows in all,
-// (I + A)^-1 and M are applied as products of three-term operands, so that r,
-// u and the outputs stay in registers; with more, u comes by substitution in
-// shared memory.
+// A warp owns 16 rows of S.  S k and S q are tf32 products with S as the A
+// operand, in two terms (22 bits; keys and queries, bf16 as they come, are
+// exact in tf32); the update is a bf16 product with u in two terms (16 bits)
+// whose accumulator is S.  Everything between is fp32.  The block computes A
+// and M once for its warps.  Up to 16 rows in all, r, u and the outputs stay
+// in the products' accumulator layout: one pass over the rows hands each u to
+// the other lanes, which subtract it from their r and add it to their o.  With
+// more rows u comes by substitution in shared memory.
 //
-// Against the row-by-row kernel this takes about a quarter of the
-// instructions for 4 + 4 rows, which were its bound.
+// A block of 64 state rows; a warp copies its rows to shared memory while the
+// chain of small steps (gates, norms, A) runs, and back.
 
 constexpr int GB_MAX = 2 * GD_MAX_ROWS;         // rows of prev and new together
 constexpr int GB_KPAD = 8, GB_FPAD = 4;         // padding of a row in shared memory, bf16 and fp32 values
@@ -370,12 +370,6 @@ __device__ __forceinline__ void gb_split(float a, float b, uint32_t &hi, uint32_
 {
     hi = gb_pack(a, b);
     lo = gb_pack(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
-}
-
-__device__ __forceinline__ void gb_split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo)
-{
-    hi = gb_pack(a, b);
-    gb_split(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u), mid, lo);
 }
 
 __device__ __forceinline__ void gb_ldmatrix(uint32_t (&r)[4], const uint16_t *p)
@@ -415,64 +409,43 @@ __device__ __forceinline__ float exp_diff(Sum2 a, float bhi, float blo) { return
 
 constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
 
-// Shared memory (bytes) for np rows in all (a multiple of 16), nq new rows (a
-// multiple of 16), `cols` state rows.
-__host__ __device__ constexpr int gb_smem_bytes(int np, int nq, int dk, int cols)
+constexpr int GB_COLS = 64;                     // state rows of a block
+constexpr int GB_THREADS = 2 * GB_COLS;         // a warp for 16 of them
+
+// Shared memory of a block: NP rows in all, NQR new ones (multiples of 16).
+template <int DK, int NP, int NQR>
+struct GbSmem {
+    static constexpr bool SMALL = NP == 16;     // r, u and o stay in registers
+    float s[GB_COLS][DK + 8];                   // the state (rows padded: fragment loads free of bank conflicts)
+    uint16_t k[NP][DK + GB_KPAD], q[NQR][DK + GB_KPAD], v[NP][GB_COLS + GB_KPAD];
+    float a[NP][NP + GB_FPAD];                  // A, [t][s]; SMALL: [s][t]
+    float m[NP > NQR && SMALL ? NP : NQR][NP + GB_FPAD];    // M, [t][s]; SMALL: [s][t]
+    float u[SMALL ? 1 : GB_COLS][NP + GB_FPAD];
+    float ed[SMALL ? NP : 1][NP + GB_FPAD];     // decays between rows
+    float g_hi[GB_MAX], g_lo[GB_MAX], beta[GB_MAX], rk[GB_MAX], rq[GB_MAX], f_p[GB_MAX], f_s[GB_MAX], f_o;
+};
+
+// D (16x8 fp32) += A (16x8 tf32, row) * B (8x8 tf32, col); the operands' low 13 bits are not read.
+__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
 {
-    return (np + nq) * (dk + GB_KPAD) * 2 + np * (cols + GB_KPAD) * 2 + 8 * GB_MAX * 4 +
-           (np == 16 ? 2 * np * (np + GB_FPAD) * 4 + (np + nq) * (np + GB_KPAD) * 6
-                     : (np + nq) * (np + GB_FPAD) * 4 + cols * (np + GB_FPAD) * 4);
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// S += u' K for the eight rows of tile j, u' = u f_s r_k in two terms: x0, x1
-// are this lane's values of u for rows 8 j + 2 c, + 1 and state row g, y0, y1
-// for state row g + 8.
-template <int DK>
-__device__ __forceinline__ void gb_update(float (&st)[DK / 8][4], float x0, float x1, float y0, float y1, const float *f_s,
-                                          const float *rk, const uint16_t *ks, int kst, int j)
-{
-    const int lane = threadIdx.x & 31, t = 8 * j + 2 * (lane & 3);
-    const float w0 = f_s[t] * rk[t], w1 = f_s[t + 1] * rk[t + 1];
-    uint32_t hi[2], lo[2];
-    gb_split(x0 * w0, x1 * w1, hi[0], lo[0]);
-    gb_split(y0 * w0, y1 * w1, hi[1], lo[1]);
-#pragma unroll
-    for (int i = 0; i < DK / 32; ++i) {
-        uint32_t bb[4];
-        gb_ldmatrix_trans(bb, ks + (8 * j + (lane & 7)) * kst + 32 * i + (lane >> 3) * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            mma_bf16_1688(st[4 * i + e], lo[0], lo[1], bb[e]);
-            mma_bf16_1688(st[4 * i + e], hi[0], hi[1], bb[e]);
-        }
-    }
-}
-
-// NK, NQ: most n8 tiles of rows and of new rows.  Grid: x = dv / cols,
-// y = Hv, z = B; cols / 16 warps.
+// NK, NQ: most n8 tiles of rows and of new rows.  Grid: x = dv / GB_COLS,
+// y = Hv, z = B.
 template <int DK, int NK, int NQ>
-__global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(16) uint8_t gb_smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
-    const int g = lane >> 2, c = lane & 3;
-    const int cols = p.cols, col0 = blockIdx.x * cols, hv = blockIdx.y, b = blockIdx.z, hk = hv / (p.Hv / p.Hk);
     constexpr int NP = 8 * NK < 16 ? 16 : 8 * NK, NQR = 8 * NQ < 16 ? 16 : 8 * NQ;
-    constexpr int KST = DK + GB_KPAD, AST = NP + GB_FPAD;
-    const int vst = cols + GB_KPAD;
-    uint16_t *ks = reinterpret_cast<uint16_t *>(gb_smem);       // [NP][KST]
-    uint16_t *qs = ks + NP * KST;                               // [NQR][KST]
-    uint16_t *vs = qs + NQR * KST;                              // [NP][vst]
-    float *g_hi = reinterpret_cast<float *>(vs + NP * vst), *g_lo = g_hi + GB_MAX, *beta = g_lo + GB_MAX, *rk = beta + GB_MAX,
-          *rq = rk + GB_MAX, *f_p = rq + GB_MAX, *f_s = f_p + GB_MAX, *f_o = f_s + GB_MAX;
-    float *as = f_o + GB_MAX;                                   // [NP][AST]
-    // up to 16 rows: (I + A)^-1 and M as three bf16 terms; more: M and u, fp32
-    constexpr bool SMALL = NP == 16;
-    constexpr int TST = NP + GB_KPAD, TT = NP * TST, MT = NQR * TST;
-    float *ed = as + NP * AST;                                  // [NP][AST], decays between rows
-    uint16_t *tt = reinterpret_cast<uint16_t *>(ed + NP * AST), *mt3 = tt + 3 * TT;     // [3][NP][TST], [3][NQR][TST]
-    float *ms = as + NP * AST;                                  // [NQR][AST]
-    float *us = ms + NQR * AST;                                 // [cols][AST]
+    using Smem = GbSmem<DK, NP, NQR>;
+    constexpr bool SMALL = Smem::SMALL;
+    Smem &sm = *reinterpret_cast<Smem *>(gb_smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    constexpr int NWARP = GB_THREADS / 32;
+    const int col0 = blockIdx.x * GB_COLS, hv = blockIdx.y, b = blockIdx.z, hk = hv / (p.Hv / p.Hk);
     pdl_launch_dependents();
     pdl_wait_prior();
     int na = p.prev_T;                          // accepted rows
@@ -480,16 +453,17 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
     const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
     uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
     if (slot < 0) {                             // an inactive entry: its outputs are zero
-        for (int i = tid; i < p.T * cols; i += nthr) o[(i / cols) * p.ldo + i % cols] = 0;
+        for (int i = tid; i < p.T * GB_COLS; i += GB_THREADS) o[(i / GB_COLS) * p.ldo + i % GB_COLS] = 0;
         return;
     }
+    float *state = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0) * DK;
     if (na > 0) na = min(na, max(0, min(accept, na) + 1));
-    const int ta = (na + 7) >> 3, tn = (p.T + 7) >> 3, first = 8 * ta, rows = first + 8 * tn;
+    const int ta = (na + 7) >> 3, tn = (p.T + 7) >> 3, first = 8 * ta, rows = first + 8 * tn, nk = ta + tn;
     const long long pr0 = static_cast<long long>(b) * p.prev_T, nr0 = static_cast<long long>(b) * p.T;
 
     // gates of two rows a lane, for the last warp; asked for first, as the
     // chain of small steps that the block waits for begins with them
-    const bool gate_warp = warp == nwarp - 1;
+    const bool gate_warp = warp == NWARP - 1;
     float gate[2] = {0.f, 0.f}, rate[2] = {0.f, 0.f};
     if (gate_warp)
 #pragma unroll
@@ -504,61 +478,42 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
             }
         }
     // ---- rows into shared memory as they are; absent rows are zero
-    constexpr int PR = DK / 8;                  // 16-byte pieces of a key row
-    for (int i = tid; i < (NP + NQR) * PR; i += nthr) {
-        const int t = i / PR, j = (i % PR) * 8;
-        const uint16_t *src = nullptr;
-        if (t >= NP) {
-            if (t - NP < p.T) src = p.rows.q + (nr0 + t - NP) * p.rows.ldq;
-        } else if (t < na) {
-            src = p.prev.k + (pr0 + t) * p.prev.ldk;
-        } else if (t >= first && t - first < p.T) {
-            src = p.rows.k + (nr0 + t - first) * p.rows.ldk;
+    constexpr int PR = DK / 8, PV = GB_COLS / 8;    // 16-byte pieces of a key row, of a value row
+#pragma unroll 1
+    for (int i = tid; i < (NP + NQR) * PR + NP * PV; i += GB_THREADS) {
+        const bool is_v = i >= (NP + NQR) * PR;
+        const int i2 = is_v ? i - (NP + NQR) * PR : i;
+        const int t = is_v ? i2 / PV : i2 / PR, j = (is_v ? i2 % PV : i2 % PR) * 8;
+        const bool is_q = !is_v && t >= NP;
+        const int tr = is_q ? t - NP : t - first;               // among the new rows
+        const bool old = !is_q && t < na, live = old || (tr >= 0 && tr < p.T);
+        uint16_t *dst = is_v ? &sm.v[t][j] : is_q ? &sm.q[t - NP][j] : &sm.k[t][j];
+        if (live) {
+            const uint16_t *src = is_v ? (old ? p.prev.v : p.rows.v) : is_q ? p.rows.q : old ? p.prev.k : p.rows.k;
+            const long long ld = is_v ? (old ? p.prev.ldv : p.rows.ldv) : is_q ? p.rows.ldq : old ? p.prev.ldk : p.rows.ldk;
+            cp_async_16(smem_addr(dst), src + (old ? pr0 + t : nr0 + tr) * ld + (is_v ? hv * p.dv + col0 : hk * DK) + j);
+        } else {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
         }
-        uint16_t *dst = ks + t * KST + j;       // (the queries follow the keys)
-        if (src)
-            cp_async_16(smem_addr(dst), src + static_cast<long long>(hk) * DK + j);
-        else
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    const int vl = cols == 128 ? 4 : 3;         // log2 of a value row's pieces
-    for (int i = tid; i < rows << vl; i += nthr) {
-        const int t = i >> vl, j = (i & ((1 << vl) - 1)) * 8;
-        const uint16_t *src = nullptr;
-        if (t < na)
-            src = p.prev.v + (pr0 + t) * p.prev.ldv;
-        else if (t >= first && t - first < p.T)
-            src = p.rows.v + (nr0 + t - first) * p.rows.ldv;
-        uint16_t *dst = vs + t * vst + j;
-        if (src)
-            cp_async_16(smem_addr(dst), src + static_cast<long long>(hv) * p.dv + col0 + j);
-        else
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
     }
     cp_async_commit();
-    // the state's rows 16 warp + g and + 8, columns 8 j + 2 c, + 1
-    float *srow = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0 + 16 * warp + g) * DK + 2 * c;
-    float st[DK / 8][4];
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j) {
-        const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * j), y = *reinterpret_cast<const float2 *>(srow + 8 * DK + 8 * j);
-        st[j][0] = x.x;
-        st[j][1] = x.y;
-        st[j][2] = y.x;
-        st[j][3] = y.y;
-    }
+    // ---- the warp's state rows
+    float *srows = state + 16 * warp * DK;
+#pragma unroll 4
+    for (int i = lane; i < 16 * DK / 4; i += 32)
+        cp_async_16(smem_addr(&sm.s[16 * warp + i / (DK / 4)][(i % (DK / 4)) * 4]), srows + 4 * i);
+    cp_async_commit();
     if (gate_warp) {
         // the running sum of the log decays
         Sum2 G[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             G[e] = Sum2{gate[e] < GB_MIN_LOG ? GB_MIN_LOG : gate[e], 0.f};
-            beta[2 * lane + e] = rate[e];
+            sm.beta[2 * lane + e] = rate[e];
         }
         Sum2 run = add2(G[0], G[1]);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            if (2 * d >= 8 * NK) break;
+#pragma unroll 1
+        for (int d = 1; d < 4 * NK; d <<= 1) {
             const Sum2 below{__shfl_up_sync(0xFFFFFFFFu, run.hi, d), __shfl_up_sync(0xFFFFFFFFu, run.lo, d)};
             if (lane >= d) run = add2(below, run);
         }
@@ -568,19 +523,21 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
         G[1] = run;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            g_hi[2 * lane + e] = G[e].hi;
-            g_lo[2 * lane + e] = G[e].lo;
+            sm.g_hi[2 * lane + e] = G[e].hi;
+            sm.g_lo[2 * lane + e] = G[e].lo;
         }
     }
-    cp_async_wait_all();
+    asm volatile("cp.async.wait_group 1;" ::: "memory");        // the rows; the state may take longer
     __syncthreads();
     // ---- inverse norms, eight lanes a row
-    for (int t0 = 4 * warp; t0 < NP + NQR; t0 += 4 * nwarp) {
+#pragma unroll 1
+    for (int t0 = 4 * warp; t0 < NP + NQR; t0 += 4 * NWARP) {
         const int t = t0 + (lane >> 3);
+        const uint16_t *row = t >= NP ? sm.q[t - NP] : sm.k[t];
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < DK / 64; ++j) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(ks + t * KST + 64 * j + 8 * (lane & 7));
+            const uint4 u = *reinterpret_cast<const uint4 *>(row + 64 * j + 8 * (lane & 7));
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -593,30 +550,34 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
         const float inv = p.l2norm ? 1.f / sqrtf(ss + GD_L2_EPS) : 1.f;
         if ((lane & 7) == 0) {
             if (t >= NP)
-                rq[t - NP] = inv * p.scale;
+                sm.rq[t - NP] = inv * p.scale;
             else
-                rk[t] = inv;
+                sm.rk[t] = inv;
         }
     }
     // ---- decays: up to each row, from it to where the state is wanted (after
     // the accepted rows, or all), between rows
-    if (tid < 8 * NK) {
+    {
         const int m = p.commit ? rows : first;
-        const float mh = m > 0 ? g_hi[m - 1] : 0.f, ml = m > 0 ? g_lo[m - 1] : 0.f;
-        const Sum2 G{g_hi[tid], g_lo[tid]};
-        f_p[tid] = expf(G.hi + G.lo);
-        f_s[tid] = tid < m ? expf((mh - G.hi) + (ml - G.lo)) : 0.f;
-        if (tid == 0) f_o[0] = expf(mh + ml);
+        const float mh = m > 0 ? sm.g_hi[m - 1] : 0.f, ml = m > 0 ? sm.g_lo[m - 1] : 0.f;
+        if (tid < 8 * NK) {
+            const float hi = sm.g_hi[tid], lo = sm.g_lo[tid];
+            sm.f_p[tid] = expf(hi + lo);
+            sm.f_s[tid] = tid < m ? expf((mh - hi) + (ml - lo)) : 0.f;
+        }
+        if (tid == 0) sm.f_o = expf(mh + ml);
     }
     if constexpr (SMALL)
-        for (int i = tid; i < NP * NP; i += nthr) {
+#pragma unroll 1
+        for (int i = tid; i < NP * NP; i += GB_THREADS) {
             const int t = i / NP, s = i % NP;
-            ed[t * AST + s] = s <= t ? exp_diff(Sum2{g_hi[t], g_lo[t]}, g_hi[s], g_lo[s]) : 0.f;
+            sm.ed[t][s] = s <= t ? exp_diff(Sum2{sm.g_hi[t], sm.g_lo[t]}, sm.g_hi[s], sm.g_lo[s]) : 0.f;
         }
     __syncthreads();
 
     // ---- A and M: one 16-row tile of either a warp
-    for (int task = warp; task < NP / 16 + NQR / 16; task += nwarp) {
+#pragma unroll 1
+    for (int task = warp; task < NP / 16 + NQR / 16; task += NWARP) {
         const bool is_m = task >= NP / 16;
         const int mt = is_m ? task - NP / 16 : task;
         const int r0 = is_m ? first + 16 * mt : 16 * mt;        // the tile's first row among all
@@ -627,8 +588,8 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
         for (int j = 0; j < NK; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-        const uint16_t *arow = (is_m ? qs : ks) + (16 * mt + (lane & 15)) * KST + (lane >> 4) * 8;
-#pragma unroll
+        const uint16_t *arow = (is_m ? sm.q[16 * mt + (lane & 15)] : sm.k[16 * mt + (lane & 15)]) + (lane >> 4) * 8;
+#pragma unroll 1
         for (int s = 0; s < DK / 32; ++s) {
             uint32_t a0[4], a1[4], bb[4];
             gb_ldmatrix(a0, arow + 32 * s);
@@ -636,7 +597,7 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 if (j >= last) break;
-                gb_ldmatrix(bb, ks + (8 * j + (lane & 7)) * KST + 32 * s + (lane >> 3) * 8);
+                gb_ldmatrix(bb, sm.k[8 * j + (lane & 7)] + 32 * s + (lane >> 3) * 8);
                 mma_bf16_16816(acc[j], a0[0], a0[1], a0[2], a0[3], bb[0], bb[1]);
                 mma_bf16_16816(acc[j], a1[0], a1[1], a1[2], a1[3], bb[2], bb[3]);
             }
@@ -645,54 +606,24 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
         for (int h = 0; h < 2; ++h) {
             const int tl = 16 * mt + g + 8 * h, t = r0 + g + 8 * h;     // within its matrix, among all rows
             const bool live = is_m ? tl < p.T : t < rows;
-            const Sum2 G = live ? Sum2{g_hi[t], g_lo[t]} : Sum2{0.f, 0.f};
-            const float f = !live ? 0.f : is_m ? rq[tl] : beta[t] * rk[t];
-            float *dst = (is_m && !SMALL ? ms : as) + tl * AST + 2 * c;
+            const Sum2 G = live ? Sum2{sm.g_hi[t], sm.g_lo[t]} : Sum2{0.f, 0.f};
+            const float f = !live ? 0.f : is_m ? sm.rq[tl] : sm.beta[t] * sm.rk[t];
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 float v[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int s = 8 * j + 2 * c + e;
-                    const float d = !live || s > t ? 0.f : SMALL ? ed[t * AST + s] : exp_diff(G, g_hi[s], g_lo[s]);
-                    v[e] = live && (is_m ? s <= t : s < t) ? acc[j][2 * h + e] * (d * rk[s] * f) : 0.f;
+                    const float d = !live || s > t ? 0.f : SMALL ? sm.ed[SMALL ? t : 0][s] : exp_diff(G, sm.g_hi[s], sm.g_lo[s]);
+                    v[e] = live && (is_m ? s <= t : s < t) ? acc[j][2 * h + e] * (d * sm.rk[s] * f) : 0.f;
                 }
-                if (SMALL && is_m) {
-                    uint32_t w[3];
-                    gb_split3(v[0], v[1], w[0], w[1], w[2]);
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t *>(mt3 + e * MT + tl * TST + 8 * j + 2 * c) = w[e];
+                const int s0 = 8 * j + 2 * c;
+                if constexpr (SMALL) {
+                    float *dst = is_m ? &sm.m[s0][tl] : &sm.a[s0][tl];
+                    dst[0] = v[0];
+                    dst[NP + GB_FPAD] = v[1];
                 } else {
-                    *reinterpret_cast<float2 *>(dst + 8 * j) = make_float2(v[0], v[1]);
-                }
-            }
-            if (SMALL && NK == 1)               // the second half of a 16-row operand
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (is_m) *reinterpret_cast<uint32_t *>(mt3 + e * MT + tl * TST + 8 + 2 * c) = 0u;
-        }
-        if (SMALL && !is_m) {
-            // column `lane` of (I + A)^-1 by forward substitution
-            __syncwarp();
-            if (lane < 16) {
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
-                    if (i < 8 * NK)
-#pragma unroll
-                        for (int k = 0; k < i; k += 4) {
-                            const float4 a = *reinterpret_cast<const float4 *>(as + i * AST + k);
-                            s0 = fmaf(-a.x, x[k], s0);
-                            if (k + 1 < i) s1 = fmaf(-a.y, x[k + 1], s1);
-                            if (k + 2 < i) s0 = fmaf(-a.z, x[k + 2], s0);
-                            if (k + 3 < i) s1 = fmaf(-a.w, x[k + 3], s1);
-                        }
-                    x[i] = s0 + s1;
-                    uint32_t w[3];
-                    gb_split3(x[i], 0.f, w[0], w[1], w[2]);
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) tt[e * TT + i * TST + lane] = static_cast<uint16_t>(w[e]);
+                    *reinterpret_cast<float2 *>(is_m ? &sm.m[tl][s0] : &sm.a[tl][s0]) = make_float2(v[0], v[1]);
                 }
             }
         }
@@ -708,31 +639,33 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) pq[j][e] = 0.f;
-    const int nk = ta + tn;
+    cp_async_wait_all();
+    __syncwarp();                               // the warp's state rows are in
+    float *srow = &sm.s[16 * warp + g][2 * c];
+    constexpr int SST = DK + 8;
+#pragma unroll 4
+    for (int s = 0; s < DK / 8; ++s) {
+        // columns 2 c and 2 c + 1 of the step are its k = c and c + 4
+        const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * s), y = *reinterpret_cast<const float2 *>(srow + 8 * SST + 8 * s);
+        const float sv[4] = {x.x, y.x, x.y, y.y};
+        uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-        uint32_t hi[2][4], mid[2][4], lo[2][4], bb[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)         // rows g, g + 8 of columns 8 (i >> 1) ..
-                gb_split3(st[4 * s + 2 * e + (i >> 1)][2 * (i & 1)], st[4 * s + 2 * e + (i >> 1)][2 * (i & 1) + 1], hi[e][i],
-                          mid[e][i], lo[e][i]);
-        auto both = [&](float (&d)[4], const uint16_t *rowp) {
-            gb_ldmatrix(bb, rowp + (lane & 7) * KST + 32 * s + (lane >> 3) * 8);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mma_bf16_16816(d, lo[e][0], lo[e][1], lo[e][2], lo[e][3], bb[2 * e], bb[2 * e + 1]);
-                mma_bf16_16816(d, mid[e][0], mid[e][1], mid[e][2], mid[e][3], bb[2 * e], bb[2 * e + 1]);
-                mma_bf16_16816(d, hi[e][0], hi[e][1], hi[e][2], hi[e][3], bb[2 * e], bb[2 * e + 1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = __float_as_uint(sv[i]) & 0xFFFFE000u;
+            lo[i] = __float_as_uint(sv[i] - __uint_as_float(hi[i]));
+        }
+        auto product = [&](float (&d)[4], const uint16_t *row) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(row + 8 * s + 2 * c);
+            const uint32_t b0 = w << 16, b1 = w & 0xFFFF0000u;
+            mma_tf32_1688(d, lo[0], lo[1], lo[2], lo[3], b0, b1);
+            mma_tf32_1688(d, hi[0], hi[1], hi[2], hi[3], b0, b1);
         };
 #pragma unroll
         for (int j = 0; j < NK; ++j)
-            if (j < nk) both(pk[j], ks + 8 * j * KST);
+            if (j < nk) product(pk[j], sm.k[8 * j + g]);
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
-            if (j < tn) both(pq[j], qs + 8 * j * KST);
+            if (j < tn) product(pq[j], sm.q[8 * j + g]);
     }
     // ---- r
 #pragma unroll
@@ -741,91 +674,64 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 8 * j + 2 * c + (e & 1);
-                pk[j][e] = beta[t] * (bf16_bits_to_float(vs[t * vst + 16 * warp + g + 8 * (e >> 1)]) - f_p[t] * rk[t] * pk[j][e]);
+                pk[j][e] = sm.beta[t] * (bf16_bits_to_float(sm.v[t][16 * warp + g + 8 * (e >> 1)]) - sm.f_p[t] * sm.rk[t] * pk[j][e]);
             }
-    const float decay = f_o[0];
     const int nu = p.commit ? nk : ta;          // tiles of the rows that the state is wanted after
+    __syncthreads();                            // A and M are complete
     if constexpr (SMALL) {
-        __syncthreads();                        // (I + A)^-1 and M are complete
-        // a product's 16 rows as A operands of three terms; two matrices of
-        // three terms each make 24 bits with the six largest term products
-        auto operand = [&](const float (&x)[NK][4], uint32_t (&a)[3][4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((i >> 1) < NK)
-                    gb_split3(x[(i >> 1) < NK ? i >> 1 : 0][2 * (i & 1)], x[(i >> 1) < NK ? i >> 1 : 0][2 * (i & 1) + 1], a[0][i], a[1][i], a[2][i]);
-                else
-                    a[0][i] = a[1][i] = a[2][i] = 0u;
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 8 * j + 2 * c + (e & 1);
+                pq[j][e] = t < p.T ? sm.f_p[first + t] * sm.rq[t] * pq[j][e] : 0.f;
             }
-        };
-        auto product = [&](float (&d)[2][4], const uint32_t (&a)[3][4], const uint16_t *m, int step) {
-            uint32_t bb[3][4];
+        // row s's u, complete once the rows before it have been taken off its
+        // r, goes to the lanes of its state rows
 #pragma unroll
-            for (int e = 0; e < 3; ++e)
-                gb_ldmatrix(bb[e], m + e * step + ((lane & 7) + ((lane >> 4) << 3)) * TST + ((lane >> 3) & 1) * 8);
+        for (int s = 0; s < 8 * NK; ++s) {
+            if (s >= rows) break;
+            const int from = (lane & ~3) | ((s & 7) >> 1);
+            const float ug = __shfl_sync(0xFFFFFFFFu, pk[s >> 3][s & 1], from), uh = __shfl_sync(0xFFFFFFFFu, pk[s >> 3][2 + (s & 1)], from);
 #pragma unroll
-            for (int k = 4; k >= 0; --k)        // (term of a, term of b): smallest products first
+            for (int j = s >> 3; j < NK; ++j) {
+                const float2 av = *reinterpret_cast<const float2 *>(&sm.a[s][8 * j + 2 * c]);   // 0 up to row s
+                pk[j][0] = fmaf(-av.x, ug, pk[j][0]);
+                pk[j][1] = fmaf(-av.y, ug, pk[j][1]);
+                pk[j][2] = fmaf(-av.x, uh, pk[j][2]);
+                pk[j][3] = fmaf(-av.y, uh, pk[j][3]);
+            }
+            if (tn > 0)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    auto one = [&](int x, int y) { mma_bf16_16816(d[j], a[x][0], a[x][1], a[x][2], a[x][3], bb[y][2 * j], bb[y][2 * j + 1]); };
-                    if (k == 4) one(1, 1);
-                    if (k == 3) one(2, 0), one(0, 2);
-                    if (k == 2) one(1, 0);
-                    if (k == 1) one(0, 1);
-                    if (k == 0) one(0, 0);
-                }
-        };
-        float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-            uint32_t a[3][4];
-            operand(pk, a);
-            product(u, a, tt, TT);
-        }
-        if (tn > 0) {
-            float s[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * j + 2 * c + (e & 1);
-                    s[j][e] = j < NQ && t < p.T ? f_p[first + t] * rq[t] * pq[j < NQ ? j : 0][e] : 0.f;
-                }
-            float uk[NK][4];
-#pragma unroll
-            for (int j = 0; j < NK; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) uk[j][e] = u[j][e];
-            uint32_t a[3][4];
-            operand(uk, a);
-            product(s, a, mt3, MT);
-#pragma unroll
-            for (int j = 0; j < NQ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * j + 2 * c + (e & 1);
-                    if (t < p.T) o[t * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[j][e]));
+                for (int j = 0; j < NQ; ++j) {
+                    const float2 mv = *reinterpret_cast<const float2 *>(&sm.m[SMALL ? s : 0][8 * j + 2 * c]);
+                    pq[j][0] = fmaf(mv.x, ug, pq[j][0]);
+                    pq[j][1] = fmaf(mv.y, ug, pq[j][1]);
+                    pq[j][2] = fmaf(mv.x, uh, pq[j][2]);
+                    pq[j][3] = fmaf(mv.y, uh, pq[j][3]);
                 }
         }
-        if (nu == 0) return;
 #pragma unroll
-        for (int j = 0; j < DK / 8; ++j)
+        for (int j = 0; j < NQ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st[j][e] *= decay;
-#pragma unroll
-        for (int j = 0; j < NK; ++j)
-            if (j < nu) gb_update<DK>(st, u[j][0], u[j][1], u[j][2], u[j][3], f_s, rk, ks, KST, j);
+            for (int e = 0; e < 4; ++e) {
+                const int t = 8 * j + 2 * c + (e & 1);
+                if (t < p.T) o[t * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(pq[j][e]));
+            }
     } else {
-        float *uw = us + 16 * warp * AST;
+        // u by forward substitution in the warp's own rows of shared memory, a
+        // state row a lane, eight rows t at a time
+        float (*uw)[NP + GB_FPAD] = &sm.u[16 * warp];
 #pragma unroll
         for (int j = 0; j < NK; ++j)
             if (j < nk)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)         // r, in the warp's own rows of shared memory
-                    *reinterpret_cast<float2 *>(uw + (g + 8 * h) * AST + 8 * j + 2 * c) = make_float2(pk[j][2 * h], pk[j][2 * h + 1]);
-        __syncthreads();                            // A and M are complete
-        // ---- u by forward substitution, a state row a lane, eight rows t at a time
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(&uw[g + 8 * h][8 * j + 2 * c]) = make_float2(pk[j][2 * h], pk[j][2 * h + 1]);
+        __syncwarp();
         if (lane < 16) {
-            float *ur = uw + lane * AST;
+            float *ur = uw[lane];
+#pragma unroll 1
             for (int j = 0; j < nk; ++j) {
                 float u[8];
 #pragma unroll
@@ -836,19 +742,20 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
                     u[i + 2] = x.z;
                     u[i + 3] = x.w;
                 }
+#pragma unroll 1
                 for (int k = 0; k < 2 * j; ++k) {   // four earlier rows
                     const float4 e = *reinterpret_cast<const float4 *>(ur + 4 * k);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 a = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 4 * k);
-                        u[i] -= (a.x * e.x + a.y * e.y) + (a.z * e.z + a.w * e.w);
+                        const float4 av = *reinterpret_cast<const float4 *>(&sm.a[8 * j + i][4 * k]);
+                        u[i] -= (av.x * e.x + av.y * e.y) + (av.z * e.z + av.w * e.w);
                     }
                 }
 #pragma unroll
                 for (int i = 1; i < 8; ++i) {
-                    const float4 a = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 8 * j);
-                    const float4 a2 = *reinterpret_cast<const float4 *>(as + (8 * j + i) * AST + 8 * j + 4);
-                    const float av[8] = {a.x, a.y, a.z, a.w, a2.x, a2.y, a2.z, a2.w};
+                    const float4 a1 = *reinterpret_cast<const float4 *>(&sm.a[8 * j + i][8 * j]);
+                    const float4 a2 = *reinterpret_cast<const float4 *>(&sm.a[8 * j + i][8 * j + 4]);
+                    const float av[8] = {a1.x, a1.y, a1.z, a1.w, a2.x, a2.y, a2.z, a2.w};
 #pragma unroll
                     for (int k = 0; k < i; ++k) u[i] = fmaf(-av[k], u[k], u[i]);
                 }
@@ -857,17 +764,17 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
             }
         }
         __syncwarp();
-        // ---- outputs
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
             if (j < tn) {
                 const int t0 = 8 * j + 2 * c;
-                float s[4];                         // (t0, g) (t0 + 1, g) (t0, g + 8) (t0 + 1, g + 8)
+                float s[4];                     // (t0, g) (t0 + 1, g) (t0, g + 8) (t0 + 1, g + 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = (t0 + (e & 1) < p.T ? f_p[first + t0 + (e & 1)] * rq[t0 + (e & 1)] : 0.f) * pq[j][e];
+                for (int e = 0; e < 4; ++e) s[e] = (t0 + (e & 1) < p.T ? sm.f_p[first + t0 + (e & 1)] * sm.rq[t0 + (e & 1)] : 0.f) * pq[j][e];
+#pragma unroll 1
                 for (int k = 0; k < first + 8 * j + 8; k += 4) {
-                    const float4 m0 = *reinterpret_cast<const float4 *>(ms + t0 * AST + k), m1 = *reinterpret_cast<const float4 *>(ms + (t0 + 1) * AST + k);
-                    const float4 u0 = *reinterpret_cast<const float4 *>(uw + g * AST + k), u1 = *reinterpret_cast<const float4 *>(uw + (g + 8) * AST + k);
+                    const float4 m0 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0][k]), m1 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0 + 1][k]);
+                    const float4 u0 = *reinterpret_cast<const float4 *>(&uw[g][k]), u1 = *reinterpret_cast<const float4 *>(&uw[g + 8][k]);
                     s[0] = fmaf(m0.x, u0.x, fmaf(m0.y, u0.y, fmaf(m0.z, u0.z, fmaf(m0.w, u0.w, s[0]))));
                     s[1] = fmaf(m1.x, u0.x, fmaf(m1.y, u0.y, fmaf(m1.z, u0.z, fmaf(m1.w, u0.w, s[1]))));
                     s[2] = fmaf(m0.x, u1.x, fmaf(m0.y, u1.y, fmaf(m0.z, u1.z, fmaf(m0.w, u1.w, s[2]))));
@@ -878,23 +785,64 @@ __global__ void __launch_bounds__(256, 2) gated_delta_block_kernel(const DeltaPa
                     if (t0 + (e & 1) < p.T)
                         o[(t0 + (e & 1)) * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[e]));
             }
-        // ---- the state after the wanted rows
-        if (nu == 0) return;
+    }
+    // ---- the state after the wanted rows: S <- decay S + u' K, u' = u f_s r_k in two terms
+    if (nu == 0) return;
+    const float decay = sm.f_o;
+    uint32_t uh[2][2], ul[2][2];
+    auto scaled_u = [&](int j, float x0, float x1, float y0, float y1, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+        const int t = 8 * j + 2 * c;            // rows t, t + 1 of state row g (x) and g + 8 (y)
+        const float w0 = sm.f_s[t] * sm.rk[t], w1 = sm.f_s[t + 1] * sm.rk[t + 1];
+        gb_split(x0 * w0, x1 * w1, hi[0], lo[0]);
+        gb_split(y0 * w0, y1 * w1, hi[1], lo[1]);
+    };
+    if constexpr (SMALL)
 #pragma unroll
-        for (int j = 0; j < DK / 8; ++j)
+        for (int j = 0; j < NK; ++j)
+            if (j < nu) scaled_u(j, pk[j][0], pk[j][1], pk[j][2], pk[j][3], uh[SMALL ? j : 0], ul[SMALL ? j : 0]);
+#pragma unroll 1
+    for (int i = 0; i < DK / 32; ++i) {
+        float st[4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st[j][e] *= decay;
-        for (int j = 0; j < nu; ++j) {
-            const float2 x = *reinterpret_cast<const float2 *>(uw + g * AST + 8 * j + 2 * c),
-                         y = *reinterpret_cast<const float2 *>(uw + (g + 8) * AST + 8 * j + 2 * c);
-            gb_update<DK>(st, x.x, x.y, y.x, y.y, f_s, rk, ks, KST, j);
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = *reinterpret_cast<const float2 *>(srow + 32 * i + 8 * e), y = *reinterpret_cast<const float2 *>(srow + 8 * SST + 32 * i + 8 * e);
+            st[e][0] = decay * x.x;
+            st[e][1] = decay * x.y;
+            st[e][2] = decay * y.x;
+            st[e][3] = decay * y.y;
+        }
+        auto add = [&](int j, const uint32_t (&hi)[2], const uint32_t (&lo)[2]) {
+            uint32_t bb[4];
+            gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + 32 * i + (lane >> 3) * 8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mma_bf16_1688(st[e], lo[0], lo[1], bb[e]);
+                mma_bf16_1688(st[e], hi[0], hi[1], bb[e]);
+            }
+        };
+        if constexpr (SMALL) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+                if (j < nu) add(j, uh[SMALL ? j : 0], ul[SMALL ? j : 0]);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < nu; ++j) {
+                const float2 x = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * warp + g][8 * j + 2 * c]),
+                             y = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * warp + g + 8][8 * j + 2 * c]);
+                scaled_u(j, x.x, x.y, y.x, y.y, uh[0], ul[0]);
+                add(j, uh[0], ul[0]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            *reinterpret_cast<float2 *>(srow + 32 * i + 8 * e) = make_float2(st[e][0], st[e][1]);
+            *reinterpret_cast<float2 *>(srow + 8 * SST + 32 * i + 8 * e) = make_float2(st[e][2], st[e][3]);
         }
     }
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j) {
-        *reinterpret_cast<float2 *>(srow + 8 * j) = make_float2(st[j][0], st[j][1]);
-        *reinterpret_cast<float2 *>(srow + 8 * DK + 8 * j) = make_float2(st[j][2], st[j][3]);
-    }
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < 16 * DK / 4; i += 32)
+        *reinterpret_cast<float4 *>(srows + 4 * i) = *reinterpret_cast<const float4 *>(&sm.s[16 * warp + i / (DK / 4)][(i % (DK / 4)) * 4]);
 }
 
 }  // namespace sv

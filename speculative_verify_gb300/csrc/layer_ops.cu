@@ -224,11 +224,16 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
 constexpr int DELTA_BLOCK_MIN_ROWS = 3;
 
 template <int DK, int NK, int NQ>
+constexpr size_t delta_block_smem()
+{
+    return sizeof(GbSmem<DK, 8 * NK < 16 ? 16 : 8 * NK, 8 * NQ < 16 ? 16 : 8 * NQ>);
+}
+
+template <int DK, int NK, int NQ>
 int delta_block_launch(const DeltaParams &p, int B, cudaStream_t stream)
 {
-    constexpr int NP = 8 * NK < 16 ? 16 : 8 * NK, NQR = 8 * NQ < 16 ? 16 : 8 * NQ;
-    const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
-    return launch(gated_delta_block_kernel<DK, NK, NQ>, grid, 2 * p.cols, gb_smem_bytes(NP, NQR, DK, p.cols), stream, p);
+    const dim3 grid(static_cast<unsigned>(p.dv / GB_COLS), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
+    return launch(gated_delta_block_kernel<DK, NK, NQ>, grid, GB_THREADS, delta_block_smem<DK, NK, NQ>(), stream, p);
 }
 
 template <int DK>
@@ -244,10 +249,10 @@ int delta_block_dispatch(const DeltaParams &p, int B, cudaStream_t stream)
 template <int DK>
 cudaError_t delta_block_raise()
 {
-    cudaError_t e = raise(gated_delta_block_kernel<DK, 1, 1>, gb_smem_bytes(16, 16, DK, 128));
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 2, 1>, gb_smem_bytes(16, 16, DK, 128));
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 4, 2>, gb_smem_bytes(32, 16, DK, 128));
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 8, 4>, gb_smem_bytes(64, 32, DK, 128));
+    cudaError_t e = raise(gated_delta_block_kernel<DK, 1, 1>, delta_block_smem<DK, 1, 1>());
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 2, 1>, delta_block_smem<DK, 2, 1>());
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 4, 2>, delta_block_smem<DK, 4, 2>());
+    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 8, 4>, delta_block_smem<DK, 8, 4>());
     return e;
 }
 
@@ -372,7 +377,6 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (T + prev_T >= DELTA_BLOCK_MIN_ROWS) {
-        p.cols = static_cast<long long>(B) * p.Hv < dev.sms ? 64 : shape->dv;
         return shape->dk == 64 ? delta_block_dispatch<64>(p, B, cs) : delta_block_dispatch<128>(p, B, cs);
     }
     return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, 4 * p.cols, smem, cs, p)
