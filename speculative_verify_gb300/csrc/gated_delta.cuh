@@ -412,17 +412,17 @@ constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log de
 constexpr int GB_COLS = 64;                     // state rows of a block
 constexpr int GB_THREADS = 2 * GB_COLS;         // a warp for 16 of them
 
-// Shared memory of a block: NP rows in all, NQR new ones (multiples of 16).
+// Shared memory of a block: NP rows in all, NQR new ones (8 or multiples of 16).
 template <int DK, int NP, int NQR>
 struct GbSmem {
-    static constexpr bool SMALL = NP == 16;     // r, u and o stay in registers
+    static constexpr bool SMALL = NP <= 16;     // r, u and o stay in registers
     float s[GB_COLS][DK + 8];                   // the state (rows padded: fragment loads free of bank conflicts)
     uint16_t k[NP][DK + GB_KPAD], q[NQR][DK + GB_KPAD], v[NP][GB_COLS + GB_KPAD];
     float a[NP][NP + GB_FPAD];                  // A, [t][s]; SMALL: [s][t]
-    float m[NP > NQR && SMALL ? NP : NQR][NP + GB_FPAD];    // M, [t][s]; SMALL: [s][t]
+    float m[SMALL ? NP : NQR][(SMALL ? NQR : NP) + GB_FPAD];    // M, [t][s]; SMALL: [s][t]
     float u[SMALL ? 1 : GB_COLS][NP + GB_FPAD];
     float ed[SMALL ? NP : 1][NP + GB_FPAD];     // decays between rows
-    float g_hi[GB_MAX], g_lo[GB_MAX], beta[GB_MAX], rk[GB_MAX], rq[GB_MAX], f_p[GB_MAX], f_s[GB_MAX], f_o;
+    float g_hi[NP], g_lo[NP], beta[NP], rk[NP], rq[NQR], f_p[NP], f_s[NP], f_o;
 };
 
 // D (16x8 fp32) += A (16x8 tf32, row) * B (8x8 tf32, col); the operands' low 13 bits are not read.
@@ -439,7 +439,7 @@ template <int DK, int NK, int NQ>
 __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(16) uint8_t gb_smem[];
-    constexpr int NP = 8 * NK < 16 ? 16 : 8 * NK, NQR = 8 * NQ < 16 ? 16 : 8 * NQ;
+    constexpr int NP = 8 * NK, NQR = 8 * NQ;
     using Smem = GbSmem<DK, NP, NQR>;
     constexpr bool SMALL = Smem::SMALL;
     Smem &sm = *reinterpret_cast<Smem *>(gb_smem);
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     }
     float *state = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0) * DK;
     if (na > 0) na = min(na, max(0, min(accept, na) + 1));
-    const int ta = (na + 7) >> 3, tn = (p.T + 7) >> 3, first = 8 * ta, rows = first + 8 * tn, nk = ta + tn;
+    const int rows = na + p.T, tn = (p.T + 7) >> 3, nk = (rows + 7) >> 3;
+    const int kept = p.commit ? rows : na;      // rows that the state is wanted after
     const long long pr0 = static_cast<long long>(b) * p.prev_T, nr0 = static_cast<long long>(b) * p.T;
 
     // gates of two rows a lane, for the last warp; asked for first, as the
@@ -472,9 +473,9 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
             if (t < na) {
                 gate[e] = p.prev.g[(pr0 + t) * p.prev.ldg + hv];
                 rate[e] = p.prev.beta[(pr0 + t) * p.prev.ldg + hv];
-            } else if (t >= first && t - first < p.T) {
-                gate[e] = p.rows.g[(nr0 + t - first) * p.rows.ldg + hv];
-                rate[e] = p.rows.beta[(nr0 + t - first) * p.rows.ldg + hv];
+            } else if (t < rows) {
+                gate[e] = p.rows.g[(nr0 + t - na) * p.rows.ldg + hv];
+                rate[e] = p.rows.beta[(nr0 + t - na) * p.rows.ldg + hv];
             }
         }
     // ---- rows into shared memory as they are; absent rows are zero
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         const int i2 = is_v ? i - (NP + NQR) * PR : i;
         const int t = is_v ? i2 / PV : i2 / PR, j = (is_v ? i2 % PV : i2 % PR) * 8;
         const bool is_q = !is_v && t >= NP;
-        const int tr = is_q ? t - NP : t - first;               // among the new rows
+        const int tr = is_q ? t - NP : t - na;                  // among the new rows
         const bool old = !is_q && t < na, live = old || (tr >= 0 && tr < p.T);
         uint16_t *dst = is_v ? &sm.v[t][j] : is_q ? &sm.q[t - NP][j] : &sm.k[t][j];
         if (live) {
@@ -509,7 +510,6 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             G[e] = Sum2{gate[e] < GB_MIN_LOG ? GB_MIN_LOG : gate[e], 0.f};
-            sm.beta[2 * lane + e] = rate[e];
         }
         Sum2 run = add2(G[0], G[1]);
 #pragma unroll 1
@@ -521,18 +521,20 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         if (lane == 0) before = Sum2{0.f, 0.f};
         G[0] = add2(before, G[0]);
         G[1] = run;
+        if (2 * lane < NP)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            sm.g_hi[2 * lane + e] = G[e].hi;
-            sm.g_lo[2 * lane + e] = G[e].lo;
-        }
+            for (int e = 0; e < 2; ++e) {
+                sm.g_hi[2 * lane + e] = G[e].hi;
+                sm.g_lo[2 * lane + e] = G[e].lo;
+                sm.beta[2 * lane + e] = rate[e];
+            }
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");        // the rows; the state may take longer
     __syncthreads();
     // ---- inverse norms, eight lanes a row
 #pragma unroll 1
     for (int t0 = 4 * warp; t0 < NP + NQR; t0 += 4 * NWARP) {
-        const int t = t0 + (lane >> 3);
+        const int t = t0 + (lane >> 3);         // NP and NQR are multiples of 8
         const uint16_t *row = t >= NP ? sm.q[t - NP] : sm.k[t];
         float ss = 0.f;
 #pragma unroll
@@ -555,15 +557,13 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                 sm.rk[t] = inv;
         }
     }
-    // ---- decays: up to each row, from it to where the state is wanted (after
-    // the accepted rows, or all), between rows
+    // ---- decays: up to each row, from it to the last kept one, between rows
     {
-        const int m = p.commit ? rows : first;
-        const float mh = m > 0 ? sm.g_hi[m - 1] : 0.f, ml = m > 0 ? sm.g_lo[m - 1] : 0.f;
-        if (tid < 8 * NK) {
+        const float mh = kept > 0 ? sm.g_hi[kept - 1] : 0.f, ml = kept > 0 ? sm.g_lo[kept - 1] : 0.f;
+        if (tid < NP) {
             const float hi = sm.g_hi[tid], lo = sm.g_lo[tid];
             sm.f_p[tid] = expf(hi + lo);
-            sm.f_s[tid] = tid < m ? expf((mh - hi) + (ml - lo)) : 0.f;
+            sm.f_s[tid] = tid < kept ? expf((mh - hi) + (ml - lo)) : 0.f;
         }
         if (tid == 0) sm.f_o = expf(mh + ml);
     }
@@ -577,10 +577,10 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 
     // ---- A and M: one 16-row tile of either a warp
 #pragma unroll 1
-    for (int task = warp; task < NP / 16 + NQR / 16; task += NWARP) {
-        const bool is_m = task >= NP / 16;
-        const int mt = is_m ? task - NP / 16 : task;
-        const int r0 = is_m ? first + 16 * mt : 16 * mt;        // the tile's first row among all
+    for (int task = warp; task < (NP + 15) / 16 + (NQR + 15) / 16; task += NWARP) {
+        const bool is_m = task >= (NP + 15) / 16;
+        const int mt = is_m ? task - (NP + 15) / 16 : task;
+        const int r0 = is_m ? na + 16 * mt : 16 * mt;           // the tile's first row among all
         if (is_m ? 16 * mt >= p.T : r0 >= rows) continue;
         const int last = min(NK, (r0 + 15) / 8 + 1);
         float acc[NK][4];
@@ -588,7 +588,8 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         for (int j = 0; j < NK; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-        const uint16_t *arow = (is_m ? sm.q[16 * mt + (lane & 15)] : sm.k[16 * mt + (lane & 15)]) + (lane >> 4) * 8;
+        // eight rows fill half a tile: the other half repeats them
+        const uint16_t *arow = (is_m ? sm.q[16 * mt + (lane & (NQR < 16 ? 7 : 15))] : sm.k[16 * mt + (lane & (NP < 16 ? 7 : 15))]) + (lane >> 4) * 8;
 #pragma unroll 1
         for (int s = 0; s < DK / 32; ++s) {
             uint32_t a0[4], a1[4], bb[4];
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         for (int h = 0; h < 2; ++h) {
             const int tl = 16 * mt + g + 8 * h, t = r0 + g + 8 * h;     // within its matrix, among all rows
             const bool live = is_m ? tl < p.T : t < rows;
+            if (tl >= (is_m ? NQR : NP)) continue;
             const Sum2 G = live ? Sum2{sm.g_hi[t], sm.g_lo[t]} : Sum2{0.f, 0.f};
             const float f = !live ? 0.f : is_m ? sm.rq[tl] : sm.beta[t] * sm.rk[t];
 #pragma unroll
@@ -619,9 +621,8 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                 }
                 const int s0 = 8 * j + 2 * c;
                 if constexpr (SMALL) {
-                    float *dst = is_m ? &sm.m[s0][tl] : &sm.a[s0][tl];
-                    dst[0] = v[0];
-                    dst[NP + GB_FPAD] = v[1];
+                    (is_m ? sm.m[s0] : sm.a[s0])[tl] = v[0];
+                    (is_m ? sm.m[s0 + 1] : sm.a[s0 + 1])[tl] = v[1];
                 } else {
                     *reinterpret_cast<float2 *>(is_m ? &sm.m[tl][s0] : &sm.a[tl][s0]) = make_float2(v[0], v[1]);
                 }
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                 const int t = 8 * j + 2 * c + (e & 1);
                 pk[j][e] = sm.beta[t] * (bf16_bits_to_float(sm.v[t][16 * warp + g + 8 * (e >> 1)]) - sm.f_p[t] * sm.rk[t] * pk[j][e]);
             }
-    const int nu = p.commit ? nk : ta;          // tiles of the rows that the state is wanted after
+    const int nu = (kept + 7) >> 3;
     __syncthreads();                            // A and M are complete
     if constexpr (SMALL) {
 #pragma unroll
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 8 * j + 2 * c + (e & 1);
-                pq[j][e] = t < p.T ? sm.f_p[first + t] * sm.rq[t] * pq[j][e] : 0.f;
+                pq[j][e] = t < p.T ? sm.f_p[na + t] * sm.rq[t] * pq[j][e] : 0.f;
             }
         // row s's u, complete once the rows before it have been taken off its
         // r, goes to the lanes of its state rows
@@ -770,9 +771,9 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                 const int t0 = 8 * j + 2 * c;
                 float s[4];                     // (t0, g) (t0 + 1, g) (t0, g + 8) (t0 + 1, g + 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = (t0 + (e & 1) < p.T ? sm.f_p[first + t0 + (e & 1)] * sm.rq[t0 + (e & 1)] : 0.f) * pq[j][e];
+                for (int e = 0; e < 4; ++e) s[e] = (t0 + (e & 1) < p.T ? sm.f_p[na + t0 + (e & 1)] * sm.rq[t0 + (e & 1)] : 0.f) * pq[j][e];
 #pragma unroll 1
-                for (int k = 0; k < first + 8 * j + 8; k += 4) {
+                for (int k = 0; k < min(na + 8 * j + 8, 8 * nk); k += 4) {
                     const float4 m0 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0][k]), m1 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0 + 1][k]);
                     const float4 u0 = *reinterpret_cast<const float4 *>(&uw[g][k]), u1 = *reinterpret_cast<const float4 *>(&uw[g + 8][k]);
                     s[0] = fmaf(m0.x, u0.x, fmaf(m0.y, u0.y, fmaf(m0.z, u0.z, fmaf(m0.w, u0.w, s[0]))));
@@ -793,8 +794,9 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     auto scaled_u = [&](int j, float x0, float x1, float y0, float y1, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
         const int t = 8 * j + 2 * c;            // rows t, t + 1 of state row g (x) and g + 8 (y)
         const float w0 = sm.f_s[t] * sm.rk[t], w1 = sm.f_s[t + 1] * sm.rk[t + 1];
-        gb_split(x0 * w0, x1 * w1, hi[0], lo[0]);
-        gb_split(y0 * w0, y1 * w1, hi[1], lo[1]);
+        const bool in0 = t < kept, in1 = t + 1 < kept;
+        gb_split(in0 ? x0 * w0 : 0.f, in1 ? x1 * w1 : 0.f, hi[0], lo[0]);
+        gb_split(in0 ? y0 * w0 : 0.f, in1 ? y1 * w1 : 0.f, hi[1], lo[1]);
     };
     if constexpr (SMALL)
 #pragma unroll

@@ -226,7 +226,7 @@ constexpr int DELTA_BLOCK_MIN_ROWS = 3;
 template <int DK, int NK, int NQ>
 constexpr size_t delta_block_smem()
 {
-    return sizeof(GbSmem<DK, 8 * NK < 16 ? 16 : 8 * NK, 8 * NQ < 16 ? 16 : 8 * NQ>);
+    return sizeof(GbSmem<DK, 8 * NK, 8 * NQ>);
 }
 
 template <int DK, int NK, int NQ>
@@ -239,7 +239,7 @@ int delta_block_launch(const DeltaParams &p, int B, cudaStream_t stream)
 template <int DK>
 int delta_block_dispatch(const DeltaParams &p, int B, cudaStream_t stream)
 {
-    const int nk = (p.prev_T + 7) / 8 + (p.T + 7) / 8;
+    const int nk = (p.prev_T + p.T + 7) / 8;
     if (nk <= 1) return delta_block_launch<DK, 1, 1>(p, B, stream);
     if (nk <= 2 && p.T <= 8) return delta_block_launch<DK, 2, 1>(p, B, stream);
     if (nk <= 4 && p.T <= 16) return delta_block_launch<DK, 4, 2>(p, B, stream);
