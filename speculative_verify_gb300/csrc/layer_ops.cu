@@ -220,8 +220,18 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
     return p;
 }
 
-// Rows from which a step takes them all at once (gated_delta_block_kernel).
-constexpr int DELTA_BLOCK_MIN_ROWS = 3;
+// Whether a step runs row by row (gated_delta_step_kernel) or takes its rows
+// all at once (gated_delta_block_kernel).  One or two rows whose state is a
+// wave of small blocks at most are quicker without the second kernel's tiles:
+// 48 heads of 128 x 128, one row, 1 / 4 sequences 4.5 / 7.2 us against 5.9 /
+// 9.2, two rows 5.2 / 8.1 against 5.8 / 9.4.  Beyond that its asynchronous
+// copies win: 16 / 64 / 256 sequences of two rows 19.0 / 69 / 251 us against
+// 21.0 / 100 / 389.  At three rows the two are even (1 / 4 sequences 5.7 / 9.4
+// us, row by row 5.7 / 9.0), with more the tiles win.
+bool delta_step_by_rows(int rows, long long state_rows, const DeviceInfo &dev)
+{
+    return rows < 3 && state_rows <= 5LL * GB_COLS * dev.sms;
+}
 
 template <int DK, int NK, int NQ>
 constexpr size_t delta_block_smem()
@@ -372,13 +382,12 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
     p.prev_T = prev_T;
     if (prev_T > 0) p.prev = delta_rows(prev);
     p.accept_len = accept_len;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (!delta_step_by_rows(T + prev_T, static_cast<long long>(B) * p.Hv * p.dv, dev))
+        return shape->dk == 64 ? delta_block_dispatch<64>(p, B, cs) : delta_block_dispatch<128>(p, B, cs);
     const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
     const int cap = T > prev_T ? T : prev_T;
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));
-    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (T + prev_T >= DELTA_BLOCK_MIN_ROWS) {
-        return shape->dk == 64 ? delta_block_dispatch<64>(p, B, cs) : delta_block_dispatch<128>(p, B, cs);
-    }
     return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, 4 * p.cols, smem, cs, p)
                            : launch(gated_delta_step_kernel<128>, grid, 4 * p.cols, smem, cs, p);
 }
