@@ -532,32 +532,6 @@ struct DsSmem {                                 // from a 1024-byte boundary
 // even and one for odd steps: their next phase needs the waiter to go on.
 enum { B_FULL0, B_FULL1, B_P, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_MREADY, B_YFREE, B_COUNT };
 
-constexpr uint32_t ds_idesc(int n, bool b_mn)
-{
-    // fp32 accumulator, bf16 operands; B along the rows' length (K-major) or across
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-           ((128u >> 4) << 24);
-}
-
-// The rare long wait, out of line: the roles' loops share the instruction cache.
-static __device__ __noinline__ void ds_long_wait(uint32_t bar, uint32_t parity, volatile int *flag, int *err)
-{
-    if (mbar_wait_bounded(bar, parity, *flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) return;
-    *flag = 1;
-    atomicOr(err, 2);
-}
-
-// Whole warps wait (with one lane polling for the others the prompts' scan
-// took 298 instead of 255 us).
-struct DsWait {
-    volatile int *flag;
-    int *err;
-    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const
-    {
-        if (!mbar_sleep_wait(bar, parity & 1u, 100000u)) ds_long_wait(bar, parity & 1u, flag, err);
-    }
-};
-
 // A CTA's part of the chains: segments of one head of one sequence each.
 struct DsWalk {
     const DeltaChunkParams *cp;
@@ -660,7 +634,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
     volatile int *flag = reinterpret_cast<volatile int *>(bars + B_COUNT);
     volatile uint32_t *slot_tm = reinterpret_cast<volatile uint32_t *>(flag + 1);
     auto bar = [&](int i) { return base + static_cast<uint32_t>(L::BARS + 8 * i); };
-    const DsWait wait{flag, p.err};
+    const TcWait wait{flag, p.err};
 
     if (base & 1023u) {
         if (threadIdx.x == 0) atomicOr(p.err, 4);
@@ -729,8 +703,8 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 const uint32_t y = tmem + DS_O;
                 auto s_product = [&](uint32_t d, uint32_t rows, int s) {
                     const uint64_t b = desc_k_sw128(rows + (s >> 2) * DC_ROWS * 128 + (s & 3) * 32);
-                    tc_mma_f16_ts_warp(d, tmem + DS_SHI + 8 * s, b, ds_idesc(64, false), s > 0);
-                    tc_mma_f16_ts_warp(d, tmem + DS_SLO + 8 * s, b, ds_idesc(64, false), 1);
+                    tc_mma_f16_ts_warp(d, tmem + DS_SHI + 8 * s, b, tc_idesc_bf16(64, false), s > 0);
+                    tc_mma_f16_ts_warp(d, tmem + DS_SLO + 8 * s, b, tc_idesc_bf16(64, false), 1);
                 };
                 // P: S x K
                 wait(bar(B_FULL0 + (t & 1)), t >> 1);
@@ -756,7 +730,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 for (int s = 0; s < 4; ++s) {
                     const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
                     const uint64_t hi = desc_mn_sw128(mb + off), lo = desc_mn_sw128(mb + DC_MAT + off);
-                    const uint32_t id = ds_idesc(64 - 16 * s, true), d = tmem + DS_U + 16 * s, r = tmem + DS_R + 8 * s;
+                    const uint32_t id = tc_idesc_bf16(64 - 16 * s, true), d = tmem + DS_U + 16 * s, r = tmem + DS_R + 8 * s;
                     tc_mma_f16_ts_warp(d, r, hi, id, s > 0);
                     tc_mma_f16_ts_warp(d, r + 32, hi, id, 1);
                     tc_mma_f16_ts_warp(d, r, lo, id, 1);
@@ -772,8 +746,8 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint64_t d = desc_mn_sw128(kb + s * 2048);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 8 * s, d, ds_idesc(DK, true), s > 0);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 32 + 8 * s, d, ds_idesc(DK, true), 1);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 8 * s, d, tc_idesc_bf16(DK, true), s > 0);
+                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 32 + 8 * s, d, tc_idesc_bf16(DK, true), 1);
                 }
                 tc_commit_warp(bar(B_D));
                 // M: u x M
@@ -784,7 +758,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 for (int s = 0; s < 4; ++s) {
                     const uint32_t off = static_cast<uint32_t>(2048 * s + 32 * s);
                     const uint64_t hi = desc_k_sw128(mb + 2 * DC_MAT + off), lo = desc_k_sw128(mb + 3 * DC_MAT + off);
-                    const uint32_t id = ds_idesc(64 - 16 * s, false), d = tmem + DS_M + 16 * s, u = tmem + DS_U + 8 * s;
+                    const uint32_t id = tc_idesc_bf16(64 - 16 * s, false), d = tmem + DS_M + 16 * s, u = tmem + DS_U + 8 * s;
                     tc_mma_f16_ts_warp(d, u, hi, id, s > 0);
                     tc_mma_f16_ts_warp(d, u + 32, hi, id, 1);
                     tc_mma_f16_ts_warp(d, u, lo, id, 1);

@@ -14,6 +14,7 @@
 #include "specverify.h"
 #include "sv_host.h"
 #include "w4a16_gate_up.cuh"
+#include "w4a16_gate_up_tc.cuh"
 
 namespace sv {
 namespace {
@@ -22,19 +23,26 @@ constexpr int MAX_DEVICES = 64;
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-// Tensor map of `rows` bf16 rows of `cols` values, `ld` elements apart; boxes
-// of 64 rows and `width` values, 128-byte swizzled where they are 64 wide.
-int encode_rows(CUtensorMap *m, const void *base, long long cols, long long rows, long long ld, int width, bool swizzled)
+// Tensor map of `rows` rows of `cols` values, `pitch` bytes apart; boxes of
+// `height` rows and `width` values, 128-byte swizzled where asked.
+int encode_rows(CUtensorMap *m, CUtensorMapDataType type, const void *base, long long cols, long long rows,
+                long long pitch, int width, int height, bool swizzled)
 {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), DC_ROWS};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(height)};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUresult r = g_encode(m, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SV_OK : SV_ERR_CUDA;
+}
+
+// bf16 rows, `ld` values apart, in boxes of a block of prompt rows.
+int encode_blocks(CUtensorMap *m, const void *base, long long cols, long long rows, long long ld, int width, bool swizzled)
+{
+    return encode_rows(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, 2 * ld, width, DC_ROWS, swizzled);
 }
 
 template <class F>
@@ -78,6 +86,8 @@ int ops_device(DeviceInfo *out)
     up(raise(w4a16_gate_up_kernel<1>, gu_smem_bytes(1)));
     up(raise(w4a16_gate_up_kernel<2>, gu_smem_bytes(2)));
     up(raise(w4a16_gate_up_kernel<4>, gu_smem_bytes(4)));
+    up(raise(w4a16_gate_up_tc_kernel<16>, GtSmem<16>::BYTES));
+    up(raise(w4a16_gate_up_tc_kernel<32>, GtSmem<32>::BYTES));
     if (e != cudaSuccess) {
         cudaGetLastError();
         return SV_ERR_CUDA;
@@ -278,9 +288,9 @@ int delta_chunk_launch(const DeltaChunkParams &p, const DeviceInfo &dev, cudaStr
     CUtensorMap tmK, tmQ, tmV;
     const DeltaRows &r = p.d.rows;
     const long long nk = static_cast<long long>(p.d.Hk) * DK, nv = static_cast<long long>(p.d.Hv) * p.d.dv;
-    int rc = encode_rows(&tmK, r.k, nk, p.R, r.ldk, 64, true);
-    if (rc == SV_OK) rc = encode_rows(&tmQ, r.q, nk, p.R, r.ldq, 64, true);
-    if (rc == SV_OK) rc = encode_rows(&tmV, r.v, nv, p.R, r.ldv, p.d.dv, false);
+    int rc = encode_blocks(&tmK, r.k, nk, p.R, r.ldk, 64, true);
+    if (rc == SV_OK) rc = encode_blocks(&tmQ, r.q, nk, p.R, r.ldq, 64, true);
+    if (rc == SV_OK) rc = encode_blocks(&tmV, r.v, nv, p.R, r.ldv, p.d.dv, false);
     if (rc != SV_OK) return rc;
     const long long blocks = delta_blocks(p.R, p.B), parts = std::min<long long>(dev.sms, blocks * p.d.Hv);
     rc = launch(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.d.Hk)), 128,
@@ -291,6 +301,50 @@ int delta_chunk_launch(const DeltaChunkParams &p, const DeviceInfo &dev, cudaStr
 }
 
 // ------------------------------------------------------ gated feed-forward
+
+// Columns of a tile of the wide kernel: the result divided evenly over the
+// multiprocessors, in as few rounds of 128 lanes as hold it.
+int gate_up_cols(int F, int sms)
+{
+    const long long rounds = (F + 1LL * sms * GT_ROWS - 1) / (1LL * sms * GT_ROWS);
+    return static_cast<int>((F + sms * rounds - 1) / (sms * rounds));
+}
+
+// Whether the wide kernel (w4a16_gate_up_tc_kernel) is the quicker one.  Its
+// time goes with the groups of K and the rounds (4 + 0.44 us a group up to 16
+// tokens, 5 + 0.53 beyond), whatever the tile's columns, the other kernel's
+// with the weights.  Measured, wide against other, K 5,120: F 9,728 (64
+// columns a tile) 32 tokens 25.9 / 26.4 us; F 10,944 (72) 16 tokens 21.5 /
+// 23.0, 32 tokens 26.0 / 33.4; F 12,768 (84) 8 tokens 21.1 / 18.9; F 15,048
+// (99) 8 tokens 21.2 / 22.8; F 17,408 (115) 1 / 8 / 16 / 32 tokens 21.5 / 21.7 /
+// 22.1 / 26.6 against 23.5 / 23.9 / 30.0 / 42.3.  With K 1,280 the wide
+// kernel's start weighs more: F 17,408, 8 / 16 / 32 tokens 9.0 / 9.4 / 11.7
+// against 7.5 / 9.3 / 12.9.
+bool gate_up_wide(int T, int G, int cols)
+{
+    return cols >= (T > 16 ? 54 + 430 / G : T > 8 ? 60 + 430 / G : 82 + 680 / G);
+}
+
+template <int N>
+int gate_up_tc_launch(const GateUpParams &q, const DeviceInfo &dev, cudaStream_t stream)
+{
+    GateUpTcParams p{};
+    p.scales = q.scales;
+    p.h = q.h;
+    p.T = q.T;
+    p.G = q.G;
+    p.F = q.F;
+    p.act = q.act;
+    p.err = dev.err;
+    p.cols = gate_up_cols(q.F, dev.sms);
+    p.tiles = (q.F + p.cols - 1) / p.cols;
+    CUtensorMap tmW, tmX;
+    int rc = encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT32, q.Wq, q.K / 8, 2LL * q.F, q.K / 2, 32, p.cols, true);
+    if (rc == SV_OK) rc = encode_rows(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.x, q.K, q.T, 2LL * q.K, 64, N, true);
+    if (rc != SV_OK) return rc;
+    const unsigned grid = static_cast<unsigned>(std::min(p.tiles, dev.sms));
+    return launch(w4a16_gate_up_tc_kernel<N>, dim3(grid), GT_THREADS, GtSmem<N>::BYTES, stream, p, tmW, tmX);
+}
 
 template <int NT>
 int gate_up_launch(const GateUpParams &p, const DeviceInfo &dev, cudaStream_t stream)
@@ -457,9 +511,11 @@ int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, i
     p.F = F;
     p.tiles = (F + 7) / 8;
     p.act = act;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (gate_up_wide(T, p.G, gate_up_cols(F, dev.sms)))
+        return T <= 16 ? gate_up_tc_launch<16>(p, dev, cs) : gate_up_tc_launch<32>(p, dev, cs);
     const int per = (p.tiles + dev.sms - 1) / dev.sms;      // tiles of a block
     while (p.ks_log < 4 && (per << (p.ks_log + 1)) <= GU_WARPS) ++p.ks_log;
-    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (T <= 8) return gate_up_launch<1>(p, dev, cs);
     if (T <= 16) return gate_up_launch<2>(p, dev, cs);
     return gate_up_launch<4>(p, dev, cs);

@@ -7,6 +7,7 @@
 
 #include "gated_delta.cuh"
 #include "sv_ptx.cuh"
+#include "w4a16_stream.cuh"
 
 namespace sv {
 
@@ -122,5 +123,32 @@ __device__ __forceinline__ void prefetch_l2_2d(const void *tmap, int c0, int c1)
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
                  ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1) : "memory");
 }
+
+// Instruction descriptor of an M = 128 product of N = n columns: bf16
+// operands, fp32 accumulator; B's rows along the products' K, or across.
+constexpr uint32_t tc_idesc_bf16(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+// The rare long wait, out of line: the roles' loops share the instruction cache.
+static __device__ __noinline__ void tc_long_wait(uint32_t bar, uint32_t parity, volatile int *flag, int *err)
+{
+    if (mbar_wait_bounded(bar, parity, *flag ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) return;
+    *flag = 1;
+    atomicOr(err, 2);
+}
+
+// Whole warps wait (with one lane polling for the others the gated delta
+// scan took 298 instead of 255 us).
+struct TcWait {
+    volatile int *flag;                         // in shared memory: a wait ran out
+    int *err;
+    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const
+    {
+        if (!mbar_sleep_wait(bar, parity & 1u, 100000u)) tc_long_wait(bar, parity & 1u, flag, err);
+    }
+};
 
 }  // namespace sv

@@ -1,6 +1,8 @@
 // w4a16_gate_up.cuh -- the first half of a gated feed-forward block from int4
 // weights: h = act(x Wg^T) * (x Wu^T), both projections, the activation and
 // the product in one pass over the packed weights.
+// w4a16_gate_up_tc.cuh has the form for wide projections; this one is the
+// quicker for narrow ones and few tokens, where its time goes with the weights.
 //
 // Wq holds the F gate rows and then the F up rows in the library's W4A16
 // format.  The m16n8k16 MMA leaves rows g and g + 8 of its A operand in the
