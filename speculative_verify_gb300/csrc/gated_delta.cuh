@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 //
 // A warp owns 16 rows of S.  S k and S q are tf32 products with S as the A
 // operand, in two terms (22 bits; keys and queries, bf16 as they come, are
-// exact in tf32); the update is a bf16 product with u in two terms (16 bits)
-// whose accumulator is S.  Everything between is fp32.  The block computes A
+// exact in tf32), and so is the update, with u in two terms and S as the
+// accumulator.  Everything between is fp32.  The block computes A
 // and M once for its warps.  Up to 16 rows in all, r, u and the outputs stay
 // in the products' accumulator layout: one pass over the rows hands each u to
 // the other lanes, which subtract it from their r and add it to their o.  With
@@ -359,17 +359,11 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 constexpr int GB_MAX = 2 * GD_MAX_ROWS;         // rows of prev and new together
 constexpr int GB_KPAD = 8, GB_FPAD = 4;         // padding of a row in shared memory, bf16 and fp32 values
 
-__device__ __forceinline__ uint32_t gb_pack(float lo, float hi)
+// v as two tf32 terms, 22 bits of it; the second's low bits are not read.
+__device__ __forceinline__ void gb_split_tf32(float v, uint32_t &hi, uint32_t &lo)
 {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ void gb_split(float a, float b, uint32_t &hi, uint32_t &lo)
-{
-    hi = gb_pack(a, b);
-    lo = gb_pack(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+    hi = __float_as_uint(v) & 0xFFFFE000u;
+    lo = __float_as_uint(v - __uint_as_float(hi));
 }
 
 __device__ __forceinline__ void gb_ldmatrix(uint32_t (&r)[4], const uint16_t *p)
@@ -382,13 +376,6 @@ __device__ __forceinline__ void gb_ldmatrix_trans(uint32_t (&r)[4], const uint16
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
-}
-
-// D (16x8 fp32) += A (16x8 bf16, row) * B (8x8 bf16, col).
-__device__ __forceinline__ void mma_bf16_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b)
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(b));
 }
 
 // Sums of two floats each, kept as the rounded sum and what it leaves:
@@ -651,10 +638,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         const float sv[4] = {x.x, y.x, x.y, y.y};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi[i] = __float_as_uint(sv[i]) & 0xFFFFE000u;
-            lo[i] = __float_as_uint(sv[i] - __uint_as_float(hi[i]));
-        }
+        for (int i = 0; i < 4; ++i) gb_split_tf32(sv[i], hi[i], lo[i]);
         auto product = [&](float (&d)[4], const uint16_t *row) {
             const uint32_t w = *reinterpret_cast<const uint32_t *>(row + 8 * s + 2 * c);
             const uint32_t b0 = w << 16, b1 = w & 0xFFFF0000u;
@@ -790,13 +774,14 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     // ---- the state after the wanted rows: S <- decay S + u' K, u' = u f_s r_k in two terms
     if (nu == 0) return;
     const float decay = sm.f_o;
-    uint32_t uh[2][2], ul[2][2];
-    auto scaled_u = [&](int j, float x0, float x1, float y0, float y1, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-        const int t = 8 * j + 2 * c;            // rows t, t + 1 of state row g (x) and g + 8 (y)
+    uint32_t uh[2][4], ul[2][4];
+    auto scaled_u = [&](int j, float x0, float x1, float y0, float y1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+        const int t = 8 * j + 2 * c;            // rows t, t + 1 of state row g (x) and g + 8 (y): the products' k = c and c + 4
         const float w0 = sm.f_s[t] * sm.rk[t], w1 = sm.f_s[t + 1] * sm.rk[t + 1];
         const bool in0 = t < kept, in1 = t + 1 < kept;
-        gb_split(in0 ? x0 * w0 : 0.f, in1 ? x1 * w1 : 0.f, hi[0], lo[0]);
-        gb_split(in0 ? y0 * w0 : 0.f, in1 ? y1 * w1 : 0.f, hi[1], lo[1]);
+        const float v[4] = {in0 ? x0 * w0 : 0.f, in0 ? y0 * w0 : 0.f, in1 ? x1 * w1 : 0.f, in1 ? y1 * w1 : 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gb_split_tf32(v[e], hi[e], lo[e]);
     };
     if constexpr (SMALL)
 #pragma unroll
@@ -813,13 +798,14 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
             st[e][2] = decay * y.x;
             st[e][3] = decay * y.y;
         }
-        auto add = [&](int j, const uint32_t (&hi)[2], const uint32_t (&lo)[2]) {
+        auto add = [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
             uint32_t bb[4];
             gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + 32 * i + (lane >> 3) * 8);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                mma_bf16_1688(st[e], lo[0], lo[1], bb[e]);
-                mma_bf16_1688(st[e], hi[0], hi[1], bb[e]);
+                const uint32_t b0 = bb[e] << 16, b1 = bb[e] & 0xFFFF0000u;
+                mma_tf32_1688(st[e], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                mma_tf32_1688(st[e], hi[0], hi[1], hi[2], hi[3], b0, b1);
             }
         };
         if constexpr (SMALL) {
