@@ -233,11 +233,11 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
 // Whether a step runs row by row (gated_delta_step_kernel) or takes its rows
 // all at once (gated_delta_block_kernel).  One or two rows whose state is a
 // wave of small blocks at most are quicker without the second kernel's tiles:
-// 48 heads of 128 x 128, one row, 1 / 4 sequences 4.5 / 7.2 us against 5.9 /
-// 9.2, two rows 5.2 / 8.1 against 5.8 / 9.4.  Beyond that its asynchronous
-// copies win: 16 / 64 / 256 sequences of two rows 19.0 / 69 / 251 us against
-// 21.0 / 100 / 389.  At three rows the two are even (1 / 4 sequences 5.7 / 9.4
-// us, row by row 5.7 / 9.0), with more the tiles win.
+// 48 heads of 128 x 128, one row, 1 / 4 sequences 4.5 / 7.1 us against 5.9 /
+// 9.2, two rows 5.0 / 8.1 against 5.8 / 9.4.  Beyond that its asynchronous
+// copies win: 16 / 64 / 256 sequences of two rows 19 / 66 / 244 us against
+// 21 / 100 / 389, and so do its tiles with more rows: 3 rows of 1 / 4
+// sequences 5.3 / 9.2 us, row by row 5.7 / 9.0.
 bool delta_step_by_rows(int rows, long long state_rows, const DeviceInfo &dev)
 {
     return rows < 3 && state_rows <= 5LL * GB_COLS * dev.sms;
