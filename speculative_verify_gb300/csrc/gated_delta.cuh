@@ -357,13 +357,14 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 // chain of small steps (gates, norms, A) runs, and back through it (8-byte
 // stores from the accumulators: 248 instead of 238 us).
 //
+// A NaN or an infinity in a row reaches that row and later ones only.
+//
 // Measured, 48 heads of 128 x 128: 256 sequences with 4 rows and 4 replayed
-// 238 us, 6.98 TB/s, HBM-bound (five blocks a multiprocessor); with 8 and 8,
-// 320 us (four).  4 sequences with 8 and 8 rows 10.2 us, of which 3.9 are
+// 245 us, 6.8 TB/s, HBM-bound (five blocks a multiprocessor); with 8 and 8,
+// 320 us (four).  4 sequences with 8 and 8 rows 10.4 us, of which 3.9 are
 // traffic: the chain of a block -- slot and gates from memory, running sum,
 // decays, A, S k, u, update -- takes 5.3 us by itself (one sequence).
 
-constexpr int GB_MAX = 2 * GD_MAX_ROWS;         // rows of prev and new together
 constexpr int GB_KPAD = 8, GB_FPAD = 4;         // padding of a row in shared memory, bf16 and fp32 values
 
 // v as two tf32 terms, 22 bits of it; the second's low bits are not read.
@@ -697,20 +698,22 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
             const float ug = __shfl_sync(0xFFFFFFFFu, pk[s >> 3][s & 1], from), uh = __shfl_sync(0xFFFFFFFFu, pk[s >> 3][2 + (s & 1)], from);
 #pragma unroll
             for (int j = s >> 3; j < NK; ++j) {
-                const float2 av = *reinterpret_cast<const float2 *>(&sm.a[s][8 * j + 2 * c]);   // 0 up to row s
-                pk[j][0] = fmaf(-av.x, ug, pk[j][0]);
-                pk[j][1] = fmaf(-av.y, ug, pk[j][1]);
-                pk[j][2] = fmaf(-av.x, uh, pk[j][2]);
-                pk[j][3] = fmaf(-av.y, uh, pk[j][3]);
+                const float2 av = *reinterpret_cast<const float2 *>(&sm.a[s][8 * j + 2 * c]);
+                const bool on0 = 8 * j + 2 * c > s, on1 = 8 * j + 2 * c + 1 > s;   // (a NaN stays with later rows)
+                if (on0) pk[j][0] = fmaf(-av.x, ug, pk[j][0]);
+                if (on1) pk[j][1] = fmaf(-av.y, ug, pk[j][1]);
+                if (on0) pk[j][2] = fmaf(-av.x, uh, pk[j][2]);
+                if (on1) pk[j][3] = fmaf(-av.y, uh, pk[j][3]);
             }
             if (tn > 0)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
                     const float2 mv = *reinterpret_cast<const float2 *>(&sm.m[SMALL ? s : 0][8 * j + 2 * c]);
-                    pq[j][0] = fmaf(mv.x, ug, pq[j][0]);
-                    pq[j][1] = fmaf(mv.y, ug, pq[j][1]);
-                    pq[j][2] = fmaf(mv.x, uh, pq[j][2]);
-                    pq[j][3] = fmaf(mv.y, uh, pq[j][3]);
+                    const bool on0 = na + 8 * j + 2 * c >= s, on1 = na + 8 * j + 2 * c + 1 >= s;
+                    if (on0) pq[j][0] = fmaf(mv.x, ug, pq[j][0]);
+                    if (on1) pq[j][1] = fmaf(mv.y, ug, pq[j][1]);
+                    if (on0) pq[j][2] = fmaf(mv.x, uh, pq[j][2]);
+                    if (on1) pq[j][3] = fmaf(mv.y, uh, pq[j][3]);
                 }
         }
 #pragma unroll
@@ -777,10 +780,16 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                 for (int k = 0; k < min(na + 8 * j + 8, 8 * nk); k += 4) {
                     const float4 m0 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0][k]), m1 = *reinterpret_cast<const float4 *>(&sm.m[SMALL ? 0 : t0 + 1][k]);
                     const float4 u0 = *reinterpret_cast<const float4 *>(&uw[g][k]), u1 = *reinterpret_cast<const float4 *>(&uw[g + 8][k]);
-                    s[0] = fmaf(m0.x, u0.x, fmaf(m0.y, u0.y, fmaf(m0.z, u0.z, fmaf(m0.w, u0.w, s[0]))));
-                    s[1] = fmaf(m1.x, u0.x, fmaf(m1.y, u0.y, fmaf(m1.z, u0.z, fmaf(m1.w, u0.w, s[1]))));
-                    s[2] = fmaf(m0.x, u1.x, fmaf(m0.y, u1.y, fmaf(m0.z, u1.z, fmaf(m0.w, u1.w, s[2]))));
-                    s[3] = fmaf(m1.x, u1.x, fmaf(m1.y, u1.y, fmaf(m1.z, u1.z, fmaf(m1.w, u1.w, s[3]))));
+                    const float ma[4] = {m0.x, m0.y, m0.z, m0.w}, mb[4] = {m1.x, m1.y, m1.z, m1.w};
+                    const float ua[4] = {u0.x, u0.y, u0.z, u0.w}, ub[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool on0 = na + t0 >= k + i, on1 = na + t0 + 1 >= k + i;   // (a NaN stays with later rows)
+                        if (on0) s[0] = fmaf(ma[i], ua[i], s[0]);
+                        if (on1) s[1] = fmaf(mb[i], ua[i], s[1]);
+                        if (on0) s[2] = fmaf(ma[i], ub[i], s[2]);
+                        if (on1) s[3] = fmaf(mb[i], ub[i], s[3]);
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -818,9 +827,12 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         auto add = [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
             uint32_t bb[4];
             gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + 32 * i + (lane >> 3) * 8);
+            // rows 8 j + 2 c and + 1, zero where not kept: their u is, but a key may hold a NaN
+            const int t = 8 * j + 2 * c;
+            const uint32_t rows_in = t + 1 < kept ? 0xFFFFFFFFu : t < kept ? 0xFFFFu : 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t b0 = bb[e] << 16, b1 = bb[e] & 0xFFFF0000u;
+                const uint32_t b = bb[e] & rows_in, b0 = b << 16, b1 = b & 0xFFFF0000u;
                 mma_tf32_1688(st[e], lo[0], lo[1], lo[2], lo[3], b0, b1);
                 mma_tf32_1688(st[e], hi[0], hi[1], hi[2], hi[3], b0, b1);
             }
