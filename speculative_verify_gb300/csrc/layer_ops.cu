@@ -279,8 +279,13 @@ cudaError_t delta_block_raise()
 // Blocks of the workspace: every sequence's whole and part blocks.
 long long delta_blocks(int R, int B) { return static_cast<long long>(R / DC_ROWS) + B; }
 
-// Short prompts (fewer rows than a block on average) go row by row.
-bool delta_by_rows(int R, int B) { return R < static_cast<long long>(DC_ROWS) * B; }
+// A few rows go row by row, without blocks.  48 heads of 128 x 128, row by row
+// against by blocks: one sequence of 16 / 32 / 48 / 64 rows 14 / 25 / 36 / 47 us
+// against 25 / 25 / 25 / 26, four of 16 / 32 rows 24 / 43 against 39 / 39, 64 of
+// 16 rows 284 against 268.  How the rows are shared out is known on the device
+// only, so the limit on their number also bounds the loss where one sequence
+// has them all.
+bool delta_by_rows(int R, int B) { return R <= DC_ROWS && R < 32LL * B; }
 
 template <int DK>
 int delta_chunk_launch(const DeltaChunkParams &p, const DeviceInfo &dev, cudaStream_t stream)

@@ -661,3 +661,30 @@ def test_repeat_calls_are_bit_identical(sv):
     a, b = state.clone(), state.clone()
     oa, ob = run_chunk(sv, rows, lens, a, idx), run_chunk(sv, rows, lens, b, idx)
     assert torch.equal(oa, ob) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens", [[16], [31], [3, 0, 20, 1], [16, 15, 17], [64, 0, 0], [1] * 40])
+@pytest.mark.parametrize("zero", [False, True])
+def test_chunk_of_few_rows(sv, lens, zero):
+    """Prompts of a few rows in all, one of them inactive."""
+    g = rng_of(sum(lens) + len(lens))
+    Hk, Hv, d, B = 2, 4, 128, len(lens)
+    rows = delta_rows(g, (sum(lens),), Hk, Hv, d, d)
+    state = randn(g, B + 2, Hv, d, d)
+    idx = torch.randperm(B + 2, device="cuda", generator=g)[:B].to(torch.int32)
+    own = idx.clone()                           # (the reference's place for the inactive one's state)
+    if B > 2:
+        idx[1] = -1
+    got = state.clone()
+    o = run_chunk(sv, rows, lens, got, idx, zero)
+    outs, want = chunk64(rows, lens, state, own, zero, d ** -0.5, True)
+    live = [b for b in range(B) if int(idx[b]) >= 0]
+    for b, part in enumerate(o.split(lens)):
+        if b in live:
+            check_out(part, outs[b], 2.0 ** -7)
+            check_state(got[int(idx[b])], want[int(idx[b])])
+        else:
+            assert bool((part == 0).all())
+    untouched = [s for s in range(B + 2) if s not in idx.tolist()]
+    assert torch.equal(got[untouched], state[untouched])
+    assert sv.last_device_error() == 0
