@@ -93,7 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, LIB_PATH)
         # torch's libraries are in the process before the binding is
         _run([[cxx, "-shared", "-o", bind_tmp, bind_obj, LIB_PATH, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
-               "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]], verbose)
+               "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]],
+             verbose)
         os.replace(bind_tmp, BIND_PATH)
     finally:
         for o in [*objs, bind_obj]:

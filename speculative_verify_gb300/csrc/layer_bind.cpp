@@ -11,7 +11,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -135,7 +135,7 @@ struct Stream {
 
 at::Tensor make(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType type)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 bool truth(PyObject *o)
