@@ -118,39 +118,75 @@ struct GdSmem {
     }
 };
 
-// Stage `n` rows (first row r0) of head hv in shared memory: keys and queries
-// in fp32 (normalised where asked, the query times `scale`), q.k, this
-// block's values, the gates and their running products.  Returns whether the
-// running products may be used (uniform over the block).
+// What a thread reads first of a block of rows: its values of the warp's first
+// row, its first values, the gates of a row (the last warp).
+template <int DK>
+struct GdFirst {
+    uint32_t k[DK / 64], q[DK / 64];
+    uint4 v;
+    float g, beta;
+};
+
+template <int N>
+__device__ __forceinline__ void gd_read(const uint16_t *src, uint32_t (&d)[N])
+{
+    if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(src);
+        d[0] = u.x;
+        d[1] = u.y;
+    } else {
+        d[0] = *reinterpret_cast<const uint32_t *>(src);
+    }
+}
+
+template <int DK>
+__device__ __forceinline__ void gd_first(const DeltaParams &p, const DeltaRows &r, long long r0, int n, int hv, int col0,
+                                         int cols, bool want_q, GdFirst<DK> &f)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = hv / (p.Hv / p.Hk);
+    if (warp < n) {
+        gd_read(r.k + (r0 + warp) * r.ldk + static_cast<long long>(hk) * DK + lane * (DK / 32), f.k);
+        if (want_q) gd_read(r.q + (r0 + warp) * r.ldq + static_cast<long long>(hk) * DK + lane * (DK / 32), f.q);
+    }
+    if (tid < n * (cols / 8)) {
+        const int t = tid / (cols / 8), j = (tid - t * (cols / 8)) * 8;
+        f.v = *reinterpret_cast<const uint4 *>(r.v + (r0 + t) * r.ldv + static_cast<long long>(hv) * p.dv + col0 + j);
+    }
+    if (warp == (blockDim.x >> 5) - 1 && lane < n) {
+        f.g = r.g[(r0 + lane) * r.ldg + hv];
+        f.beta = r.beta[(r0 + lane) * r.ldg + hv];
+    }
+}
+
+// Stage `n` rows (first row r0) of head hv in shared memory, `f` of them
+// having been read: keys and queries in fp32 (normalised where asked, the
+// query times `scale`), q.k, this block's values, the gates and their running
+// products.  Returns whether the running products may be used (uniform over
+// the block).
 template <int DK>
 __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &r, long long r0, int n, int hv, int col0,
-                                         int cols, const GdSmem<DK> &sm, bool want_q)
+                                         int cols, const GdSmem<DK> &sm, bool want_q, const GdFirst<DK> &f)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
     constexpr int E = DK / 32;                  // a lane's values of a row, consecutive
     const int hk = hv / (p.Hv / p.Hk);
     for (int t = warp; t < n; t += nwarp) {
+        uint32_t kw[E / 2], qw[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            kw[e] = f.k[e];
+            qw[e] = want_q ? f.q[e] : 0u;
+        }
+        if (t != warp) {
+            gd_read(r.k + (r0 + t) * r.ldk + static_cast<long long>(hk) * DK + lane * E, kw);
+            if (want_q) gd_read(r.q + (r0 + t) * r.ldq + static_cast<long long>(hk) * DK + lane * E, qw);
+        }
         float k[E], q[E];
         float kk = 0.f, qq = 0.f, qk = 0.f;
-        auto load = [&](const uint16_t *src, float (&d)[E]) {
-            if constexpr (E == 4) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(src + lane * E);
-                d[0] = __uint_as_float(u.x << 16);
-                d[1] = __uint_as_float(u.x & 0xFFFF0000u);
-                d[2] = __uint_as_float(u.y << 16);
-                d[3] = __uint_as_float(u.y & 0xFFFF0000u);
-            } else {
-                const uint32_t u = *reinterpret_cast<const uint32_t *>(src + lane * E);
-                d[0] = __uint_as_float(u << 16);
-                d[1] = __uint_as_float(u & 0xFFFF0000u);
-            }
-        };
-        load(r.k + (r0 + t) * r.ldk + static_cast<long long>(hk) * DK, k);
-        if (want_q) {
-            load(r.q + (r0 + t) * r.ldq + static_cast<long long>(hk) * DK, q);
-        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[e] = 0.f;
+        for (int e = 0; e < E; ++e) {
+            k[e] = __uint_as_float((e & 1) ? kw[e / 2] & 0xFFFF0000u : kw[e / 2] << 16);
+            q[e] = __uint_as_float((e & 1) ? qw[e / 2] & 0xFFFF0000u : qw[e / 2] << 16);
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -176,7 +212,7 @@ __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &
     // values: eight per thread (cols is a multiple of 32)
     for (int i = tid; i < n * (cols / 8); i += blockDim.x) {
         const int t = i / (cols / 8), j = (i - t * (cols / 8)) * 8;
-        const uint4 u = *reinterpret_cast<const uint4 *>(r.v + (r0 + t) * r.ldv + static_cast<long long>(hv) * p.dv + col0 + j);
+        const uint4 u = i == tid ? f.v : *reinterpret_cast<const uint4 *>(r.v + (r0 + t) * r.ldv + static_cast<long long>(hv) * p.dv + col0 + j);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -186,8 +222,8 @@ __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &
     }
     // gates; the running sum of the log decays by a warp scan (n <= 32)
     bool ok = true;
-    if (warp == 0) {
-        const float g = lane < n ? r.g[(r0 + lane) * r.ldg + hv] : 0.f;
+    if (warp == nwarp - 1) {
+        const float g = lane < n ? f.g : 0.f;
         float G = g;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -196,7 +232,7 @@ __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &
         }
         ok = fabsf(G) <= GD_MAX_LOG;            // false for a NaN too
         if (lane < n) {
-            sm.beta[lane] = r.beta[(r0 + lane) * r.ldg + hv];
+            sm.beta[lane] = f.beta;
             sm.eg[lane] = expf(g);
             sm.c[lane] = expf(G);
             sm.cinv[lane] = expf(-G);
@@ -307,9 +343,16 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
     const GdSmem<DK> sm(gd_smem, cap, cols);
     pdl_launch_dependents();
     pdl_wait_prior();
+    // rows, which need no slot, are asked for before it is waited for
+    const DeltaRows &lead = p.prev_T > 0 ? p.prev : p.rows;
+    const int lead_T = p.prev_T > 0 ? p.prev_T : p.T;
+    const int slot = p.state_idx ? p.state_idx[b] : b;
+    const int accept = p.accept_len && p.prev_T > 0 ? p.accept_len[b] : p.prev_T;
+    GdFirst<DK> f;
+    gd_first<DK>(p, lead, static_cast<long long>(b) * lead_T, lead_T, hv, col0, cols, p.prev_T == 0, f);
     uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
-    const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
-    if (slot < 0) {                             // an inactive entry: its outputs are zero
+    if (slot < 0 || slot >= p.n_slots) {        // an inactive entry: its outputs are zero
+        if (slot >= 0 && threadIdx.x == 0) atomicOr(p.err, 8);
         for (int t = 0; t < p.T; ++t)
             if (i == 0) o[t * p.ldo + col] = 0;
         return;
@@ -317,16 +360,18 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
     float *s = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0 + col) * DK;
     GdState<DK> st;
     st.load(s, i);
-    int n = p.prev_T;
-    if (p.accept_len && n > 0) n = min(n, max(0, min(p.accept_len[b], n) + 1));
-    if (n > 0) {
-        const bool running = gd_stage<DK>(p, p.prev, static_cast<long long>(b) * p.prev_T, n, hv, col0, cols, sm, false);
-        gd_rows<DK, false>(st, sm, n, cols, running, nullptr, 0);
-        if (!p.commit) st.store(s, i);
-        __syncthreads();
+    if (p.prev_T > 0) {
+        const int n = p.accept_len ? min(p.prev_T, max(0, min(accept, p.prev_T) + 1)) : p.prev_T;
+        if (n > 0) {
+            const bool running = gd_stage<DK>(p, p.prev, static_cast<long long>(b) * p.prev_T, n, hv, col0, cols, sm, false, f);
+            gd_rows<DK, false>(st, sm, n, cols, running, nullptr, 0);
+            if (!p.commit) st.store(s, i);
+            __syncthreads();
+        }
+        if (p.T > 0) gd_first<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, cols, true, f);
     }
     if (p.T > 0) {
-        const bool running = gd_stage<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, cols, sm, true);
+        const bool running = gd_stage<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, cols, sm, true, f);
         gd_rows<DK, true>(st, sm, p.T, cols, running, o, p.ldo);
     }
     if (p.commit) st.store(s, i);

@@ -93,7 +93,9 @@ __global__ void __launch_bounds__(512) gated_delta_rows_kernel(const DeltaChunkP
         st.load(s, i);
     for (int r0 = begin; r0 < end; r0 += GD_MAX_ROWS) {
         const int n = min(GD_MAX_ROWS, end - r0);
-        const bool running = gd_stage<DK>(p, p.rows, r0, n, hv, col0, cols, sm, true);
+        GdFirst<DK> f;
+        gd_first<DK>(p, p.rows, r0, n, hv, col0, cols, true, f);
+        const bool running = gd_stage<DK>(p, p.rows, r0, n, hv, col0, cols, sm, true, f);
         gd_rows<DK, true>(st, sm, n, cols, running, o, p.ldo);
         o += n * p.ldo;
         __syncthreads();
