@@ -230,7 +230,7 @@ __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &
             const float below = __shfl_up_sync(0xFFFFFFFFu, G, o);
             if (lane >= o) G += below;
         }
-        ok = fabsf(G) <= GD_MAX_LOG;            // false for a NaN too
+        ok = !(fabsf(G) > GD_MAX_LOG);          // (a NaN spoils its row and later ones either way)
         if (lane < n) {
             sm.beta[lane] = f.beta;
             sm.eg[lane] = expf(g);
@@ -389,14 +389,15 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 //   S'  = e^(G_m) S + sum_{s<m} (e^(G_m - G_s) r_k,s u_s) k_s^T
 // where the state is wanted after the first m rows: the accepted ones, or all.
 //
-// A warp owns 16 rows of S.  S k and S q are tf32 products with S as the A
-// operand, in two terms (22 bits; keys and queries, bf16 as they come, are
-// exact in tf32), and so is the update, with u in two terms and S as the
-// accumulator.  Everything between is fp32.  The block computes A
-// and M once for its warps.  Up to 16 rows in all, r, u and the outputs stay
-// in the products' accumulator layout: one pass over the rows hands each u to
-// the other lanes, which subtract it from their r and add it to their o.  With
-// more rows u comes by substitution in shared memory.
+// A warp owns 16 rows of S, or half the columns of 16 rows (KS = 2: the two
+// warps' parts of S k and S q meet in shared memory, and both go on).  S k and
+// S q are tf32 products with S as the A operand, in two terms (22 bits; keys
+// and queries, bf16 as they come, are exact in tf32), and so is the update,
+// with u in two terms and S as the accumulator.  Everything between is fp32.
+// The block computes A and M once for its warps.  Up to 16 rows in all, r, u
+// and the outputs stay in the products' accumulator layout: one pass over the
+// rows hands each u to the other lanes, which subtract it from their r and add
+// it to their o.  With more rows u comes by substitution in shared memory.
 //
 // A block has 64 state rows; a warp copies its rows to shared memory while the
 // chain of small steps (gates, norms, A) runs, and back through it (8-byte
@@ -406,9 +407,10 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 //
 // Measured, 48 heads of 128 x 128: 256 sequences with 4 rows and 4 replayed
 // 245 us, 6.8 TB/s, HBM-bound (five blocks a multiprocessor); with 8 and 8,
-// 320 us (four).  4 sequences with 8 and 8 rows 10.4 us, of which 3.9 are
-// traffic: the chain of a block -- slot and gates from memory, running sum,
-// decays, A, S k, u, update -- takes 5.3 us by itself (one sequence).
+// 320 us (four).  4 sequences with 8 and 8 rows 9.7 us (10.5 with one warp for
+// 16 state rows), of which 3.9 are traffic: the chain of a block -- slot and
+// gates from memory, running sum, decays, A, S k, u, update -- takes 5.4 us by
+// itself (one sequence).
 
 constexpr int GB_KPAD = 8, GB_FPAD = 4;         // padding of a row in shared memory, bf16 and fp32 values
 
@@ -450,10 +452,10 @@ __device__ __forceinline__ float exp_diff(Sum2 a, float bhi, float blo) { return
 constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
 
 constexpr int GB_COLS = 64;                     // state rows of a block
-constexpr int GB_THREADS = 2 * GB_COLS;         // a warp for 16 of them
+constexpr int gb_threads(int KS) { return 2 * GB_COLS * KS; }  // KS warps for 16 of them, a part of the columns each
 
 // Shared memory of a block: NP rows in all, NQR new ones (8 or multiples of 16).
-template <int DK, int NP, int NQR>
+template <int DK, int NP, int NQR, int KS>
 struct GbSmem {
     static constexpr bool SMALL = NP <= 16;     // r, u and o stay in registers
     float s[GB_COLS][DK + 8];                   // the state (rows padded: fragment loads free of bank conflicts)
@@ -463,6 +465,7 @@ struct GbSmem {
     float u[SMALL ? 1 : GB_COLS][NP + GB_FPAD];
     float ed[SMALL ? NP : 1][NP + GB_FPAD];     // decays between rows
     float g_hi[NP], g_lo[NP], beta[NP], rk[NP], rq[NQR], f_p[NP], f_s[NP], f_o;
+    float part[KS == 1 ? 1 : 4 * KS][(NP + NQR) / 2][32];   // KS > 1: the warps' parts of S k and S q
 };
 
 // D (16x8 fp32) += A (16x8 tf32, row) * B (8x8 tf32, col); the operands' low 13 bits are not read.
@@ -475,16 +478,18 @@ __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32
 
 // NK, NQ: most n8 tiles of rows and of new rows.  Grid: x = dv / GB_COLS,
 // y = Hv, z = B.
-template <int DK, int NK, int NQ>
-__global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const DeltaParams p)
+template <int DK, int NK, int NQ, int KS>
+__global__ void __launch_bounds__(gb_threads(KS), 4 / KS) gated_delta_block_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(16) uint8_t gb_smem[];
     constexpr int NP = 8 * NK, NQR = 8 * NQ;
-    using Smem = GbSmem<DK, NP, NQR>;
+    using Smem = GbSmem<DK, NP, NQR, KS>;
     constexpr bool SMALL = Smem::SMALL;
     Smem &sm = *reinterpret_cast<Smem *>(gb_smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    constexpr int NWARP = GB_THREADS / 32;
+    constexpr int THREADS = gb_threads(KS), NWARP = THREADS / 32, COLS = DK / KS;
+    static_assert(KS == 1 || SMALL, "the parts meet in the accumulator layout");
+    const int wr = warp & 3, wk = warp >> 2;    // 16 state rows, COLS columns
     const int col0 = blockIdx.x * GB_COLS, hv = blockIdx.y, b = blockIdx.z, hk = hv / (p.Hv / p.Hk);
     pdl_launch_dependents();
     pdl_wait_prior();
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     const int slot = gd_slot(p.state_idx, p.n_slots, b, p.err);
     uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
     if (slot < 0) {                             // an inactive entry: its outputs are zero
-        for (int i = tid; i < p.T * GB_COLS; i += GB_THREADS) o[(i / GB_COLS) * p.ldo + i % GB_COLS] = 0;
+        for (int i = tid; i < p.T * GB_COLS; i += THREADS) o[(i / GB_COLS) * p.ldo + i % GB_COLS] = 0;
         return;
     }
     float *state = p.state + ((static_cast<long long>(slot) * p.Hv + hv) * p.dv + col0) * DK;
@@ -533,21 +538,23 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
                        *v_new = p.rows.v + (nr0 - na) * p.rows.ldv + hv * p.dv + col0 + jv;
         const uint16_t *q_new = p.rows.q + nr0 * p.rows.ldq + hk * DK + jk;
 #pragma unroll
-        for (int t0 = 0; t0 < NP; t0 += GB_THREADS / PR)
+        for (int t0 = 0; t0 < NP; t0 += THREADS / PR)
             if (const int t = t0 + tid / PR; t < NP) piece(&sm.k[t][jk], t < na ? k_old + t * p.prev.ldk : k_new + t * p.rows.ldk, t < rows);
 #pragma unroll
-        for (int t0 = 0; t0 < NQR; t0 += GB_THREADS / PR)
+        for (int t0 = 0; t0 < NQR; t0 += THREADS / PR)
             if (const int t = t0 + tid / PR; t < NQR) piece(&sm.q[t][jk], q_new + t * p.rows.ldq, t < p.T);
 #pragma unroll
-        for (int t0 = 0; t0 < NP; t0 += GB_THREADS / PV)
+        for (int t0 = 0; t0 < NP; t0 += THREADS / PV)
             if (const int t = t0 + tid / PV; t < NP) piece(&sm.v[t][jv], t < na ? v_old + t * p.prev.ldv : v_new + t * p.rows.ldv, t < rows);
     }
     cp_async_commit();
     // ---- the warp's state rows
-    float *srows = state + 16 * warp * DK;
+    float *srows = state + 16 * wr * DK + wk * COLS;
 #pragma unroll 4
-    for (int i = lane; i < 16 * DK / 4; i += 32)
-        cp_async_16(smem_addr(&sm.s[16 * warp + i / (DK / 4)][(i % (DK / 4)) * 4]), srows + 4 * i);
+    for (int i = lane; i < 16 * COLS / 4; i += 32) {
+        const int r = i / (COLS / 4), j = i % (COLS / 4) * 4;
+        cp_async_16(smem_addr(&sm.s[16 * wr + r][wk * COLS + j]), srows + r * DK + j);
+    }
     cp_async_commit();
     if (gate_warp) {
         // the running sum of the log decays
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     }
     // ---- inverse norms, four lanes a row
 #pragma unroll 1
-    for (int t = tid >> 2; t < NP + NQR; t += GB_THREADS / 4) {
+    for (int t = tid >> 2; t < NP + NQR; t += THREADS / 4) {
         const uint16_t *row = t >= NP ? sm.q[t - NP] : sm.k[t];
         float ss[2] = {0.f, 0.f};
 #pragma unroll
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     }
     if constexpr (SMALL) {
 #pragma unroll
-        for (int i0 = 0; i0 < NP * NP; i0 += GB_THREADS) {
+        for (int i0 = 0; i0 < NP * NP; i0 += THREADS) {
             const int i = i0 + tid, t = i / NP, s = i % NP;
             if (i < NP * NP) sm.ed[t][s] = s <= t ? exp_diff(Sum2{sm.g_hi[t], sm.g_lo[t]}, sm.g_hi[s], sm.g_lo[s]) : 0.f;
         }
@@ -684,10 +691,10 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         for (int e = 0; e < 4; ++e) pq[j][e] = 0.f;
     cp_async_wait_all();
     __syncwarp();                               // the warp's state rows are in
-    float *srow = &sm.s[16 * warp + g][2 * c];
+    float *srow = &sm.s[16 * wr + g][wk * COLS + 2 * c];
     constexpr int SST = DK + 8;
 #pragma unroll 4
-    for (int s = 0; s < DK / 8; ++s) {
+    for (int s = 0; s < COLS / 8; ++s) {
         // columns 2 c and 2 c + 1 of the step are its k = c and c + 4
         const float2 x = *reinterpret_cast<const float2 *>(srow + 8 * s), y = *reinterpret_cast<const float2 *>(srow + 8 * SST + 8 * s);
         const float sv[4] = {x.x, y.x, x.y, y.y};
@@ -695,7 +702,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) gb_split_tf32(sv[i], hi[i], lo[i]);
         auto product = [&](float (&d)[4], float (&d_lo)[4], const uint16_t *row) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(row + 8 * s + 2 * c);
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(row + wk * COLS + 8 * s + 2 * c);
             const uint32_t b0 = w << 16, b1 = w & 0xFFFF0000u;
             mma_tf32_1688(d_lo, lo[0], lo[1], lo[2], lo[3], b0, b1);
             mma_tf32_1688(d, hi[0], hi[1], hi[2], hi[3], b0, b1);
@@ -715,6 +722,26 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
             pq[0][e] += lq[e];
         }
     }
+    const int nu = (kept + 7) >> 3;
+    if constexpr (KS > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j) sm.part[warp][4 * j + e][lane] = pk[j][e];
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) sm.part[warp][4 * (NK + j) + e][lane] = pq[j][e];
+        }
+    }
+    __syncthreads();                            // A and M are complete, and the parts
+    if constexpr (KS > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j) pk[j][e] = sm.part[wr][4 * j + e][lane] + sm.part[wr + 4][4 * j + e][lane];
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) pq[j][e] = sm.part[wr][4 * (NK + j) + e][lane] + sm.part[wr + 4][4 * (NK + j) + e][lane];
+        }
+    }
     // ---- r
 #pragma unroll
     for (int j = 0; j < NK; ++j)
@@ -722,10 +749,8 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 8 * j + 2 * c + (e & 1);
-                pk[j][e] = sm.beta[t] * (bf16_bits_to_float(sm.v[t][16 * warp + g + 8 * (e >> 1)]) - sm.f_p[t] * sm.rk[t] * pk[j][e]);
+                pk[j][e] = sm.beta[t] * (bf16_bits_to_float(sm.v[t][16 * wr + g + 8 * (e >> 1)]) - sm.f_p[t] * sm.rk[t] * pk[j][e]);
             }
-    const int nu = (kept + 7) >> 3;
-    __syncthreads();                            // A and M are complete
     if constexpr (SMALL) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
@@ -766,12 +791,12 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 8 * j + 2 * c + (e & 1);
-                if (t < p.T) o[t * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(pq[j][e]));
+                if (wk == 0 && t < p.T) o[t * p.ldo + 16 * wr + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(pq[j][e]));
             }
     } else {
         // u by forward substitution in the warp's own rows of shared memory, a
         // state row a lane, eight rows t at a time
-        float (*uw)[NP + GB_FPAD] = &sm.u[16 * warp];
+        float (*uw)[NP + GB_FPAD] = &sm.u[16 * wr];
 #pragma unroll
         for (int j = 0; j < NK; ++j)
             if (j < nk)
@@ -839,7 +864,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (t0 + (e & 1) < p.T)
-                        o[(t0 + (e & 1)) * p.ldo + 16 * warp + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[e]));
+                        o[(t0 + (e & 1)) * p.ldo + 16 * wr + g + 8 * (e >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(s[e]));
             }
     }
     // ---- the state after the wanted rows: S <- decay S + u' K, u' = u f_s r_k in two terms
@@ -859,7 +884,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         for (int j = 0; j < NK; ++j)
             if (j < nu) scaled_u(j, pk[j][0], pk[j][1], pk[j][2], pk[j][3], uh[SMALL ? j : 0], ul[SMALL ? j : 0]);
 #pragma unroll 1
-    for (int i = 0; i < DK / 32; ++i) {
+    for (int i = 0; i < COLS / 32; ++i) {
         float st[4][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -871,7 +896,7 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         }
         auto add = [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
             uint32_t bb[4];
-            gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + 32 * i + (lane >> 3) * 8);
+            gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + wk * COLS + 32 * i + (lane >> 3) * 8);
             // rows 8 j + 2 c and + 1, zero where not kept: their u is, but a key may hold a NaN
             const int t = 8 * j + 2 * c;
             const uint32_t rows_in = t + 1 < kept ? 0xFFFFFFFFu : t < kept ? 0xFFFFu : 0u;
@@ -889,8 +914,8 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
         } else {
 #pragma unroll 1
             for (int j = 0; j < nu; ++j) {
-                const float2 x = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * warp + g][8 * j + 2 * c]),
-                             y = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * warp + g + 8][8 * j + 2 * c]);
+                const float2 x = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * wr + g][8 * j + 2 * c]),
+                             y = *reinterpret_cast<const float2 *>(&sm.u[SMALL ? 0 : 16 * wr + g + 8][8 * j + 2 * c]);
                 scaled_u(j, x.x, x.y, y.x, y.y, uh[0], ul[0]);
                 add(j, uh[0], ul[0]);
             }
@@ -903,8 +928,10 @@ __global__ void __launch_bounds__(GB_THREADS, 4) gated_delta_block_kernel(const 
     }
     __syncwarp();
 #pragma unroll 4
-    for (int i = lane; i < 16 * DK / 4; i += 32)
-        *reinterpret_cast<float4 *>(srows + 4 * i) = *reinterpret_cast<const float4 *>(&sm.s[16 * warp + i / (DK / 4)][(i % (DK / 4)) * 4]);
+    for (int i = lane; i < 16 * COLS / 4; i += 32) {
+        const int r = i / (COLS / 4), j = i % (COLS / 4) * 4;
+        *reinterpret_cast<float4 *>(srows + r * DK + j) = *reinterpret_cast<const float4 *>(&sm.s[16 * wr + r][wk * COLS + j]);
+    }
 }
 
 }  // namespace sv

@@ -233,46 +233,64 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
 // Whether a step runs row by row (gated_delta_step_kernel) or takes its rows
 // all at once (gated_delta_block_kernel).  One or two rows whose state is a
 // wave of small blocks at most are quicker without the second kernel's tiles:
-// 48 heads of 128 x 128, one row, 1 / 4 sequences 4.5 / 7.1 us against 5.9 /
-// 9.2, two rows 5.0 / 8.1 against 5.8 / 9.4.  Beyond that its asynchronous
+// 48 heads of 128 x 128, one row, 1 / 4 sequences 3.9 / 6.2 us against 5.4 /
+// 9.0, two rows 4.4 / 7.1 against 5.5 / 9.2.  Beyond that its asynchronous
 // copies win: 16 / 64 / 256 sequences of two rows 19 / 66 / 244 us against
-// 21 / 100 / 389, and so do its tiles with more rows: 3 rows of 1 / 4
-// sequences 5.3 / 9.2 us, row by row 5.7 / 9.0.
+// 21 / 100 / 389, and so do its tiles with more rows: 4 and 4 rows of 1 / 4
+// sequences 5.8 / 9.6 us, row by row 7.0 / 11.7.
 bool delta_step_by_rows(int rows, long long state_rows, const DeviceInfo &dev)
 {
     return rows < 3 && state_rows <= 5LL * GB_COLS * dev.sms;
 }
 
-template <int DK, int NK, int NQ>
-constexpr size_t delta_block_smem()
+// Whether a block of up to 16 rows has two warps for 16 state rows.  With two
+// or three blocks a multiprocessor the chain of a block counts, which that
+// shortens: 2 / 4 sequences of 48 heads of 128 x 128, 8 and 8 rows 8.0 / 9.7 us
+// against 9.2 / 10.5, 4 and 4 rows 7.0 / 7.5 against 6.2 / 9.7, 3 rows 6.7 / 7.1
+// against 8.2 / 9.4.  A single block (one sequence: 5.7 against 5.4 us) and more
+// of them (6 sequences 13.1 against 10.6, 16 29 against 25) do better without.
+bool delta_step_split(long long state_rows, const DeviceInfo &dev)
 {
-    return sizeof(GbSmem<DK, 8 * NK, 8 * NQ>);
+    const long long blocks = state_rows / GB_COLS;
+    return blocks > dev.sms && blocks <= 3LL * dev.sms;
 }
 
-template <int DK, int NK, int NQ>
+template <int DK, int NK, int NQ, int KS>
+constexpr size_t delta_block_smem()
+{
+    return sizeof(GbSmem<DK, 8 * NK, 8 * NQ, KS>);
+}
+
+template <int DK, int NK, int NQ, int KS>
 int delta_block_launch(const DeltaParams &p, int B, cudaStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>(p.dv / GB_COLS), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
-    return launch(gated_delta_block_kernel<DK, NK, NQ>, grid, GB_THREADS, delta_block_smem<DK, NK, NQ>(), stream, p);
+    return launch(gated_delta_block_kernel<DK, NK, NQ, KS>, grid, gb_threads(KS), delta_block_smem<DK, NK, NQ, KS>(), stream, p);
 }
 
+// `split`: two warps for 16 state rows, half the columns each (up to 16 rows).
 template <int DK>
-int delta_block_dispatch(const DeltaParams &p, int B, cudaStream_t stream)
+int delta_block_dispatch(const DeltaParams &p, int B, bool split, cudaStream_t stream)
 {
     const int nk = (p.prev_T + p.T + 7) / 8;
-    if (nk <= 1) return delta_block_launch<DK, 1, 1>(p, B, stream);
-    if (nk <= 2 && p.T <= 8) return delta_block_launch<DK, 2, 1>(p, B, stream);
-    if (nk <= 4 && p.T <= 16) return delta_block_launch<DK, 4, 2>(p, B, stream);
-    return delta_block_launch<DK, 8, 4>(p, B, stream);
+    if (nk <= 1) return split ? delta_block_launch<DK, 1, 1, 2>(p, B, stream) : delta_block_launch<DK, 1, 1, 1>(p, B, stream);
+    if (nk <= 2 && p.T <= 8)
+        return split ? delta_block_launch<DK, 2, 1, 2>(p, B, stream) : delta_block_launch<DK, 2, 1, 1>(p, B, stream);
+    if (nk <= 4 && p.T <= 16) return delta_block_launch<DK, 4, 2, 1>(p, B, stream);
+    return delta_block_launch<DK, 8, 4, 1>(p, B, stream);
 }
 
 template <int DK>
 cudaError_t delta_block_raise()
 {
-    cudaError_t e = raise(gated_delta_block_kernel<DK, 1, 1>, delta_block_smem<DK, 1, 1>());
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 2, 1>, delta_block_smem<DK, 2, 1>());
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 4, 2>, delta_block_smem<DK, 4, 2>());
-    if (e == cudaSuccess) e = raise(gated_delta_block_kernel<DK, 8, 4>, delta_block_smem<DK, 8, 4>());
+    cudaError_t e = cudaSuccess;
+    auto up = [&](cudaError_t r) { e = e != cudaSuccess ? e : r; };
+    up(raise(gated_delta_block_kernel<DK, 1, 1, 1>, delta_block_smem<DK, 1, 1, 1>()));
+    up(raise(gated_delta_block_kernel<DK, 1, 1, 2>, delta_block_smem<DK, 1, 1, 2>()));
+    up(raise(gated_delta_block_kernel<DK, 2, 1, 1>, delta_block_smem<DK, 2, 1, 1>()));
+    up(raise(gated_delta_block_kernel<DK, 2, 1, 2>, delta_block_smem<DK, 2, 1, 2>()));
+    up(raise(gated_delta_block_kernel<DK, 4, 2, 1>, delta_block_smem<DK, 4, 2, 1>()));
+    up(raise(gated_delta_block_kernel<DK, 8, 4, 1>, delta_block_smem<DK, 8, 4, 1>()));
     return e;
 }
 
@@ -442,8 +460,9 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
     if (prev_T > 0) p.prev = delta_rows(prev);
     p.accept_len = accept_len;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const bool split = delta_step_split(static_cast<long long>(B) * p.Hv * p.dv, dev);
     if (!delta_step_by_rows(T + prev_T, static_cast<long long>(B) * p.Hv * p.dv, dev))
-        return shape->dk == 64 ? delta_block_dispatch<64>(p, B, cs) : delta_block_dispatch<128>(p, B, cs);
+        return shape->dk == 64 ? delta_block_dispatch<64>(p, B, split, cs) : delta_block_dispatch<128>(p, B, split, cs);
     const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
     const int cap = T > prev_T ? T : prev_T;
     const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));

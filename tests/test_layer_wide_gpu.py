@@ -1,6 +1,7 @@
 """The gated feed-forward at widths that take the tcgen05 kernel -- tiles that
 do not divide the result, an odd number of 128-column groups, two rounds of
-tiles -- and rows with a NaN among a step's rows."""
+tiles -- steps of as many heads as give a multiprocessor two or three blocks,
+and rows with a NaN among a step's rows."""
 import numpy as np
 import pytest
 
@@ -84,13 +85,14 @@ def test_gate_up_wide_nan_stays_in_its_row(sv, layers, T):
     assert not bool(torch.isfinite(h[2]).any())
 
 
+@pytest.mark.parametrize("Hk,Hv", [(2, 4), (16, 96)])
 @pytest.mark.parametrize("T,P,bad", [(2, 0, 1), (4, 0, 2), (8, 8, 3), (12, 0, 11), (9, 9, 1), (20, 4, 13), (32, 32, 30)])
-def test_step_nan_stays_with_later_rows(sv, T, P, bad):
+def test_step_nan_stays_with_later_rows(sv, T, P, bad, Hk, Hv):
     """A draft with a NaN in its key, query, value or gates changes no earlier row's output, no other sequence, and
     not the state, which holds the rows before the drafts."""
     g = torch.Generator(device="cuda")
     g.manual_seed(T)
-    B, Hk, Hv, d = 2, 2, 4, 128
+    B, d = 2, 128
 
     def rows(n):
         r = lambda *a: torch.randn(B, n, *a, device="cuda", generator=g)                   # noqa: E731
@@ -117,3 +119,52 @@ def test_step_nan_stays_with_later_rows(sv, T, P, bad):
         got_s = start.clone()
         got = sv.gated_delta_step(*new, got_s, prev=tuple(hurt), accept_len=acc, commit=False, l2norm=True)
         assert torch.equal(got, want) and torch.equal(got_s, want_s)
+
+
+def rule64(S, q, k, v, gate, beta, scale):
+    """The recurrence on rows [B][n][heads][d] with S [B][Hv][dv][dk], keys and queries normalised; (o, S)."""
+    rep, out = v.shape[2] // k.shape[2], []
+    for t in range(k.shape[1]):
+        kt, qt = (a[:, t].double() for a in (k, q))
+        kt, qt = ((a / torch.sqrt((a * a).sum(-1, keepdim=True) + 1e-6)).repeat_interleave(rep, 1) for a in (kt, qt))
+        S = S * torch.exp(gate[:, t].double())[..., None, None]
+        u = beta[:, t].double()[..., None] * (v[:, t].double() - torch.einsum("bhvk,bhk->bhv", S, kt))
+        S = S + u[..., None] * kt[:, :, None, :]
+        out.append(scale * torch.einsum("bhvk,bhk->bhv", S, qt))
+    return torch.stack(out, 1) if out else None, S
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv,B", [(16, 48, 128, 128, 4), (32, 96, 64, 64, 3), (16, 48, 128, 64, 5),
+                                           (8, 40, 64, 128, 4)])
+@pytest.mark.parametrize("T,P", [(3, 0), (5, 0), (4, 4), (8, 8), (8, 5), (1, 7), (0, 6)])
+@pytest.mark.parametrize("commit", [False, True])
+def test_step_of_many_heads(sv, Hk, Hv, dk, dv, B, T, P, commit):
+    """The state to 2e-6 of a head's norm (22-bit factors; fp32 sums of at most 17 terms), outputs to bf16's
+    rounding and 1e-5 of the head's rms."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(Hk + Hv + dk + dv + 31 * T + P)
+
+    def rows(n):
+        r = lambda *a: torch.randn(B, n, *a, device="cuda", generator=g)                   # noqa: E731
+        return [r(Hk, dk).bfloat16(), r(Hk, dk).bfloat16(), r(Hv, dv).bfloat16(), -r(Hv).abs(), torch.sigmoid(r(Hv))]
+
+    new, old = rows(T), rows(P)
+    state = torch.randn(B, Hv, dv, dk, device="cuda", generator=g)
+    acc = torch.tensor([(3 * b + 1) % (P + 2) - 1 for b in range(B)], dtype=torch.int32, device="cuda") if P else None
+    got = state.clone()
+    o = sv.gated_delta_step(*new, got, prev=tuple(old[1:]) if P else None, accept_len=acc, commit=commit, l2norm=True)
+    scale = dk ** -0.5
+    for b in range(B):
+        S = state[b:b + 1].double()
+        n = min(max(int(acc[b]) + 1, 0), P) if P else 0
+        if n:
+            _, S = rule64(S, *(t[b:b + 1, :n] for t in old), scale)
+        ref, after = rule64(S, *(t[b:b + 1] for t in new), scale)
+        want = (after if commit else S)[0].flatten(1)
+        err = (got[b].double().flatten(1) - want).norm(dim=1)
+        assert bool((err <= 2e-6 * want.norm(dim=1)).all()), float((err / want.norm(dim=1)).max())
+        if T:
+            rms = (ref ** 2).mean((1, 3), keepdim=True).sqrt()
+            bad = (o[b:b + 1].double() - ref).abs() - (U * ref.abs() + 1e-5 * rms)
+            assert bool((bad <= 0).all()), float(bad.max())
+    assert sv.last_device_error() == 0
