@@ -23,9 +23,8 @@
 // within 5e-6 of the rule in exact arithmetic (row by row in fp32: 2e-7), well
 // below the 2^-9 of the bf16 rows that it is made from and of the outputs.
 //
-// Measured, 16 key and 48 value heads of 128: 4 prompts of 8,192 rows 764 us
-// (prep 275, scan 476), one of 3,847 rows 222 (42, 180), nine ragged ones with
-// 6,317 rows 191.  Prep is bound by its instructions (4,700 a warp, 43 % issue),
+// Measured, 16 key and 48 value heads of 128: 4 prompts of 8,192 rows 745 us
+// (prep 275), one of 3,847 rows 214 (42), nine ragged ones with 6,317 rows 190.  Prep is bound by its instructions (4,700 a warp, 43 % issue),
 // the scan by the chain of a block.
 #pragma once
 
@@ -503,12 +502,14 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
 // 16 issues the products, warp 17 the loads, two blocks ahead.
 //
 // The chain of a block, P, r, U, u', D, S, bounds the kernel; O, M and the
-// outputs fill its gaps.  Measured: 5,700 cycles a block of 128 x 128 states;
-// by clock stamps P 1,100 with its hand-offs, r 550, U 650, u' 700, D 900, S
-// 950, the rest outputs and values.  A 128 x 64 x 16 product with its A operand
-// in tensor memory takes up to 56 cycles, one of width 128 takes 88, so O is
-// issued in two halves, into the gaps after P and after U, where it delays
-// neither.
+// outputs fill its gaps.  D goes by halves of the state's columns: the first
+// half's new state is converted, and P's steps over it begun, while the second
+// half's D and conversion run (4 prompts of 8,192 rows 764 -> 745 us).  A block
+// of 128 x 128 states then takes 5,400 cycles; by clock stamps before that, of
+// 5,700, P 1,100 with its hand-offs, r 550, U 650, u' 700, D 900, S 950, the
+// rest outputs and values.  A 128 x 64 x 16 product with its A operand in
+// tensor memory takes up to 56 cycles, so O is issued in two halves, into the
+// gaps after P and after U, where it delays neither.
 
 // Work.  The chains of all heads and sequences are laid end to end, each as
 // long as its blocks and DS_EXTRA more for its start and end (loading and
@@ -539,7 +540,7 @@ struct DsSmem {                                 // from a 1024-byte boundary
 
 // Barriers that a waiter could find two phases ahead come in pairs, one for
 // even and one for odd steps: their next phase needs the waiter to go on.
-enum { B_FULL0, B_FULL1, B_P, B_U, B_D, B_M0, B_M1, B_SREADY, B_RREADY, B_UREADY, B_MREADY, B_YFREE, B_COUNT };
+enum { B_FULL0, B_FULL1, B_P, B_U, B_D0, B_D1, B_M0, B_M1, B_SREADY0, B_SREADY1, B_RREADY, B_UREADY, B_MREADY, B_YFREE, B_COUNT };
 
 // A CTA's part of the chains: segments of one head of one sequence each.
 struct DsWalk {
@@ -635,6 +636,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
 {
     extern __shared__ __align__(1024) uint8_t ds_smem[];
     using L = DsSmem<DK>;
+    constexpr int HALVES = DK / 64;             // D, and P's steps, go by 64 state columns
     const DeltaParams &p = cp.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = gridDim.x - 1 - blockIdx.x;
@@ -650,7 +652,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_SREADY ? DS_WARPS : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i < B_SREADY0 ? 1 : i < B_RREADY ? DS_WARPS / HALVES : DS_WARPS);
         *flag = 0;
         fence_barrier_init();
     }
@@ -717,11 +719,14 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 };
                 // P: S x K
                 wait(bar(B_FULL0 + (t & 1)), t >> 1);
-                wait(bar(B_SREADY), t);
-                __syncwarp();
-                tc_fence_after_sync();
 #pragma unroll
-                for (int s = 0; s < DK / 16; ++s) s_product(tmem + DS_P, kb, s);
+                for (int half = 0; half < HALVES; ++half) {
+                    wait(bar(B_SREADY0 + half), t);
+                    __syncwarp();
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int s = 4 * half; s < 4 * half + 4; ++s) s_product(tmem + DS_P, kb, s);
+                }
                 tc_commit_warp(bar(B_P));
                 // O: S x Q, first half
                 if (t > 0) wait(bar(B_YFREE), t - 1);
@@ -753,12 +758,16 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 __syncwarp();
                 tc_fence_after_sync();
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint64_t d = desc_mn_sw128(kb + s * 2048);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 8 * s, d, tc_idesc_bf16(DK, true), s > 0);
-                    tc_mma_f16_ts_warp(tmem + DS_P, tmem + DS_UP + 32 + 8 * s, d, tc_idesc_bf16(DK, true), 1);
+                for (int half = 0; half < HALVES; ++half) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint64_t k = desc_mn_sw128(kb + half * DC_ROWS * 128 + s * 2048);
+                        const uint32_t d = tmem + DS_P + 64 * half;
+                        tc_mma_f16_ts_warp(d, tmem + DS_UP + 8 * s, k, tc_idesc_bf16(64, true), s > 0);
+                        tc_mma_f16_ts_warp(d, tmem + DS_UP + 32 + 8 * s, k, tc_idesc_bf16(64, true), 1);
+                    }
+                    tc_commit_warp(bar(B_D0 + half));
                 }
-                tc_commit_warp(bar(B_D));
                 // M: u x M
                 wait(bar(B_MREADY), t);
                 __syncwarp();
@@ -780,6 +789,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
         const bool live = l < p.dv;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
         constexpr int SC = DK / 4;              // state columns of a thread
+        const int half = h * SC / 64;           // of the state's columns
         constexpr int NTHR = DS_WARPS * 32;
         f32x2 s[SC / 2];
         auto arrive = [&](int i) {              // this warp's tensor memory accesses are done
@@ -881,7 +891,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                     // (the last state's terms have been read: O is issued before D, which has been waited for)
                     tmem_st<SC / 2>(lanes + DS_SHI + h * (SC / 2), hi);
                     tmem_st<SC / 2>(lanes + DS_SLO + h * (SC / 2), lo);
-                    arrive(B_SREADY);
+                    arrive(B_SREADY0 + half);
                 }
                 if (c > w.c0) take_out(t - 1);
                 const float *f = reinterpret_cast<const float *>(ds_smem + L::F + (t & 3) * DC_FACTORS);
@@ -950,7 +960,7 @@ delta_scan_kernel(const __grid_constant__ DeltaChunkParams cp, const __grid_cons
                 }
                 {   // S <- e^(G_n) S + D
                     const f32x2 decay = pack_x2(f[3 * DC_ROWS], f[3 * DC_ROWS]);
-                    wait(bar(B_D), t);
+                    wait(bar(B_D0 + half), t);
                     tc_fence_after_sync();
 #pragma unroll
                     for (int j = 0; j < SC; j += 16) {
