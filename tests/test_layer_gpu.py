@@ -688,3 +688,27 @@ def test_chunk_of_few_rows(sv, lens, zero):
     untouched = [s for s in range(B + 2) if s not in idx.tolist()]
     assert torch.equal(got[untouched], state[untouched])
     assert sv.last_device_error() == 0
+
+
+@pytest.mark.parametrize("T,D,pad,off", [(300, 5119, 0, 0), (64, 1003, 0, 0), (40, 2049, 0, 3), (33, 9001, 6, 1), (700, 67, 0, 5),
+                                         (9, 65519, 0, 0), (5, 40001, 2, 7)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_unaligned_rows(sv, T, D, pad, off, residual):
+    """Rows at every 2-byte offset, the same in all tensors; in place; nothing written between or past them."""
+    g = rng_of(T + D + off)
+    x, r = strided(randn(g, T, D).bfloat16(), pad, off), strided((2 * randn(g, T, D)).bfloat16(), pad, off)
+    w = randn(g, D + 1).bfloat16()[1:]
+    y = strided(torch.zeros(T, D, device="cuda").bfloat16(), pad, off)
+    want = (x.float() + r.float()).bfloat16() if residual else x.clone()
+    sv.rmsnorm(x, w, r if residual else None, y=y, residual_out=r if residual else None)
+    if residual:
+        assert torch.equal(r, want)
+    check_bf16(y, norm64(want, w, 1e-6, 0))
+    for t in (y, r):
+        full = t._base if t._base is not None else t
+        keep = torch.ones_like(full.flatten(), dtype=torch.bool)
+        for i in range(T):
+            a = off + i * (D + pad)
+            keep[a:a + D] = False
+        assert bool((full.flatten()[keep] == 0).all())
+    assert sv.last_device_error() == 0
