@@ -155,22 +155,23 @@ int norm_call(NormParams p, int T, cudaStream_t stream)
                       aligned_to(p.weight, 16) && aligned_to(FP8 ? static_cast<const void *>(p.y8) : p.y, FP8 ? 8 : 16) &&
                       (!p.residual || (p.ldr % 8 == 0 && p.ldro % 8 == 0 && aligned_to(p.residual, 16) &&
                                        aligned_to(p.residual_out, 16)));
-    // bf16 rows that are not 16-byte aligned, but all off by as much (odd
-    // lengths): 16-byte pieces all the same.  16,384 rows of 1,001 / 5,119
-    // columns 28 / 166 us (one column a thread 87 / 666), one of 5,119 2.1
-    // (4.6); a few short rows are quicker by columns (one of 1,001 1.4, by
-    // pieces 1.7)
-    auto off = [](const void *a, long long ld) { return ((reinterpret_cast<uintptr_t>(a) >> 1) & 7) * 8 + (ld & 7); };
-    const bool odd = !FP8 && !wide && p.D >= 64 && 1LL * T * p.D >= 2048 && p.D <= 8 * 8 * RN_MAX_THREADS - 16 && off(p.x, p.ldx) == off(p.y, p.ldy) &&
-                     (!p.residual || (off(p.residual, p.ldr) == off(p.x, p.ldx) && off(p.residual_out, p.ldro) == off(p.x, p.ldx)));
+    // rows that are not 16-byte aligned, but all off by as much (odd lengths):
+    // 16-byte pieces all the same.  16,384 rows of 1,001 / 5,119 columns 28 /
+    // 167 us (one column a thread 87 / 666), of 5,119 to 8 bits 454 (909), one
+    // row of 5,119 2.0 (4.6); a few short rows are quicker by columns (one of
+    // 1,001 1.4, by pieces 1.7)
+    auto off = [](const void *a, long long ld, int log) { return ((reinterpret_cast<uintptr_t>(a) >> log) & 7) * 8 + (ld & 7); };
+    const unsigned long long at = off(p.x, p.ldx, 1);
+    const bool odd = !wide && p.D >= 64 && 1LL * T * p.D >= 2048 && p.D <= RN_ODD_MAX_D &&
+                     (FP8 ? off(p.y8, p.ldy, 0) : off(p.y, p.ldy, 1)) == at &&
+                     (!p.residual || (off(p.residual, p.ldr, 1) == at && off(p.residual_out, p.ldro, 1) == at));
     const int n = wide ? p.D / 8 : odd ? p.D / 8 + 2 : p.D;     // most pieces of a row
     int vpt = 1;
     while (n > vpt * RN_MAX_THREADS) vpt *= 2;
     if (!wide && vpt == 32) vpt = 64;
     const int per = 128;                         // the scalar 8-bit path groups four warps
     const int threads = ((n + vpt - 1) / vpt + per - 1) / per * per;
-    if constexpr (!FP8)
-        if (odd) return norm_launch<8, false, true>(p, T, vpt, threads, stream);
+    if (odd) return norm_launch<8, FP8, true>(p, T, vpt, threads, stream);
     return wide ? norm_launch<8, FP8>(p, T, vpt, threads, stream) : norm_launch<1, FP8>(p, T, vpt, threads, stream);
 }
 

@@ -12,8 +12,8 @@
 // and the output, so that every byte crosses memory once: the kernel is
 // bound by HBM for long inputs and by its launch and one memory round trip
 // for a few rows.  VEC columns per access: 8 (16 bytes) where the row length,
-// the strides and the addresses allow it, or, for a bf16 output, are off by as
-// much in every tensor; else 1.  Sums, the norm and the scales are fp32; the
+// the strides and the addresses allow it, or are off by as much in every
+// tensor; else 1.  Sums, the norm and the scales are fp32; the
 // only roundings to fewer bits are s (the value that the next layer adds to,
 // as the residual stream is kept in bf16) and the output's.
 //
@@ -31,6 +31,7 @@ namespace sv {
 
 constexpr int RN_GROUP = 128;                   // columns of an 8-bit output's scale
 constexpr int RN_MAX_THREADS = 1024;
+constexpr int RN_ODD_MAX_D = 8 * 8 * RN_MAX_THREADS - 16;  // columns of a row that is not 16-byte aligned
 constexpr float RN_FP8_MAX = 448.f;
 constexpr float RN_MIN_SCALE = 1.17549435e-38f; // 2^-126: an all-zero group's scale, and the smallest
 
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
             q.load(p.weight + i * VEC);
     };
     __shared__ float part[32];
+    __shared__ unsigned group_max[FP8 && ODD ? RN_ODD_MAX_D / RN_GROUP + 1 : 1];    // bits of each group's largest |s w|
     pdl_launch_dependents();
     // The weight is model data: a short row's is read before the previous
     // kernel's end, a longer one's (more registers) when it is used.
@@ -205,6 +207,8 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) part[warp] = sum;
+    if constexpr (FP8 && ODD)
+        for (int i = tid; i <= p.D / RN_GROUP; i += nthr) group_max[i] = 0u;
     __syncthreads();
     sum = lane < nwarp ? part[lane] : 0.f;
 #pragma unroll
@@ -258,6 +262,27 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
             rowmax = lanes_max(lane < nwarp ? part[lane] : 0.f, 32);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) m[j] = rowmax;
+        } else if (ODD) {                       // pieces straddle groups
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = tid + j * nthr, c = i * VEC - before;
+                if (i >= n) continue;
+                const RnPiece<VEC> wj = weight(j, i);
+                const int g0 = max(c, 0) / RN_GROUP, end = (g0 + 1) * RN_GROUP;
+                float a = 0.f, b = 0.f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float z = fabsf(s[j].get(e) * (wj.get(e) + p.w_add));
+                    if (c + e < end)
+                        a = max_nan(a, z);
+                    else
+                        b = max_nan(b, z);
+                }
+                // (non-negative floats compare as their bits, a NaN above all)
+                atomicMax(&group_max[g0], __float_as_uint(a));
+                if (c + VEC > end && end < p.D) atomicMax(&group_max[g0 + 1], __float_as_uint(b));
+            }
+            __syncthreads();
         } else if (VEC == 8) {                  // a group is a half warp's pieces
 #pragma unroll
             for (int j = 0; j < VPT; ++j) m[j] = lanes_max(m[j], RN_GROUP / 8);
@@ -275,16 +300,28 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = tid + j * nthr;
-            const float scale = max_nan(m[j] * inv / RN_FP8_MAX, RN_MIN_SCALE);
+            auto scale_of = [&](float most) { return max_nan(most * inv / RN_FP8_MAX, RN_MIN_SCALE); };
             if (i < n) {
-                const int col = i * VEC;
+                const int col = i * VEC - before;
                 const RnPiece<VEC> wj = weight(j, i);
+                // ODD: the group of the piece's first columns and the next one
+                const int g0 = max(col, 0) / RN_GROUP, end = (g0 + 1) * RN_GROUP;
+                const bool grouped = ODD && !p.row_scale, two = grouped && col + VEC > end && end < p.D;
+                const float m0 = grouped ? __uint_as_float(group_max[ODD ? g0 : 0]) : m[j], scale0 = scale_of(m0);
+                const float m1 = two ? __uint_as_float(group_max[ODD ? g0 + 1 : 0]) : m0, scale1 = two ? scale_of(m1) : scale0;
                 // at the smallest scale (and for NaNs) the quotient itself
                 auto quant = [&](int e) {
                     const float z = s[j].get(e) * (wj.get(e) + p.w_add);
-                    return rn_e4m3(scale > RN_MIN_SCALE ? z * RN_FP8_MAX / m[j] : z * inv / scale);
+                    const bool second = two && col + e >= end;
+                    const float scale = second ? scale1 : scale0, most = second ? m1 : m0;
+                    return rn_e4m3(scale > RN_MIN_SCALE ? z * RN_FP8_MAX / most : z * inv / scale);
                 };
-                if (p.row_scale ? col == 0 : col % RN_GROUP == 0) sc[p.row_scale ? 0 : col / RN_GROUP] = scale;
+                if (p.row_scale) {
+                    if (col <= 0) sc[0] = scale0;
+                } else {
+                    if (col <= g0 * RN_GROUP) sc[g0] = scale0;
+                    if (two) sc[g0 + 1] = scale1;
+                }
                 if constexpr (VEC == 8) {
                     uint32_t lo = 0u, hi = 0u;
 #pragma unroll
@@ -292,7 +329,13 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
                         lo |= quant(e) << (8 * e);
                         hi |= quant(e + 4) << (8 * e);
                     }
-                    *reinterpret_cast<uint2 *>(y + col) = make_uint2(lo, hi);
+                    if (ODD && (col < 0 || col + VEC > p.D)) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e >= 0 && col + e < p.D) y[col + e] = static_cast<uint8_t>((e < 4 ? lo : hi) >> (8 * (e & 3)));
+                    } else {
+                        *reinterpret_cast<uint2 *>(y + col) = make_uint2(lo, hi);
+                    }
                 } else {
                     y[col] = static_cast<uint8_t>(quant(0));
                 }

@@ -712,3 +712,31 @@ def test_rmsnorm_unaligned_rows(sv, T, D, pad, off, residual):
             keep[a:a + D] = False
         assert bool((full.flatten()[keep] == 0).all())
     assert sv.last_device_error() == 0
+
+
+@pytest.mark.parametrize("group", [128, 0])
+@pytest.mark.parametrize("T,D,pad,off", [(40, 5119, 0, 0), (300, 1003, 0, 0), (64, 9001, 6, 3), (33, 129, 0, 0), (50, 127, 2, 1),
+                                         (7, 65519, 0, 0)])
+def test_rmsnorm_fp8_unaligned_rows(sv, T, D, pad, off, group):
+    """8-bit rows at every offset: groups of 128 columns that straddle the 16-byte pieces."""
+    g = rng_of(D + group + T)
+    x, r = strided(randn(g, T, D).bfloat16(), pad, off), strided(randn(g, T, D).bfloat16(), pad, off)
+    w = randn(g, D).bfloat16()
+    y8 = strided(torch.zeros(T, D, device="cuda").to(torch.float8_e4m3fn), pad, off)
+    y, sc, s = sv.rmsnorm_fp8(x, w, r, group=group, unit_offset=True, y=y8, residual_out=r)
+    ref = norm64(s, w, 1e-6, 1)
+    n = group or D
+    cols = torch.arange(D, device="cuda") // n
+    most = torch.stack([ref[:, cols == i].abs().amax(1) for i in range(sc.shape[1])], 1)
+    want = most.clamp_min(448 * 2.0 ** -126) / 448      # (a group of one column may hold a zero alone)
+    assert bool(((sc.double() - want).abs() <= 1e-5 * want).all())
+    per = sc.double()[:, cols]
+    err = (y.float().double() * per - ref).abs()
+    assert bool((err <= (2.0 ** -4) * (1 + 1e-4) * ref.abs() + (2.0 ** -10) * (1 + 1e-4) * per).all())
+    full = y8._base if y8._base is not None else y8
+    keep = torch.ones(full.numel(), dtype=torch.bool, device="cuda")
+    for i in range(T):
+        a = off + i * (D + pad)
+        keep[a:a + D] = False
+    assert bool((full.flatten().view(torch.uint8)[keep] == 0).all())
+    assert sv.last_device_error() == 0
