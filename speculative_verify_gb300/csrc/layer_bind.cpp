@@ -329,13 +329,15 @@ PyObject *gated_delta_step(PyObject *, PyObject *const *a, Py_ssize_t n)
         const sv_delta_rows rows = delta_rows(a[0], a[1], a[2], a[3], a[4], 2, B, T, Hk, s);
         sv_delta_rows prev{};
         int64_t P = 0;
+        // the sequence that prev gave, held until the launch: an iterator's
+        // tensors may have no other owner, and `o` is allocated before it
+        struct Held {
+            PyObject *p = nullptr;
+            ~Held() { Py_XDECREF(p); }
+        } held;
         if (a[7] != Py_None) {
-            PyObject *f = PySequence_Fast(a[7], "prev must be (k, v, g, beta)");
+            PyObject *f = held.p = PySequence_Fast(a[7], "prev must be (k, v, g, beta)");
             if (!f) throw PyFail{};
-            struct Drop {
-                PyObject *p;
-                ~Drop() { Py_DECREF(p); }
-            } drop{f};
             if (PySequence_Fast_GET_SIZE(f) != 4) fail(PyExc_ValueError, "prev must be (k, v, g, beta)");
             PyObject **i = PySequence_Fast_ITEMS(f);
             const at::Tensor &pk = tensor(i[0], "k of prev", BF16);

@@ -1,0 +1,54 @@
+"""How the layer operators are called: who owns the tensors of a call, and what
+its operands may be.  The definitions' checks are in test_layer_gpu.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_verify_gb300 as m
+    from speculative_verify_gb300 import build
+    build.build()
+    m.load()
+    assert m.last_device_error() == 0
+    return m
+
+
+def rng_of(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *s):
+    return torch.randn(*s, device="cuda", generator=g)
+
+
+def delta_rows(g, lead, Hk, Hv, dk, dv):
+    q, k = randn(g, *lead, Hk, dk).bfloat16(), randn(g, *lead, Hk, dk).bfloat16()
+    v = randn(g, *lead, Hv, dv).bfloat16()
+    return q, k, v, -torch.rand(*lead, Hv, device="cuda", generator=g), torch.sigmoid(randn(g, *lead, Hv))
+
+
+def test_prev_from_an_iterator(sv):
+    """prev may be any iterable; tensors that only it owns are held until the launch (an output of the size of
+    prev's values would otherwise be given their memory)."""
+    g = rng_of(3)
+    B, T, Hk, Hv, d = 8, 8, 16, 48, 128
+    rows, prev = delta_rows(g, (B, T), Hk, Hv, d, d), delta_rows(g, (B, T), Hk, Hv, d, d)[1:]
+    state = randn(g, B, Hv, d, d)
+    want = state.clone()
+    o = sv.gated_delta_step(*rows, want, prev=prev, commit=False, l2norm=True)
+    for it in (lambda: (t.clone() for t in prev), lambda: map(torch.Tensor.clone, prev), lambda: list(prev)):
+        got = state.clone()
+        torch.cuda.synchronize()
+        o2 = sv.gated_delta_step(*rows, got, prev=it(), commit=False, l2norm=True)
+        assert torch.equal(o, o2) and torch.equal(want, got)
+    with pytest.raises(TypeError):
+        sv.gated_delta_step(*rows, got, prev=3, commit=False)
+    with pytest.raises(ValueError):
+        sv.gated_delta_step(*rows, got, prev=(t for t in prev[:3]), commit=False)
