@@ -111,13 +111,32 @@ const int32_t *indices(PyObject *o, const char *name, int64_t n = -1)
     return ptr<const int32_t>(t);
 }
 
+// A device made the current one, and the one before it again at the end.
+struct Device {
+    c10::DeviceIndex before = -1;               // -1: it was the current one already
+
+    explicit Device(c10::DeviceIndex d)
+    {
+        if (d == c10::cuda::current_device()) return;
+        before = c10::cuda::ExchangeDevice(d);
+    }
+    Device(const Device &) = delete;
+    ~Device()
+    {
+        if (before >= 0) C10_CUDA_CHECK_WARN(c10::cuda::SetDevice(before));
+    }
+};
+
 // The stream of a call: the given stream object's, or the current one of the
-// tensor's device.  Outputs allocated meanwhile belong to that stream.
+// tensor's device.  That device is the current one meanwhile (the library, and
+// a launch on the default stream, go by it), and outputs allocated meanwhile
+// belong to that stream.
 struct Stream {
     sv_stream raw;
+    Device device;
     c10::cuda::OptionalCUDAStreamGuard guard;
 
-    Stream(PyObject *o, const at::Tensor &t)
+    Stream(PyObject *o, const at::Tensor &t) : device(t.get_device())
     {
         if (o == Py_None) {
             raw = reinterpret_cast<sv_stream>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
