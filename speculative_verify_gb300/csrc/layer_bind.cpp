@@ -6,8 +6,8 @@
 // a call costs little more than its launch and its outputs' allocations.
 // Python (layer.py) holds the signatures and their documentation.
 //
-// Wrong types raise TypeError, wrong shapes and strides ValueError, and a
-// status of the library the package's SpecVerifyError.
+// Wrong types raise TypeError, wrong shapes, strides and devices ValueError,
+// and a status of the library the package's SpecVerifyError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -54,13 +54,27 @@ void check_status(const char *fn, int rc)
 constexpr auto BF16 = at::kBFloat16;
 constexpr auto F32 = at::kFloat;
 
+// The device of a call's tensors: the first one's.
+struct Where {
+    int device = -1;
+
+    const at::Tensor &operator()(const at::Tensor &t, const char *name)
+    {
+        if (device < 0) device = t.get_device();
+        if (t.get_device() != device)
+            fail(PyExc_ValueError, "%s is on device %d, the call's first tensor on device %d", name,
+                 static_cast<int>(t.get_device()), device);
+        return t;
+    }
+};
+
 // A CUDA tensor of that type.
-const at::Tensor &tensor(PyObject *o, const char *name, at::ScalarType type)
+const at::Tensor &tensor(PyObject *o, const char *name, at::ScalarType type, Where &on)
 {
     if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a tensor", name);
     const at::Tensor &t = THPVariable_Unpack(o);
     if (t.scalar_type() != type || !t.is_cuda()) fail(PyExc_TypeError, "%s must be a %s CUDA tensor", name, c10::toString(type));
-    return t;
+    return on(t, name);
 }
 
 bool same(at::IntArrayRef a, std::initializer_list<int64_t> b)
@@ -103,9 +117,9 @@ T *ptr(const at::Tensor &t)
     return static_cast<T *>(t.data_ptr());
 }
 
-const int32_t *indices(PyObject *o, const char *name, int64_t n = -1)
+const int32_t *indices(PyObject *o, const char *name, Where &on, int64_t n = -1)
 {
-    const at::Tensor &t = tensor(o, name, at::kInt);
+    const at::Tensor &t = tensor(o, name, at::kInt, on);
     if (!t.is_contiguous()) fail(PyExc_TypeError, "%s must be contiguous", name);
     if (n >= 0 && t.numel() != n) fail(PyExc_ValueError, "%s must have one entry per sequence", name);
     return ptr<const int32_t>(t);
@@ -178,9 +192,9 @@ int count(int64_t n, const char *what)
 }
 
 // A given output, or a new one.
-at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, const at::Tensor &like, at::ScalarType type)
+at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, const at::Tensor &like, at::ScalarType type, Where &on)
 {
-    return o == Py_None ? make(shape, like, type) : tensor(o, name, type);
+    return o == Py_None ? make(shape, like, type) : tensor(o, name, type, on);
 }
 
 PyObject *wrap(PyObject *given, const at::Tensor &t)
@@ -203,8 +217,12 @@ struct NormArgs {
     int64_t T, D;
     long long ldx, ldr = 0, ldro = 0;
 
-    NormArgs(PyObject *x_, PyObject *w_, PyObject *r_) : x(&tensor(x_, "x", BF16)), w(&tensor(w_, "weight", BF16)), r(nullptr)
+    Where on;
+
+    NormArgs(PyObject *x_, PyObject *w_, PyObject *r_) : x(nullptr), w(nullptr), r(nullptr)
     {
+        x = &tensor(x_, "x", BF16, on);
+        w = &tensor(w_, "weight", BF16, on);
         if (x->dim() != 2) fail(PyExc_TypeError, "x must be [T][D]");
         T = x->size(0);
         D = x->size(1);
@@ -212,7 +230,7 @@ struct NormArgs {
         if (w->dim() != 1 || w->size(0) != D || !w->is_contiguous())
             fail(PyExc_ValueError, "weight must be contiguous with %lld entries", static_cast<long long>(D));
         if (r_ != Py_None) {
-            r = &tensor(r_, "residual", BF16);
+            r = &tensor(r_, "residual", BF16, on);
             ldr = row_distance(*r, 1, {T, D}, "residual");
         }
     }
@@ -222,7 +240,7 @@ struct NormArgs {
             if (ro_ != Py_None) fail(PyExc_ValueError, "residual_out without a residual");
             return;
         }
-        ro = output(ro_, "residual_out", {T, D}, *x, BF16);
+        ro = output(ro_, "residual_out", {T, D}, *x, BF16, on);
         ldro = row_distance(ro, 1, {T, D}, "residual_out");
     }
     PyObject *wrapped(PyObject *ro_) const
@@ -241,7 +259,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
         NormArgs s(a[0], a[1], a[2]);
         const Stream stream(a[7], *s.x);
         s.out(a[6]);
-        const at::Tensor y = output(a[5], "y", {s.T, s.D}, *s.x, BF16);
+        const at::Tensor y = output(a[5], "y", {s.T, s.D}, *s.x, BF16, s.on);
         const long long ldy = row_distance(y, 1, {s.T, s.D}, "y");
         check_status("rmsnorm_residual",
                      rmsnorm_residual(ptr<const sv_bf16>(*s.x), s.ldx, s.r ? ptr<const sv_bf16>(*s.r) : nullptr, s.ldr,
@@ -268,8 +286,8 @@ PyObject *rmsnorm_fp8(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int64_t ns = group ? (s.D + group - 1) / group : 1;
         const Stream stream(a[9], *s.x);
         s.out(a[8]);
-        const at::Tensor y = output(a[6], "y", {s.T, s.D}, *s.x, at::kFloat8_e4m3fn);
-        const at::Tensor sc = output(a[7], "scales", {s.T, ns}, *s.x, F32);
+        const at::Tensor y = output(a[6], "y", {s.T, s.D}, *s.x, at::kFloat8_e4m3fn, s.on);
+        const at::Tensor sc = output(a[7], "scales", {s.T, ns}, *s.x, F32, s.on);
         const long long ldy = row_distance(y, 1, {s.T, s.D}, "y"), lds = row_distance(sc, 1, {s.T, ns}, "scales");
         check_status("rmsnorm_residual_fp8",
                      rmsnorm_residual_fp8(ptr<const sv_bf16>(*s.x), s.ldx, s.r ? ptr<const sv_bf16>(*s.r) : nullptr,
@@ -290,7 +308,7 @@ struct State {
     const at::Tensor *t;
     int64_t slots, Hv, dv, dk;
 
-    State(PyObject *o, int64_t dk_) : t(&tensor(o, "state", F32)), dk(dk_)
+    State(PyObject *o, int64_t dk_, Where &on) : t(&tensor(o, "state", F32, on)), dk(dk_)
     {
         if (t->dim() != 4 || !t->is_contiguous()) fail(PyExc_TypeError, "state must be contiguous [slots][Hv][dv][dk]");
         slots = t->size(0);
@@ -302,11 +320,11 @@ struct State {
 
 // sv_delta_rows of B x T rows (lead 2) or T rows (lead 1); q may be null.
 sv_delta_rows delta_rows(PyObject *q, PyObject *k, PyObject *v, PyObject *g, PyObject *beta, size_t lead, int64_t B,
-                         int64_t T, int64_t Hk, const State &s)
+                         int64_t T, int64_t Hk, const State &s, Where &on)
 {
     sv_delta_rows r{};
     auto take = [&](PyObject *o, const char *name, at::ScalarType type, int64_t heads, int64_t d, long long *ld) {
-        const at::Tensor &t = tensor(o, name, type);
+        const at::Tensor &t = tensor(o, name, type, on);
         if (lead == 2)
             *ld = d ? row_distance(t, 2, {B, T, heads, d}, name) : row_distance(t, 2, {B, T, heads}, name);
         else
@@ -341,11 +359,12 @@ PyObject *gated_delta_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     HANDLE_TH_ERRORS
     try {
         arguments("gated_delta_step", n, 14);
-        const at::Tensor &k = tensor(a[1], "k", BF16);
+        Where on;
+        const at::Tensor &k = tensor(a[1], "k", BF16, on);
         if (k.dim() != 4) fail(PyExc_TypeError, "k must be [B][T][Hk][dk]");
         const int64_t B = k.size(0), T = k.size(1), Hk = k.size(2);
-        const State s(a[5], k.size(3));
-        const sv_delta_rows rows = delta_rows(a[0], a[1], a[2], a[3], a[4], 2, B, T, Hk, s);
+        const State s(a[5], k.size(3), on);
+        const sv_delta_rows rows = delta_rows(a[0], a[1], a[2], a[3], a[4], 2, B, T, Hk, s, on);
         sv_delta_rows prev{};
         int64_t P = 0;
         // the sequence that prev gave, held until the launch: an iterator's
@@ -359,17 +378,17 @@ PyObject *gated_delta_step(PyObject *, PyObject *const *a, Py_ssize_t n)
             if (!f) throw PyFail{};
             if (PySequence_Fast_GET_SIZE(f) != 4) fail(PyExc_ValueError, "prev must be (k, v, g, beta)");
             PyObject **i = PySequence_Fast_ITEMS(f);
-            const at::Tensor &pk = tensor(i[0], "k of prev", BF16);
+            const at::Tensor &pk = tensor(i[0], "k of prev", BF16, on);
             if (pk.dim() != 4) fail(PyExc_ValueError, "prev must be rows of the same sequences");
             P = pk.size(1);
-            prev = delta_rows(nullptr, i[0], i[1], i[2], i[3], 2, B, P, Hk, s);
+            prev = delta_rows(nullptr, i[0], i[1], i[2], i[3], 2, B, P, Hk, s, on);
         }
         if (a[8] != Py_None && a[7] == Py_None) fail(PyExc_ValueError, "accept_len needs prev");
-        const int32_t *accept = a[8] == Py_None ? nullptr : indices(a[8], "accept_len", B);
-        const int32_t *idx = a[6] == Py_None ? nullptr : indices(a[6], "state_idx", B);
+        const int32_t *accept = a[8] == Py_None ? nullptr : indices(a[8], "accept_len", on, B);
+        const int32_t *idx = a[6] == Py_None ? nullptr : indices(a[6], "state_idx", on, B);
         const sv_delta_shape shape = delta_shape(Hk, s, a[10], (truth(a[11]) ? SV_DELTA_L2NORM : 0) | (truth(a[9]) ? SV_DELTA_COMMIT : 0));
         const Stream stream(a[13], k);
-        const at::Tensor o = output(a[12], "o", {B, T, s.Hv, s.dv}, k, BF16);
+        const at::Tensor o = output(a[12], "o", {B, T, s.Hv, s.dv}, k, BF16, on);
         const long long ldo = row_distance(o, 2, {B, T, s.Hv, s.dv}, "o");
         if (B)
             check_status("gated_delta_step",
@@ -389,18 +408,19 @@ PyObject *gated_delta_chunk(PyObject *, PyObject *const *a, Py_ssize_t n)
     HANDLE_TH_ERRORS
     try {
         arguments("gated_delta_chunk", n, 14);
-        const at::Tensor &k = tensor(a[1], "k", BF16);
+        Where on;
+        const at::Tensor &k = tensor(a[1], "k", BF16, on);
         if (k.dim() != 3) fail(PyExc_TypeError, "k must be [R][Hk][dk]");
         const int64_t R = k.size(0), Hk = k.size(1);
-        const State s(a[6], k.size(2));
-        const sv_delta_rows rows = delta_rows(a[0], a[1], a[2], a[3], a[4], 1, 1, R, Hk, s);
-        const int32_t *cu = indices(a[5], "cu_seqlens");
+        const State s(a[6], k.size(2), on);
+        const sv_delta_rows rows = delta_rows(a[0], a[1], a[2], a[3], a[4], 1, 1, R, Hk, s, on);
+        const int32_t *cu = indices(a[5], "cu_seqlens", on);
         const int64_t B = THPVariable_Unpack(a[5]).numel() - 1;
         if (B < 0) fail(PyExc_ValueError, "cu_seqlens must have B + 1 entries");
-        const int32_t *idx = a[7] == Py_None ? nullptr : indices(a[7], "state_idx", B);
+        const int32_t *idx = a[7] == Py_None ? nullptr : indices(a[7], "state_idx", on, B);
         const sv_delta_shape shape = delta_shape(Hk, s, a[9], (truth(a[10]) ? SV_DELTA_L2NORM : 0) | (truth(a[8]) ? SV_DELTA_ZERO_INIT : 0));
         const Stream stream(a[13], k);
-        const at::Tensor o = output(a[11], "o", {R, s.Hv, s.dv}, k, BF16);
+        const at::Tensor o = output(a[11], "o", {R, s.Hv, s.dv}, k, BF16, on);
         const long long ldo = row_distance(o, 1, {R, s.Hv, s.dv}, "o");
         if (B) {
             const int r = count(R, "rows"), b = count(B, "sequences");
@@ -409,7 +429,7 @@ PyObject *gated_delta_chunk(PyObject *, PyObject *const *a, Py_ssize_t n)
                 const size_t need = gated_delta_chunk_bytes(r, b, &shape);
                 ws = make({static_cast<int64_t>(need < 16 ? 16 : need)}, k, at::kByte);
             } else {
-                ws = tensor(a[12], "workspace", at::kByte);
+                ws = tensor(a[12], "workspace", at::kByte, on);
                 if (!ws.is_contiguous()) fail(PyExc_TypeError, "workspace must be contiguous");
             }
             check_status("gated_delta_chunk",
@@ -426,14 +446,14 @@ PyObject *gated_delta_chunk(PyObject *, PyObject *const *a, Py_ssize_t n)
 // ------------------------------------------------------- gated feed-forward
 
 // A contiguous CUDA tensor of one of the types that hold such bits.
-const at::Tensor &bits(PyObject *o, const char *name, std::initializer_list<at::ScalarType> types)
+const at::Tensor &bits(PyObject *o, const char *name, std::initializer_list<at::ScalarType> types, Where &on)
 {
     if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a tensor", name);
     const at::Tensor &t = THPVariable_Unpack(o);
     if (std::find(types.begin(), types.end(), t.scalar_type()) == types.end())
         fail(PyExc_TypeError, "%s must not be %s", name, c10::toString(t.scalar_type()));
     if (!t.is_cuda() || !t.is_contiguous()) fail(PyExc_ValueError, "%s must be a contiguous CUDA tensor", name);
-    return t;
+    return on(t, name);
 }
 
 // (x, Wq, scales, act, h, stream); act is SV_ACT_*
@@ -443,7 +463,9 @@ PyObject *w4a16_gate_up(PyObject *, PyObject *const *a, Py_ssize_t n)
     try {
         arguments("w4a16_gate_up", n, 6);
         const auto b16 = {BF16, at::kShort, at::kUInt16};
-        const at::Tensor &x = bits(a[0], "x", b16), &W = bits(a[1], "Wq", {at::kInt, at::kUInt32}), &sc = bits(a[2], "scales", b16);
+        Where on;
+        const at::Tensor &x = bits(a[0], "x", b16, on), &W = bits(a[1], "Wq", {at::kInt, at::kUInt32}, on),
+                         &sc = bits(a[2], "scales", b16, on);
         const long act = PyLong_AsLong(a[3]);
         if (act == -1 && PyErr_Occurred()) throw PyFail{};
         if (x.dim() != 2 || W.dim() != 2) fail(PyExc_ValueError, "x must be [T][K] and Wq [2F][K/8]");
@@ -451,7 +473,7 @@ PyObject *w4a16_gate_up(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (N % 2 || W.size(1) * 8 != K || !same(sc.sizes(), {N, K / 128}))
             fail(PyExc_ValueError, "shape mismatch between x, Wq and scales");
         const Stream stream(a[5], x);
-        const at::Tensor h = output(a[4], "h", {T, F}, x, BF16);
+        const at::Tensor h = output(a[4], "h", {T, F}, x, BF16, on);
         if (!same(h.sizes(), {T, F}) || !h.is_contiguous()) fail(PyExc_ValueError, "h must be contiguous [T][F]");
         check_status("w4a16_gate_up",
                      ::w4a16_gate_up(ptr<const sv_bf16>(x), ptr<const uint32_t>(W), ptr<const sv_bf16>(sc), count(T, "rows"),

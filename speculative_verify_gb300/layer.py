@@ -4,11 +4,11 @@ gated delta rule and gated feed-forward (the second half of
 
 Signatures and documentation; the argument checks, the outputs' allocation and
 the calls are in ``csrc/layer_bind.cpp`` (native, as each call is only a few
-microseconds of GPU time).  Tensors are torch CUDA tensors, each call is
-enqueued on ``stream`` (default: the current stream) and returns at once, and
-outputs are allocated unless given.  A tensor may be a strided view where its
+microseconds of GPU time).  Tensors are torch CUDA tensors, all on one device,
+each call is enqueued on ``stream`` (default: that device's current stream)
+and returns at once, and outputs are allocated unless given.  A tensor may be a strided view where its
 rows are equally far apart and dense inside.  Wrong types raise TypeError,
-wrong shapes or strides ValueError, and a refusal of the library
+wrong shapes, strides or devices ValueError, and a refusal of the library
 SpecVerifyError.
 """
 from __future__ import annotations
