@@ -17,8 +17,9 @@
 // only roundings to fewer bits are s (the value that the next layer adds to,
 // as the residual stream is kept in bf16) and the output's.
 //
-// Measured: 16,384 rows of 5,120 with a residual 103 us, 6.5 TB/s; one row 1.6
-// us, 32 rows to 8 bits 2.5 us.
+// Measured: 16,384 rows of 5,120 with a residual 103 us, 6.5 TB/s; one row 1.75
+// us, 32 rows to 8 bits 2.8 us (0.18 of it for the weight, which is read after
+// the wait for the kernel before: that one may have written it).
 #pragma once
 
 #include <cstdint>
@@ -165,18 +166,11 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
     __shared__ float part[32];
     __shared__ unsigned group_max[FP8 && ODD ? RN_ODD_MAX_D / RN_GROUP + 1 : 1];    // bits of each group's largest |s w|
     pdl_launch_dependents();
-    // The weight is model data: a short row's is read before the previous
-    // kernel's end, a longer one's (more registers) when it is used.
-    constexpr bool W_EARLY = VPT <= 2;
-    RnPiece<VEC> w[W_EARLY ? VPT : 1], s[VPT];
-    if constexpr (W_EARLY)
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = tid + j * nthr;
-            w[j].zero();
-            if (i < n) load_weight(w[j], i);
-        }
-    pdl_wait_prior();
+    pdl_wait_prior();                           // x, and the weight too, may come from the kernel before
+    // A short row's weight is read with x, a longer one's (more registers)
+    // when it is used.
+    constexpr bool W_KEPT = VPT <= 2;
+    RnPiece<VEC> w[W_KEPT ? VPT : 1], s[VPT];
     float sum = 0.f;
     {
         const uint16_t *x = p.x + row * p.ldx;
@@ -190,6 +184,13 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
             if (i < n) load(s[j], x, i);
             if (r && i < n) load(b[j], r, i);
         }
+        if constexpr (W_KEPT)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = tid + j * nthr;
+                w[j].zero();
+                if (i < n) load_weight(w[j], i);
+            }
         if (r) {
             uint16_t *ro = p.residual_out + row * p.ldro;
 #pragma unroll
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(RN_MAX_THREADS) rmsnorm_kernel(const NormParam
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     const float inv = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
     auto weight = [&](int j, int i) {
-        if constexpr (W_EARLY) return w[j];
+        if constexpr (W_KEPT) return w[j];
         RnPiece<VEC> v;
         load_weight(v, i);
         return v;

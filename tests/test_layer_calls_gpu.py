@@ -52,3 +52,24 @@ def test_prev_from_an_iterator(sv):
         sv.gated_delta_step(*rows, got, prev=3, commit=False)
     with pytest.raises(ValueError):
         sv.gated_delta_step(*rows, got, prev=(t for t in prev[:3]), commit=False)
+
+
+@pytest.mark.parametrize("D", [512, 5120, 5119, 30000])
+def test_norm_weight_from_the_kernel_before(sv, D):
+    """The weight may be what the kernel just before wrote (here the last row of a long norm's output)."""
+    g = rng_of(D)
+    T = 4096 if D < 10000 else 512
+    x, w = randn(g, 2, D).bfloat16(), randn(g, D).bfloat16()
+    y = torch.zeros(T, D, device="cuda").bfloat16()
+    for _ in range(8):
+        a = randn(g, T, D).bfloat16()
+        torch.cuda.synchronize()
+        sv.rmsnorm(a, w, y=y)
+        got, _ = sv.rmsnorm(x, y[-1])
+        got8, sc, _ = sv.rmsnorm_fp8(x, y[-1])
+        torch.cuda.synchronize()
+        last = y[-1].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, sv.rmsnorm(x, last)[0])
+        want8, wsc, _ = sv.rmsnorm_fp8(x, last)
+        assert torch.equal(got8.view(torch.uint8), want8.view(torch.uint8)) and torch.equal(sc, wsc)
