@@ -73,3 +73,29 @@ def test_norm_weight_from_the_kernel_before(sv, D):
         assert torch.equal(got, sv.rmsnorm(x, last)[0])
         want8, wsc, _ = sv.rmsnorm_fp8(x, last)
         assert torch.equal(got8.view(torch.uint8), want8.view(torch.uint8)) and torch.equal(sc, wsc)
+
+
+@pytest.mark.parametrize("T,K,F", [(1, 256, 200), (8, 2048, 640), (17, 256, 77), (32, 2048, 14000)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_negative_gates(sv, T, K, F, act):
+    """Gates down to -8, exact in fp32 (one activation of 1): a small output is as exact as a large one.
+
+    The bound is relative: half a bf16 unit, 2^-8; and of the activation's exponential, whose argument (50 at most)
+    is rounded a few times, 4 * 50 * 2^-24 < 2e-5."""
+    g = rng_of(T + F)
+    lv = torch.randint(0, 16, (2 * F, K), device="cuda", generator=g)
+    shift = 4 * torch.arange(8, device="cuda")
+    W = (lv.view(2 * F, K // 8, 8) << shift).sum(-1)
+    W = torch.where(W >= 2 ** 31, W - 2 ** 32, W).to(torch.int32)
+    s = (0.5 + 0.5 * torch.rand(2 * F, K // 128, device="cuda", generator=g)).bfloat16()
+    at = torch.randint(0, K, (T,), device="cuda", generator=g)
+    x = torch.zeros(T, K, device="cuda").bfloat16()
+    x[torch.arange(T, device="cuda"), at] = 1
+    h = sv.w4a16_gate_up(x, W, s, act=act).double()
+    y = ((lv[:, at] - 8).double() * s.double()[:, at // 128]).t()
+    gate, up = y[:, :F], y[:, F:]
+    z = gate if act == "silu" else 2 * (2 / torch.pi) ** 0.5 * (gate + 0.044715 * gate ** 3)
+    ref = gate / (1 + torch.exp(-z)) * up
+    err = (h - ref).abs()
+    assert bool((err <= (2.0 ** -8 + 2e-5) * ref.abs()).all()), float((err / ref.abs().clamp_min(1e-300)).max())
+    assert sv.last_device_error() == 0
