@@ -63,6 +63,7 @@ enum sv_status {
 #define SV_DEVERR_TIMEOUT     0x2   /* a pipeline wait gave up; outputs are invalid */
 #define SV_DEVERR_SMEM_ALIGN  0x4   /* shared memory not 1024-byte aligned; nothing was computed */
 #define SV_DEVERR_BAD_SLOT    0x8   /* a state_idx entry >= n_slots was skipped */
+#define SV_DEVERR_BAD_SEQLENS 0x10  /* decreasing cu_seqlens claim more blocks than the rows have: taken as empty */
 
 /*
  * w4a16_gemm -- y[t][n] = bf16_rne( sum_g float(scales[n][g]) *
@@ -533,7 +534,9 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
  * Whole prompts: R rows of B sequences one after another, sequence b having
  * rows cu_seqlens[b] .. cu_seqlens[b + 1] (B + 1 entries on the device, not
  * decreasing, within 0..R; out-of-range entries are moved into the range; a
- * sequence may be empty).  Each sequence's state is read from its slot
+ * sequence may be empty; entries that decrease and so claim more blocks of
+ * 64 than the rows have set SV_DEVERR_BAD_SEQLENS, the sequences then count
+ * as empty).  Each sequence's state is read from its slot
  * (taken as zero with SV_DELTA_ZERO_INIT), carried through its rows and
  * written back.  Rows of no sequence are not touched.  `ws` is device
  * memory of at least gated_delta_chunk_bytes(R, B, shape) bytes (0 when the

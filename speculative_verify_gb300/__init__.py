@@ -23,6 +23,7 @@ STATUS = {0: "SV_OK", -1: "SV_ERR_NULL", -2: "SV_ERR_SHAPE", -3: "SV_ERR_ALIGN",
 DEVERR_BAD_MAP_ID = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_BAD_SLOT = 0x8
+DEVERR_BAD_SEQLENS = 0x10
 
 _lib = None
 

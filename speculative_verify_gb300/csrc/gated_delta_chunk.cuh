@@ -50,6 +50,7 @@ struct DeltaChunkParams {
     int zero_init;
     unsigned *flags;                            // [DC_FLAGS / 4], zero when the scan starts
     uint8_t *blocks;                            // [R / 64 + B][Hv][DC_BLOCK]
+    int32_t *cu_run;                            // [B + 1]: cu as the scan reads it
 };
 
 // The rows of sequence b: cu[b] .. cu[b + 1], kept within [0, R].
@@ -149,6 +150,7 @@ struct DcPrepSmem {
     float near[DC_HEADS][DC_ROWS];              // e^(G_i - G_r)
     float far[DC_HEADS][4][DC_ROWS];            // [row block][j]: e^(G_r - G_j)
     int seq;
+    unsigned long long claimed;                 // blocks of all sequences
 };
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
@@ -186,8 +188,25 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
     const int id = blockIdx.x, hk = blockIdx.y, rep = p.Hv / p.Hk;
     pdl_launch_dependents();
     pdl_wait_prior();
-    if (id == 0 && hk == 0)
+    if (id == 0 && hk == 0) {
         for (int i = tid; i < DC_FLAGS / 4; i += 128) cp.flags[i] = 0u;
+        // The scan counts blocks in 32 bits.  Rows claimed twice (by cu_seqlens
+        // that decrease) may be any number of them: with more than the rows have
+        // once, the sequences count as empty.
+        if (tid == 0) sm.claimed = 0;
+        __syncthreads();
+        unsigned long long mine = 0;
+        for (int b = tid; b < cp.B; b += 128) {
+            int begin, end;
+            gd_range(cp.cu, cp.R, b, begin, end);
+            mine += static_cast<unsigned>(end - begin + DC_ROWS - 1) / DC_ROWS;
+        }
+        atomicAdd(&sm.claimed, mine);
+        __syncthreads();
+        const bool bad = sm.claimed > static_cast<unsigned>(cp.R / DC_ROWS + cp.B);
+        if (bad && tid == 0) atomicOr(p.err, 16);       // SV_DEVERR_BAD_SEQLENS
+        for (int b = tid; b <= cp.B; b += 128) cp.cu_run[b] = bad ? 0 : cp.cu[b];
+    }
     // the sequence whose blocks hold this one (the last such, where rows are
     // claimed twice, which cu_seqlens must not do)
     if (tid == 0) sm.seq = -1;

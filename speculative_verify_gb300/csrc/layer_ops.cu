@@ -308,6 +308,8 @@ cudaError_t delta_block_raise()
 // Blocks of the workspace: every sequence's whole and part blocks.
 long long delta_blocks(int R, int B) { return static_cast<long long>(R / DC_ROWS) + B; }
 
+size_t delta_block_bytes(int R, int B, int Hv) { return static_cast<size_t>(delta_blocks(R, B)) * static_cast<size_t>(Hv) * DC_BLOCK; }
+
 // A few rows go row by row, without blocks.  48 heads of 128 x 128, row by row
 // against by blocks: one sequence of 16 / 32 / 48 / 64 rows 14 / 25 / 36 / 47 us
 // against 25 / 25 / 25 / 26, four of 16 / 32 rows 24 / 43 against 39 / 39, 64 of
@@ -330,8 +332,10 @@ int delta_chunk_launch(const DeltaChunkParams &p, const DeviceInfo &dev, cudaStr
     rc = launch(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.d.Hk)), 128,
                 sizeof(DcPrepSmem<DK>), stream, p);
     if (rc != SV_OK) return rc;
+    DeltaChunkParams s = p;
+    s.cu = p.cu_run;
     return launch(delta_scan_kernel<DK>, dim3(static_cast<unsigned>(std::min<long long>(parts, DC_FLAGS / 4))), DS_THREADS,
-                  DsSmem<DK>::BYTES, stream, p, tmK, tmQ, tmV);
+                  DsSmem<DK>::BYTES, stream, s, tmK, tmQ, tmV);
 }
 
 // ------------------------------------------------------ gated feed-forward
@@ -485,7 +489,7 @@ size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape)
 {
     if (sv::check_delta_shape(shape) != SV_OK || R < 0 || B < 0) return 0;
     if (sv::delta_by_rows(R, B)) return 16;
-    return sv::DC_FLAGS + static_cast<size_t>(sv::delta_blocks(R, B)) * static_cast<size_t>(shape->Hv) * sv::DC_BLOCK;
+    return sv::DC_FLAGS + sv::delta_block_bytes(R, B, shape->Hv) + 4 * (static_cast<size_t>(B) + 1);
 }
 
 int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
@@ -496,7 +500,8 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     int rc = check_delta_shape(shape);
     if (rc != SV_OK) return rc;
     if (shape->flags & SV_DELTA_COMMIT) return SV_ERR_SHAPE;
-    if (R < 0 || delta_blocks(R, B) * shape->Hv > 0x7FFFFFFF) return SV_ERR_SHAPE;
+    // (a kernel counts the heads' blocks, and DS_EXTRA more a sequence, in 32 bits)
+    if (R < 0 || (delta_blocks(R, B) + 1LL * DS_EXTRA * B) * shape->Hv > 0x7FFFFFFF) return SV_ERR_SHAPE;
     if (R > 0 && (rc = check_delta_rows(rows, shape, true)) != SV_OK) return rc;
     if (R > 0 && (rc = check_delta_out(shape, o, ldo)) != SV_OK) return rc;
     rc = check_delta_state(shape, state, state_idx, n_slots, B);
@@ -515,6 +520,7 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     p.B = B;
     p.flags = static_cast<unsigned *>(ws);
     p.blocks = static_cast<uint8_t *>(ws) + DC_FLAGS;
+    p.cu_run = reinterpret_cast<int32_t *>(p.blocks + delta_block_bytes(R, B, shape->Hv));
     p.zero_init = (shape->flags & SV_DELTA_ZERO_INIT) != 0;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (!delta_by_rows(R, B)) return shape->dk == 64 ? delta_chunk_launch<64>(p, dev, cs) : delta_chunk_launch<128>(p, dev, cs);

@@ -99,3 +99,21 @@ def test_negative_gates(sv, T, K, F, act):
     err = (h - ref).abs()
     assert bool((err <= (2.0 ** -8 + 2e-5) * ref.abs()).all()), float((err / ref.abs().clamp_min(1e-300)).max())
     assert sv.last_device_error() == 0
+
+
+def test_chunk_rows_claimed_too_often(sv):
+    """cu_seqlens that go back and forth claim the rows many times over: nothing is run, and the error word says so."""
+    g = rng_of(8)
+    R, B, Hk, Hv, d = 6400, 9, 1, 2, 64
+    rows = delta_rows(g, (R,), Hk, Hv, d, d)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = R
+    state = randn(g, B, Hv, d, d)
+    got, o = state.clone(), torch.full((R, Hv, d), 7.0, device="cuda").bfloat16()
+    sv.gated_delta_chunk(*rows, cu, got, l2norm=True, o=o)
+    assert sv.last_device_error() == sv.DEVERR_BAD_SEQLENS
+    assert torch.equal(got, state) and bool((o == 7).all())
+    cu[:2], cu[2:] = torch.tensor([0, R]), R        # once: as always
+    sv.gated_delta_chunk(*rows, cu, got, l2norm=True, o=o)
+    assert sv.last_device_error() == 0
+    assert not torch.equal(got[0], state[0]) and torch.equal(got[1:], state[1:])
