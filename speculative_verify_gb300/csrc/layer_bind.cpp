@@ -7,11 +7,13 @@
 // Python (layer.py) holds the signatures and their documentation.
 //
 // Wrong types raise TypeError, wrong shapes, strides and devices ValueError,
-// and a status of the library the package's SpecVerifyError.
+// tensors that require a gradient RuntimeError (outside torch.no_grad()), and
+// a status of the library the package's SpecVerifyError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -54,12 +56,15 @@ void check_status(const char *fn, int rc)
 constexpr auto BF16 = at::kBFloat16;
 constexpr auto F32 = at::kFloat;
 
-// The device of a call's tensors: the first one's.
+// The device of a call's tensors: the first one's.  The calls have no
+// gradients, so a tensor that wants one is refused rather than its lost.
 struct Where {
     int device = -1;
 
     const at::Tensor &operator()(const at::Tensor &t, const char *name)
     {
+        if (t.requires_grad() && c10::GradMode::is_enabled())
+            fail(PyExc_RuntimeError, "%s requires a gradient, which this call does not compute (use torch.no_grad())", name);
         if (device < 0) device = t.get_device();
         if (t.get_device() != device)
             fail(PyExc_ValueError, "%s is on device %d, the call's first tensor on device %d", name,

@@ -9,7 +9,8 @@ each call is enqueued on ``stream`` (default: that device's current stream)
 and returns at once, and outputs are allocated unless given.  A tensor may be a strided view where its
 rows are equally far apart and dense inside.  Wrong types raise TypeError,
 wrong shapes, strides or devices ValueError, and a refusal of the library
-SpecVerifyError.
+SpecVerifyError.  There are no gradients: a tensor that requires one raises
+RuntimeError unless gradients are off (``torch.no_grad()``).
 """
 from __future__ import annotations
 

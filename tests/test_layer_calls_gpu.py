@@ -117,3 +117,36 @@ def test_chunk_rows_claimed_too_often(sv):
     sv.gated_delta_chunk(*rows, cu, got, l2norm=True, o=o)
     assert sv.last_device_error() == 0
     assert not torch.equal(got[0], state[0]) and torch.equal(got[1:], state[1:])
+
+
+def operands(g):
+    """{operator: its tensors}, small."""
+    q, k, v, gt, be = delta_rows(g, (2, 3), 1, 2, 64, 64)
+    state = randn(g, 2, 2, 64, 64)
+    cu = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    x, w = randn(g, 4, 256).bfloat16(), randn(g, 256).bfloat16()
+    W = torch.randint(-2 ** 31, 2 ** 31, (64, 32), device="cuda", generator=g).to(torch.int32)
+    return {"rmsnorm": dict(x=x, weight=w, residual=x.clone()), "rmsnorm_fp8": dict(x=x, weight=w, residual=x.clone()),
+            "gated_delta_step": dict(q=q, k=k, v=v, g=gt, beta=be, state=state, prev=(k, v, gt, be)),
+            "gated_delta_chunk": dict(q=q.flatten(0, 1), k=k.flatten(0, 1), v=v.flatten(0, 1), g=gt.flatten(0, 1),
+                                      beta=be.flatten(0, 1), cu_seqlens=cu, state=state),
+            "w4a16_gate_up": dict(x=x, Wq=W, scales=randn(g, 64, 2).bfloat16())}
+
+
+@pytest.mark.parametrize("op", ["rmsnorm", "rmsnorm_fp8", "gated_delta_step", "gated_delta_chunk", "w4a16_gate_up"])
+def test_no_gradient_is_lost(sv, op):
+    """A tensor that requires a gradient is refused, unless gradients are off."""
+    args = operands(rng_of(4))[op]
+    call = getattr(sv, op)
+    call(**args)
+    for name, t in args.items():
+        if name == "prev":
+            wants = tuple(a.detach().requires_grad_() for a in t)
+        elif t.is_floating_point():
+            wants = t.detach().requires_grad_()
+        else:
+            continue
+        with pytest.raises(RuntimeError, match="gradient"):
+            call(**dict(args, **{name: wants}))
+        with torch.no_grad():
+            call(**dict(args, **{name: wants}))
