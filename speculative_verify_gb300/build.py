@@ -3,9 +3,9 @@
 ``build()`` compiles the translation units of ``csrc/`` (which include the
 kernel headers) side by side and links them into
 ``speculative_verify_gb300/_build/libspecverify.so``, one ``-gencode`` for
-``sm_103a``, position-independent, static CUDA runtime; and
-``csrc/layer_bind.cpp``, the Python binding of the calls between the weight
-reads, against the installed torch's headers.
+``sm_103a``, position-independent, static CUDA runtime; and, where torch is
+installed, ``csrc/layer_bind.cpp``, the Python binding of the calls between
+the weight reads, against its headers.  The library needs nvcc alone.
 """
 from __future__ import annotations
 
@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspecverify.so")
 BIND_PATH = os.path.join(BUILD_DIR, "_layer.so")
+BIND_SOURCE = os.path.join(CSRC, "layer_bind.cpp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -36,25 +37,32 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libspecverify")
 
 
-def _sources():
+def _lib_sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(CSRC, "*.h"))
-                  + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BIND_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
-    return all(os.path.getmtime(s) <= t for s in _sources())
+def _newer(path, sources) -> bool:
+    """Whether `path` exists and none of the sources is newer."""
+    return os.path.exists(path) and all(os.path.getmtime(s) <= os.path.getmtime(path) for s in sources)
 
 
-def _torch_paths():
-    """(include directories, library directory) of the installed torch, CUDA and Python."""
+def lib_up_to_date() -> bool:
+    return _newer(LIB_PATH, _lib_sources())
+
+
+def bind_up_to_date() -> bool:
+    return _newer(BIND_PATH, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def _torch_root():
+    """The installed torch's folder, or None."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch is required to build the Python binding")
-    root = os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec else None
+
+
+def _torch_paths(root):
+    """(include directories, library directory) of that torch, CUDA and Python."""
     inc = os.path.join(root, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     return [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda], \
@@ -67,35 +75,44 @@ def _run(cmds, verbose: bool) -> None:
     outs = [p.communicate()[0] for p in procs]
     for cmd, p, out in zip(cmds, procs, outs):
         if p.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + out)
+            raise RuntimeError("build failed:\n" + " ".join(cmd) + "\n" + out)
         if verbose:
             print(out)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
-    if not force and up_to_date():
+    """Compile what is older than its sources -- the library, and the binding
+    where torch is installed; return the library's path."""
+    torch_root = _torch_root()
+    lib, bind = force or not lib_up_to_date(), torch_root is not None and (force or not bind_up_to_date())
+    if not lib and not bind:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     tag = ".%d.tmp" % os.getpid()
-    tmp = LIB_PATH + tag
-    nvcc, flags = _nvcc(), [*ARCH_FLAGS, *NVCC_FLAGS, "-I" + INCLUDE] + (["-Xptxas=-v"] if verbose else [])
-    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    objs = [os.path.join(BUILD_DIR, os.path.basename(u) + tag + ".o") for u in units]
-    bind_obj, bind_tmp = os.path.join(BUILD_DIR, "layer_bind" + tag + ".o"), BIND_PATH + tag
-    torch_inc, torch_lib = _torch_paths()
-    cxx = shutil.which("g++") or "g++"
+    compile_cmds, objs = [], []
+    if lib:
+        nvcc, flags = _nvcc(), [*ARCH_FLAGS, *NVCC_FLAGS, "-I" + INCLUDE] + (["-Xptxas=-v"] if verbose else [])
+        units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+        objs = [os.path.join(BUILD_DIR, os.path.basename(u) + tag + ".o") for u in units]
+        compile_cmds += [[nvcc, *flags, "-c", "-o", o, u] for u, o in zip(units, objs)]
+    bind_obj = os.path.join(BUILD_DIR, "layer_bind" + tag + ".o")
+    if bind:
+        cxx, (torch_inc, torch_lib) = shutil.which("g++") or "g++", _torch_paths(torch_root)
+        compile_cmds += [[cxx, "-std=c++17", "-O2", "-fPIC", "-Wall", "-I" + INCLUDE, *("-isystem" + d for d in torch_inc),
+                          "-c", "-o", bind_obj, BIND_SOURCE]]
     try:
-        _run([[nvcc, *flags, "-c", "-o", o, u] for u, o in zip(units, objs)]
-             + [[cxx, "-std=c++17", "-O2", "-fPIC", "-Wall", "-I" + INCLUDE, *("-isystem" + d for d in torch_inc), "-c",
-                 "-o", bind_obj, os.path.join(CSRC, "layer_bind.cpp")]], verbose)
-        _run([[nvcc, *ARCH_FLAGS, "-shared", "-Xlinker", "-soname=libspecverify.so", "-o", tmp, *objs]], verbose)
-        os.replace(tmp, LIB_PATH)
-        # torch's libraries are in the process before the binding is
-        _run([[cxx, "-shared", "-o", bind_tmp, bind_obj, LIB_PATH, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
-               "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]],
-             verbose)
-        os.replace(bind_tmp, BIND_PATH)
+        _run(compile_cmds, verbose)
+        if lib:
+            tmp = LIB_PATH + tag
+            _run([[nvcc, *ARCH_FLAGS, "-shared", "-Xlinker", "-soname=libspecverify.so", "-o", tmp, *objs]], verbose)
+            os.replace(tmp, LIB_PATH)
+        if bind:
+            # torch's libraries are in the process before the binding is
+            tmp = BIND_PATH + tag
+            _run([[cxx, "-shared", "-o", tmp, bind_obj, LIB_PATH, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu",
+                   "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]],
+                 verbose)
+            os.replace(tmp, BIND_PATH)
     finally:
         for o in [*objs, bind_obj]:
             if os.path.exists(o):
