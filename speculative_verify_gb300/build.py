@@ -5,7 +5,8 @@ kernel headers) side by side and links them into
 ``speculative_verify_gb300/_build/libspecverify.so``, one ``-gencode`` for
 ``sm_103a``, position-independent, static CUDA runtime; and, where torch is
 installed, ``csrc/layer_bind.cpp``, the Python binding of the calls between
-the weight reads, against its headers.  The library needs nvcc alone.
+the weight reads, against its headers (and again when torch or Python are
+others).  The library needs nvcc alone.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspecverify.so")
 BIND_PATH = os.path.join(BUILD_DIR, "_layer.so")
 BIND_SOURCE = os.path.join(CSRC, "layer_bind.cpp")
+BIND_FOR = BIND_PATH + ".for"           # the torch and Python that the binding was compiled against
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -51,8 +53,17 @@ def lib_up_to_date() -> bool:
     return _newer(LIB_PATH, _lib_sources())
 
 
-def bind_up_to_date() -> bool:
-    return _newer(BIND_PATH, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+def _bind_for(torch_root) -> str:
+    """The torch (its version file) and the Python (its ABI) that a binding built now belongs to."""
+    with open(os.path.join(torch_root, "version.py")) as f:
+        return "%s %s\n%s" % (sysconfig.get_config_var("SOABI"), torch_root, f.read())
+
+
+def bind_up_to_date(torch_root) -> bool:
+    if not _newer(BIND_PATH, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]) or not os.path.exists(BIND_FOR):
+        return False
+    with open(BIND_FOR) as f:
+        return f.read() == _bind_for(torch_root)
 
 
 def _torch_root():
@@ -84,7 +95,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile what is older than its sources -- the library, and the binding
     where torch is installed; return the library's path."""
     torch_root = _torch_root()
-    lib, bind = force or not lib_up_to_date(), torch_root is not None and (force or not bind_up_to_date())
+    lib, bind = force or not lib_up_to_date(), torch_root is not None and (force or not bind_up_to_date(torch_root))
     if not lib and not bind:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -113,6 +124,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
                    "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]],
                  verbose)
             os.replace(tmp, BIND_PATH)
+            with open(tmp, "w") as f:
+                f.write(_bind_for(torch_root))
+            os.replace(tmp, BIND_FOR)
     finally:
         for o in [*objs, bind_obj]:
             if os.path.exists(o):

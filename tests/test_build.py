@@ -22,6 +22,7 @@ def ran(tmp_path, monkeypatch):
     monkeypatch.setattr(b, "BUILD_DIR", str(tmp_path))
     monkeypatch.setattr(b, "LIB_PATH", str(tmp_path / "libspecverify.so"))
     monkeypatch.setattr(b, "BIND_PATH", str(tmp_path / "_layer.so"))
+    monkeypatch.setattr(b, "BIND_FOR", str(tmp_path / "_layer.so.for"))
     return cmds
 
 
@@ -59,3 +60,22 @@ def test_both_are_built_once(ran):
     b.build()
     assert built(b.LIB_PATH, ran) == 1 and built(b.BIND_PATH, ran) == 0
     assert not [f for f in os.listdir(b.BUILD_DIR) if f.endswith(".tmp") or f.endswith(".o")]
+
+
+def test_binding_is_rebuilt_for_another_torch(ran, tmp_path, monkeypatch):
+    """The binding uses torch's C++ internals: another torch or Python needs another one, the library does not."""
+    root = tmp_path / "torch"
+    root.mkdir()
+    monkeypatch.setattr(b, "_torch_root", lambda: str(root))
+    (root / "version.py").write_text("__version__ = '1'\n")
+    b.build()
+    ran.clear()
+    b.build()
+    assert not ran
+    (root / "version.py").write_text("__version__ = '2'\n")
+    b.build()
+    assert built(b.BIND_PATH, ran) == 1 and built(b.LIB_PATH, ran) == 0
+    ran.clear()
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: "cpython-399")
+    b.build()
+    assert built(b.BIND_PATH, ran) == 1 and built(b.LIB_PATH, ran) == 0
