@@ -256,10 +256,12 @@ bool delta_step_by_rows(int rows, long long state_rows, const DeviceInfo &dev)
 
 // Whether a block of up to 16 rows has two warps for 16 state rows.  With two
 // or three blocks a multiprocessor the chain of a block counts, which that
-// shortens: 2 / 4 sequences of 48 heads of 128 x 128, 8 and 8 rows 8.0 / 9.7 us
-// against 9.2 / 10.5, 4 and 4 rows 7.0 / 7.5 against 6.2 / 9.7, 3 rows 6.7 / 7.1
-// against 8.2 / 9.4.  A single block (one sequence: 5.7 against 5.4 us) and more
-// of them (6 sequences 13.1 against 10.6, 16 29 against 25) do better without.
+// shortens, whatever the rows: 48 heads of 128 x 128, 4 and 4 rows (all, one or
+// none replayed) of 2 sequences 7.3 / 7.0 / 5.0 us against 8.7 / 8.3 / 5.4, of 4
+// 7.6 / 7.3 / 5.1 against 9.9 / 9.6 / 6.3; 8 and 8 of 2 / 4 8.9 / 9.9 against
+// 10.2 / 10.7; 4 rows alone 7.0 / 7.2 against 8.4 / 9.5.  A single block (one
+// sequence: 5.7 against 5.4 us) and more of them (5 sequences, 8 and 8 rows 11.6
+// against 10.6; 16 of them 29 against 25) do better without.
 bool delta_step_split(long long state_rows, const DeviceInfo &dev)
 {
     const long long blocks = state_rows / GB_COLS;
