@@ -22,6 +22,11 @@
  *    and returns before the GPU has run it.  It performs no host<->device
  *    copy and no synchronisation.  Results are valid once the stream has
  *    been synchronised.
+ *  * Wq and scales are model data: a kernel reads them before the kernels
+ *    before it on the stream have ended, so no kernel still in flight may be
+ *    writing them (after loading weights, synchronise before the first call
+ *    with them).  Everything else may come from the kernel just before
+ *    (vocab_map unless SV_MAP_STATIC is given).
  *  * A call returns SV_OK or a negative status.  On any error nothing is
  *    launched and no output is touched.
  *  * The library keeps one scratch area per device (split-tile fp32
@@ -445,9 +450,11 @@ int sv_debug_set_wait_stall(uint32_t ns);
  * above with these differences, stated per call: rows may be strided (an
  * `ld` argument is the distance between rows in elements), row counts are
  * not limited to 32 where the call says so, and a call with no rows (T = 0,
- * B = 0) succeeds without a launch.  None of them allocates, and none uses
- * the per-device scratch area, so they may overlap with other calls.  The
- * framework serves frozen int4 weights; there are no gradients.
+ * B = 0) succeeds without a launch, w4a16_gate_up excepted (1 <= T <= 32).
+ * Of the per-device scratch area, which the first call on a device makes
+ * (outside stream capture, as above), they use the error word only, so they
+ * may overlap with other calls.  The framework serves frozen int4 weights;
+ * there are no gradients.
  */
 
 #define SV_NORM_UNIT_OFFSET 0x1     /* the weight is stored as an offset from 1 */
@@ -546,7 +553,8 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
  * an infinity in a row makes the outputs of its 64 rows, and the state, NaN
  * (gated_delta_step keeps it from earlier rows).  The state comes out within
  * about 1e-5 of the rule in exact arithmetic (the products' fp32 factors
- * have 16 bits), gated_delta_step's within 1e-6.
+ * have 16 bits), gated_delta_step's within 1e-6: a prompt that needs that is
+ * taken through it, 32 rows at a time.
  */
 size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape);
 int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlens, int B, const sv_delta_shape *shape,
@@ -562,6 +570,9 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
  * [2F][K/8] and scales [2F][K/128] hold the F gate rows, then the F up rows
  * (the fused gate+up matrix as w4a16_gemm reads it); x [T][K], h [T][F].
  * The sums are fp32 and not rounded before the activation and the product.
+ *   Errors: SV_ERR_NULL, SV_ERR_SHAPE (T outside 1..32, K < 128 or
+ *   K % 128 != 0, F outside 1..2^30, an unknown act), SV_ERR_ALIGN,
+ *   SV_ERR_CUDA, SV_ERR_NOMEM.
  */
 int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, int T, int K, int F, int act,
                   sv_bf16 *h, sv_stream stream);

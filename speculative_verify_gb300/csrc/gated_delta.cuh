@@ -401,12 +401,12 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
 //
 // A block has 64 state rows; a warp copies its rows to shared memory while the
 // chain of small steps (gates, norms, A) runs, and back through it (8-byte
-// stores from the accumulators: 248 instead of 238 us).
+// stores from the accumulators take 10 us more at 256 x (4 + 4) rows).
 //
 // A NaN or an infinity in a row reaches that row and later ones only.
 //
 // Measured, 48 heads of 128 x 128: 256 sequences with 4 rows and 4 replayed
-// 245 us, 6.8 TB/s, HBM-bound (five blocks a multiprocessor); with 8 and 8,
+// 242 us, 6.9 TB/s, HBM-bound (five blocks a multiprocessor); with 8 and 8,
 // 320 us (four).  4 sequences with 8 and 8 rows 9.7 us (10.5 with one warp for
 // 16 state rows), of which 3.9 are traffic: the chain of a block -- slot and
 // gates from memory, running sum, decays, A, S k, u, update -- takes 5.4 us by

@@ -359,7 +359,7 @@ int gate_up_cols(int F, int sms)
 // (99) 8 tokens 21.2 / 22.8; F 17,408 (115) 1 / 8 / 16 / 32 tokens 21.5 / 21.7 /
 // 22.1 / 26.6 against 23.5 / 23.9 / 30.0 / 42.3.  With K 1,280 the wide
 // kernel's start weighs more: F 17,408, 8 / 16 / 32 tokens 9.0 / 9.4 / 11.7
-// against 7.5 / 9.3 / 12.9.
+// against 7.5 / 9.3 / 12.9 (16 tokens: no difference).
 bool gate_up_wide(int T, int G, int cols)
 {
     return cols >= (T > 16 ? 54 + 430 / G : T > 8 ? 60 + 430 / G : 82 + 680 / G);

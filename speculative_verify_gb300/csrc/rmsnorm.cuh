@@ -6,7 +6,8 @@
 //   8 bits: scale = max|y| / 448 over 128 columns or the row, q = e4m3(y / scale)
 //
 // The row's norm cancels from y / scale: with z = s w, exact in fp32 (two
-// bf16 factors), q = e4m3(448 z / max|z|) has one rounding before its own.
+// bf16 factors; z = s (1 + w) is rounded twice), q = e4m3(448 z / max|z|) has
+// one more rounding before its own.
 //
 // One block per row, the row held in registers (as bf16) between the sum of squares
 // and the output, so that every byte crosses memory once: the kernel is
@@ -15,7 +16,10 @@
 // the strides and the addresses allow it, or are off by as much in every
 // tensor; else 1.  Sums, the norm and the scales are fp32; the
 // only roundings to fewer bits are s (the value that the next layer adds to,
-// as the residual stream is kept in bf16) and the output's.
+// as the residual stream is kept in bf16) and the output's.  Long rows do not
+// fit 64 registers a thread whole: of those beyond 32,768 columns 100 to 280
+// bytes a thread are in local memory, of those that go column by column
+// beyond 8,192 40 to 160, beyond 16,384 2 to 3 KB (L1, in part L2).
 //
 // Measured: 16,384 rows of 5,120 with a residual 103 us, 6.5 TB/s; one row 1.75
 // us, 32 rows to 8 bits 2.8 us (0.18 of it for the weight, which is read after

@@ -130,8 +130,9 @@ def gated_delta_chunk(q, k, v, g, beta, cu_seqlens, state, state_idx=None, zero_
 def w4a16_gate_up(x, Wq, scales, act="silu", h=None, stream=None):
     """h[T][F] (bf16) = act(x Wg^T) * (x Wu^T) from the fused int4 gate+up
     matrix: Wq [2F][K/8], scales [2F][K/128], the F gate rows first; act:
-    "silu" or "gelu" (tanh form).  See ``w4a16_gate_up`` in
-    include/specverify.h."""
+    "silu" or "gelu" (tanh form); 1 to 32 rows, all tensors contiguous.  Wq
+    and scales must not be written by a kernel still in flight.  See
+    ``w4a16_gate_up`` in include/specverify.h."""
     if _ext is None:
         _load()
     if act not in ACTS:
