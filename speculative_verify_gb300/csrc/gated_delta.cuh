@@ -38,6 +38,7 @@ namespace sv {
 constexpr int GD_MAX_ROWS = 32;                 // rows of one staged block
 constexpr float GD_MAX_LOG = 10.f;              // largest |sum of log decays| kept outside the state
 constexpr float GD_L2_EPS = 1e-6f;
+constexpr float GD_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this by the block forms
 
 struct DeltaRows {
     const uint16_t *q, *k, *v;                  // bf16 bits, [rows][heads][d]
@@ -421,18 +422,6 @@ __device__ __forceinline__ void gb_split_tf32(float v, uint32_t &hi, uint32_t &l
     lo = __float_as_uint(v - __uint_as_float(hi));
 }
 
-__device__ __forceinline__ void gb_ldmatrix(uint32_t (&r)[4], const uint16_t *p)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
-}
-
-__device__ __forceinline__ void gb_ldmatrix_trans(uint32_t (&r)[4], const uint16_t *p)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
-}
-
 // Sums of two floats each, kept as the rounded sum and what it leaves:
 // differences of large sums give the decays between near rows.
 struct Sum2 {
@@ -448,8 +437,6 @@ __device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b)
 }
 
 __device__ __forceinline__ float exp_diff(Sum2 a, float bhi, float blo) { return expf((a.hi - bhi) + (a.lo - blo)); }
-
-constexpr float GB_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
 
 constexpr int GB_COLS = 64;                     // state rows of a block
 constexpr int gb_threads(int KS) { return 2 * GB_COLS * KS; }  // KS warps for 16 of them, a part of the columns each
@@ -561,7 +548,7 @@ __global__ void __launch_bounds__(gb_threads(KS), 4 / KS) gated_delta_block_kern
         Sum2 G[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            G[e] = Sum2{gate[e] < GB_MIN_LOG ? GB_MIN_LOG : gate[e], 0.f};
+            G[e] = Sum2{gate[e] < GD_MIN_LOG ? GD_MIN_LOG : gate[e], 0.f};
         }
         Sum2 run = add2(G[0], G[1]);
 #pragma unroll 1
@@ -647,9 +634,9 @@ __global__ void __launch_bounds__(gb_threads(KS), 4 / KS) gated_delta_block_kern
 #pragma unroll
             for (int s = 0; s < DK / 32; ++s) {
                 uint32_t a0[4], a1[4], bb[4];
-                gb_ldmatrix(a0, arow + 32 * s);
-                gb_ldmatrix(a1, arow + 32 * s + 16);
-                gb_ldmatrix(bb, sm.k[8 * j + (lane & 7)] + 32 * s + (lane >> 3) * 8);
+                ldmatrix_x4(a0, smem_addr(arow + 32 * s));
+                ldmatrix_x4(a1, smem_addr(arow + 32 * s + 16));
+                ldmatrix_x4(bb, smem_addr(sm.k[8 * j + (lane & 7)] + 32 * s + (lane >> 3) * 8));
                 mma_bf16_16816(acc[0], a0[0], a0[1], a0[2], a0[3], bb[0], bb[1]);
                 mma_bf16_16816(acc[1], a1[0], a1[1], a1[2], a1[3], bb[2], bb[3]);
             }
@@ -896,7 +883,7 @@ __global__ void __launch_bounds__(gb_threads(KS), 4 / KS) gated_delta_block_kern
         }
         auto add = [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
             uint32_t bb[4];
-            gb_ldmatrix_trans(bb, sm.k[8 * j + (lane & 7)] + wk * COLS + 32 * i + (lane >> 3) * 8);
+            ldmatrix_x4_trans(bb, smem_addr(sm.k[8 * j + (lane & 7)] + wk * COLS + 32 * i + (lane >> 3) * 8));
             // rows 8 j + 2 c and + 1, zero where not kept: their u is, but a key may hold a NaN
             const int t = 8 * j + 2 * c;
             const uint32_t rows_in = t + 1 < kept ? 0xFFFFFFFFu : t < kept ? 0xFFFFu : 0u;

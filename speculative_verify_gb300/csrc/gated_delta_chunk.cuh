@@ -41,7 +41,6 @@ constexpr int DC_MAT = DC_ROWS * 128;           // bytes of one 64 x 64 bf16 mat
 constexpr int DC_FACTORS = 1024;                // bytes of a block's row factors
 constexpr int DC_BLOCK = 4 * DC_MAT + DC_FACTORS;   // T transposed (two terms), M (two terms), factors
 constexpr int DC_FLAGS = 4096;                  // bytes of hand-over flags before the blocks, one word a CTA
-constexpr float DC_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this
 
 struct DeltaChunkParams {
     DeltaParams d;                              // rows, shape, state; T and prev unused
@@ -152,18 +151,6 @@ struct DcPrepSmem {
     int seq;
     unsigned long long claimed;                 // blocks of all sequences
 };
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 
 // d (two n8 tiles of 16 rows) += a x b over 16 columns, both in two terms.
 __device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&a_hi)[4], const uint32_t (&a_lo)[4],
@@ -312,7 +299,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const DeltaChunkPara
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
                     float v = t < n ? p.rows.g[(row0 + t) * p.rows.ldg + hv] : 0.f;
-                    if (v < DC_MIN_LOG) v = DC_MIN_LOG;
+                    if (v < GD_MIN_LOG) v = GD_MIN_LOG;
                     G[e] = Sum2{v, 0.f};
                     sm.beta[warp][t] = t < n ? p.rows.beta[(row0 + t) * p.rows.ldg + hv] : 0.f;
                 }

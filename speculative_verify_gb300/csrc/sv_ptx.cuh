@@ -322,6 +322,22 @@ __device__ __forceinline__ float fma2_f16_f32(uint32_t a, uint32_t b, float c)
     return d;
 }
 
+// ---------------------------------------------------------------- ldmatrix
+
+// Four 8x8 matrices of 16-bit values; lane l's address is row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// The same, each matrix transposed.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
 // ---------------------------------------------------------------- tensor core
 
 // D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col).
