@@ -6,7 +6,7 @@
 //
 //   S <- e^g S;  u = beta (v - S k);  S <- S + u k^T;  o = scale S q
 //
-// The dv rows of S never mix, so a block takes `cols` of them of one head of
+// The dv rows of S never mix, so a block takes 32 of them of one head of
 // one sequence and a thread a quarter of one: DK / 4 state values in
 // registers, read and written once.  Four lanes share a row of S, and each
 // takes every fourth 16-byte piece of it, so that a warp's access is eight
@@ -36,6 +36,8 @@
 namespace sv {
 
 constexpr int GD_MAX_ROWS = 32;                 // rows of one staged block
+constexpr int GD_COLS = 32, GD_THREADS = 4 * GD_COLS;   // state rows of a block
+constexpr int gd_blocks(int dk) { return 512 / dk; }    // of a multiprocessor: DK registers a thread
 constexpr float GD_MAX_LOG = 10.f;              // largest |sum of log decays| kept outside the state
 constexpr float GD_L2_EPS = 1e-6f;
 constexpr float GD_MIN_LOG = -200.f;            // e^-200 is 0 in fp32: a log decay of -inf is taken as this by the block forms
@@ -58,7 +60,6 @@ struct DeltaParams {
     int n_slots;
     uint16_t *o;
     long long ldo;
-    int cols;                                   // state rows of a block, blockDim.x / 4
     int *err;
 };
 
@@ -100,18 +101,18 @@ __device__ __forceinline__ ulonglong2 lds_x4(uint32_t addr)
 }
 
 // Shared memory of a block (floats): keys and queries [GD][DK] each, values
-// [GD][cols], then per row beta, e^g, the running decay, its inverse, q.k.
-__host__ __device__ constexpr int gd_smem_floats(int rows, int dk, int cols) { return rows * (2 * dk + cols + 5); }
+// [GD][GD_COLS], then per row beta, e^g, the running decay, its inverse, q.k.
+__host__ __device__ constexpr int gd_smem_floats(int rows, int dk) { return rows * (2 * dk + GD_COLS + 5); }
 
 template <int DK>
 struct GdSmem {
     float *k, *q, *v, *beta, *eg, *c, *cinv, *qk;
-    __device__ __forceinline__ GdSmem(float *base, int rows, int cols)
+    __device__ __forceinline__ GdSmem(float *base, int rows)
     {
         k = base;
         q = k + rows * DK;
         v = q + rows * DK;
-        beta = v + rows * cols;
+        beta = v + rows * GD_COLS;
         eg = beta + rows;
         c = eg + rows;
         cinv = c + rows;
@@ -142,18 +143,18 @@ __device__ __forceinline__ void gd_read(const uint16_t *src, uint32_t (&d)[N])
 
 template <int DK>
 __device__ __forceinline__ void gd_first(const DeltaParams &p, const DeltaRows &r, long long r0, int n, int hv, int col0,
-                                         int cols, bool want_q, GdFirst<DK> &f)
+                                         bool want_q, GdFirst<DK> &f)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = hv / (p.Hv / p.Hk);
     if (warp < n) {
         gd_read(r.k + (r0 + warp) * r.ldk + static_cast<long long>(hk) * DK + lane * (DK / 32), f.k);
         if (want_q) gd_read(r.q + (r0 + warp) * r.ldq + static_cast<long long>(hk) * DK + lane * (DK / 32), f.q);
     }
-    if (tid < n * (cols / 8)) {
-        const int t = tid / (cols / 8), j = (tid - t * (cols / 8)) * 8;
+    if (tid < n * (GD_COLS / 8)) {
+        const int t = tid / (GD_COLS / 8), j = tid % (GD_COLS / 8) * 8;
         f.v = *reinterpret_cast<const uint4 *>(r.v + (r0 + t) * r.ldv + static_cast<long long>(hv) * p.dv + col0 + j);
     }
-    if (warp == (blockDim.x >> 5) - 1 && lane < n) {
+    if (warp == GD_THREADS / 32 - 1 && lane < n) {
         f.g = r.g[(r0 + lane) * r.ldg + hv];
         f.beta = r.beta[(r0 + lane) * r.ldg + hv];
     }
@@ -166,12 +167,13 @@ __device__ __forceinline__ void gd_first(const DeltaParams &p, const DeltaRows &
 // the block).
 template <int DK>
 __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &r, long long r0, int n, int hv, int col0,
-                                         int cols, const GdSmem<DK> &sm, bool want_q, const GdFirst<DK> &f)
+                                         const GdSmem<DK> &sm, bool want_q, const GdFirst<DK> &f)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NWARP = GD_THREADS / 32;
     constexpr int E = DK / 32;                  // a lane's values of a row, consecutive
     const int hk = hv / (p.Hv / p.Hk);
-    for (int t = warp; t < n; t += nwarp) {
+    for (int t = warp; t < n; t += NWARP) {
         uint32_t kw[E / 2], qw[E / 2];
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
@@ -210,20 +212,20 @@ __device__ __forceinline__ bool gd_stage(const DeltaParams &p, const DeltaRows &
         }
         if (lane == 0) sm.qk[t] = qk * rk * rq;
     }
-    // values: eight per thread (cols is a multiple of 32)
-    for (int i = tid; i < n * (cols / 8); i += blockDim.x) {
-        const int t = i / (cols / 8), j = (i - t * (cols / 8)) * 8;
+    // values: eight per thread
+    for (int i = tid; i < n * (GD_COLS / 8); i += GD_THREADS) {
+        const int t = i / (GD_COLS / 8), j = i % (GD_COLS / 8) * 8;
         const uint4 u = i == tid ? f.v : *reinterpret_cast<const uint4 *>(r.v + (r0 + t) * r.ldv + static_cast<long long>(hv) * p.dv + col0 + j);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            sm.v[t * cols + j + 2 * e] = __uint_as_float(w[e] << 16);
-            sm.v[t * cols + j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            sm.v[t * GD_COLS + j + 2 * e] = __uint_as_float(w[e] << 16);
+            sm.v[t * GD_COLS + j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
         }
     }
     // gates; the running sum of the log decays by a warp scan (n <= 32)
     bool ok = true;
-    if (warp == nwarp - 1) {
+    if (warp == NWARP - 1) {
         const float g = lane < n ? f.g : 0.f;
         float G = g;
 #pragma unroll
@@ -279,7 +281,7 @@ struct GdState {
 // Run `n` staged rows through the state.  OUT: write their outputs (to
 // o + t * ldo, bf16).  Afterwards the registers hold S itself.
 template <int DK, bool OUT>
-__device__ __forceinline__ void gd_rows(GdState<DK> &st, const GdSmem<DK> &sm, int n, int cols, bool running,
+__device__ __forceinline__ void gd_rows(GdState<DK> &st, const GdSmem<DK> &sm, int n, bool running,
                                         uint16_t *o, long long ldo)
 {
     const int i = threadIdx.x & 3, col = threadIdx.x >> 2;
@@ -313,7 +315,7 @@ __device__ __forceinline__ void gd_rows(GdState<DK> &st, const GdSmem<DK> &sm, i
             a += __shfl_xor_sync(0xFFFFFFFFu, a, d);
             if (OUT) b += __shfl_xor_sync(0xFFFFFFFFu, b, d);
         }
-        const float u = sm.beta[t] * (sm.v[t * cols + col] - c * a);
+        const float u = sm.beta[t] * (sm.v[t * GD_COLS + col] - c * a);
         if (OUT && i == 0) o[t * ldo + col] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(c, b, u * sm.qk[t])));
         const float uc = u * cinv;
         const f32x2 u2 = pack_x2(uc, uc);
@@ -333,15 +335,15 @@ __device__ __forceinline__ int gd_slot(const int32_t *state_idx, int n_slots, in
     return -1;
 }
 
-// Grid: x = dv / cols, y = Hv, z = B.
+// One or two rows in all.  Grid: x = dv / GD_COLS, y = Hv, z = B.
 template <int DK>
-__global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(GD_THREADS, gd_blocks(DK)) gated_delta_step_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(16) float gd_smem[];
-    const int cols = p.cols, col0 = blockIdx.x * cols, hv = blockIdx.y, b = blockIdx.z;
+    const int col0 = blockIdx.x * GD_COLS, hv = blockIdx.y, b = blockIdx.z;
     const int i = threadIdx.x & 3, col = threadIdx.x >> 2;
     const int cap = max(p.T, p.prev_T);
-    const GdSmem<DK> sm(gd_smem, cap, cols);
+    const GdSmem<DK> sm(gd_smem, cap);
     pdl_launch_dependents();
     pdl_wait_prior();
     // rows, which need no slot, are asked for before it is waited for
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
     const int slot = p.state_idx ? p.state_idx[b] : b;
     const int accept = p.accept_len && p.prev_T > 0 ? p.accept_len[b] : p.prev_T;
     GdFirst<DK> f;
-    gd_first<DK>(p, lead, static_cast<long long>(b) * lead_T, lead_T, hv, col0, cols, p.prev_T == 0, f);
+    gd_first<DK>(p, lead, static_cast<long long>(b) * lead_T, lead_T, hv, col0, p.prev_T == 0, f);
     uint16_t *o = p.o + static_cast<long long>(b) * p.T * p.ldo + static_cast<long long>(hv) * p.dv + col0;
     if (slot < 0 || slot >= p.n_slots) {        // an inactive entry: its outputs are zero
         if (slot >= 0 && threadIdx.x == 0) atomicOr(p.err, 8);
@@ -364,16 +366,16 @@ __global__ void __launch_bounds__(512) gated_delta_step_kernel(const DeltaParams
     if (p.prev_T > 0) {
         const int n = p.accept_len ? min(p.prev_T, max(0, min(accept, p.prev_T) + 1)) : p.prev_T;
         if (n > 0) {
-            const bool running = gd_stage<DK>(p, p.prev, static_cast<long long>(b) * p.prev_T, n, hv, col0, cols, sm, false, f);
-            gd_rows<DK, false>(st, sm, n, cols, running, nullptr, 0);
+            const bool running = gd_stage<DK>(p, p.prev, static_cast<long long>(b) * p.prev_T, n, hv, col0, sm, false, f);
+            gd_rows<DK, false>(st, sm, n, running, nullptr, 0);
             if (!p.commit) st.store(s, i);
             __syncthreads();
         }
-        if (p.T > 0) gd_first<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, cols, true, f);
+        if (p.T > 0) gd_first<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, true, f);
     }
     if (p.T > 0) {
-        const bool running = gd_stage<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, cols, sm, true, f);
-        gd_rows<DK, true>(st, sm, p.T, cols, running, o, p.ldo);
+        const bool running = gd_stage<DK>(p, p.rows, static_cast<long long>(b) * p.T, p.T, hv, col0, sm, true, f);
+        gd_rows<DK, true>(st, sm, p.T, running, o, p.ldo);
     }
     if (p.commit) st.store(s, i);
 }

@@ -64,15 +64,15 @@ __device__ __forceinline__ void gd_range(const int32_t *cu, int R, int b, int &b
 // part block of every sequence before it.
 __device__ __forceinline__ int dc_base(int begin, int b) { return begin / DC_ROWS + b; }
 
-// Row by row, for short sequences.  Grid: x = dv / cols, y = Hv, z = B.
+// Row by row, for short sequences.  Grid: x = dv / GD_COLS, y = Hv, z = B.
 template <int DK>
-__global__ void __launch_bounds__(512) gated_delta_rows_kernel(const DeltaChunkParams cp)
+__global__ void __launch_bounds__(GD_THREADS, gd_blocks(DK)) gated_delta_rows_kernel(const DeltaChunkParams cp)
 {
     extern __shared__ __align__(16) float gd_smem[];
     const DeltaParams &p = cp.d;
-    const int cols = p.cols, col0 = blockIdx.x * cols, hv = blockIdx.y, b = blockIdx.z;
+    const int col0 = blockIdx.x * GD_COLS, hv = blockIdx.y, b = blockIdx.z;
     const int i = threadIdx.x & 3, col = threadIdx.x >> 2;
-    const GdSmem<DK> sm(gd_smem, GD_MAX_ROWS, cols);
+    const GdSmem<DK> sm(gd_smem, GD_MAX_ROWS);
     pdl_launch_dependents();
     pdl_wait_prior();
     int begin, end;
@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(512) gated_delta_rows_kernel(const DeltaChunkP
     for (int r0 = begin; r0 < end; r0 += GD_MAX_ROWS) {
         const int n = min(GD_MAX_ROWS, end - r0);
         GdFirst<DK> f;
-        gd_first<DK>(p, p.rows, r0, n, hv, col0, cols, true, f);
-        const bool running = gd_stage<DK>(p, p.rows, r0, n, hv, col0, cols, sm, true, f);
-        gd_rows<DK, true>(st, sm, n, cols, running, o, p.ldo);
+        gd_first<DK>(p, p.rows, r0, n, hv, col0, true, f);
+        const bool running = gd_stage<DK>(p, p.rows, r0, n, hv, col0, sm, true, f);
+        gd_rows<DK, true>(st, sm, n, running, o, p.ldo);
         o += n * p.ldo;
         __syncthreads();
     }

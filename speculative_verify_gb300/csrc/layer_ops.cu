@@ -66,10 +66,6 @@ int ops_device(DeviceInfo *out)
     if (ready[out->dev]) return SV_OK;
     cudaError_t e = cudaSuccess;
     auto up = [&](cudaError_t r) { e = e != cudaSuccess ? e : r; };
-    up(raise(gated_delta_step_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
-    up(raise(gated_delta_step_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
-    up(raise(gated_delta_rows_kernel<64>, 4 * gd_smem_floats(GD_MAX_ROWS, 64, 128)));
-    up(raise(gated_delta_rows_kernel<128>, 4 * gd_smem_floats(GD_MAX_ROWS, 128, 128)));
     up(delta_block_raise<64>());
     up(delta_block_raise<128>());
     up(raise(delta_prep_kernel<64>, sizeof(DcPrepSmem<64>)));
@@ -236,7 +232,6 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
     p.n_slots = n_slots;
     p.o = o;
     p.ldo = ldo;
-    p.cols = s->dv < 32 ? s->dv : 32;
     p.err = dev.err;
     return p;
 }
@@ -480,11 +475,11 @@ int gated_delta_step(const sv_delta_rows *rows, int T, const sv_delta_rows *prev
     const bool split = delta_step_split(static_cast<long long>(B) * p.Hv * p.dv, dev);
     if (!delta_step_by_rows(T + prev_T, static_cast<long long>(B) * p.Hv * p.dv, dev))
         return shape->dk == 64 ? delta_block_dispatch<64>(p, B, split, cs) : delta_block_dispatch<128>(p, B, split, cs);
-    const dim3 grid(static_cast<unsigned>(p.dv / p.cols), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
+    const dim3 grid(static_cast<unsigned>(p.dv / GD_COLS), static_cast<unsigned>(p.Hv), static_cast<unsigned>(B));
     const int cap = T > prev_T ? T : prev_T;
-    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk, p.cols));
-    return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, 4 * p.cols, smem, cs, p)
-                           : launch(gated_delta_step_kernel<128>, grid, 4 * p.cols, smem, cs, p);
+    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(cap, shape->dk));
+    return shape->dk == 64 ? launch(gated_delta_step_kernel<64>, grid, GD_THREADS, smem, cs, p)
+                           : launch(gated_delta_step_kernel<128>, grid, GD_THREADS, smem, cs, p);
 }
 
 size_t gated_delta_chunk_bytes(int R, int B, const sv_delta_shape *shape)
@@ -526,10 +521,11 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
     p.zero_init = (shape->flags & SV_DELTA_ZERO_INIT) != 0;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (!delta_by_rows(R, B)) return shape->dk == 64 ? delta_chunk_launch<64>(p, dev, cs) : delta_chunk_launch<128>(p, dev, cs);
-    const dim3 grid(static_cast<unsigned>(p.d.dv / p.d.cols), static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(B));
-    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(GD_MAX_ROWS, shape->dk, p.d.cols));
-    return shape->dk == 64 ? launch(gated_delta_rows_kernel<64>, grid, 4 * p.d.cols, smem, cs, p)
-                           : launch(gated_delta_rows_kernel<128>, grid, 4 * p.d.cols, smem, cs, p);
+    const dim3 grid(static_cast<unsigned>(p.d.dv / GD_COLS), static_cast<unsigned>(p.d.Hv), static_cast<unsigned>(B));
+    const size_t smem = 4 * static_cast<size_t>(gd_smem_floats(GD_MAX_ROWS, shape->dk));
+    static_assert(4 * gd_smem_floats(GD_MAX_ROWS, 128) <= 48 * 1024, "no launch needs the limit raised");
+    return shape->dk == 64 ? launch(gated_delta_rows_kernel<64>, grid, GD_THREADS, smem, cs, p)
+                           : launch(gated_delta_rows_kernel<128>, grid, GD_THREADS, smem, cs, p);
 }
 
 int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, int T, int K, int F, int act,
