@@ -23,9 +23,10 @@
 // within 5e-6 of the rule in exact arithmetic (row by row in fp32: 2e-7), well
 // below the 2^-9 of the bf16 rows that it is made from and of the outputs.
 //
-// Measured, 16 key and 48 value heads of 128: 4 prompts of 8,192 rows 745 us
-// (prep 275), one of 3,847 rows 214 (42), nine ragged ones with 6,317 rows 190.  Prep is bound by its instructions (4,700 a warp, 43 % issue),
-// the scan by the chain of a block.
+// Measured, 16 key and 48 value heads of 128: 4 prompts of 8,192 rows 747 us
+// (prep 275), one of 3,847 rows 215 (42), nine ragged ones with 6,317 rows 190.
+// Prep is bound by its instructions (4,700 a warp, 43 % issue), the scan by
+// the chain of a block.
 #pragma once
 
 #include <cuda.h>

@@ -239,8 +239,8 @@ DeltaParams delta_params(const sv_delta_rows *rows, const sv_delta_shape *s, flo
 // Whether a step runs row by row (gated_delta_step_kernel) or takes its rows
 // all at once (gated_delta_block_kernel).  One or two rows whose state is a
 // wave of small blocks at most are quicker without the second kernel's tiles:
-// 48 heads of 128 x 128, one row, 1 / 4 sequences 3.9 / 6.2 us against 5.4 /
-// 9.0, two rows 4.4 / 7.1 against 5.5 / 9.2.  Beyond that its asynchronous
+// 48 heads of 128 x 128, one row, 1 / 4 sequences 3.8 / 6.0 us against 5.4 /
+// 9.0, two rows 4.1 / 6.9 against 5.5 / 9.2.  Beyond that its asynchronous
 // copies win: 16 / 64 / 256 sequences of two rows 19 / 66 / 244 us against
 // 21 / 100 / 389, and so do its tiles with more rows: 4 and 4 rows of 1 / 4
 // sequences 5.8 / 9.6 us, row by row 7.0 / 11.7.
