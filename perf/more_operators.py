@@ -1,0 +1,408 @@
+"""The operators of a hybrid decoder's attention layers, as measured cases.
+
+The layers that keep a cache run these entry points of
+``speculative_verify_gb300`` between the projections of ``w4a16_gemm``:
+
+  rotary   rotary                     positions into queries and keys, one or several axes
+  append   kv4_append + kv4_gather    rows into the pages of a 4-bit cache, and back
+  step     kv4_attention              decode and verify rows over the cache
+  chunk    kv4_attention, cu_seqlens  whole prompts over the cache
+
+``run`` computes them in plain 32-bit torch operations where ``own`` is false
+and calls the library where it is true.  ``exact`` evaluates the definitions
+in 64 bits.
+
+The cache: pages of 64 tokens, [pages][Hk][72 d] bytes: K codes [64][d / 2],
+V codes, K scales [64][d / 16], V scales.  A code is a 4-bit e2m1 number (the
+even dimension in the low half of a byte), a scale an e4m3 number for 16
+dimensions: value = code * scale * (k_scale or v_scale).  seq_lens counts the
+tokens before a call's rows, and row t of a sequence sees the tokens up to its
+own, seq_lens + t; with a window only the last `window` of them and the first
+`sinks` tokens of the sequence.
+"""
+import math
+
+import torch
+
+own = False
+
+PAGE = 64
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# --------------------------------------------------------------------------
+# cases
+
+
+def _rotary(rows, Hq, Hk, d, rot, axes=1, far=262144, interleaved=False):
+    return dict(op="rotary", rows=rows, Hq=Hq, Hk=Hk, d=d, rot=rot, axes=axes, far=far, interleaved=interleaved)
+
+
+def _append(lens, ctx, Hk, d, scale=1.0):
+    return dict(op="append", lens=",".join(str(n) for n in lens), ctx=ctx, Hk=Hk, d=d, scale=scale)
+
+
+def _step(B, T, ctx, Hq, Hk, d, window=0, sinks=0):
+    return dict(op="step", B=B, T=T, ctx=ctx, Hq=Hq, Hk=Hk, d=d, window=window, sinks=sinks)
+
+
+def _chunk(lens, ctx, Hq, Hk, d, window=0, sinks=0):
+    return dict(op="chunk", lens=",".join(str(n) for n in lens), ctx=ctx, Hq=Hq, Hk=Hk, d=d, window=window, sinks=sinks)
+
+
+def listed():
+    return [
+        # one row of single-stream decode, a quarter of each head rotated, far into a long context
+        dict(_rotary(1, 24, 4, 256, 64), name="rotary T1"),
+        # a prompt of video frames: time, height and width
+        dict(_rotary(8192, 32, 8, 128, 128, axes=3, far=16384), name="rotary T8192 3 axes"),
+        # a verify cycle of four streams of eight rows
+        dict(_append([8] * 4, 4096, 4, 256), name="append 4x8"),
+        # prompts of mixed lengths, an empty one and a single token among them, behind what the cache holds
+        dict(_append([1, 700, 63, 0, 2049, 129, 1500, 64, 311], 500, 8, 128, scale=0.05), name="append ragged 9"),
+        # plain decode of one stream, a short context
+        dict(_step(1, 1, 1000, 24, 4, 256), name="step 1x1 ctx 1000"),
+        # a verify block of four rows of one stream, a very long context
+        dict(_step(1, 4, 131072, 24, 4, 256), name="step 1x4 ctx 131072"),
+        # four streams of eight verify rows
+        dict(_step(4, 8, 16384, 24, 4, 256), name="step 4x8 ctx 16384"),
+        # a large serving batch of uneven contexts
+        dict(_step(256, 1, 4096, 32, 8, 128), name="step 256x1 ctx 4096"),
+        # a sliding window behind a few first tokens
+        dict(_step(64, 4, 20001, 16, 8, 64, window=4096, sinks=4), name="step 64x4 window 4096"),
+        # prompts of mixed lengths, as above
+        dict(_chunk([1, 700, 63, 0, 2049, 129, 1500, 64, 311], 500, 32, 8, 128), name="chunk ragged 9"),
+        # a piece of a long prompt, sliding window
+        dict(_chunk([2048], 30011, 32, 8, 128, window=4096, sinks=64), name="chunk 2048 window 4096"),
+        # one long prompt
+        dict(_chunk([8192], 0, 24, 4, 256), name="chunk 1x8192"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def _cut(rng, rows, B):
+    cuts = sorted(rng.randint(0, rows) for _ in range(B - 1))
+    return [b - a for a, b in zip([0] + cuts, cuts + [rows])]
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "append", "step", "step", "chunk", "chunk"])
+    Hq, Hk, d = rng.choice([(24, 4, 256), (32, 8, 128), (16, 2, 256), (16, 8, 64), (8, 4, 128), (20, 4, 128), (7, 1, 64),
+                            (16, 1, 128), (40, 8, 128)])
+    if op == "rotary":
+        rot = rng.choice([d, d, d // 2, d // 4])
+        return _rotary(_log(rng, 1, 8192), Hq, Hk, d, rot, rng.choice([1, 1, 2, 3, 4]), _log(rng, 1024, 1 << 20),
+                       rng.random() < 0.4)
+    if op == "append":
+        rows, B = _log(rng, 1, 8192), rng.randint(1, 16)
+        lens = [max(1, rows // B)] * B if rng.random() < 0.4 else _cut(rng, rows, B)
+        return _append(lens, rng.choice([0, _log(rng, 1, 20000)]), Hk, d, rng.choice([1.0, 1.0, 0.05]))
+    window = rng.choice([0, 0, _log(rng, 16, 8192)])
+    sinks = rng.choice([0, 4, rng.randint(1, 130)]) if window else 0
+    if op == "step":
+        B, T = _log(rng, 1, 256), rng.choice([1, 1, 2, 3, 4, 5, 8, 11, 16, 32])
+        ctx = _log(rng, 16, max(16, min(131072, 800_000_000 // (B * Hk * d))))
+        ctx = max(16, min(ctx, 1_000_000_000 // (B * T * Hq)))
+        return _step(B, T, ctx, Hq, Hk, d, window, sinks)
+    rows, B = _log(rng, 65, 8192), rng.randint(1, 8)
+    ctx = rng.choice([0, 0, _log(rng, 64, 30000)])
+    lens = _cut(rng, rows, B)
+    while B * max(lens) * (max(lens) + ctx) * Hq > 1_600_000_000:
+        ctx, lens = ctx // 2, [n - n // 4 for n in lens]
+    return _chunk(lens, ctx, Hq, Hk, d, window, sinks)
+
+
+def _rows(case):
+    """Rows of each sequence."""
+    return [case["T"]] * case["B"] if case["op"] == "step" else [int(n) for n in case["lens"].split(",")]
+
+
+def _before(case):
+    """Tokens of each sequence before the call's rows: uneven, ctx at most, the first one ctx."""
+    return [int(case["ctx"] * (1 - 0.5 * (b * 0.618034 % 1))) for b in range(len(_rows(case)))]
+
+
+def _seen(before, rows, window, sinks):
+    """(token and row pairs that are visible, tokens that some row sees) of a sequence."""
+    pairs = tokens = 0
+    if rows:
+        for p in range(before, before + rows):
+            first = max(0, p - window + 1) if window else 0
+            pairs += p + 1 - first + min(sinks if window else 0, first)
+        first = max(0, before - window + 1) if window else 0
+        tokens = before + rows - first + min(sinks if window else 0, first)
+    return pairs, tokens
+
+
+def work(case):
+    c = case
+    if c["op"] == "rotary":
+        n = c["rows"] * (c["Hq"] + c["Hk"]) * c["d"]
+        return {"bytes": 4 * n + 4 * c["rows"] * c["axes"] + 4 * c["rot"],
+                "flops": 3 * c["rows"] * (c["Hq"] + c["Hk"]) * c["rot"]}
+    Hk, d, rows, before = c["Hk"], c["d"], _rows(c), _before(c)
+    token = Hk * (d + d // 8)                   # a token's K and V in the cache
+    if c["op"] == "append":
+        n = sum(rows)
+        return {"bytes": n * (8 * Hk * d + 2 * token), "flops": 8 * n * Hk * d}
+    seen = [_seen(b, n, c["window"], c["sinks"]) for b, n in zip(before, rows)]
+    return {"bytes": token * sum(t for _, t in seen) + 4 * sum(rows) * c["Hq"] * d,
+            "flops": 4 * d * c["Hq"] * sum(p for p, _ in seen)}
+
+
+# --------------------------------------------------------------------------
+# inputs
+
+
+def _codes(x, g):
+    """(codes [..., d / 2], scales [..., d / 16]) bytes of 32-bit rows x [..., d]: for each 16 dimensions
+    scale = e4m3(max|x| / 6 g), code = e2m1(x / (g scale)), both to the nearest, ties to the even one."""
+    x = x.unflatten(-1, (-1, 16))
+    six = torch.full((), 6 * g, device=x.device)
+    scale = (x.abs().amax(-1) / six).clamp_max(448).to(torch.float8_e4m3fn)
+    s = (scale.float() * torch.full((), g, device=x.device))[..., None]
+    r = (x / s).abs()
+    code = (r > 0.25).to(torch.uint8)
+    code += r >= 0.75
+    code += r > 1.25
+    code += r >= 1.75
+    code += r > 2.5
+    code += r >= 3.5
+    code += r > 5
+    code += 8 * torch.signbit(x).to(torch.uint8)
+    code = torch.where(s == 0, 0, code).flatten(-2)
+    return code[..., ::2] + 16 * code[..., 1::2], scale.view(torch.uint8)
+
+
+def _views(cache):
+    """K codes, V codes, K scales, V scales [pages][Hk][64][...] of the cache's bytes."""
+    d = cache.shape[-1] // 72
+    return [cache[..., a * d:b * d].unflatten(-1, (PAGE, -1)) for a, b in ((0, 32), (32, 64), (64, 68), (68, 72))]
+
+
+def _table(case, gen):
+    """Page table [B][most pages] of a shuffled pool, and the pool's size."""
+    pages = [-(-(b + n) // PAGE) for b, n in zip(_before(case), _rows(case))]
+    order = torch.randperm(sum(pages) + 3, device="cuda", generator=gen).to(torch.int32)
+    table = torch.full((len(pages), max(max(pages), 1)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(pages):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return table, len(order)
+
+
+def prepare(case, seed):
+    c = case
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    rand = lambda *s: torch.rand(*s, device="cuda", generator=gen)                       # noqa: E731
+    randn = lambda *s: torch.randn(*s, device="cuda", generator=gen)                     # noqa: E731
+    st = {"case": c}
+    Hk, d = c["Hk"], c["d"]
+    if c["op"] == "rotary":
+        n, Hq, axes = c["rows"], c["Hq"], c["axes"]
+        qkv = randn(n, (Hq + 2 * Hk) * d).bfloat16()        # q and k are slices of one projection's output
+        st["q"], st["k"] = qkv[:, :Hq * d].unflatten(1, (Hq, d)), qkv[:, Hq * d:(Hq + Hk) * d].unflatten(1, (Hk, d))
+        first = torch.randint(0, c["far"], (1,), device="cuda", generator=gen)
+        run = torch.arange(n, device="cuda") + first
+        # further axes (height, width) go over a grid of 64 columns, the first over its cells
+        st["positions"] = torch.stack([run // 64 ** min(axes - 1, 2)] + [run // 64 ** (axes - 2 - a) % 64
+                                                                         for a in range(axes - 1)]).to(torch.int32)
+        st["inv_freq"] = (1e7 ** (-torch.arange(c["rot"] // 2, dtype=torch.float64, device="cuda") * 2 / c["rot"])).float()
+        st["axes"] = (torch.arange(c["rot"] // 2, device="cuda") % axes).to(torch.int32) if axes > 1 else None
+        return st
+    rows, before = _rows(c), _before(c)
+    st["table"], n_pages = _table(c, gen)
+    st["before"] = torch.tensor(before, dtype=torch.int32, device="cuda")
+    st["cu"] = None
+    if c["op"] != "step":
+        st["cu"] = torch.tensor([0] + rows).cumsum(0).to(torch.int32).cuda()
+    st["cache"] = cache = torch.empty(n_pages, Hk, 72 * d, dtype=torch.uint8, device="cuda")
+    g = c.get("scale", 1.0)
+    some = max(1, (1 << 24) // (Hk * PAGE * d))             # pages at a time
+    for a in range(0, n_pages, some):
+        part = cache[a:a + some]
+        for i in range(2):                                  # keys with channels of uneven size, values without
+            x = randn(len(part), Hk, PAGE, d) * (0.4 + 1.2 * rand(Hk, 1, d) ** 2 if i == 0 else 1)
+            for view, got in zip(_views(part)[i::2], _codes(x.bfloat16().float(), g)):
+                view.copy_(got)
+    n = sum(rows)
+    if c["op"] == "append":
+        qkv = randn(n, 8 * Hk * d).bfloat16()               # k and v are slices of one projection's output
+        st["k"], st["v"] = qkv[:, 6 * Hk * d:7 * Hk * d].unflatten(1, (Hk, d)), qkv[:, 7 * Hk * d:].unflatten(1, (Hk, d))
+        return st
+    q = (2.5 * randn(n, c["Hq"], d)).bfloat16()             # a few units of spread among the scores
+    st["q"] = q if st["cu"] is not None else q.unflatten(0, (c["B"], c["T"]))
+    return st
+
+
+# --------------------------------------------------------------------------
+# plain forms, 32 bits
+
+
+def _plain_rotary(st):
+    c, rot = st["case"], st["case"]["rot"]
+    axis = st["axes"].long() if st["axes"] is not None else torch.zeros(rot // 2, dtype=torch.long, device="cuda")
+    angle = st["positions"].double().t()[:, axis] * st["inv_freq"].double()
+    cos, sin = torch.cos(angle).float()[:, None], torch.sin(angle).float()[:, None]
+    out = []
+    for x in (st["q"], st["k"]):
+        f = x[..., :rot].float()
+        a, b = (f[..., ::2], f[..., 1::2]) if c["interleaved"] else f.chunk(2, -1)
+        a, b = a * cos - b * sin, b * cos + a * sin
+        y = torch.stack((a, b), -1).flatten(-2) if c["interleaved"] else torch.cat((a, b), -1)
+        out.append(torch.cat((y.bfloat16(), x[..., rot:]), -1))
+    return tuple(out)
+
+
+def _places(st):
+    """(page, place in it) of every row of the call."""
+    cu = st["cu"].long()
+    seq = torch.repeat_interleave(torch.arange(len(cu) - 1, device="cuda"), cu.diff(), output_size=len(st["k"]))
+    pos = st["before"].long()[seq] + torch.arange(len(seq), device="cuda") - cu[seq]
+    return st["table"][seq, pos // PAGE].long(), pos % PAGE
+
+
+def _values(codes, scales, g):
+    """32-bit values of codes [..., d / 2] and scales [..., d / 16] bytes."""
+    level = torch.tensor(E2M1, device="cuda")
+    level = torch.cat((level, -level))
+    pair = torch.stack((level.repeat(16), level.repeat_interleave(16)), 1)      # of a byte
+    x = pair.index_select(0, codes.flatten().int()).view(*codes.shape[:-1], -1, 16)
+    return (x * scales.view(torch.float8_e4m3fn).float()[..., None] * g).flatten(-2)
+
+
+def _plain_append(st):
+    page, at = _places(st)
+    g = st["case"]["scale"]
+    kc, vc, ks, vs = _views(st["cache"])
+    kc[page, :, at], ks[page, :, at] = _codes(st["k"].float(), g)
+    vc[page, :, at], vs[page, :, at] = _codes(st["v"].float(), g)
+    return (_values(kc[page, :, at], ks[page, :, at].contiguous(), g).bfloat16(),
+            _values(vc[page, :, at], vs[page, :, at].contiguous(), g).bfloat16())
+
+
+def _visible(pos, n, window, sinks):
+    """Whether a row at pos [...] sees token 0 .. n - 1: [..., n]."""
+    j = torch.arange(n, device="cuda")
+    p = pos[..., None]
+    seen = j <= p
+    if window:
+        seen &= (p - j < window) | (j < sinks)
+    return seen
+
+
+def _plain_attention(st):
+    c = st["case"]
+    Hq, Hk, d = c["Hq"], c["Hk"], c["d"]
+    q = st["q"]
+    if st["cu"] is not None:                    # rows of equal count: [B][most rows]
+        rows = st["cu"].long().diff()
+        at = st["cu"].long()[:-1, None] + torch.arange(max(_rows(c)), device="cuda")
+        real = at < st["cu"].long()[1:, None]
+        q = q[at.clamp_max(len(q) - 1)]
+    B, T = q.shape[:2]
+    used = st["cache"][st["table"].long().clamp_min(0)].transpose(1, 2)         # [B][Hk][pages][72 d]
+    kc, vc, ks, vs = (v.flatten(2, 3) for v in _views(used))
+    k, v = _values(kc, ks, 1.0), _values(vc, vs, 1.0)                           # [B][Hk][tokens][d]
+    seen = _visible(st["before"].long()[:, None] + torch.arange(T, device="cuda"), k.shape[2], c["window"], c["sinks"])
+    q = q.float().unflatten(2, (Hk, Hq // Hk)).permute(0, 2, 3, 1, 4)           # [B][Hk][group][T][d]
+    s = (q.flatten(2, 3) @ k.transpose(-1, -2)).mul_(d ** -0.5).unflatten(2, (Hq // Hk, T))
+    s.masked_fill_(~seen[:, None, None], -math.inf)
+    s.sub_(s.amax(-1, keepdim=True)).exp_()
+    total = s.sum(-1)
+    o = (s.flatten(2, 3) @ v).unflatten(2, (Hq // Hk, T)) / total[..., None]
+    o = o.permute(0, 3, 1, 2, 4).flatten(2, 3).bfloat16()                       # [B][T][Hq][d]
+    return o[real] if st["cu"] is not None else o
+
+
+def _own(st):
+    import speculative_verify_gb300 as sv
+    c = st["case"]
+    if c["op"] == "rotary":
+        return sv.rotary(st["q"], st["k"], st["positions"], st["inv_freq"], axes=st["axes"], interleaved=c["interleaved"])
+    if c["op"] == "append":
+        sv.kv4_append(st["k"], st["v"], st["cache"], st["table"], st["before"], cu_seqlens=st["cu"],
+                      k_scale=c["scale"], v_scale=c["scale"])
+        return sv.kv4_gather(st["cache"], st["table"], st["before"], len(st["k"]), cu_seqlens=st["cu"],
+                             k_scale=c["scale"], v_scale=c["scale"])
+    return sv.kv4_attention(st["q"], st["cache"], st["table"], st["before"], cu_seqlens=st["cu"], window=c["window"],
+                            sinks=c["sinks"])
+
+
+PLAIN = {"rotary": _plain_rotary, "append": _plain_append, "step": _plain_attention, "chunk": _plain_attention}
+
+
+def run(state):
+    return _own(state) if own else PLAIN[state["case"]["op"]](state)
+
+
+# --------------------------------------------------------------------------
+# definitions in 64 bits
+
+
+def _exact_values(codes, scales):
+    """64-bit values of codes [..., d / 2] and e4m3 scales [..., d / 16]."""
+    half = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).long()
+    e, m = half >> 1 & 3, (half & 1).double()
+    x = torch.where(e > 0, (1 + m / 2) * 2.0 ** (e - 1).double(), m / 2) * (1 - 2 * (half >> 3)).double()
+    return x * scales.contiguous().view(torch.float8_e4m3fn).double().repeat_interleave(16, -1)
+
+
+def _nearest(x, levels):
+    """The nearest of the levels (rising) for each x, the even-numbered of two that are as near."""
+    hi = torch.searchsorted(levels, x.contiguous()).clamp(1, len(levels) - 1)
+    a, b = x - levels[hi - 1], levels[hi] - x
+    return torch.where((a < b) | ((a == b) & (hi % 2 == 1)), levels[hi - 1], levels[hi])
+
+
+def exact(case, seed):
+    c, st = case, prepare(case, seed)
+    Hk, d = c["Hk"], c["d"]
+    if c["op"] == "rotary":
+        h = c["rot"] // 2
+        out = []
+        for x in (st["q"], st["k"]):
+            y = x.double().clone()
+            for i in range(h):
+                at = (2 * i, 2 * i + 1) if c["interleaved"] else (i, i + h)
+                t = st["positions"][i % c["axes"]].double() * st["inv_freq"][i].double()
+                z = torch.polar(torch.ones_like(t), t)[:, None] * torch.complex(x[..., at[0]].double(), x[..., at[1]].double())
+                y[..., at[0]], y[..., at[1]] = z.real, z.imag
+            out.append(y)
+        return tuple(out)
+    if c["op"] == "append":
+        fp8 = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
+        fp4 = torch.tensor(E2M1, dtype=torch.float64, device="cuda")
+        out = []
+        for x in (st["k"], st["v"]):
+            x = x.double().unflatten(-1, (-1, 16))
+            scale = _nearest(x.abs().amax(-1, keepdim=True) / (6 * c["scale"]), fp8)
+            r = torch.where(scale > 0, x.abs() / (scale * c["scale"]), 0)
+            out.append((_nearest(r, fp4) * x.sign() * scale * c["scale"]).flatten(-2))
+        return tuple(out)
+    rows, before = _rows(c), _before(c)
+    if max(rows, default=0) * max(b + n for b, n in zip(before, rows)) * c["Hq"] * len(rows) > 1 << 31:
+        return None
+    q = st["q"].flatten(0, -3).double()
+    out = torch.empty(*q.shape, dtype=torch.float64, device="cuda")
+    first = 0
+    for b, n in enumerate(rows):
+        if not n:
+            continue
+        end = before[b] + n
+        used = st["cache"][st["table"][b, :-(-end // PAGE)].long()]             # [pages][Hk][72 d]
+        p = torch.arange(before[b], end, device="cuda")
+        for h in range(Hk):
+            kc, vc, ks, vs = (v[:, h].flatten(0, 1)[:end] for v in _views(used))
+            k, v = _exact_values(kc, ks), _exact_values(vc, vs)
+            G = c["Hq"] // Hk
+            s = torch.einsum("tgd,jd->gtj", q[first:first + n, h * G:(h + 1) * G], k) / math.sqrt(d)
+            s = torch.where(_visible(p, end, c["window"], c["sinks"]), s, -math.inf)
+            out[first:first + n, h * G:(h + 1) * G] = torch.einsum("gtj,jd->tgd", torch.softmax(s, -1), v)
+        first += n
+    return out.view(st["q"].shape)
