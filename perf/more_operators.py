@@ -12,8 +12,8 @@ The layers that keep a cache run these entry points of
 and calls the library where it is true.  ``exact`` evaluates the definitions
 in 64 bits.
 
-The cache: pages of 64 tokens, [pages][Hk][72 d] bytes: K codes [64][d / 2],
-V codes, K scales [64][d / 16], V scales.  A code is a 4-bit e2m1 number (the
+The cache: pages of 32 tokens, [pages][Hk][36 d] bytes: K codes [32][d / 2],
+V codes, K scales [32][d / 16], V scales.  A code is a 4-bit e2m1 number (the
 even dimension in the low half of a byte), a scale an e4m3 number for 16
 dimensions: value = code * scale * (k_scale or v_scale).  seq_lens counts the
 tokens before a call's rows, and row t of a sequence sees the tokens up to its
@@ -26,7 +26,7 @@ import torch
 
 own = False
 
-PAGE = 64
+PAGE = 32
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
@@ -178,9 +178,9 @@ def _codes(x, g):
 
 
 def _views(cache):
-    """K codes, V codes, K scales, V scales [pages][Hk][64][...] of the cache's bytes."""
-    d = cache.shape[-1] // 72
-    return [cache[..., a * d:b * d].unflatten(-1, (PAGE, -1)) for a, b in ((0, 32), (32, 64), (64, 68), (68, 72))]
+    """K codes, V codes, K scales, V scales [pages][Hk][32][...] of the cache's bytes."""
+    d = cache.shape[-1] // 36
+    return [cache[..., a * d:b * d].unflatten(-1, (PAGE, -1)) for a, b in ((0, 16), (16, 32), (32, 34), (34, 36))]
 
 
 def _table(case, gen):
@@ -221,7 +221,7 @@ def prepare(case, seed):
     st["cu"] = None
     if c["op"] != "step":
         st["cu"] = torch.tensor([0] + rows).cumsum(0).to(torch.int32).cuda()
-    st["cache"] = cache = torch.empty(n_pages, Hk, 72 * d, dtype=torch.uint8, device="cuda")
+    st["cache"] = cache = torch.empty(n_pages, Hk, 36 * d, dtype=torch.uint8, device="cuda")
     g = c.get("scale", 1.0)
     some = max(1, (1 << 24) // (Hk * PAGE * d))             # pages at a time
     for a in range(0, n_pages, some):
@@ -306,7 +306,7 @@ def _plain_attention(st):
         real = at < st["cu"].long()[1:, None]
         q = q[at.clamp_max(len(q) - 1)]
     B, T = q.shape[:2]
-    used = st["cache"][st["table"].long().clamp_min(0)].transpose(1, 2)         # [B][Hk][pages][72 d]
+    used = st["cache"][st["table"].long().clamp_min(0)].transpose(1, 2)         # [B][Hk][pages][36 d]
     kc, vc, ks, vs = (v.flatten(2, 3) for v in _views(used))
     k, v = _values(kc, ks, 1.0), _values(vc, vs, 1.0)                           # [B][Hk][tokens][d]
     seen = _visible(st["before"].long()[:, None] + torch.arange(T, device="cuda"), k.shape[2], c["window"], c["sinks"])
