@@ -395,7 +395,7 @@ def exact(case, seed):
         if not n:
             continue
         end = before[b] + n
-        used = st["cache"][st["table"][b, :-(-end // PAGE)].long()]             # [pages][Hk][72 d]
+        used = st["cache"][st["table"][b, :-(-end // PAGE)].long()]             # [pages][Hk][36 d]
         p = torch.arange(before[b], end, device="cuda")
         for h in range(Hk):
             kc, vc, ks, vs = (v[:, h].flatten(0, 1)[:end] for v in _views(used))
