@@ -69,6 +69,8 @@ enum sv_status {
 #define SV_DEVERR_SMEM_ALIGN  0x4   /* shared memory not 1024-byte aligned; nothing was computed */
 #define SV_DEVERR_BAD_SLOT    0x8   /* a state_idx entry >= n_slots was skipped */
 #define SV_DEVERR_BAD_SEQLENS 0x10  /* decreasing cu_seqlens claim more blocks than the rows have: taken as empty */
+#define SV_DEVERR_BAD_PAGE    0x20  /* a token without a page of the cache: not appended, read as zero, not attended to */
+#define SV_DEVERR_BAD_AXIS    0x40  /* a rotary axis outside [0, n_axes): axis 0 was taken */
 
 /*
  * w4a16_gemm -- y[t][n] = bf16_rne( sum_g float(scales[n][g]) *
@@ -576,6 +578,109 @@ int gated_delta_chunk(const sv_delta_rows *rows, int R, const int32_t *cu_seqlen
  */
 int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, int T, int K, int F, int act,
                   sv_bf16 *h, sv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Attention layers of a hybrid decoder: rotary positions, a key and value
+ * cache held in 4 bits, and attention over it for decode, verify and prompt
+ * rows.  Conventions as for the calls above (strided rows; no rows, no
+ * launch; of the per-device scratch area only the error word; no gradients).
+ */
+
+#define SV_ROTARY_PAIRED 0x1        /* pairs are (2i, 2i + 1); else (i, i + rot / 2) */
+
+/*
+ * Rotary positions: pair i of every head of a row is turned by the angle
+ *   positions[axes[i]][row] * inv_freq[i]
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
+ * for the first `rot` dimensions; the others are copied.  q [rows][Hq][d] and
+ * k [rows][Hk][d] bf16, rows ldq and ldk apart (either may have no heads);
+ * positions int32 [n_axes][rows], ldp apart; axes int32 [rot / 2] on the
+ * device (NULL: axis 0 for all pairs), so that time, height and width may
+ * turn any pairs, in sections or interleaved; inv_freq fp32 [rot / 2].
+ * q_out may be q, and k_out k (otherwise they must not overlap).  The angle is
+ * reduced exactly, for every 32-bit position (within 2^-24 of a turn for
+ * frequencies up to 1 a step); cos, sin and the products are fp32, rounded
+ * once to bf16.
+ * 16 <= rot <= d <= 1024, rot a multiple of 16, d of 8; 1 <= n_axes <= 16;
+ * the lds of q and k multiples of 8, addresses 16-byte aligned.
+ */
+int rotary_embed(const sv_bf16 *q, long long ldq, int Hq, const sv_bf16 *k, long long ldk, int Hk, int rows, int d, int rot,
+                 const int32_t *positions, long long ldp, int n_axes, const int32_t *axes, const float *inv_freq,
+                 float factor, int flags, sv_bf16 *q_out, long long ldqo, sv_bf16 *k_out, long long ldko, sv_stream stream);
+
+/*
+ * The cache.  A page holds SV_KV4_PAGE tokens of all Hk key/value heads, a
+ * head's part being 36 d bytes:
+ *   K codes [32][d / 2], V codes [32][d / 2], K scales [32][d / 16], V scales [32][d / 16]
+ * A code is an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+ * the even dimension in bits 0..3 of its byte), a scale an e4m3 number for 16
+ * dimensions: value = code * scale * k_scale (v_scale).  Token j of sequence b
+ * is in page page_table[b][j / 32], at j % 32; pages may be in any order and
+ * shared between sequences as long as no call writes a shared one.  An entry
+ * outside 0 .. n_pages - 1 is no page; one that a call needs sets
+ * SV_DEVERR_BAD_PAGE and its tokens are left out.
+ */
+#define SV_KV4_PAGE 32
+
+typedef struct sv_kv4_cache {
+    uint8_t *pages;                        /* [n_pages][Hk][36 d], 16-byte aligned               */
+    const int32_t *page_table;             /* [B][max_pages], rows ldt apart                     */
+    long long ldt;
+    int n_pages, max_pages;                /* max_pages <= 2^24                                  */
+    int Hk, d;                             /* d 64, 128 or 256                                   */
+    float k_scale, v_scale;                /* 1e-30 .. 1e30; a power of two keeps values exact   */
+} sv_kv4_cache;
+
+size_t kv4_page_bytes(int Hk, int d);      /* Hk * 36 * d; 0 when the sizes are invalid          */
+
+/*
+ * The rows of the three calls below are those of B sequences: R / B rows each
+ * when cu_seqlens is NULL (decode and verify rows), else sequence b has rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] (int32 [B + 1] on the device, not
+ * decreasing, within 0..R; a sequence may be empty; rows of no sequence are not
+ * touched).  seq_lens[b] (int32 on the device) counts the tokens before them:
+ * row t of the sequence has position seq_lens[b] + t.  A sequence with a
+ * negative length is inactive: nothing of it is appended, its rows of the
+ * other calls are zeros.  R <= 2^29, B <= 2^20.
+ *
+ * kv4_append puts rows of keys and values, k and v [R][Hk][d] bf16 (rows ldk
+ * and ldv apart, multiples of 8, 16-byte aligned), into the cache: for each 16
+ * dimensions
+ *   scale = e4m3(max|x| / (6 k_scale)), at most 448
+ *   code  = e2m1(x / (k_scale * scale)), 0 where the scale is 0
+ * both to the nearest, ties to even.  16 dimensions that hold a NaN or an
+ * infinity get a NaN scale (they read as NaN), and the token's first K scale
+ * of that head too.  No other byte of the cache is written.  Two rows of a call
+ * must not have the same place.
+ *
+ * kv4_gather reads rows back as bf16, one rounding of code * scale * k_scale.
+ */
+int kv4_append(const sv_bf16 *k, long long ldk, const sv_bf16 *v, long long ldv, int R, const int32_t *cu_seqlens,
+               const int32_t *seq_lens, int B, const sv_kv4_cache *cache, sv_stream stream);
+int kv4_gather(sv_bf16 *k, long long ldk, sv_bf16 *v, long long ldv, int R, const int32_t *cu_seqlens,
+               const int32_t *seq_lens, int B, const sv_kv4_cache *cache, sv_stream stream);
+
+/*
+ * Attention of R query rows over the cache, which holds their own tokens
+ * already (kv4_append): query head h uses key/value head h / (Hq / Hk),
+ *   o = sum_j p_j v_j,  p = softmax over the visible j of scale * (q . k_j)
+ * Position p sees tokens j <= p; with a window > 0 only those with
+ * p - j < window or j < sinks.  A row that sees no token gives zeros.  q, o
+ * [R][Hq][d] bf16, rows ldq and ldo apart (multiples of 8, 16-byte aligned; o
+ * must not overlap q).  Scores, their softmax and sums are fp32; keys and values are
+ * exact in the products, the probabilities in them fp16.  A token with a NaN
+ * scale among its K scales makes the rows that see it NaN, others not; NaN V
+ * scales alone count as 448.
+ * `ws` is device memory of at least kv4_attention_bytes (0 when the sizes are
+ * invalid; `ragged`: cu_seqlens is given), 16-byte aligned, free until the
+ * call has run; calls that may overlap need one each.  R * (Hq / Hk) <= 2^29.
+ * Results do not depend on timing.  Decreasing cu_seqlens that claim more
+ * rows than R set SV_DEVERR_BAD_SEQLENS, and nothing is written.
+ */
+size_t kv4_attention_bytes(int R, int B, int ragged, int Hq, const sv_kv4_cache *cache);
+int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t *cu_seqlens, const int32_t *seq_lens, int B,
+                  const sv_kv4_cache *cache, float scale, int window, int sinks, sv_bf16 *o, long long ldo, void *ws,
+                  size_t ws_bytes, sv_stream stream);
 
 #ifdef __cplusplus
 }

@@ -14,8 +14,8 @@ import re
 
 from . import build as _build
 from . import layer as _layer
-from .layer import (gated_delta_chunk, gated_delta_step, rmsnorm, rmsnorm_fp8,  # noqa: F401
-                    w4a16_gate_up)
+from .layer import (KV4_PAGE, gated_delta_chunk, gated_delta_step, kv4_append, kv4_attention,  # noqa: F401
+                    kv4_cache, kv4_gather, rmsnorm, rmsnorm_fp8, rotary, w4a16_gate_up)
 
 SV_OK = 0
 STATUS = {0: "SV_OK", -1: "SV_ERR_NULL", -2: "SV_ERR_SHAPE", -3: "SV_ERR_ALIGN",
@@ -24,6 +24,8 @@ DEVERR_BAD_MAP_ID = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_BAD_SLOT = 0x8
 DEVERR_BAD_SEQLENS = 0x10
+DEVERR_BAD_PAGE = 0x20
+DEVERR_BAD_AXIS = 0x40
 
 _lib = None
 

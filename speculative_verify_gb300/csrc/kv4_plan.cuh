@@ -1,0 +1,264 @@
+// kv4_plan.cuh -- how the attention kernels share out their work, and the
+// kernel that joins what they leave in parts.
+//
+// Query rows are packed: row r of a sequence and key/value head is token
+// r / G, query head r % G of the head's G.  An item is a tile of packed rows of
+// one head; its units are the pages that some row of the tile sees (the pages
+// of the first tokens, then those of the window).  The items of head 0, then
+// head 1 and so on make one line of units, cut into equal parts, one for a
+// thread block: uneven sequences and triangles of prompts cost no balance, and
+// one long sequence is spread over the whole GPU.
+//
+// A block whose part holds an item whole writes its outputs; of an item that
+// goes on into other parts each block leaves its sums, unnormalised, with
+// their maximum: the block where the item starts in its slot 1, the others in
+// their slot 0.  kv4_join_kernel adds them in the parts' order, so results are
+// the same every time.  Nothing has to be cleared first and no atomic is
+// involved: calls with workspaces of their own may overlap, in graphs too.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kv4.cuh"
+
+namespace sv {
+
+struct KvAttnParams {
+    KvRows rows;
+    KvPages kv;
+    const uint16_t *q;
+    uint16_t *o;
+    long long ldq, ldo;
+    int G;                                      // query heads of a key/value head
+    int tile;                                   // packed rows of an item
+    float scale;                                // of scores, with k_scale and log2 e
+    float v_scale;
+    int window, sinks;                          // 0: no window
+    int least;                                  // units of a part at least
+    float *sums, *stats;                        // [2 parts][tile][d], [2 parts][tile][2]
+    int4 *joins;                                // [parts]
+    int *err;
+};
+
+// A sequence's rows, and the position of its first one (negative: inactive).
+struct KvSeq {
+    int first = 0, n = 0, before = 0;
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b)
+{
+    KvSeq s;
+    int end;
+    p.rows.range(b, s.first, end);
+    s.n = end - s.first;
+    s.before = min(p.rows.lens[b], p.kv.max_pages * KV_PAGE);
+    return s;
+}
+
+// A tile's visible pages: 0 .. sinks - 1, then from .. to - 1.
+struct KvSpan {
+    int sinks, from, to;
+    __device__ __forceinline__ int units() const { return max(1, sinks + to - from); }
+    __device__ __forceinline__ int page(int u) const { return u < sinks ? u : from + u - sinks; }
+};
+
+__device__ __forceinline__ int kv_tiles(const KvAttnParams &p, const KvSeq &s) { return (s.n * p.G + p.tile - 1) / p.tile; }
+
+__device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, const KvSeq &s, int tile)
+{
+    if (s.before < 0) return KvSpan{0, 0, 0};   // (one unit of no page)
+    const int t0 = tile * p.tile / p.G, t1 = (min((tile + 1) * p.tile, s.n * p.G) - 1) / p.G;
+    const int lo = p.window > 0 ? max(0, s.before + t0 - p.window + 1) : 0;
+    const int to = min((s.before + t1) / KV_PAGE + 1, p.kv.max_pages);
+    const int sinks = min((min(p.sinks, lo) + KV_PAGE - 1) / KV_PAGE, to);
+    return KvSpan{sinks, min(max(sinks, lo / KV_PAGE), to), to};
+}
+
+// An item, and a unit of it.
+struct KvItem {
+    int h, b, tile, unit;
+    KvSeq seq;
+    KvSpan span;
+};
+
+// Called by whole warps.  Units of one head's items; with `want` >= 0 also
+// the item, with the unit in it, that holds unit `want` of the head.
+__device__ __forceinline__ long long kv_line(const KvAttnParams &p, long long want, KvItem *found)
+{
+    const int lane = threadIdx.x & 31;
+    long long total = 0, rows = 0;
+    for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
+        const KvSeq mine = b0 + lane < p.rows.B ? kv_seq(p, b0 + lane) : KvSeq{};
+        const int tiles = kv_tiles(p, mine);
+        rows += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) & 0xFFFFu) +
+                (static_cast<long long>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) >> 16)) << 16);
+        if (rows > p.rows.R) {                  // cu_seqlens that decrease
+            if (lane == 0) atomicOr(p.err, KV_ERR_SEQLENS);
+            return 0;
+        }
+        // long sequences one after another, their tiles over the lanes; short
+        // ones side by side
+        const bool one = __reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tiles)) > 32u;
+        for (int s = 0; s < (one ? 32 : 1); ++s) {
+            KvSeq seq = mine;
+            int n = 1;                          // rounds
+            if (one) {
+                seq.first = __shfl_sync(0xFFFFFFFFu, mine.first, s);
+                seq.n = __shfl_sync(0xFFFFFFFFu, mine.n, s);
+                seq.before = __shfl_sync(0xFFFFFFFFu, mine.before, s);
+                n = (kv_tiles(p, seq) + 31) / 32;
+            }
+            for (int k = 0; k < n; ++k) {
+                long long units = 0;
+                if (one) {
+                    const int t = 32 * k + lane;
+                    if (t < kv_tiles(p, seq)) units = kv_span(p, seq, t).units();
+                } else {
+                    for (int t = 0; t < tiles; ++t) units += kv_span(p, seq, t).units();
+                }
+                long long run = units;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long below = __shfl_up_sync(0xFFFFFFFFu, run, o);
+                    if (lane >= o) run += below;
+                }
+                const unsigned past = want >= 0 ? __ballot_sync(0xFFFFFFFFu, total + run > want) : 0u;
+                if (past) {
+                    const int w = __ffs(past) - 1;
+                    long long rest = want - total - __shfl_sync(0xFFFFFFFFu, run - units, w);
+                    found->b = one ? b0 + s : b0 + w;
+                    found->seq.first = __shfl_sync(0xFFFFFFFFu, seq.first, w);
+                    found->seq.n = __shfl_sync(0xFFFFFFFFu, seq.n, w);
+                    found->seq.before = __shfl_sync(0xFFFFFFFFu, seq.before, w);
+                    found->tile = one ? 32 * k + w : 0;
+                    found->span = kv_span(p, found->seq, found->tile);
+                    while (rest >= found->span.units()) {
+                        rest -= found->span.units();
+                        found->span = kv_span(p, found->seq, ++found->tile);
+                    }
+                    found->unit = static_cast<int>(rest);
+                    return total;
+                }
+                total += __shfl_sync(0xFFFFFFFFu, run, 31);
+            }
+        }
+    }
+    return total;
+}
+
+// A block's part of the line: the units that are left, and the item they are in.
+struct KvPart {
+    long long left = 0, share = 0;
+    KvItem item;
+
+    // Part k of `parts` (whole warps call it).
+    __device__ __forceinline__ void start(const KvAttnParams &p, int k, int parts)
+    {
+        const long long line = kv_line(p, -1, nullptr), all = line * p.kv.Hk;
+        share = max(static_cast<long long>(p.least), (all + parts - 1) / parts);
+        const long long lo = min(share * k, all);
+        left = min(share, all - lo);
+        if (left <= 0) return;
+        item.h = static_cast<int>(lo / line);
+        kv_line(p, lo - item.h * line, &item);
+    }
+    // Units of the item in this part.
+    __device__ __forceinline__ int units() const
+    {
+        return static_cast<int>(min(left, static_cast<long long>(item.span.units() - item.unit)));
+    }
+    // To the next item, whose units begin here.
+    __device__ __forceinline__ void next(const KvAttnParams &p)
+    {
+        left -= units();
+        if (left <= 0) return;
+        item.unit = 0;
+        if (++item.tile >= kv_tiles(p, item.seq)) {
+            item.tile = 0;
+            do {
+                if (++item.b == p.rows.B) {
+                    item.b = 0;
+                    if (++item.h == p.kv.Hk) {  // (lengths written meanwhile)
+                        left = 0;
+                        return;
+                    }
+                }
+                item.seq = kv_seq(p, item.b);
+            } while (item.seq.n <= 0);
+        }
+        item.span = kv_span(p, item.seq, item.tile);
+    }
+    __device__ __forceinline__ bool whole() const { return item.unit == 0 && units() == item.span.units(); }
+    // Whether the item starts here, and goes on in this many parts in all.
+    __device__ __forceinline__ int parts() const
+    {
+        return item.unit ? 0 : 1 + static_cast<int>((item.span.units() - units() + share - 1) / share);
+    }
+};
+
+constexpr int KJ_THREADS = 128;
+constexpr int KJ_VALUES = 4 * KJ_THREADS;       // output values of a block
+constexpr int KJ_MAX_PARTS = 1024;
+
+// Block (p, s): values s KJ_VALUES .. of the item that starts in part p and
+// goes on, joined from its parts.
+template <int D>
+__global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams p)
+{
+    constexpr int ROWS = KJ_VALUES / D;
+    __shared__ float weight[ROWS][KJ_MAX_PARTS];
+    __shared__ float norm[ROWS];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int part = blockIdx.x, row0 = blockIdx.y * ROWS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 join = p.joins[part];            // parts; head, sequence, tile
+    if (join.x < 2) return;
+    const KvSeq seq = kv_seq(p, join.z);
+    const int rows = min(p.tile, seq.n * p.G - join.w * p.tile), n = join.x;
+    if (row0 >= rows) return;
+    auto slot = [&](int i) { return static_cast<long long>(2 * (part + i) + (i == 0)) * p.tile; };
+    for (int r = warp; r < ROWS; r += KJ_THREADS / 32) {
+        if (row0 + r >= rows) continue;
+        const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + row0 + r;
+        float top = -INFINITY;
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(stats + slot(i)).x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (top == -INFINITY) top = 0.f;
+        float total = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float2 s = __ldcg(stats + slot(i));
+            const float w = exp2f(s.x - top);
+            weight[r][i] = w;
+            total += w * s.y;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        if (lane == 0) norm[r] = total == 0.f ? 0.f : p.v_scale / total;
+    }
+    __syncthreads();
+    const int r = 4 * threadIdx.x / D, d = 4 * threadIdx.x % D, row = row0 + r;
+    if (row >= rows) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *sums = p.sums + static_cast<long long>(row) * D + d;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float4 v = ldcg_f4(sums + slot(i) * D);
+        const float w = weight[r][i];
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+    }
+    const int packed = join.w * p.tile + row, t = packed / p.G, g = packed - t * p.G;
+    uint16_t *o = p.o + (seq.first + t) * p.ldo + static_cast<long long>(join.y * p.G + g) * D + d;
+    const float f = norm[r];
+    uint2 out;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.x) : "f"(acc.y * f), "f"(acc.x * f));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.y) : "f"(acc.w * f), "f"(acc.z * f));
+    *reinterpret_cast<uint2 *>(o) = out;
+}
+
+}  // namespace sv

@@ -490,6 +490,222 @@ PyObject *w4a16_gate_up(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------- attention layers
+
+// Rows of heads, [T][H][d] or [B][T][H][d]: their number and distance.
+struct HeadRows {
+    int64_t rows = 0, heads = 0, d = 0;
+    long long ld = 0;
+    const at::Tensor *t = nullptr;
+
+    HeadRows() = default;
+    HeadRows(const at::Tensor &x, const char *name) : t(&x)
+    {
+        if (x.dim() != 3 && x.dim() != 4) fail(PyExc_ValueError, "%s must be [T][heads][d] or [B][T][heads][d]", name);
+        heads = x.size(-2);
+        d = x.size(-1);
+        if (x.dim() == 3) {
+            rows = x.size(0);
+            ld = row_distance(x, 1, {rows, heads, d}, name);
+        } else {
+            rows = x.size(0) * x.size(1);
+            ld = row_distance(x, 2, {x.size(0), x.size(1), heads, d}, name);
+        }
+    }
+    // Rows of the same shape as `like`, `heads` heads.
+    HeadRows(const at::Tensor &x, const char *name, const at::Tensor &like, int64_t heads_) : HeadRows(x, name)
+    {
+        if (x.dim() != like.dim() || x.size(0) != like.size(0) || (x.dim() == 4 && x.size(1) != like.size(1)) ||
+            heads != heads_ || d != like.size(-1))
+            fail(PyExc_ValueError, "%s must have the same rows and dimensions", name);
+    }
+};
+
+// (q, k, positions, inv_freq, axes, interleaved, factor, q_out, k_out, stream); k may be None
+PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        arguments("rotary", n, 10);
+        Where on;
+        const HeadRows q(tensor(a[0], "q", BF16, on), "q");
+        const HeadRows k = a[1] == Py_None ? HeadRows() : HeadRows(tensor(a[1], "k", BF16, on), "k");
+        if (k.t && (k.t->dim() != q.t->dim() || k.rows != q.rows || k.t->size(0) != q.t->size(0) || k.d != q.d))
+            fail(PyExc_ValueError, "k must have the rows and dimensions of q");
+        const at::Tensor &freq = tensor(a[3], "inv_freq", F32, on);
+        if (freq.dim() != 1 || !freq.is_contiguous()) fail(PyExc_ValueError, "inv_freq must be contiguous [rot / 2]");
+        const at::Tensor &pos = tensor(a[2], "positions", at::kInt, on);
+        if (!pos.is_contiguous()) fail(PyExc_TypeError, "positions must be contiguous");
+        // [axes] and the rows' dimensions, or those alone
+        const int64_t lead = q.t->dim() - 2;
+        if (pos.dim() != lead && pos.dim() != lead + 1) fail(PyExc_ValueError, "positions must be one for each row, or [axes] of them");
+        const bool many = pos.dim() == lead + 1;
+        for (int64_t i = 0; i < lead; ++i)
+            if (pos.size(i + many) != q.t->size(i)) fail(PyExc_ValueError, "positions must be one for each row, or [axes] of them");
+        const int64_t axes = many ? pos.size(0) : 1;
+        const int32_t *axis = nullptr;
+        if (a[4] != Py_None) {
+            const at::Tensor &t = tensor(a[4], "axes", at::kInt, on);
+            if (!t.is_contiguous() || t.numel() != freq.numel()) fail(PyExc_ValueError, "axes must have one entry per frequency");
+            axis = ptr<const int32_t>(t);
+        }
+        const Stream stream(a[9], *q.t);
+        const at::Tensor qo = output(a[7], "q_out", q.t->sizes(), *q.t, BF16, on);
+        const HeadRows to(qo, "q_out", *q.t, q.heads);
+        if (!k.t && a[8] != Py_None) fail(PyExc_ValueError, "k_out without k");
+        at::Tensor ko;
+        HeadRows kto;
+        if (k.t) {
+            ko = output(a[8], "k_out", k.t->sizes(), *k.t, BF16, on);
+            kto = HeadRows(ko, "k_out", *k.t, k.heads);
+        }
+        check_status("rotary_embed",
+                     rotary_embed(ptr<const sv_bf16>(*q.t), q.ld, count(q.heads, "heads"), k.t ? ptr<const sv_bf16>(*k.t) : nullptr,
+                                  k.ld, count(k.heads, "heads"), count(q.rows, "rows"), count(q.d, "dimensions"),
+                                  count(2 * freq.numel(), "frequencies"), ptr<const int32_t>(pos), q.rows, count(axes, "axes"),
+                                  axis, ptr<const float>(freq), static_cast<float>(real(a[6])), truth(a[5]) ? SV_ROTARY_PAIRED : 0,
+                                  ptr<sv_bf16>(qo), to.ld, k.t ? ptr<sv_bf16>(ko) : nullptr, kto.ld, stream.raw));
+        if (!k.t) return Py_BuildValue("(NO)", wrap(a[7], qo), Py_None);
+        return Py_BuildValue("(NN)", wrap(a[7], qo), wrap(a[8], ko));
+    } catch (const PyFail &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// The cache of a call, its sequences' pages and lengths.
+struct Cache {
+    sv_kv4_cache c{};
+    const int32_t *lens = nullptr, *cu = nullptr;
+    bool ragged = false;                        // cu_seqlens is given
+    int64_t B = 0;
+
+    Cache(PyObject *cache, PyObject *table, PyObject *lens_, PyObject *cu_, PyObject *k_scale, PyObject *v_scale, Where &on)
+    {
+        const at::Tensor &t = tensor(cache, "cache", at::kByte, on);
+        if (t.dim() != 3 || !t.is_contiguous()) fail(PyExc_TypeError, "cache must be contiguous [pages][Hk][36 d]");
+        if (t.size(2) % 36) fail(PyExc_ValueError, "cache must be [pages][Hk][36 d]");
+        const at::Tensor &pt = tensor(table, "page_table", at::kInt, on);
+        if (pt.dim() != 2) fail(PyExc_TypeError, "page_table must be [B][pages]");
+        B = pt.size(0);
+        c.pages = ptr<uint8_t>(t);
+        c.page_table = ptr<const int32_t>(pt);
+        c.ldt = row_distance(pt, 1, {B, pt.size(1)}, "page_table");
+        c.n_pages = count(t.size(0), "pages");
+        c.max_pages = count(pt.size(1), "pages");
+        c.Hk = count(t.size(1), "heads");
+        c.d = count(t.size(2) / 36, "dimensions");
+        c.k_scale = static_cast<float>(real(k_scale));
+        c.v_scale = static_cast<float>(real(v_scale));
+        lens = indices(lens_, "seq_lens", on, B);
+        if ((ragged = cu_ != Py_None)) {
+            cu = indices(cu_, "cu_seqlens", on);
+            if (THPVariable_Unpack(cu_).numel() != B + 1) fail(PyExc_ValueError, "cu_seqlens must have B + 1 entries");
+        }
+    }
+    // The rows of x, [R][heads][d] with cu_seqlens, [B][T][heads][d] without.
+    HeadRows rows(const at::Tensor &x, const char *name, int64_t heads) const
+    {
+        const HeadRows r(x, name);
+        if (x.dim() != (ragged ? 3 : 4)) fail(PyExc_ValueError, "%s must be %s", name, ragged ? "[R][heads][d]" : "[B][T][heads][d]");
+        if (!ragged && x.size(0) != B) fail(PyExc_ValueError, "%s must have as many sequences as page_table", name);
+        if (heads >= 0 && r.heads != heads) fail(PyExc_ValueError, "%s must have the cache's heads", name);
+        if (r.d != c.d) fail(PyExc_ValueError, "%s must have the cache's dimensions", name);
+        return r;
+    }
+};
+
+// (k, v, cache, page_table, seq_lens, cu_seqlens, k_scale, v_scale, stream)
+PyObject *kv4_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        arguments("kv4_append", n, 9);
+        Where on;
+        const at::Tensor &k = tensor(a[0], "k", BF16, on), &v = tensor(a[1], "v", BF16, on);
+        const Cache c(a[2], a[3], a[4], a[5], a[6], a[7], on);
+        const HeadRows kr = c.rows(k, "k", c.c.Hk), vr = c.rows(v, "v", c.c.Hk);
+        if (kr.rows != vr.rows) fail(PyExc_ValueError, "k and v must have as many rows");
+        const Stream stream(a[8], k);
+        check_status("kv4_append", ::kv4_append(ptr<const sv_bf16>(k), kr.ld, ptr<const sv_bf16>(v), vr.ld, count(kr.rows, "rows"),
+                                                c.cu, c.lens, count(c.B, "sequences"), &c.c, stream.raw));
+        Py_RETURN_NONE;
+    } catch (const PyFail &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (cache, page_table, seq_lens, rows, cu_seqlens, k_scale, v_scale, k, v, stream); rows: T, or R with cu_seqlens
+PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        arguments("kv4_gather", n, 10);
+        Where on;
+        const Cache c(a[0], a[1], a[2], a[4], a[5], a[6], on);
+        const at::Tensor &t = THPVariable_Unpack(a[0]);
+        const long rows = PyLong_AsLong(a[3]);
+        if (rows == -1 && PyErr_Occurred()) throw PyFail{};
+        if (rows < 0 || rows > 0x7FFFFFFF) fail(PyExc_ValueError, "rows must not be negative");
+        const Stream stream(a[9], t);
+        const int64_t four[4] = {c.B, rows, c.c.Hk, c.c.d}, three[3] = {rows, c.c.Hk, c.c.d};
+        const at::IntArrayRef shape = c.ragged ? at::IntArrayRef(three, 3) : at::IntArrayRef(four, 4);
+        const at::Tensor k = output(a[7], "k", shape, t, BF16, on), v = output(a[8], "v", shape, t, BF16, on);
+        const HeadRows kr = c.rows(k, "k", c.c.Hk), vr = c.rows(v, "v", c.c.Hk);
+        const int64_t R = c.ragged ? rows : c.B * rows;
+        if (kr.rows != R || vr.rows != R) fail(PyExc_ValueError, "k and v must have as many rows");
+        check_status("kv4_gather", ::kv4_gather(ptr<sv_bf16>(k), kr.ld, ptr<sv_bf16>(v), vr.ld, count(R, "rows"), c.cu, c.lens,
+                                                count(c.B, "sequences"), &c.c, stream.raw));
+        return Py_BuildValue("(NN)", wrap(a[7], k), wrap(a[8], v));
+    } catch (const PyFail &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, cache, page_table, seq_lens, cu_seqlens, scale, window, sinks, k_scale, v_scale, o, workspace, stream)
+PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        arguments("kv4_attention", n, 13);
+        Where on;
+        const at::Tensor &q = tensor(a[0], "q", BF16, on);
+        const Cache c(a[1], a[2], a[3], a[4], a[8], a[9], on);
+        const HeadRows r = c.rows(q, "q", -1);
+        if (r.heads < 1 || c.c.Hk < 1 || r.heads % c.c.Hk) fail(PyExc_ValueError, "the heads of q must be a multiple of the cache's");
+        const long window = PyLong_AsLong(a[6]);
+        if (window == -1 && PyErr_Occurred()) throw PyFail{};
+        const long sinks = PyLong_AsLong(a[7]);
+        if (sinks == -1 && PyErr_Occurred()) throw PyFail{};
+        if (window < 0 || window > 1 << 30 || sinks < 0 || sinks > 1 << 30) fail(PyExc_ValueError, "window and sinks must be 0 .. 2^30");
+        const double scale = a[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.c.d)) : real(a[5]);
+        const Stream stream(a[12], q);
+        const at::Tensor o = output(a[10], "o", q.sizes(), q, BF16, on);
+        const HeadRows to(o, "o", q, r.heads);
+        const int R = count(r.rows, "rows"), B = count(c.B, "sequences"), Hq = count(r.heads, "heads");
+        if (R && B) {
+            at::Tensor ws;
+            if (a[11] == Py_None) {
+                const size_t need = kv4_attention_bytes(R, B, c.ragged, Hq, &c.c);
+                ws = make({static_cast<int64_t>(need < 16 ? 16 : need)}, q, at::kByte);
+            } else {
+                ws = tensor(a[11], "workspace", at::kByte, on);
+                if (!ws.is_contiguous()) fail(PyExc_TypeError, "workspace must be contiguous");
+            }
+            check_status("kv4_attention",
+                         ::kv4_attention(ptr<const sv_bf16>(q), r.ld, R, Hq, c.cu, c.lens, B, &c.c, static_cast<float>(scale),
+                                         static_cast<int>(window), static_cast<int>(sinks), ptr<sv_bf16>(o), to.ld, ws.data_ptr(),
+                                         static_cast<size_t>(ws.numel()), stream.raw));
+        }
+        return wrap(a[10], o);
+    } catch (const PyFail &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 // (SpecVerifyError)
 PyObject *set_error(PyObject *, PyObject *type)
 {
@@ -500,7 +716,8 @@ PyObject *set_error(PyObject *, PyObject *type)
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(rmsnorm), FAST(rmsnorm_fp8), FAST(gated_delta_step), FAST(gated_delta_chunk),
-                           FAST(w4a16_gate_up), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                           FAST(w4a16_gate_up), FAST(rotary), FAST(kv4_append), FAST(kv4_gather), FAST(kv4_attention),
+                           {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer", "Calls between the weight reads, on torch tensors.", -1,
                         g_methods, nullptr, nullptr, nullptr, nullptr};
 

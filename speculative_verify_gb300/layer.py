@@ -1,6 +1,6 @@
 """What a hybrid decoder layer runs between its weight reads: residual norm,
-gated delta rule and gated feed-forward (the second half of
-``include/specverify.h``).
+gated delta rule or attention over a 4-bit cache, and gated feed-forward (the
+second half of ``include/specverify.h``).
 
 Signatures and documentation; the argument checks, the outputs' allocation and
 the calls are in ``csrc/layer_bind.cpp`` (native, as each call is only a few
@@ -55,6 +55,13 @@ class DeltaShape(ctypes.Structure):
                 ("scale", ctypes.c_float), ("flags", ctypes.c_int)]
 
 
+class Kv4Cache(ctypes.Structure):
+    """sv_kv4_cache of include/specverify.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("ldt", ctypes.c_longlong),
+                ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 def declare(lib) -> None:
     """The C signatures of this module's calls."""
     vp, ci, cl, cf, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
@@ -71,6 +78,19 @@ def declare(lib) -> None:
     lib.gated_delta_chunk.restype = ci
     lib.w4a16_gate_up.argtypes = [vp, vp, vp, ci, ci, ci, ci, vp, vp]
     lib.w4a16_gate_up.restype = ci
+    cache = ctypes.POINTER(Kv4Cache)
+    lib.rotary_embed.argtypes = [vp, cl, ci, vp, cl, ci, ci, ci, ci, vp, cl, ci, vp, vp, cf, ci, vp, cl, vp, cl, vp]
+    lib.rotary_embed.restype = ci
+    lib.kv4_page_bytes.argtypes = [ci, ci]
+    lib.kv4_page_bytes.restype = sz
+    lib.kv4_append.argtypes = [vp, cl, vp, cl, ci, vp, vp, ci, cache, vp]
+    lib.kv4_append.restype = ci
+    lib.kv4_gather.argtypes = [vp, cl, vp, cl, ci, vp, vp, ci, cache, vp]
+    lib.kv4_gather.restype = ci
+    lib.kv4_attention_bytes.argtypes = [ci, ci, ci, ci, cache]
+    lib.kv4_attention_bytes.restype = sz
+    lib.kv4_attention.argtypes = [vp, cl, ci, ci, vp, vp, ci, cache, cf, ci, ci, vp, cl, vp, sz, vp]
+    lib.kv4_attention.restype = ci
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6, unit_offset=False, y=None, residual_out=None, stream=None):
@@ -138,3 +158,66 @@ def w4a16_gate_up(x, Wq, scales, act="silu", h=None, stream=None):
     if act not in ACTS:
         raise ValueError("act must be one of %s" % sorted(ACTS))
     return _ext.w4a16_gate_up(x, Wq, scales, ACTS[act], h, stream)
+
+
+def rotary(q, k, positions, inv_freq, axes=None, interleaved=False, factor=1.0, q_out=None, k_out=None, stream=None):
+    """(q', k'): rotary positions into the first 2 * len(inv_freq) dimensions
+    of every head (``rotary_embed`` in include/specverify.h).
+
+    q, k: [T][H][d] or [B][T][H][d] bf16 (k may be None); positions: int32, one
+    for each row, or [axes] of them (time, height, width); axes: int32
+    [len(inv_freq)], the axis that each pair turns by (None: the first for
+    all).  Pairs are (i, i + half), with interleaved=True (2i, 2i + 1).
+    q_out=q and k_out=k rotate in place."""
+    if _ext is None:
+        _load()
+    return _ext.rotary(q, k, positions, inv_freq, axes, interleaved, factor, q_out, k_out, stream)
+
+
+KV4_PAGE = 32                           # tokens of a page
+
+
+def kv4_cache(n_pages, Hk, d, device="cuda"):
+    """Zeroed pages of a 4-bit cache: uint8 [n_pages][Hk][36 d], 32 tokens a
+    page (the format is in include/specverify.h); d 64, 128 or 256."""
+    import torch
+    return torch.zeros(n_pages, Hk, 36 * d, dtype=torch.uint8, device=device)
+
+
+def kv4_append(k, v, cache, page_table, seq_lens, cu_seqlens=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """Rows of keys and values into the 4-bit cache, in place.
+
+    k, v: [B][T][Hk][d] bf16, or [R][Hk][d] with cu_seqlens (int32 [B + 1]);
+    page_table: int32 [B][pages]; seq_lens: int32 [B], the tokens before these
+    rows (negative: the sequence is left alone).  k_scale, v_scale: what the
+    cache's values are multiples of, the same for every call on a cache."""
+    if _ext is None:
+        _load()
+    return _ext.kv4_append(k, v, cache, page_table, seq_lens, cu_seqlens, k_scale, v_scale, stream)
+
+
+def kv4_gather(cache, page_table, seq_lens, rows, cu_seqlens=None, k_scale=1.0, v_scale=1.0, k=None, v=None, stream=None):
+    """(k, v): rows of the cache as bf16, [B][rows][Hk][d] from position
+    seq_lens on, or [rows][Hk][d] with cu_seqlens (rows: their number in all;
+    rows of no sequence are not written)."""
+    if _ext is None:
+        _load()
+    return _ext.kv4_gather(cache, page_table, seq_lens, rows, cu_seqlens, k_scale, v_scale, k, v, stream)
+
+
+def kv4_attention(q, cache, page_table, seq_lens, cu_seqlens=None, scale=None, window=0, sinks=0, k_scale=1.0,
+                  v_scale=1.0, o=None, workspace=None, stream=None):
+    """Causal attention of query rows over the 4-bit cache, which holds the
+    rows' own tokens already (``kv4_attention`` in include/specverify.h);
+    returns o, of q's shape.
+
+    q: [B][T][Hq][d] bf16 (decode and verify rows), or [R][Hq][d] with
+    cu_seqlens (prompts of uneven lengths); row t of sequence b sees the tokens
+    up to seq_lens[b] + t, with a window only the last `window` of them and the
+    first `sinks` of the sequence.  A sequence of negative length gives zeros.
+    scale defaults to d ** -0.5.  workspace: a uint8 CUDA tensor of
+    kv4_attention_bytes, else one is allocated."""
+    if _ext is None:
+        _load()
+    return _ext.kv4_attention(q, cache, page_table, seq_lens, cu_seqlens, scale, window, sinks, k_scale, v_scale, o,
+                              workspace, stream)
