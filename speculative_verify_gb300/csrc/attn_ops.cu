@@ -7,6 +7,7 @@
 
 #include "kv4.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_attn_tc.cuh"
 #include "kv4_plan.cuh"
 #include "rotary.cuh"
 #include "specverify.h"
@@ -35,6 +36,11 @@ int attn_device(DeviceInfo *out)
     up(kv4_attn_kernel<64>, KaShape<64>::BYTES);
     up(kv4_attn_kernel<128>, KaShape<128>::BYTES);
     up(kv4_attn_kernel<256>, KaShape<256>::BYTES);
+    up(kv4_attn_tc_kernel<64, 1>, KtSmem<64, 1>::BYTES);
+    up(kv4_attn_tc_kernel<64, 2>, KtSmem<64, 2>::BYTES);
+    up(kv4_attn_tc_kernel<128, 1>, KtSmem<128, 1>::BYTES);
+    up(kv4_attn_tc_kernel<128, 2>, KtSmem<128, 2>::BYTES);
+    up(kv4_attn_tc_kernel<256, 1>, KtSmem<256, 1>::BYTES);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return SV_ERR_CUDA;
@@ -129,24 +135,33 @@ int kv_rows_call(uint16_t *k, long long ldk, uint16_t *v, long long ldv, int R, 
 
 // ------------------------------------------------------------ attention
 
-// How a call's work is cut: packed rows of an item, parts at most, units of a
-// part at least.
+// How a call's work is cut: the kernel (0: kv4_attn_kernel, else the tiles of
+// kv4_attn_tc_kernel), packed rows of an item, tokens of a unit, parts at most,
+// units of a part at least.
 struct AttnPlan {
-    int tile, parts, least;
+    int tiles, tile, unit, parts, least;
     bool joins;                                 // an item may go over several parts
 };
 
-AttnPlan attn_plan(int R, int B, bool ragged, int G, int d, int Hk, int max_pages, int sms)
+// The parts are counted for a GPU of this size whatever the device, so that
+// the workspace's size does not ask the device.
+constexpr int ATTN_SMS = 152;
+
+AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
 {
     AttnPlan a{};
-    a.tile = KA_ROWS;
-    a.least = 2 * KA_WARPS;
-    const int blocks = d == 64 ? KaShape<64>::BLOCKS : d == 128 ? KaShape<128>::BLOCKS : KaShape<256>::BLOCKS;
+    // packed rows of a sequence, on average where they are uneven
+    const long long packed = (1LL * R * G + B - 1) / B;
+    a.tiles = packed <= KA_ROWS ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
+    a.tile = a.tiles ? a.tiles * KT_ROWS : KA_ROWS;
+    a.unit = a.tiles ? KT_UNIT : KV_PAGE;
+    a.least = a.tiles ? 2 : 2 * KA_WARPS;
+    const int blocks = a.tiles ? 1 : d == 64 ? KaShape<64>::BLOCKS : d == 128 ? KaShape<128>::BLOCKS : KaShape<256>::BLOCKS;
     // (items, and their units, at most)
-    const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B), units = items * std::max(1, max_pages);
-    a.parts = static_cast<int>(std::min<long long>(1LL * sms * blocks, (units + a.least - 1) / a.least));
-    a.joins = a.parts > 1 && max_pages > 1;
-    (void)ragged;
+    const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);
+    const long long units = items * std::max(1, (max_pages * KV_PAGE + a.unit - 1) / a.unit);
+    a.parts = static_cast<int>(std::min<long long>(1LL * ATTN_SMS * blocks, (units + a.least - 1) / a.least));
+    a.joins = a.parts > 1 && max_pages * KV_PAGE > a.unit;
     return a;
 }
 
@@ -162,10 +177,6 @@ struct AttnSpace {
     }
 };
 
-// The parts are counted for a GPU of this size whatever the device, so that
-// the workspace's size does not ask the device.
-constexpr int ATTN_SMS = 152;
-
 int check_attention(int R, int B, int Hq, const sv_kv4_cache *c)
 {
     if (Hq < 1 || Hq % c->Hk || 1LL * R * (Hq / c->Hk) > (1 << 29)) return SV_ERR_SHAPE;
@@ -175,7 +186,16 @@ int check_attention(int R, int B, int Hq, const sv_kv4_cache *c)
 template <int D>
 int attn_launch(const KvAttnParams &p, const AttnPlan &a, cudaStream_t stream)
 {
-    int rc = launch(kv4_attn_kernel<D>, dim3(static_cast<unsigned>(a.parts)), KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
+    const dim3 grid(static_cast<unsigned>(a.parts));
+    int rc;
+    if constexpr (D == 256) {
+        rc = a.tiles ? launch(kv4_attn_tc_kernel<D, 1>, grid, KT_THREADS, KtSmem<D, 1>::BYTES, stream, p)
+                     : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
+    } else {
+        rc = a.tiles == 2   ? launch(kv4_attn_tc_kernel<D, 2>, grid, KT_THREADS, KtSmem<D, 2>::BYTES, stream, p)
+             : a.tiles == 1 ? launch(kv4_attn_tc_kernel<D, 1>, grid, KT_THREADS, KtSmem<D, 1>::BYTES, stream, p)
+                            : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
+    }
     if (rc != SV_OK || !a.joins) return rc;
     constexpr int rows = KJ_VALUES / D;
     return launch(kv4_join_kernel<D>, dim3(static_cast<unsigned>(a.parts), static_cast<unsigned>((a.tile + rows - 1) / rows)),
@@ -243,7 +263,9 @@ size_t kv4_attention_bytes(int R, int B, int ragged, int Hq, const sv_kv4_cache 
     using namespace sv;
     if (!cache || (cache->d != 64 && cache->d != 128 && cache->d != 256) || cache->Hk < 1 || R < 0 || B < 0) return 0;
     if (check_attention(R, B, Hq, cache) != SV_OK) return 0;
-    return AttnSpace(attn_plan(R, B, ragged != 0, Hq / cache->Hk, cache->d, cache->Hk, cache->max_pages, ATTN_SMS), cache->d).bytes;
+    if (cache->max_pages < 0 || cache->max_pages > KV_MAX_PAGES || (!ragged && (B ? R % B : R))) return 0;
+    if (R == 0 || B == 0) return 16;
+    return AttnSpace(attn_plan(R, B, Hq / cache->Hk, cache->d, cache->Hk, cache->max_pages), cache->d).bytes;
 }
 
 int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t *cu_seqlens, const int32_t *seq_lens, int B,
@@ -264,7 +286,7 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     if (!ws) return SV_ERR_NULL;
     if (!aligned_to(ws, 16)) return SV_ERR_ALIGN;
     const int G = Hq / cache->Hk;
-    const AttnPlan a = attn_plan(R, B, cu_seqlens != nullptr, G, cache->d, cache->Hk, cache->max_pages, ATTN_SMS);
+    const AttnPlan a = attn_plan(R, B, G, cache->d, cache->Hk, cache->max_pages);
     const AttnSpace at(a, cache->d);
     if (ws_bytes < at.bytes) return SV_ERR_SHAPE;
     DeviceInfo dev;
@@ -279,6 +301,7 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     p.ldo = ldo;
     p.G = G;
     p.tile = a.tile;
+    p.unit = a.unit;
     p.scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
     p.v_scale = cache->v_scale;
     p.window = window;

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
         const KvItem &it = part.item;
         const int u0 = it.unit, n = part.units();
         const int mine = n > warp ? (n - warp + KA_WARPS - 1) / KA_WARPS : 0;   // this warp's pages
-        auto page_of = [&](int i) { return it.seq.before < 0 ? -1 : p.kv.at(it.b, it.span.page(u0 + warp + KA_WARPS * i)); };
+        auto page_of = [&](int i) { return it.seq.before < 0 ? -1 : p.kv.at(it.b, it.span.at(u0 + warp + KA_WARPS * i)); };
         uint32_t there = 0;
         auto ask = [&](int i, int page) {
             const int st = i % S::STAGES;
@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
         w.clear();
         for (int i = 0; i < mine; ++i) {
             const int nx = i + S::STAGES - 1;
-            __syncwarp();                       // (the stage has been read)
+            fence_proxy_async();                // (the stage has been read before a copy may write there)
+            __syncwarp();
             if (nx < mine) ask(nx, page_of(nx));
             const int st = i % S::STAGES;
             if (there >> st & 1) {
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
                     atomicOr(p.err, 2);
                 }
                 phases ^= 1u << st;
-                const int first = KV_PAGE * it.span.page(u0 + warp + KA_WARPS * i);
+                const int first = KV_PAGE * it.span.at(u0 + warp + KA_WARPS * i);
                 const bool all = first + KV_PAGE - 1 <= to && (first >= from || first + KV_PAGE <= p.sinks);
                 w.page(ring + st * S::STAGE, query, first, all, pos, low, p.window > 0 ? p.sinks : 0, scale);
             }

@@ -1,0 +1,603 @@
+// kv4_attn_tc.cuh -- attention of many query rows over the 4-bit cache on the
+// 5th-generation tensor cores: prompts, and verify rows with more packed rows
+// than one mma.sync tile.
+//
+// An item (kv4_plan.cuh) is NT tiles of 128 packed rows, a unit 128 tokens.  A
+// unit's keys and values become fp16 in shared memory once for all tiles,
+// exactly (kv4.cuh), in a ring of 64-token blocks in the order in which the
+// products use them.  Scores S = Q K^T go to tensor memory (M128 N128, Q and K
+// from shared memory); the softmax warps turn them into fp16 probabilities over
+// S, in the same columns; O += P V takes P from tensor memory and V across.
+//
+// NT = 2 (d 64 and 128, more than 128 rows): each tile has its S and O and a
+// softmax warpgroup; while one tile's probabilities are formed, the tensor
+// cores work on the other's.  NT = 1 (fewer rows, or d 256, whose O fills half
+// of the tensor memory): the scores of consecutive units alternate between two
+// buffers, so that those of the next unit are formed during a softmax, which
+// both warpgroups share, half of the columns each.
+//
+// The softmax is that of kv4_attn.cuh: fp32, relative to a maximum that moves
+// only when a score passes it by 2^8, when O is rescaled in tensor memory by
+// the rows' own threads.
+//
+// Roles (18 warps): 0 .. 7 queries, softmax, O and outputs; 8 .. 15 codes to
+// fp16; 16 products; 17 copies (bulk copies of the pages' codes and scales, 64
+// tokens of K or V an entry).
+#pragma once
+
+#include "kv4_attn.cuh"
+#include "kv4_plan.cuh"
+#include "tc_ops.cuh"
+
+namespace sv {
+
+constexpr int KT_ROWS = 128;                    // packed rows of a tile
+constexpr int KT_UNIT = 128;                    // tokens of a unit
+constexpr int KT_BLOCK = 64;                    // tokens of a ring block
+constexpr int KT_SOFT = 8, KT_CODE = 8;         // warps
+constexpr int KT_MMA_WARP = 16, KT_COPY_WARP = 17;
+constexpr int KT_THREADS = 18 * 32;
+
+template <int D, int NT>
+struct KtSmem {
+    static constexpr int BLOCK = KT_BLOCK * D * 2;      // fp16 of 64 tokens' keys or values
+    static constexpr int BLOCKS = D == 256 ? 4 : 8;
+    static constexpr int ENTRY = KT_BLOCK * D / 2 + KT_BLOCK * D / 16;  // their codes and scales
+    static constexpr int ENTRIES = D == 256 ? 3 : 6;
+    static constexpr int Q = NT * KT_ROWS * D * 2;
+    static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
+    static constexpr int MASK = STAT + 2 * KT_ROWS * 4;         // missing pages of the last eight units
+    static constexpr int BARS = MASK + 8 * 4;
+    // barriers
+    static constexpr int RAW_FULL = 0, RAW_EMPTY = ENTRIES, B_FULL = 2 * ENTRIES, B_EMPTY = B_FULL + BLOCKS,
+                         S_FULL = B_EMPTY + BLOCKS, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, Q_FULL = O_DONE + 2,
+                         COUNT = Q_FULL + 2;
+    static constexpr int USED = BARS + 8 * COUNT + 16;
+    // (more than half of a multiprocessor's: two blocks would wait for each other's tensor memory)
+    static constexpr int BYTES = USED > 116 * 1024 ? USED : 116 * 1024;
+    static_assert(BYTES <= 232448, "shared memory of a block");
+    // tensor memory: O of a tile, then S
+    static constexpr uint32_t O(int tile) { return static_cast<uint32_t>(tile * D); }
+    static constexpr uint32_t S(int i) { return static_cast<uint32_t>(NT * D + 128 * i); }
+    static constexpr int TMEM = 512;
+    static_assert(NT * D + 256 <= TMEM, "tensor memory");
+};
+
+// Instruction descriptor of an M = 128 product of n columns, fp16 operands.
+constexpr uint32_t kt_idesc(int n, bool b_mn)
+{
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Descriptor of 128-byte swizzled rows (tc_ops.cuh), strides in bytes.
+__device__ __forceinline__ uint64_t kt_desc(uint32_t saddr, uint32_t leading, uint32_t stride)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(leading >> 4) << 16) |
+           (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// D[tmem] (+)= A[smem] x B[smem]; whole-warp form, one elected lane issues.
+__device__ __forceinline__ void kt_mma_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ f32x2 kt_add_x2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// What a row sees: tokens up to pos in its window, from `low` on, or below
+// `sinks`; bit i of `missing`: the unit's page i is not there.
+struct KtSight {
+    int pos, low, sinks;
+    __device__ __forceinline__ bool operator()(int token, unsigned missing) const
+    {
+        return token <= pos && (token >= low || token < sinks) && !(missing >> ((token % KT_UNIT) / KV_PAGE) & 1u);
+    }
+};
+
+// 32 scores, of tokens first .. first + 31, that the row does not see to -inf.
+__device__ __forceinline__ void kt_mask(uint32_t (&s)[32], const KtSight &sight, int first, unsigned missing)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (!sight(first + i, missing)) s[i] = 0xFF800000u;
+}
+
+__device__ __forceinline__ float kt_max(const uint32_t (&s)[32], float top)
+{
+    float a = top, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        a = fmaxf(a, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+        b = fmaxf(b, fmaxf(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])));
+    }
+    return fmaxf(a, b);
+}
+
+// Probabilities 2^(scale s - ref) of 32 scores as fp16 pairs; their sum is added.
+__device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 scale, f32x2 minus, f32x2 &sum, uint32_t (&p)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const f32x2 x = fma_x2(pair_x2(s[2 * i], s[2 * i + 1]), scale, minus);
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+        a = ka_exp2(a);
+        b = ka_exp2(b);
+        sum = kt_add_x2(sum, pack_x2(a, b));
+        p[i] = pack_f16x2(a, b);
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttnParams p)
+{
+    using L = KtSmem<D, NT>;
+    extern __shared__ __align__(1024) uint8_t kt_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(kt_smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(kt_smem + L::BARS);
+    volatile int *flag = reinterpret_cast<volatile int *>(bars + L::COUNT);
+    volatile uint32_t *slot_tm = reinterpret_cast<volatile uint32_t *>(flag + 1);
+    volatile unsigned *missing = reinterpret_cast<volatile unsigned *>(kt_smem + L::MASK);
+    auto bar = [&](int i) { return base + static_cast<uint32_t>(L::BARS + 8 * i); };
+    const TcWait wait{flag, p.err};
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.err, 4);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::COUNT; ++i) {
+            const bool codes = (i >= L::RAW_EMPTY && i < L::B_EMPTY);           // (RAW_EMPTY, B_FULL)
+            const bool soft = (i >= L::P_FULL && i < L::O_DONE) || i >= L::Q_FULL;
+            mbar_init(bar(i), codes ? KT_CODE : soft ? KT_SOFT / NT : 1);
+        }
+        *flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == KT_MMA_WARP) {
+        tmem_alloc(smem_addr(const_cast<uint32_t *>(slot_tm)), L::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *slot_tm;
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    KvPart part;
+    part.start(p, blockIdx.x, gridDim.x);
+
+    // The order of a unit's K and V blocks: with two tiles K0 V0 K1 V1 ..,
+    // with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
+    // f(i, is_v) for the n units of an item
+    auto in_order = [](int n, auto &&f) {
+        if (NT == 2) {
+            for (int i = 0; i < n; ++i) {
+                f(i, false);
+                f(i, true);
+            }
+        } else {
+            f(0, false);
+            for (int i = 0; i < n; ++i) {
+                if (i + 1 < n) f(i + 1, false);
+                f(i, true);
+            }
+        }
+    };
+
+    if (warp == KT_COPY_WARP) {
+        const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
+        int entry = 0, units = 0;
+        uint32_t round = 0;
+        for (; part.left > 0; part.next(p)) {
+            const KvItem &it = part.item;
+            const int last = it.seq.before + (min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1) / p.G;
+            if (lane == 0 && it.seq.before >= 0 && last >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
+            in_order(part.units(), [&](int i, bool v) {
+                // lanes 0 .. 3: the unit's pages
+                const int first = it.span.at(it.unit + i) * KT_UNIT, at = first / KV_PAGE + (lane & 3);
+                const bool want = it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages;
+                const int page = want ? p.kv.at(it.b, at) : -1;
+                if (!v) {
+                    if (want && page < 0 && lane < 4) atomicOr(p.err, KV_ERR_PAGE);
+                    const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 15u;
+                    if (lane == 0) missing[(units + i) & 7] = gone;
+                }
+                for (int half = 0; half < 2; ++half) {
+                    const int e = entry;
+                    if (round) wait(bar(L::RAW_EMPTY + e), round - 1);
+                    const uint32_t full = bar(L::RAW_FULL + e), to = base + L::RAW + e * L::ENTRY;
+                    const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0 && lane < 4) >> (2 * half) & 3u;
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here) * (L::ENTRY / 2));
+                    __syncwarp();
+                    if (lane < 4 && (lane >> 1) == half && page >= 0) {
+                        const uint8_t *src = p.kv.head<D>(page, it.h);
+                        const uint32_t sub = lane & 1;
+                        bulk_g2s(to + sub * (KV_PAGE * D / 2), src + (v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
+                        bulk_g2s(to + KT_BLOCK * D / 2 + sub * (KV_PAGE * D / 16), src + (v ? kv_v_scales(D) : kv_k_scales(D)),
+                                 KV_PAGE * D / 16, full, policy);
+                    }
+                    if (++entry == L::ENTRIES) {
+                        entry = 0;
+                        ++round;
+                    }
+                }
+            });
+            units += part.units();
+        }
+    } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
+        // ------------------------------------------------ codes to fp16
+        constexpr int Q32 = D / 32;             // 32-dimension pieces of a token
+        constexpr int ROUNDS = KT_BLOCK * Q32 / (KT_CODE * 32);
+        constexpr int ROUNDS1 = ROUNDS > 0 ? ROUNDS : 1;
+        const int me = threadIdx.x - KT_SOFT * 32;
+        const bool live = me < KT_BLOCK * Q32;  // (d 64: half of the threads)
+        int entry = 0, block = 0;
+        uint32_t eround = 0, bround = 0;
+        for (; part.left > 0; part.next(p)) {
+            in_order(part.units(), [&](int, bool v) {
+                for (int half = 0; half < 2; ++half) {
+                    wait(bar(L::RAW_FULL + entry), eround);
+                    const uint8_t *raw = kt_smem + L::RAW + entry * L::ENTRY;
+                    uint4 w[ROUNDS1];
+                    uint32_t sc[ROUNDS1];
+#pragma unroll
+                    for (int k = 0; k < ROUNDS1; ++k) {
+                        const int i = me + k * KT_CODE * 32, row = i / Q32, q = i % Q32;
+                        if (live) {
+                            w[k] = *reinterpret_cast<const uint4 *>(raw + row * (D / 2) + 16 * q);
+                            sc[k] = *reinterpret_cast<const uint16_t *>(raw + KT_BLOCK * D / 2 + row * (D / 16) + 2 * q);
+                        }
+                    }
+                    // (the reads are done before a bulk copy may write here: without the fence it overtook them)
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::RAW_EMPTY + entry));
+                    if (++entry == L::ENTRIES) {
+                        entry = 0;
+                        ++eround;
+                    }
+                    if (bround) wait(bar(L::B_EMPTY + block), bround - 1);
+                    const uint32_t to = base + L::RING + block * L::BLOCK;
+#pragma unroll
+                    for (int k = 0; k < ROUNDS1; ++k) {
+                        const int i = me + k * KT_CODE * 32, row = i / Q32, q = i % Q32;
+                        if (!live) continue;
+                        uint32_t s2 = kv_scales2(sc[k]);
+                        if (v) s2 = kv_finite2(s2);
+                        // pieces of eight dimensions in an order of the thread's own, so that neighbours write
+                        // different banks: piece e xor x
+                        const int x = D == 64 ? 0 : D == 128 ? 2 * (q >> 1) : q >> 1;
+                        uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                        uint32_t f[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+                        if (D == 256 && (x & 1)) {
+                            const uint32_t a = c[0], b = c[2];
+                            c[0] = c[1], c[1] = a, c[2] = c[3], c[3] = b;
+                        }
+                        if (D >= 128 && (x & 2)) {
+                            const uint32_t a = c[0], b = c[1], g = f[0];
+                            c[0] = c[2], c[1] = c[3], c[2] = a, c[3] = b;
+                            f[0] = f[1], f[1] = g;
+                        }
+                        const uint32_t line = to + (row >> 3) * (D / 64 * 1024) + (q >> 1) * 1024 + (row & 7) * 128;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t y[4];
+                            kv_values8(c[e], y);
+                            const int chunk = ((q & 1) * 4 + (e ^ x)) ^ (row & 7);
+                            sts128(line + chunk * 16, make_uint4(kv_mul2(y[0], f[e >> 1]), kv_mul2(y[1], f[e >> 1]),
+                                                                 kv_mul2(y[2], f[e >> 1]), kv_mul2(y[3], f[e >> 1])));
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::B_FULL + block));
+                    if (++block == L::BLOCKS) {
+                        block = 0;
+                        ++bround;
+                    }
+                }
+            });
+        }
+    } else if (warp == KT_MMA_WARP) {
+        // ------------------------------------------------ products
+        int block = 0;
+        uint32_t bround = 0, items[2] = {0, 0};
+        uint32_t run[2] = {0, 0};               // units of each tile (NT 1: of both buffers together, in run[0])
+        constexpr uint32_t GROUP = D / 64 * 1024;       // bytes of eight tokens of a block
+        auto scores = [&](int tile, uint32_t s, int at) {
+            const uint32_t a0 = base + tile * (KT_ROWS * D * 2), b0 = base + L::RING + at * L::BLOCK;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                kt_mma_ss_warp(tmem + s, kt_desc(a0 + (k / 4) * (KT_ROWS * 128) + (k % 4) * 32, 16, 1024),
+                               kt_desc(b0 + (k / 4) * 1024 + (k % 4) * 32, 16, GROUP), kt_idesc(KT_UNIT, false), k > 0);
+        };
+        auto values = [&](int tile, uint32_t s, int at, bool first) {
+            const uint32_t b0 = base + L::RING + at * L::BLOCK;
+#pragma unroll
+            for (int k = 0; k < KT_UNIT / 16; ++k)
+                tc_mma_f16_ts_warp(tmem + L::O(tile), tmem + s + 8 * k, kt_desc(b0 + 2 * k * GROUP, 1024, GROUP), kt_idesc(D, true),
+                                   !first || k > 0);
+        };
+        auto full = [&](int at, uint32_t r) {
+            wait(bar(L::B_FULL + at), r);
+            wait(bar(L::B_FULL + at + 1), r);
+            __syncwarp();
+            tc_fence_after_sync();
+        };
+        auto empty = [&](int at) {
+            tc_commit_warp(bar(L::B_EMPTY + at));
+            tc_commit_warp(bar(L::B_EMPTY + at + 1));
+        };
+        auto next = [&]() {                     // the next unit's pair of blocks
+            block += 2;
+            if (block == L::BLOCKS) {
+                block = 0;
+                ++bround;
+            }
+        };
+        for (; part.left > 0; part.next(p)) {
+            const KvItem &it = part.item;
+            const int n = part.units();
+            const int tiles = NT == 2 && it.seq.n * p.G - it.tile * p.tile > KT_ROWS ? 2 : 1;
+            for (int t = 0; t < tiles; ++t) wait(bar(L::Q_FULL + t), items[t]++);
+            __syncwarp();
+            tc_fence_after_sync();
+            if (NT == 1) {
+                full(block, bround);
+                scores(0, L::S(run[0] & 1), block);
+                tc_commit_warp(bar(L::S_FULL + (run[0] & 1)));
+                empty(block);
+                next();
+                for (int i = 0; i < n; ++i, ++run[0]) {
+                    const uint32_t j = run[0];
+                    if (i + 1 < n) {
+                        full(block, bround);
+                        scores(0, L::S((j + 1) & 1), block);
+                        tc_commit_warp(bar(L::S_FULL + ((j + 1) & 1)));
+                        empty(block);
+                        next();
+                    }
+                    full(block, bround);
+                    wait(bar(L::P_FULL + (j & 1)), j >> 1);
+                    __syncwarp();
+                    tc_fence_after_sync();
+                    values(0, L::S(j & 1), block, i == 0);
+                    tc_commit_warp(bar(L::O_DONE));
+                    empty(block);
+                    next();
+                }
+            } else {
+                // (a tile's next scores go over its probabilities: after their product, in order)
+                int kb = block;
+                uint32_t kr = bround;
+                full(kb, kr);
+                for (int t = 0; t < tiles; ++t) {
+                    scores(t, L::S(t), kb);
+                    tc_commit_warp(bar(L::S_FULL + t));
+                }
+                empty(kb);
+                next();
+                for (int i = 0; i < n; ++i) {
+                    const int vb = block;
+                    full(vb, bround);
+                    next();
+                    kb = block;
+                    kr = bround;
+                    for (int t = 0; t < tiles; ++t) {
+                        wait(bar(L::P_FULL + t), run[t]++);
+                        __syncwarp();
+                        tc_fence_after_sync();
+                        values(t, L::S(t), vb, i == 0);
+                        tc_commit_warp(bar(L::O_DONE + t));
+                        if (t + 1 == tiles) empty(vb);
+                        if (i + 1 < n) {
+                            if (t == 0) full(kb, kr);
+                            scores(t, L::S(t), kb);
+                            tc_commit_warp(bar(L::S_FULL + t));
+                        }
+                    }
+                    if (i + 1 < n) {
+                        empty(kb);
+                        next();
+                    }
+                }
+            }
+        }
+    } else if (warp < KT_SOFT) {
+        // ------------------------------------------------ queries, softmax, outputs
+        const int group = warp >> 2, row = threadIdx.x & (KT_ROWS - 1);
+        const int tile = NT == 2 ? group : 0;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT);
+        uint32_t run = 0;                       // units of this thread's tile
+        int units = 0;
+        if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        for (; part.left > 0; part.next(p)) {
+            const KvItem &it = part.item;
+            const int n = part.units(), rows = min(p.tile, it.seq.n * p.G - it.tile * p.tile);
+            const bool active = tile * KT_ROWS < rows;
+            const int mine = tile * KT_ROWS + row, packed = it.tile * p.tile + mine;
+            const bool in = mine < rows;
+            const int t = packed / p.G, hq = packed - t * p.G;
+            const uint16_t *q = p.q + (it.seq.first + (in ? t : 0)) * p.ldq + static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D;
+            float scale = 0.f;
+            if (active) {
+                // the row as fp16, times a power of two that brings its largest value to [2^14, 2^15), and the
+                // scores' sign
+                unsigned top = 0;
+#pragma unroll 8
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                }
+                const int shift = xres_shift(top);
+                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
+                scale = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                constexpr int PIECES = NT == 2 ? D / 8 : D / 16;        // (one tile: half a row each)
+                const int from = NT == 2 ? 0 : group * PIECES;
+#pragma unroll 8
+                for (int i = from; i < from + PIECES; ++i) {
+                    const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                    sts128(base + tile * (KT_ROWS * D * 2) + (i / 8) * (KT_ROWS * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4),
+                           make_uint4(y[0], y[1], y[2], y[3]));
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && active) mbar_arrive(bar(L::Q_FULL + tile));
+
+            KtSight sight;
+            sight.pos = in && it.seq.before >= 0 ? it.seq.before + t : -1;
+            sight.low = p.window > 0 ? sight.pos - p.window + 1 : 0;
+            sight.sinks = p.window > 0 ? p.sinks : 0;
+            // tokens that every row of the tile sees: from .. to, and below the sinks
+            const int t0 = (it.tile * p.tile + tile * KT_ROWS) / p.G;
+            const int t1 = (it.tile * p.tile + min(rows, (tile + 1) * KT_ROWS) - 1) / p.G;
+            const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
+            const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
+            float m = -INFINITY;
+            f32x2 l2 = pack_x2(0.f, 0.f);
+            for (int i = 0; active && i < n; ++i, ++run) {
+                const uint32_t buf = NT == 2 ? tile : run & 1, parity = NT == 2 ? run : run >> 1;
+                const uint32_t s0 = lanes + L::S(buf);
+                wait(bar(L::S_FULL + buf), parity);
+                __syncwarp();
+                tc_fence_after_sync();
+                const int first = it.span.at(it.unit + i) * KT_UNIT;
+                const unsigned gone = missing[(units + i) & 7];
+                const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
+                constexpr int CHUNKS = NT == 2 ? 4 : 2;         // of 32 columns
+                const int col0 = NT == 2 ? 0 : 64 * group;
+                uint32_t s[NT == 2 ? 1 : 2][32];
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) {
+                    uint32_t (&x)[32] = s[NT == 2 ? 0 : j];
+                    tmem_ld32(s0 + col0 + 32 * j, x);
+                    tmem_wait_ld();
+                    if (!all) kt_mask(x, sight, first + col0 + 32 * j, gone);
+                    top = kt_max(x, top);
+                }
+                if (NT == 1) {                  // the row's other half
+                    stat[group * KT_ROWS + row] = top;
+                    named_bar_sync(1, KT_SOFT * 32);    // (and P may go over S now)
+                    top = fmaxf(top, stat[(group ^ 1) * KT_ROWS + row]);
+                    named_bar_sync(2, KT_SOFT * 32);
+                }
+                if (top != -INFINITY) top *= scale;
+                const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
+                    m = to_m;
+                    l2 = mul_x2(l2, pack_x2(f, f));
+                    if (i > 0) {
+                        if (NT == 1) wait(bar(L::O_DONE), run - 1);     // (with two tiles S has waited for it)
+                        __syncwarp();
+                        tc_fence_after_sync();
+                        constexpr int COLS = NT == 2 ? D : D / 2;
+                        const uint32_t o0 = lanes + L::O(tile) + (NT == 2 ? 0 : group * COLS);
+#pragma unroll 1
+                        for (int c = 0; c < COLS; c += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(o0 + c, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                            tmem_st32(o0 + c, x);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) {
+                    uint32_t (&x)[32] = s[NT == 2 ? 0 : j];
+                    if (NT == 2) {
+                        tmem_ld32(s0 + 32 * j, x);
+                        tmem_wait_ld();
+                        if (!all) kt_mask(x, sight, first + 32 * j, gone);
+                    }
+                    uint32_t pr[16];
+                    kt_probabilities(x, scale2, minus, l2, pr);
+                    tmem_st(s0 + col0 / 2 + 16 * j, pr);
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::P_FULL + buf));
+            }
+            units += n;
+
+            // the row's sums
+            float l = sum_x2(l2);
+            if (NT == 1) {
+                stat[group * KT_ROWS + row] = l;
+                named_bar_sync(1, KT_SOFT * 32);
+                l = stat[row] + stat[KT_ROWS + row];
+                named_bar_sync(2, KT_SOFT * 32);
+            }
+            if (active) {
+                wait(bar(L::O_DONE + tile), run - 1);
+                __syncwarp();
+                tc_fence_after_sync();
+                const bool whole = part.whole();
+                const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
+                constexpr int COLS = NT == 2 ? D : D / 2;
+                const int c0 = NT == 2 ? 0 : group * COLS;
+                const long long slot = (2LL * blockIdx.x + (it.unit == 0)) * p.tile + mine;
+                uint16_t *o = p.o + (it.seq.first + (in ? t : 0)) * p.ldo + static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D + c0;
+#pragma unroll 1
+                for (int c = 0; c < COLS; c += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(lanes + L::O(tile) + c0 + c, x);
+                    tmem_wait_ld();
+                    if (in && whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                y[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * f, __uint_as_float(x[8 * e + 2 * k + 1]) * f);
+                            *reinterpret_cast<uint4 *>(o + c + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    } else if (in) {
+                        uint4 *to4 = reinterpret_cast<uint4 *>(p.sums + slot * D + c0 + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) to4[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (!whole && in && c0 == 0) reinterpret_cast<float2 *>(p.stats)[slot] = make_float2(m, l);
+                tc_fence_before_sync();         // (O has been read: the next item's products come after Q_FULL)
+            }
+            if (threadIdx.x == 0 && part.parts() > 1) p.joins[blockIdx.x] = make_int4(part.parts(), it.h, it.b, it.tile);
+        }
+    }
+    // every copy has landed and every product is done: the warps above have
+    // waited for each
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == KT_MMA_WARP) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, L::TMEM);
+    }
+}
+
+}  // namespace sv

@@ -3,8 +3,8 @@
 //
 // Query rows are packed: row r of a sequence and key/value head is token
 // r / G, query head r % G of the head's G.  An item is a tile of packed rows of
-// one head; its units are the pages that some row of the tile sees (the pages
-// of the first tokens, then those of the window).  The items of head 0, then
+// one head; its units are the pages, or blocks of four, that some row of the
+// tile sees (those of the first tokens, then those of the window).  The items of head 0, then
 // head 1 and so on make one line of units, cut into equal parts, one for a
 // thread block: uneven sequences and triangles of prompts cost no balance, and
 // one long sequence is spread over the whole GPU.
@@ -33,6 +33,7 @@ struct KvAttnParams {
     long long ldq, ldo;
     int G;                                      // query heads of a key/value head
     int tile;                                   // packed rows of an item
+    int unit;                                   // tokens of a unit
     float scale;                                // of scores, with k_scale and log2 e
     float v_scale;
     int window, sinks;                          // 0: no window
@@ -57,23 +58,23 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b)
     return s;
 }
 
-// A tile's visible pages: 0 .. sinks - 1, then from .. to - 1.
+// A tile's visible units of tokens: 0 .. sinks - 1, then from .. to - 1.
 struct KvSpan {
     int sinks, from, to;
     __device__ __forceinline__ int units() const { return max(1, sinks + to - from); }
-    __device__ __forceinline__ int page(int u) const { return u < sinks ? u : from + u - sinks; }
+    __device__ __forceinline__ int at(int u) const { return u < sinks ? u : from + u - sinks; }
 };
 
 __device__ __forceinline__ int kv_tiles(const KvAttnParams &p, const KvSeq &s) { return (s.n * p.G + p.tile - 1) / p.tile; }
 
 __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, const KvSeq &s, int tile)
 {
-    if (s.before < 0) return KvSpan{0, 0, 0};   // (one unit of no page)
+    if (s.before < 0) return KvSpan{0, 0, 0};   // (one unit of no tokens)
     const int t0 = tile * p.tile / p.G, t1 = (min((tile + 1) * p.tile, s.n * p.G) - 1) / p.G;
     const int lo = p.window > 0 ? max(0, s.before + t0 - p.window + 1) : 0;
-    const int to = min((s.before + t1) / KV_PAGE + 1, p.kv.max_pages);
-    const int sinks = min((min(p.sinks, lo) + KV_PAGE - 1) / KV_PAGE, to);
-    return KvSpan{sinks, min(max(sinks, lo / KV_PAGE), to), to};
+    const int to = min(s.before + t1, p.kv.max_pages * KV_PAGE - 1) / p.unit + 1;
+    const int sinks = min((min(p.sinks, lo) + p.unit - 1) / p.unit, to);
+    return KvSpan{sinks, min(max(sinks, lo / p.unit), to), to};
 }
 
 // An item, and a unit of it.
