@@ -46,7 +46,7 @@ struct KtSmem {
     static constexpr int ENTRIES = D == 256 ? 3 : 6;
     static constexpr int Q = NT * KT_ROWS * D * 2;
     static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
-    static constexpr int MASK = STAT + 2 * KT_ROWS * 4;         // missing pages of the last eight units
+    static constexpr int MASK = STAT + 6 * KT_ROWS * 4;         // missing pages of the last eight units
     static constexpr int BARS = MASK + 8 * 4;
     // barriers
     static constexpr int RAW_FULL = 0, RAW_EMPTY = ENTRIES, B_FULL = 2 * ENTRIES, B_EMPTY = B_FULL + BLOCKS,
@@ -76,13 +76,33 @@ __device__ __forceinline__ uint64_t kt_desc(uint32_t saddr, uint32_t leading, ui
            (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// D[tmem] (+)= A[smem] x B[smem]; whole-warp form, one elected lane issues.
-__device__ __forceinline__ void kt_mma_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+// D[tmem] (+)= A[smem] x B[smem], four K steps of 16 (64 columns) 32 bytes
+// apart in both; whole-warp form, one elected lane issues.
+__device__ __forceinline__ void kt_mma4_ss_warp(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p, e, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"
                  "elect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n\t}"
+                 ::"r"(d_tmem), "l"(a), "l"(a + 2u), "l"(a + 4u), "l"(a + 6u), "l"(b), "l"(b + 2u), "l"(b + 4u), "l"(b + 6u),
+                   "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// D[tmem] (+)= A[tmem] x B[smem], four K steps of 16: A 8 columns, B `step`
+// (in 16 bytes) apart.
+__device__ __forceinline__ void kt_mma4_ts_warp(uint32_t d_tmem, uint32_t a, uint64_t b, uint64_t step, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, e, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}"
+                 ::"r"(d_tmem), "r"(a), "r"(a + 8u), "r"(a + 16u), "r"(a + 24u), "l"(b), "l"(b + step), "l"(b + 2u * step),
+                   "l"(b + 3u * step), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
@@ -93,22 +113,25 @@ __device__ __forceinline__ f32x2 kt_add_x2(f32x2 a, f32x2 b)
     return d;
 }
 
-// What a row sees: tokens up to pos in its window, from `low` on, or below
-// `sinks`; bit i of `missing`: the unit's page i is not there.
+// What a row sees: tokens up to pos in its window, from `low` on, or below `sinks`.
 struct KtSight {
     int pos, low, sinks;
-    __device__ __forceinline__ bool operator()(int token, unsigned missing) const
+    // The bits below n of 32.
+    static __device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+    // Bit i: token first + i is seen.  (first is a page's; bit 0 of `missing`: the page is not there)
+    __device__ __forceinline__ unsigned operator()(int first, unsigned missing) const
     {
-        return token <= pos && (token >= low || token < sinks) && !(missing >> ((token % KT_UNIT) / KV_PAGE) & 1u);
+        const unsigned seen = below(pos - first + 1) & (~below(low - first) | below(sinks - first));
+        return missing & 1u ? 0u : seen;
     }
 };
 
-// 32 scores, of tokens first .. first + 31, that the row does not see to -inf.
-__device__ __forceinline__ void kt_mask(uint32_t (&s)[32], const KtSight &sight, int first, unsigned missing)
+// Scores that are not seen to -inf.
+__device__ __forceinline__ void kt_mask(uint32_t (&s)[32], unsigned seen)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        if (!sight(first + i, missing)) s[i] = 0xFF800000u;
+        if (!(seen & (1u << i))) s[i] = 0xFF800000u;
 }
 
 __device__ __forceinline__ float kt_max(const uint32_t (&s)[32], float top)
@@ -176,22 +199,16 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
     KvPart part;
     part.start(p, blockIdx.x, gridDim.x);
 
-    // The order of a unit's K and V blocks: with two tiles K0 V0 K1 V1 ..,
-    // with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
-    // f(i, is_v) for the n units of an item
-    auto in_order = [](int n, auto &&f) {
-        if (NT == 2) {
-            for (int i = 0; i < n; ++i) {
-                f(i, false);
-                f(i, true);
-            }
-        } else {
-            f(0, false);
-            for (int i = 0; i < n; ++i) {
-                if (i + 1 < n) f(i + 1, false);
-                f(i, true);
-            }
-        }
+    // The order of an item's K and V blocks, step s of 2 n: with two tiles K0 V0
+    // K1 V1 .., with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
+    struct Step {
+        int unit;
+        bool v;
+    };
+    auto step = [](int s, int n) {
+        if (NT == 2) return Step{s >> 1, (s & 1) != 0};
+        if (s == 2 * n - 1) return Step{n - 1, true};
+        return s & 1 ? Step{(s + 1) >> 1, false} : s ? Step{(s >> 1) - 1, true} : Step{0, false};
     };
 
     if (warp == KT_COPY_WARP) {
@@ -202,28 +219,39 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const KvItem &it = part.item;
             const int last = it.seq.before + (min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1) / p.G;
             if (lane == 0 && it.seq.before >= 0 && last >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
-            in_order(part.units(), [&](int i, bool v) {
-                // lanes 0 .. 3: the unit's pages
-                const int first = it.span.at(it.unit + i) * KT_UNIT, at = first / KV_PAGE + (lane & 3);
-                const bool want = it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages;
-                const int page = want ? p.kv.at(it.b, at) : -1;
-                if (!v) {
-                    if (want && page < 0 && lane < 4) atomicOr(p.err, KV_ERR_PAGE);
+            const int n = part.units();
+            // lanes 0 .. 3: the unit's pages (-2: none is needed), asked for a unit ahead
+            auto page_of = [&](int i) {
+                const int at = it.span.at(it.unit + i) * (KT_UNIT / KV_PAGE) + (lane & 3);
+                return i < n && it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages ? p.kv.at(it.b, at) : -2;
+            };
+            int ahead = page_of(0), now = -2, prior = -2;
+#pragma unroll 1
+            for (int k = 0; k < 2 * n; ++k) {
+                const Step x = step(k, n);
+                int page;
+                if (!x.v) {
+                    prior = now;
+                    page = now = ahead;
+                    ahead = page_of(x.unit + 1);
+                    if (page == -1 && lane < 4) atomicOr(p.err, KV_ERR_PAGE);
                     const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 15u;
-                    if (lane == 0) missing[(units + i) & 7] = gone;
+                    if (lane == 0) missing[(units + x.unit) & 7] = gone;
+                } else {
+                    page = NT == 2 || k == 2 * n - 1 ? now : prior;
                 }
+                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0) & 15u;
+                const uint8_t *src = page >= 0 ? p.kv.head<D>(page, it.h) : nullptr;
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    const int e = entry;
-                    if (round) wait(bar(L::RAW_EMPTY + e), round - 1);
-                    const uint32_t full = bar(L::RAW_FULL + e), to = base + L::RAW + e * L::ENTRY;
-                    const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0 && lane < 4) >> (2 * half) & 3u;
-                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here) * (L::ENTRY / 2));
+                    if (round) wait(bar(L::RAW_EMPTY + entry), round - 1);
+                    const uint32_t full = bar(L::RAW_FULL + entry), to = base + L::RAW + entry * L::ENTRY;
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here >> (2 * half) & 3u) * (L::ENTRY / 2));
                     __syncwarp();
-                    if (lane < 4 && (lane >> 1) == half && page >= 0) {
-                        const uint8_t *src = p.kv.head<D>(page, it.h);
+                    if (lane < 4 && (lane >> 1) == half && src) {
                         const uint32_t sub = lane & 1;
-                        bulk_g2s(to + sub * (KV_PAGE * D / 2), src + (v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
-                        bulk_g2s(to + KT_BLOCK * D / 2 + sub * (KV_PAGE * D / 16), src + (v ? kv_v_scales(D) : kv_k_scales(D)),
+                        bulk_g2s(to + sub * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
+                        bulk_g2s(to + KT_BLOCK * D / 2 + sub * (KV_PAGE * D / 16), src + (x.v ? kv_v_scales(D) : kv_k_scales(D)),
                                  KV_PAGE * D / 16, full, policy);
                     }
                     if (++entry == L::ENTRIES) {
@@ -231,7 +259,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                         ++round;
                     }
                 }
-            });
+            }
             units += part.units();
         }
     } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
@@ -244,8 +272,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         int entry = 0, block = 0;
         uint32_t eround = 0, bround = 0;
         for (; part.left > 0; part.next(p)) {
-            in_order(part.units(), [&](int, bool v) {
-                for (int half = 0; half < 2; ++half) {
+            const int n = part.units();
+#pragma unroll 1
+            for (int b = 0; b < 4 * n; ++b) {   // two blocks a step
+                {
+                    const bool v = step(b >> 1, n).v;
                     wait(bar(L::RAW_FULL + entry), eround);
                     const uint8_t *raw = kt_smem + L::RAW + entry * L::ENTRY;
                     uint4 w[ROUNDS1];
@@ -306,7 +337,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                         ++bround;
                     }
                 }
-            });
+            }
         }
     } else if (warp == KT_MMA_WARP) {
         // ------------------------------------------------ products
@@ -315,18 +346,18 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         uint32_t run[2] = {0, 0};               // units of each tile (NT 1: of both buffers together, in run[0])
         constexpr uint32_t GROUP = D / 64 * 1024;       // bytes of eight tokens of a block
         auto scores = [&](int tile, uint32_t s, int at) {
-            const uint32_t a0 = base + tile * (KT_ROWS * D * 2), b0 = base + L::RING + at * L::BLOCK;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                kt_mma_ss_warp(tmem + s, kt_desc(a0 + (k / 4) * (KT_ROWS * 128) + (k % 4) * 32, 16, 1024),
-                               kt_desc(b0 + (k / 4) * 1024 + (k % 4) * 32, 16, GROUP), kt_idesc(KT_UNIT, false), k > 0);
+            const uint64_t a0 = kt_desc(base + tile * (KT_ROWS * D * 2), 16, 1024);
+            const uint64_t b0 = kt_desc(base + L::RING + at * L::BLOCK, 16, GROUP);
+#pragma unroll 1
+            for (int k = 0; k < D / 64; ++k)
+                kt_mma4_ss_warp(tmem + s, a0 + k * (KT_ROWS * 128 >> 4), b0 + k * (1024 >> 4), kt_idesc(KT_UNIT, false), k > 0);
         };
         auto values = [&](int tile, uint32_t s, int at, bool first) {
-            const uint32_t b0 = base + L::RING + at * L::BLOCK;
-#pragma unroll
-            for (int k = 0; k < KT_UNIT / 16; ++k)
-                tc_mma_f16_ts_warp(tmem + L::O(tile), tmem + s + 8 * k, kt_desc(b0 + 2 * k * GROUP, 1024, GROUP), kt_idesc(D, true),
-                                   !first || k > 0);
+            const uint64_t b0 = kt_desc(base + L::RING + at * L::BLOCK, 1024, GROUP);
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+                kt_mma4_ts_warp(tmem + L::O(tile), tmem + s + (NT == 2 ? 32 : 64) * k, b0 + k * (L::BLOCK >> 4), 2 * GROUP >> 4, kt_idesc(D, true),
+                                !first || k > 0);
         };
         auto full = [&](int at, uint32_t r) {
             wait(bar(L::B_FULL + at), r);
@@ -358,6 +389,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 tc_commit_warp(bar(L::S_FULL + (run[0] & 1)));
                 empty(block);
                 next();
+#pragma unroll 1
                 for (int i = 0; i < n; ++i, ++run[0]) {
                     const uint32_t j = run[0];
                     if (i + 1 < n) {
@@ -372,7 +404,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                     __syncwarp();
                     tc_fence_after_sync();
                     values(0, L::S(j & 1), block, i == 0);
-                    tc_commit_warp(bar(L::O_DONE));
+                    tc_commit_warp(bar(L::O_DONE + (j & 1)));  // (two: the softmax may be that far behind)
                     empty(block);
                     next();
                 }
@@ -381,20 +413,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 int kb = block;
                 uint32_t kr = bround;
                 full(kb, kr);
+#pragma unroll 1
                 for (int t = 0; t < tiles; ++t) {
                     scores(t, L::S(t), kb);
                     tc_commit_warp(bar(L::S_FULL + t));
                 }
                 empty(kb);
                 next();
+#pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int vb = block;
                     full(vb, bround);
                     next();
                     kb = block;
                     kr = bround;
+#pragma unroll 1
                     for (int t = 0; t < tiles; ++t) {
-                        wait(bar(L::P_FULL + t), run[t]++);
+                        wait(bar(L::P_FULL + t), t ? run[1]++ : run[0]++);
                         __syncwarp();
                         tc_fence_after_sync();
                         values(t, L::S(t), vb, i == 0);
@@ -435,7 +470,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 // the row as fp16, times a power of two that brings its largest value to [2^14, 2^15), and the
                 // scores' sign
                 unsigned top = 0;
-#pragma unroll 8
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
                     const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -447,7 +482,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 scale = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
                 constexpr int PIECES = NT == 2 ? D / 8 : D / 16;        // (one tile: half a row each)
                 const int from = NT == 2 ? 0 : group * PIECES;
-#pragma unroll 8
+#pragma unroll 2
                 for (int i = from; i < from + PIECES; ++i) {
                     const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -485,21 +520,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
                 constexpr int CHUNKS = NT == 2 ? 4 : 2;         // of 32 columns
                 const int col0 = NT == 2 ? 0 : 64 * group;
-                uint32_t s[NT == 2 ? 1 : 2][32];
+                uint32_t x[32];                 // (read again for the probabilities: 64 or 128 would not fit)
                 float top = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < CHUNKS; ++j) {
-                    uint32_t (&x)[32] = s[NT == 2 ? 0 : j];
+                auto chunk = [&](int j) {
                     tmem_ld32(s0 + col0 + 32 * j, x);
                     tmem_wait_ld();
-                    if (!all) kt_mask(x, sight, first + col0 + 32 * j, gone);
+                    if (!all) kt_mask(x, sight(first + col0 + 32 * j, gone >> (col0 / 32 + j)));
+                };
+#pragma unroll 1
+                for (int j = 0; j < CHUNKS; ++j) {
+                    chunk(j);
                     top = kt_max(x, top);
                 }
                 if (NT == 1) {                  // the row's other half
-                    stat[group * KT_ROWS + row] = top;
-                    named_bar_sync(1, KT_SOFT * 32);    // (and P may go over S now)
-                    top = fmaxf(top, stat[(group ^ 1) * KT_ROWS + row]);
-                    named_bar_sync(2, KT_SOFT * 32);
+                    float *of = stat + (run & 1) * (2 * KT_ROWS) + row;     // (two of them: read before they are written again)
+                    of[group * KT_ROWS] = top;
+                    named_bar_sync(1, KT_SOFT * 32);
+                    top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
                 }
                 if (top != -INFINITY) top *= scale;
                 const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
@@ -508,7 +545,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                     m = to_m;
                     l2 = mul_x2(l2, pack_x2(f, f));
                     if (i > 0) {
-                        if (NT == 1) wait(bar(L::O_DONE), run - 1);     // (with two tiles S has waited for it)
+                        if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
                         __syncwarp();
                         tc_fence_after_sync();
                         constexpr int COLS = NT == 2 ? D : D / 2;
@@ -526,17 +563,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < CHUNKS; ++j) {
-                    uint32_t (&x)[32] = s[NT == 2 ? 0 : j];
-                    if (NT == 2) {
-                        tmem_ld32(s0 + 32 * j, x);
-                        tmem_wait_ld();
-                        if (!all) kt_mask(x, sight, first + 32 * j, gone);
-                    }
+                    chunk(j);
                     uint32_t pr[16];
                     kt_probabilities(x, scale2, minus, l2, pr);
-                    tmem_st(s0 + col0 / 2 + 16 * j, pr);
+                    tmem_st(s0 + col0 + 16 * j, pr);        // (of this thread's columns, those that it has read)
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
@@ -548,13 +580,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             // the row's sums
             float l = sum_x2(l2);
             if (NT == 1) {
-                stat[group * KT_ROWS + row] = l;
+                float *of = stat + 4 * KT_ROWS + row;
+                of[group * KT_ROWS] = l;
                 named_bar_sync(1, KT_SOFT * 32);
-                l = stat[row] + stat[KT_ROWS + row];
-                named_bar_sync(2, KT_SOFT * 32);
+                l = of[0] + of[KT_ROWS];
             }
             if (active) {
-                wait(bar(L::O_DONE + tile), run - 1);
+                wait(bar(L::O_DONE + (NT == 2 ? tile : (run - 1) & 1)), NT == 2 ? run - 1 : (run - 1) >> 1);
                 __syncwarp();
                 tc_fence_after_sync();
                 const bool whole = part.whole();

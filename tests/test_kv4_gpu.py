@@ -460,3 +460,20 @@ def test_graphs_and_streams(sv):
     o = sv.kv4_attention(q, c[0], c[1], c[-1], stream=s)
     s.synchronize()
     assert torch.equal(o, sv.kv4_attention(q, c[0], c[1], c[-1]))
+
+
+@pytest.mark.parametrize("d,Hq", [(64, 16), (128, 16), (256, 16), (128, 40), (256, 6)])
+def test_outputs_follow_the_last_products(sv, d, Hq):
+    """Items of a few units, many at a time and again and again: a block's outputs are read when its last products are
+    done, however late they come."""
+    gen = rng_of(16)
+    for n, B in ((200, 40), (500, 50), (300, 50), (2000, 30)):
+        need = [(n + 39) // 32] * B
+        table, cache = ref.shuffled(gen, need), ref.filled(gen, sum(need), 1, d)
+        q = randn(gen, B, 8, Hq, d).bfloat16()
+        lens = ints([n] * B)
+        want = ref.attention(q, cache, table, lens)
+        first = sv.kv4_attention(q, cache, table, lens)
+        ref.check_attention(first, want)
+        for _ in range(8):
+            assert torch.equal(sv.kv4_attention(q, cache, table, lens), first)
