@@ -21,8 +21,7 @@
 // the rows' own threads.
 //
 // Roles (18 warps): 0 .. 7 queries, softmax, O and outputs; 8 .. 15 codes to
-// fp16; 16 products; 17 copies (bulk copies of the pages' codes and scales, 64
-// tokens of K or V an entry).
+// fp16; 16 products; 17 copies (bulk copies of the pages' codes and scales).
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -42,11 +41,15 @@ template <int D, int NT>
 struct KtSmem {
     static constexpr int BLOCK = KT_BLOCK * D * 2;      // fp16 of 64 tokens' keys or values
     static constexpr int BLOCKS = D == 256 ? 4 : 8;
-    static constexpr int ENTRY = KT_BLOCK * D / 2 + KT_BLOCK * D / 16;  // their codes and scales
-    static constexpr int ENTRIES = D == 256 ? 3 : 6;
+    // codes and scales of an entry's tokens; each conversion group has a ring of
+    // its own
+    static constexpr int PIECES = D == 256 ? 2 : 1;     // entries of a block
+    static constexpr int ENTRY = KT_BLOCK / PIECES * (D / 2 + D / 16);
+    static constexpr int TURN = 3, ENTRIES = 2 * TURN;  // entries of a group, and of both
     static constexpr int Q = NT * KT_ROWS * D * 2;
     static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
-    static constexpr int MASK = STAT + 6 * KT_ROWS * 4;         // missing pages of the last eight units
+    static constexpr int FACTOR = STAT + 6 * KT_ROWS * 4;       // scores' factors of the rows
+    static constexpr int MASK = FACTOR + NT * KT_ROWS * 4;          // missing pages of the last eight units
     static constexpr int BARS = MASK + 8 * 4;
     // barriers
     static constexpr int RAW_FULL = 0, RAW_EMPTY = ENTRIES, B_FULL = 2 * ENTRIES, B_EMPTY = B_FULL + BLOCKS,
@@ -112,6 +115,20 @@ __device__ __forceinline__ f32x2 kt_add_x2(f32x2 a, f32x2 b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+
+// A ring's place, and how many times the ring has been round.
+template <int N>
+struct KtTurn {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            ++round;
+        }
+    }
+};
 
 // What a row sees: tokens up to pos in its window, from `low` on, or below `sinks`.
 struct KtSight {
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         for (int i = 0; i < L::COUNT; ++i) {
             const bool codes = (i >= L::RAW_EMPTY && i < L::B_EMPTY);           // (RAW_EMPTY, B_FULL)
             const bool soft = (i >= L::P_FULL && i < L::O_DONE) || i >= L::Q_FULL;
-            mbar_init(bar(i), codes ? KT_CODE : soft ? KT_SOFT / NT : 1);
+            mbar_init(bar(i), codes ? KT_CODE / 2 : soft ? KT_SOFT / NT : 1);
         }
         *flag = 0;
         fence_barrier_init();
@@ -213,8 +230,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
 
     if (warp == KT_COPY_WARP) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
-        int entry = 0, units = 0;
-        uint32_t round = 0;
+        int units = 0;
+        KtTurn<L::TURN> turn0, turn1;           // of the groups' rings
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
             const int last = it.seq.before + (min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1) / p.G;
@@ -242,101 +259,103 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 }
                 const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0) & 15u;
                 const uint8_t *src = page >= 0 ? p.kv.head<D>(page, it.h) : nullptr;
+                constexpr int PAGES = KT_BLOCK / KV_PAGE / L::PIECES;   // of an entry
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (round) wait(bar(L::RAW_EMPTY + entry), round - 1);
-                    const uint32_t full = bar(L::RAW_FULL + entry), to = base + L::RAW + entry * L::ENTRY;
-                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here >> (2 * half) & 3u) * (L::ENTRY / 2));
+                for (int e = 0; e < 2 * L::PIECES; ++e) {       // the first block's entries, the second's
+                    const int first = e * PAGES, ring = e / L::PIECES;
+                    KtTurn<L::TURN> &at = ring ? turn1 : turn0;
+                    const int slot = ring * L::TURN + at.at;
+                    if (at.round) wait(bar(L::RAW_EMPTY + slot), at.round - 1);
+                    const uint32_t full = bar(L::RAW_FULL + slot), to = base + L::RAW + slot * L::ENTRY;
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here >> first & ((1u << PAGES) - 1u)) * (L::ENTRY / PAGES));
                     __syncwarp();
-                    if (lane < 4 && (lane >> 1) == half && src) {
-                        const uint32_t sub = lane & 1;
+                    const int sub = lane - first;
+                    if (sub >= 0 && sub < PAGES && src) {
                         bulk_g2s(to + sub * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
-                        bulk_g2s(to + KT_BLOCK * D / 2 + sub * (KV_PAGE * D / 16), src + (x.v ? kv_v_scales(D) : kv_k_scales(D)),
+                        bulk_g2s(to + PAGES * (KV_PAGE * D / 2) + sub * (KV_PAGE * D / 16), src + (x.v ? kv_v_scales(D) : kv_k_scales(D)),
                                  KV_PAGE * D / 16, full, policy);
                     }
-                    if (++entry == L::ENTRIES) {
-                        entry = 0;
-                        ++round;
-                    }
+                    at.next();
                 }
             }
             units += part.units();
         }
     } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
         // ------------------------------------------------ codes to fp16
+        // Two groups of four warps take every other block: one's waits and
+        // stores overlap the other's.
         constexpr int Q32 = D / 32;             // 32-dimension pieces of a token
-        constexpr int ROUNDS = KT_BLOCK * Q32 / (KT_CODE * 32);
-        constexpr int ROUNDS1 = ROUNDS > 0 ? ROUNDS : 1;
-        const int me = threadIdx.x - KT_SOFT * 32;
-        const bool live = me < KT_BLOCK * Q32;  // (d 64: half of the threads)
-        int entry = 0, block = 0;
-        uint32_t eround = 0, bround = 0;
+        constexpr int THREADS = KT_CODE * 16, ROUNDS = KT_BLOCK * Q32 / THREADS;
+        const int group = (warp - KT_SOFT) >> 2, me = threadIdx.x & (THREADS - 1);
+        KtTurn<L::TURN> entry;
+        KtTurn<L::BLOCKS> block;
+        if (group) block.next();
         for (; part.left > 0; part.next(p)) {
             const int n = part.units();
 #pragma unroll 1
-            for (int b = 0; b < 4 * n; ++b) {   // two blocks a step
-                {
-                    const bool v = step(b >> 1, n).v;
-                    wait(bar(L::RAW_FULL + entry), eround);
-                    const uint8_t *raw = kt_smem + L::RAW + entry * L::ENTRY;
-                    uint4 w[ROUNDS1];
-                    uint32_t sc[ROUNDS1];
+            for (int b = 0; b < 2 * n; ++b) {   // (an item has whole pairs of blocks)
+                const bool v = step(b, n).v;
+                uint4 w[ROUNDS];
+                uint32_t sc[ROUNDS];
+                uint32_t free[L::PIECES];
 #pragma unroll
-                    for (int k = 0; k < ROUNDS1; ++k) {
-                        const int i = me + k * KT_CODE * 32, row = i / Q32, q = i % Q32;
-                        if (live) {
-                            w[k] = *reinterpret_cast<const uint4 *>(raw + row * (D / 2) + 16 * q);
-                            sc[k] = *reinterpret_cast<const uint16_t *>(raw + KT_BLOCK * D / 2 + row * (D / 16) + 2 * q);
-                        }
-                    }
-                    // (the reads are done before a bulk copy may write here: without the fence it overtook them)
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::RAW_EMPTY + entry));
-                    if (++entry == L::ENTRIES) {
-                        entry = 0;
-                        ++eround;
-                    }
-                    if (bround) wait(bar(L::B_EMPTY + block), bround - 1);
-                    const uint32_t to = base + L::RING + block * L::BLOCK;
+                for (int e = 0; e < L::PIECES; ++e) {
+                    const int slot = group * L::TURN + entry.at;
+                    wait(bar(L::RAW_FULL + slot), entry.round);
+                    const uint8_t *raw = kt_smem + L::RAW + slot * L::ENTRY;
+                    constexpr int N = ROUNDS / L::PIECES;
 #pragma unroll
-                    for (int k = 0; k < ROUNDS1; ++k) {
-                        const int i = me + k * KT_CODE * 32, row = i / Q32, q = i % Q32;
-                        if (!live) continue;
-                        uint32_t s2 = kv_scales2(sc[k]);
-                        if (v) s2 = kv_finite2(s2);
-                        // pieces of eight dimensions in an order of the thread's own, so that neighbours write
-                        // different banks: piece e xor x
-                        const int x = D == 64 ? 0 : D == 128 ? 2 * (q >> 1) : q >> 1;
-                        uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                        uint32_t f[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
-                        if (D == 256 && (x & 1)) {
-                            const uint32_t a = c[0], b = c[2];
-                            c[0] = c[1], c[1] = a, c[2] = c[3], c[3] = b;
-                        }
-                        if (D >= 128 && (x & 2)) {
-                            const uint32_t a = c[0], b = c[1], g = f[0];
-                            c[0] = c[2], c[1] = c[3], c[2] = a, c[3] = b;
-                            f[0] = f[1], f[1] = g;
-                        }
-                        const uint32_t line = to + (row >> 3) * (D / 64 * 1024) + (q >> 1) * 1024 + (row & 7) * 128;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t y[4];
-                            kv_values8(c[e], y);
-                            const int chunk = ((q & 1) * 4 + (e ^ x)) ^ (row & 7);
-                            sts128(line + chunk * 16, make_uint4(kv_mul2(y[0], f[e >> 1]), kv_mul2(y[1], f[e >> 1]),
-                                                                 kv_mul2(y[2], f[e >> 1]), kv_mul2(y[3], f[e >> 1])));
-                        }
+                    for (int k = 0; k < N; ++k) {
+                        const int i = me + k * THREADS, row = i / Q32, q = i % Q32;
+                        w[e * N + k] = *reinterpret_cast<const uint4 *>(raw + row * (D / 2) + 16 * q);
+                        sc[e * N + k] = *reinterpret_cast<const uint16_t *>(raw + KT_BLOCK / L::PIECES * D / 2 + row * (D / 16) + 2 * q);
                     }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::B_FULL + block));
-                    if (++block == L::BLOCKS) {
-                        block = 0;
-                        ++bround;
+                    free[e] = bar(L::RAW_EMPTY + slot);
+                    entry.next();
+                }
+                // (the reads are done before a bulk copy may write here: without the fence it overtook them)
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int e = 0; e < L::PIECES; ++e) mbar_arrive(free[e]);
+                }
+                if (block.round) wait(bar(L::B_EMPTY + block.at), block.round - 1);
+                const uint32_t to = base + L::RING + block.at * L::BLOCK;
+#pragma unroll
+                for (int k = 0; k < ROUNDS; ++k) {
+                    const int i = me + k * THREADS, row = i / Q32, q = i % Q32;
+                    uint32_t s2 = kv_scales2(sc[k]);
+                    if (v) s2 = kv_finite2(s2);
+                    // pieces of eight dimensions in an order of the thread's own, so that neighbours write
+                    // different banks: piece e xor x
+                    const int x = D == 64 ? 0 : D == 128 ? 2 * (q >> 1) : q >> 1;
+                    uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    uint32_t f[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+                    if (D == 256 && (x & 1)) {
+                        const uint32_t a = c[0], b2 = c[2];
+                        c[0] = c[1], c[1] = a, c[2] = c[3], c[3] = b2;
+                    }
+                    if (D >= 128 && (x & 2)) {
+                        const uint32_t a = c[0], b2 = c[1], g = f[0];
+                        c[0] = c[2], c[1] = c[3], c[2] = a, c[3] = b2;
+                        f[0] = f[1], f[1] = g;
+                    }
+                    const uint32_t line = to + (row >> 3) * (D / 64 * 1024) + (q >> 1) * 1024 + (row & 7) * 128;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
+                        kv_values8(c[e], y);
+                        const int chunk = ((q & 1) * 4 + (e ^ x)) ^ (row & 7);
+                        sts128(line + chunk * 16, make_uint4(kv_mul2(y[0], f[e >> 1]), kv_mul2(y[1], f[e >> 1]),
+                                                             kv_mul2(y[2], f[e >> 1]), kv_mul2(y[3], f[e >> 1])));
                     }
                 }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_FULL + block.at));
+                block.next();
+                block.next();
             }
         }
     } else if (warp == KT_MMA_WARP) {
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         const int group = warp >> 2, row = threadIdx.x & (KT_ROWS - 1);
         const int tile = NT == 2 ? group : 0;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT);
+        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT), *factor = reinterpret_cast<float *>(kt_smem + L::FACTOR);
         uint32_t run = 0;                       // units of this thread's tile
         int units = 0;
         if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -464,34 +483,39 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const int mine = tile * KT_ROWS + row, packed = it.tile * p.tile + mine;
             const bool in = mine < rows;
             const int t = packed / p.G, hq = packed - t * p.G;
-            const uint16_t *q = p.q + (it.seq.first + (in ? t : 0)) * p.ldq + static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D;
-            float scale = 0.f;
+            // The tile's queries as fp16, each row times a power of two that brings its largest value to [2^14, 2^15),
+            // and the scores' sign: a row is D / 8 lanes' 16 bytes.
             if (active) {
-                // the row as fp16, times a power of two that brings its largest value to [2^14, 2^15), and the
-                // scores' sign
-                unsigned top = 0;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, WARPS = KT_SOFT / NT, LOADS = KT_ROWS / (AT_ONCE * WARPS), BATCH = 4;
+                const int wq = NT == 2 ? warp & 3 : warp, sub = lane / LANES, piece = lane % LANES;
+                const unsigned peers = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << (sub * LANES);
+#pragma unroll 1
+                for (int i0 = 0; i0 < LOADS; i0 += BATCH) {
+                    uint4 v[BATCH];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                }
-                const int shift = xres_shift(top);
-                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
-                scale = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-                constexpr int PIECES = NT == 2 ? D / 8 : D / 16;        // (one tile: half a row each)
-                const int from = NT == 2 ? 0 : group * PIECES;
-#pragma unroll 2
-                for (int i = from; i < from + PIECES; ++i) {
-                    const uint4 v = in ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t y[4];
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = pk / p.G;
+                        const uint16_t *q = p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D;
+                        v[i] = tile * KT_ROWS + r < rows ? reinterpret_cast<const uint4 *>(q)[piece] : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                    sts128(base + tile * (KT_ROWS * D * 2) + (i / 8) * (KT_ROWS * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4),
-                           make_uint4(y[0], y[1], y[2], y[3]));
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub;
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        unsigned top = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                        top = __reduce_max_sync(peers, top);
+                        const int shift = xres_shift(top);
+                        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                        sts128(base + tile * (KT_ROWS * D * 2) + (piece / 8) * (KT_ROWS * 128) + r * 128 + (((piece % 8) ^ (r & 7)) << 4),
+                               make_uint4(y[0], y[1], y[2], y[3]));
+                        if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                    }
                 }
             }
             fence_proxy_async();
@@ -507,6 +531,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const int t1 = (it.tile * p.tile + min(rows, (tile + 1) * KT_ROWS) - 1) / p.G;
             const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
             const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
+            // (a warp's rows' factors come from other warps, which also arrive at this barrier)
+            __syncwarp();
+            named_bar_sync(NT == 2 ? 1 + group : 1, KT_SOFT * 32 / NT);
+            const float scale = factor[tile * KT_ROWS + row];
             float m = -INFINITY;
             f32x2 l2 = pack_x2(0.f, 0.f);
             for (int i = 0; active && i < n; ++i, ++run) {
@@ -535,6 +563,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 if (NT == 1) {                  // the row's other half
                     float *of = stat + (run & 1) * (2 * KT_ROWS) + row;     // (two of them: read before they are written again)
                     of[group * KT_ROWS] = top;
+                    __syncwarp();
                     named_bar_sync(1, KT_SOFT * 32);
                     top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
                 }
@@ -582,6 +611,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             if (NT == 1) {
                 float *of = stat + 4 * KT_ROWS + row;
                 of[group * KT_ROWS] = l;
+                __syncwarp();
                 named_bar_sync(1, KT_SOFT * 32);
                 l = of[0] + of[KT_ROWS];
             }
@@ -624,6 +654,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
     }
     // every copy has landed and every product is done: the warps above have
     // waited for each
+    __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     if (warp == KT_MMA_WARP) {

@@ -163,7 +163,9 @@ struct KvPart {
         left = min(share, all - lo);
         if (left <= 0) return;
         item.h = static_cast<int>(lo / line);
+        item.b = -1;
         kv_line(p, lo - item.h * line, &item);
+        if (item.b < 0) left = 0;               // (lengths written meanwhile)
     }
     // Units of the item in this part.
     __device__ __forceinline__ int units() const
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams
     pdl_wait_prior();
     const int part = blockIdx.x, row0 = blockIdx.y * ROWS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 join = p.joins[part];            // parts; head, sequence, tile
-    if (join.x < 2) return;
+    if (join.x < 2 || join.x > KJ_MAX_PARTS) return;
     const KvSeq seq = kv_seq(p, join.z);
     const int rows = min(p.tile, seq.n * p.G - join.w * p.tile), n = join.x;
     if (row0 >= rows) return;
