@@ -63,12 +63,9 @@ struct KvPages {
     int n_pages, max_pages, Hk;
 
     // The page that holds a sequence's tokens 32 i .. 32 i + 31; -1: none.
-    __device__ __forceinline__ int at(int b, int i) const
-    {
-        if (i < 0 || i >= max_pages) return -1;
-        const int id = table[b * ldt + i];
-        return id >= 0 && id < n_pages ? id : -1;
-    }
+    __device__ __forceinline__ int at(int b, int i) const { return i < 0 || i >= max_pages ? -1 : page(table[b * ldt + i]); }
+    // A table's entry as a page; -1: none.
+    __device__ __forceinline__ int page(int id) const { return id >= 0 && id < n_pages ? id : -1; }
     template <int D>
     __device__ __forceinline__ uint8_t *head(int page, int h) const
     {

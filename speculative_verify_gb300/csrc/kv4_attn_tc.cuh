@@ -230,55 +230,62 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
 
     if (warp == KT_COPY_WARP) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
+        // Lane j of 0 .. 3 has the unit's page j: of block j / 2, its entry's only
+        // page or one of two.
+        constexpr bool OWN = L::PIECES == 2;
+        const int ring = (lane & 3) >> 1, sub = lane & 1;
+        KtTurn<L::TURN> turn;                   // of that entry, in the ring of the block's group
+        if (OWN && sub) turn.next();
         int units = 0;
-        KtTurn<L::TURN> turn0, turn1;           // of the groups' rings
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
             const int last = it.seq.before + (min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1) / p.G;
             if (lane == 0 && it.seq.before >= 0 && last >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
             const int n = part.units();
-            // lanes 0 .. 3: the unit's pages (-2: none is needed), asked for a unit ahead
-            auto page_of = [&](int i) {
+            // a unit's pages: entries of the table, asked for a unit ahead and looked at when they are needed
+            auto wanted = [&](int i) {
                 const int at = it.span.at(it.unit + i) * (KT_UNIT / KV_PAGE) + (lane & 3);
-                return i < n && it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages ? p.kv.at(it.b, at) : -2;
+                return i < n && it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages ? at : -1;
             };
-            int ahead = page_of(0), now = -2, prior = -2;
+            const int32_t *table = p.kv.table + it.b * p.kv.ldt;
+            int at_next = wanted(0), id_next = at_next >= 0 ? table[at_next] : 0, now = -1, prior = -1;
 #pragma unroll 1
             for (int k = 0; k < 2 * n; ++k) {
                 const Step x = step(k, n);
                 int page;
                 if (!x.v) {
                     prior = now;
-                    page = now = ahead;
-                    ahead = page_of(x.unit + 1);
-                    if (page == -1 && lane < 4) atomicOr(p.err, KV_ERR_PAGE);
+                    page = now = at_next >= 0 ? p.kv.page(id_next) : -1;
+                    if (at_next >= 0 && page < 0) atomicOr(p.err, KV_ERR_PAGE);
+                    at_next = wanted(x.unit + 1);
+                    if (at_next >= 0) id_next = table[at_next];
                     const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 15u;
                     if (lane == 0) missing[(units + x.unit) & 7] = gone;
                 } else {
                     page = NT == 2 || k == 2 * n - 1 ? now : prior;
                 }
-                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0) & 15u;
-                const uint8_t *src = page >= 0 ? p.kv.head<D>(page, it.h) : nullptr;
-                constexpr int PAGES = KT_BLOCK / KV_PAGE / L::PIECES;   // of an entry
-#pragma unroll 1
-                for (int e = 0; e < 2 * L::PIECES; ++e) {       // the first block's entries, the second's
-                    const int first = e * PAGES, ring = e / L::PIECES;
-                    KtTurn<L::TURN> &at = ring ? turn1 : turn0;
-                    const int slot = ring * L::TURN + at.at;
-                    if (at.round) wait(bar(L::RAW_EMPTY + slot), at.round - 1);
+                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0);
+                if (lane < 4) {
+                    const int slot = ring * L::TURN + turn.at;
+                    if (turn.round) wait(bar(L::RAW_EMPTY + slot), turn.round - 1);
                     const uint32_t full = bar(L::RAW_FULL + slot), to = base + L::RAW + slot * L::ENTRY;
-                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(here >> first & ((1u << PAGES) - 1u)) * (L::ENTRY / PAGES));
-                    __syncwarp();
-                    const int sub = lane - first;
-                    if (sub >= 0 && sub < PAGES && src) {
-                        bulk_g2s(to + sub * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
-                        bulk_g2s(to + PAGES * (KV_PAGE * D / 2) + sub * (KV_PAGE * D / 16), src + (x.v ? kv_v_scales(D) : kv_k_scales(D)),
-                                 KV_PAGE * D / 16, full, policy);
+                    constexpr int PAGES = OWN ? 1 : 2;
+                    const int mine = OWN ? 0 : sub;
+                    // (a copy may land before the entry's bytes are announced: the arrival is still to come)
+                    if (mine == 0)
+                        mbar_arrive_expect_tx(full, (OWN ? here >> lane & 1u : __popc(here >> lane & 3u)) * (L::ENTRY / PAGES));
+                    if (page >= 0) {
+                        const uint8_t *src = p.kv.head<D>(page, it.h);
+                        bulk_g2s(to + mine * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
+                        bulk_g2s(to + PAGES * (KV_PAGE * D / 2) + mine * (KV_PAGE * D / 16),
+                                 src + (x.v ? kv_v_scales(D) : kv_k_scales(D)), KV_PAGE * D / 16, full, policy);
                     }
-                    at.next();
+                    turn.next();
+                    if (OWN) turn.next();
                 }
+                __syncwarp();
             }
-            units += part.units();
+            units += n;
         }
     } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
         // ------------------------------------------------ codes to fp16
