@@ -20,8 +20,8 @@
 // only when a score passes it by 2^8, when O is rescaled in tensor memory by
 // the rows' own threads.
 //
-// Roles (18 warps): 0 .. 7 queries, softmax, O and outputs; 8 .. 15 codes to
-// fp16; 16 products; 17 copies (bulk copies of the pages' codes and scales).
+// Roles (14 warps): 0 .. 7 queries, softmax, O and outputs; 8 .. 11 codes to
+// fp16; 12 products; 13 copies (bulk copies of the pages' codes and scales).
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -33,9 +33,9 @@ namespace sv {
 constexpr int KT_ROWS = 128;                    // packed rows of a tile
 constexpr int KT_UNIT = 128;                    // tokens of a unit
 constexpr int KT_BLOCK = 64;                    // tokens of a ring block
-constexpr int KT_SOFT = 8, KT_CODE = 8;         // warps
-constexpr int KT_MMA_WARP = 16, KT_COPY_WARP = 17;
-constexpr int KT_THREADS = 18 * 32;
+constexpr int KT_SOFT = 8, KT_CODE = 4;         // warps
+constexpr int KT_MMA_WARP = KT_SOFT + KT_CODE, KT_COPY_WARP = KT_MMA_WARP + 1;
+constexpr int KT_THREADS = 32 * (KT_COPY_WARP + 1);     // 14 warps: 128 registers a thread
 
 template <int D, int NT>
 struct KtSmem {
@@ -177,6 +177,37 @@ __device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 
     }
 }
 
+// COLS columns of this thread's row times f (rare: out of line of the others).
+template <int COLS>
+__device__ __forceinline__ void kt_scale(uint32_t at, float f)
+{
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 16) {
+        uint32_t x[16];
+        tmem_ld(at + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+        tmem_st(at + c, x);
+    }
+}
+
+// 32 columns of this thread's row, fp16 pairs, times f.
+__device__ __forceinline__ void kt_scale_pairs(uint32_t at, float f)
+{
+    const uint32_t f2 = pack_f16x2(f, f);
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 16) {
+        uint32_t x[16];
+        tmem_wait_st();                         // (they were stored just before)
+        tmem_ld(at + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = kv_mul2(x[e], f2);
+        tmem_st(at + c, x);
+    }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttnParams p)
 {
@@ -289,11 +320,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         }
     } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
         // ------------------------------------------------ codes to fp16
-        // Two groups of four warps take every other block: one's waits and
-        // stores overlap the other's.
+        // Two groups of warps take every other block: one's waits and stores
+        // overlap the other's.
         constexpr int Q32 = D / 32;             // 32-dimension pieces of a token
         constexpr int THREADS = KT_CODE * 16, ROUNDS = KT_BLOCK * Q32 / THREADS;
-        const int group = (warp - KT_SOFT) >> 2, me = threadIdx.x & (THREADS - 1);
+        const int group = (warp - KT_SOFT) / (KT_CODE / 2), me = threadIdx.x & (THREADS - 1);
         KtTurn<L::TURN> entry;
         KtTurn<L::BLOCKS> block;
         if (group) block.next();
@@ -553,58 +584,53 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 const int first = it.span.at(it.unit + i) * KT_UNIT;
                 const unsigned gone = missing[(units + i) & 7];
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
-                constexpr int CHUNKS = NT == 2 ? 4 : 2;         // of 32 columns
+                // 64 scores at a time, in registers from their maximum to their probabilities
+                constexpr int HALVES = NT == 2 ? 2 : 1;
                 const int col0 = NT == 2 ? 0 : 64 * group;
-                uint32_t x[32];                 // (read again for the probabilities: 64 or 128 would not fit)
-                float top = -INFINITY;
-                auto chunk = [&](int j) {
-                    tmem_ld32(s0 + col0 + 32 * j, x);
+#pragma unroll 1
+                for (int h = 0; h < HALVES; ++h) {
+                    uint32_t x[2][32];
+                    const uint32_t at = s0 + col0 + 64 * h;
+                    tmem_ld32(at, x[0]);
+                    tmem_ld32(at + 32, x[1]);
                     tmem_wait_ld();
-                    if (!all) kt_mask(x, sight(first + col0 + 32 * j, gone >> (col0 / 32 + j)));
-                };
-#pragma unroll 1
-                for (int j = 0; j < CHUNKS; ++j) {
-                    chunk(j);
-                    top = kt_max(x, top);
-                }
-                if (NT == 1) {                  // the row's other half
-                    float *of = stat + (run & 1) * (2 * KT_ROWS) + row;     // (two of them: read before they are written again)
-                    of[group * KT_ROWS] = top;
-                    __syncwarp();
-                    named_bar_sync(1, KT_SOFT * 32);
-                    top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
-                }
-                if (top != -INFINITY) top *= scale;
-                const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-                    const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
-                    m = to_m;
-                    l2 = mul_x2(l2, pack_x2(f, f));
-                    if (i > 0) {
-                        if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
+                    if (!all) {
+                        const int page = col0 / 32 + 2 * h;
+                        kt_mask(x[0], sight(first + 32 * page, gone >> page));
+                        kt_mask(x[1], sight(first + 32 * page + 32, gone >> (page + 1)));
+                    }
+                    float top = kt_max(x[1], kt_max(x[0], -INFINITY));
+                    if (NT == 1) {              // the row's other half
+                        float *of = stat + (run & 1) * (2 * KT_ROWS) + row;     // (two of them: read before they are written again)
+                        of[group * KT_ROWS] = top;
                         __syncwarp();
-                        tc_fence_after_sync();
-                        constexpr int COLS = NT == 2 ? D : D / 2;
-                        const uint32_t o0 = lanes + L::O(tile) + (NT == 2 ? 0 : group * COLS);
-#pragma unroll 1
-                        for (int c = 0; c < COLS; c += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(o0 + c, x);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                            tmem_st32(o0 + c, x);
+                        named_bar_sync(1, KT_SOFT * 32);
+                        top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
+                    }
+                    if (top != -INFINITY) top *= scale;
+                    const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
+                        m = to_m;
+                        l2 = mul_x2(l2, pack_x2(f, f));
+                        if (h) kt_scale_pairs(s0, f);
+                        if (i > 0) {
+                            if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
+                            __syncwarp();
+                            tc_fence_after_sync();
+                            constexpr int COLS = NT == 2 ? D : D / 2;
+                            kt_scale<COLS>(lanes + L::O(tile) + (NT == 2 ? 0 : group * COLS), f);
                         }
                     }
-                }
-                const float ref = m == -INFINITY ? 0.f : m;
-                const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
-#pragma unroll 1
-                for (int j = 0; j < CHUNKS; ++j) {
-                    chunk(j);
-                    uint32_t pr[16];
-                    kt_probabilities(x, scale2, minus, l2, pr);
-                    tmem_st(s0 + col0 + 16 * j, pr);        // (of this thread's columns, those that it has read)
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t pr[16];
+                        kt_probabilities(x[j], scale2, minus, l2, pr);
+                        // (of this thread's columns, those that it has read)
+                        tmem_st(s0 + (NT == 2 ? 32 * h : col0) + 16 * j, pr);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
