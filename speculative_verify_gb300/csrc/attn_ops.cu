@@ -301,7 +301,12 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     p.ldo = ldo;
     p.G = G;
     p.tile = a.tile;
-    p.unit = a.unit;
+    for (p.tile_log = 0; 1 << p.tile_log < a.tile; ++p.tile_log) {}
+    for (p.unit_log = 0; 1 << p.unit_log < a.unit; ++p.unit_log) {}
+    unsigned c = 0;
+    while (1 << c < G) ++c;
+    p.g_shift = 30 + c;
+    p.g_mul = static_cast<unsigned>(((1ull << p.g_shift) + static_cast<unsigned>(G) - 1) / static_cast<unsigned>(G));
     p.scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
     p.v_scale = cache->v_scale;
     p.window = window;

@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
     pdl_launch_dependents();
     pdl_wait_prior();
     const uint64_t policy = policy_evict_first();
-    KvPart part;
-    part.start(p, blockIdx.x, gridDim.x);
+    __shared__ KvPartSmem part_sm;
+    KvPart part = kv_part(p, part_sm);
     if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     uint32_t phases = 0;                        // bit i: the parity that stage i completes next
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
         uint32_t a[S::SK][4];                   // (one section: kept)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = packed / p.G, hq = packed - t * p.G;
+            const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
             const bool in = row < rows;
             pos[r] = in && it.seq.before >= 0 ? it.seq.before + t : -1;
             low[r] = p.window > 0 ? pos[r] - p.window + 1 : 0;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
             }
         };
         // tokens that every row of the tile sees: from .. to, and below `sunk`
-        const int t0 = it.tile * KA_ROWS / p.G, t1 = (it.tile * KA_ROWS + rows - 1) / p.G;
+        const int t0 = kv_token(p, it.tile * KA_ROWS), t1 = kv_token(p, it.tile * KA_ROWS + rows - 1);
         const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
         const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
 
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
             const int slot = 2 * blockIdx.x + (it.unit == 0);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = packed / p.G, hq = packed - t * p.G;
+                const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
                 if (row >= rows) continue;
                 if (whole) {
                     const float f = w.l[r] == 0.f ? 0.f : p.v_scale / w.l[r];

@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
     const uint32_t tmem = *slot_tm;
     pdl_launch_dependents();
     pdl_wait_prior();
-    KvPart part;
-    part.start(p, blockIdx.x, gridDim.x);
+    __shared__ KvPartSmem part_sm;
+    KvPart part = kv_part(p, part_sm);
 
     // The order of an item's K and V blocks, step s of 2 n: with two tiles K0 V0
     // K1 V1 .., with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         int units = 0;
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
-            const int last = it.seq.before + (min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1) / p.G;
+            const int last = it.seq.before + kv_token(p, min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1);
             if (lane == 0 && it.seq.before >= 0 && last >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
             const int n = part.units();
             // a unit's pages: entries of the table, asked for a unit ahead and looked at when they are needed
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const bool active = tile * KT_ROWS < rows;
             const int mine = tile * KT_ROWS + row, packed = it.tile * p.tile + mine;
             const bool in = mine < rows;
-            const int t = packed / p.G, hq = packed - t * p.G;
+            const int t = kv_token(p, packed), hq = packed - t * p.G;
             // The tile's queries as fp16, each row times a power of two that brings its largest value to [2^14, 2^15),
             // and the scores' sign: a row is D / 8 lanes' 16 bytes.
             if (active) {
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                     uint4 v[BATCH];
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
-                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = pk / p.G;
+                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = kv_token(p, pk);
                         const uint16_t *q = p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D;
                         v[i] = tile * KT_ROWS + r < rows ? reinterpret_cast<const uint4 *>(q)[piece] : make_uint4(0, 0, 0, 0);
                     }
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             sight.low = p.window > 0 ? sight.pos - p.window + 1 : 0;
             sight.sinks = p.window > 0 ? p.sinks : 0;
             // tokens that every row of the tile sees: from .. to, and below the sinks
-            const int t0 = (it.tile * p.tile + tile * KT_ROWS) / p.G;
-            const int t1 = (it.tile * p.tile + min(rows, (tile + 1) * KT_ROWS) - 1) / p.G;
+            const int t0 = kv_token(p, it.tile * p.tile + tile * KT_ROWS);
+            const int t1 = kv_token(p, it.tile * p.tile + min(rows, (tile + 1) * KT_ROWS) - 1);
             const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
             const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
             // (a warp's rows' factors come from other warps, which also arrive at this barrier)

@@ -32,8 +32,9 @@ struct KvAttnParams {
     uint16_t *o;
     long long ldq, ldo;
     int G;                                      // query heads of a key/value head
-    int tile;                                   // packed rows of an item
-    int unit;                                   // tokens of a unit
+    unsigned g_mul, g_shift;                    // r / G = r g_mul >> g_shift for r < 2^30
+    int tile, tile_log;                         // packed rows of an item, a power of two
+    int unit_log;                               // log2 of the tokens of a unit
     float scale;                                // of scores, with k_scale and log2 e
     float v_scale;
     int window, sinks;                          // 0: no window
@@ -43,9 +44,15 @@ struct KvAttnParams {
     int *err;
 };
 
+// The token of a packed row.
+__device__ __forceinline__ int kv_token(const KvAttnParams &p, int r)
+{
+    return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(r)) * p.g_mul >> p.g_shift);
+}
+
 // A sequence's rows, and the position of its first one (negative: inactive).
 struct KvSeq {
-    int first = 0, n = 0, before = 0;
+    int first, n, before;
 };
 
 __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b)
@@ -65,16 +72,16 @@ struct KvSpan {
     __device__ __forceinline__ int at(int u) const { return u < sinks ? u : from + u - sinks; }
 };
 
-__device__ __forceinline__ int kv_tiles(const KvAttnParams &p, const KvSeq &s) { return (s.n * p.G + p.tile - 1) / p.tile; }
+__device__ __forceinline__ int kv_tiles(const KvAttnParams &p, const KvSeq &s) { return (s.n * p.G + p.tile - 1) >> p.tile_log; }
 
 __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, const KvSeq &s, int tile)
 {
     if (s.before < 0) return KvSpan{0, 0, 0};   // (one unit of no tokens)
-    const int t0 = tile * p.tile / p.G, t1 = (min((tile + 1) * p.tile, s.n * p.G) - 1) / p.G;
+    const int t0 = kv_token(p, tile * p.tile), t1 = kv_token(p, min((tile + 1) * p.tile, s.n * p.G) - 1);
     const int lo = p.window > 0 ? max(0, s.before + t0 - p.window + 1) : 0;
-    const int to = min(s.before + t1, p.kv.max_pages * KV_PAGE - 1) / p.unit + 1;
-    const int sinks = min((min(p.sinks, lo) + p.unit - 1) / p.unit, to);
-    return KvSpan{sinks, min(max(sinks, lo / p.unit), to), to};
+    const int to = (min(s.before + t1, p.kv.max_pages * KV_PAGE - 1) >> p.unit_log) + 1;
+    const int sinks = min((min(p.sinks, lo) + (1 << p.unit_log) - 1) >> p.unit_log, to);
+    return KvSpan{sinks, min(max(sinks, lo >> p.unit_log), to), to};
 }
 
 // An item, and a unit of it.
@@ -84,66 +91,62 @@ struct KvItem {
     KvSpan span;
 };
 
-// Called by whole warps.  Units of one head's items; with `want` >= 0 also
-// the item, with the unit in it, that holds unit `want` of the head.
-__device__ __forceinline__ long long kv_line(const KvAttnParams &p, long long want, KvItem *found)
+// Units of one head's items of the 32 sequences from b0 on, and their rows
+// (whole warps call it); with `want` >= 0 also the item, with the unit in it,
+// that holds unit `want` of them.
+__device__ __forceinline__ long long kv_group(const KvAttnParams &p, int b0, long long want, KvItem *found, long long &rows)
 {
     const int lane = threadIdx.x & 31;
-    long long total = 0, rows = 0;
-    for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
-        const KvSeq mine = b0 + lane < p.rows.B ? kv_seq(p, b0 + lane) : KvSeq{};
-        const int tiles = kv_tiles(p, mine);
-        rows += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) & 0xFFFFu) +
-                (static_cast<long long>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) >> 16)) << 16);
-        if (rows > p.rows.R) {                  // cu_seqlens that decrease
-            if (lane == 0) atomicOr(p.err, KV_ERR_SEQLENS);
-            return 0;
+    const KvSeq mine = b0 + lane < p.rows.B ? kv_seq(p, b0 + lane) : KvSeq{};
+    const int tiles = kv_tiles(p, mine);
+    rows = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) & 0xFFFFu) +
+           (static_cast<long long>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(mine.n) >> 16)) << 16);
+    // sequences side by side, or one after another with their tiles over the
+    // lanes, whichever takes fewer rounds
+    const unsigned many = (static_cast<unsigned>(tiles) + 31u) >> 5;
+    const bool one = __reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tiles)) > __reduce_add_sync(0xFFFFFFFFu, min(many, 1u << 24));
+    long long total = 0;
+    for (int s = 0; s < (one ? 32 : 1); ++s) {
+        KvSeq seq = mine;
+        int n = 1;                              // rounds
+        if (one) {
+            seq.first = __shfl_sync(0xFFFFFFFFu, mine.first, s);
+            seq.n = __shfl_sync(0xFFFFFFFFu, mine.n, s);
+            seq.before = __shfl_sync(0xFFFFFFFFu, mine.before, s);
+            n = (kv_tiles(p, seq) + 31) / 32;
         }
-        // long sequences one after another, their tiles over the lanes; short
-        // ones side by side
-        const bool one = __reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tiles)) > 32u;
-        for (int s = 0; s < (one ? 32 : 1); ++s) {
-            KvSeq seq = mine;
-            int n = 1;                          // rounds
+        for (int k = 0; k < n; ++k) {
+            long long units = 0;
             if (one) {
-                seq.first = __shfl_sync(0xFFFFFFFFu, mine.first, s);
-                seq.n = __shfl_sync(0xFFFFFFFFu, mine.n, s);
-                seq.before = __shfl_sync(0xFFFFFFFFu, mine.before, s);
-                n = (kv_tiles(p, seq) + 31) / 32;
+                const int t = 32 * k + lane;
+                if (t < kv_tiles(p, seq)) units = kv_span(p, seq, t).units();
+            } else {
+                for (int t = 0; t < tiles; ++t) units += kv_span(p, seq, t).units();
             }
-            for (int k = 0; k < n; ++k) {
-                long long units = 0;
-                if (one) {
-                    const int t = 32 * k + lane;
-                    if (t < kv_tiles(p, seq)) units = kv_span(p, seq, t).units();
-                } else {
-                    for (int t = 0; t < tiles; ++t) units += kv_span(p, seq, t).units();
-                }
-                long long run = units;
+            long long run = units;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long below = __shfl_up_sync(0xFFFFFFFFu, run, o);
-                    if (lane >= o) run += below;
-                }
-                const unsigned past = want >= 0 ? __ballot_sync(0xFFFFFFFFu, total + run > want) : 0u;
-                if (past) {
-                    const int w = __ffs(past) - 1;
-                    long long rest = want - total - __shfl_sync(0xFFFFFFFFu, run - units, w);
-                    found->b = one ? b0 + s : b0 + w;
-                    found->seq.first = __shfl_sync(0xFFFFFFFFu, seq.first, w);
-                    found->seq.n = __shfl_sync(0xFFFFFFFFu, seq.n, w);
-                    found->seq.before = __shfl_sync(0xFFFFFFFFu, seq.before, w);
-                    found->tile = one ? 32 * k + w : 0;
-                    found->span = kv_span(p, found->seq, found->tile);
-                    while (rest >= found->span.units()) {
-                        rest -= found->span.units();
-                        found->span = kv_span(p, found->seq, ++found->tile);
-                    }
-                    found->unit = static_cast<int>(rest);
-                    return total;
-                }
-                total += __shfl_sync(0xFFFFFFFFu, run, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long below = __shfl_up_sync(0xFFFFFFFFu, run, o);
+                if (lane >= o) run += below;
             }
+            const unsigned past = want >= 0 ? __ballot_sync(0xFFFFFFFFu, total + run > want) : 0u;
+            if (past) {
+                const int w = __ffs(past) - 1;
+                long long rest = want - total - __shfl_sync(0xFFFFFFFFu, run - units, w);
+                found->b = one ? b0 + s : b0 + w;
+                found->seq.first = __shfl_sync(0xFFFFFFFFu, seq.first, w);
+                found->seq.n = __shfl_sync(0xFFFFFFFFu, seq.n, w);
+                found->seq.before = __shfl_sync(0xFFFFFFFFu, seq.before, w);
+                found->tile = one ? 32 * k + w : 0;
+                found->span = kv_span(p, found->seq, found->tile);
+                while (rest >= found->span.units()) {
+                    rest -= found->span.units();
+                    found->span = kv_span(p, found->seq, ++found->tile);
+                }
+                found->unit = static_cast<int>(rest);
+                return total;
+            }
+            total += __shfl_sync(0xFFFFFFFFu, run, 31);
         }
     }
     return total;
@@ -151,21 +154,54 @@ __device__ __forceinline__ long long kv_line(const KvAttnParams &p, long long wa
 
 // A block's part of the line: the units that are left, and the item they are in.
 struct KvPart {
-    long long left = 0, share = 0;
+    long long left, share;
     KvItem item;
 
-    // Part k of `parts` (whole warps call it).
-    __device__ __forceinline__ void start(const KvAttnParams &p, int k, int parts)
+    // Part k of `parts`, by one whole warp.  unit[g] and rows[g] are those of
+    // group g of `groups`, or null: there are too many, and it goes through all.
+    __device__ __forceinline__ void find(const KvAttnParams &p, int k, int parts, const long long *unit, const long long *rows, int groups)
     {
-        const long long line = kv_line(p, -1, nullptr), all = line * p.kv.Hk;
+        const int lane = threadIdx.x & 31;
+        left = 0;
+        share = 1;
+        long long line = 0, n = 0;
+        if (unit) {
+            for (int g = lane; g < groups; g += 32) {
+                line += unit[g];
+                n += rows[g];
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                line += __shfl_xor_sync(0xFFFFFFFFu, line, o);
+                n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+            }
+        } else {
+            for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
+                long long r;
+                line += kv_group(p, b0, -1, nullptr, r);
+                n += r;
+            }
+        }
+        if (n > p.rows.R) {                     // cu_seqlens that decrease
+            if (lane == 0) atomicOr(p.err, KV_ERR_SEQLENS);
+            return;
+        }
+        if (line == 0) return;
+        const long long all = line * p.kv.Hk;
         share = max(static_cast<long long>(p.least), (all + parts - 1) / parts);
         const long long lo = min(share * k, all);
-        left = min(share, all - lo);
-        if (left <= 0) return;
+        if (lo == all) return;
         item.h = static_cast<int>(lo / line);
         item.b = -1;
-        kv_line(p, lo - item.h * line, &item);
-        if (item.b < 0) left = 0;               // (lengths written meanwhile)
+        long long at = lo - item.h * line, r;
+        for (int b0 = 0; b0 < p.rows.B && item.b < 0; b0 += 32) {
+            if (unit && at >= unit[b0 >> 5]) {
+                at -= unit[b0 >> 5];
+                continue;
+            }
+            at -= kv_group(p, b0, at, &item, r);
+        }
+        if (item.b >= 0) left = min(share, all - lo);   // (else lengths were written meanwhile)
     }
     // Units of the item in this part.
     __device__ __forceinline__ int units() const
@@ -200,6 +236,40 @@ struct KvPart {
         return item.unit ? 0 : 1 + static_cast<int>((item.span.units() - units() + share - 1) / share);
     }
 };
+
+// The block's part, found by all its warps (all its threads call it).
+constexpr int KP_GROUPS = 64;                   // of 32 sequences, that the warps share out
+
+struct KvPartSmem {
+    long long unit[KP_GROUPS], rows[KP_GROUPS];
+    KvPart part;
+};
+
+__device__ __forceinline__ KvPart kv_part(const KvAttnParams &p, KvPartSmem &sm)
+{
+    const int groups = (p.rows.B + 31) >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool shared = groups <= KP_GROUPS;
+    if (shared) {
+        for (int g = warp; g < groups; g += static_cast<int>(blockDim.x >> 5)) {
+            long long rows;
+            const long long units = kv_group(p, 32 * g, -1, nullptr, rows);
+            if (lane == 0) {
+                sm.unit[g] = units;
+                sm.rows[g] = rows;
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    if (warp == 0) {
+        KvPart part{};
+        part.find(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), shared ? sm.unit : nullptr, sm.rows, groups);
+        if (lane == 0) sm.part = part;
+        __syncwarp();
+    }
+    __syncthreads();
+    return sm.part;
+}
 
 constexpr int KJ_THREADS = 128;
 constexpr int KJ_VALUES = 4 * KJ_THREADS;       // output values of a block
@@ -255,7 +325,7 @@ __global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams
         acc.z = fmaf(w, v.z, acc.z);
         acc.w = fmaf(w, v.w, acc.w);
     }
-    const int packed = join.w * p.tile + row, t = packed / p.G, g = packed - t * p.G;
+    const int packed = join.w * p.tile + row, t = kv_token(p, packed), g = packed - t * p.G;
     uint16_t *o = p.o + (seq.first + t) * p.ldo + static_cast<long long>(join.y * p.G + g) * D + d;
     const float f = norm[r];
     uint2 out;
