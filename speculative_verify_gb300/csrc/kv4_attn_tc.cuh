@@ -272,6 +272,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const KvItem &it = part.item;
             const int last = it.seq.before + kv_token(p, min((it.tile + 1) * p.tile, it.seq.n * p.G) - 1);
             if (lane == 0 && it.seq.before >= 0 && last >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
+            // the item's queries on their way to L2 while the item before is at its end
+            for (int r = lane; r < p.tile; r += 32) {
+                const int pk = it.tile * p.tile + r, tt = kv_token(p, pk);
+                if (pk < it.seq.n * p.G)
+                    prefetch_l2(p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D, 2 * D);
+            }
             const int n = part.units();
             // a unit's pages: entries of the table, asked for a unit ahead and looked at when they are needed
             auto wanted = [&](int i) {
@@ -520,40 +526,44 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const bool active = tile * KT_ROWS < rows;
             const int mine = tile * KT_ROWS + row, packed = it.tile * p.tile + mine;
             const bool in = mine < rows;
-            const int t = kv_token(p, packed), hq = packed - t * p.G;
+            const int t = kv_token(p, packed);
             // The tile's queries as fp16, each row times a power of two that brings its largest value to [2^14, 2^15),
-            // and the scores' sign: a row is D / 8 lanes' 16 bytes.
+            // and the scores' sign: copied to their places and changed there, a row by D / 8 lanes with 16 bytes each.
             if (active) {
-                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, WARPS = KT_SOFT / NT, LOADS = KT_ROWS / (AT_ONCE * WARPS), BATCH = 4;
+                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, WARPS = KT_SOFT / NT, LOADS = KT_ROWS / (AT_ONCE * WARPS);
                 const int wq = NT == 2 ? warp & 3 : warp, sub = lane / LANES, piece = lane % LANES;
                 const unsigned peers = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << (sub * LANES);
-#pragma unroll 1
-                for (int i0 = 0; i0 < LOADS; i0 += BATCH) {
-                    uint4 v[BATCH];
+                const uint32_t to = base + tile * (KT_ROWS * D * 2) + (piece / 8) * (KT_ROWS * 128);
+                const int r0 = wq * LOADS * AT_ONCE + sub;
+                auto place = [&](int r) { return to + r * 128 + (((piece % 8) ^ (r & 7)) << 4); };
+                __syncwarp();
+                named_bar_sync(NT == 2 ? 1 + group : 1, KT_SOFT * 32 / NT);     // (the outputs before have left these places)
+#pragma unroll 4
+                for (int i = 0; i < LOADS; ++i) {
+                    const int r = r0 + i * AT_ONCE, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = kv_token(p, pk);
+                    const uint16_t *q = p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D;
+                    if (tile * KT_ROWS + r < rows) cp_async_16(place(r), q + 8 * piece);
+                }
+                cp_async_commit();
+                cp_async_wait_all();
+#pragma unroll 2
+                for (int i = 0; i < LOADS; ++i) {
+                    const int r = r0 + i * AT_ONCE;
+                    uint4 v = lds128(place(r));
+                    if (tile * KT_ROWS + r >= rows) v = make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    unsigned top = 0;
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = kv_token(p, pk);
-                        const uint16_t *q = p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D;
-                        v[i] = tile * KT_ROWS + r < rows ? reinterpret_cast<const uint4 *>(q)[piece] : make_uint4(0, 0, 0, 0);
-                    }
+                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                    top = __reduce_max_sync(peers, top);
+                    const int shift = xres_shift(top);
+                    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
+                    uint32_t y[4];
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int r = (wq * LOADS + i0 + i) * AT_ONCE + sub;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        unsigned top = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                        top = __reduce_max_sync(peers, top);
-                        const int shift = xres_shift(top);
-                        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                        sts128(base + tile * (KT_ROWS * D * 2) + (piece / 8) * (KT_ROWS * 128) + r * 128 + (((piece % 8) ^ (r & 7)) << 4),
-                               make_uint4(y[0], y[1], y[2], y[3]));
-                        if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                    sts128(place(r), make_uint4(y[0], y[1], y[2], y[3]));
+                    if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
                 }
             }
             fence_proxy_async();
@@ -657,20 +667,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 constexpr int COLS = NT == 2 ? D : D / 2;
                 const int c0 = NT == 2 ? 0 : group * COLS;
                 const long long slot = (2LL * blockIdx.x + (it.unit == 0)) * p.tile + mine;
-                uint16_t *o = p.o + (it.seq.first + (in ? t : 0)) * p.ldo + static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D + c0;
+                // whole rows go through the queries' place, a warp's 32 rows in its eighth, so that a store has whole
+                // rows of neighbouring lanes
+                constexpr int CHUNKS = COLS / 8, TURNS = CHUNKS < 8 ? CHUNKS - 1 : 7;      // 16-byte pieces of a row
+                const uint32_t out = base + warp * (L::Q / KT_SOFT);
 #pragma unroll 1
                 for (int c = 0; c < COLS; c += 32) {
                     uint32_t x[32];
                     tmem_ld32(lanes + L::O(tile) + c0 + c, x);
                     tmem_wait_ld();
-                    if (in && whole) {
+                    if (whole) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t y[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 y[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * f, __uint_as_float(x[8 * e + 2 * k + 1]) * f);
-                            *reinterpret_cast<uint4 *>(o + c + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+                            sts128(out + lane * (COLS * 2) + (((c / 8 + e) ^ (lane & TURNS)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
                         }
                     } else if (in) {
                         uint4 *to4 = reinterpret_cast<uint4 *>(p.sums + slot * D + c0 + c);
@@ -678,6 +691,15 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                         for (int e = 0; e < 8; ++e) to4[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                     }
                     __syncwarp();
+                }
+                if (whole) {
+                    const int first = tile * KT_ROWS + (warp & 3) * 32;         // the warp's rows
+#pragma unroll 4
+                    for (int i = lane; i < 32 * CHUNKS; i += 32) {
+                        const int r = i / CHUNKS, piece = i % CHUNKS, pk = it.tile * p.tile + first + r, tt = kv_token(p, pk);
+                        uint16_t *o = p.o + (it.seq.first + tt) * p.ldo + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D + c0;
+                        if (first + r < rows) reinterpret_cast<uint4 *>(o)[piece] = lds128(out + r * (COLS * 2) + ((piece ^ (r & TURNS)) << 4));
+                    }
                 }
                 if (!whole && in && c0 == 0) reinterpret_cast<float2 *>(p.stats)[slot] = make_float2(m, l);
                 tc_fence_before_sync();         // (O has been read: the next item's products come after Q_FULL)
