@@ -189,11 +189,11 @@ int attn_launch(const KvAttnParams &p, const AttnPlan &a, cudaStream_t stream)
     const dim3 grid(static_cast<unsigned>(a.parts));
     int rc;
     if constexpr (D == 256) {
-        rc = a.tiles ? launch(kv4_attn_tc_kernel<D, 1>, grid, KT_THREADS, KtSmem<D, 1>::BYTES, stream, p)
+        rc = a.tiles ? launch(kv4_attn_tc_kernel<D, 1>, grid, KtWarps<1>::THREADS, KtSmem<D, 1>::BYTES, stream, p)
                      : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
     } else {
-        rc = a.tiles == 2   ? launch(kv4_attn_tc_kernel<D, 2>, grid, KT_THREADS, KtSmem<D, 2>::BYTES, stream, p)
-             : a.tiles == 1 ? launch(kv4_attn_tc_kernel<D, 1>, grid, KT_THREADS, KtSmem<D, 1>::BYTES, stream, p)
+        rc = a.tiles == 2   ? launch(kv4_attn_tc_kernel<D, 2>, grid, KtWarps<2>::THREADS, KtSmem<D, 2>::BYTES, stream, p)
+             : a.tiles == 1 ? launch(kv4_attn_tc_kernel<D, 1>, grid, KtWarps<1>::THREADS, KtSmem<D, 1>::BYTES, stream, p)
                             : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
     }
     if (rc != SV_OK || !a.joins) return rc;

@@ -9,19 +9,18 @@
 // from shared memory); the softmax warps turn them into fp16 probabilities over
 // S, in the same columns; O += P V takes P from tensor memory and V across.
 //
-// NT = 2 (d 64 and 128, more than 128 rows): each tile has its S and O and a
-// softmax warpgroup; while one tile's probabilities are formed, the tensor
-// cores work on the other's.  NT = 1 (fewer rows, or d 256, whose O fills half
-// of the tensor memory): the scores of consecutive units alternate between two
-// buffers, so that those of the next unit are formed during a softmax, which
-// both warpgroups share, half of the columns each.
+// NT = 2 (d 64 and 128, more than 128 rows): each tile has its S and O and
+// softmax warps; while one tile's probabilities are formed, the tensor cores
+// work on the other's.  NT = 1 (fewer rows, or d 256, whose O fills half of the
+// tensor memory): the scores of consecutive units alternate between two
+// buffers, so that those of the next unit are formed during a softmax.
 //
 // The softmax is that of kv4_attn.cuh: fp32, relative to a maximum that moves
 // only when a score passes it by 2^8, when O is rescaled in tensor memory by
 // the rows' own threads.
 //
-// Roles (14 warps): 0 .. 7 queries, softmax, O and outputs; 8 .. 11 codes to
-// fp16; 12 products; 13 copies (bulk copies of the pages' codes and scales).
+// Roles: the first 8 warps of each tile queries, softmax, O and outputs; then
+// codes to fp16; products; copies (bulk copies of the pages' codes and scales).
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -33,9 +32,15 @@ namespace sv {
 constexpr int KT_ROWS = 128;                    // packed rows of a tile
 constexpr int KT_UNIT = 128;                    // tokens of a unit
 constexpr int KT_BLOCK = 64;                    // tokens of a ring block
-constexpr int KT_SOFT = 8, KT_CODE = 4;         // warps
-constexpr int KT_MMA_WARP = KT_SOFT + KT_CODE, KT_COPY_WARP = KT_MMA_WARP + 1;
-constexpr int KT_THREADS = 32 * (KT_COPY_WARP + 1);     // 14 warps: 128 registers a thread
+
+// Warps: a tile's softmax by 8 (two threads a row, 64 of a unit's scores each),
+// the conversion by as many as it takes to keep up.  18 or 20 in all: 96
+// registers a thread.
+template <int NT>
+struct KtWarps {
+    static constexpr int SOFT = 8 * NT, CODE = NT == 2 ? 2 : 8;
+    static constexpr int MMA = SOFT + CODE, COPY = MMA + 1, THREADS = 32 * (COPY + 1);
+};
 
 template <int D, int NT>
 struct KtSmem {
@@ -48,7 +53,7 @@ struct KtSmem {
     static constexpr int TURN = 3, ENTRIES = 2 * TURN;  // entries of a group, and of both
     static constexpr int Q = NT * KT_ROWS * D * 2;
     static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
-    static constexpr int FACTOR = STAT + 6 * KT_ROWS * 4;       // scores' factors of the rows
+    static constexpr int FACTOR = STAT + NT * 6 * KT_ROWS * 4;       // scores' factors of the rows
     static constexpr int MASK = FACTOR + NT * KT_ROWS * 4;          // missing pages of the last eight units
     static constexpr int BARS = MASK + 8 * 4;
     // barriers
@@ -192,26 +197,11 @@ __device__ __forceinline__ void kt_scale(uint32_t at, float f)
     }
 }
 
-// 32 columns of this thread's row, fp16 pairs, times f.
-__device__ __forceinline__ void kt_scale_pairs(uint32_t at, float f)
-{
-    const uint32_t f2 = pack_f16x2(f, f);
-#pragma unroll 1
-    for (int c = 0; c < 32; c += 16) {
-        uint32_t x[16];
-        tmem_wait_st();                         // (they were stored just before)
-        tmem_ld(at + c, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = kv_mul2(x[e], f2);
-        tmem_st(at + c, x);
-    }
-}
-
 template <int D, int NT>
-__global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttnParams p)
+__global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(const KvAttnParams p)
 {
     using L = KtSmem<D, NT>;
+    using W = KtWarps<NT>;
     extern __shared__ __align__(1024) uint8_t kt_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(kt_smem);
@@ -229,12 +219,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         for (int i = 0; i < L::COUNT; ++i) {
             const bool codes = (i >= L::RAW_EMPTY && i < L::B_EMPTY);           // (RAW_EMPTY, B_FULL)
             const bool soft = (i >= L::P_FULL && i < L::O_DONE) || i >= L::Q_FULL;
-            mbar_init(bar(i), codes ? KT_CODE / 2 : soft ? KT_SOFT / NT : 1);
+            mbar_init(bar(i), codes ? W::CODE / 2 : soft ? 8 : 1);
         }
         *flag = 0;
         fence_barrier_init();
     }
-    if (warp == KT_MMA_WARP) {
+    if (warp == W::MMA) {
         tmem_alloc(smem_addr(const_cast<uint32_t *>(slot_tm)), L::TMEM);
         tmem_relinquish();
     }
@@ -244,8 +234,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
     const uint32_t tmem = *slot_tm;
     pdl_launch_dependents();
     pdl_wait_prior();
-    __shared__ KvPartSmem part_sm;
-    KvPart part = kv_part(p, part_sm);
+    // (found in what the ring is later)
+    static_assert(sizeof(KvPartSmem) <= L::BLOCK, "room for the parts");
+    KvPart part = kv_part(p, *reinterpret_cast<KvPartSmem *>(kt_smem + L::RING));
+    __syncthreads();
 
     // The order of an item's K and V blocks, step s of 2 n: with two tiles K0 V0
     // K1 V1 .., with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
@@ -259,7 +251,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
         return s & 1 ? Step{(s + 1) >> 1, false} : s ? Step{(s >> 1) - 1, true} : Step{0, false};
     };
 
-    if (warp == KT_COPY_WARP) {
+    if (warp == W::COPY) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
         // Lane j of 0 .. 3 has the unit's page j: of block j / 2, its entry's only
         // page or one of two.
@@ -324,13 +316,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             }
             units += n;
         }
-    } else if (warp >= KT_SOFT && warp < KT_MMA_WARP) {
+    } else if (warp >= W::SOFT && warp < W::MMA) {
         // ------------------------------------------------ codes to fp16
         // Two groups of warps take every other block: one's waits and stores
         // overlap the other's.
         constexpr int Q32 = D / 32;             // 32-dimension pieces of a token
-        constexpr int THREADS = KT_CODE * 16, ROUNDS = KT_BLOCK * Q32 / THREADS;
-        const int group = (warp - KT_SOFT) / (KT_CODE / 2), me = threadIdx.x & (THREADS - 1);
+        constexpr int THREADS = W::CODE * 16, ROUNDS = KT_BLOCK * Q32 / THREADS;
+        const int group = (warp - W::SOFT) / (W::CODE / 2), me = threadIdx.x & (THREADS - 1);
         KtTurn<L::TURN> entry;
         KtTurn<L::BLOCKS> block;
         if (group) block.next();
@@ -402,7 +394,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 block.next();
             }
         }
-    } else if (warp == KT_MMA_WARP) {
+    } else if (warp == W::MMA) {
         // ------------------------------------------------ products
         int block = 0;
         uint32_t bround = 0, items[2] = {0, 0};
@@ -419,7 +411,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const uint64_t b0 = kt_desc(base + L::RING + at * L::BLOCK, 1024, GROUP);
 #pragma unroll 1
             for (int k = 0; k < 2; ++k)
-                kt_mma4_ts_warp(tmem + L::O(tile), tmem + s + (NT == 2 ? 32 : 64) * k, b0 + k * (L::BLOCK >> 4), 2 * GROUP >> 4, kt_idesc(D, true),
+                kt_mma4_ts_warp(tmem + L::O(tile), tmem + s + 64 * k, b0 + k * (L::BLOCK >> 4), 2 * GROUP >> 4, kt_idesc(D, true),
                                 !first || k > 0);
         };
         auto full = [&](int at, uint32_t r) {
@@ -511,12 +503,16 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 }
             }
         }
-    } else if (warp < KT_SOFT) {
+    } else if (warp < W::SOFT) {
         // ------------------------------------------------ queries, softmax, outputs
-        const int group = warp >> 2, row = threadIdx.x & (KT_ROWS - 1);
-        const int tile = NT == 2 ? group : 0;
+        const int tile = warp >> 3, group = (warp >> 2) & 1, row = threadIdx.x & (KT_ROWS - 1);
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT), *factor = reinterpret_cast<float *>(kt_smem + L::FACTOR);
+        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT) + tile * 6 * KT_ROWS + row;
+        float *factor = reinterpret_cast<float *>(kt_smem + L::FACTOR);
+        auto together = [&]() {                 // the tile's warps
+            __syncwarp();
+            named_bar_sync(1 + tile, 256);
+        };
         uint32_t run = 0;                       // units of this thread's tile
         int units = 0;
         if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -530,14 +526,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             // The tile's queries as fp16, each row times a power of two that brings its largest value to [2^14, 2^15),
             // and the scores' sign: copied to their places and changed there, a row by D / 8 lanes with 16 bytes each.
             if (active) {
-                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, WARPS = KT_SOFT / NT, LOADS = KT_ROWS / (AT_ONCE * WARPS);
-                const int wq = NT == 2 ? warp & 3 : warp, sub = lane / LANES, piece = lane % LANES;
+                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, LOADS = KT_ROWS / (AT_ONCE * 8), BATCH = 4;
+                const int wq = warp & 7, sub = lane / LANES, piece = lane % LANES;
                 const unsigned peers = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << (sub * LANES);
                 const uint32_t to = base + tile * (KT_ROWS * D * 2) + (piece / 8) * (KT_ROWS * 128);
                 const int r0 = wq * LOADS * AT_ONCE + sub;
                 auto place = [&](int r) { return to + r * 128 + (((piece % 8) ^ (r & 7)) << 4); };
-                __syncwarp();
-                named_bar_sync(NT == 2 ? 1 + group : 1, KT_SOFT * 32 / NT);     // (the outputs before have left these places)
+                together();                     // (the outputs before have left these places)
 #pragma unroll 4
                 for (int i = 0; i < LOADS; ++i) {
                     const int r = r0 + i * AT_ONCE, pk = it.tile * p.tile + tile * KT_ROWS + r, tt = kv_token(p, pk);
@@ -546,24 +541,36 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 }
                 cp_async_commit();
                 cp_async_wait_all();
-#pragma unroll 2
-                for (int i = 0; i < LOADS; ++i) {
-                    const int r = r0 + i * AT_ONCE;
-                    uint4 v = lds128(place(r));
-                    if (tile * KT_ROWS + r >= rows) v = make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    unsigned top = 0;
+#pragma unroll 1
+                for (int i0 = 0; i0 < LOADS; i0 += BATCH) {
+                    uint4 v[BATCH];
+                    unsigned top[BATCH];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                    top = __reduce_max_sync(peers, top);
-                    const int shift = xres_shift(top);
-                    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
-                    uint32_t y[4];
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = r0 + (i0 + i) * AT_ONCE;
+                        v[i] = lds128(place(r));
+                        if (tile * KT_ROWS + r >= rows) v[i] = make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                    sts128(place(r), make_uint4(y[0], y[1], y[2], y[3]));
-                    if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                    for (int i = 0; i < BATCH; ++i) {
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        top[i] = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[i] = max(top[i], max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                    }
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) top[i] = __reduce_max_sync(peers, top[i]);
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = r0 + (i0 + i) * AT_ONCE, shift = xres_shift(top[i]);
+                        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale);
+                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                        sts128(place(r), make_uint4(w[0], w[1], w[2], w[3]));
+                        if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                    }
                 }
             }
             fence_proxy_async();
@@ -580,8 +587,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
             const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
             const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
             // (a warp's rows' factors come from other warps, which also arrive at this barrier)
-            __syncwarp();
-            named_bar_sync(NT == 2 ? 1 + group : 1, KT_SOFT * 32 / NT);
+            together();
             const float scale = factor[tile * KT_ROWS + row];
             float m = -INFINITY;
             f32x2 l2 = pack_x2(0.f, 0.f);
@@ -594,53 +600,49 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
                 const int first = it.span.at(it.unit + i) * KT_UNIT;
                 const unsigned gone = missing[(units + i) & 7];
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
-                // 64 scores at a time, in registers from their maximum to their probabilities
-                constexpr int HALVES = NT == 2 ? 2 : 1;
-                const int col0 = NT == 2 ? 0 : 64 * group;
-#pragma unroll 1
-                for (int h = 0; h < HALVES; ++h) {
+                // this thread's 64 scores: read for their maximum, and again for the probabilities (96 registers do
+                // not hold them meanwhile)
+                const uint32_t at = s0 + 64 * group;
+                const int page = 2 * group;
+                float top;
+                {
                     uint32_t x[2][32];
-                    const uint32_t at = s0 + col0 + 64 * h;
                     tmem_ld32(at, x[0]);
                     tmem_ld32(at + 32, x[1]);
                     tmem_wait_ld();
                     if (!all) {
-                        const int page = col0 / 32 + 2 * h;
                         kt_mask(x[0], sight(first + 32 * page, gone >> page));
                         kt_mask(x[1], sight(first + 32 * page + 32, gone >> (page + 1)));
                     }
-                    float top = kt_max(x[1], kt_max(x[0], -INFINITY));
-                    if (NT == 1) {              // the row's other half
-                        float *of = stat + (run & 1) * (2 * KT_ROWS) + row;     // (two of them: read before they are written again)
-                        of[group * KT_ROWS] = top;
+                    top = kt_max(x[1], kt_max(x[0], -INFINITY));
+                }
+                float *of = stat + (run & 1) * (2 * KT_ROWS);   // (two of them: read before they are written again)
+                of[group * KT_ROWS] = top;
+                together();
+                top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
+                if (top != -INFINITY) top *= scale;
+                const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
+                    m = to_m;
+                    l2 = mul_x2(l2, pack_x2(f, f));
+                    if (i > 0) {
+                        if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
                         __syncwarp();
-                        named_bar_sync(1, KT_SOFT * 32);
-                        top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
+                        tc_fence_after_sync();
+                        kt_scale<D / 2>(lanes + L::O(tile) + group * (D / 2), f);
                     }
-                    if (top != -INFINITY) top *= scale;
-                    const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
-                    if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
-                        m = to_m;
-                        l2 = mul_x2(l2, pack_x2(f, f));
-                        if (h) kt_scale_pairs(s0, f);
-                        if (i > 0) {
-                            if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
-                            __syncwarp();
-                            tc_fence_after_sync();
-                            constexpr int COLS = NT == 2 ? D : D / 2;
-                            kt_scale<COLS>(lanes + L::O(tile) + (NT == 2 ? 0 : group * COLS), f);
-                        }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t pr[16];
-                        kt_probabilities(x[j], scale2, minus, l2, pr);
-                        // (of this thread's columns, those that it has read)
-                        tmem_st(s0 + (NT == 2 ? 32 * h : col0) + 16 * j, pr);
-                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t x[32], pr[16];
+                    tmem_ld32(at + 32 * j, x);
+                    tmem_wait_ld();
+                    if (!all) kt_mask(x, sight(first + 32 * (page + j), gone >> (page + j)));
+                    kt_probabilities(x, scale2, minus, l2, pr);
+                    tmem_st(at + 16 * j, pr);   // (of this thread's columns, those that it has read)
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
@@ -651,26 +653,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
 
             // the row's sums
             float l = sum_x2(l2);
-            if (NT == 1) {
-                float *of = stat + 4 * KT_ROWS + row;
-                of[group * KT_ROWS] = l;
-                __syncwarp();
-                named_bar_sync(1, KT_SOFT * 32);
-                l = of[0] + of[KT_ROWS];
-            }
             if (active) {
+                float *of = stat + 4 * KT_ROWS;
+                of[group * KT_ROWS] = l;
+                together();
+                l = of[0] + of[KT_ROWS];
                 wait(bar(L::O_DONE + (NT == 2 ? tile : (run - 1) & 1)), NT == 2 ? run - 1 : (run - 1) >> 1);
                 __syncwarp();
                 tc_fence_after_sync();
                 const bool whole = part.whole();
                 const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
-                constexpr int COLS = NT == 2 ? D : D / 2;
-                const int c0 = NT == 2 ? 0 : group * COLS;
+                constexpr int COLS = D / 2;
+                const int c0 = group * COLS;
                 const long long slot = (2LL * blockIdx.x + (it.unit == 0)) * p.tile + mine;
                 // whole rows go through the queries' place, a warp's 32 rows in its eighth, so that a store has whole
                 // rows of neighbouring lanes
                 constexpr int CHUNKS = COLS / 8, TURNS = CHUNKS < 8 ? CHUNKS - 1 : 7;      // 16-byte pieces of a row
-                const uint32_t out = base + warp * (L::Q / KT_SOFT);
+                const uint32_t out = base + warp * (L::Q / W::SOFT);
 #pragma unroll 1
                 for (int c = 0; c < COLS; c += 32) {
                     uint32_t x[32];
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KvAttn
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == KT_MMA_WARP) {
+    if (warp == W::MMA) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, L::TMEM);
     }

@@ -31,15 +31,15 @@ def step(s, n, NT):
 
 
 def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
-    """items: (units, active tiles).  warps: of a conversion group, and of a softmax warpgroup."""
+    """items: (units, active tiles).  warps: of a conversion group, and half of a tile's softmax warps."""
     ENTRIES = 2 * TURN
-    soft = 2 * warps                             # softmax warps
+    soft = 2 * warps                             # of a tile
     raw_full = [Bar("raw_full%d" % i, 1) for i in range(ENTRIES)]
     raw_empty = [Bar("raw_empty%d" % i, warps) for i in range(ENTRIES)]
     b_full = [Bar("b_full%d" % i, warps) for i in range(BLOCKS)]
     b_empty = [Bar("b_empty%d" % i, 1) for i in range(BLOCKS)]
-    s_full, p_full = [Bar("s_full%d" % i, 1) for i in range(2)], [Bar("p_full%d" % i, soft // NT) for i in range(2)]
-    o_done, q_full = [Bar("o_done%d" % i, 1) for i in range(2)], [Bar("q_full%d" % i, soft // NT) for i in range(2)]
+    s_full, p_full = [Bar("s_full%d" % i, 1) for i in range(2)], [Bar("p_full%d" % i, soft) for i in range(2)]
+    o_done, q_full = [Bar("o_done%d" % i, 1) for i in range(2)], [Bar("q_full%d" % i, soft) for i in range(2)]
     tensor = []                                  # operations of the product warp, completing in order
     entry_holds, slot_holds = [None] * ENTRIES, [[None] * warps for _ in range(BLOCKS)]
     S = [None, None]                             # ("s" | "p", item, unit, parts written)
@@ -102,7 +102,7 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
         def scores(buf, tile, k, i, b):
             def done():
                 blocks(b, (k, i, False))
-                assert all(q == k for q in Q[tile][:soft // NT])
+                assert all(q == k for q in Q[tile][:soft])
                 S[buf] = ("s", k, i, set())
             tensor.append(("op", done))
             tensor.append(("commit", s_full[buf]))
@@ -110,7 +110,7 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
         def values(buf, tile, k, i, b, done_bar):
             def done():
                 blocks(b, (k, i, True))
-                assert S[buf][:3] == ("p", k, i) and len(S[buf][3]) == soft // NT, S[buf]
+                assert S[buf][:3] == ("p", k, i) and len(S[buf][3]) == soft, S[buf]
                 if i:
                     assert O[tile] == (k, i)
                 O[tile] = (k, i + 1)
@@ -175,23 +175,21 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
             yield None
 
     def softmax(warp):
-        group, run = warp // warps, 0
-        tile = group if NT == 2 else 0
-        me = warp % warps if NT == 2 else warp
+        tile, me, run = warp // soft, warp % soft, 0
         for k, (n, tiles) in enumerate(items):
             active = tile < tiles
             if active:
                 Q[tile][me] = k
                 yield None
                 q_full[tile].arrive()
-            yield from meet(("q", k, tile), me, soft // NT)
+            if active:
+                yield from meet(("q", k, tile), me, soft)
             for i in range(n if active else 0):
                 buf = tile if NT == 2 else run & 1
                 yield s_full[buf], run if NT == 2 else run >> 1
                 assert S[buf][1:3] == (k, i) and (S[buf][0] == "s" or me not in S[buf][3]), (S[buf], k, i)
                 yield None
-                if NT == 1:
-                    yield from meet(("max", k, i), me, soft)
+                yield from meet(("max", k, tile, i), me, soft)
                 if i and rng.random() < 0.5:     # the maximum moved: O is rescaled
                     if NT == 1:
                         yield o_done[(run - 1) & 1], (run - 1) >> 1
@@ -202,8 +200,8 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
                 S[buf] = ("p", k, i, S[buf][3] | {me})
                 p_full[buf].arrive()
                 run += 1
-            if NT == 1:
-                yield from meet(("sum", k), me, soft)
+            if active:
+                yield from meet(("sum", k, tile), me, soft)
             if active:
                 if NT == 2:
                     yield o_done[tile], run - 1
@@ -215,7 +213,7 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
 
     gens = {"copies": copies(), "products": products()}
     gens.update({"convert%d.%d" % (g, w): convert(g, w) for g in range(2) for w in range(warps)})
-    gens.update({"softmax%d" % w: softmax(w) for w in range(soft)})
+    gens.update({"softmax%d" % w: softmax(w) for w in range(NT * soft)})
     want = dict.fromkeys(gens)
     speed = {g: rng.random() ** 2 + 0.02 for g in gens}
     drain, idle = rng.random() ** 2 + 0.02, 0
