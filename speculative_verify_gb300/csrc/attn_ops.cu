@@ -155,7 +155,7 @@ AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
     a.tiles = packed <= KA_ROWS ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
     a.tile = a.tiles ? a.tiles * KT_ROWS : KA_ROWS;
     a.unit = a.tiles ? KT_UNIT : KV_PAGE;
-    a.least = a.tiles ? 2 : 2 * KA_WARPS;
+    a.least = a.tiles ? 4 : 2 * KA_WARPS;
     const int blocks = a.tiles ? 1 : d == 64 ? KaShape<64>::BLOCKS : d == 128 ? KaShape<128>::BLOCKS : KaShape<256>::BLOCKS;
     // (items, and their units, at most)
     const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);

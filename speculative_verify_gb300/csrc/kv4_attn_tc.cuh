@@ -2,25 +2,26 @@
 // 5th-generation tensor cores: prompts, and verify rows with more packed rows
 // than one mma.sync tile.
 //
-// An item (kv4_plan.cuh) is NT tiles of 128 packed rows, a unit 128 tokens.  A
-// unit's keys and values become fp16 in shared memory once for all tiles,
-// exactly (kv4.cuh), in a ring of 64-token blocks in the order in which the
-// products use them.  Scores S = Q K^T go to tensor memory (M128 N128, Q and K
-// from shared memory); the softmax warps turn them into fp16 probabilities over
-// S, in the same columns; O += P V takes P from tensor memory and V across.
+// An item (kv4_plan.cuh) is NT tiles of 128 packed rows, a unit 64 tokens.  A
+// unit's keys and its values become fp16 in shared memory once for all tiles,
+// exactly (kv4.cuh), as blocks of a ring in the order in which the products use
+// them.  Scores S = Q K^T (M128 N64) go to tensor memory, one buffer while the
+// softmax warps turn the other's into fp16 probabilities, in the same columns;
+// O += P V takes P from tensor memory and V across.  So the tensor cores form
+// the next unit's scores during a softmax.
 //
-// NT = 2 (d 64 and 128, more than 128 rows): each tile has its S and O and
-// softmax warps; while one tile's probabilities are formed, the tensor cores
-// work on the other's.  NT = 1 (fewer rows, or d 256, whose O fills half of the
-// tensor memory): the scores of consecutive units alternate between two
-// buffers, so that those of the next unit are formed during a softmax.
+// NT = 2 (d 64 and 128, more than 128 rows): O and two buffers of S for each
+// tile fill the tensor memory, and the queries stay in shared memory.  NT = 1
+// (fewer rows, or d 256): the queries are in tensor memory too -- from shared
+// memory they would take as much of its bandwidth as an M128 N64 product has.
 //
 // The softmax is that of kv4_attn.cuh: fp32, relative to a maximum that moves
 // only when a score passes it by 2^8, when O is rescaled in tensor memory by
 // the rows' own threads.
 //
-// Roles: the first 8 warps of each tile queries, softmax, O and outputs; then
-// codes to fp16; products; copies (bulk copies of the pages' codes and scales).
+// Roles: the first 8 warps queries, softmax, O and outputs (a thread a row with
+// two tiles, two with one); then codes to fp16; products; copies (bulk copies
+// of the pages' codes and scales).
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -30,45 +31,44 @@
 namespace sv {
 
 constexpr int KT_ROWS = 128;                    // packed rows of a tile
-constexpr int KT_UNIT = 128;                    // tokens of a unit
-constexpr int KT_BLOCK = 64;                    // tokens of a ring block
+constexpr int KT_UNIT = 64;                     // tokens of a unit, and of a ring block
 
-// Warps: a tile's softmax by 8 (two threads a row, 64 of a unit's scores each),
-// the conversion by as many as it takes to keep up.  18 or 20 in all: 96
-// registers a thread.
+// Warps.  18 with one tile, 96 registers a thread; 14 with two, 128.
 template <int NT>
 struct KtWarps {
-    static constexpr int SOFT = 8 * NT, CODE = NT == 2 ? 2 : 8;
+    static constexpr int SOFT = 8, CODE = NT == 2 ? 4 : 8;
     static constexpr int MMA = SOFT + CODE, COPY = MMA + 1, THREADS = 32 * (COPY + 1);
+    static constexpr int TILE = SOFT / NT;      // softmax warps of a tile
 };
 
 template <int D, int NT>
 struct KtSmem {
-    static constexpr int BLOCK = KT_BLOCK * D * 2;      // fp16 of 64 tokens' keys or values
+    static constexpr int BLOCK = KT_UNIT * D * 2;       // fp16 of a unit's keys or values
     static constexpr int BLOCKS = D == 256 ? 4 : 8;
     // codes and scales of an entry's tokens; each conversion group has a ring of
     // its own
     static constexpr int PIECES = D == 256 ? 2 : 1;     // entries of a block
-    static constexpr int ENTRY = KT_BLOCK / PIECES * (D / 2 + D / 16);
+    static constexpr int ENTRY = KT_UNIT / PIECES * (D / 2 + D / 16);
     static constexpr int TURN = 3, ENTRIES = 2 * TURN;  // entries of a group, and of both
     static constexpr int Q = NT * KT_ROWS * D * 2;
     static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
-    static constexpr int FACTOR = STAT + NT * 6 * KT_ROWS * 4;       // scores' factors of the rows
-    static constexpr int MASK = FACTOR + NT * KT_ROWS * 4;          // missing pages of the last eight units
-    static constexpr int BARS = MASK + 8 * 4;
+    static constexpr int FACTOR = STAT + 6 * KT_ROWS * 4;       // scores' factors of the rows
+    static constexpr int MASK = FACTOR + NT * KT_ROWS * 4;          // missing pages of the last 16 units
+    static constexpr int BARS = MASK + 16 * 4;
     // barriers
     static constexpr int RAW_FULL = 0, RAW_EMPTY = ENTRIES, B_FULL = 2 * ENTRIES, B_EMPTY = B_FULL + BLOCKS,
-                         S_FULL = B_EMPTY + BLOCKS, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, Q_FULL = O_DONE + 2,
-                         COUNT = Q_FULL + 2;
+                         S_FULL = B_EMPTY + BLOCKS, P_FULL = S_FULL + 2 * NT, O_DONE = P_FULL + 2 * NT,
+                         Q_FULL = O_DONE + 2 * NT, COUNT = Q_FULL + NT;
     static constexpr int USED = BARS + 8 * COUNT + 16;
     // (more than half of a multiprocessor's: two blocks would wait for each other's tensor memory)
     static constexpr int BYTES = USED > 116 * 1024 ? USED : 116 * 1024;
     static_assert(BYTES <= 232448, "shared memory of a block");
-    // tensor memory: O of a tile, then S
+    // tensor memory: O of the tiles, the queries (one tile), two S a tile
     static constexpr uint32_t O(int tile) { return static_cast<uint32_t>(tile * D); }
-    static constexpr uint32_t S(int i) { return static_cast<uint32_t>(NT * D + 128 * i); }
+    static constexpr uint32_t QUERY = NT * D;
+    static constexpr uint32_t S(int tile, int i) { return static_cast<uint32_t>(NT * D + (NT == 1 ? D / 2 : 0) + 64 * (2 * tile + i)); }
     static constexpr int TMEM = 512;
-    static_assert(NT * D + 256 <= TMEM, "tensor memory");
+    static_assert(S(NT - 1, 1) + 64 <= TMEM, "tensor memory");
 };
 
 // Instruction descriptor of an M = 128 product of n columns, fp16 operands.
@@ -99,9 +99,10 @@ __device__ __forceinline__ void kt_mma4_ss_warp(uint32_t d_tmem, uint64_t a, uin
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem] x B[smem], four K steps of 16: A 8 columns, B `step`
-// (in 16 bytes) apart.
-__device__ __forceinline__ void kt_mma4_ts_warp(uint32_t d_tmem, uint32_t a, uint64_t b, uint64_t step, uint32_t idesc, uint32_t accumulate)
+// D[tmem] (+)= A[tmem] x B[smem], four K steps of 16: A 8 columns apart, the
+// last two `skip` further, B `step` (in 16 bytes) apart.
+__device__ __forceinline__ void kt_mma4_ts_warp(uint32_t d_tmem, uint32_t a, uint32_t skip, uint64_t b, uint64_t step, uint32_t idesc,
+                                                uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p, e, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"
                  "elect.sync _|e, 0xffffffff;\n\t"
@@ -109,7 +110,7 @@ __device__ __forceinline__ void kt_mma4_ts_warp(uint32_t d_tmem, uint32_t a, uin
                  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
                  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
                  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}"
-                 ::"r"(d_tmem), "r"(a), "r"(a + 8u), "r"(a + 16u), "r"(a + 24u), "l"(b), "l"(b + step), "l"(b + 2u * step),
+                 ::"r"(d_tmem), "r"(a), "r"(a + 8u), "r"(a + 16u + skip), "r"(a + 24u + skip), "l"(b), "l"(b + step), "l"(b + 2u * step),
                    "l"(b + 3u * step), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
@@ -140,7 +141,7 @@ struct KtSight {
     int pos, low, sinks;
     // The bits below n of 32.
     static __device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
-    // Bit i: token first + i is seen.  (first is a page's; bit 0 of `missing`: the page is not there)
+    // Bit i: token first + i is seen.  (first is a page's first; bit 0 of `missing`: the page is not there)
     __device__ __forceinline__ unsigned operator()(int first, unsigned missing) const
     {
         const unsigned seen = below(pos - first + 1) & (~below(low - first) | below(sinks - first));
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         for (int i = 0; i < L::COUNT; ++i) {
             const bool codes = (i >= L::RAW_EMPTY && i < L::B_EMPTY);           // (RAW_EMPTY, B_FULL)
             const bool soft = (i >= L::P_FULL && i < L::O_DONE) || i >= L::Q_FULL;
-            mbar_init(bar(i), codes ? W::CODE / 2 : soft ? 8 : 1);
+            mbar_init(bar(i), codes ? W::CODE / 2 : soft ? W::TILE : 1);
         }
         *flag = 0;
         fence_barrier_init();
@@ -239,26 +240,28 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     KvPart part = kv_part(p, *reinterpret_cast<KvPartSmem *>(kt_smem + L::RING));
     __syncthreads();
 
-    // The order of an item's K and V blocks, step s of 2 n: with two tiles K0 V0
-    // K1 V1 .., with one K0 K1 V0 K2 V1 .. (the scores run a unit ahead).
+    // The order of an item's K and V blocks, step s of 2 n: K0 K1 V0 K2 V1 ..
+    // (the scores run a unit ahead).
     struct Step {
         int unit;
         bool v;
     };
     auto step = [](int s, int n) {
-        if (NT == 2) return Step{s >> 1, (s & 1) != 0};
         if (s == 2 * n - 1) return Step{n - 1, true};
         return s & 1 ? Step{(s + 1) >> 1, false} : s ? Step{(s >> 1) - 1, true} : Step{0, false};
     };
 
     if (warp == W::COPY) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
-        // Lane j of 0 .. 3 has the unit's page j: of block j / 2, its entry's only
-        // page or one of two.
+        // Lane j of 0 .. 1 has the unit's page j: its entry's only page or one of
+        // two.  The blocks' entries are the two groups' in turn.
         constexpr bool OWN = L::PIECES == 2;
-        const int ring = (lane & 3) >> 1, sub = lane & 1;
-        KtTurn<L::TURN> turn;                   // of that entry, in the ring of the block's group
-        if (OWN && sub) turn.next();
+        const int sub = lane & 1;
+        KtTurn<L::TURN> turn[2];
+        if (OWN && sub) {
+            turn[0].next();
+            turn[1].next();
+        }
         int units = 0;
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
@@ -273,14 +276,12 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
             const int n = part.units();
             // a unit's pages: entries of the table, asked for a unit ahead and looked at when they are needed
             auto wanted = [&](int i) {
-                const int at = it.span.at(it.unit + i) * (KT_UNIT / KV_PAGE) + (lane & 3);
+                const int at = it.span.at(it.unit + i) * (KT_UNIT / KV_PAGE) + sub;
                 return i < n && it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages ? at : -1;
             };
             const int32_t *table = p.kv.table + it.b * p.kv.ldt;
             int at_next = wanted(0), id_next = at_next >= 0 ? table[at_next] : 0, now = -1, prior = -1;
-#pragma unroll 1
-            for (int k = 0; k < 2 * n; ++k) {
-                const Step x = step(k, n);
+            auto block = [&](const Step &x, int k, KtTurn<L::TURN> &turn, int ring) {
                 int page;
                 if (!x.v) {
                     prior = now;
@@ -288,13 +289,13 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     if (at_next >= 0 && page < 0) atomicOr(p.err, KV_ERR_PAGE);
                     at_next = wanted(x.unit + 1);
                     if (at_next >= 0) id_next = table[at_next];
-                    const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 15u;
-                    if (lane == 0) missing[(units + x.unit) & 7] = gone;
+                    const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 3u;
+                    if (lane == 0) missing[(units + x.unit) & 15] = gone;
                 } else {
-                    page = NT == 2 || k == 2 * n - 1 ? now : prior;
+                    page = k == 2 * n - 1 ? now : prior;
                 }
                 const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0);
-                if (lane < 4) {
+                if (lane < 2) {
                     const int slot = ring * L::TURN + turn.at;
                     if (turn.round) wait(bar(L::RAW_EMPTY + slot), turn.round - 1);
                     const uint32_t full = bar(L::RAW_FULL + slot), to = base + L::RAW + slot * L::ENTRY;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     const int mine = OWN ? 0 : sub;
                     // (a copy may land before the entry's bytes are announced: the arrival is still to come)
                     if (mine == 0)
-                        mbar_arrive_expect_tx(full, (OWN ? here >> lane & 1u : __popc(here >> lane & 3u)) * (L::ENTRY / PAGES));
+                        mbar_arrive_expect_tx(full, (OWN ? here >> lane & 1u : __popc(here & 3u)) * (L::ENTRY / PAGES));
                     if (page >= 0) {
                         const uint8_t *src = p.kv.head<D>(page, it.h);
                         bulk_g2s(to + mine * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
@@ -313,6 +314,11 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     if (OWN) turn.next();
                 }
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int k = 0; k < 2 * n; k += 2) {
+                block(step(k, n), k, turn[0], 0);
+                block(step(k + 1, n), k + 1, turn[1], 1);
             }
             units += n;
         }
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         // Two groups of warps take every other block: one's waits and stores
         // overlap the other's.
         constexpr int Q32 = D / 32;             // 32-dimension pieces of a token
-        constexpr int THREADS = W::CODE * 16, ROUNDS = KT_BLOCK * Q32 / THREADS;
+        constexpr int THREADS = W::CODE * 16, ROUNDS = KT_UNIT * Q32 / THREADS;
         const int group = (warp - W::SOFT) / (W::CODE / 2), me = threadIdx.x & (THREADS - 1);
         KtTurn<L::TURN> entry;
         KtTurn<L::BLOCKS> block;
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         for (; part.left > 0; part.next(p)) {
             const int n = part.units();
 #pragma unroll 1
-            for (int b = 0; b < 2 * n; ++b) {   // (an item has whole pairs of blocks)
+            for (int b = group; b < 2 * n; b += 2) {    // (an item has an even number of blocks)
                 const bool v = step(b, n).v;
                 uint4 w[ROUNDS];
                 uint32_t sc[ROUNDS];
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     for (int k = 0; k < N; ++k) {
                         const int i = me + k * THREADS, row = i / Q32, q = i % Q32;
                         w[e * N + k] = *reinterpret_cast<const uint4 *>(raw + row * (D / 2) + 16 * q);
-                        sc[e * N + k] = *reinterpret_cast<const uint16_t *>(raw + KT_BLOCK / L::PIECES * D / 2 + row * (D / 16) + 2 * q);
+                        sc[e * N + k] = *reinterpret_cast<const uint16_t *>(raw + KT_UNIT / L::PIECES * D / 2 + row * (D / 16) + 2 * q);
                     }
                     free[e] = bar(L::RAW_EMPTY + slot);
                     entry.next();
@@ -396,122 +402,83 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         }
     } else if (warp == W::MMA) {
         // ------------------------------------------------ products
-        int block = 0;
-        uint32_t bround = 0, items[2] = {0, 0};
-        uint32_t run[2] = {0, 0};               // units of each tile (NT 1: of both buffers together, in run[0])
+        KtTurn<L::BLOCKS> block;
+        uint32_t items[NT] = {}, run[NT] = {};  // of each tile: items, units
         constexpr uint32_t GROUP = D / 64 * 1024;       // bytes of eight tokens of a block
-        auto scores = [&](int tile, uint32_t s, int at) {
-            const uint64_t a0 = kt_desc(base + tile * (KT_ROWS * D * 2), 16, 1024);
-            const uint64_t b0 = kt_desc(base + L::RING + at * L::BLOCK, 16, GROUP);
+        auto scores = [&](int tile, uint32_t s) {
+            const uint64_t b0 = kt_desc(base + L::RING + block.at * L::BLOCK, 16, GROUP);
+            if (NT == 1) {
 #pragma unroll 1
-            for (int k = 0; k < D / 64; ++k)
-                kt_mma4_ss_warp(tmem + s, a0 + k * (KT_ROWS * 128 >> 4), b0 + k * (1024 >> 4), kt_idesc(KT_UNIT, false), k > 0);
-        };
-        auto values = [&](int tile, uint32_t s, int at, bool first) {
-            const uint64_t b0 = kt_desc(base + L::RING + at * L::BLOCK, 1024, GROUP);
+                for (int k = 0; k < D / 64; ++k)
+                    kt_mma4_ts_warp(tmem + s, tmem + L::QUERY + 32 * k, 0, b0 + k * (1024 >> 4), 2, kt_idesc(KT_UNIT, false), k > 0);
+            } else {
+                const uint64_t a0 = kt_desc(base + tile * (KT_ROWS * D * 2), 16, 1024);
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k)
-                kt_mma4_ts_warp(tmem + L::O(tile), tmem + s + 64 * k, b0 + k * (L::BLOCK >> 4), 2 * GROUP >> 4, kt_idesc(D, true),
-                                !first || k > 0);
+                for (int k = 0; k < D / 64; ++k)
+                    kt_mma4_ss_warp(tmem + s, a0 + k * (KT_ROWS * 128 >> 4), b0 + k * (1024 >> 4), kt_idesc(KT_UNIT, false), k > 0);
+            }
         };
-        auto full = [&](int at, uint32_t r) {
-            wait(bar(L::B_FULL + at), r);
-            wait(bar(L::B_FULL + at + 1), r);
+        // (a row's first 32 probabilities are in the first 16 columns of S, the others from 32 on)
+        auto values = [&](int tile, uint32_t s, bool first) {
+            kt_mma4_ts_warp(tmem + L::O(tile), tmem + s, NT == 1 ? 16 : 0, kt_desc(base + L::RING + block.at * L::BLOCK, 1024, GROUP),
+                            2 * GROUP >> 4, kt_idesc(D, true), !first);
+        };
+        auto full = [&]() {
+            wait(bar(L::B_FULL + block.at), block.round);
             __syncwarp();
             tc_fence_after_sync();
         };
-        auto empty = [&](int at) {
-            tc_commit_warp(bar(L::B_EMPTY + at));
-            tc_commit_warp(bar(L::B_EMPTY + at + 1));
-        };
-        auto next = [&]() {                     // the next unit's pair of blocks
-            block += 2;
-            if (block == L::BLOCKS) {
-                block = 0;
-                ++bround;
-            }
+        auto done = [&]() {
+            tc_commit_warp(bar(L::B_EMPTY + block.at));
+            block.next();
         };
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
             const int n = part.units();
             const int tiles = NT == 2 && it.seq.n * p.G - it.tile * p.tile > KT_ROWS ? 2 : 1;
-            for (int t = 0; t < tiles; ++t) wait(bar(L::Q_FULL + t), items[t]++);
+            for (int t = 0; t < tiles; ++t) wait(bar(L::Q_FULL + t), t ? items[NT - 1]++ : items[0]++);
             __syncwarp();
             tc_fence_after_sync();
-            if (NT == 1) {
-                full(block, bround);
-                scores(0, L::S(run[0] & 1), block);
-                tc_commit_warp(bar(L::S_FULL + (run[0] & 1)));
-                empty(block);
-                next();
+            // (scores go over the probabilities of the unit before the last: after their product, in order)
 #pragma unroll 1
-                for (int i = 0; i < n; ++i, ++run[0]) {
-                    const uint32_t j = run[0];
-                    if (i + 1 < n) {
-                        full(block, bround);
-                        scores(0, L::S((j + 1) & 1), block);
-                        tc_commit_warp(bar(L::S_FULL + ((j + 1) & 1)));
-                        empty(block);
-                        next();
+            for (int i = -1; i < n; ++i) {
+                if (i + 1 < n) {
+                    full();
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (t >= tiles) continue;
+                        const uint32_t buf = (run[t] + (i < 0 ? 0 : 1)) & 1;
+                        scores(t, L::S(t, 0) + 64 * buf);
+                        tc_commit_warp(bar(L::S_FULL + 2 * t + buf));
                     }
-                    full(block, bround);
-                    wait(bar(L::P_FULL + (j & 1)), j >> 1);
+                    done();
+                }
+                if (i < 0) continue;
+                full();
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= tiles) continue;
+                    const uint32_t buf = run[t] & 1;
+                    wait(bar(L::P_FULL + 2 * t + buf), run[t] >> 1);
                     __syncwarp();
                     tc_fence_after_sync();
-                    values(0, L::S(j & 1), block, i == 0);
-                    tc_commit_warp(bar(L::O_DONE + (j & 1)));  // (two: the softmax may be that far behind)
-                    empty(block);
-                    next();
+                    values(t, L::S(t, 0) + 64 * buf, i == 0);
+                    tc_commit_warp(bar(L::O_DONE + 2 * t + buf));       // (two: the softmax may be that far behind)
+                    ++run[t];
                 }
-            } else {
-                // (a tile's next scores go over its probabilities: after their product, in order)
-                int kb = block;
-                uint32_t kr = bround;
-                full(kb, kr);
-#pragma unroll 1
-                for (int t = 0; t < tiles; ++t) {
-                    scores(t, L::S(t), kb);
-                    tc_commit_warp(bar(L::S_FULL + t));
-                }
-                empty(kb);
-                next();
-#pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    const int vb = block;
-                    full(vb, bround);
-                    next();
-                    kb = block;
-                    kr = bround;
-#pragma unroll 1
-                    for (int t = 0; t < tiles; ++t) {
-                        wait(bar(L::P_FULL + t), t ? run[1]++ : run[0]++);
-                        __syncwarp();
-                        tc_fence_after_sync();
-                        values(t, L::S(t), vb, i == 0);
-                        tc_commit_warp(bar(L::O_DONE + t));
-                        if (t + 1 == tiles) empty(vb);
-                        if (i + 1 < n) {
-                            if (t == 0) full(kb, kr);
-                            scores(t, L::S(t), kb);
-                            tc_commit_warp(bar(L::S_FULL + t));
-                        }
-                    }
-                    if (i + 1 < n) {
-                        empty(kb);
-                        next();
-                    }
-                }
+                done();
             }
         }
     } else if (warp < W::SOFT) {
         // ------------------------------------------------ queries, softmax, outputs
-        const int tile = warp >> 3, group = (warp >> 2) & 1, row = threadIdx.x & (KT_ROWS - 1);
+        constexpr int SPLIT = 2 / NT;           // threads of a row
+        const int tile = NT == 2 ? warp >> 2 : 0, group = NT == 2 ? 0 : warp >> 2, row = threadIdx.x & (KT_ROWS - 1);
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT) + tile * 6 * KT_ROWS + row;
+        float *stat = reinterpret_cast<float *>(kt_smem + L::STAT) + row;
         float *factor = reinterpret_cast<float *>(kt_smem + L::FACTOR);
         auto together = [&]() {                 // the tile's warps
             __syncwarp();
-            named_bar_sync(1 + tile, 256);
+            named_bar_sync(1 + tile, 32 * W::TILE);
         };
         uint32_t run = 0;                       // units of this thread's tile
         int units = 0;
@@ -526,8 +493,8 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
             // The tile's queries as fp16, each row times a power of two that brings its largest value to [2^14, 2^15),
             // and the scores' sign: copied to their places and changed there, a row by D / 8 lanes with 16 bytes each.
             if (active) {
-                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, LOADS = KT_ROWS / (AT_ONCE * 8), BATCH = 4;
-                const int wq = warp & 7, sub = lane / LANES, piece = lane % LANES;
+                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, LOADS = KT_ROWS / (AT_ONCE * W::TILE), BATCH = 4;
+                const int wq = warp & (W::TILE - 1), sub = lane / LANES, piece = lane % LANES;
                 const unsigned peers = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << (sub * LANES);
                 const uint32_t to = base + tile * (KT_ROWS * D * 2) + (piece / 8) * (KT_ROWS * 128);
                 const int r0 = wq * LOADS * AT_ONCE + sub;
@@ -573,7 +540,24 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     }
                 }
             }
-            fence_proxy_async();
+            if (NT == 1) {                      // and this thread's part of its row to tensor memory
+                together();
+#pragma unroll 1
+                for (int c = 0; c < D / 4; c += 16) {
+                    uint32_t x[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int piece = group * (D / 16) + c / 4 + e;
+                        const uint4 v = lds128(base + (piece / 8) * (KT_ROWS * 128) + row * 128 + (((piece % 8) ^ (row & 7)) << 4));
+                        x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
+                    }
+                    tmem_st(lanes + L::QUERY + group * (D / 4) + c, x);
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+            } else {
+                fence_proxy_async();
+            }
             __syncwarp();
             if (lane == 0 && active) mbar_arrive(bar(L::Q_FULL + tile));
 
@@ -592,34 +576,32 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
             float m = -INFINITY;
             f32x2 l2 = pack_x2(0.f, 0.f);
             for (int i = 0; active && i < n; ++i, ++run) {
-                const uint32_t buf = NT == 2 ? tile : run & 1, parity = NT == 2 ? run : run >> 1;
-                const uint32_t s0 = lanes + L::S(buf);
-                wait(bar(L::S_FULL + buf), parity);
+                const uint32_t buf = run & 1;
+                constexpr int CHUNKS = 2 / SPLIT;       // of 32 scores: this thread's
+                const uint32_t at = lanes + L::S(tile, 0) + 64 * buf + 32 * group;
+                wait(bar(L::S_FULL + 2 * tile + buf), run >> 1);
                 __syncwarp();
                 tc_fence_after_sync();
+                uint32_t x[CHUNKS][32];
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) tmem_ld32(at + 32 * j, x[j]);
                 const int first = it.span.at(it.unit + i) * KT_UNIT;
-                const unsigned gone = missing[(units + i) & 7];
+                const unsigned gone = missing[(units + i) & 15];
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
-                // this thread's 64 scores: read for their maximum, and again for the probabilities (96 registers do
-                // not hold them meanwhile)
-                const uint32_t at = s0 + 64 * group;
-                const int page = 2 * group;
-                float top;
-                {
-                    uint32_t x[2][32];
-                    tmem_ld32(at, x[0]);
-                    tmem_ld32(at + 32, x[1]);
-                    tmem_wait_ld();
-                    if (!all) {
-                        kt_mask(x[0], sight(first + 32 * page, gone >> page));
-                        kt_mask(x[1], sight(first + 32 * page + 32, gone >> (page + 1)));
-                    }
-                    top = kt_max(x[1], kt_max(x[0], -INFINITY));
+                tmem_wait_ld();
+                if (!all) {
+#pragma unroll
+                    for (int j = 0; j < CHUNKS; ++j) kt_mask(x[j], sight(first + 32 * (group + j), gone >> (group + j)));
                 }
-                float *of = stat + (run & 1) * (2 * KT_ROWS);   // (two of them: read before they are written again)
-                of[group * KT_ROWS] = top;
-                together();
-                top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) top = kt_max(x[j], top);
+                if (SPLIT == 2) {               // the row's other half
+                    float *of = stat + (run & 1) * (2 * KT_ROWS);       // (two of them: read before they are written again)
+                    of[group * KT_ROWS] = top;
+                    together();
+                    top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
+                }
                 if (top != -INFINITY) top *= scale;
                 const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
                 if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -627,43 +609,42 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     m = to_m;
                     l2 = mul_x2(l2, pack_x2(f, f));
                     if (i > 0) {
-                        if (NT == 1) wait(bar(L::O_DONE + ((run - 1) & 1)), (run - 1) >> 1);    // (with two tiles S has waited for it)
+                        wait(bar(L::O_DONE + 2 * tile + ((run - 1) & 1)), (run - 1) >> 1);
                         __syncwarp();
                         tc_fence_after_sync();
-                        kt_scale<D / 2>(lanes + L::O(tile) + group * (D / 2), f);
+                        kt_scale<D / SPLIT>(lanes + L::O(tile) + group * (D / SPLIT), f);
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t x[32], pr[16];
-                    tmem_ld32(at + 32 * j, x);
-                    tmem_wait_ld();
-                    if (!all) kt_mask(x, sight(first + 32 * (page + j), gone >> (page + j)));
-                    kt_probabilities(x, scale2, minus, l2, pr);
-                    tmem_st(at + 16 * j, pr);   // (of this thread's columns, those that it has read)
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) {
+                    uint32_t pr[16];
+                    kt_probabilities(x[j], scale2, minus, l2, pr);
+                    tmem_st(at + 16 * j, pr);   // (of this thread's columns, which it has read)
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::P_FULL + buf));
+                if (lane == 0) mbar_arrive(bar(L::P_FULL + 2 * tile + buf));
             }
             units += n;
 
             // the row's sums
             float l = sum_x2(l2);
             if (active) {
-                float *of = stat + 4 * KT_ROWS;
-                of[group * KT_ROWS] = l;
-                together();
-                l = of[0] + of[KT_ROWS];
-                wait(bar(L::O_DONE + (NT == 2 ? tile : (run - 1) & 1)), NT == 2 ? run - 1 : (run - 1) >> 1);
+                if (SPLIT == 2) {
+                    float *of = stat + 4 * KT_ROWS;
+                    of[group * KT_ROWS] = l;
+                    together();
+                    l = of[0] + of[KT_ROWS];
+                }
+                wait(bar(L::O_DONE + 2 * tile + ((run - 1) & 1)), (run - 1) >> 1);
                 __syncwarp();
                 tc_fence_after_sync();
                 const bool whole = part.whole();
                 const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
-                constexpr int COLS = D / 2;
+                constexpr int COLS = D / SPLIT;
                 const int c0 = group * COLS;
                 const long long slot = (2LL * blockIdx.x + (it.unit == 0)) * p.tile + mine;
                 // whole rows go through the queries' place, a warp's 32 rows in its eighth, so that a store has whole

@@ -3,7 +3,7 @@
 //
 // Query rows are packed: row r of a sequence and key/value head is token
 // r / G, query head r % G of the head's G.  An item is a tile of packed rows of
-// one head; its units are the pages, or blocks of four, that some row of the
+// one head; its units are the pages, or pairs of them, that some row of the
 // tile sees (those of the first tokens, then those of the window).  The items of head 0, then
 // head 1 and so on make one line of units, cut into equal parts, one for a
 // thread block: uneven sequences and triangles of prompts cost no balance, and

@@ -1,55 +1,55 @@
 """The barrier protocol of the tcgen05 attention kernel, replayed on the CPU.
 
 Each role of `kv4_attn_tc_kernel` (copies, the two conversion groups' warps,
-products, the softmax warpgroups' warps) is written here as the sequence of
-mbarrier waits and arrivals it performs, with the same counts and phase
-arithmetic as the kernel; the tensor core's completions come later, in order.
-A random scheduler runs the roles.  A wait is checked the way the hardware
-answers it (the parity of the barrier's current phase): the run fails if a
-wait could be answered before its phase completed or after the barrier moved
-two phases past it, or if no role can move.  What the barriers protect is
-checked too: the codes in an entry when they are read, the block in a ring slot
-when a product reads it, the scores, probabilities and outputs in tensor memory."""
+products, the tiles' softmax warps) is written here as the sequence of mbarrier
+waits and arrivals it performs, with the same counts and phase arithmetic as
+the kernel; the tensor core's completions come later, in order.  A random
+scheduler runs the roles.  A wait is checked the way the hardware answers it
+(the parity of the barrier's current phase): the run fails if a wait could be
+answered before its phase completed or after the barrier moved two phases past
+it, or if no role can move.  What the barriers protect is checked too: the
+codes in an entry when they are read, the block in a ring slot when a product
+reads it, the scores, probabilities and outputs in tensor memory, and the marks
+of missing pages."""
 import os
 import random
 import re
 
 import pytest
 
-from test_tc_protocol import Aliasing, Bar
+from test_tc_protocol import Bar
 
 SRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_verify_gb300", "csrc",
                    "kv4_attn_tc.cuh")
 
 
-def step(s, n, NT):
-    if NT == 2:
-        return s >> 1, bool(s & 1)
+def step(s, n):
+    """The block of step s: (unit, whether it is of values)."""
     if s == 2 * n - 1:
         return n - 1, True
     return ((s + 1) >> 1, False) if s & 1 else ((s >> 1) - 1, True) if s else (0, False)
 
 
-def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
-    """items: (units, active tiles).  warps: of a conversion group, and half of a tile's softmax warps."""
+def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
+    """items: (units, active tiles).  warps: of a conversion group, and of a tile's softmax."""
     ENTRIES = 2 * TURN
-    soft = 2 * warps                             # of a tile
     raw_full = [Bar("raw_full%d" % i, 1) for i in range(ENTRIES)]
     raw_empty = [Bar("raw_empty%d" % i, warps) for i in range(ENTRIES)]
     b_full = [Bar("b_full%d" % i, warps) for i in range(BLOCKS)]
     b_empty = [Bar("b_empty%d" % i, 1) for i in range(BLOCKS)]
-    s_full, p_full = [Bar("s_full%d" % i, 1) for i in range(2)], [Bar("p_full%d" % i, soft) for i in range(2)]
-    o_done, q_full = [Bar("o_done%d" % i, 1) for i in range(2)], [Bar("q_full%d" % i, soft) for i in range(2)]
+    s_full, o_done = ([[Bar("%s%d.%d" % (x, t, i), 1) for i in range(2)] for t in range(NT)] for x in "so")
+    p_full = [[Bar("p_full%d.%d" % (t, i), warps) for i in range(2)] for t in range(NT)]
+    q_full = [Bar("q_full%d" % t, warps) for t in range(NT)]
     tensor = []                                  # operations of the product warp, completing in order
     entry_holds, slot_holds = [None] * ENTRIES, [[None] * warps for _ in range(BLOCKS)]
-    S = [None, None]                             # ("s" | "p", item, unit, parts written)
-    O = [None, None]                             # (item, units added) of a tile
-    Q = [[None] * soft for _ in range(2)]
-    names = []                                   # every block in order: (item, unit, v, half)
+    S = [[None, None] for _ in range(NT)]        # ("s" | "p", item, unit, parts written)
+    O = [None] * NT                              # (item, units added)
+    Q = [[None] * warps for _ in range(NT)]
+    marks = [None] * MARKS                       # the unit that a mark is of
+    names, unit0 = [], []                        # every block in order: (item, unit, v); units before an item
     for k, (n, _) in enumerate(items):
-        for s in range(2 * n):
-            i, v = step(s, n, NT)
-            names += [(k, i, v, 0), (k, i, v, 1)]
+        unit0.append(sum(m for m, _ in items[:k]))
+        names += [(k, *step(s, n)) for s in range(2 * n)]
 
     def entries(e):
         """(slot, round) of the entries of block e."""
@@ -59,6 +59,8 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
 
     def copies():
         for e, name in enumerate(names):
+            if not name[2]:
+                marks[(unit0[name[0]] + name[1]) % MARKS] = name[:2]
             for at, rnd in entries(e):
                 if rnd:
                     yield raw_empty[at], rnd - 1
@@ -83,137 +85,92 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
             b_full[at].arrive()
 
     def products():
-        at, items_of, units_of = [0], [0, 0], [0, 0]
+        block, items_of, units_of = 0, [0] * NT, [0] * NT
 
-        def pair(move=True):
-            b = at[0]
-            if move:
-                at[0] += 2
-            return b
+        def holds(b, name):
+            assert all(x == name for x in slot_holds[b % BLOCKS]), (slot_holds[b % BLOCKS], name)
 
-        def full(b):
-            for h in range(2):
-                yield b_full[(b + h) % BLOCKS], (b + h) // BLOCKS
-
-        def blocks(b, name):
-            for h in range(2):
-                assert all(x == (*name, h) for x in slot_holds[(b + h) % BLOCKS]), (slot_holds[(b + h) % BLOCKS], name, h)
-
-        def scores(buf, tile, k, i, b):
+        def scores(t, buf, k, i, b):
             def done():
-                blocks(b, (k, i, False))
-                assert all(q == k for q in Q[tile][:soft])
-                S[buf] = ("s", k, i, set())
-            tensor.append(("op", done))
-            tensor.append(("commit", s_full[buf]))
+                holds(b, (k, i, False))
+                assert all(q == k for q in Q[t])
+                S[t][buf] = ("s", k, i, set())
+            tensor.extend([("op", done), ("commit", s_full[t][buf])])
 
-        def values(buf, tile, k, i, b, done_bar):
+        def values(t, buf, k, i, b):
             def done():
-                blocks(b, (k, i, True))
-                assert S[buf][:3] == ("p", k, i) and len(S[buf][3]) == soft, S[buf]
+                holds(b, (k, i, True))
+                assert S[t][buf][:3] == ("p", k, i) and len(S[t][buf][3]) == warps, S[t][buf]
                 if i:
-                    assert O[tile] == (k, i)
-                O[tile] = (k, i + 1)
-            tensor.append(("op", done))
-            tensor.append(("commit", o_done[done_bar]))
-
-        def empty(b):
-            for h in range(2):
-                tensor.append(("commit", b_empty[(b + h) % BLOCKS]))
+                    assert O[t] == (k, i)
+                O[t] = (k, i + 1)
+            tensor.extend([("op", done), ("commit", o_done[t][buf])])
 
         for k, (n, tiles) in enumerate(items):
             for t in range(tiles):
                 yield q_full[t], items_of[t]
                 items_of[t] += 1
-            if NT == 1:
-                b = pair()
-                yield from full(b)
-                scores(units_of[0] & 1, 0, k, 0, b)
-                empty(b)
-                for i in range(n):
-                    j = units_of[0]
-                    if i + 1 < n:
-                        b = pair()
-                        yield from full(b)
-                        scores((j + 1) & 1, 0, k, i + 1, b)
-                        empty(b)
-                    b = pair()
-                    yield from full(b)
-                    yield p_full[j & 1], j >> 1
-                    values(j & 1, 0, k, i, b, j & 1)
-                    empty(b)
-                    units_of[0] += 1
-            else:
-                b = pair()
-                yield from full(b)
-                for t in range(tiles):
-                    scores(t, t, k, 0, b)
-                empty(b)
-                for i in range(n):
-                    vb = pair()
-                    yield from full(vb)
-                    kb = pair(False)
+            for i in range(-1, n):
+                if i + 1 < n:
+                    yield b_full[block % BLOCKS], block // BLOCKS
                     for t in range(tiles):
-                        yield p_full[t], units_of[t]
-                        units_of[t] += 1
-                        values(t, t, k, i, vb, t)
-                        if t + 1 == tiles:
-                            empty(vb)
-                        if i + 1 < n:
-                            if t == 0:
-                                yield from full(kb)
-                            scores(t, t, k, i + 1, kb)
-                    if i + 1 < n:
-                        empty(kb)
-                        pair()
+                        scores(t, (units_of[t] + (i >= 0)) & 1, k, i + 1, block)
+                    tensor.append(("commit", b_empty[block % BLOCKS]))
+                    block += 1
+                if i < 0:
+                    continue
+                yield b_full[block % BLOCKS], block // BLOCKS
+                for t in range(tiles):
+                    yield p_full[t][units_of[t] & 1], units_of[t] >> 1
+                    values(t, units_of[t] & 1, k, i, block)
+                    units_of[t] += 1
+                tensor.append(("commit", b_empty[block % BLOCKS]))
+                block += 1
 
     arrived = {}
 
-    def meet(key, who, count):                   # a named barrier
+    def meet(key, who):                          # a named barrier of a tile
         arrived.setdefault(key, set()).add(who)
-        while len(arrived[key]) < count:
+        while len(arrived[key]) < warps:
             yield None
 
-    def softmax(warp):
-        tile, me, run = warp // soft, warp % soft, 0
+    def softmax(t, me):
+        u = 0
         for k, (n, tiles) in enumerate(items):
-            active = tile < tiles
-            if active:
-                Q[tile][me] = k
+            if t >= tiles:
+                continue
+            yield from meet(("before", k, t), me)
+            Q[t][me] = k
+            yield None
+            q_full[t].arrive()
+            yield from meet(("q", k, t), me)
+            for i in range(n):
+                buf = u & 1
+                yield s_full[t][buf], u >> 1
+                assert S[t][buf][1:3] == (k, i) and (S[t][buf][0] == "s" or me not in S[t][buf][3]), (S[t][buf], k, i)
+                assert marks[(unit0[k] + i) % MARKS] == (k, i), (marks, k, i)
                 yield None
-                q_full[tile].arrive()
-            if active:
-                yield from meet(("q", k, tile), me, soft)
-            for i in range(n if active else 0):
-                buf = tile if NT == 2 else run & 1
-                yield s_full[buf], run if NT == 2 else run >> 1
-                assert S[buf][1:3] == (k, i) and (S[buf][0] == "s" or me not in S[buf][3]), (S[buf], k, i)
-                yield None
-                yield from meet(("max", k, tile, i), me, soft)
+                if NT == 1:
+                    yield from meet(("max", k, i), me)
                 if i and rng.random() < 0.5:     # the maximum moved: O is rescaled
-                    if NT == 1:
-                        yield o_done[(run - 1) & 1], (run - 1) >> 1
-                    assert O[tile] == (k, i), (O[tile], k, i)
+                    yield o_done[t][(u - 1) & 1], (u - 1) >> 1
+                    assert O[t] == (k, i), (O[t], k, i)
                     yield None
-                    assert O[tile] == (k, i)
+                    assert O[t] == (k, i)
                 yield None
-                S[buf] = ("p", k, i, S[buf][3] | {me})
-                p_full[buf].arrive()
-                run += 1
-            if active:
-                yield from meet(("sum", k, tile), me, soft)
-            if active:
-                if NT == 2:
-                    yield o_done[tile], run - 1
-                else:
-                    yield o_done[(run - 1) & 1], (run - 1) >> 1
-                assert O[tile] == (k, n)
-                yield None
-                assert O[tile] == (k, n)
+                S[t][buf] = ("p", k, i, S[t][buf][3] | {me})
+                p_full[t][buf].arrive()
+                u += 1
+            if NT == 1:
+                yield from meet(("sum", k), me)
+            yield o_done[t][(u - 1) & 1], (u - 1) >> 1
+            assert O[t] == (k, n)
+            yield None
+            assert O[t] == (k, n)
 
     gens = {"copies": copies(), "products": products()}
     gens.update({"convert%d.%d" % (g, w): convert(g, w) for g in range(2) for w in range(warps)})
-    gens.update({"softmax%d" % w: softmax(w) for w in range(NT * soft)})
+    gens.update({"softmax%d.%d" % (t, w): softmax(t, w) for t in range(NT) for w in range(warps)})
     want = dict.fromkeys(gens)
     speed = {g: rng.random() ** 2 + 0.02 for g in gens}
     drain, idle = rng.random() ** 2 + 0.02, 0
@@ -241,16 +198,16 @@ def run(NT, BLOCKS, PIECES, TURN, items, rng, warps=2):
 
 
 def items(rng, NT):
-    return [(rng.choice([1, 1, 2, 3, 4, 7, 11]), rng.randint(1, NT)) for _ in range(rng.randint(1, 8))]
+    return [(rng.choice([1, 1, 2, 3, 4, 7, 11, 25]), rng.randint(1, NT)) for _ in range(rng.randint(1, 8))]
 
 
 def constants():
-    """(blocks, entries of a block, entries of a group) of d 256, and of the others, as the kernel has them."""
+    """(blocks, entries of a block, entries of a group, marks) of d 256, and of the others, as the kernel has them."""
     s = open(SRC).read()
     b = re.search(r"BLOCKS = D == 256 \? (\d+) : (\d+);", s)
     e = re.search(r"PIECES = D == 256 \? (\d+) : (\d+);", s)
-    t = re.search(r"TURN = (\d+),", s)
-    return tuple((int(b[i]), int(e[i]), int(t[1])) for i in (1, 2))
+    t, m = re.search(r"TURN = (\d+),", s), re.search(r"BARS = MASK \+ (\d+) \* 4;", s)
+    return tuple((int(b[i]), int(e[i]), int(t[1]), int(m[1])) for i in (1, 2))
 
 
 @pytest.mark.parametrize("NT,wide", [(1, True), (1, False), (2, False)])
