@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     using L = KtSmem<D, NT>;
     using W = KtWarps<NT>;
     extern __shared__ __align__(1024) uint8_t kt_smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the same for the warp, and so that the compiler knows it)
+    auto uniform = [](auto x) { return __shfl_sync(0xFFFFFFFFu, x, 0); };
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(kt_smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(kt_smem + L::BARS);
     volatile int *flag = reinterpret_cast<volatile int *>(bars + L::COUNT);
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *slot_tm;
+    const uint32_t tmem = uniform(static_cast<uint32_t>(*slot_tm));
     pdl_launch_dependents();
     pdl_wait_prior();
     // (found in what the ring is later)
@@ -253,15 +255,14 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
 
     if (warp == W::COPY) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
-        // Lane j of 0 .. 1 has the unit's page j: its entry's only page or one of
-        // two.  The blocks' entries are the two groups' in turn.
+        // Two blocks at a time: lanes 0 and 1 have the pages of the first, in the
+        // first conversion group's ring, lanes 2 and 3 those of the second; a page
+        // is its entry's only one or one of two.
         constexpr bool OWN = L::PIECES == 2;
-        const int sub = lane & 1;
-        KtTurn<L::TURN> turn[2];
-        if (OWN && sub) {
-            turn[0].next();
-            turn[1].next();
-        }
+        constexpr int PAGES = OWN ? 1 : 2;
+        const int ring = (lane >> 1) & 1, sub = lane & 1, mine = OWN ? 0 : sub;
+        KtTurn<L::TURN> turn;
+        if (OWN && sub) turn.next();
         int units = 0;
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
@@ -274,36 +275,26 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     prefetch_l2(p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D, 2 * D);
             }
             const int n = part.units();
-            // a unit's pages: entries of the table, asked for a unit ahead and looked at when they are needed
-            auto wanted = [&](int i) {
-                const int at = it.span.at(it.unit + i) * (KT_UNIT / KV_PAGE) + sub;
-                return i < n && it.seq.before >= 0 && at * KV_PAGE <= last && at < p.kv.max_pages ? at : -1;
-            };
+            // a block's page: its entry in the table, asked for two blocks ahead and looked at when it is needed
             const int32_t *table = p.kv.table + it.b * p.kv.ldt;
-            int at_next = wanted(0), id_next = at_next >= 0 ? table[at_next] : 0, now = -1, prior = -1;
-            auto block = [&](const Step &x, int k, KtTurn<L::TURN> &turn, int ring) {
-                int page;
-                if (!x.v) {
-                    prior = now;
-                    page = now = at_next >= 0 ? p.kv.page(id_next) : -1;
-                    if (at_next >= 0 && page < 0) atomicOr(p.err, KV_ERR_PAGE);
-                    at_next = wanted(x.unit + 1);
-                    if (at_next >= 0) id_next = table[at_next];
-                    const unsigned gone = __ballot_sync(0xFFFFFFFFu, page < 0) & 3u;
-                    if (lane == 0) missing[(units + x.unit) & 15] = gone;
-                } else {
-                    page = k == 2 * n - 1 ? now : prior;
-                }
-                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0);
-                if (lane < 2) {
+            const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
+            auto wanted = [&](int k) { return k < 2 * n ? it.span.at(it.unit + step(k, n).unit) * (KT_UNIT / KV_PAGE) + sub : pages; };
+            int at = wanted(ring), id = at < pages ? table[at] : 0;
+#pragma unroll 1
+            for (int k = ring; k < 2 * n; k += 2) {
+                const Step x = step(k, n);
+                const int page = at < pages ? p.kv.page(id) : -1;
+                if (at < pages && page < 0) atomicOr(p.err, KV_ERR_PAGE);
+                at = wanted(k + 2);
+                if (at < pages) id = table[at];
+                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0) >> (2 * ring) & 3u;
+                if (lane < 4) {
+                    if (!x.v && sub == 0) missing[(units + x.unit) & 15] = ~here & 3u;
                     const int slot = ring * L::TURN + turn.at;
                     if (turn.round) wait(bar(L::RAW_EMPTY + slot), turn.round - 1);
                     const uint32_t full = bar(L::RAW_FULL + slot), to = base + L::RAW + slot * L::ENTRY;
-                    constexpr int PAGES = OWN ? 1 : 2;
-                    const int mine = OWN ? 0 : sub;
                     // (a copy may land before the entry's bytes are announced: the arrival is still to come)
-                    if (mine == 0)
-                        mbar_arrive_expect_tx(full, (OWN ? here >> lane & 1u : __popc(here & 3u)) * (L::ENTRY / PAGES));
+                    if (mine == 0) mbar_arrive_expect_tx(full, (OWN ? here >> sub & 1u : __popc(here)) * (L::ENTRY / PAGES));
                     if (page >= 0) {
                         const uint8_t *src = p.kv.head<D>(page, it.h);
                         bulk_g2s(to + mine * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
@@ -314,11 +305,6 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     if (OWN) turn.next();
                 }
                 __syncwarp();
-            };
-#pragma unroll 1
-            for (int k = 0; k < 2 * n; k += 2) {
-                block(step(k, n), k, turn[0], 0);
-                block(step(k + 1, n), k + 1, turn[1], 1);
             }
             units += n;
         }
@@ -408,12 +394,12 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         auto scores = [&](int tile, uint32_t s) {
             const uint64_t b0 = kt_desc(base + L::RING + block.at * L::BLOCK, 16, GROUP);
             if (NT == 1) {
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < D / 64; ++k)
                     kt_mma4_ts_warp(tmem + s, tmem + L::QUERY + 32 * k, 0, b0 + k * (1024 >> 4), 2, kt_idesc(KT_UNIT, false), k > 0);
             } else {
                 const uint64_t a0 = kt_desc(base + tile * (KT_ROWS * D * 2), 16, 1024);
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < D / 64; ++k)
                     kt_mma4_ss_warp(tmem + s, a0 + k * (KT_ROWS * 128 >> 4), b0 + k * (1024 >> 4), kt_idesc(KT_UNIT, false), k > 0);
             }
@@ -432,10 +418,10 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
             tc_commit_warp(bar(L::B_EMPTY + block.at));
             block.next();
         };
-        for (; part.left > 0; part.next(p)) {
+        for (; uniform(static_cast<int>(part.left > 0)); part.next(p)) {
             const KvItem &it = part.item;
-            const int n = part.units();
-            const int tiles = NT == 2 && it.seq.n * p.G - it.tile * p.tile > KT_ROWS ? 2 : 1;
+            const int n = uniform(part.units());
+            const int tiles = uniform(NT == 2 && it.seq.n * p.G - it.tile * p.tile > KT_ROWS ? 2 : 1);
             for (int t = 0; t < tiles; ++t) wait(bar(L::Q_FULL + t), t ? items[NT - 1]++ : items[0]++);
             __syncwarp();
             tc_fence_after_sync();

@@ -57,16 +57,20 @@ def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
             i = e // 2 * PIECES + x
             yield e % 2 * TURN + i % TURN, i // TURN
 
-    def copies():
-        for e, name in enumerate(names):
-            if not name[2]:
-                marks[(unit0[name[0]] + name[1]) % MARKS] = name[:2]
-            for at, rnd in entries(e):
-                if rnd:
-                    yield raw_empty[at], rnd - 1
-                entry_holds[at] = name
-                yield None
-                raw_full[at].arrive()
+    def copies():                                # two blocks at a time: all their waits, then all their copies
+        for pair in zip(range(0, len(names), 2), range(1, len(names), 2)):
+            for e in pair:
+                if not names[e][2]:
+                    marks[(unit0[names[e][0]] + names[e][1]) % MARKS] = names[e][:2]
+            for e in pair:
+                for at, rnd in entries(e):
+                    if rnd:
+                        yield raw_empty[at], rnd - 1
+            for e in pair:
+                for at, rnd in entries(e):
+                    entry_holds[at] = names[e]
+                    yield None
+                    raw_full[at].arrive()
 
     def convert(group, w):
         for e in range(group, len(names), 2):
