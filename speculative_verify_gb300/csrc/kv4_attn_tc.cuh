@@ -54,7 +54,7 @@ struct KtSmem {
     static constexpr int RING = Q, RAW = RING + BLOCKS * BLOCK, STAT = RAW + ENTRIES * ENTRY;
     static constexpr int FACTOR = STAT + 6 * KT_ROWS * 4;       // scores' factors of the rows
     static constexpr int MASK = FACTOR + NT * KT_ROWS * 4;          // missing pages of the last 16 units
-    static constexpr int BARS = MASK + 16 * 4;
+    static constexpr int BARS = MASK + 16 * 2;
     // barriers
     static constexpr int RAW_FULL = 0, RAW_EMPTY = ENTRIES, B_FULL = 2 * ENTRIES, B_EMPTY = B_FULL + BLOCKS,
                          S_FULL = B_EMPTY + BLOCKS, P_FULL = S_FULL + 2 * NT, O_DONE = P_FULL + 2 * NT,
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     uint64_t *bars = reinterpret_cast<uint64_t *>(kt_smem + L::BARS);
     volatile int *flag = reinterpret_cast<volatile int *>(bars + L::COUNT);
     volatile uint32_t *slot_tm = reinterpret_cast<volatile uint32_t *>(flag + 1);
-    volatile unsigned *missing = reinterpret_cast<volatile unsigned *>(kt_smem + L::MASK);
+    volatile uint8_t *missing = kt_smem + L::MASK;      // of a page each
     auto bar = [&](int i) { return base + static_cast<uint32_t>(L::BARS + 8 * i); };
     const TcWait wait{flag, p.err};
     if (base & 1023u) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         for (int i = 0; i < L::COUNT; ++i) {
             const bool codes = (i >= L::RAW_EMPTY && i < L::B_EMPTY);           // (RAW_EMPTY, B_FULL)
             const bool soft = (i >= L::P_FULL && i < L::O_DONE) || i >= L::Q_FULL;
-            mbar_init(bar(i), codes ? W::CODE / 2 : soft ? W::TILE : 1);
+            mbar_init(bar(i), i < L::RAW_EMPTY ? 2 / L::PIECES : codes ? W::CODE / 2 : soft ? W::TILE : 1);
         }
         *flag = 0;
         fence_barrier_init();
@@ -255,14 +255,18 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
 
     if (warp == W::COPY) {
         const uint64_t policy = policy_evict_last();    // (other blocks read the same pages)
-        // Two blocks at a time: lanes 0 and 1 have the pages of the first, in the
-        // first conversion group's ring, lanes 2 and 3 those of the second; a page
-        // is its entry's only one or one of two.
+        // Four lanes, each with pages of its own: lanes 0 and 1 those of the even
+        // blocks (the first conversion group's ring: K0 V0 V1 V2 ..), 2 and 3 of
+        // the odd ones (K1 K2 .. and the last V).  A page is its entry's only one
+        // or one of two.
         constexpr bool OWN = L::PIECES == 2;
         constexpr int PAGES = OWN ? 1 : 2;
         const int ring = (lane >> 1) & 1, sub = lane & 1, mine = OWN ? 0 : sub;
         KtTurn<L::TURN> turn;
         if (OWN && sub) turn.next();
+        const long long stride = static_cast<long long>(p.kv.Hk) * kv_head_bytes(D);
+        const uint32_t codes0 = base + L::RAW + ring * L::TURN * L::ENTRY + mine * (KV_PAGE * D / 2);
+        const uint32_t scales0 = base + L::RAW + ring * L::TURN * L::ENTRY + PAGES * (KV_PAGE * D / 2) + mine * (KV_PAGE * D / 16);
         int units = 0;
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
@@ -275,37 +279,37 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     prefetch_l2(p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D, 2 * D);
             }
             const int n = part.units();
-            // a block's page: its entry in the table, asked for two blocks ahead and looked at when it is needed
-            const int32_t *table = p.kv.table + it.b * p.kv.ldt;
-            const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
-            auto wanted = [&](int k) { return k < 2 * n ? it.span.at(it.unit + step(k, n).unit) * (KT_UNIT / KV_PAGE) + sub : pages; };
-            int at = wanted(ring), id = at < pages ? table[at] : 0;
+            // a block's page: its entry in the table, asked for a step ahead and looked at when it is needed
+            if (lane < 4) {
+                const int32_t *table = p.kv.table + it.b * p.kv.ldt;
+                const uint8_t *head = p.kv.pages + static_cast<long long>(it.h) * kv_head_bytes(D);
+                const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
+                // the unit of step j, and whether it is of values
+                auto unit = [&](int j) { return ring ? min(j + 1, n - 1) : max(j - 1, 0); };
+                auto page_at = [&](int j) { return it.span.at(it.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
+                int at = page_at(0), id = at < pages ? table[at] : -1;
 #pragma unroll 1
-            for (int k = ring; k < 2 * n; k += 2) {
-                const Step x = step(k, n);
-                const int page = at < pages ? p.kv.page(id) : -1;
-                if (at < pages && page < 0) atomicOr(p.err, KV_ERR_PAGE);
-                at = wanted(k + 2);
-                if (at < pages) id = table[at];
-                const unsigned here = __ballot_sync(0xFFFFFFFFu, page >= 0) >> (2 * ring) & 3u;
-                if (lane < 4) {
-                    if (!x.v && sub == 0) missing[(units + x.unit) & 15] = ~here & 3u;
+                for (int j = 0; j < n; ++j) {
+                    const bool v = ring ? j == n - 1 : j > 0, here = at < pages && id >= 0 && id < p.kv.n_pages;
+                    if (at < pages && !here) atomicOr(p.err, KV_ERR_PAGE);
+                    const uint8_t *src = head + id * stride;
+                    const int u = unit(j);
+                    at = page_at(j + 1);
+                    if (j + 1 < n) id = at < pages ? table[at] : -1;
+                    if (!v) missing[2 * ((units + u) & 15) + sub] = !here;
                     const int slot = ring * L::TURN + turn.at;
                     if (turn.round) wait(bar(L::RAW_EMPTY + slot), turn.round - 1);
-                    const uint32_t full = bar(L::RAW_FULL + slot), to = base + L::RAW + slot * L::ENTRY;
-                    // (a copy may land before the entry's bytes are announced: the arrival is still to come)
-                    if (mine == 0) mbar_arrive_expect_tx(full, (OWN ? here >> sub & 1u : __popc(here)) * (L::ENTRY / PAGES));
-                    if (page >= 0) {
-                        const uint8_t *src = p.kv.head<D>(page, it.h);
-                        bulk_g2s(to + mine * (KV_PAGE * D / 2), src + (x.v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
-                        bulk_g2s(to + PAGES * (KV_PAGE * D / 2) + mine * (KV_PAGE * D / 16),
-                                 src + (x.v ? kv_v_scales(D) : kv_k_scales(D)), KV_PAGE * D / 16, full, policy);
+                    const uint32_t full = bar(L::RAW_FULL + slot);
+                    mbar_arrive_expect_tx(full, here ? KV_PAGE * D / 2 + KV_PAGE * D / 16 : 0);
+                    if (here) {
+                        bulk_g2s(codes0 + turn.at * L::ENTRY, src + (v ? kv_v_codes(D) : 0), KV_PAGE * D / 2, full, policy);
+                        bulk_g2s(scales0 + turn.at * L::ENTRY, src + (v ? kv_v_scales(D) : kv_k_scales(D)), KV_PAGE * D / 16, full, policy);
                     }
                     turn.next();
                     if (OWN) turn.next();
                 }
-                __syncwarp();
             }
+            __syncwarp();
             units += n;
         }
     } else if (warp >= W::SOFT && warp < W::MMA) {
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j) tmem_ld32(at + 32 * j, x[j]);
                 const int first = it.span.at(it.unit + i) * KT_UNIT;
-                const unsigned gone = missing[(units + i) & 15];
+                const unsigned gone = missing[2 * ((units + i) & 15)] | missing[2 * ((units + i) & 15) + 1] << 1;
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
                 tmem_wait_ld();
                 if (!all) {

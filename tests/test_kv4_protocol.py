@@ -1,6 +1,6 @@
 """The barrier protocol of the tcgen05 attention kernel, replayed on the CPU.
 
-Each role of `kv4_attn_tc_kernel` (copies, the two conversion groups' warps,
+Each role of `kv4_attn_tc_kernel` (the copying lanes, the two conversion groups' warps,
 products, the tiles' softmax warps) is written here as the sequence of mbarrier
 waits and arrivals it performs, with the same counts and phase arithmetic as
 the kernel; the tensor core's completions come later, in order.  A random
@@ -33,7 +33,7 @@ def step(s, n):
 def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
     """items: (units, active tiles).  warps: of a conversion group, and of a tile's softmax."""
     ENTRIES = 2 * TURN
-    raw_full = [Bar("raw_full%d" % i, 1) for i in range(ENTRIES)]
+    raw_full = [Bar("raw_full%d" % i, 2 // PIECES) for i in range(ENTRIES)]
     raw_empty = [Bar("raw_empty%d" % i, warps) for i in range(ENTRIES)]
     b_full = [Bar("b_full%d" % i, warps) for i in range(BLOCKS)]
     b_empty = [Bar("b_empty%d" % i, 1) for i in range(BLOCKS)]
@@ -41,11 +41,11 @@ def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
     p_full = [[Bar("p_full%d.%d" % (t, i), warps) for i in range(2)] for t in range(NT)]
     q_full = [Bar("q_full%d" % t, warps) for t in range(NT)]
     tensor = []                                  # operations of the product warp, completing in order
-    entry_holds, slot_holds = [None] * ENTRIES, [[None] * warps for _ in range(BLOCKS)]
+    entry_holds, slot_holds = [[None] * (2 // PIECES) for _ in range(ENTRIES)], [[None] * warps for _ in range(BLOCKS)]
     S = [[None, None] for _ in range(NT)]        # ("s" | "p", item, unit, parts written)
     O = [None] * NT                              # (item, units added)
     Q = [[None] * warps for _ in range(NT)]
-    marks = [None] * MARKS                       # the unit that a mark is of
+    marks = [[None, None] for _ in range(MARKS)] # the unit that a mark is of
     names, unit0 = [], []                        # every block in order: (item, unit, v); units before an item
     for k, (n, _) in enumerate(items):
         unit0.append(sum(m for m, _ in items[:k]))
@@ -57,28 +57,25 @@ def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
             i = e // 2 * PIECES + x
             yield e % 2 * TURN + i % TURN, i // TURN
 
-    def copies():                                # two blocks at a time: all their waits, then all their copies
-        for pair in zip(range(0, len(names), 2), range(1, len(names), 2)):
-            for e in pair:
-                if not names[e][2]:
-                    marks[(unit0[names[e][0]] + names[e][1]) % MARKS] = names[e][:2]
-            for e in pair:
-                for at, rnd in entries(e):
-                    if rnd:
-                        yield raw_empty[at], rnd - 1
-            for e in pair:
-                for at, rnd in entries(e):
-                    entry_holds[at] = names[e]
-                    yield None
-                    raw_full[at].arrive()
+    def copies(ring, sub):
+        """A lane: its page of every block of a ring."""
+        for e in range(ring, len(names), 2):
+            if not names[e][2]:
+                marks[(unit0[names[e][0]] + names[e][1]) % MARKS][sub] = names[e][:2]
+            at, rnd = list(entries(e))[sub if PIECES == 2 else 0]
+            if rnd:
+                yield raw_empty[at], rnd - 1
+            entry_holds[at][0 if PIECES == 2 else sub] = names[e]
+            yield None
+            raw_full[at].arrive()
 
     def convert(group, w):
         for e in range(group, len(names), 2):
             for at, rnd in entries(e):
                 yield raw_full[at], rnd
-                assert entry_holds[at] == names[e]
+                assert all(x == names[e] for x in entry_holds[at])
                 yield None
-                assert entry_holds[at] == names[e]
+                assert all(x == names[e] for x in entry_holds[at])
             for at, rnd in entries(e):
                 raw_empty[at].arrive()
             at, rnd = e % BLOCKS, e // BLOCKS
@@ -152,7 +149,7 @@ def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
                 buf = u & 1
                 yield s_full[t][buf], u >> 1
                 assert S[t][buf][1:3] == (k, i) and (S[t][buf][0] == "s" or me not in S[t][buf][3]), (S[t][buf], k, i)
-                assert marks[(unit0[k] + i) % MARKS] == (k, i), (marks, k, i)
+                assert marks[(unit0[k] + i) % MARKS] == [(k, i)] * 2, (marks, k, i)
                 yield None
                 if NT == 1:
                     yield from meet(("max", k, i), me)
@@ -172,7 +169,8 @@ def run(NT, BLOCKS, PIECES, TURN, MARKS, items, rng, warps=2):
             yield None
             assert O[t] == (k, n)
 
-    gens = {"copies": copies(), "products": products()}
+    gens = {"products": products()}
+    gens.update({"copies%d.%d" % (r, i): copies(r, i) for r in range(2) for i in range(2)})
     gens.update({"convert%d.%d" % (g, w): convert(g, w) for g in range(2) for w in range(warps)})
     gens.update({"softmax%d.%d" % (t, w): softmax(t, w) for t in range(NT) for w in range(warps)})
     want = dict.fromkeys(gens)
@@ -210,7 +208,7 @@ def constants():
     s = open(SRC).read()
     b = re.search(r"BLOCKS = D == 256 \? (\d+) : (\d+);", s)
     e = re.search(r"PIECES = D == 256 \? (\d+) : (\d+);", s)
-    t, m = re.search(r"TURN = (\d+),", s), re.search(r"BARS = MASK \+ (\d+) \* 4;", s)
+    t, m = re.search(r"TURN = (\d+),", s), re.search(r"BARS = MASK \+ (\d+) \* 2;", s)
     return tuple((int(b[i]), int(e[i]), int(t[1]), int(m[1])) for i in (1, 2))
 
 
