@@ -33,9 +33,12 @@ int attn_device(DeviceInfo *out)
         const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e = e != cudaSuccess ? e : r;
     };
-    up(kv4_attn_kernel<64>, KaShape<64>::BYTES);
-    up(kv4_attn_kernel<128>, KaShape<128>::BYTES);
-    up(kv4_attn_kernel<256>, KaShape<256>::BYTES);
+    up(kv4_attn_kernel<64, 1>, KaShape<64, 1>::BYTES);
+    up(kv4_attn_kernel<64, 2>, KaShape<64, 2>::BYTES);
+    up(kv4_attn_kernel<128, 1>, KaShape<128, 1>::BYTES);
+    up(kv4_attn_kernel<128, 2>, KaShape<128, 2>::BYTES);
+    up(kv4_attn_kernel<256, 1>, KaShape<256, 1>::BYTES);
+    up(kv4_attn_kernel<256, 2>, KaShape<256, 2>::BYTES);
     up(kv4_attn_tc_kernel<64, 1>, KtSmem<64, 1>::BYTES);
     up(kv4_attn_tc_kernel<64, 2>, KtSmem<64, 2>::BYTES);
     up(kv4_attn_tc_kernel<128, 1>, KtSmem<128, 1>::BYTES);
@@ -135,11 +138,11 @@ int kv_rows_call(uint16_t *k, long long ldk, uint16_t *v, long long ldv, int R, 
 
 // ------------------------------------------------------------ attention
 
-// How a call's work is cut: the kernel (0: kv4_attn_kernel, else the tiles of
-// kv4_attn_tc_kernel), packed rows of an item, tokens of a unit, parts at most,
-// units of a part at least.
+// How a call's work is cut: the kernel (rows of eight of kv4_attn_kernel, or
+// tiles of kv4_attn_tc_kernel), packed rows of an item, tokens of a unit, parts
+// at most, units of a part at least.
 struct AttnPlan {
-    int tiles, tile, unit, parts, least;
+    int eights, tiles, tile, unit, parts, least;
     bool joins;                                 // an item may go over several parts
 };
 
@@ -147,16 +150,20 @@ struct AttnPlan {
 // the workspace's size does not ask the device.
 constexpr int ATTN_SMS = 152;
 
+template <int D>
+constexpr int attn_blocks(int eights) { return eights == 1 ? KaShape<D, 1>::BLOCKS : KaShape<D, 2>::BLOCKS; }
+
 AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
 {
     AttnPlan a{};
     // packed rows of a sequence, on average where they are uneven
     const long long packed = (1LL * R * G + B - 1) / B;
-    a.tiles = packed <= KA_ROWS ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
-    a.tile = a.tiles ? a.tiles * KT_ROWS : KA_ROWS;
+    a.eights = packed <= 8 ? 1 : packed <= KA_MAX_ROWS ? 2 : 0;
+    a.tiles = a.eights ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
+    a.tile = a.tiles ? a.tiles * KT_ROWS : 8 * a.eights;
     a.unit = a.tiles ? KT_UNIT : KV_PAGE;
     a.least = a.tiles ? 4 : 2 * KA_WARPS;
-    const int blocks = a.tiles ? 1 : d == 64 ? KaShape<64>::BLOCKS : d == 128 ? KaShape<128>::BLOCKS : KaShape<256>::BLOCKS;
+    const int blocks = a.tiles ? 1 : d == 64 ? attn_blocks<64>(a.eights) : d == 128 ? attn_blocks<128>(a.eights) : attn_blocks<256>(a.eights);
     // (items, and their units, at most)
     const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);
     const long long units = items * std::max(1, (max_pages * KV_PAGE + a.unit - 1) / a.unit);
@@ -188,13 +195,17 @@ int attn_launch(const KvAttnParams &p, const AttnPlan &a, cudaStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>(a.parts));
     int rc;
-    if constexpr (D == 256) {
-        rc = a.tiles ? launch(kv4_attn_tc_kernel<D, 1>, grid, KtWarps<1>::THREADS, KtSmem<D, 1>::BYTES, stream, p)
-                     : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
-    } else {
-        rc = a.tiles == 2   ? launch(kv4_attn_tc_kernel<D, 2>, grid, KtWarps<2>::THREADS, KtSmem<D, 2>::BYTES, stream, p)
-             : a.tiles == 1 ? launch(kv4_attn_tc_kernel<D, 1>, grid, KtWarps<1>::THREADS, KtSmem<D, 1>::BYTES, stream, p)
-                            : launch(kv4_attn_kernel<D>, grid, KA_WARPS * 32, KaShape<D>::BYTES, stream, p);
+    if (a.eights == 1)
+        rc = launch(kv4_attn_kernel<D, 1>, grid, KA_WARPS * 32, KaShape<D, 1>::BYTES, stream, p);
+    else if (a.eights == 2)
+        rc = launch(kv4_attn_kernel<D, 2>, grid, KA_WARPS * 32, KaShape<D, 2>::BYTES, stream, p);
+    else if (a.tiles == 1)
+        rc = launch(kv4_attn_tc_kernel<D, 1>, grid, KtWarps<1>::THREADS, KtSmem<D, 1>::BYTES, stream, p);
+    else {
+        if constexpr (D != 256)
+            rc = launch(kv4_attn_tc_kernel<D, 2>, grid, KtWarps<2>::THREADS, KtSmem<D, 2>::BYTES, stream, p);
+        else
+            rc = SV_ERR_SHAPE;                  // (not planned)
     }
     if (rc != SV_OK || !a.joins) return rc;
     constexpr int rows = KJ_VALUES / D;

@@ -4,17 +4,19 @@
 //
 // A warp takes a page of its head's item (kv4_plan.cuh) at a time, from a ring
 // of its own filled by bulk copies, and keeps a running softmax of its own; the
-// warps of a block join at the item's end.  Products are m16n8k16 of fp16: rows
-// are up to 16 packed query rows.  Keys and values become fp16 in registers,
-// exactly (kv4.cuh): one conversion and one product a pair.
-//   * Scores: a thread's B column is a token and its K steps are that token's
-//     32 neighbouring dimensions, so a token's codes come in one 16-byte load.
+// warps of a block join at the item's end.  Products are m16n8k16 of fp16, with
+// the cache as the operand of 16 rows: scores^T = K Q^T and o^T = V^T P^T, NQ
+// times 8 packed query rows (with queries as the 16 rows, half of the products
+// and of the softmax are of rows that are not there).  Keys and values become
+// fp16 in registers, exactly (kv4.cuh): one conversion and one product a pair.
+//   * Scores: a thread's A rows are two tokens and its K steps are a token's 32
+//     neighbouring dimensions, so a token's codes come in one 16-byte load.
 //     Queries are laid out the same, times a power of two of their row that
 //     puts the largest in [2^14, 2^15): exact but for values 2^-25 of it.
-//   * Values: probabilities are the A operand as the score product leaves
-//     them, and a B column is a dimension; a pair of tokens' values are put
-//     together by byte permutation.  Thread column n has dimensions n d / 8 ..,
-//     so that it ends with neighbouring ones.
+//   * Values: probabilities, transposed in registers (movmatrix), are the B
+//     operand; an A row is a dimension, and a pair of tokens' values are put
+//     together by byte permutation.  Thread row g has dimensions g d / 8 .., so
+//     that it ends with neighbouring ones.
 //   * Sums and the softmax are fp32, probabilities fp16 (2^-12 of each,
 //     independent).  They are taken relative to a maximum that is only moved
 //     when a score passes it by 2^8, so most pages rescale nothing.
@@ -26,26 +28,29 @@
 namespace sv {
 
 constexpr int KA_WARPS = 4;
-constexpr int KA_ROWS = 16;                     // packed rows of an item
+constexpr int KA_MAX_ROWS = 16;                 // packed rows of an item at most
 constexpr float KA_SLACK = 8.f;                 // log2 of the largest probability
 
-template <int D>
+template <int D, int NQ>
 struct KaShape {
+    static constexpr int ROWS = 8 * NQ;                 // packed rows of an item
     static constexpr int STAGES = D == 64 ? 4 : D == 128 ? 3 : 2;
-    static constexpr int BLOCKS = D == 64 ? 4 : D == 128 ? 3 : 2;   // on a multiprocessor
+    // blocks on a multiprocessor, by registers and shared memory
+    static constexpr int BLOCKS = D == 64 ? (NQ == 1 ? 5 : 4) : D == 128 ? (NQ == 1 ? 4 : 3) : NQ == 1 ? 3 : 2;
     static constexpr int STAGE = kv_head_bytes(D);
     static constexpr int KSTEPS = D / 16;
     static constexpr int SECTIONS = D == 256 ? 2 : 1;   // of 128 dimensions (64) of the queries and keys
     static constexpr int SK = KSTEPS / SECTIONS;        // K steps of a section
-    static constexpr int VN = D / 8;                    // dimensions of a thread's value column
+    static constexpr int VN = D / 8;                    // dimensions of a thread's rows
+    static constexpr bool STORED = D == 256 && NQ == 2; // the queries are in shared memory
     // shared memory: rings (a warp's sums at an item's end), two warps'
-    // statistics, queries (SECTIONS > 1), barriers
+    // statistics, queries, barriers
     static constexpr int RING = STAGES * STAGE;
     static constexpr int STATS = KA_WARPS * RING;
-    static constexpr int QUERIES = STATS + 2 * KA_ROWS * 8;
-    static constexpr int BARS = QUERIES + (SECTIONS > 1 ? KSTEPS * 512 : 0);
+    static constexpr int QUERIES = STATS + 2 * ROWS * 8;
+    static constexpr int BARS = QUERIES + (STORED ? KSTEPS * 512 : 0);
     static constexpr int BYTES = BARS + 8 * KA_WARPS * STAGES;
-    static_assert(RING >= KA_ROWS * D * 4, "a warp's sums fit its ring");
+    static_assert(RING >= ROWS * D * 4, "a warp's sums fit its ring");
 };
 
 __device__ __forceinline__ float ka_exp2(float x)
@@ -55,9 +60,8 @@ __device__ __forceinline__ float ka_exp2(float x)
     return r;
 }
 
-// The token (of 8) that column n of a score tile stands for.  Rows of
-// neighbouring columns differ in parity, and four threads' rows are two even,
-// two odd: with 64 bytes a token, no bank conflict among the loads of keys and
+// The token (of 8) that row n of a half tile of scores stands for.  Those of
+// neighbouring rows differ in parity, and four threads' are two even, two odd: with 64 bytes a token, no bank conflict among the loads of keys and
 // two ways among those of values.
 __device__ __forceinline__ int ka_token(int n) { return n & 1 ? 4 + ((n >> 1) ^ 1) : n >> 1; }
 
@@ -76,107 +80,144 @@ __device__ __forceinline__ void ka_words(const uint8_t *at, uint32_t (&w)[N])
     }
 }
 
-template <int D>
+// An 8 x 8 matrix of 16-bit values, a row's neighbours in a register, transposed.
+__device__ __forceinline__ uint32_t ka_transpose(uint32_t a)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+template <int D, int NQ>
 struct KaWarp {
-    using S = KaShape<D>;
-    float o[S::VN][4];                          // dimension n VN + i: rows g, columns 2c, 2c + 1; rows g + 8
-    float m[2], l[2];                           // reference maximum, this thread's sum; rows g, g + 8
+    using S = KaShape<D, NQ>;
+    static constexpr int MT = D / 16;
+    float o[MT][NQ][4];                         // dimensions 2 i, 2 i + 1 of the thread's: rows 2c, 2c + 1 of the first, of the second
+    float m[NQ][2], l[NQ][2];                   // rows 2c, 2c + 1: reference maximum, this thread's sum
 
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int i = 0; i < S::VN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) o[i][q][0] = o[i][q][1] = o[i][q][2] = o[i][q][3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            m[q][0] = m[q][1] = -INFINITY;
+            l[q][0] = l[q][1] = 0.f;
+        }
     }
 
     // A page in shared memory: tokens at positions first .. first + 31; row r
     // sees those up to pos[r] that are in its window or among the sinks.
     // `all`: every row sees every token.
     template <class Query>
-    __device__ __forceinline__ void page(const uint8_t *st, const Query &query, int first, bool all, const int (&pos)[2],
-                                         const int (&low)[2], int sinks, const float (&scale)[2])
+    __device__ __forceinline__ void page(const uint8_t *st, const Query &query, int first, bool all, const int (&pos)[NQ][2],
+                                         const int (&low)[NQ][2], int sinks, const float (&scale)[NQ][2])
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-        float s[4][4];
+        float s[2][NQ][4];                      // 16 tokens each: rows g and g + 8
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) s[j][q][0] = s[j][q][1] = s[j][q][2] = s[j][q][3] = 0.f;
 #pragma unroll
         for (int sec = 0; sec < S::SECTIONS; ++sec) {
-            uint32_t a[S::SK][4];
-            query(sec, a);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 8 * j + ka_token(g);
-                uint32_t w[S::SK / 2];
-                ka_words(st + t * (D / 2) + sec * 64 + c * (2 * S::SK), w);
-                uint32_t s2[2];                 // the scales of the steps' first and second half, twice each
-                if constexpr (D == 64) {
-                    const uint32_t b = st[kv_k_scales(D) + t * 4 + c];
-                    s2[0] = s2[1] = kv_scales2(b | b << 8);
-                } else {
-                    const uint32_t v = kv_scales2(*reinterpret_cast<const uint16_t *>(st + kv_k_scales(D) + t * (D / 16) + sec * 8 + 2 * c));
-                    s2[0] = __byte_perm(v, v, 0x1010);
-                    s2[1] = __byte_perm(v, v, 0x3232);
+            for (int j = 0; j < 2; ++j) {
+                uint32_t w[2][S::SK / 2], s2[2][2];     // the scales of the steps' first and second half, twice each
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 16 * j + 8 * h + ka_token(g);
+                    ka_words(st + t * (D / 2) + sec * 64 + c * (2 * S::SK), w[h]);
+                    if constexpr (D == 64) {
+                        const uint32_t b = st[kv_k_scales(D) + t * 4 + c];
+                        s2[h][0] = s2[h][1] = kv_scales2(b | b << 8);
+                    } else {
+                        const uint32_t v = kv_scales2(*reinterpret_cast<const uint16_t *>(st + kv_k_scales(D) + t * (D / 16) + sec * 8 + 2 * c));
+                        s2[h][0] = __byte_perm(v, v, 0x1010);
+                        s2[h][1] = __byte_perm(v, v, 0x3232);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < S::SK / 2; ++i) {
-                    uint32_t v[4];
-                    kv_values8(w[i], v);
-                    const uint32_t f = s2[2 * i >= S::SK / 2];
+                    uint32_t v[2][4];
+                    kv_values8(w[0][i], v[0]);
+                    kv_values8(w[1][i], v[1]);
+                    const uint32_t f0 = s2[0][2 * i >= S::SK / 2], f1 = s2[1][2 * i >= S::SK / 2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        mma_f16_16816(s[j], a[2 * i + e][0], a[2 * i + e][1], a[2 * i + e][2], a[2 * i + e][3],
-                                      kv_mul2(v[2 * e], f), kv_mul2(v[2 * e + 1], f));
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a0 = kv_mul2(v[0][2 * e], f0), a1 = kv_mul2(v[1][2 * e], f1);
+                        const uint32_t a2 = kv_mul2(v[0][2 * e + 1], f0), a3 = kv_mul2(v[1][2 * e + 1], f1);
+                        uint32_t b[2 * NQ];
+                        query(sec * S::SK + 2 * i + e, b);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) mma_f16_16816(s[j][q], a0, a1, a2, a3, b[2 * q], b[2 * q + 1]);
+                    }
                 }
             }
         }
         // in units of log2, masked
-        float top[2] = {-INFINITY, -INFINITY};
+        float top[NQ][2];
+        bool grow = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = e >> 1;
-                float x = s[j][e] * scale[r];
-                if (!all) {
-                    const int t = first + 8 * j + ka_token(2 * c + (e & 1));
-                    x = t <= pos[r] && (t >= low[r] || t < sinks) ? x : -INFINITY;
-                }
-                s[j][e] = x;
-                top[r] = fmaxf(top[r], x);
-            }
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + KA_SLACK || top[1] > m[1] + KA_SLACK || (top[0] > m[0] && m[0] == -INFINITY) ||
-                                        (top[1] > m[1] && m[1] == -INFINITY))) {
-            float f[2];
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
-                const float to = fmaxf(m[r], top[r]);
-                f[r] = m[r] == -INFINITY ? 0.f : ka_exp2(m[r] - to);    // (nothing was added before)
-                f[r] = to == m[r] ? 1.f : f[r];
-                m[r] = to;
-                l[r] *= f[r];
-            }
+                top[q][r] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < S::VN; ++i) {
-                o[i][0] *= f[0];
-                o[i][1] *= f[0];
-                o[i][2] *= f[1];
-                o[i][3] *= f[1];
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = s[j][q][2 * h + r] * scale[q][r];
+                        if (!all) {
+                            const int t = first + 16 * j + 8 * h + ka_token(g);
+                            x = t <= pos[q][r] && (t >= low[q][r] || t < sinks) ? x : -INFINITY;
+                        }
+                        s[j][q][2 * h + r] = x;
+                        top[q][r] = fmaxf(top[q][r], x);
+                    }
+                // (with -inf before: 0 scores further are enough)
+                grow |= top[q][r] > (m[q][r] == -INFINITY ? -INFINITY : m[q][r] + KA_SLACK);
+            }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float x = top[q][r];
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    const float to = fmaxf(m[q][r], x);
+                    f[r] = to == m[q][r] ? 1.f : m[q][r] == -INFINITY ? 0.f : ka_exp2(m[q][r] - to);   // (0: nothing was added before)
+                    m[q][r] = to;
+                    l[q][r] *= f[r];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[i][q][0] *= f[0];
+                    o[i][q][1] *= f[1];
+                    o[i][q][2] *= f[0];
+                    o[i][q][3] *= f[1];
+                }
             }
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-        uint32_t p[4][2];
+        uint32_t p[2][NQ][2];                   // 16 tokens: tokens 2c, 2c + 1 of row g, 2c + 8, 2c + 9
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int q = 0; q < NQ; ++q) {
+            const float ref[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0], m[q][1] == -INFINITY ? 0.f : m[q][1]};
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float x = ka_exp2(s[j][2 * r] - ref[r]), y = ka_exp2(s[j][2 * r + 1] - ref[r]);
-                l[r] += x + y;
-                p[j][r] = pack_f16x2(x, y);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = ka_exp2(s[j][q][2 * h] - ref[0]), y = ka_exp2(s[j][q][2 * h + 1] - ref[1]);
+                    l[q][0] += x;
+                    l[q][1] += y;
+                    p[j][q][h] = ka_transpose(pack_f16x2(x, y));
+                }
+        }
         const uint8_t *vc = st + kv_v_codes(D) + g * (S::VN / 2), *vs = st + kv_v_scales(D) + g * S::VN / KV_GROUP;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {           // 16 tokens
@@ -184,7 +225,7 @@ struct KaWarp {
             uint32_t w[4][W], f[GROUPS][2];
             uint32_t sc[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {       // tile 2k's columns 2c, 2c + 1, tile 2k + 1's
+            for (int q = 0; q < 4; ++q) {       // tokens 2c, 2c + 1, 2c + 8, 2c + 9
                 const int t = 16 * k + 8 * (q >> 1) + ka_token(2 * c + (q & 1));
                 ka_words(vc + t * (D / 2), w[q]);
                 sc[q] = GROUPS == 2 ? *reinterpret_cast<const uint16_t *>(vs + t * (D / 16)) : vs[t * (D / 16)];
@@ -202,22 +243,22 @@ struct KaWarp {
                 const int n = GROUPS == 2 ? i / 2 : 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t b0 = kv_mul2(__byte_perm(v[0][j], v[1][j], 0x5410), f[n][0]);
-                    const uint32_t b1 = kv_mul2(__byte_perm(v[2][j], v[3][j], 0x5410), f[n][1]);
-                    mma_f16_16816(o[8 * i + 2 * j], p[2 * k][0], p[2 * k][1], p[2 * k + 1][0], p[2 * k + 1][1], b0, b1);
-                    const uint32_t c0 = kv_mul2(__byte_perm(v[0][j], v[1][j], 0x7632), f[n][0]);
-                    const uint32_t c1 = kv_mul2(__byte_perm(v[2][j], v[3][j], 0x7632), f[n][1]);
-                    mma_f16_16816(o[8 * i + 2 * j + 1], p[2 * k][0], p[2 * k][1], p[2 * k + 1][0], p[2 * k + 1][1], c0, c1);
+                    const uint32_t a0 = kv_mul2(__byte_perm(v[0][j], v[1][j], 0x5410), f[n][0]);
+                    const uint32_t a1 = kv_mul2(__byte_perm(v[0][j], v[1][j], 0x7632), f[n][0]);
+                    const uint32_t a2 = kv_mul2(__byte_perm(v[2][j], v[3][j], 0x5410), f[n][1]);
+                    const uint32_t a3 = kv_mul2(__byte_perm(v[2][j], v[3][j], 0x7632), f[n][1]);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) mma_f16_16816(o[4 * i + j][q], a0, a1, a2, a3, p[k][q][0], p[k][q][1]);
                 }
             }
         }
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_kernel(const KvAttnParams p)
+template <int D, int NQ>
+__global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_attn_kernel(const KvAttnParams p)
 {
-    using S = KaShape<D>;
+    using S = KaShape<D, NQ>;
     extern __shared__ __align__(128) uint8_t ka_smem[];
     __shared__ volatile int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -258,25 +299,22 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
         };
         for (int i = 0; i < S::STAGES - 1 && i < mine; ++i) ask(i, page_of(i));
 
-        // the tile's rows: this thread has rows g and g + 8
-        const int rows = min(KA_ROWS, it.seq.n * p.G - it.tile * KA_ROWS);
-        int pos[2], low[2];
-        float scale[2];
-        uint32_t a[S::SK][4];                   // (one section: kept)
+        // the tile's queries: this thread has row g of each eight
+        const int rows = min(S::ROWS, it.seq.n * p.G - it.tile * S::ROWS);
+        uint32_t b[S::STORED ? 1 : S::KSTEPS][2 * NQ];
+        float scale_g[NQ];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
+        for (int q = 0; q < NQ; ++q) {
+            const int row = 8 * q + g, packed = it.tile * S::ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
             const bool in = row < rows;
-            pos[r] = in && it.seq.before >= 0 ? it.seq.before + t : -1;
-            low[r] = p.window > 0 ? pos[r] - p.window + 1 : 0;
-            const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (it.seq.first + (in ? t : 0)) * p.ldq +
-                                                             static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D);
+            const uint4 *at = reinterpret_cast<const uint4 *>(p.q + (it.seq.first + (in ? t : 0)) * p.ldq +
+                                                              static_cast<long long>(it.h * p.G + (in ? hq : 0)) * D);
             unsigned top = 0;
 #pragma unroll
             for (int sec = 0; sec < S::SECTIONS; ++sec)
 #pragma unroll
                 for (int i = 0; i < S::SK / 2; ++i) {
-                    const uint4 v = in ? q[sec * 16 + c * (S::SK / 2) + i] : make_uint4(0, 0, 0, 0);
+                    const uint4 v = in ? at[sec * 16 + c * (S::SK / 2) + i] : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
@@ -285,44 +323,53 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             const int shift = xres_shift(top);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-            scale[r] = p.scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+            scale_g[q] = p.scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 #pragma unroll
             for (int sec = 0; sec < S::SECTIONS; ++sec)
 #pragma unroll
                 for (int i = 0; i < S::SK / 2; ++i) {
-                    const uint4 v = in ? q[sec * 16 + c * (S::SK / 2) + i] : make_uint4(0, 0, 0, 0);
+                    const uint4 v = in ? at[sec * 16 + c * (S::SK / 2) + i] : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t x = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                        const int k = 2 * i + (e >> 1), reg = r + 2 * (e & 1);
-                        if constexpr (S::SECTIONS == 1)
-                            a[k][reg] = x;
+                        const int k = sec * S::SK + 2 * i + (e >> 1), reg = 2 * q + (e & 1);
+                        if constexpr (!S::STORED)
+                            b[k][reg] = x;
                         else if (warp == 0)
-                            reinterpret_cast<uint32_t *>(ka_smem + S::QUERIES)[((sec * S::SK + k) * 32 + lane) * 4 + reg] = x;
+                            reinterpret_cast<uint32_t *>(ka_smem + S::QUERIES)[(k * 32 + lane) * 4 + reg] = x;
                     }
                 }
         }
-        if constexpr (S::SECTIONS > 1) __syncthreads();
-        auto query = [&](int sec, uint32_t (&to)[S::SK][4]) {
+        if constexpr (S::STORED) __syncthreads();
+        auto query = [&](int k, uint32_t (&to)[2 * NQ]) {
+            if constexpr (!S::STORED) {
 #pragma unroll
-            for (int k = 0; k < S::SK; ++k) {
-                if constexpr (S::SECTIONS == 1) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) to[k][e] = a[k][e];
-                } else {
-                    const uint4 v = reinterpret_cast<const uint4 *>(ka_smem + S::QUERIES)[(sec * S::SK + k) * 32 + lane];
-                    to[k][0] = v.x, to[k][1] = v.y, to[k][2] = v.z, to[k][3] = v.w;
-                }
+                for (int e = 0; e < 2 * NQ; ++e) to[e] = b[k][e];
+            } else {
+                const uint4 v = reinterpret_cast<const uint4 *>(ka_smem + S::QUERIES)[k * 32 + lane];
+                to[0] = v.x, to[1] = v.y, to[2 * NQ - 2] = v.z, to[2 * NQ - 1] = v.w;
             }
         };
-        // tokens that every row of the tile sees: from .. to, and below `sunk`
-        const int t0 = kv_token(p, it.tile * KA_ROWS), t1 = kv_token(p, it.tile * KA_ROWS + rows - 1);
+        // the softmax's rows: 2c and 2c + 1 of each eight
+        int pos[NQ][2], low[NQ][2];
+        float scale[NQ][2];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = 8 * q + 2 * c + r;
+                pos[q][r] = row < rows && it.seq.before >= 0 ? it.seq.before + kv_token(p, it.tile * S::ROWS + row) : -1;
+                low[q][r] = p.window > 0 ? pos[q][r] - p.window + 1 : 0;
+                scale[q][r] = __shfl_sync(0xFFFFFFFFu, scale_g[q], 4 * (2 * c + r));
+            }
+        // tokens that every row of the tile sees: from .. to, and below the sinks
+        const int t0 = kv_token(p, it.tile * S::ROWS), t1 = kv_token(p, it.tile * S::ROWS + rows - 1);
         const int to = it.seq.before < 0 ? -1 : it.seq.before + t0;
         const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
 
         if (threadIdx.x == 0 && it.seq.before >= 0 && it.seq.before + t1 >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
-        KaWarp<D> w;
+        KaWarp<D, NQ> w;
         w.clear();
         for (int i = 0; i < mine; ++i) {
             const int nx = i + S::STAGES - 1;
@@ -345,44 +392,54 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
 
         // the warps' sums: 2 and 3 to 0 and 1, then 1 to 0
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            w.l[r] += __shfl_xor_sync(0xFFFFFFFFu, w.l[r], 1);
-            w.l[r] += __shfl_xor_sync(0xFFFFFFFFu, w.l[r], 2);
-        }
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) w.l[q][r] += __shfl_xor_sync(0xFFFFFFFFu, w.l[q][r], x);
         float2 *stats = reinterpret_cast<float2 *>(ka_smem + S::STATS);
         for (int half = KA_WARPS / 2; half; half >>= 1) {
             if (warp >= half && warp < 2 * half) {
-                const int at = warp - half;
-                if (c == 0) {
-                    stats[at * KA_ROWS + g] = make_float2(w.m[0], w.l[0]);
-                    stats[at * KA_ROWS + g + 8] = make_float2(w.m[1], w.l[1]);
+                const int at = (warp - half) * S::ROWS;
+                if (g == 0) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) stats[at + 8 * q + 2 * c + r] = make_float2(w.m[q][r], w.l[q][r]);
                 }
                 float4 *sums = reinterpret_cast<float4 *>(ring);
 #pragma unroll
-                for (int i = 0; i < S::VN; ++i) sums[i * 32 + lane] = make_float4(w.o[i][0], w.o[i][1], w.o[i][2], w.o[i][3]);
+                for (int i = 0; i < w.MT; ++i)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+                        sums[(i * NQ + q) * 32 + lane] = make_float4(w.o[i][q][0], w.o[i][q][1], w.o[i][q][2], w.o[i][q][3]);
                 fence_proxy_async();            // (the ring's next copies come after)
             }
             __syncthreads();
             if (warp < half) {
                 const float4 *sums = reinterpret_cast<const float4 *>(ring + half * S::RING);
-                float f[2], e[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float2 s = stats[warp * KA_ROWS + g + 8 * r];
-                    const float top = fmaxf(w.m[r], s.x), ref = top == -INFINITY ? 0.f : top;
-                    f[r] = ka_exp2(w.m[r] - ref);
-                    e[r] = ka_exp2(s.x - ref);
-                    w.m[r] = top;
-                    w.l[r] = f[r] * w.l[r] + e[r] * s.y;
-                }
+                for (int q = 0; q < NQ; ++q) {
+                    float f[2], e[2];
 #pragma unroll
-                for (int i = 0; i < S::VN; ++i) {
-                    const float4 v = sums[i * 32 + lane];
-                    w.o[i][0] = f[0] * w.o[i][0] + e[0] * v.x;
-                    w.o[i][1] = f[0] * w.o[i][1] + e[0] * v.y;
-                    w.o[i][2] = f[1] * w.o[i][2] + e[1] * v.z;
-                    w.o[i][3] = f[1] * w.o[i][3] + e[1] * v.w;
+                    for (int r = 0; r < 2; ++r) {
+                        const float2 x = stats[warp * S::ROWS + 8 * q + 2 * c + r];
+                        const float top = fmaxf(w.m[q][r], x.x), ref = top == -INFINITY ? 0.f : top;
+                        f[r] = ka_exp2(w.m[q][r] - ref);
+                        e[r] = ka_exp2(x.x - ref);
+                        w.m[q][r] = top;
+                        w.l[q][r] = f[r] * w.l[q][r] + e[r] * x.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < w.MT; ++i) {
+                        const float4 v = sums[(i * NQ + q) * 32 + lane];
+                        w.o[i][q][0] = f[0] * w.o[i][q][0] + e[0] * v.x;
+                        w.o[i][q][1] = f[1] * w.o[i][q][1] + e[1] * v.y;
+                        w.o[i][q][2] = f[0] * w.o[i][q][2] + e[0] * v.z;
+                        w.o[i][q][3] = f[1] * w.o[i][q][3] + e[1] * v.w;
+                    }
                 }
+                fence_proxy_async();
             }
             __syncthreads();
         }
@@ -390,37 +447,33 @@ __global__ void __launch_bounds__(KA_WARPS * 32, KaShape<D>::BLOCKS) kv4_attn_ke
             const bool whole = part.whole();
             const int slot = 2 * blockIdx.x + (it.unit == 0);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, packed = it.tile * KA_ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
-                if (row >= rows) continue;
-                if (whole) {
-                    const float f = w.l[r] == 0.f ? 0.f : p.v_scale / w.l[r];
-                    // columns 2c and 2c + 1: 2 VN neighbouring dimensions
-                    uint4 *o = reinterpret_cast<uint4 *>(p.o + (it.seq.first + t) * p.ldo +
-                                                         static_cast<long long>(it.h * p.G + hq) * D + 2 * c * S::VN);
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 8 * q + 2 * c + r, packed = it.tile * S::ROWS + row, t = kv_token(p, packed), hq = packed - t * p.G;
+                    if (row >= rows) continue;
+                    if (whole) {
+                        const float f = w.l[q][r] == 0.f ? 0.f : p.v_scale / w.l[q][r];
+                        uint4 *o = reinterpret_cast<uint4 *>(p.o + (it.seq.first + t) * p.ldo +
+                                                             static_cast<long long>(it.h * p.G + hq) * D + g * S::VN);
 #pragma unroll
                         for (int i = 0; i < S::VN / 8; ++i) {
                             uint32_t x[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[e])
-                                    : "f"(w.o[8 * i + 2 * e + 1][2 * r + k] * f), "f"(w.o[8 * i + 2 * e][2 * r + k] * f));
-                            o[k * (S::VN / 8) + i] = make_uint4(x[0], x[1], x[2], x[3]);
+                                    : "f"(w.o[4 * i + e][q][2 + r] * f), "f"(w.o[4 * i + e][q][r] * f));
+                            o[i] = make_uint4(x[0], x[1], x[2], x[3]);
                         }
-                } else {
-                    float4 *o = reinterpret_cast<float4 *>(p.sums + (static_cast<long long>(slot) * KA_ROWS + row) * D + 2 * c * S::VN);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    } else {
+                        float4 *o = reinterpret_cast<float4 *>(p.sums + (static_cast<long long>(slot) * S::ROWS + row) * D + g * S::VN);
 #pragma unroll
                         for (int i = 0; i < S::VN / 4; ++i)
-                            o[k * (S::VN / 4) + i] = make_float4(w.o[4 * i][2 * r + k], w.o[4 * i + 1][2 * r + k],
-                                                                 w.o[4 * i + 2][2 * r + k], w.o[4 * i + 3][2 * r + k]);
-                    if (c == 0)
-                        reinterpret_cast<float2 *>(p.stats)[static_cast<long long>(slot) * KA_ROWS + row] = make_float2(w.m[r], w.l[r]);
+                            o[i] = make_float4(w.o[2 * i][q][r], w.o[2 * i][q][2 + r], w.o[2 * i + 1][q][r], w.o[2 * i + 1][q][2 + r]);
+                        if (g == 0)
+                            reinterpret_cast<float2 *>(p.stats)[static_cast<long long>(slot) * S::ROWS + row] = make_float2(w.m[q][r], w.l[q][r]);
+                    }
                 }
-            }
             if (lane == 0 && part.parts() > 1) p.joins[blockIdx.x] = make_int4(part.parts(), it.h, it.b, it.tile);
         }
         part.next(p);
