@@ -30,7 +30,10 @@ int attn_device(DeviceInfo *out)
     if (ready[out->dev]) return SV_OK;
     cudaError_t e = cudaSuccess;
     auto up = [&](auto *kernel, int bytes) {
-        const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaError_t r = bytes ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+        e = e != cudaSuccess ? e : r;
+        // (else a smaller share than the blocks that fit are counted with)
+        r = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         e = e != cudaSuccess ? e : r;
     };
     up(kv4_attn_kernel<64, 1>, KaShape<64, 1>::BYTES);
@@ -39,6 +42,9 @@ int attn_device(DeviceInfo *out)
     up(kv4_attn_kernel<128, 2>, KaShape<128, 2>::BYTES);
     up(kv4_attn_kernel<256, 1>, KaShape<256, 1>::BYTES);
     up(kv4_attn_kernel<256, 2>, KaShape<256, 2>::BYTES);
+    up(kv4_join_kernel<64>, 0);         // (the same share: a multiprocessor changes it only when it is empty)
+    up(kv4_join_kernel<128>, 0);
+    up(kv4_join_kernel<256>, 0);
     up(kv4_attn_tc_kernel<64, 1>, KtSmem<64, 1>::BYTES);
     up(kv4_attn_tc_kernel<64, 2>, KtSmem<64, 2>::BYTES);
     up(kv4_attn_tc_kernel<128, 1>, KtSmem<128, 1>::BYTES);

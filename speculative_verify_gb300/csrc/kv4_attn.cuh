@@ -273,8 +273,11 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
     pdl_launch_dependents();
     pdl_wait_prior();
     const uint64_t policy = policy_evict_first();
-    __shared__ KvPartSmem part_sm;
-    KvPart part = kv_part(p, part_sm);
+    // (found in what the rings are later)
+    static_assert(sizeof(KvPartSmem) <= S::STATS, "room for the parts");
+    KvPart part = kv_part(p, *reinterpret_cast<KvPartSmem *>(ka_smem));
+    fence_proxy_async();
+    __syncthreads();
     if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     uint32_t phases = 0;                        // bit i: the parity that stage i completes next
 
