@@ -145,10 +145,11 @@ int kv_rows_call(uint16_t *k, long long ldk, uint16_t *v, long long ldv, int R, 
 // ------------------------------------------------------------ attention
 
 // How a call's work is cut: the kernel (rows of eight of kv4_attn_kernel, or
-// tiles of kv4_attn_tc_kernel), packed rows of an item, tokens of a unit, parts
-// at most, units of a part at least.
+// tiles of kv4_attn_tc_kernel), packed rows of an item, tokens of a unit, units
+// that an item's start and end are counted as, parts at most, units of a part at
+// least.
 struct AttnPlan {
-    int eights, tiles, tile, unit, parts, least;
+    int eights, tiles, tile, unit, extra, parts, least;
     bool joins;                                 // an item may go over several parts
 };
 
@@ -168,11 +169,12 @@ AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
     a.tiles = a.eights ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
     a.tile = a.tiles ? a.tiles * KT_ROWS : 8 * a.eights;
     a.unit = a.tiles ? KT_UNIT : KV_PAGE;
-    a.least = a.tiles ? 4 : 2 * KA_WARPS;
+    a.extra = a.tiles ? 10 : 4;
+    a.least = a.tiles ? 4 + a.extra : 2 * KA_WARPS + a.extra;
     const int blocks = a.tiles ? 1 : d == 64 ? attn_blocks<64>(a.eights) : d == 128 ? attn_blocks<128>(a.eights) : attn_blocks<256>(a.eights);
     // (items, and their units, at most)
     const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);
-    const long long units = items * std::max(1, (max_pages * KV_PAGE + a.unit - 1) / a.unit);
+    const long long units = items * (a.extra + std::max(1, (max_pages * KV_PAGE + a.unit - 1) / a.unit));
     a.parts = static_cast<int>(std::min<long long>(1LL * ATTN_SMS * blocks, (units + a.least - 1) / a.least));
     a.joins = a.parts > 1 && max_pages * KV_PAGE > a.unit;
     return a;
@@ -328,6 +330,7 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     p.v_scale = cache->v_scale;
     p.window = window;
     p.sinks = sinks;
+    p.extra = a.extra;
     p.least = a.least;
     p.joins = static_cast<int4 *>(ws);
     p.stats = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + at.stats);

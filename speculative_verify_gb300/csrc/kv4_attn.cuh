@@ -270,7 +270,6 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
         fence_barrier_init();
     }
     __syncthreads();
-    pdl_launch_dependents();
     pdl_wait_prior();
     const uint64_t policy = policy_evict_first();
     // (found in what the rings are later)
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
 
     while (part.left > 0) {
         const KvItem &it = part.item;
-        const int u0 = it.unit, n = part.units();
+        const int u0 = part.unit, n = part.n;
         const int mine = n > warp ? (n - warp + KA_WARPS - 1) / KA_WARPS : 0;   // this warp's pages
         auto page_of = [&](int i) { return it.seq.before < 0 ? -1 : p.kv.at(it.b, it.span.at(u0 + warp + KA_WARPS * i)); };
         uint32_t there = 0;
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
         }
         if (warp == 0) {
             const bool whole = part.whole();
-            const int slot = 2 * blockIdx.x + (it.unit == 0);
+            const int slot = 2 * blockIdx.x + (part.unit == 0);
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -481,6 +480,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
         }
         part.next(p);
     }
+    // (only now: a join's blocks would wait in the places of later blocks of this kernel)
+    pdl_launch_dependents();
 }
 
 }  // namespace sv

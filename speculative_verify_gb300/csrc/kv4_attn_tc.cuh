@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = uniform(static_cast<uint32_t>(*slot_tm));
-    pdl_launch_dependents();
     pdl_wait_prior();
     // (found in what the ring is later)
     static_assert(sizeof(KvPartSmem) <= L::BLOCK, "room for the parts");
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 if (pk < it.seq.n * p.G)
                     prefetch_l2(p.q + (it.seq.first + tt) * p.ldq + static_cast<long long>(it.h * p.G + pk - tt * p.G) * D, 2 * D);
             }
-            const int n = part.units();
+            const int n = part.n;
             // a block's page: its entry in the table, asked for a step ahead and looked at when it is needed
             if (lane < 4) {
                 const int32_t *table = p.kv.table + it.b * p.kv.ldt;
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
                 // the unit of step j, and whether it is of values
                 auto unit = [&](int j) { return ring ? min(j + 1, n - 1) : max(j - 1, 0); };
-                auto page_at = [&](int j) { return it.span.at(it.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
+                auto page_at = [&](int j) { return it.span.at(part.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
                 int at = page_at(0), id = at < pages ? table[at] : -1;
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         KtTurn<L::BLOCKS> block;
         if (group) block.next();
         for (; part.left > 0; part.next(p)) {
-            const int n = part.units();
+            const int n = part.n;
 #pragma unroll 1
             for (int b = group; b < 2 * n; b += 2) {    // (an item has an even number of blocks)
                 const bool v = step(b, n).v;
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         };
         for (; uniform(static_cast<int>(part.left > 0)); part.next(p)) {
             const KvItem &it = part.item;
-            const int n = uniform(part.units());
+            const int n = uniform(part.n);
             const int tiles = uniform(NT == 2 && it.seq.n * p.G - it.tile * p.tile > KT_ROWS ? 2 : 1);
             for (int t = 0; t < tiles; ++t) wait(bar(L::Q_FULL + t), t ? items[NT - 1]++ : items[0]++);
             __syncwarp();
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
         if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (; part.left > 0; part.next(p)) {
             const KvItem &it = part.item;
-            const int n = part.units(), rows = min(p.tile, it.seq.n * p.G - it.tile * p.tile);
+            const int n = part.n, rows = min(p.tile, it.seq.n * p.G - it.tile * p.tile);
             const bool active = tile * KT_ROWS < rows;
             const int mine = tile * KT_ROWS + row, packed = it.tile * p.tile + mine;
             const bool in = mine < rows;
@@ -575,7 +574,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 uint32_t x[CHUNKS][32];
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j) tmem_ld32(at + 32 * j, x[j]);
-                const int first = it.span.at(it.unit + i) * KT_UNIT;
+                const int first = it.span.at(part.unit + i) * KT_UNIT;
                 const unsigned gone = missing[2 * ((units + i) & 15)] | missing[2 * ((units + i) & 15) + 1] << 1;
                 const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
                 tmem_wait_ld();
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
                 constexpr int COLS = D / SPLIT;
                 const int c0 = group * COLS;
-                const long long slot = (2LL * blockIdx.x + (it.unit == 0)) * p.tile + mine;
+                const long long slot = (2LL * blockIdx.x + (part.unit == 0)) * p.tile + mine;
                 // whole rows go through the queries' place, a warp's 32 rows in its eighth, so that a store has whole
                 // rows of neighbouring lanes
                 constexpr int CHUNKS = COLS / 8, TURNS = CHUNKS < 8 ? CHUNKS - 1 : 7;      // 16-byte pieces of a row
@@ -679,6 +678,7 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     }
     // every copy has landed and every product is done: the warps above have
     // waited for each
+    pdl_launch_dependents();
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();

@@ -7,7 +7,9 @@
 // tile sees (those of the first tokens, then those of the window).  The items of head 0, then
 // head 1 and so on make one line of units, cut into equal parts, one for a
 // thread block: uneven sequences and triangles of prompts cost no balance, and
-// one long sequence is spread over the whole GPU.
+// one long sequence is spread over the whole GPU.  An item's start and end cost
+// as much as some units (`extra`): it is that much longer on the line, and a part
+// that ends there leaves it to the next.
 //
 // A block whose part holds an item whole writes its outputs; of an item that
 // goes on into other parts each block leaves its sums, unnormalised, with
@@ -38,6 +40,7 @@ struct KvAttnParams {
     float scale;                                // of scores, with k_scale and log2 e
     float v_scale;
     int window, sinks;                          // 0: no window
+    int extra;                                  // what an item takes besides its units, in units
     int least;                                  // units of a part at least
     float *sums, *stats;                        // [2 parts][tile][d], [2 parts][tile][2]
     int4 *joins;                                // [parts]
@@ -84,16 +87,16 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, const KvSeq &s,
     return KvSpan{sinks, min(max(sinks, lo >> p.unit_log), to), to};
 }
 
-// An item, and a unit of it.
+// An item, and a place on the line that is its.
 struct KvItem {
-    int h, b, tile, unit;
+    int h, b, tile, place;
     KvSeq seq;
     KvSpan span;
 };
 
-// Units of one head's items of the 32 sequences from b0 on, and their rows
-// (whole warps call it); with `want` >= 0 also the item, with the unit in it,
-// that holds unit `want` of them.
+// Length of the line of one head's items of the 32 sequences from b0 on, and
+// their rows (whole warps call it); with `want` >= 0 also the item that has place
+// `want` of it.
 __device__ __forceinline__ long long kv_group(const KvAttnParams &p, int b0, long long want, KvItem *found, long long &rows)
 {
     const int lane = threadIdx.x & 31;
@@ -119,9 +122,9 @@ __device__ __forceinline__ long long kv_group(const KvAttnParams &p, int b0, lon
             long long units = 0;
             if (one) {
                 const int t = 32 * k + lane;
-                if (t < kv_tiles(p, seq)) units = kv_span(p, seq, t).units();
+                if (t < kv_tiles(p, seq)) units = p.extra + kv_span(p, seq, t).units();
             } else {
-                for (int t = 0; t < tiles; ++t) units += kv_span(p, seq, t).units();
+                for (int t = 0; t < tiles; ++t) units += p.extra + kv_span(p, seq, t).units();
             }
             long long run = units;
 #pragma unroll
@@ -139,11 +142,11 @@ __device__ __forceinline__ long long kv_group(const KvAttnParams &p, int b0, lon
                 found->seq.before = __shfl_sync(0xFFFFFFFFu, seq.before, w);
                 found->tile = one ? 32 * k + w : 0;
                 found->span = kv_span(p, found->seq, found->tile);
-                while (rest >= found->span.units()) {
-                    rest -= found->span.units();
+                while (rest >= p.extra + found->span.units()) {
+                    rest -= p.extra + found->span.units();
                     found->span = kv_span(p, found->seq, ++found->tile);
                 }
-                found->unit = static_cast<int>(rest);
+                found->place = static_cast<int>(rest);
                 return total;
             }
             total += __shfl_sync(0xFFFFFFFFu, run, 31);
@@ -152,10 +155,21 @@ __device__ __forceinline__ long long kv_group(const KvAttnParams &p, int b0, lon
     return total;
 }
 
-// A block's part of the line: the units that are left, and the item they are in.
+// A block's part of the line: what is left of it, and the item that it is in,
+// of which it has n > 0 units from `unit` on.
 struct KvPart {
     long long left, share;
+    int unit, n;
     KvItem item;
+
+    // The item's units in this part.
+    __device__ __forceinline__ void enter(const KvAttnParams &p)
+    {
+        const long long end = min(item.place + left, static_cast<long long>(p.extra + item.span.units()));
+        unit = max(0, item.place - p.extra);
+        n = max(0, static_cast<int>(end) - p.extra) - unit;
+        if (n <= 0) left = 0;                   // (it ends with the item's start)
+    }
 
     // Part k of `parts`, by one whole warp.  unit[g] and rows[g] are those of
     // group g of `groups`, or null: there are too many, and it goes through all.
@@ -201,19 +215,16 @@ struct KvPart {
             }
             at -= kv_group(p, b0, at, &item, r);
         }
-        if (item.b >= 0) left = min(share, all - lo);   // (else lengths were written meanwhile)
+        if (item.b < 0) return;                 // (lengths were written meanwhile)
+        left = min(share, all - lo);
+        enter(p);
     }
-    // Units of the item in this part.
-    __device__ __forceinline__ int units() const
-    {
-        return static_cast<int>(min(left, static_cast<long long>(item.span.units() - item.unit)));
-    }
-    // To the next item, whose units begin here.
+    // To the next item.
     __device__ __forceinline__ void next(const KvAttnParams &p)
     {
-        left -= units();
+        left -= p.extra + unit + n - item.place;
         if (left <= 0) return;
-        item.unit = 0;
+        item.place = 0;
         if (++item.tile >= kv_tiles(p, item.seq)) {
             item.tile = 0;
             do {
@@ -228,12 +239,13 @@ struct KvPart {
             } while (item.seq.n <= 0);
         }
         item.span = kv_span(p, item.seq, item.tile);
+        enter(p);
     }
-    __device__ __forceinline__ bool whole() const { return item.unit == 0 && units() == item.span.units(); }
+    __device__ __forceinline__ bool whole() const { return unit == 0 && n == item.span.units(); }
     // Whether the item starts here, and goes on in this many parts in all.
     __device__ __forceinline__ int parts() const
     {
-        return item.unit ? 0 : 1 + static_cast<int>((item.span.units() - units() + share - 1) / share);
+        return unit ? 0 : 1 + static_cast<int>((item.span.units() - n + share - 1) / share);
     }
 };
 
