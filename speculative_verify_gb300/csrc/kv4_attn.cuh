@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
     using S = KaShape<D, NQ>;
     extern __shared__ __align__(128) uint8_t ka_smem[];
     __shared__ volatile int failed;
+    const TcWait wait{&failed, p.err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     uint8_t *ring = ka_smem + warp * S::RING;
     const uint32_t bars = smem_addr(ka_smem + S::BARS) + 8 * warp * S::STAGES;
@@ -284,22 +285,32 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
         const KvItem &it = part.item;
         const int u0 = part.unit, n = part.n;
         const int mine = n > warp ? (n - warp + KA_WARPS - 1) / KA_WARPS : 0;   // this warp's pages
-        auto page_of = [&](int i) { return it.seq.before < 0 ? -1 : p.kv.at(it.b, it.span.at(u0 + warp + KA_WARPS * i)); };
-        uint32_t there = 0;
-        auto ask = [&](int i, int page) {
-            const int st = i % S::STAGES;
-            if (page < 0) {
-                there &= ~(1u << st);
+        // its i-th page's place in the sequence, and its entry in the table
+        auto place = [&](int i) { return it.span.at(u0 + warp + KA_WARPS * i); };
+        const int32_t *table = p.kv.table + it.b * p.kv.ldt;
+        const int pages = it.seq.before < 0 ? 0 : p.kv.max_pages;
+        auto entry = [&](int i) { return i < mine && place(i) < pages ? table[place(i)] : -1; };
+        const uint8_t *head = p.kv.pages + static_cast<long long>(it.h) * S::STAGE;
+        const long long stride = static_cast<long long>(p.kv.Hk) * S::STAGE;
+        uint32_t there = 0;                     // bit i: stage i holds a page
+        int at_in = 0, at = 0;                  // stages: of the next copy, of the next page
+        auto ask = [&](int id) {
+            if (id >= 0 && id < p.kv.n_pages) {
+                there |= 1u << at_in;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bars + 8 * at_in, S::STAGE);
+                    bulk_g2s(smem_addr(ring) + at_in * S::STAGE, head + id * stride, S::STAGE, bars + 8 * at_in, policy);
+                }
+            } else {
+                there &= ~(1u << at_in);
                 if (it.seq.before >= 0 && lane == 0) atomicOr(p.err, KV_ERR_PAGE);
-                return;
             }
-            there |= 1u << st;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bars + 8 * st, S::STAGE);
-                bulk_g2s(smem_addr(ring + st * S::STAGE), p.kv.head<D>(page, it.h), S::STAGE, bars + 8 * st, policy);
-            }
+            if (++at_in == S::STAGES) at_in = 0;
         };
-        for (int i = 0; i < S::STAGES - 1 && i < mine; ++i) ask(i, page_of(i));
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; ++i)
+            if (i < mine) ask(entry(i));
+        int id_next = entry(S::STAGES - 1);     // (read a page ahead)
 
         // the tile's queries: this thread has row g of each eight
         const int rows = min(S::ROWS, it.seq.n * p.G - it.tile * S::ROWS);
@@ -371,24 +382,25 @@ __global__ void __launch_bounds__(KA_WARPS * 32, (KaShape<D, NQ>::BLOCKS)) kv4_a
         const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
 
         if (threadIdx.x == 0 && it.seq.before >= 0 && it.seq.before + t1 >= p.kv.max_pages * KV_PAGE) atomicOr(p.err, KV_ERR_PAGE);
+        const int sinks = p.window > 0 ? p.sinks : 0;
         KaWarp<D, NQ> w;
         w.clear();
+#pragma unroll 1
         for (int i = 0; i < mine; ++i) {
-            const int nx = i + S::STAGES - 1;
             fence_proxy_async();                // (the stage has been read before a copy may write there)
             __syncwarp();
-            if (nx < mine) ask(nx, page_of(nx));
-            const int st = i % S::STAGES;
-            if (there >> st & 1) {
-                if (!mbar_wait_bounded(bars + 8 * st, phases >> st & 1, failed ? WAIT_LIMIT_AFTER_ERR_NS : WAIT_LIMIT_NS)) {
-                    failed = 1;
-                    atomicOr(p.err, 2);
-                }
-                phases ^= 1u << st;
-                const int first = KV_PAGE * it.span.at(u0 + warp + KA_WARPS * i);
-                const bool all = first + KV_PAGE - 1 <= to && (first >= from || first + KV_PAGE <= p.sinks);
-                w.page(ring + st * S::STAGE, query, first, all, pos, low, p.window > 0 ? p.sinks : 0, scale);
+            if (i + S::STAGES - 1 < mine) {
+                ask(id_next);
+                id_next = entry(i + S::STAGES);
             }
+            if (there >> at & 1) {
+                wait(bars + 8 * at, phases >> at);
+                phases ^= 1u << at;
+                const int first = KV_PAGE * place(i);
+                const bool all = first + KV_PAGE - 1 <= to && (first >= from || first + KV_PAGE <= p.sinks);
+                w.page(ring + at * S::STAGE, query, first, all, pos, low, sinks, scale);
+            }
+            if (++at == S::STAGES) at = 0;
         }
         __syncwarp();
 
