@@ -287,6 +287,11 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 auto unit = [&](int j) { return ring ? min(j + 1, n - 1) : max(j - 1, 0); };
                 auto page_at = [&](int j) { return it.span.at(part.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
                 int at = page_at(0), id = at < pages ? table[at] : -1;
+                // and of the keys' lanes, the whole page of some units ahead on its way to L2: the ring is too short for
+                // a copy from HBM
+                constexpr int AHEAD = 8;
+                auto far = [&](int j) { return ring && j + AHEAD < n ? it.span.at(part.unit + j + AHEAD) * (KT_UNIT / KV_PAGE) + sub : pages; };
+                int at_far = far(0), id_far = at_far < pages ? table[at_far] : -1;
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     const bool v = ring ? j == n - 1 : j > 0, here = at < pages && id >= 0 && id < p.kv.n_pages;
@@ -295,6 +300,9 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     const int u = unit(j);
                     at = page_at(j + 1);
                     if (j + 1 < n) id = at < pages ? table[at] : -1;
+                    if (id_far >= 0 && id_far < p.kv.n_pages) prefetch_l2(head + id_far * stride, kv_head_bytes(D));
+                    at_far = far(j + 1);
+                    id_far = at_far < pages ? table[at_far] : -1;
                     if (!v) missing[2 * ((units + u) & 15) + sub] = !here;
                     const int slot = ring * L::TURN + turn.at;
                     if (turn.round) wait(bar(L::RAW_EMPTY + slot), turn.round - 1);
