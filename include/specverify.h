@@ -601,7 +601,7 @@ int w4a16_gate_up(const sv_bf16 *x, const uint32_t *Wq, const sv_bf16 *scales, i
  * reduced exactly, for every 32-bit position (within 2^-24 of a turn for
  * frequencies up to 1 a step); cos, sin and the products are fp32, rounded
  * once to bf16.
- * 16 <= rot <= d <= 1024, rot a multiple of 16, d of 8; 1 <= n_axes <= 16;
+ * rows <= 2^30; 16 <= rot <= d <= 1024, rot a multiple of 16, d of 8; 1 <= n_axes <= 16;
  * the lds of q and k multiples of 8, addresses 16-byte aligned.
  */
 int rotary_embed(const sv_bf16 *q, long long ldq, int Hq, const sv_bf16 *k, long long ldk, int Hk, int rows, int d, int rot,
@@ -673,7 +673,9 @@ int kv4_gather(sv_bf16 *k, long long ldk, sv_bf16 *v, long long ldv, int R, cons
  * scales alone count as 448.
  * `ws` is device memory of at least kv4_attention_bytes (0 when the sizes are
  * invalid; `ragged`: cu_seqlens is given), 16-byte aligned, free until the
- * call has run; calls that may overlap need one each.  R * (Hq / Hk) <= 2^29.
+ * call has run; calls that may overlap need one each.  R * (Hq / Hk) <= 2^29,
+ * R * Hq <= 2^33, scale * k_scale within fp32's range.  Pages that no row of the
+ * call sees (before all windows) may be gone from the table.
  * Results do not depend on timing.  Decreasing cu_seqlens that claim more
  * rows than R set SV_DEVERR_BAD_SEQLENS, and nothing is written.
  */

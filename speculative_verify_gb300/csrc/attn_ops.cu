@@ -194,7 +194,7 @@ struct AttnSpace {
 
 int check_attention(int R, int B, int Hq, const sv_kv4_cache *c)
 {
-    if (Hq < 1 || Hq % c->Hk || 1LL * R * (Hq / c->Hk) > (1 << 29)) return SV_ERR_SHAPE;
+    if (Hq < 1 || Hq % c->Hk || 1LL * R * (Hq / c->Hk) > (1 << 29) || 1LL * R * Hq > (1LL << 33)) return SV_ERR_SHAPE;
     return SV_OK;
 }
 
@@ -231,7 +231,7 @@ int rotary_embed(const sv_bf16 *q, long long ldq, int Hq, const sv_bf16 *k, long
                  float factor, int flags, sv_bf16 *q_out, long long ldqo, sv_bf16 *k_out, long long ldko, sv_stream stream)
 {
     using namespace sv;
-    if (rows < 0 || Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535 || Hq + Hk < 1) return SV_ERR_SHAPE;
+    if (rows < 0 || rows > 1 << 30 || Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535 || Hq + Hk < 1) return SV_ERR_SHAPE;
     if (d < 16 || d > RO_MAX_DIM || d % 8 || rot < 16 || rot > d || rot % 16) return SV_ERR_SHAPE;
     if (n_axes < 1 || n_axes > 16 || (flags & ~SV_ROTARY_PAIRED) || !std::isfinite(factor)) return SV_ERR_SHAPE;
     if (rows == 0) return SV_OK;
@@ -297,7 +297,9 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     if (rc == SV_OK) rc = check_attention(R, B, Hq, cache);
     if (rc != SV_OK) return rc;
     const long long n = 1LL * Hq * cache->d;
-    if (!std::isfinite(scale) || window < 0 || sinks < 0 || window > (1 << 30) || sinks > (1 << 30)) return SV_ERR_SHAPE;
+    // (of scores in units of log2)
+    const float log_scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+    if (!std::isfinite(log_scale) || window < 0 || sinks < 0 || window > (1 << 30) || sinks > (1 << 30)) return SV_ERR_SHAPE;
     if (R > 0 && (ldq < n || ldo < n)) return SV_ERR_SHAPE;
     if (R > 0 && (!q || !o)) return SV_ERR_NULL;
     if (R > 0 && (ldq % 8 || ldo % 8 || !aligned_to(q, 16) || !aligned_to(o, 16))) return SV_ERR_ALIGN;
@@ -326,7 +328,7 @@ int kv4_attention(const sv_bf16 *q, long long ldq, int R, int Hq, const int32_t 
     while (1 << c < G) ++c;
     p.g_shift = 30 + c;
     p.g_mul = static_cast<unsigned>(((1ull << p.g_shift) + static_cast<unsigned>(G) - 1) / static_cast<unsigned>(G));
-    p.scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+    p.scale = log_scale;
     p.v_scale = cache->v_scale;
     p.window = window;
     p.sinks = sinks;

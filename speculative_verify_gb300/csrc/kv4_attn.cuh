@@ -17,8 +17,8 @@
 //     operand; an A row is a dimension, and a pair of tokens' values are put
 //     together by byte permutation.  Thread row g has dimensions g d / 8 .., so
 //     that it ends with neighbouring ones.
-//   * Sums and the softmax are fp32, probabilities fp16 (2^-12 of each,
-//     independent).  They are taken relative to a maximum that is only moved
+//   * Sums and the softmax are fp32, probabilities fp16 (off by 2^-11 at
+//     most of each, independent, where 8 bits of bf16 would show in the outputs).  They are taken relative to a maximum that is only moved
 //     when a score passes it by 2^8, so most pages rescale nothing.
 #pragma once
 

@@ -283,10 +283,14 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 const int32_t *table = p.kv.table + it.b * p.kv.ldt;
                 const uint8_t *head = p.kv.pages + static_cast<long long>(it.h) * kv_head_bytes(D);
                 const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
+                // (a unit at the window's start, or at the sinks' end, may hold a page that no row sees: it may be gone)
+                const int low = p.window > 0 ? max(0, it.seq.before + kv_token(p, it.tile * p.tile) - p.window + 1) : 0;
+                const int low_page = low / KV_PAGE, sink_pages = (min(p.sinks, low) + KV_PAGE - 1) / KV_PAGE;
+                auto seen = [&](int i) { return i < pages && (i >= low_page || i < sink_pages); };
                 // the unit of step j, and whether it is of values
                 auto unit = [&](int j) { return ring ? min(j + 1, n - 1) : max(j - 1, 0); };
                 auto page_at = [&](int j) { return it.span.at(part.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
-                int at = page_at(0), id = at < pages ? table[at] : -1;
+                int at = page_at(0), id = seen(at) ? table[at] : -1;
                 // and of the keys' lanes, the whole page of some units ahead on its way to L2: the ring is too short for
                 // a copy from HBM
                 constexpr int AHEAD = 8;
@@ -294,12 +298,12 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 int at_far = far(0), id_far = at_far < pages ? table[at_far] : -1;
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
-                    const bool v = ring ? j == n - 1 : j > 0, here = at < pages && id >= 0 && id < p.kv.n_pages;
-                    if (at < pages && !here) atomicOr(p.err, KV_ERR_PAGE);
+                    const bool v = ring ? j == n - 1 : j > 0, here = seen(at) && id >= 0 && id < p.kv.n_pages;
+                    if (seen(at) && !here) atomicOr(p.err, KV_ERR_PAGE);
                     const uint8_t *src = head + id * stride;
                     const int u = unit(j);
                     at = page_at(j + 1);
-                    if (j + 1 < n) id = at < pages ? table[at] : -1;
+                    if (j + 1 < n) id = seen(at) ? table[at] : -1;
                     if (id_far >= 0 && id_far < p.kv.n_pages) prefetch_l2(head + id_far * stride, kv_head_bytes(D));
                     at_far = far(j + 1);
                     id_far = at_far < pages ? table[at_far] : -1;

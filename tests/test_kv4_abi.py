@@ -70,6 +70,22 @@ def test_rotary_refusals(lib, kw, code):
     assert lib.rotary_embed(*a.values(), None) == code
 
 
+@nogpu
+def test_sizes_past_the_index_range_are_refused(lib):
+    """Rows whose count rounds up past 31 bits, query heads beyond any memory, a scale that leaves fp32 with k_scale."""
+    assert lib.rotary_embed(A, 16, 1, None, 0, 0, (1 << 30) + 1, 16, 16, A, (1 << 30) + 1, 1, None, A, 1.0, 0, A, 16, None, 0,
+                            None) == SHAPE
+
+    def attention(R, Hq, scale=1.0, **kw):
+        c = cache_of(kw)
+        assert (lib.kv4_attention_bytes(R, 4, 0, Hq, ctypes.byref(c)) == 0) == (scale == 1.0)
+        return lib.kv4_attention(A, Hq * 64, R, Hq, None, A, 4, ctypes.byref(c), scale, 0, 0, A, Hq * 64, A, 1 << 60, None)
+
+    assert attention(1 << 29, 64, Hk=64) == SHAPE
+    assert attention(8, 8, scale=1e38, k_scale=1e3) == SHAPE
+    assert attention(8, 8, scale=-3.4e38) == SHAPE
+
+
 def cache_of(kw):
     c = dict(pages=A, page_table=A, ldt=8, n_pages=20, max_pages=8, Hk=2, d=64, k_scale=1.0, v_scale=1.0)
     c.update({n: kw.pop(n) for n in list(kw) if n in c})

@@ -262,6 +262,27 @@ def test_window_and_sinks(sv, d, Hq, Hk, T, window, sinks):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(1, 4), (4, 4), (9, 3), (150, 2)])
+@pytest.mark.parametrize("before", [300, 320, 345, 363])
+@pytest.mark.parametrize("window,sinks", [(70, 0), (33, 7), (96, 40), (64, 70)])
+def test_pages_before_the_windows_may_be_gone(sv, d, T, G, before, window, sinks):
+    """Table entries of pages that no row sees are no pages: not reported, and the same bits."""
+    gen = rng_of(17)
+    n = (before + T + 31) // 32
+    cache, table = ref.filled(gen, n, 1, d), ref.shuffled(gen, [n])
+    q = randn(gen, 1, T, G, d).bfloat16()
+    kw = dict(window=window, sinks=sinks)
+    want = sv.kv4_attention(q, cache, table, ints([before]), **kw)
+    first = max(0, before - window + 1)         # that the first row sees, besides the sinks
+    for i in range((min(sinks, first) + 31) // 32, first // 32):
+        table[0, i] = -1
+    assert bool((table < 0).any())
+    got = sv.kv4_attention(q, cache, table, ints([before]), **kw)
+    assert sv.last_device_error() == 0 and torch.equal(got, want)
+    ref.check_attention(got, ref.attention(q, cache, table.clamp(min=0), ints([before]), **kw))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
 @pytest.mark.parametrize("Hq,Hk", [(4, 1), (8, 8), (24, 4), (7, 1)])
 def test_prompts(sv, d, window, sinks, Hq, Hk):
