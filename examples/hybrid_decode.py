@@ -10,9 +10,18 @@ never advanced past unverified drafts: a cycle hands its rows to the next one
 as ``prev`` with the accept_len that the head wrote, on the device, and the
 accepted ones are replayed there.
 
+With Config(attention_every=n) every n-th layer is an attention layer instead:
+
+    rmsnorm -> w4a16_gemm (QKV) -> rotary -> kv4_append -> kv4_attention -> w4a16_gemm (out) ...
+
+over a cache of 4-bit pages.  Its rows are appended before they are verified: a
+cycle moves the sequences' lengths on by the accepted rows alone, on the
+device, and the next one writes over the others.
+
 Weights are random (seeded), so the text means nothing and no cheap drafter
 could guess it: the drafts are the text of a run without drafts, with every
 fifth token wrong.  Run: python examples/hybrid_decode.py
+[attention_every]
 """
 import os
 import sys
@@ -39,6 +48,24 @@ class Config:
     dv: int = 128
     ffn: int = 1408
     vocab: int = 4096
+    attention_every: int = 0            # every n-th layer attends; 0: none
+    heads: int = 8                      # of its queries
+    kv_heads: int = 2
+    head_dim: int = 128
+    window: int = 0                     # tokens that it sees besides the first `sinks`; 0: all
+    sinks: int = 4
+    max_tokens: int = 1024              # of a sequence
+
+    def attends(self, i):
+        return self.attention_every > 0 and (i + 1) % self.attention_every == 0
+
+
+class Cache:
+    """An attention layer's pages and the sequences' tables of them."""
+    def __init__(self, cfg, B):
+        n = -(-cfg.max_tokens // sv.KV4_PAGE)
+        self.pages = sv.kv4_cache(B * n, cfg.kv_heads, cfg.head_dim)
+        self.table = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n)
 
 
 class Model:
@@ -54,25 +81,46 @@ class Model:
         def dense(*shape, scale=1.0):
             return torch.from_numpy(rng.standard_normal(shape).astype(np.float32) * scale).to(dev)
 
-        c, nv = cfg, cfg.value_heads * cfg.dv
+        c = cfg
         self.embed = dense(c.vocab, c.hidden).bfloat16()
         self.layers = [dict(norm1=(1 + 0.1 * dense(c.hidden)).bfloat16(), norm2=(1 + 0.1 * dense(c.hidden)).bfloat16(),
-                            qkv=packed(2 * c.key_heads * c.dk + nv, c.hidden), out=packed(c.hidden, nv),
+                            qkv=packed(self.widths(i)[0], c.hidden), out=packed(c.hidden, self.widths(i)[1]),
                             gates=dense(c.hidden, 2 * c.value_heads, scale=c.hidden ** -0.5).bfloat16(),
                             rate=torch.from_numpy(rng.uniform(0.02, 0.5, c.value_heads).astype(np.float32)).to(dev),
                             gate_up=packed(2 * c.ffn, c.hidden), down=packed(c.hidden, c.ffn))
-                       for _ in range(c.layers)]
+                       for i in range(c.layers)]
         self.norm = (1 + 0.1 * dense(c.hidden)).bfloat16()
         self.head = packed(c.vocab, c.hidden)
+        half = c.head_dim // 2
+        self.inv_freq = 1e4 ** (-torch.arange(half, device=dev) / half)
+
+    def widths(self, i):
+        """Columns of layer i's fused QKV projection and of its heads' outputs."""
+        c = self.cfg
+        if c.attends(i):
+            return (c.heads + 2 * c.kv_heads) * c.head_dim, c.heads * c.head_dim
+        return 2 * c.key_heads * c.dk + c.value_heads * c.dv, c.value_heads * c.dv
 
     def states(self, B):
-        """Zero states of B sequences, one tensor a layer."""
+        """Zero states of B sequences, one tensor a layer; attention layers' caches."""
         c = self.cfg
-        return [torch.zeros(B, c.value_heads, c.dv, c.dk, device="cuda") for _ in range(c.layers)]
+        return [Cache(c, B) if c.attends(i) else torch.zeros(B, c.value_heads, c.dv, c.dk, device="cuda")
+                for i in range(c.layers)]
 
-    def forward(self, tokens, delta):
+    def attend(self, cache, qkv, positions, lens, cu=None):
+        """An attention layer: qkv [B][T] or, with cu, [R] rows of queries, keys
+        and values, whose sequences have lens tokens before them."""
+        c = self.cfg
+        nq, nk = c.heads * c.head_dim, c.kv_heads * c.head_dim
+        q, k, v = (t.unflatten(-1, (-1, c.head_dim)) for t in qkv.split((nq, nk, nk), -1))
+        q, k = sv.rotary(q, k, positions, self.inv_freq)
+        sv.kv4_append(k, v, cache.pages, cache.table, lens, cu)
+        return sv.kv4_attention(q, cache.pages, cache.table, lens, cu, window=c.window, sinks=c.sinks if c.window else 0)
+
+    def forward(self, tokens, delta, attend=None):
         """The last norm's rows [n][hidden] for tokens [n]; delta(layer, q, k,
-        v, g, beta) runs the gated delta rule on the n rows."""
+        v, g, beta) runs the gated delta rule on the n rows, attend(layer, qkv)
+        an attention layer."""
         c, n, nk = self.cfg, tokens.numel(), self.cfg.key_heads * self.cfg.dk
 
         def by_slices(f, x, *w):        # a weight pass takes up to 32 rows
@@ -83,12 +131,16 @@ class Model:
         res = self.embed[tokens]
         y, _ = sv.rmsnorm(res, self.layers[0]["norm1"])
         for i, w in enumerate(self.layers):
-            qkv = torch.nn.functional.silu(by_slices(sv.w4a16_gemm, y, *w["qkv"]))
-            gates = (y @ w["gates"]).float()
-            g = -w["rate"] * torch.nn.functional.softplus(gates[:, :c.value_heads])
-            beta = torch.sigmoid(gates[:, c.value_heads:]).contiguous()
-            o = delta(i, qkv[:, :nk].unflatten(1, (c.key_heads, c.dk)), qkv[:, nk:2 * nk].unflatten(1, (c.key_heads, c.dk)),
-                      qkv[:, 2 * nk:].unflatten(1, (c.value_heads, c.dv)), g, beta)
+            qkv = by_slices(sv.w4a16_gemm, y, *w["qkv"])
+            if c.attends(i):
+                o = attend(i, qkv)
+            else:
+                qkv = torch.nn.functional.silu(qkv)
+                gates = (y @ w["gates"]).float()
+                g = -w["rate"] * torch.nn.functional.softplus(gates[:, :c.value_heads])
+                beta = torch.sigmoid(gates[:, c.value_heads:]).contiguous()
+                o = delta(i, qkv[:, :nk].unflatten(1, (c.key_heads, c.dk)), qkv[:, nk:2 * nk].unflatten(1, (c.key_heads, c.dk)),
+                          qkv[:, 2 * nk:].unflatten(1, (c.value_heads, c.dv)), g, beta)
             a = by_slices(sv.w4a16_gemm, o.reshape(n, -1), *w["out"])
             y, res = sv.rmsnorm(a, w["norm2"], residual=res)
             h = by_slices(sv.w4a16_gate_up, y, *w["gate_up"])
@@ -102,30 +154,40 @@ class Model:
         lens = [len(p) for p in prompts]
         cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
         tokens = torch.tensor(sum(prompts, []), device="cuda")
+        positions = torch.cat([torch.arange(n, dtype=torch.int32, device="cuda") for n in lens])
         y = self.forward(tokens, lambda i, q, k, v, g, beta: sv.gated_delta_chunk(
-            q, k, v, g, beta, cu, states[i], zero_init=True, l2norm=True))
+            q, k, v, g, beta, cu, states[i], zero_init=True, l2norm=True),
+            lambda i, qkv: self.attend(states[i], qkv, positions, torch.zeros_like(cu[1:]), cu))
         ends = y[(cu[1:] - 1).long()].contiguous()
         return sv.lmhead_argmax(ends, *self.head)[0]
 
-    def verify(self, tokens, states, prev=None, accept_len=None, commit=False):
+    def verify(self, tokens, states, prev=None, accept_len=None, commit=False, lens=None):
         """One cycle over tokens [B][1 + drafts]: (accept_len, next_token, rows
-        for the next cycle's prev)."""
+        for the next cycle's prev).  lens [B] (with attention layers): the tokens
+        before them."""
         B, T = tokens.shape
-        rows = []
+        rows = [None] * self.cfg.layers
 
         def delta(i, q, k, v, g, beta):
             q, k, v, g, beta = (t.unflatten(0, (B, T)) for t in (q, k, v, g, beta))
-            rows.append((k, v, g, beta))
+            rows[i] = (k, v, g, beta)
             return sv.gated_delta_step(q, k, v, g, beta, states[i], prev=prev and prev[i], accept_len=accept_len,
                                        commit=commit, l2norm=True)
 
-        y = self.forward(tokens.reshape(-1).long(), delta)
+        def attend(i, qkv):
+            positions = lens[:, None] + torch.arange(T, dtype=torch.int32, device="cuda")
+            return self.attend(states[i], qkv.unflatten(0, (B, T)), positions, lens)
+
+        y = self.forward(tokens.reshape(-1).long(), delta, attend)
         acc, nxt = sv.lmhead_verify_batched(y, *self.head, tokens[:, 1:].contiguous())
         return acc, nxt, rows
 
     def replay(self, states, prev, accept_len):
         """The last cycle's accepted rows into the states, no new rows."""
-        for i, (k, v, g, beta) in enumerate(prev):
+        for i, rows in enumerate(prev):
+            if rows is None:            # (an attention layer)
+                continue
+            k, v, g, beta = rows
             q = k[:, :0]
             sv.gated_delta_step(q, q, v[:, :0], g[:, :0], beta[:, :0], states[i], prev=(k, v, g, beta),
                                 accept_len=accept_len, l2norm=True)
@@ -150,10 +212,12 @@ def generate(model, prompts, n_tokens, n_draft=0, draft=None):
     text = [p + [t] for p, t in zip(prompts, first)]
     prev = acc = None
     cycles = 0
+    lens = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device="cuda")
     while min(len(t) - len(p) for t, p in zip(text, prompts)) < n_tokens:
         drafts = [draft(t, n_draft) if n_draft else [] for t in text]
         tokens = torch.tensor([[t[-1]] + d for t, d in zip(text, drafts)], dtype=torch.int32, device="cuda")
-        acc, nxt, prev = model.verify(tokens, states, prev, acc)
+        acc, nxt, prev = model.verify(tokens, states, prev, acc, lens=lens)
+        lens = lens + acc + 1
         for t, d, a, x in zip(text, drafts, acc.tolist(), nxt.tolist()):
             t += d[:a] + [x]
         cycles += 1
@@ -164,7 +228,7 @@ def generate(model, prompts, n_tokens, n_draft=0, draft=None):
 
 def main():
     rng = np.random.default_rng(1)
-    cfg = Config()
+    cfg = Config(attention_every=int(sys.argv[1]) if len(sys.argv) > 1 else 0)
     model = Model(cfg)
     prompts = [rng.integers(0, cfg.vocab, n).tolist() for n in (300, 41)]
     new, cycles, _ = generate(model, prompts, 48)
