@@ -42,9 +42,12 @@ int attn_device(DeviceInfo *out)
     up(kv4_attn_kernel<128, 2>, KaShape<128, 2>::BYTES);
     up(kv4_attn_kernel<256, 1>, KaShape<256, 1>::BYTES);
     up(kv4_attn_kernel<256, 2>, KaShape<256, 2>::BYTES);
-    up(kv4_join_kernel<64>, 0);         // (the same share: a multiprocessor changes it only when it is empty)
-    up(kv4_join_kernel<128>, 0);
-    up(kv4_join_kernel<256>, 0);
+    up(kv4_join_kernel<64, 1>, 0);      // (the same share: a multiprocessor changes it only when it is empty)
+    up(kv4_join_kernel<64, 4>, 0);
+    up(kv4_join_kernel<128, 1>, 0);
+    up(kv4_join_kernel<128, 4>, 0);
+    up(kv4_join_kernel<256, 1>, 0);
+    up(kv4_join_kernel<256, 4>, 0);
     up(kv4_attn_tc_kernel<64, 1>, KtSmem<64, 1>::BYTES);
     up(kv4_attn_tc_kernel<64, 2>, KtSmem<64, 2>::BYTES);
     up(kv4_attn_tc_kernel<128, 1>, KtSmem<128, 1>::BYTES);
@@ -151,6 +154,7 @@ int kv_rows_call(uint16_t *k, long long ldk, uint16_t *v, long long ldv, int R, 
 struct AttnPlan {
     int eights, tiles, tile, unit, extra, parts, least;
     bool joins;                                 // an item may go over several parts
+    int groups;                                 // of threads of a block that joins them
 };
 
 // The parts are counted for a GPU of this size whatever the device, so that
@@ -170,12 +174,14 @@ AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
     a.tile = a.tiles ? a.tiles * KT_ROWS : 8 * a.eights;
     a.unit = a.tiles ? KT_UNIT : KV_PAGE;
     a.extra = a.tiles ? 10 : 4;
-    a.least = a.tiles ? 4 + a.extra : 2 * KA_WARPS + a.extra;
+    a.least = KA_WARPS;
     const int blocks = a.tiles ? 1 : d == 64 ? attn_blocks<64>(a.eights) : d == 128 ? attn_blocks<128>(a.eights) : attn_blocks<256>(a.eights);
     // (items, and their units, at most)
     const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);
     const long long units = items * (a.extra + std::max(1, (max_pages * KV_PAGE + a.unit - 1) / a.unit));
     a.parts = static_cast<int>(std::min<long long>(1LL * ATTN_SMS * blocks, (units + a.least - 1) / a.least));
+    const long long least_items = Hk * std::max<long long>(B, (1LL * R * G + a.tile - 1) / a.tile);
+    a.groups = a.parts >= 8 * least_items ? 4 : 1;
     a.joins = a.parts > 1 && max_pages * KV_PAGE > a.unit;
     return a;
 }
@@ -216,9 +222,12 @@ int attn_launch(const KvAttnParams &p, const AttnPlan &a, cudaStream_t stream)
             rc = SV_ERR_SHAPE;                  // (not planned)
     }
     if (rc != SV_OK || !a.joins) return rc;
-    constexpr int rows = KJ_VALUES / D;
-    return launch(kv4_join_kernel<D>, dim3(static_cast<unsigned>(a.parts), static_cast<unsigned>((a.tile + rows - 1) / rows)),
-                  KJ_THREADS, 0, stream, p);
+    // (rows that an item has at most: a block without rows costs its launch all the same)
+    constexpr int ROWS = KJ_VALUES / D;
+    const long long rows = std::min<long long>(a.tile, 1LL * (p.rows.cu ? p.rows.R : p.rows.T) * p.G);
+    const dim3 joins(static_cast<unsigned>(a.parts), static_cast<unsigned>((rows + ROWS - 1) / ROWS));
+    return a.groups == 4 ? launch(kv4_join_kernel<D, 4>, joins, 4 * KJ_THREADS, 0, stream, p)
+                         : launch(kv4_join_kernel<D, 1>, joins, KJ_THREADS, 0, stream, p);
 }
 
 }  // namespace

@@ -283,18 +283,21 @@ __device__ __forceinline__ KvPart kv_part(const KvAttnParams &p, KvPartSmem &sm)
     return sm.part;
 }
 
-constexpr int KJ_THREADS = 128;
-constexpr int KJ_VALUES = 4 * KJ_THREADS;       // output values of a block
+constexpr int KJ_VALUES = 512;                  // output values of a block, four of a thread
+constexpr int KJ_THREADS = KJ_VALUES / 4;       // of a group
 constexpr int KJ_MAX_PARTS = 1024;
 
 // Block (p, s): values s KJ_VALUES .. of the item that starts in part p and
-// goes on, joined from its parts.
-template <int D>
-__global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams p)
+// goes on, joined from its parts.  What bounds it is the chain of loads over
+// the parts: hence eight loads at a time, and where the parts are many GROUPS
+// of threads that share them out.
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(GROUPS *KJ_THREADS) kv4_join_kernel(const KvAttnParams p)
 {
     constexpr int ROWS = KJ_VALUES / D;
     __shared__ float weight[ROWS][KJ_MAX_PARTS];
     __shared__ float norm[ROWS];
+    __shared__ float4 others[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? KJ_THREADS : 1];    // (not the first group's)
     pdl_wait_prior();                           // (without an early start of the next kernel: it cost an attention 70 of 190 us)
     const int part = blockIdx.x, row0 = blockIdx.y * ROWS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 join = p.joins[part];            // parts; head, sequence, tile
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams
     const int rows = min(p.tile, seq.n * p.G - join.w * p.tile), n = join.x;
     if (row0 >= rows) return;
     auto slot = [&](int i) { return static_cast<long long>(2 * (part + i) + (i == 0)) * p.tile; };
-    for (int r = warp; r < ROWS; r += KJ_THREADS / 32) {
+    for (int r = warp; r < ROWS; r += GROUPS * KJ_THREADS / 32) {
         if (row0 + r >= rows) continue;
         const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + row0 + r;
         float top = -INFINITY;
@@ -323,12 +326,13 @@ __global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams
         if (lane == 0) norm[r] = total == 0.f ? 0.f : p.v_scale / total;
     }
     __syncthreads();
-    const int r = 4 * threadIdx.x / D, d = 4 * threadIdx.x % D, row = row0 + r;
-    if (row >= rows) return;
+    const int group = threadIdx.x / KJ_THREADS, value = threadIdx.x % KJ_THREADS;
+    const int r = 4 * value / D, d = 4 * value % D, row = row0 + r;
+    const bool in = row < rows;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const float *sums = p.sums + static_cast<long long>(row) * D + d;
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
+    for (int i = group; i < n && in; i += GROUPS) {
         const float4 v = ldcg_f4(sums + slot(i) * D);
         const float w = weight[r][i];
         acc.x = fmaf(w, v.x, acc.x);
@@ -336,6 +340,19 @@ __global__ void __launch_bounds__(KJ_THREADS) kv4_join_kernel(const KvAttnParams
         acc.z = fmaf(w, v.z, acc.z);
         acc.w = fmaf(w, v.w, acc.w);
     }
+    if (GROUPS > 1) {
+        if (group) others[group][value] = acc;
+        __syncthreads();
+#pragma unroll
+        for (int k = 1; k < GROUPS; ++k) {
+            const float4 v = others[k][value];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+    }
+    if (group || !in) return;
     const int packed = join.w * p.tile + row, t = kv_token(p, packed), g = packed - t * p.G;
     uint16_t *o = p.o + (seq.first + t) * p.ldo + static_cast<long long>(join.y * p.G + g) * D + d;
     const float f = norm[r];
