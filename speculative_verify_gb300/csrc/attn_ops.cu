@@ -164,17 +164,40 @@ constexpr int ATTN_SMS = 152;
 template <int D>
 constexpr int attn_blocks(int eights) { return eights == 1 ? KaShape<D, 1>::BLOCKS : KaShape<D, 2>::BLOCKS; }
 
+// Packed rows (a sequence's tokens times G) choose the kernel.
+//   * Items of 8 rows, else 16, of kv4_attn_kernel: its time is the codes'
+//     conversion, which an item has once whatever its rows, and products of rows
+//     that are not there: 256 x 8 rows of 4,096 tokens (4 heads of 128) 101 us,
+//     as items of 16 143.
+//   * kv4_attn_tc_kernel converts once for 128 rows and more, but through
+//     shared memory, and an item's start and end are long.  Against two or three
+//     items of 16 rows (us, 64 sequences of 4,096 tokens, 4 heads):
+//         d 64:  16 rows 34 and 82, 24 rows 53 and 83, 48 rows 75 and 84
+//         d 128: 16 rows 48 and 86, 24 rows 79 and 87, 32 rows 80 and 87
+//     (one sequence of 131,072 tokens, 32 rows: 62 and 60); d 256, one sequence
+//     of 131,072 tokens: 16 rows 61 and 79, 24 rows 91 and 80.
+//   * Two tiles share a unit's conversion, one tile leaves more items side by
+//     side and has shorter hand-offs (us, 4 sequences of 8,192 tokens, 4 heads):
+//         d 128: 256 rows 45 and 39, 320 rows 54 and 48, 512 rows 55 and 59, 2,048 rows 142 and 176
+//         d 64:  256 rows 34 and 36, 512 rows 47 and 57
+//     d 256 has room for one only.
+// An item's start and end are counted as `extra` units: 8,192 rows of d 256 were
+// 1,054 us with 1, 776 with 10; twice as many made verify rows no faster.  A part
+// is four units at least, a page a warp (1 row of 1,000 tokens 11.0 us, 12.5
+// with 8, 18 with 20).  Where items are expected in eight parts and more, four
+// groups of threads join them (1 row of 16,000 tokens 19 us, 32 with one group),
+// elsewhere one (nine ragged prompts 161 us, 176 with four).
 AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
 {
     AttnPlan a{};
-    // packed rows of a sequence, on average where they are uneven
+    // (a sequence's, on average where they are uneven)
     const long long packed = (1LL * R * G + B - 1) / B;
-    a.eights = packed <= 8 ? 1 : packed <= KA_MAX_ROWS ? 2 : 0;
-    a.tiles = a.eights ? 0 : d == 256 || packed <= KT_ROWS ? 1 : 2;
+    a.eights = packed <= 8 ? 1 : packed <= (d == 64 ? 48 : d == 128 ? 32 : 16) ? 2 : 0;
+    a.tiles = a.eights ? 0 : d == 256 || packed <= (d == 64 ? 1 : 3) * KT_ROWS ? 1 : 2;
     a.tile = a.tiles ? a.tiles * KT_ROWS : 8 * a.eights;
     a.unit = a.tiles ? KT_UNIT : KV_PAGE;
     a.extra = a.tiles ? 10 : 4;
-    a.least = KA_WARPS;
+    a.least = 4;
     const int blocks = a.tiles ? 1 : d == 64 ? attn_blocks<64>(a.eights) : d == 128 ? attn_blocks<128>(a.eights) : attn_blocks<256>(a.eights);
     // (items, and their units, at most)
     const long long items = Hk * ((1LL * R * G + a.tile - 1) / a.tile + B);

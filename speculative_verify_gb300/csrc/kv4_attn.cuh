@@ -28,7 +28,6 @@
 namespace sv {
 
 constexpr int KA_WARPS = 4;
-constexpr int KA_MAX_ROWS = 16;                 // packed rows of an item at most
 constexpr float KA_SLACK = 8.f;                 // log2 of the largest probability
 
 template <int D, int NQ>

@@ -285,15 +285,16 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 const int pages = it.seq.before < 0 ? 0 : min(last / KV_PAGE + 1, p.kv.max_pages);
                 // (a unit at the window's start, or at the sinks' end, may hold a page that no row sees: it may be gone)
                 const int low = p.window > 0 ? max(0, it.seq.before + kv_token(p, it.tile * p.tile) - p.window + 1) : 0;
-                const int low_page = low / KV_PAGE, sink_pages = (min(p.sinks, low) + KV_PAGE - 1) / KV_PAGE;
-                auto seen = [&](int i) { return i < pages && (i >= low_page || i < sink_pages); };
+                const int sink_pages = (min(p.sinks, low) + KV_PAGE - 1) / KV_PAGE;
+                const unsigned gone = static_cast<unsigned>(max(0, low / KV_PAGE - sink_pages));
+                auto seen = [&](int i) { return i < pages && static_cast<unsigned>(i - sink_pages) >= gone; };
                 // the unit of step j, and whether it is of values
                 auto unit = [&](int j) { return ring ? min(j + 1, n - 1) : max(j - 1, 0); };
                 auto page_at = [&](int j) { return it.span.at(part.unit + unit(j)) * (KT_UNIT / KV_PAGE) + sub; };
                 int at = page_at(0), id = seen(at) ? table[at] : -1;
                 // and of the keys' lanes, the whole page of some units ahead on its way to L2: the ring is too short for
                 // a copy from HBM
-                constexpr int AHEAD = 8;
+                constexpr int AHEAD = 5;
                 auto far = [&](int j) { return ring && j + AHEAD < n ? it.span.at(part.unit + j + AHEAD) * (KT_UNIT / KV_PAGE) + sub : pages; };
                 int at_far = far(0), id_far = at_far < pages ? table[at_far] : -1;
 #pragma unroll 1
