@@ -22,6 +22,15 @@
 // Roles: the first 8 warps queries, softmax, O and outputs (a thread a row with
 // two tiles, two with one); then codes to fp16; products; copies (bulk copies
 // of the pages' codes and scales).
+//
+// d 256 is bound by shared memory: a unit's keys and values are 64 KB of fp16,
+// written once and read once by the products, 1,300 of the 1,600 cycles that a
+// unit takes; d 128 with two tiles by the hand-offs between softmax and
+// products.  8,192 rows of 24 query heads (4 of 256) from nothing take 745 us,
+// 1.1 PFLOP/s; 2,048 rows of 32 (8 of 128) in a window of 4,096 179 us, 0.78;
+// nine ragged prompts after 500 tokens each (4,817 rows, same heads) 161 us.
+// Verify rows, of which a tile has few: 1 x 4 rows of 131,072 tokens (24 heads
+// over 4 of 256) 80 us, 4 x 8 rows of 16,384 44 us.
 #pragma once
 
 #include "kv4_attn.cuh"

@@ -4,18 +4,18 @@
 // Query rows are packed: row r of a sequence and key/value head is token
 // r / G, query head r % G of the head's G.  An item is a tile of packed rows of
 // one head; its units are the pages, or pairs of them, that some row of the
-// tile sees (those of the first tokens, then those of the window).  The items of head 0, then
-// head 1 and so on make one line of units, cut into equal parts, one for a
-// thread block: uneven sequences and triangles of prompts cost no balance, and
-// one long sequence is spread over the whole GPU.  An item's start and end cost
+// tile sees (those of the first tokens, then those of the window).  The items
+// of head 0, then head 1 and so on make one line of units, cut into equal parts,
+// one for a thread block: uneven sequences and triangles of prompts cost no
+// balance, and one long sequence is spread over the whole GPU.  An item's start and end cost
 // as much as some units (`extra`): it is that much longer on the line, and a part
 // that ends there leaves it to the next.
 //
 // A block whose part holds an item whole writes its outputs; of an item that
 // goes on into other parts each block leaves its sums, unnormalised, with
 // their maximum: the block where the item starts in its slot 1, the others in
-// their slot 0.  kv4_join_kernel adds them in the parts' order, so results are
-// the same every time.  Nothing has to be cleared first and no atomic is
+// their slot 0.  kv4_join_kernel adds them in an order that is fixed, so results
+// are the same every time.  Nothing has to be cleared first and no atomic is
 // involved: calls with workspaces of their own may overlap, in graphs too.
 #pragma once
 

@@ -13,7 +13,10 @@
 //
 // The rotation is fp32 and rounded once to bf16.  Each value is read and
 // written once, 16 bytes at a time; a thread block computes its rows' angles
-// once for all their heads.
+// once for all their heads.  Bound by HBM: 8,192 rows of 32 + 8 heads of 128
+// with three axes take 32.7 us, 5.1 TB/s; several items in flight in a thread
+// (33.7 to 42 us), and blocks of one or two rows (40 to 42), were slower.  One
+// row is at its launch (2.0 us in a graph).
 #pragma once
 
 #include <cuda_bf16.h>
