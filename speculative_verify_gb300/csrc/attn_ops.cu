@@ -284,7 +284,7 @@ int rotary_embed(const sv_bf16 *q, long long ldq, int Hq, const sv_bf16 *k, long
     if (rows < 2 * dev.sms) p.heads = std::max(1, RO_THREADS / items);
     const dim3 grid(static_cast<unsigned>((rows + p.block_rows - 1) / p.block_rows),
                     static_cast<unsigned>((Hq + Hk + p.heads - 1) / p.heads));
-    const size_t smem = static_cast<size_t>(p.block_rows) * (rot / 2) * sizeof(float2);
+    const size_t smem = static_cast<size_t>(p.block_rows) * ro_place(rot / 2) * sizeof(float2);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     return flags & SV_ROTARY_PAIRED ? launch(rotary_kernel<true>, grid, RO_THREADS, smem, cs, p)
                                     : launch(rotary_kernel<false>, grid, RO_THREADS, smem, cs, p);

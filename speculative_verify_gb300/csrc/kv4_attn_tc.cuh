@@ -24,8 +24,8 @@
 // of the pages' codes and scales).
 //
 // d 256 is bound by shared memory: a unit's keys and values are 64 KB of fp16,
-// written once and read once by the products, 1,300 of the 1,600 cycles that a
-// unit takes; d 128 with two tiles by the hand-offs between softmax and
+// written once and read once by the products, and with the codes they take 70 %
+// of its cycles; d 128 with two tiles by the hand-offs between softmax and
 // products.  8,192 rows of 24 query heads (4 of 256) from nothing take 745 us,
 // 1.1 PFLOP/s; 2,048 rows of 32 (8 of 128) in a window of 4,096 179 us, 0.78;
 // nine ragged prompts after 500 tokens each (4,817 rows, same heads) 161 us.

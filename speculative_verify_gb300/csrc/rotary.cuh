@@ -14,7 +14,7 @@
 // The rotation is fp32 and rounded once to bf16.  Each value is read and
 // written once, 16 bytes at a time; a thread block computes its rows' angles
 // once for all their heads.  Bound by HBM: 8,192 rows of 32 + 8 heads of 128
-// with three axes take 32.7 us, 5.1 TB/s; several items in flight in a thread
+// with three axes take 29.4 us, 5.7 TB/s; several items in flight in a thread
 // (33.7 to 42 us), and blocks of one or two rows (40 to 42), were slower.  One
 // row is at its launch (2.0 us in a graph).
 #pragma once
@@ -45,6 +45,10 @@ struct RotaryParams {
     float factor;
     int *err;
 };
+
+// Places of a row's angles in shared memory, eight and two to spare: threads
+// that read eight each, 80 bytes apart, meet no bank conflict.
+__host__ __device__ constexpr int ro_place(int j) { return (j >> 3) * 10 + (j & 7); }
 
 // cos and sin of `pos` steps of frequency f, times the factor.
 __device__ __forceinline__ float2 ro_turn(float f, int pos, float factor)
@@ -79,8 +83,8 @@ __device__ __forceinline__ float ro_hi(uint32_t w) { return __uint_as_float(w & 
 template <bool PAIRED>
 __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const RotaryParams p)
 {
-    extern __shared__ float2 ro_cs[];           // [block_rows][rot / 2]
-    const int half = p.rot / 2, row0 = static_cast<int>(blockIdx.x) * p.block_rows;
+    extern __shared__ __align__(16) float2 ro_cs[];     // [block_rows][ro_place(rot / 2)]
+    const int half = p.rot / 2, wide = ro_place(half), row0 = static_cast<int>(blockIdx.x) * p.block_rows;
     const int rows = min(p.block_rows, p.rows - row0);
     pdl_launch_dependents();
     pdl_wait_prior();
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const RotaryParams p
             atomicOr(p.err, RO_ERR_AXIS);
             axis = 0;
         }
-        ro_cs[i] = ro_turn(p.inv_freq[j], p.positions[axis * p.ldp + row0 + r], p.factor);
+        ro_cs[r * wide + ro_place(j)] = ro_turn(p.inv_freq[j], p.positions[axis * p.ldp + row0 + r], p.factor);
     }
     __syncthreads();
     // a thread's item: 8 pairs of a head (two 16-byte pieces), or 16 bytes past the rotated part
@@ -114,7 +118,13 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const RotaryParams p
         const uint4 a = *reinterpret_cast<const uint4 *>(in + a0), b = *reinterpret_cast<const uint4 *>(in + b0);
         const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
         uint32_t x[4], y[4];
-        const float2 *cs = ro_cs + r * half + 8 * it;
+        float2 cs[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 two = reinterpret_cast<const float4 *>(ro_cs + r * wide + 10 * it)[j];
+            cs[2 * j] = make_float2(two.x, two.y);
+            cs[2 * j + 1] = make_float2(two.z, two.w);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float s0, s1, t0, t1;
