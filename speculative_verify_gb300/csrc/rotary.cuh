@@ -15,8 +15,8 @@
 // written once, 16 bytes at a time; a thread block computes its rows' angles
 // once for all their heads.  Bound by HBM: 8,192 rows of 32 + 8 heads of 128
 // with three axes take 29.4 us, 5.7 TB/s; several items in flight in a thread
-// (33.7 to 42 us), and blocks of one or two rows (40 to 42), were slower.  One
-// row is at its launch (2.0 us in a graph).
+// and blocks of 512 threads (30.9 us) or 128 (34.5) were slower.  One row is at
+// its launch (2.0 us in a graph).
 #pragma once
 
 #include <cuda_bf16.h>
