@@ -307,6 +307,29 @@ def test_many_sequences(sv):
     run(sv, 2, [(11 * b) % 90 for b in range(70)], [b % 5 for b in range(70)], 8, 2, 64, ragged=True)
 
 
+def test_more_sequences_than_the_warps_share_out(sv):
+    """Beyond 64 groups of 32 sequences: rows everywhere, and a few among thousands that have none."""
+    run(sv, 3, [(7 * b) % 70 for b in range(2100)], [1] * 2100, 2, 1, 64)
+    rows = [0] * 2300
+    for b, n in ((0, 3), (31, 1), (1000, 40), (2047, 2), (2048, 17), (2299, 5)):
+        rows[b] = n
+    run(sv, 4, [(13 * b) % 200 - 1 for b in range(2300)], rows, 4, 2, 128, ragged=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("many,long,G", [(40, 700, 4), (60, 300, 2), (3, 2000, 1)])
+def test_decode_rows_beside_a_prompt(sv, d, many, long, G):
+    """Single rows and a long prompt in a call, whichever kernel their average picks; some sequences inactive."""
+    lens = [(97 * b) % 900 - (b % 7 == 3) * 1000 for b in range(many)]
+    run(sv, 5, lens[:many // 2] + [130] + lens[many // 2:], [1] * (many // 2) + [long] + [1] * (many - many // 2), 2 * G, 2, d,
+        ragged=True)
+
+
+def test_nothing_active(sv):
+    q, cache, table, o = run(sv, 6, [-1, -5, -1], [4] * 3, 8, 2, 128)
+    assert not o.any()
+
+
 def test_scales(sv):
     """A scale of the scores, and scales of the cache that are no powers of two."""
     run(sv, 3, [100, 700], [3, 3], 6, 2, 128, scale=0.3, g=(0.05, 3.7), peak=1.0)
@@ -358,6 +381,21 @@ def test_not_a_number_stays_with_rows_that_see_it(sv, d, T):
         p[(p & 0x7F) == 0x7F] = 0x30
     r = ref.attention(clean, cache, table, ints(lens), window=window, sinks=4)
     ref.check_attention(torch.where(want[..., None], 0, o), [torch.where(want[..., None], 0, x) for x in r])
+
+
+@pytest.mark.parametrize("d,T", [(64, 3), (128, 3), (256, 3), (64, 150), (128, 150), (256, 150)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_queries_that_are_no_numbers(sv, d, T, bad):
+    """A row and head with a NaN or an infinity gives NaNs, the others what they give without it."""
+    gen = rng_of(18)
+    cache, table = ref.filled(gen, 12, 1, d), ref.shuffled(gen, [12])
+    q = randn(gen, 1, T, 4, d).bfloat16()
+    want = ref.attention(q, cache, table, ints([200]))
+    q[0, T // 2, 1, 5] = q[0, T // 2, 1, d - 1] = bad
+    o = sv.kv4_attention(q, cache, table, ints([200]))
+    assert bool(o[0, T // 2, 1].isnan().all()) and int(o.isnan().sum()) == d
+    o[0, T // 2, 1] = want[0][0, T // 2, 1].bfloat16()
+    ref.check_attention(o, want)
 
 
 def test_large_values(sv):
