@@ -1,6 +1,6 @@
 // kv4_attn_tc.cuh -- attention of many query rows over the 4-bit cache on the
-// 5th-generation tensor cores: prompts, and verify rows with more packed rows
-// than one mma.sync tile.
+// 5th-generation tensor cores: prompts, and verify rows with many packed rows
+// (attn_plan in attn_ops.cu has the rule).
 //
 // An item (kv4_plan.cuh) is NT tiles of 128 packed rows, a unit 64 tokens.  A
 // unit's keys and its values become fp16 in shared memory once for all tiles,
@@ -10,7 +10,7 @@
 // O += P V takes P from tensor memory and V across.  So the tensor cores form
 // the next unit's scores during a softmax.
 //
-// NT = 2 (d 64 and 128, more than 128 rows): O and two buffers of S for each
+// NT = 2 (d 64 and 128, many rows): O and two buffers of S for each
 // tile fill the tensor memory, and the queries stay in shared memory.  NT = 1
 // (fewer rows, or d 256): the queries are in tensor memory too -- from shared
 // memory they would take as much of its bandwidth as an M128 N64 product has.
