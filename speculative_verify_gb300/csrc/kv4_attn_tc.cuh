@@ -547,7 +547,10 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
                         sts128(place(r), make_uint4(w[0], w[1], w[2], w[3]));
-                        if (piece == 0) factor[tile * KT_ROWS + r] = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                        // (not zero, which times the -inf of a masked score were NaN: below the smallest normal number the
+                        // scores, at most 2^34 before it, are all nothing to the softmax)
+                        if (piece == 0)
+                            factor[tile * KT_ROWS + r] = fmaxf(fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 0x1p-126f);
                     }
                 }
             }
