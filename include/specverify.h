@@ -668,7 +668,8 @@ int kv4_gather(sv_bf16 *k, long long ldk, sv_bf16 *v, long long ldv, int R, cons
  * p - j < window or j < sinks.  A row that sees no token gives zeros.  q, o
  * [R][Hq][d] bf16, rows ldq and ldo apart (multiples of 8, 16-byte aligned; o
  * must not overlap q).  Scores, their softmax and sums are fp32; keys and values are
- * exact in the products, the probabilities in them fp16.  A token with a NaN
+ * exact in the products, the probabilities in them fp16 (each off by 2^-11 of
+ * itself at most, or by 2^-32 of the row's largest where that is more).  A token with a NaN
  * scale among its K scales makes the rows that see it NaN, others not; NaN V
  * scales alone count as 448.
  * `ws` is device memory of at least kv4_attention_bytes (0 when the sizes are

@@ -17,9 +17,13 @@
 //     operand; an A row is a dimension, and a pair of tokens' values are put
 //     together by byte permutation.  Thread row g has dimensions g d / 8 .., so
 //     that it ends with neighbouring ones.
-//   * Sums and the softmax are fp32, probabilities fp16 (off by 2^-11 at
-//     most of each, independent, where 8 bits of bf16 would show in the outputs).  They are taken relative to a maximum that is only moved
-//     when a score passes it by 2^8, so most pages rescale nothing.
+//   * Sums and the softmax are fp32, probabilities fp16 (where 8 bits of bf16
+//     would show in the outputs).  They are taken relative to 2^-7 of a maximum
+//     that is only moved when a score passes it by 2^8, so most pages rescale
+//     nothing and fp16's range is used up to 2^15: each is off by 2^-11 of itself
+//     at most, or by 2^-32 of the largest where that is more.  Relative to the
+//     maximum it is 2^-25, and their sum has the unrounded ones: of 131,072 tokens
+//     at 2^-25.2 of the largest, 0.3 % of the weight, nothing reached the outputs.
 //
 // Bound by instructions, not by HBM: about 680 a warp and page of d 128, most
 // of them conversions and the products and permutations that go with them.
@@ -35,7 +39,8 @@
 namespace sv {
 
 constexpr int KA_WARPS = 4;
-constexpr float KA_SLACK = 8.f;                 // log2 of the largest probability
+constexpr float KA_LIFT = 7.f;                  // log2 of the largest probability when the reference moves
+constexpr float KA_TOP = 15.f;                  // and of the largest before it moves
 
 template <int D, int NQ>
 struct KaShape {
@@ -63,6 +68,15 @@ __device__ __forceinline__ float ka_exp2(float x)
 {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two probabilities as an fp16 pair.  (Scores past 2^23, whose fp32 steps are
+// as wide as the slack, may pass fp16's range: its largest number then.)
+__device__ __forceinline__ uint32_t ka_pack(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
@@ -100,7 +114,7 @@ struct KaWarp {
     using S = KaShape<D, NQ>;
     static constexpr int MT = D / 16;
     float o[MT][NQ][4];                         // dimensions 2 i, 2 i + 1 of the thread's: rows 2c, 2c + 1 of the first, of the second
-    float m[NQ][2], l[NQ][2];                   // rows 2c, 2c + 1: reference maximum, this thread's sum
+    float m[NQ][2], l[NQ][2];                   // rows 2c, 2c + 1: reference, KA_LIFT below a maximum; this thread's sum
 
     __device__ __forceinline__ void clear()
     {
@@ -185,7 +199,7 @@ struct KaWarp {
                         top[q][r] = fmaxf(top[q][r], x);
                     }
                 // (with -inf before: 0 scores further are enough)
-                grow |= top[q][r] > (m[q][r] == -INFINITY ? -INFINITY : m[q][r] + KA_SLACK);
+                grow |= top[q][r] > (m[q][r] == -INFINITY ? -INFINITY : m[q][r] + KA_TOP);
             }
         if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -197,7 +211,7 @@ struct KaWarp {
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    const float to = fmaxf(m[q][r], x);
+                    const float to = fmaxf(m[q][r], x - KA_LIFT);
                     f[r] = to == m[q][r] ? 1.f : m[q][r] == -INFINITY ? 0.f : ka_exp2(m[q][r] - to);   // (0: nothing was added before)
                     m[q][r] = to;
                     l[q][r] *= f[r];
@@ -222,7 +236,7 @@ struct KaWarp {
                     const float x = ka_exp2(s[j][q][2 * h] - ref[0]), y = ka_exp2(s[j][q][2 * h + 1] - ref[1]);
                     l[q][0] += x;
                     l[q][1] += y;
-                    p[j][q][h] = ka_transpose(pack_f16x2(x, y));
+                    p[j][q][h] = ka_transpose(ka_pack(x, y));
                 }
         }
         const uint8_t *vc = st + kv_v_codes(D) + g * (S::VN / 2), *vs = st + kv_v_scales(D) + g * S::VN / KV_GROUP;

@@ -15,9 +15,9 @@
 // (fewer rows, or d 256): the queries are in tensor memory too -- from shared
 // memory they would take as much of its bandwidth as an M128 N64 product has.
 //
-// The softmax is that of kv4_attn.cuh: fp32, relative to a maximum that moves
-// only when a score passes it by 2^8, when O is rescaled in tensor memory by
-// the rows' own threads.
+// The softmax is that of kv4_attn.cuh: fp32, relative to 2^-7 of a maximum that
+// moves only when a score passes it by 2^8, when O is rescaled in tensor memory
+// by the rows' own threads.
 //
 // Roles: the first 8 warps queries, softmax, O and outputs (a thread a row with
 // two tiles, two with one); then codes to fp16; products; copies (bulk copies
@@ -188,7 +188,7 @@ __device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 
         a = ka_exp2(a);
         b = ka_exp2(b);
         sum = kt_add_x2(sum, pack_x2(a, b));
-        p[i] = pack_f16x2(a, b);
+        p[i] = ka_pack(a, b);
     }
 }
 
@@ -617,9 +617,9 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                     top = fmaxf(top, of[(group ^ 1) * KT_ROWS]);
                 }
                 if (top != -INFINITY) top *= scale;
-                const bool grow = top > m + KA_SLACK || (m == -INFINITY && top > m);
+                const bool grow = top > m + KA_TOP || (m == -INFINITY && top > m);
                 if (__any_sync(0xFFFFFFFFu, grow)) {
-                    const float to_m = fmaxf(m, top), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
+                    const float to_m = fmaxf(m, top - KA_LIFT), f = to_m == m ? 1.f : m == -INFINITY ? 0.f : ka_exp2(m - to_m);
                     m = to_m;
                     l2 = mul_x2(l2, pack_x2(f, f));
                     if (i > 0) {
