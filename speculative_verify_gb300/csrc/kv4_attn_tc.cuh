@@ -158,12 +158,12 @@ struct KtSight {
     }
 };
 
-// Scores that are not seen to -inf.
-__device__ __forceinline__ void kt_mask(uint32_t (&s)[32], unsigned seen)
+// Scores times a factor, those that are not seen to -inf.
+__device__ __forceinline__ void kt_mask(uint32_t (&s)[32], unsigned seen, float times)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        if (!(seen & (1u << i))) s[i] = 0xFF800000u;
+        s[i] = seen & (1u << i) ? __float_as_uint(__uint_as_float(s[i]) * times) : 0xFF800000u;
 }
 
 __device__ __forceinline__ float kt_max(const uint32_t (&s)[32], float top)
@@ -586,7 +586,14 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
             const int from = p.window > 0 ? it.seq.before + t1 - p.window + 1 : 0;
             // (a warp's rows' factors come from other warps, which also arrive at this barrier)
             together();
-            const float scale = factor[tile * KT_ROWS + row];
+            float scale = factor[tile * KT_ROWS + row], times = 1.f;
+            // Scores that may pass 2^23 (queries are below 2^15 and keys 2,688 at most) are multiplied where they are masked,
+            // not in the softmax's fma: there the maximum, a rounded product, and fma's exact one may be powers of two apart.
+            const bool round = __any_sync(0xFFFFFFFFu, in && scale * (0x1p15f * 2688.f * D) > 0x1p23f);
+            if (round) {
+                times = scale;
+                scale = 1.f;
+            }
             float m = -INFINITY;
             f32x2 l2 = pack_x2(0.f, 0.f);
             for (int i = 0; active && i < n; ++i, ++run) {
@@ -601,11 +608,11 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 for (int j = 0; j < CHUNKS; ++j) tmem_ld32(at + 32 * j, x[j]);
                 const int first = it.span.at(part.unit + i) * KT_UNIT;
                 const unsigned gone = missing[2 * ((units + i) & 15)] | missing[2 * ((units + i) & 15) + 1] << 1;
-                const bool all = !gone && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
+                const bool all = !gone && !round && first + KT_UNIT - 1 <= to && (first >= from || first + KT_UNIT <= sight.sinks);
                 tmem_wait_ld();
                 if (!all) {
 #pragma unroll
-                    for (int j = 0; j < CHUNKS; ++j) kt_mask(x[j], sight(first + 32 * (group + j), gone >> (group + j)));
+                    for (int j = 0; j < CHUNKS; ++j) kt_mask(x[j], sight(first + 32 * (group + j), gone >> (group + j)), times);
                 }
                 float top = -INFINITY;
 #pragma unroll

@@ -72,3 +72,18 @@ def test_long_tail(sv, d, T, G, many, n):  # noqa: F811
     B = 1 if not many else 800 if T * G <= 16 else 160
     o, want = tail(sv, d, T, G, n, B)
     check(o, want, n)
+
+
+@pytest.mark.parametrize("d,T,G", INSTANCES)
+@pytest.mark.parametrize("scale", [1e4, 3e5, 1e7, -1e8, 1e12])
+def test_scores_that_fp32_tells_apart_by_more_than_the_slack(sv, d, T, G, scale):  # noqa: F811
+    """Which token wins is then a matter of rounding, but the output lies among the values: off by the roundings of
+    `check`, and by fp16's largest number where a weight is up to 2^16 (2^-11)."""
+    gen = rng_of(d)
+    cache, table = ref.filled(gen, 12, 1, d), ref.shuffled(gen, [12])
+    q = (20 * randn(gen, 1, T, G, d)).bfloat16()
+    o = sv.kv4_attention(q, cache, table, ints([384 - T]), scale=scale)
+    assert sv.last_device_error() == 0
+    _, v = ref.tokens(cache, table[0], 384)
+    most = v[:, 0].abs().amax(0) * (1 + 2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -12)
+    assert bool((o.double().abs() <= most).all())
