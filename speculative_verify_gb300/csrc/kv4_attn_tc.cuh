@@ -177,8 +177,8 @@ __device__ __forceinline__ float kt_max(const uint32_t (&s)[32], float top)
     return fmaxf(a, b);
 }
 
-// Probabilities 2^(scale s - ref) of 32 scores as fp16 pairs; their sum is added.
-__device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 scale, f32x2 minus, f32x2 &sum, uint32_t (&p)[16])
+// Probabilities 2^(scale s - ref) of 32 scores as fp16 pairs; their sums are added, or put (`first`).
+__device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 scale, f32x2 minus, bool first, f32x2 &sum, uint32_t (&p)[16])
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -187,7 +187,7 @@ __device__ __forceinline__ void kt_probabilities(const uint32_t (&s)[32], f32x2 
         asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
         a = ka_exp2(a);
         b = ka_exp2(b);
-        sum = kt_add_x2(sum, pack_x2(a, b));
+        sum = first && i == 0 ? pack_x2(a, b) : kt_add_x2(sum, pack_x2(a, b));
         p[i] = ka_pack(a, b);
     }
 }
@@ -638,12 +638,14 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const f32x2 scale2 = pack_x2(scale, scale), minus = pack_x2(-ref, -ref);
+                f32x2 unit2;                    // (the unit's alone first: one by one, small ones would leave a large sum as it is)
 #pragma unroll
                 for (int j = 0; j < CHUNKS; ++j) {
                     uint32_t pr[16];
-                    kt_probabilities(x[j], scale2, minus, l2, pr);
+                    kt_probabilities(x[j], scale2, minus, j == 0, unit2, pr);
                     tmem_st(at + 16 * j, pr);   // (of this thread's columns, which it has read)
                 }
+                l2 = kt_add_x2(l2, unit2);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();

@@ -13,11 +13,11 @@ from test_kv4_gpu import ints, randn, rng_of, sv  # noqa: E402,F401
 BELOW = [17.0, 24.5, 25.25, 28.0]               # log2 of the first token's weight over one of the others'
 
 
-def tail(sv, d, T, G, n, B):  # noqa: F811
+def tail(sv, d, T, G, n, B, spread=0.004, below=BELOW, values=range(1, 8)):  # noqa: F811
     """o of T rows of B sequences of n tokens, the last row's position n - 1, and the same from the definition.
 
     The first page holds the token that outweighs the others; all later pages of all sequences are one page, so that
-    the sums over them have a closed form.  Query head h is BELOW[h % 4] above the others' mean."""
+    the sums over them have a closed form.  Query head h is below[h % 4] above the others' mean."""
     gen = rng_of(d + T)
     pages = -(-n // 32)
     cache = torch.zeros(2, 1, 36 * d, dtype=torch.uint8, device="cuda")
@@ -28,11 +28,12 @@ def tail(sv, d, T, G, n, B):  # noqa: F811
     # has zeros in the even dimensions, the others are positive
     kc[..., 0] = torch.randint(0, 16, kc.shape[:-1], device="cuda", generator=gen).to(torch.uint8) << 4
     kc[0, 0, 0, 0] = 6                          # 4.0 and 0
-    vc[:] = torch.randint(1, 8, vc.shape, device="cuda", generator=gen).to(torch.uint8) * 17
+    some = torch.tensor(list(values), dtype=torch.uint8, device="cuda")
+    vc[:] = some[torch.randint(0, len(values), vc.shape, device="cuda", generator=gen)] * 17
     vc[0, 0, 0] = 2 << 4
     q = torch.zeros(B, T, G, d, device="cuda")
-    q[..., 0] = torch.tensor(BELOW, device="cuda").repeat(-(-G // 4))[:G] / 32
-    q[..., 1] = 0.004 * randn(gen, T, G)        # (the same rows in every sequence)
+    q[..., 0] = torch.tensor(below, device="cuda").repeat(-(-G // 4))[:G] / 32
+    q[..., 1] = spread * randn(gen, T, G)        # (the same rows in every sequence)
     q = q.bfloat16()
     scale = 8 * math.log(2)                     # 4 * BELOW / 32 * scale = BELOW ln 2
     table = torch.ones(B, pages, dtype=torch.int32, device="cuda")
@@ -87,3 +88,15 @@ def test_scores_that_fp32_tells_apart_by_more_than_the_slack(sv, d, T, G, scale)
     _, v = ref.tokens(cache, table[0], 384)
     most = v[:, 0].abs().amax(0) * (1 + 2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -12)
     assert bool((o.double().abs() <= most).all())
+
+
+@pytest.mark.parametrize("d,T,G", INSTANCES)
+def test_sums_of_weights(sv, d, T, G):  # noqa: F811
+    """The others at 2^-25 of the first token, each, their values 1 and 2: a sum of products of an even dimension is a
+    multiple of 2^-18 below 2^24 of them, and exact.  What is left is the output's rounding, 2^-8; the
+    score's, 2^-12; and the sum of the weights, each addition off by 2^-24 of the total: a unit's 64 weights at most and
+    n / 64 units in kv4_attn_tc_kernel, a thread's n / 32 weights in kv4_attn_kernel."""
+    n = 1 << 22
+    o, want = tail(sv, d, T, G, n, 800 if T * G <= 16 else 160, 0.0, [25.0] * 4, [2, 4])
+    err = ((o.double() - want) / want)[..., ::2].abs()
+    assert float(err.max()) <= 2.0 ** -8 + 2.0 ** -12 + (64 + n // 32) * 2.0 ** -24, float(err.max())
