@@ -53,6 +53,11 @@ __device__ __forceinline__ int kv_token(const KvAttnParams &p, int r)
     return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(r)) * p.g_mul >> p.g_shift);
 }
 
+// The largest position of a sequence's first row: with 2^29 rows at most no
+// position passes 31 bits, and a window of 2^30 at most has left the 2^29 tokens
+// that a table may have, as it has for any position beyond.
+constexpr int KP_MAX_BEFORE = (1 << 30) + (1 << 29) - 1;
+
 // A sequence's rows, and the position of its first one (negative: inactive).
 struct KvSeq {
     int first, n, before;
@@ -64,7 +69,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b)
     int end;
     p.rows.range(b, s.first, end);
     s.n = end - s.first;
-    s.before = min(p.rows.lens[b], p.kv.max_pages * KV_PAGE);
+    s.before = min(p.rows.lens[b], KP_MAX_BEFORE);
     return s;
 }
 
