@@ -91,12 +91,22 @@ constexpr int KV_MAX_PAGES = 1 << 24;           // of a sequence: positions stay
 
 bool fine_scale(float s) { return std::isfinite(s) && s >= 1e-30f && s <= 1e30f; }
 
+bool fine_sizes(const sv_kv4_cache *c)
+{
+    return (c->d == 64 || c->d == 128 || c->d == 256) && c->Hk >= 1 && c->Hk <= 65535 && c->n_pages >= 0 && c->max_pages >= 0 &&
+           c->max_pages <= KV_MAX_PAGES;
+}
+
+bool fine_rows(int R, int B, bool ragged)
+{
+    if (R < 0 || R > (1 << 29) || B < 0 || B > (1 << 20)) return false;
+    return ragged || (B ? R % B : R) == 0;      // (as many rows a sequence)
+}
+
 int check_cache(const sv_kv4_cache *c, int B)
 {
     if (!c) return SV_ERR_NULL;
-    if ((c->d != 64 && c->d != 128 && c->d != 256) || c->Hk < 1 || c->Hk > 65535) return SV_ERR_SHAPE;
-    if (c->n_pages < 0 || c->max_pages < 0 || c->max_pages > KV_MAX_PAGES) return SV_ERR_SHAPE;
-    if (B > 0 && c->ldt < c->max_pages) return SV_ERR_SHAPE;
+    if (!fine_sizes(c) || (B > 0 && c->ldt < c->max_pages)) return SV_ERR_SHAPE;
     if (!fine_scale(c->k_scale) || !fine_scale(c->v_scale)) return SV_ERR_SHAPE;
     if ((c->n_pages > 0 && !c->pages) || (B > 0 && c->max_pages > 0 && !c->page_table)) return SV_ERR_NULL;
     if (!aligned_to(c->pages, 16) || !aligned_to(c->page_table, 4)) return SV_ERR_ALIGN;
@@ -105,8 +115,7 @@ int check_cache(const sv_kv4_cache *c, int B)
 
 int check_kv_rows(int R, const int32_t *cu, const int32_t *lens, int B)
 {
-    if (R < 0 || R > (1 << 29) || B < 0 || B > (1 << 20)) return SV_ERR_SHAPE;
-    if (!cu && (B ? R % B : R)) return SV_ERR_SHAPE;     // (as many rows a sequence)
+    if (!fine_rows(R, B, cu)) return SV_ERR_SHAPE;
     if (B > 0 && !lens) return SV_ERR_NULL;
     if (!aligned_to(cu, 4) || !aligned_to(lens, 4)) return SV_ERR_ALIGN;
     return SV_OK;
@@ -312,9 +321,7 @@ int kv4_gather(sv_bf16 *k, long long ldk, sv_bf16 *v, long long ldv, int R, cons
 size_t kv4_attention_bytes(int R, int B, int ragged, int Hq, const sv_kv4_cache *cache)
 {
     using namespace sv;
-    if (!cache || (cache->d != 64 && cache->d != 128 && cache->d != 256) || cache->Hk < 1 || R < 0 || B < 0) return 0;
-    if (check_attention(R, B, Hq, cache) != SV_OK) return 0;
-    if (cache->max_pages < 0 || cache->max_pages > KV_MAX_PAGES || (!ragged && (B ? R % B : R))) return 0;
+    if (!cache || !fine_sizes(cache) || !fine_rows(R, B, ragged) || check_attention(R, B, Hq, cache) != SV_OK) return 0;
     if (R == 0 || B == 0) return 16;
     return AttnSpace(attn_plan(R, B, Hq / cache->Hk, cache->d, cache->Hk, cache->max_pages), cache->d).bytes;
 }
