@@ -673,8 +673,8 @@ int kv4_gather(sv_bf16 *k, long long ldk, sv_bf16 *v, long long ldv, int R, cons
  * scale among its K scales makes the rows that see it NaN, others not; NaN V
  * scales alone count as 448.
  * `ws` is device memory of at least kv4_attention_bytes (0 when the sizes are
- * invalid; `ragged`: cu_seqlens is given), 16-byte aligned, free until the
- * call has run; calls that may overlap need one each.  R * (Hq / Hk) <= 2^29,
+ * invalid; `ragged`: cu_seqlens is given; more rows do not always need more),
+ * 16-byte aligned, free until the call has run; calls that may overlap need one each.  R * (Hq / Hk) <= 2^29,
  * R * Hq <= 2^33, scale * k_scale within fp32's range.  Pages that no row of the
  * call sees (before all windows) may be gone from the table.
  * Results do not depend on timing.  Decreasing cu_seqlens that claim more

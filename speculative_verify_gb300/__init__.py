@@ -15,7 +15,7 @@ import re
 from . import build as _build
 from . import layer as _layer
 from .layer import (KV4_PAGE, gated_delta_chunk, gated_delta_step, kv4_append, kv4_attention,  # noqa: F401
-                    kv4_cache, kv4_gather, rmsnorm, rmsnorm_fp8, rotary, w4a16_gate_up)
+                    kv4_attention_bytes, kv4_cache, kv4_gather, rmsnorm, rmsnorm_fp8, rotary, w4a16_gate_up)
 
 SV_OK = 0
 STATUS = {0: "SV_OK", -1: "SV_ERR_NULL", -2: "SV_ERR_SHAPE", -3: "SV_ERR_ALIGN",

@@ -205,6 +205,24 @@ def kv4_gather(cache, page_table, seq_lens, rows, cu_seqlens=None, k_scale=1.0, 
     return _ext.kv4_gather(cache, page_table, seq_lens, rows, cu_seqlens, k_scale, v_scale, k, v, stream)
 
 
+def kv4_attention_bytes(q, cache, page_table, cu_seqlens=None):
+    """Bytes of the workspace of such a kv4_attention call, from its tensors'
+    shapes alone.  More rows do not always need more: with their number the cut
+    of the work changes."""
+    import speculative_verify_gb300 as root
+    if q.dim() != (4 if cu_seqlens is None else 3) or cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("q must be [B][T][heads][d], or [R][heads][d] with cu_seqlens, cache [pages][Hk][36 d], "
+                         "page_table [B][pages]")
+    if cache.shape[2] != 36 * q.shape[-1] or (cu_seqlens is None and q.shape[0] != page_table.shape[0]):
+        raise ValueError("q must have the cache's dimensions and as many sequences as page_table")
+    c = Kv4Cache(None, None, page_table.shape[1], cache.shape[0], page_table.shape[1], cache.shape[1], q.shape[-1], 1.0, 1.0)
+    n = root.load().kv4_attention_bytes(q.shape[:-2].numel(), page_table.shape[0], cu_seqlens is not None, q.shape[-2],
+                                        ctypes.byref(c))
+    if n == 0:
+        raise ValueError("kv4_attention does not take these sizes")
+    return n
+
+
 def kv4_attention(q, cache, page_table, seq_lens, cu_seqlens=None, scale=None, window=0, sinks=0, k_scale=1.0,
                   v_scale=1.0, o=None, workspace=None, stream=None):
     """Causal attention of query rows over the 4-bit cache, which holds the
@@ -215,8 +233,11 @@ def kv4_attention(q, cache, page_table, seq_lens, cu_seqlens=None, scale=None, w
     cu_seqlens (prompts of uneven lengths); row t of sequence b sees the tokens
     up to seq_lens[b] + t, with a window only the last `window` of them and the
     first `sinks` of the sequence.  A sequence of negative length gives zeros.
-    scale defaults to d ** -0.5.  workspace: a uint8 CUDA tensor of
-    kv4_attention_bytes, else one is allocated."""
+    scale defaults to d ** -0.5.  workspace: a uint8 CUDA tensor of at least
+    kv4_attention_bytes(q, cache, page_table, cu_seqlens), that no call which may
+    overlap this one has, else one is allocated.  A call takes one kernel, by the
+    query rows of a sequence on average: single rows are better not mixed with
+    prompts of hundreds of rows in one."""
     if _ext is None:
         _load()
     return _ext.kv4_attention(q, cache, page_table, seq_lens, cu_seqlens, scale, window, sinks, k_scale, v_scale, o,

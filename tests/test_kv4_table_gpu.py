@@ -47,3 +47,27 @@ def test_sequences_longer_than_their_table(sv, d, T, G, pages, window, sinks):  
     ref.check_attention(o, want)
     nothing = want[1].sum(-1) == 0
     assert not o[nothing].any() and (sinks > 0 or window == 0 or bool(nothing.any()))
+
+
+@pytest.mark.parametrize("d,T,G", INSTANCES)
+@pytest.mark.parametrize("ragged", [False, True])
+def test_workspace_of_just_the_size(sv, d, T, G, ragged):  # noqa: F811
+    """As many bytes as asked for give the same bits, and none behind them is written; with one fewer the call is
+    refused."""
+    gen = rng_of(d + T)
+    lens = [1500, 0, 333]
+    need = [-(-(n + T) // 32) for n in lens]
+    cache, table = ref.filled(gen, sum(need), 2, d), ref.shuffled(gen, need)
+    q = randn(gen, 3, T, 2 * G, d).bfloat16()
+    cu = None
+    if ragged:
+        q, cu = q.flatten(0, 1), ints([0, T, 2 * T, 3 * T])
+    n = sv.kv4_attention_bytes(q, cache, table, cu)
+    want = sv.kv4_attention(q, cache, table, ints(lens), cu)
+    whole = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert torch.equal(sv.kv4_attention(q, cache, table, ints(lens), cu, workspace=whole[:n]), want)
+    assert bool((whole[n:] == 0xA5).all())
+    with pytest.raises(sv.SpecVerifyError):
+        sv.kv4_attention(q, cache, table, ints(lens), cu, workspace=whole[:n - 1])
+    ref.check_attention(want, ref.attention(q, cache, table, ints(lens), cu))
+    assert sv.last_device_error() == 0
