@@ -71,3 +71,29 @@ def test_workspace_of_just_the_size(sv, d, T, G, ragged):  # noqa: F811
         sv.kv4_attention(q, cache, table, ints(lens), cu, workspace=whole[:n - 1])
     ref.check_attention(want, ref.attention(q, cache, table, ints(lens), cu))
     assert sv.last_device_error() == 0
+
+
+@pytest.mark.parametrize("d,T,G", INSTANCES)
+def test_slices(sv, d, T, G):  # noqa: F811
+    """A page table and outputs that are slices of wider ones: the same bits, and nothing beside them is written."""
+    gen = rng_of(d + G)
+    lens = [700, 31, 2000]
+    need = [-(-(n + T) // 32) for n in lens]
+    cache, table = ref.filled(gen, sum(need), 2, d), ref.shuffled(gen, need)
+    wide = torch.full((3, table.shape[1] + 9), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, 4:-5] = table
+    q = randn(gen, 3, T, 2 * G + 3, d).bfloat16()[:, :, 1:-2]
+    want = sv.kv4_attention(q.contiguous(), cache, table, ints(lens))
+    ref.check_attention(want, ref.attention(q, cache, table, ints(lens)))
+    out = torch.full((3, T, 2 * G + 2, d), 7.0, device="cuda").bfloat16()
+    o = out[:, :, 1:-1]
+    assert sv.kv4_attention(q, cache, wide[:, 4:-5], ints(lens), o=o) is o
+    assert torch.equal(o, want) and bool((out[:, :, 0] == 7).all()) and bool((out[:, :, -1] == 7).all())
+    k, v = (randn(gen, 3, T, 2, d).bfloat16() for _ in range(2))
+    same = cache.clone()
+    sv.kv4_append(k, v, cache, table, ints(lens))
+    sv.kv4_append(k, v, same, wide[:, 4:-5], ints(lens))
+    assert torch.equal(cache, same)
+    for a, b in zip(sv.kv4_gather(cache, table, ints(lens), T), sv.kv4_gather(cache, wide[:, 4:-5], ints(lens), T)):
+        assert torch.equal(a, b)
+    assert sv.last_device_error() == 0
