@@ -6,10 +6,10 @@
 // Far positions: position * frequency in fp32 is off by 2^-24 of an angle of
 // up to a million radians.  A frequency is instead taken once as a fraction of
 // a turn in 64-bit fixed point (from its product with 1 / 2 pi in fp64), and
-// the position multiplies it as an integer: whole turns drop off the top, and
-// what is left is the angle within 2^-24 of a turn for every 32-bit position
-// (2^-35 for those below a million).  cos and sin are then of an angle of half
-// a turn at most.
+// the position multiplies it as an integer: whole turns drop off the top.  For
+// frequencies up to 1 a step the product is within 2^-24 of a turn for every
+// 32-bit position, 2^-35 for those below a million.  cos and sin are then of an
+// angle of half a turn at most, as an fp32 number: 2^-26 of a turn more.
 //
 // The rotation is fp32 and rounded once to bf16.  Each value is read and
 // written once, 16 bytes at a time; a thread block computes its rows' angles
