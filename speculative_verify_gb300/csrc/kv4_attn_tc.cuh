@@ -224,7 +224,11 @@ __global__ void __launch_bounds__(KtWarps<NT>::THREADS, 1) kv4_attn_tc_kernel(co
     auto bar = [&](int i) { return base + static_cast<uint32_t>(L::BARS + 8 * i); };
     const TcWait wait{flag, p.err};
     if (base & 1023u) {
-        if (threadIdx.x == 0) atomicOr(p.err, 4);
+        if (threadIdx.x == 0) {
+            atomicOr(p.err, 4);
+            pdl_wait_prior();
+            p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);        // (the joining kernel goes by them)
+        }
         return;
     }
     if (threadIdx.x == 0) {
