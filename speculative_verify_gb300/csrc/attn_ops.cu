@@ -176,26 +176,29 @@ constexpr int attn_blocks(int eights) { return eights == 1 ? KaShape<D, 1>::BLOC
 // Packed rows (a sequence's tokens times G) choose the kernel.
 //   * Items of 8 rows, else 16, of kv4_attn_kernel: its time is the codes'
 //     conversion, which an item has once whatever its rows, and products of rows
-//     that are not there: 256 x 8 rows of 4,096 tokens (4 heads of 128) 101 us,
-//     as items of 16 143.
+//     that are not there: 256 x 8 rows of 4,096 tokens (4 heads of 128) 128 us,
+//     as items of 16 182.
 //   * kv4_attn_tc_kernel converts once for 128 rows and more, but through
 //     shared memory, and an item's start and end are long.  Against two or three
 //     items of 16 rows (us, 64 sequences of 4,096 tokens, 4 heads):
-//         d 64:  16 rows 34 and 82, 24 rows 53 and 83, 48 rows 75 and 84
-//         d 128: 16 rows 48 and 86, 24 rows 79 and 87, 32 rows 80 and 87
-//     (one sequence of 131,072 tokens, 32 rows: 62 and 60); d 256, one sequence
-//     of 131,072 tokens: 16 rows 61 and 79, 24 rows 91 and 80.
+//         d 64:  16 rows 40 and 103, 32 rows 66 and 104, 48 rows 93 and 105, 64 rows 118 and 108
+//         d 128: 16 rows 57 and 108, 32 rows 99 and 109, 48 rows 140 and 110
+//         d 256: 16 rows 89 and 143, 24 rows 160 and 144
+//     and one sequence of 131,072 tokens: d 64, 48 rows 55 and 58; d 128, 32 rows
+//     63 and 60, 48 rows 80 and 61; d 256, 16 rows 60 and 78, 24 rows 90 and 80.
 //   * Two tiles share a unit's conversion, one tile leaves more items side by
 //     side and has shorter hand-offs (us, 4 sequences of 8,192 tokens, 4 heads):
-//         d 128: 256 rows 45 and 39, 320 rows 54 and 48, 512 rows 55 and 59, 2,048 rows 142 and 176
-//         d 64:  256 rows 34 and 36, 512 rows 47 and 57
+//         d 128: 256 rows 48 and 43, 384 rows 60 and 54, 512 rows 61 and 67, 2,048 rows 168 and 214
+//         d 64:  128 rows 27 and 28, 192 rows 33 and 40, 512 rows 51 and 65, 2,048 rows 138 and 206
 //     d 256 has room for one only.
-// An item's start and end are counted as `extra` units: 8,192 rows of d 256 were
-// 1,054 us with 1, 776 with 10; twice as many made verify rows no faster.  A part
-// is four units at least, a page a warp (1 row of 1,000 tokens 11.0 us, 12.5
-// with 8, 18 with 20).  Where items are expected in eight parts and more, four
-// groups of threads join them (1 row of 16,000 tokens 19 us, 32 with one group),
-// elsewhere one (nine ragged prompts 161 us, 176 with four).
+// An item's start and end are counted as `extra` units: 8,192 rows of d 256 take
+// 1,002 us with 1, 802 with 5, 742 with 10, 784 with 20.  A part is four units at
+// least, a page a warp (1 row of 1,000 tokens, d 256, 11.7 us in a graph, 12.8
+// with 8, 18.7 with 20).  Where items are expected in eight parts and more, four
+// groups of threads join them (1 row of 16,000 tokens 26 us, 50 with one group),
+// elsewhere one (nine ragged prompts 170 us, 185 with four).
+// A call takes one kernel: 128 single rows of 4,096 tokens and a prompt of 2,048
+// rows (4 query heads on each of 4 of 128) take 237 us together, 126 in two calls.
 AttnPlan attn_plan(int R, int B, int G, int d, int Hk, int max_pages)
 {
     AttnPlan a{};

@@ -26,11 +26,13 @@
 // d 256 is bound by shared memory: a unit's keys and values are 64 KB of fp16,
 // written once and read once by the products, and with the codes they take 70 %
 // of its cycles; d 128 with two tiles by the hand-offs between softmax and
-// products.  8,192 rows of 24 query heads (4 of 256) from nothing take 745 us,
+// products.  8,192 rows of 24 query heads (4 of 256) from nothing take 743 us,
 // 1.1 PFLOP/s; 2,048 rows of 32 (8 of 128) in a window of 4,096 179 us, 0.78;
 // nine ragged prompts after 500 tokens each (4,817 rows, same heads) 161 us.
 // Verify rows, of which a tile has few: 1 x 4 rows of 131,072 tokens (24 heads
-// over 4 of 256) 80 us, 4 x 8 rows of 16,384 44 us.
+// over 4 of 256) 80 us, 4 x 8 rows of 16,384 45 us.  No pipe is full there
+// (shared memory 54 % of its cycles, tensor cores 42): the softmax goes through
+// all 128 rows of a tile and its warps meet once a unit.
 #pragma once
 
 #include "kv4_attn.cuh"
